@@ -91,8 +91,11 @@ typedef void *qsa_stream; /* a cudaStream_t */
 #define QSA_FLAG_INTERNAL 0x4u        /* an internal consistency check failed */
 #define QSA_FLAG_SAMPLE_FALLBACK 0x8u /* not an error: some query of the sampled filter had too few
                                          or too many candidates and was selected from its whole row */
-#define QSA_FLAG_BAD_ID 0x10u         /* qsa_select_attention skipped an id outside its query's
-                                         context (an id other than -1) */
+#define QSA_FLAG_BAD_ID 0x10u         /* a call skipped an id outside its range (an id other than -1):
+                                         a query's context in the attentions, max_blocks or the
+                                         source's blocks elsewhere */
+#define QSA_FLAG_BAD_WEIGHT 0x20u     /* qsa_block_weights_add met a weight outside
+                                         [0, QSA_MAX_BLOCK_WEIGHT] or a NaN; it was clamped (NaN: 0) */
 
 /* Query heads per KV head (GQA group) of qsa_select_attention. */
 #define QSA_ATTN_GROUP 16
@@ -341,6 +344,189 @@ qsa_status qsa_select_attention(const void *qa, const void *kcache, const void *
  */
 qsa_status qsa_vcache_transpose(const void *v, void *vcache_t, int n_kv_heads, int capacity, int first_block,
                                 int n_blocks, qsa_stream stream);
+
+/*
+ * ---- The 4-bit KV cache ---------------------------------------------------------
+ *
+ * K and V rows held in 4 bits per value, for contexts whose 16-bit cache does not fit
+ * or whose reading bounds the step (a block is 8,704 bytes per KV head instead of
+ * 32,768).  No passage of the source pages defines it: it is this library's form of the
+ * reduced KV cache that the pages' engine runs with ("--kv int8"), in the block unit
+ * of the selection.
+ *
+ * Value: each token's row x[0..127] of K (and of V) per KV head has 16 levels,
+ *     x ~ scale * code + min,   min = min(x),   scale = least 16-bit number >= (max(x) - min(x)) / 15,
+ *     code = (x - min) / scale rounded half to even (0 when scale is 0),
+ * so |x - (scale * code + min)| <= scale / 2.  scale and min are held in the rows' own
+ * 16-bit format (bf16 or fp16).  A row that holds an infinity or a NaN, or whose range
+ * is not finite in fp32, is stored as scale = min = NaN and reads as NaN.
+ *
+ * Memory: cache [n_kv_heads][capacity / 64][QSA_QCACHE_BLOCK_BYTES], 16-byte aligned, one
+ * record per 64-token block:
+ *     [   0, 4096)  K codes, 4 planes c of [64 tokens][16 bytes]: byte j of a row holds
+ *                   dimension 16c + j (low nibble) and 64 + 16c + j (high nibble)
+ *     [4096, 4352)  K pairs [64 tokens]: scale (low 16 bits), min (high 16 bits)
+ *     [4352, 4608)  V pairs [64 tokens]
+ *     [4608, 8704)  V codes, 2 planes c of [128 dims][16 bytes]: byte j of a row holds
+ *                   token 16c + j (low nibble) and 32 + 16c + j (high nibble)
+ * Every call on one cache takes the same dt.  Records may be copied as bytes
+ * (qsa_gather_blocks).
+ */
+#define QSA_QCACHE_BLOCK_BYTES 8704
+
+/* Bytes of a cache of these sizes; 0 for invalid ones (n_kv_heads outside [1, 65535],
+ * capacity not a positive multiple of 64 or above 64 * QSA_MAX_BLOCKS). */
+size_t qsa_qcache_bytes(int n_kv_heads, int capacity);
+
+/*
+ * Quantise the K and V rows of n tokens into positions first .. first + n - 1.
+ *
+ *   k, v        rows of 128 values of dtype `dt` (QSA_BF16 or QSA_F16): token i of KV head g
+ *               at k + i * k_token_stride + g * k_head_stride (strides in elements, multiples
+ *               of 8, so slices of a fused projection's rows are taken as they lie); 16-byte
+ *               aligned
+ *   n           tokens, 0 (nothing is enqueued) or more
+ *   first       host int, position of the first token; used when first_dev is NULL
+ *   first_dev   int32 on the DEVICE, or NULL: the position is read when the call runs (a
+ *               captured decode step appends wherever it says).  Tokens whose position lies
+ *               outside [0, capacity) are dropped and set QSA_FLAG_NBLOCKS_CLAMPED
+ *   cache       see above; other positions, those of a shared byte among them, keep
+ *               their values
+ *   ws          a workspace of at least 256 bytes (its flags word is used), or NULL
+ *
+ * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides not multiples of 8,
+ * head_dim != 128, sizes qsa_qcache_bytes() rejects, n < 0 or > capacity, first < 0 or
+ * first + n > capacity (first_dev NULL); QSA_ERR_UNSUPPORTED for another dtype;
+ * QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not 256-byte aligned.
+ */
+qsa_status qsa_qcache_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                             int64_t v_token_stride, int64_t v_head_stride, qsa_dtype dt, int n, int n_kv_heads,
+                             int head_dim, int first, const int32_t *first_dev, void *cache, int capacity, void *ws,
+                             size_t ws_bytes, qsa_stream stream);
+
+/*
+ * The rows of positions first .. first + n - 1 back in 16 bits (scale * code + min in fp32,
+ * rounded once to `dt`), into k and v addressed as for qsa_qcache_append.
+ * Errors: as qsa_qcache_append's.
+ */
+qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int head_dim, int capacity, int first,
+                           int n, void *k, int64_t k_token_stride, int64_t k_head_stride, void *v,
+                           int64_t v_token_stride, int64_t v_head_stride, qsa_stream stream);
+
+/*
+ * qsa_select_attention over a 4-bit cache: the same formulas on the rows' values
+ * scale * code + min, for n_heads / n_kv_heads = 1 .. 16 query heads per KV head, and each
+ * selected block's share of the attention.
+ *
+ *   qa        query i, head h at qa + i * q_stride + h * q_head_stride, 128 values of dtype
+ *             `dt` (strides in elements, multiples of 8), 16-byte aligned
+ *   cache     of the same dt
+ *   ids, k, n_tokens, capacity, scale, ws   as for qsa_select_attention
+ *   out       [nq][n_heads][128] of dtype out_dt: QSA_F32, or dt
+ *   lse       [nq][n_heads] fp32 out, or NULL
+ *   weights   [nq][n_kv_heads][k] fp32 out, or NULL: the softmax weight that the group's heads
+ *             together give to slot j's tokens (a slot with id -1, an id outside the
+ *             context, or a repeat of an earlier slot gets 0); a (query, KV head)'s
+ *             weights add up to its heads, or to 0 when it sees no token
+ *
+ * Arithmetic: products of codes with the queries exact, accumulated in fp32; softmax
+ * statistics, lse and weights in fp32.
+ * Errors: as qsa_select_attention's, with n_heads a multiple of n_kv_heads of at most 16
+ * times it, the cache sizes as qsa_qcache_bytes() has them, nq * n_kv_heads < 2^28, and
+ * out_dt other than QSA_F32 or dt.
+ */
+qsa_status qsa_select_attention_qcache(const void *qa, int64_t q_stride, int64_t q_head_stride, qsa_dtype dt,
+                                       const void *cache, const int32_t *ids, int k, const int32_t *n_tokens, int nq,
+                                       int n_heads, int n_kv_heads, int head_dim, int capacity, float scale, void *out,
+                                       qsa_dtype out_dt, float *lse, float *weights, void *ws, size_t ws_bytes,
+                                       qsa_stream stream);
+
+/*
+ * ---- Eviction by accumulated attention weight ------------------------------------
+ *
+ * Blocks that the attention no longer looks at leave the cache: the weights of each
+ * attention call are added up per block (qsa_block_weights_add, with a decay), the blocks
+ * to keep are those of largest sum beside the first and the most recent ones
+ * (qsa_evict_plan), and their records, in every array that holds one record per block,
+ * move together in order (qsa_gather_blocks).  No passage of the source pages defines these
+ * calls; "block" is the selection's 64-token block, so the indexer's keys move along.
+ */
+
+/* Largest weight qsa_block_weights_add takes (an attention call's are at most 16). */
+#define QSA_MAX_BLOCK_WEIGHT 32.0f
+
+/*
+ * acc[b] = decay * prev[b] + the sum of weights[q][g][j] over all q, g, j with ids[q][j] == b.
+ *
+ *   weights   [nq][n_kv_heads][k] fp32 in [0, QSA_MAX_BLOCK_WEIGHT] (others are clamped, NaN to 0,
+ *             and set QSA_FLAG_BAD_WEIGHT)
+ *   ids       [nq][k] int32; -1 is skipped, other ids outside [0, max_blocks) too (with
+ *             QSA_FLAG_BAD_ID); the same id may appear any number of times
+ *   decay     host float, finite and >= 0
+ *   prev      [max_blocks] fp32, or NULL (zeros); may be acc itself
+ *   acc       [max_blocks] fp32 out
+ *   ws        a workspace of at least 256 bytes (its flags word is used), or NULL
+ *
+ * The weights are summed as integers in units of 2^-36, so the result does not depend on
+ * the order of the work.
+ * Errors: QSA_ERR_INVALID_ARG for NULL pointers, nq, n_kv_heads or k < 1, nq * n_kv_heads * k >
+ * 2^22, max_blocks outside [1, QSA_MAX_BLOCKS], a decay not finite or < 0;
+ * QSA_ERR_WORKSPACE as above.
+ */
+qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, float decay,
+                                 const float *prev, float *acc, int max_blocks, void *ws, size_t ws_bytes,
+                                 qsa_stream stream);
+
+/*
+ * Which blocks stay, for each of n_rows caches (rows): of a row's nb = ceil(n_tokens / 64)
+ * blocks the first n_first, the last n_last, and of the others those of largest weight (ties
+ * to the lower id), n_keep in all; all of them when nb <= n_keep.
+ *
+ *   weights     [n_rows][weights_stride] fp32, weights_stride >= max_blocks (a NaN ranks below
+ *               every number)
+ *   n_tokens    [n_rows] int32 on the DEVICE, clamped to [0, 64 * max_blocks] (a clamp sets
+ *               QSA_FLAG_NBLOCKS_CLAMPED)
+ *   keep        [n_rows][n_keep] int32 out: the kept ids in ascending order, -1 behind them
+ *   new_tokens  [n_rows] int32 out: tokens left, n_tokens - 64 * (blocks evicted): the last
+ *               block stays last, so a partial one stays valid
+ *   ws          a workspace of at least 256 bytes (its flags word is used), or NULL
+ *
+ * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, 2^20], max_blocks outside
+ * [1, QSA_MAX_BLOCKS], weights_stride < max_blocks, n_keep outside [1, max_blocks],
+ * n_first < 0, n_last < 1, n_first + n_last > n_keep; QSA_ERR_WORKSPACE as above.
+ */
+qsa_status qsa_evict_plan(const float *weights, int64_t weights_stride, const int32_t *n_tokens, int n_rows,
+                          int max_blocks, int n_keep, int n_first, int n_last, int32_t *keep, int32_t *new_tokens,
+                          void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* An array that holds one record of block_bytes per block: src [n_rows][src_blocks] records,
+ * dst [n_rows][dst_blocks] (a row per KV head for a cache, one row for the indexer's keys). */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t block_bytes; /* a multiple of 4 */
+    int32_t n_rows;
+    int32_t src_blocks;
+    int32_t dst_blocks;
+} qsa_block_array;
+
+#define QSA_GATHER_MAX_ARRAYS 8
+
+/*
+ * dst[row][i] = src[row][keep[i]] for 0 <= i < n_keep, for each of n_arrays (host array, 1 ..
+ * QSA_GATHER_MAX_ARRAYS) arrays, one launch in all.
+ *
+ *   keep   [n_keep] int32 on the DEVICE (a row of qsa_evict_plan's): where it is -1, or outside
+ *          [0, src_blocks) (QSA_FLAG_BAD_ID), dst[row][i] is left as it was
+ *   ws     a workspace of at least 256 bytes (its flags word is used), or NULL
+ *
+ * Out of place: a dst may overlap no src and no other dst.
+ * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_arrays or n_keep out of range, sizes < 1,
+ * dst_blocks < n_keep, block_bytes not a multiple of 4 or above 2^30, pointers not 4-byte
+ * aligned, a dst that overlaps; QSA_ERR_WORKSPACE as above.
+ */
+qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, int n_keep, void *ws,
+                             size_t ws_bytes, qsa_stream stream);
 
 /*
  * Copy the workspace flags word (QSA_FLAG_* bits) to host `*flags`, waiting for

@@ -1,0 +1,60 @@
+// qcache.cuh -- the record of one 64-token block of the 4-bit KV cache (qsa.h,
+// "The 4-bit KV cache"), shared by the kernels that write, read and attend over it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "qsa_internal.h"
+
+namespace qsa {
+
+// The record's two halves are each one contiguous copy: [K codes][K pairs][V pairs]
+// and [V codes].  Codes lie in planes of 16-byte rows, so that a thread per row reads
+// 16 bytes beside its neighbours' (no bank conflict from shared memory, full sectors
+// from global memory), and the low nibbles of a row are the 8-bit operand of 16
+// consecutive dimensions (K) or tokens (V), the high nibbles that of another 16: a mask
+// and a shift unpack a word into two.
+constexpr int kQBlockTok = 64;
+constexpr int kQDim = 128;
+constexpr int kQRec = QSA_QCACHE_BLOCK_BYTES;
+constexpr int kQOffKPair = 4096;    // after 4 planes of [64 tokens][16 B]
+constexpr int kQOffVPair = 4352;
+constexpr int kQOffV = 4608;        // 2 planes of [128 dims][16 B]
+static_assert(kQOffV + 4096 == kQRec, "record size");
+
+__host__ __device__ inline size_t qrec_offset(int g, int nb_cap, int b) {
+    return ((size_t)g * nb_cap + b) * (size_t)kQRec;
+}
+
+// The 16-bit formats of rows and (scale, minimum) pairs.
+template <bool F16>
+struct QFmt;
+template <>
+struct QFmt<false> {
+    static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+    static __device__ __forceinline__ uint32_t bits(float x) {
+        return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
+    }
+    static __device__ __forceinline__ uint32_t bits_up(float x) {
+        return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(x));
+    }
+};
+template <>
+struct QFmt<true> {
+    static __device__ __forceinline__ float lo(uint32_t w) {
+        return __half2float(__ushort_as_half((unsigned short)(w & 0xFFFFu)));
+    }
+    static __device__ __forceinline__ float hi(uint32_t w) {
+        return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+    }
+    static __device__ __forceinline__ uint32_t bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
+    static __device__ __forceinline__ uint32_t bits_up(float x) {
+        return (uint32_t)__half_as_ushort(__float2half_ru(x));
+    }
+};
+
+}  // namespace qsa

@@ -141,4 +141,81 @@ qsa_status launch_select_attention(const AttnArgs &a, cudaStream_t s);
 qsa_status launch_vcache_transpose(const void *v, void *vcache_t, int n_kv_heads, int capacity, int first_block,
                                    int n_blocks, cudaStream_t s);
 
+// The 4-bit cache (strides in elements).
+struct QAppendArgs {
+    const void *k, *v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    qsa_dtype dt;
+    int n;
+    int n_kv_heads;
+    int first;
+    const int32_t *first_dev;   // not null: the position is read on the device
+    void *cache;
+    int capacity;
+    uint32_t *flags;
+};
+qsa_status launch_qcache_append(const QAppendArgs &a, cudaStream_t s);
+
+struct QLoadArgs {
+    const void *cache;
+    qsa_dtype dt;
+    int n_kv_heads;
+    int capacity;
+    int first;
+    int n;
+    void *k, *v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+};
+qsa_status launch_qcache_load(const QLoadArgs &a, cudaStream_t s);
+
+struct QAttnArgs {
+    const void *qa;
+    int64_t q_stride, q_head_stride;
+    qsa_dtype dt;
+    const void *cache;
+    const int32_t *ids;
+    int k;
+    const int32_t *n_tokens;
+    int nq;
+    int n_heads;
+    int n_kv_heads;
+    int capacity;
+    float scale;
+    void *out;
+    qsa_dtype out_dt;   // QSA_F32 or dt
+    float *lse;
+    float *weights;
+    uint32_t *flags;
+};
+qsa_status launch_qcache_attention(const QAttnArgs &a, cudaStream_t s);
+
+struct WeightsAddArgs {
+    const float *weights;
+    const int32_t *ids;
+    int nq;
+    int n_kv_heads;
+    int k;
+    float decay;
+    const float *prev;   // may be null (zeros) or acc
+    float *acc;
+    int max_blocks;
+    uint32_t *flags;
+};
+qsa_status launch_weights_add(const WeightsAddArgs &a, cudaStream_t s);
+
+struct EvictPlanArgs {
+    const float *weights;
+    int64_t stride;
+    const int32_t *n_tokens;
+    int n_rows;
+    int max_blocks;
+    int n_keep, n_first, n_last;
+    int32_t *keep;
+    int32_t *new_tokens;
+    uint32_t *flags;
+};
+qsa_status launch_evict_plan(const EvictPlanArgs &a, cudaStream_t s);
+qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, int n_keep,
+                                uint32_t *flags, cudaStream_t s);
+
 }  // namespace qsa

@@ -26,17 +26,21 @@ PATH_NAMES = {PATH_AUTO: "auto", PATH_SPLIT: "split", PATH_SAMPLE: "sample",
               PATH_REGISTER: "register", PATH_RADIX: "radix", PATH_WARP: "warp"}
 # flags word bits
 FLAG_NBLOCKS_CLAMPED, FLAG_WAIT_TIMEOUT, FLAG_INTERNAL, FLAG_SAMPLE_FALLBACK = 0x1, 0x2, 0x4, 0x8
-FLAG_BAD_ID = 0x10
-ERROR_FLAGS = FLAG_NBLOCKS_CLAMPED | FLAG_WAIT_TIMEOUT | FLAG_INTERNAL | FLAG_BAD_ID
+FLAG_BAD_ID, FLAG_BAD_WEIGHT = 0x10, 0x20
+ERROR_FLAGS = FLAG_NBLOCKS_CLAMPED | FLAG_WAIT_TIMEOUT | FLAG_INTERNAL | FLAG_BAD_ID | FLAG_BAD_WEIGHT
 HEAD_DIM = 128
 MAX_K = 1024
 ATTN_GROUP = 16
 ATTN_MAX_K = 64
+QCACHE_BLOCK_BYTES = 8704
+MAX_BLOCK_WEIGHT = 32.0
+GATHER_MAX_ARRAYS = 8
 
 EXPORTS = ("qsa_workspace_bytes", "qsa_workspace_init", "qsa_block_scores", "qsa_block_topk",
            "qsa_block_topk_static", "qsa_block_candidates", "qsa_merge_candidates", "qsa_select",
-           "qsa_select_attention", "qsa_vcache_transpose", "qsa_read_flags", "qsa_auto_path", "qsa_last_error",
-           "qsa_version")
+           "qsa_select_attention", "qsa_vcache_transpose", "qsa_qcache_bytes", "qsa_qcache_append", "qsa_qcache_load",
+           "qsa_select_attention_qcache", "qsa_block_weights_add", "qsa_evict_plan", "qsa_gather_blocks",
+           "qsa_read_flags", "qsa_auto_path", "qsa_last_error", "qsa_version")
 MERGE_CAP = 4096   # candidates per query qsa_merge_candidates holds (n_shards x k)
 
 
@@ -45,6 +49,12 @@ class QSAError(RuntimeError):
         super().__init__(f"{fn} failed with status {status}: {reason}")
         self.status = status
         self.reason = reason
+
+
+class BlockArray(ctypes.Structure):
+    """qsa_block_array: an array of one record per block, moved by qsa_gather_blocks."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("block_bytes", ctypes.c_int64),
+                ("n_rows", ctypes.c_int32), ("src_blocks", ctypes.c_int32), ("dst_blocks", ctypes.c_int32)]
 
 
 _lib = None
@@ -82,6 +92,22 @@ def load() -> ctypes.CDLL:
     lib.qsa_select_attention.restype = i32
     lib.qsa_vcache_transpose.argtypes = [vp, vp, i32, i32, i32, i32, vp]
     lib.qsa_vcache_transpose.restype = i32
+    f32 = ctypes.c_float
+    lib.qsa_qcache_bytes.argtypes = [i32, i32]
+    lib.qsa_qcache_bytes.restype = sz
+    lib.qsa_qcache_append.argtypes = [vp, i64, i64, vp, i64, i64, i32, i32, i32, i32, i32, vp, vp, i32, vp, sz, vp]
+    lib.qsa_qcache_append.restype = i32
+    lib.qsa_qcache_load.argtypes = [vp, i32, i32, i32, i32, i32, i32, vp, i64, i64, vp, i64, i64, vp]
+    lib.qsa_qcache_load.restype = i32
+    lib.qsa_select_attention_qcache.argtypes = [vp, i64, i64, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp,
+                                                i32, vp, vp, vp, sz, vp]
+    lib.qsa_select_attention_qcache.restype = i32
+    lib.qsa_block_weights_add.argtypes = [vp, vp, i32, i32, i32, f32, vp, vp, i32, vp, sz, vp]
+    lib.qsa_block_weights_add.restype = i32
+    lib.qsa_evict_plan.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.qsa_evict_plan.restype = i32
+    lib.qsa_gather_blocks.argtypes = [ctypes.POINTER(BlockArray), i32, vp, i32, vp, sz, vp]
+    lib.qsa_gather_blocks.restype = i32
     lib.qsa_read_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), i32, vp]
     lib.qsa_read_flags.restype = i32
     lib.qsa_auto_path.argtypes = [i32, i32, i32, i32]
@@ -320,6 +346,207 @@ def vcache_transpose(v: torch.Tensor, vcache_t: torch.Tensor, first_block: int =
                                   _stream(stream))
     _check("qsa_vcache_transpose", st)
     return vcache_t
+
+
+def _on_current_device(tensors) -> int:
+    """The current stream, for tensors that all lie on the current CUDA device; raises otherwise."""
+    dev = torch.cuda.current_device()
+    for t, name in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device {dev} (it is on {t.device})")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _qdtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return F16
+    raise ValueError(f"{name} must be bfloat16 or float16 (got {t.dtype})")
+
+
+def _qcache_dims(cache: torch.Tensor) -> tuple[int, int]:
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or cache.shape[2] != QCACHE_BLOCK_BYTES or \
+            not cache.is_contiguous():
+        raise ValueError(f"cache must be a contiguous uint8 tensor [n_kv_heads, blocks, {QCACHE_BLOCK_BYTES}]")
+    return cache.shape[0], cache.shape[1] * 64
+
+
+def _qrows(t: torch.Tensor, name: str, kv: int) -> tuple[int, int]:
+    """(token stride, head stride) of rows [n, n_kv_heads, 128]."""
+    if t.dim() != 3 or t.shape[1] != kv or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+        raise ValueError(f"{name} must be [n, {kv}, {HEAD_DIM}] with unit inner stride (got {tuple(t.shape)})")
+    return t.stride(0), t.stride(1)
+
+
+def _ws_args(ws: torch.Tensor | None) -> tuple[int | None, int]:
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def qcache_bytes(n_kv_heads: int, capacity: int) -> int:
+    return int(load().qsa_qcache_bytes(n_kv_heads, capacity))
+
+
+def alloc_qcache(n_kv_heads: int, capacity: int, device=None) -> torch.Tensor:
+    """A zero-filled 4-bit cache [n_kv_heads, capacity / 64, 8704] (uint8 CUDA tensor)."""
+    if qcache_bytes(n_kv_heads, capacity) == 0:
+        raise ValueError("invalid cache sizes")
+    return torch.zeros(n_kv_heads, capacity // 64, QCACHE_BLOCK_BYTES, dtype=torch.uint8, device=device or "cuda")
+
+
+def qcache_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, first, ws: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Quantise k, v [n, n_kv_heads, 128] (both bfloat16 or both float16; any token and head
+    strides that are multiples of 8) into positions first .. first + n - 1 of the 4-bit
+    cache.  first: an int, or a one-element int32 CUDA tensor read when the call runs."""
+    lib = load()
+    kv, cap = _qcache_dims(cache)
+    dt = _qdtype(k, "k")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("v must match k's shape and dtype")
+    ks, vs = _qrows(k, "k", kv), _qrows(v, "v", kv)
+    dev_first = first if isinstance(first, torch.Tensor) else None
+    if dev_first is not None and (dev_first.dtype != torch.int32 or dev_first.numel() != 1):
+        raise ValueError("first must be an int or an int32 tensor of one element")
+    cur = _on_current_device(((k, "k"), (v, "v"), (cache, "cache"), (dev_first, "first"), (ws, "ws")))
+    st = lib.qsa_qcache_append(k.data_ptr(), *ks, v.data_ptr(), *vs, dt, k.shape[0], kv, HEAD_DIM,
+                               0 if dev_first is not None else int(first),
+                               None if dev_first is None else dev_first.data_ptr(), cache.data_ptr(), cap,
+                               *_ws_args(ws), cur if stream is None else _stream(stream)) if k.shape[0] else OK
+    _check("qsa_qcache_append", st)
+    return cache
+
+
+def qcache_load(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, first: int = 0, stream=None) -> None:
+    """The rows of positions first .. first + n - 1 back in 16 bits, into k, v [n, n_kv_heads, 128]."""
+    lib = load()
+    kv, cap = _qcache_dims(cache)
+    dt = _qdtype(k, "k")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("v must match k's shape and dtype")
+    ks, vs = _qrows(k, "k", kv), _qrows(v, "v", kv)
+    cur = _on_current_device(((cache, "cache"), (k, "k"), (v, "v")))
+    st = lib.qsa_qcache_load(cache.data_ptr(), dt, kv, HEAD_DIM, cap, int(first), k.shape[0], k.data_ptr(), *ks,
+                             v.data_ptr(), *vs, cur if stream is None else _stream(stream)) if k.shape[0] else OK
+    _check("qsa_qcache_load", st)
+
+
+def select_attention_qcache(qa: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, n_tokens: torch.Tensor,
+                            out: torch.Tensor, lse: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                            scale: float | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Selection attention over ids [nq, k] of a 4-bit cache: out [nq, H, 128] (fp32 or qa's
+    dtype), lse [nq, H] fp32, and weights [nq, n_kv_heads, k] fp32, each slot's softmax
+    weight summed over the group's heads.  qa [nq, H, 128] bfloat16 or float16 (the dtype of
+    the appended rows; strides multiples of 8), H = 1 .. 16 times n_kv_heads."""
+    lib = load()
+    kv, cap = _qcache_dims(cache)
+    dt = _qdtype(qa, "qa")
+    if qa.dim() != 3 or qa.stride(2) != 1:
+        raise ValueError("qa must be [nq, n_heads, 128] with unit inner stride")
+    nq, H, D = qa.shape
+    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != nq or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 tensor [nq, k]")
+    if n_tokens.dtype != torch.int32 or n_tokens.numel() != nq or not n_tokens.is_contiguous():
+        raise ValueError("n_tokens must be a contiguous int32 tensor [nq]")
+    if out.shape != qa.shape or not out.is_contiguous() or (out.dtype != torch.float32 and out.dtype != qa.dtype):
+        raise ValueError("out must be a contiguous tensor [nq, n_heads, 128], fp32 or of qa's dtype")
+    k = ids.shape[1]
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (nq, H) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [nq, n_heads]")
+    if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (nq, kv, k) or
+                                not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous fp32 tensor [nq, n_kv_heads, k]")
+    cur = _on_current_device(((qa, "qa"), (cache, "cache"), (ids, "ids"), (n_tokens, "n_tokens"), (out, "out"),
+                              (lse, "lse"), (weights, "weights"), (ws, "ws")))
+    st = lib.qsa_select_attention_qcache(
+        qa.data_ptr(), qa.stride(0), qa.stride(1), dt, cache.data_ptr(), ids.data_ptr(), k, n_tokens.data_ptr(), nq, H,
+        kv, D, cap, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        F32 if out.dtype == torch.float32 else dt, None if lse is None else lse.data_ptr(),
+        None if weights is None else weights.data_ptr(), *_ws_args(ws), cur if stream is None else _stream(stream))
+    _check("qsa_select_attention_qcache", st)
+    return out
+
+
+def block_weights_add(weights: torch.Tensor, ids: torch.Tensor, acc: torch.Tensor, prev: torch.Tensor | None = None,
+                      decay: float = 1.0, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """acc[b] = decay * prev[b] + the weights [nq, n_kv_heads, k] of the slots with ids[q, j] == b
+    (acc, prev [max_blocks] fp32; prev None: zeros, or acc itself)."""
+    lib = load()
+    if weights.dtype != torch.float32 or weights.dim() != 3 or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous fp32 tensor [nq, n_kv_heads, k]")
+    nq, kv, k = weights.shape
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (nq, k) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 tensor [nq, k]")
+    for t, name in ((acc, "acc"), (prev, "prev")):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous() or
+                              t.numel() != acc.numel()):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor [max_blocks]")
+    cur = _on_current_device(((weights, "weights"), (ids, "ids"), (acc, "acc"), (prev, "prev"), (ws, "ws")))
+    if prev is not None and prev.data_ptr() != acc.data_ptr() and \
+            abs(prev.data_ptr() - acc.data_ptr()) < 4 * acc.numel():
+        raise ValueError("prev must be acc itself or not overlap it")
+    st = lib.qsa_block_weights_add(weights.data_ptr(), ids.data_ptr(), nq, kv, k, float(decay),
+                                   None if prev is None else prev.data_ptr(), acc.data_ptr(), acc.numel(),
+                                   *_ws_args(ws), cur if stream is None else _stream(stream))
+    _check("qsa_block_weights_add", st)
+    return acc
+
+
+def evict_plan(weights: torch.Tensor, n_tokens: torch.Tensor, keep: torch.Tensor, new_tokens: torch.Tensor,
+               n_first: int = 1, n_last: int = 1, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """keep [n_rows, n_keep] int32: the blocks of each row that stay (the first n_first, the last
+    n_last, and the others of largest weights [n_rows, max_blocks]), ascending, -1 behind them;
+    new_tokens [n_rows] int32: the tokens left of n_tokens [n_rows]."""
+    lib = load()
+    if weights.dtype != torch.float32 or weights.dim() != 2 or weights.stride(1) != 1:
+        raise ValueError("weights must be a 2-D fp32 tensor with unit inner stride")
+    n_rows, max_blocks = weights.shape
+    if keep.dtype != torch.int32 or keep.dim() != 2 or keep.shape[0] != n_rows or not keep.is_contiguous():
+        raise ValueError("keep must be a contiguous int32 tensor [n_rows, n_keep]")
+    for t, name in ((n_tokens, "n_tokens"), (new_tokens, "new_tokens")):
+        if t.dtype != torch.int32 or t.numel() != n_rows or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor [n_rows]")
+    cur = _on_current_device(((weights, "weights"), (n_tokens, "n_tokens"), (keep, "keep"),
+                              (new_tokens, "new_tokens"), (ws, "ws")))
+    # a single row's stride is never used and may be anything in torch
+    stride = max(weights.stride(0), max_blocks) if n_rows == 1 else weights.stride(0)
+    st = lib.qsa_evict_plan(weights.data_ptr(), stride, n_tokens.data_ptr(), n_rows, max_blocks,
+                            keep.shape[1], n_first, n_last, keep.data_ptr(), new_tokens.data_ptr(), *_ws_args(ws),
+                            cur if stream is None else _stream(stream))
+    _check("qsa_evict_plan", st)
+    return keep
+
+
+def _block_array(src: torch.Tensor, dst: torch.Tensor) -> BlockArray:
+    """src, dst as [rows, blocks, ...], or [blocks, ...] for one row, with 1 or 2 dimensions."""
+    if src.dtype != dst.dtype or src.dim() != dst.dim() or not src.is_contiguous() or not dst.is_contiguous():
+        raise ValueError("src and dst must be contiguous tensors of one dtype and as many dimensions")
+    at = 1 if src.dim() >= 3 else 0
+    if src.shape[:at] != dst.shape[:at] or src.shape[at + 1:] != dst.shape[at + 1:]:
+        raise ValueError("src and dst may differ in their number of blocks only")
+    rows = src.shape[0] if at else 1
+    per = src.element_size()
+    for n in src.shape[at + 1:]:
+        per *= n
+    return BlockArray(src.data_ptr(), dst.data_ptr(), per, rows, src.shape[at], dst.shape[at])
+
+
+def gather_blocks(arrays, keep: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> None:
+    """dst[row, i] = src[row, keep[i]] for each (src, dst) of arrays (at most 8), in one launch.
+
+    A tensor of three or more dimensions is [rows, blocks, record...] (a cache: a row per KV
+    head), one of fewer is [blocks, record] (indexer keys) or [blocks] (weights); keep
+    [n_keep] int32, where -1 leaves dst as it was.  Nothing may overlap."""
+    lib = load()
+    if keep.dtype != torch.int32 or keep.dim() != 1 or not keep.is_contiguous():
+        raise ValueError("keep must be a contiguous int32 tensor [n_keep]")
+    if not 1 <= len(arrays) <= GATHER_MAX_ARRAYS:
+        raise ValueError(f"1 to {GATHER_MAX_ARRAYS} arrays (got {len(arrays)})")
+    cur = _on_current_device([(keep, "keep"), (ws, "ws")] + [(t, "arrays") for pair in arrays for t in pair])
+    packed = (BlockArray * len(arrays))(*(_block_array(src, dst) for src, dst in arrays))
+    st = lib.qsa_gather_blocks(packed, len(arrays), keep.data_ptr(), keep.numel(), *_ws_args(ws),
+                               cur if stream is None else _stream(stream))
+    _check("qsa_gather_blocks", st)
 
 
 def read_flags(ws: torch.Tensor, clear: bool = True, stream=None) -> int:

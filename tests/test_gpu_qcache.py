@@ -1,0 +1,473 @@
+"""The 4-bit KV cache on the GPU against the FP64 oracle: the writer byte for byte, the reader, and
+selection attention over it, within bounds made of their roundings (tests/qcache_cases.py)."""
+import numpy as np
+import pytest
+
+from oracle import qcache as oq
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from sparse_attention_kv_gb300 import qsa  # noqa: E402
+
+from .qcache_cases import DT, check_attention, random_cache, random_ids, to16  # noqa: E402
+
+FMTS = [oq.BF16, oq.F16]
+
+
+def _ws():
+    return torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+
+# ------------------------------------------------------------------ writer and reader
+
+def _rows(seed, n, kv):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(size=(n, kv, 128))
+    x[:, :, ::31] *= 6
+    x += rng.normal(size=(n, kv, 1)) * 2
+    return x
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,first,kv,blocks", [(1, 0, 1, 1), (1, 95, 3, 2), (63, 1, 2, 2), (64, 64, 1, 3), (65, 63, 2, 3),
+                                               (200, 37, 4, 5), (5, 187, 2, 3), (384, 0, 1, 6)])
+def test_append_writes_the_oracles_bytes(n, first, kv, blocks, fmt):
+    """Over a cache of random bytes: the range's bytes are the oracle's, all others keep theirs."""
+    k, kd = to16(_rows(10 * n + first, n, kv), fmt)
+    v, vd = to16(_rows(10 * n + first + 1, n, kv), fmt)
+    want = np.random.default_rng(n).integers(0, 256, size=(kv, blocks, oq.REC), dtype=np.uint8)
+    cache = torch.from_numpy(want).cuda()
+    ws = _ws()
+    qsa.qcache_append(k, v, cache, first, ws=ws)
+    oq.append(want, kd, vd, first, fmt)
+    np.testing.assert_array_equal(cache.cpu().numpy(), want)
+    assert qsa.read_flags(ws) == 0
+    ko, vo = torch.full_like(k, 7), torch.full_like(v, 7)
+    qsa.qcache_load(cache, ko, vo, first)
+    rk, rv = oq.rows(want, first, n, fmt)
+    for got, ref in ((ko, rk), (vo, rv)):   # fp64 to fp32 is exact here: 8 or 11 bits times 4, plus one 16-bit value
+        assert torch.equal(got.cpu(), torch.from_numpy(ref).float().to(DT[fmt]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_append_special_rows(fmt):
+    """Constant and zero rows, wide offsets, tiny ranges, exact ties, subnormal scales, the
+    format's largest values, and rows with an infinity or a NaN."""
+    rng = np.random.default_rng(5)
+    big = 65504.0 if fmt == oq.F16 else 3.0e38
+    rows = [np.zeros(128), np.full(128, -2.5), 1000 + rng.integers(0, 5, 128), rng.integers(0, 16, 128) + 0.0,
+            rng.integers(0, 31, 128) / 2.0, rng.integers(0, 61, 128) / 4.0 - 8, rng.normal(size=128) * 1e-6,
+            rng.normal(size=128) * 6e-8, rng.integers(0, 3, 128) * 6e-8, rng.uniform(-1, 1, 128) * big / 4,
+            np.where(rng.random(128) < 0.5, big, 0.0), np.where(rng.random(128) < 0.5, -big, big),
+            np.where(np.arange(128) == 9, np.inf, 1.0), np.where(np.arange(128) == 100, -np.inf, 1.0),
+            np.where(np.arange(128) == 3, np.nan, rng.normal(size=128)), np.full(128, np.nan),
+            np.where(np.arange(128) == 0, -7.0, 2.0 ** -11 * rng.integers(0, 9, 128)),
+            np.where(np.arange(128) == 5, 30.0, rng.normal(size=128) * 2.0 ** -9)]
+    with np.errstate(over="ignore", invalid="ignore"):
+        k, kd = to16(np.stack(rows)[:, None], fmt)
+    v, vd = k.flip(0), kd[::-1].copy()
+    cache = torch.zeros(1, 1, oq.REC, dtype=torch.uint8, device="cuda")
+    qsa.qcache_append(k, v, cache, 11)
+    want = np.zeros((1, 1, oq.REC), dtype=np.uint8)
+    oq.append(want, kd, vd, 11, fmt)
+    np.testing.assert_array_equal(cache.cpu().numpy(), want)
+
+
+def test_append_ties_and_near_ties_of_many_scales():
+    """Rows of few-bit values: quotients on and beside the half-way points, for many scales."""
+    rng = np.random.default_rng(6)
+    n = 640
+    x = rng.integers(-40, 41, size=(n, 1, 128)) * np.exp2(rng.integers(-6, 7, size=(n, 1, 1)).astype(float))
+    x[::3] += np.exp2(rng.integers(-3, 9, size=(len(x[::3]), 1, 1)).astype(float))
+    x[1::5, :, :8] *= 2.0 ** -7
+    for fmt in FMTS:
+        k, kd = to16(x, fmt)
+        cache = qsa.alloc_qcache(1, n)
+        qsa.qcache_append(k, k, cache, 0)
+        want = np.zeros((1, n // 64, oq.REC), dtype=np.uint8)
+        oq.append(want, kd, kd, 0, fmt)
+        np.testing.assert_array_equal(cache.cpu().numpy(), want)
+
+
+def test_append_takes_slices_of_a_projection():
+    kv, n = 2, 70
+    x = torch.randn(n, 12, 128, device="cuda").bfloat16()       # 8 query heads, K, V
+    k, v = x[:, 8:10], x[:, 10:]
+    a, b = qsa.alloc_qcache(kv, 192), qsa.alloc_qcache(kv, 192)
+    qsa.qcache_append(k, v, a, 50)
+    qsa.qcache_append(k.contiguous(), v.contiguous(), b, 50)
+    assert torch.equal(a, b)
+    every = torch.randn(2 * n, kv, 128, device="cuda").half()   # every other token, heads in reverse order of memory
+    qsa.qcache_append(every[::2], every[1::2], a, 0)
+    qsa.qcache_append(every[::2].contiguous(), every[1::2].contiguous(), b, 0)
+    assert torch.equal(a, b)
+    ko = torch.zeros(n, 12, 128, device="cuda").half()          # and the reader writes into slices
+    qsa.qcache_load(a, ko[:, 2:4], ko[:, 7:9], 0)
+    kc, vc = torch.empty(n, kv, 128, device="cuda").half(), torch.empty(n, kv, 128, device="cuda").half()
+    qsa.qcache_load(a, kc, vc, 0)
+    assert torch.equal(ko[:, 2:4], kc) and torch.equal(ko[:, 7:9], vc)
+    assert not ko[:, :2].any() and not ko[:, 4:7].any() and not ko[:, 9:].any()
+
+
+def test_append_in_pieces_equals_one_call():
+    k, _ = to16(_rows(20, 150, 2), oq.BF16)
+    v, _ = to16(_rows(21, 150, 2), oq.BF16)
+    a, b = qsa.alloc_qcache(2, 256), qsa.alloc_qcache(2, 256)
+    qsa.qcache_append(k, v, a, 13)
+    at = 0
+    for m in (1, 1, 30, 2, 64, 1, 51):
+        qsa.qcache_append(k[at:at + m], v[at:at + m], b, 13 + at)
+        at += m
+    assert at == 150 and torch.equal(a, b)
+
+
+def test_append_at_a_device_position_in_a_captured_graph():
+    """The captured step appends where the device says, replay after replay; positions outside
+    the cache are dropped and flagged."""
+    k, _ = to16(_rows(30, 5, 2), oq.BF16)
+    v, _ = to16(_rows(31, 5, 2), oq.BF16)
+    cache, ws = qsa.alloc_qcache(2, 192), _ws()
+    first = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        qsa.qcache_append(k, v, cache, first, ws=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qsa.qcache_append(k, v, cache, first, ws=ws)
+        first += 5
+    cache.zero_()
+    first.fill_(60)
+    want = qsa.alloc_qcache(2, 192)
+    for i in range(3):
+        graph.replay()
+        qsa.qcache_append(k, v, want, 60 + 5 * i)
+    assert torch.equal(cache, want) and qsa.read_flags(ws) == 0
+    for at, lo, hi in ((189, 0, 3), (-2, 2, 5), (192, 0, 0), (-5, 0, 0), (1 << 30, 0, 0), (-(1 << 30), 0, 0),
+                       ((1 << 31) - 1, 0, 0), (-(1 << 31), 0, 0)):
+        first.fill_(at)
+        graph.replay()
+        if hi > lo:
+            qsa.qcache_append(k[lo:hi], v[lo:hi], want, at + lo)
+        assert torch.equal(cache, want)
+        assert qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+
+
+def test_empty_append_and_load_touch_nothing():
+    cache = torch.full((1, 1, oq.REC), 9, dtype=torch.uint8, device="cuda")
+    none = torch.empty(0, 1, 128, dtype=torch.bfloat16, device="cuda")
+    qsa.qcache_append(none, none, cache, 64)
+    qsa.qcache_load(cache, none, none, 64)
+    assert (cache == 9).all()
+
+
+# ------------------------------------------------------------------ attention
+
+def _attend(q, cache, ids, nt, fmt, weights=True, lse=True, f32=False, ws=None, scale=None):
+    nq, heads, _ = q.shape
+    out = torch.full(q.shape, float("nan"), dtype=torch.float32 if f32 else DT[fmt], device="cuda")
+    ls = torch.full((nq, heads), float("nan"), device="cuda") if lse else None
+    w = torch.full((nq, cache.shape[0], ids.shape[1]), float("nan"), device="cuda") if weights else None
+    d_ids = ids if isinstance(ids, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(ids)).cuda()
+    d_nt = nt if isinstance(nt, torch.Tensor) else torch.from_numpy(np.asarray(nt, dtype=np.int32)).cuda()
+    qsa.select_attention_qcache(q, cache, d_ids, d_nt, out, ls, w, scale=scale, ws=ws)
+    return [None if t is None else t.double().cpu().numpy() for t in (out, ls, w)]
+
+
+CASES = [
+    # nq, kv, group, blocks, tokens (None: ragged), k, valid (None: k)
+    (1, 1, 16, 1, 1, 1, None),            # one token
+    (1, 1, 1, 2, 65, 2, None),            # one head, a tail block of one token
+    (2, 1, 16, 3, 129, 3, None),          # an odd number of blocks
+    (3, 2, 8, 40, 2560, 32, None),
+    (5, 3, 7, 33, None, 17, None),
+    (1, 4, 16, 70, 4477, 64, None),       # one query, the largest selection
+    (9, 2, 16, 70, None, 64, "random"),
+    (16, 1, 4, 24, None, 7, "random"),    # rows that select nothing among them
+    (80, 4, 16, 48, None, 32, None),      # more units than fit at once
+    (61, 8, 5, 20, None, 17, "random"),
+    (200, 4, 16, 12, None, 4, None),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("case", CASES, ids=[f"nq{c[0]}-kv{c[1]}x{c[2]}-k{c[5]}" for c in CASES])
+def test_attention_matches_the_oracle(case, fmt):
+    nq, kv, group, blocks, tokens, k, valid = case
+    rng = np.random.default_rng(nq * 100 + k)
+    nt = np.full(nq, tokens) if tokens else rng.integers(1, blocks * 64 + 1, size=nq)
+    if valid == "random":
+        valid = rng.integers(0, k + 1, size=nq)
+        valid[nq // 2] = 0
+    ids = random_ids(nq + k, nq, k, nt, valid)
+    host = random_cache(nq + blocks, kv, blocks, fmt)
+    cache = torch.from_numpy(host).cuda()
+    q, qd = to16(rng.normal(size=(nq, kv * group, 128)) * 1.5, fmt)
+    scale = float(np.float32(128 ** -0.5))
+    want = oq.attention(qd, host, ids, nt, scale, fmt)
+    ws = _ws()
+    check_attention(_attend(q, cache, ids, nt, fmt, ws=ws), want, fmt)
+    check_attention(_attend(q, cache, ids, nt, fmt, f32=True, ws=ws), want, fmt, out_f32=True)
+    assert qsa.read_flags(ws) == 0
+    none = (ids < 0).all(1)
+    got = _attend(q, cache, ids, nt, fmt)
+    assert not got[0][none].any() and np.isneginf(got[1][none]).all() and not got[2][none].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_same_values_with_and_without_the_optional_outputs(fmt):
+    host = random_cache(1, 2, 20, fmt)
+    cache = torch.from_numpy(host).cuda()
+    q, _ = to16(np.random.default_rng(2).normal(size=(7, 32, 128)), fmt)
+    nt = np.full(7, 1280)
+    ids = random_ids(3, 7, 12, nt)
+    full = _attend(q, cache, ids, nt, fmt, ws=_ws())
+    for w in (True, False):
+        for l in (True, False):
+            got = _attend(q, cache, ids, nt, fmt, weights=w, lse=l)
+            np.testing.assert_array_equal(got[0], full[0])
+            for a, b in zip(got[1:], full[1:]):
+                assert a is None or np.array_equal(a, b)
+    again = _attend(q, cache, ids, nt, fmt)
+    for a, b in zip(again, full):
+        np.testing.assert_array_equal(a, b)   # run to run
+
+
+def test_attention_takes_slices_of_a_projection():
+    fmt = oq.BF16
+    cache = torch.from_numpy(random_cache(4, 2, 10, fmt)).cuda()
+    x, _ = to16(np.random.default_rng(5).normal(size=(6, 40, 128)), fmt)
+    nt = np.full(6, 640)
+    ids = random_ids(6, 6, 5, nt)
+    for view in (x[:, 4:36], x[:, :32].flip(0).flip(0), x[::2, 8:24], x.transpose(0, 1)[:6, :4]):
+        got = _attend(view, cache, ids[:view.shape[0]], nt[:view.shape[0]], fmt)
+        want = _attend(view.contiguous(), cache, ids[:view.shape[0]], nt[:view.shape[0]], fmt)
+        for a, b in zip(got, want):
+            np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_unsorted_repeated_and_bad_ids(fmt):
+    rng = np.random.default_rng(7)
+    nq, kv, k, blocks = 6, 2, 24, 30
+    nt = rng.integers(700, blocks * 64 + 1, size=nq)
+    ids = random_ids(8, nq, k, nt, np.full(nq, 10))
+    for i in range(nq):
+        nb = (nt[i] + 63) // 64
+        row = ids[i]
+        row[10:15] = [row[0], row[0], nb, blocks + 3, -9]       # repeats, past the context, past the cache, negative
+        if i == 0:
+            row[15] = np.iinfo(np.int32).max
+        ids[i] = rng.permutation(row)
+    host = random_cache(9, kv, blocks, fmt)
+    q, qd = to16(rng.normal(size=(nq, kv * 16, 128)), fmt)
+    ws = _ws()
+    got = _attend(q, torch.from_numpy(host).cuda(), ids, nt, fmt, ws=ws)
+    check_attention(got, oq.attention(qd, host, ids, nt, float(np.float32(128 ** -0.5)), fmt), fmt)
+    assert qsa.read_flags(ws) == qsa.FLAG_BAD_ID
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_ignores_what_lies_past_the_context(fmt):
+    """Codes and pairs of every token past the context filled with ones (NaN pairs): the same bits."""
+    nq, kv, blocks = 4, 2, 12
+    nt = np.array([1, 70, 511, 768 - 37])
+    host = random_cache(10, kv, blocks, fmt)
+    ids = random_ids(11, nq, 6, nt)
+    q, _ = to16(np.random.default_rng(12).normal(size=(nq, kv * 16, 128)), fmt)
+    want = _attend(q, torch.from_numpy(host).cuda(), ids, nt, fmt)
+    for i in range(nq):
+        bad = host.copy()
+        for g in range(kv):
+            for t in range(int(nt[i]), blocks * 64):
+                oq.write_token(bad, g, t, "k", np.full(128, 15), np.nan, np.nan, fmt)
+                oq.write_token(bad, g, t, "v", np.full(128, 15), np.nan, np.nan, fmt)
+        got = _attend(q[i:i + 1], torch.from_numpy(bad).cuda(), ids[i:i + 1], nt[i:i + 1], fmt)
+        clean = _attend(q[i:i + 1], torch.from_numpy(host).cuda(), ids[i:i + 1], nt[i:i + 1], fmt)
+        for a, b, c in zip(got, clean, want):
+            np.testing.assert_array_equal(a, b)
+            assert np.isfinite(a).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_clamps_the_context(fmt):
+    host = random_cache(13, 1, 6, fmt)
+    cache = torch.from_numpy(host).cuda()
+    q, _ = to16(np.random.default_rng(14).normal(size=(3, 16, 128)), fmt)
+    ids = np.array([[0, 3, 5], [1, 2, 5], [-1, -1, -1]], dtype=np.int32)
+    ws = _ws()
+    got = _attend(q, cache, ids, [385, 1 << 30, -4], fmt, ws=ws)
+    assert qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+    want = _attend(q, cache, ids, [384, 384, 0], fmt, ws=ws)
+    assert qsa.read_flags(ws) == 0
+    for a, b in zip(got, want):
+        np.testing.assert_array_equal(a, b)
+
+
+def _special(seed, fmt, kind):
+    """(K, V rows, q) of one KV head whose logits or scales move in an unusual way over the blocks."""
+    rng = np.random.default_rng(seed)
+    n = 20 * 64
+    k, v, q = rng.normal(size=(n, 1, 128)), rng.normal(size=(n, 1, 128)), rng.normal(size=(2, 16, 128))
+    t = np.arange(n)[:, None, None]
+    if kind == "rising":            # the running maximum grows in every block
+        k = k * 0.2 + q[0, 3] * (t // 64) * 0.4
+    elif kind == "falling":
+        k = k * 0.2 + q[0, 3] * (20 - t // 64) * 0.4
+    elif kind == "one":             # one token takes all the weight
+        k[777] = 4 * q[0, 5]
+    elif kind == "v growing":       # V's scale grows by 2^20 over the blocks
+        v = v * np.exp2((t // 64 - 10.0) if fmt == oq.BF16 else (t // 64) * 0.5 - 5)
+    elif kind == "v mixed":
+        v = v * np.exp2(rng.integers(-8, 9, size=(n, 1, 1)).astype(float))
+    elif kind == "v constant":      # scale 0: every row's values are its minimum
+        v = np.broadcast_to(rng.normal(size=(n, 1, 1)), v.shape).copy()
+    elif kind == "k constant":
+        k = np.broadcast_to(rng.normal(size=(n, 1, 1)), k.shape).copy()
+    elif kind == "zero queries":
+        q[:, ::2] = 0
+    elif kind == "unlike heads":    # query heads of very different sizes
+        q = q * np.exp2(np.arange(16) - 12.0)[None, :, None]
+    elif kind == "unlike dims":     # each head's dimensions over 2^12
+        q = q * np.exp2(-(np.arange(128) % 13))[None, None]
+    elif kind == "v offset":
+        v = v * 0.05 + 30
+    elif kind == "flat":            # equal logits
+        k = np.zeros_like(k) + rng.normal(size=128)
+    return k, v, q
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("kind", ["rising", "falling", "one", "v growing", "v mixed", "v constant", "k constant",
+                                  "zero queries", "unlike heads", "unlike dims", "v offset", "flat"])
+def test_attention_on_unusual_values(kind, fmt):
+    k, v, q = _special(40, fmt, kind)
+    n = k.shape[0] - 13
+    kt, kd = to16(k[:n], fmt)
+    vt, vd = to16(v[:n], fmt)
+    cache = qsa.alloc_qcache(1, 20 * 64)
+    qsa.qcache_append(kt, vt, cache, 0)
+    host = cache.cpu().numpy()
+    qt, qd = to16(q, fmt)
+    nt = np.array([n, n - 100])
+    for kk in (3, 19):
+        ids = np.stack([np.sort(np.random.default_rng(kk).permutation(18)[:kk])] * 2).astype(np.int32)
+        ids[0, -1] = 19
+        want = oq.attention(qd, host, ids, nt, float(np.float32(128 ** -0.5)), fmt)
+        check_attention(_attend(qt, cache, ids, nt, fmt), want, fmt)
+        check_attention(_attend(qt, cache, ids, nt, fmt, f32=True), want, fmt, out_f32=True)
+
+
+def test_attention_other_scales():
+    fmt = oq.BF16
+    host = random_cache(15, 1, 9, fmt)
+    q, qd = to16(np.random.default_rng(16).normal(size=(2, 16, 128)), fmt)
+    nt = np.full(2, 570)
+    ids = random_ids(17, 2, 9, nt)
+    for scale in (1e-3, 0.5, 2.0):
+        s = float(np.float32(scale))
+        check_attention(_attend(q, torch.from_numpy(host).cuda(), ids, nt, fmt, scale=s),
+                        oq.attention(qd, host, ids, nt, s, fmt), fmt)
+
+
+def test_attention_nan_rows_and_queries_reach_only_their_own_outputs():
+    fmt = oq.BF16
+    k, v, q = _special(41, fmt, "plain")
+    k[100, 0, 5], v[500, 0, 7], q[1, 4, 0] = np.nan, np.inf, np.inf
+    kt, _ = to16(k, fmt)
+    vt, _ = to16(v, fmt)
+    qt, _ = to16(q, fmt)
+    cache = qsa.alloc_qcache(1, 20 * 64)
+    qsa.qcache_append(kt, vt, cache, 0)
+    out, lse, w = _attend(qt, cache, np.array([[0, 2, 3], [4, 5, 6]], dtype=np.int32), [1280, 1280], fmt)
+    assert np.isfinite(out[0]).all() and np.isfinite(lse[0]).all() and np.isfinite(w[0]).all()
+    heads = np.arange(16) != 4
+    assert np.isnan(out[1, 4]).all() and np.isfinite(out[1, heads]).all() and np.isfinite(lse[1, heads]).all()
+    out, lse, w = _attend(qt, cache, np.array([[0, 1, 3], [4, 5, 7]], dtype=np.int32), [1280, 1280], fmt)
+    assert np.isnan(out[0]).all() and np.isnan(lse[0]).all()           # block 1 holds the NaN key
+    assert np.isnan(out[1, heads]).all() and np.isfinite(lse[1, heads]).all()   # block 7 the infinite value
+
+
+def test_attention_past_four_gigabytes():
+    """Records at offsets past 2^32 bytes, written and attended over where they lie."""
+    fmt = oq.BF16
+    blocks = 300_000
+    cache = qsa.alloc_qcache(2, 64 * blocks)
+    assert cache.numel() > 1 << 32
+    at = [7, 246_000, 299_999]
+    for i, b in enumerate(at):
+        k, _ = to16(_rows(50 + i, 64, 2), fmt)
+        v, _ = to16(_rows(60 + i, 64, 2), fmt)
+        qsa.qcache_append(k, v, cache, 64 * b)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        qsa.qcache_load(cache, ko, vo, 64 * b)
+        assert float((ko - k).abs().max()) < 2.0
+    small = cache[:, at].contiguous()
+    q, qd = to16(np.random.default_rng(18).normal(size=(2, 32, 128)), fmt)
+    ids = np.array([at, at], dtype=np.int32)
+    got = _attend(q, cache, ids, [64 * blocks, 64 * blocks - 5], fmt)
+    near = np.array([[0, 1, 2]] * 2, dtype=np.int32)
+    want = _attend(q, small, near, [192, 187], fmt)
+    for a, b in zip(got, want):
+        np.testing.assert_array_equal(a, b)
+    check_attention(got, oq.attention(qd, small.cpu().numpy(), near, np.array([192, 187]), float(np.float32(128 ** -0.5)), fmt),
+                    fmt)
+
+
+def test_attention_on_a_side_stream_and_in_a_graph():
+    fmt = oq.F16
+    host = random_cache(19, 4, 40, fmt)
+    cache = torch.from_numpy(host).cuda()
+    q, _ = to16(np.random.default_rng(20).normal(size=(3, 64, 128)), fmt)
+    nt = np.full(3, 2500)
+    ids = random_ids(21, 3, 32, nt)
+    want = _attend(q, cache, ids, nt, fmt)
+    side = torch.cuda.Stream()
+    d_ids, d_nt = torch.from_numpy(ids).cuda(), torch.from_numpy(nt.astype(np.int32)).cuda()
+    out, lse = torch.empty_like(q), torch.empty(3, 64, device="cuda")
+    w = torch.empty(3, 4, 32, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        qsa.select_attention_qcache(q, cache, d_ids, d_nt, out, lse, w)
+    side.synchronize()
+    np.testing.assert_array_equal(out.double().cpu().numpy(), want[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qsa.select_attention_qcache(q, cache, d_ids, d_nt, out, lse, w)
+    for seed in (22, 23):
+        nq, _ = to16(np.random.default_rng(seed).normal(size=(3, 64, 128)), fmt)
+        q.copy_(nq)
+        out.zero_()
+        graph.replay()
+        for a, b in zip((out, lse, w), _attend(q, cache, ids, nt, fmt)):
+            np.testing.assert_array_equal(a.double().cpu().numpy(), b)
+
+
+def test_two_streams_at_once():
+    """Calls without a workspace share nothing: two streams, interleaved, each its own result."""
+    fmt = oq.BF16
+    cache = torch.from_numpy(random_cache(24, 4, 60, fmt)).cuda()
+    nt = torch.full((40,), 3840, dtype=torch.int32, device="cuda")
+    sets = []
+    for seed in (25, 26):
+        q, _ = to16(np.random.default_rng(seed).normal(size=(40, 64, 128)), fmt)
+        ids = torch.from_numpy(random_ids(seed, 40, 32, np.full(40, 3840))).cuda()
+        sets.append((q, ids, _attend(q, cache, ids, nt, fmt)))
+    outs = [[(torch.empty_like(q), torch.empty(40, 64, device="cuda"), torch.empty(40, 4, 32, device="cuda"))
+             for _ in range(6)] for q, _, _ in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for s, (q, ids, _), o in zip(streams, sets, outs):
+            with torch.cuda.stream(s):
+                qsa.select_attention_qcache(q, cache, ids, nt, *o[i])
+    torch.cuda.synchronize()
+    for (_, _, want), o in zip(sets, outs):
+        for got in o:
+            for a, b in zip(got, want):
+                np.testing.assert_array_equal(a.double().cpu().numpy(), b)
