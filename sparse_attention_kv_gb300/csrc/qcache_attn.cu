@@ -49,16 +49,16 @@ namespace qsa {
 namespace {
 
 constexpr int kG = 16;                    // head columns of a unit (heads past the group are zeros)
+constexpr int kH = 8;                     // heads of a thread: two warpgroups share the 16
 constexpr int kSel = QSA_ATTN_MAX_K;
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kStages = 2;
 constexpr int kStageBytes = 2 * kQRec;
 constexpr int kMaxSplit = 8;
 constexpr float kTop = 4.0f;              // log2 of the largest weight when the references are set
 constexpr float kMostWeight = 256.0f;     // a weight above this moves them (e4m3 holds 448)
 constexpr float kMostY = 30.0f;           // and a y above this
-
-constexpr int kTileRows(int terms) { return kG * terms; }   // rows of 128 bytes of an operand B tile
+constexpr float kFaint = 0x1p-60f;        // V scales whose weights never reach kMostWeight before p overflows
 
 struct QCtrl {
     uint64_t full[kStages];
@@ -70,21 +70,24 @@ struct QCtrl {
     int32_t slot[kSel];                   // and the slots they came from
     alignas(16) float f[kG];              // scale log2(e) 2^9 / (the head's power-of-two scaling of q)
     alignas(16) float qs[kG];             // scale log2(e) sum(q)
-    alignas(16) float m[kG];              // reference of the exponents (log2 units)
+    alignas(16) float nm[kG];             // minus the reference of the exponents (log2 units)
     alignas(16) float g[kG];              // power of two of the weights
+    alignas(16) float fl[kG];             // rescaling of the sums and of the outputs
+    alignas(16) float fo[kG];
     float top[kG], eg[kG];                // largest log2(p vs) + m seen, log2(g)
-    float fl[kG], fo[kG];                 // rescaling of the sums and of the outputs
-    uint32_t red[2][4][kG];
-    float l[kG], mv[kG];
+    float least_g;
+    uint32_t red[3][4][kG];
+    float sum[3][kG];                     // l, sum of p vm, 16 x what the weights' rounding took away
     float2 ml[kMaxSplit][kG];             // (m, l) of every CTA of a cluster
     float w[kSel][kG];                    // sums of p over a slot's tokens
 };
 
 template <int TERMS>
 struct QLayout {
-    static constexpr int kOffQ = 0;                                   // 1024-byte aligned
-    static constexpr int kOffP = kOffQ + kTileRows(TERMS) * 128;
-    static constexpr int kOffRing = kOffP + kTileRows(TERMS) * 128;
+    static constexpr int kOffQ = 0;                              // heads x terms rows of 128 bytes, swizzled
+    static constexpr int kOffP = kOffQ + kG * TERMS * 128;       // per term [128 tokens][16 heads]
+    static constexpr int kTermP = 128 * kG;
+    static constexpr int kOffRing = kOffP + TERMS * kTermP;
     static constexpr int kOffCtrl = kOffRing + kStages * kStageBytes;
     static constexpr int kBytes = kOffCtrl + (int)sizeof(QCtrl) + 1024;   // + alignment slack
     // tensor memory: S, O, the unpacked K tile and the unpacked V tile (fp16: one region for both)
@@ -94,7 +97,6 @@ struct QLayout {
     static constexpr uint32_t kColV = 96;
     static constexpr uint32_t kCols = 128;
 };
-static_assert(QLayout<2>::kOffP % 1024 == 0 && QLayout<3>::kOffP % 1024 == 0, "swizzle atoms");
 // four CTAs (and 1 KB each that the system keeps) in an SM's 228 KB
 static_assert(4 * (QLayout<3>::kBytes + 1024) <= 228 * 1024, "four CTAs per SM");
 // the combine's buffers fit the ring: outputs sent and received, 16 heads x 128 fp32 each
@@ -163,6 +165,16 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t h2_max(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -172,18 +184,22 @@ __device__ __forceinline__ float h2_lo(uint32_t h) { return __half2float(__ushor
 __device__ __forceinline__ float h2_hi(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)(h >> 16))); }
 constexpr uint32_t kH16 = 0x4C004C00u, kHNeg16 = 0xCC00CC00u;   // (16, 16) and (-16, -16)
 
-// The e4m3 terms of two values: v = t0 + t1 / 16 + t2 / 256, |v| <= 448.
+// The e4m3 terms of two values, |v| <= 448: v = t0 + t1 / 16 + t2 / 256 + what is left.  Two terms: from
+// the fp16 pair h = (a, b), whose 11 bits are more than theirs; returns 16 x what is left (exact).
 template <int TERMS>
-__device__ __forceinline__ void split_terms(float a, float b, uint32_t h, uint16_t (&t)[TERMS]) {
-    if constexpr (TERMS == 2) {   // from the fp16 pair h = (a, b): its 11 bits are more than the terms'
+__device__ __forceinline__ uint32_t split_terms(float a, float b, uint32_t h, uint16_t (&t)[TERMS]) {
+    if constexpr (TERMS == 2) {
         t[0] = h2_to_e4m3(h);
-        t[1] = h2_to_e4m3(h2_fma(e4m3_to_h2(t[0]), kHNeg16, h2_mul(h, kH16)));
-    } else {                      // the first remainder in fp32; it fits fp16 with bits to spare
+        const uint32_t r = h2_fma(e4m3_to_h2(t[0]), kHNeg16, h2_mul(h, kH16));
+        t[1] = h2_to_e4m3(r);
+        return h2_sub(r, e4m3_to_h2(t[1]));
+    } else {   // the first remainder in fp32; it fits fp16 with bits to spare
         t[0] = f2_to_e4m3(a, b);
         const uint32_t h0 = e4m3_to_h2(t[0]);
         const uint32_t r = to_h2((a - h2_lo(h0)) * 16.0f, (b - h2_hi(h0)) * 16.0f);
         t[1] = h2_to_e4m3(r);
         t[2] = h2_to_e4m3(h2_fma(e4m3_to_h2(t[1]), kHNeg16, h2_mul(r, kH16)));
+        return 0u;
     }
 }
 
@@ -209,28 +225,24 @@ __device__ __forceinline__ void st_cluster(float2 *local, int rank, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(local, rank)), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Sums of 16 values over the warp's 32 lanes in 16 shuffles: each step halves the values a lane
-// holds.  Lanes 2h and 2h + 1 return the sum of value h.
-__device__ __forceinline__ float warp_sum16(const float (&x)[kG], int lane) {
-    float a[8], b[4], c[2];
+// Sums of 8 values over the warp's 32 lanes in 9 shuffles: the first three steps halve the values
+// a lane holds.  Lanes 4h .. 4h + 3 return the sum of value h.
+__device__ __forceinline__ float warp_sum8(const float (&x)[kH], int lane) {
+    float a[4], b[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float send = (lane & 16) ? x[i] : x[8 + i], keep = (lane & 16) ? x[8 + i] : x[i];
+    for (int i = 0; i < 4; ++i) {
+        const float send = (lane & 16) ? x[i] : x[4 + i], keep = (lane & 16) ? x[4 + i] : x[i];
         a[i] = keep + __shfl_xor_sync(kFull, send, 16);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float send = (lane & 8) ? a[i] : a[4 + i], keep = (lane & 8) ? a[4 + i] : a[i];
+    for (int i = 0; i < 2; ++i) {
+        const float send = (lane & 8) ? a[i] : a[2 + i], keep = (lane & 8) ? a[2 + i] : a[i];
         b[i] = keep + __shfl_xor_sync(kFull, send, 8);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float send = (lane & 4) ? b[i] : b[2 + i], keep = (lane & 4) ? b[2 + i] : b[i];
-        c[i] = keep + __shfl_xor_sync(kFull, send, 4);
-    }
-    const float send = (lane & 2) ? c[0] : c[1], keep = (lane & 2) ? c[1] : c[0];
-    const float d = keep + __shfl_xor_sync(kFull, send, 2);
-    return d + __shfl_xor_sync(kFull, d, 1);
+    const float send = (lane & 4) ? b[0] : b[1], keep = (lane & 4) ? b[1] : b[0];
+    float c = keep + __shfl_xor_sync(kFull, send, 4);
+    c += __shfl_xor_sync(kFull, c, 2);
+    return c + __shfl_xor_sync(kFull, c, 1);
 }
 
 // Every thread waits; the warp is converged behind it (the tcgen05 loads and stores need that).
@@ -322,43 +334,39 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             if (lane + 32 < a.k && !take1) w[lane + 32] = 0.0f;
         }
     }
-    {   // the group's queries: eight threads per head, 16 dimensions each
-        const int h = tid >> 3, part = tid & 7;
-        float x[16];
+    {   // the group's queries: sixteen threads per head, 8 dimensions each
+        const int h = tid >> 4, part = tid & 15;
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
         if (h < group) {
-            const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.qa) + qi * a.q_stride +
-                                                               (int64_t)(g * group + h) * a.q_head_stride + part * 16);
-            const uint4 u[2] = {row[0], row[1]};
+            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.qa) + qi * a.q_stride +
+                                                             (int64_t)(g * group + h) * a.q_head_stride + part * 8);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[8 * i + 2 * j] = QFmt<F16>::lo(w[j]);
-                    x[8 * i + 2 * j + 1] = QFmt<F16>::hi(w[j]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = QFmt<F16>::lo(w[j]);
+                x[2 * j + 1] = QFmt<F16>::hi(w[j]);
             }
         }
         uint32_t big = 0u;   // the bits of the largest magnitude (an infinity or a NaN stays the largest)
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
             sum += x[i];
         }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
+        for (int o = 1; o < 16; o <<= 1) {
             big = max(big, __shfl_xor_sync(kFull, big, o));
             sum += __shfl_xor_sync(kFull, sum, o);
         }
         const bool finite = big < 0x7F800000u;
         // a power of two that puts the largest magnitude into [128, 256)
         const int e = finite && big != 0u ? 7 - ilogbf(__uint_as_float(big)) : 0;
-        uint32_t out[TERMS][4];
+        uint32_t out[TERMS][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float v0 = finite ? scalbnf(x[2 * i], e) : 0.0f, v1 = finite ? scalbnf(x[2 * i + 1], e) : 0.0f;
             uint16_t t[TERMS];
             split_terms<TERMS>(v0, v1, to_h2(v0, v1), t);
@@ -370,12 +378,12 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
         }
 #pragma unroll
         for (int u = 0; u < TERMS; ++u)
-            *reinterpret_cast<uint4 *>(sQ + (u * kG + h) * 128 + ((part ^ (h & 7)) << 4)) =
-                make_uint4(out[u][0], out[u][1], out[u][2], out[u][3]);
+            *reinterpret_cast<uint2 *>(sQ + (u * kG + h) * 128 + (((part >> 1) ^ (h & 7)) << 4) + (part & 1) * 8) =
+                make_uint2(out[u][0], out[u][1]);
         if (part == 0) {
             ct.f[h] = finite ? scalbnf(p.scale_log2, 9 - e) : __uint_as_float(0x7FC00000u);
             ct.qs[h] = p.scale_log2 * sum;
-            ct.m[h] = 0.0f;
+            ct.nm[h] = 0.0f;
             ct.top[h] = -INFINITY;
         }
     }
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ct.tmem_base;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int nsel = ct.nsel, ntok = ct.ntok;
     // this CTA's tiles: all of them, or a slice of a cluster's split
     const int T = (nsel + 1) >> 1;
@@ -403,35 +411,58 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     if (tid == 0)
         for (int i = 0; i < kStages && i < tl; ++i) fetch(i);
 
+    // Two warpgroups: both hold every token of a tile (and every dimension of O), one head half each.
+    // The first unpacks K, the second V.
     const uint32_t id = idesc(0, 128, L::kN);
-    const int half = tid >> 6, tok = tid & 63;
-    f32x2 l[kG / 2], mv[kG / 2];
+    const int wg = tid >> 7, row = tid & 127, half = row >> 6, tok = row & 63;
+    const int h0 = wg * kH;
+    f32x2 l[kH / 2], mv[kH / 2];
+    uint32_t left[kH / 2];                // fp16 pairs: 16 x what the rounding of this token's weights left
 #pragma unroll
-    for (int h = 0; h < kG / 2; ++h) l[h] = mv[h] = 0ull;
-    float e[kG];
+    for (int h = 0; h < kH / 2; ++h) {
+        l[h] = mv[h] = 0ull;
+        left[h] = 0u;
+    }
+    float e[kH];
 
     for (int i = 0; i < tl; ++i) {
         const int s = i % kStages;
         const uint8_t *st = ring + s * kStageBytes;
-        if (TERMS == 3 && i > 0) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // V(i - 1) is read
+        if (i > 0 && (TERMS == 3 || wg == 1)) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // V(i - 1) is read
         wait_all(&ct.full[s], (uint32_t)(i / kStages) & 1u, abort_flag);
-        // ---- K: this thread's token, 128 codes into 32 columns
         const uint8_t *rec = st + half * kQRec;
-        {
-            uint32_t lo[16], hi[16];
+        // 16 bytes of codes to 4 + 4 columns of a row of A
+        uint32_t lo[8], hi[8];
+        auto unpack = [&](const uint8_t *src, int at) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(src);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(rec + c * 1024 + tok * 16);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    lo[4 * c + j] = w[j] & 0x0F0F0F0Fu;
-                    hi[4 * c + j] = (w[j] >> 4) & 0x0F0F0F0Fu;
-                }
+            for (int j = 0; j < 4; ++j) {
+                lo[at + j] = w[j] & 0x0F0F0F0Fu;
+                hi[at + j] = (w[j] >> 4) & 0x0F0F0F0Fu;
             }
-            tc_fence_after();
-            tmem_st16(tmem + lanes + L::kColK, lo);
-            tmem_st16(tmem + lanes + L::kColK + 16, hi);
+        };
+        auto unpack_v = [&]() {           // this thread's dimension, the tokens of the two blocks
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint8_t *src = st + b * kQRec + kQOffV + row * 16;
+                unpack(src, 0);
+                unpack(src + 2048, 4);
+                tmem_st8(tmem + lanes + L::kColV + b * 16, lo);
+                tmem_st8(tmem + lanes + L::kColV + b * 16 + 8, hi);
+            }
+        };
+        tc_fence_after();
+        if (wg == 0) {                    // this thread's token, its 128 dimensions
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                unpack(rec + (2 * c) * 1024 + tok * 16, 0);
+                unpack(rec + (2 * c + 1) * 1024 + tok * 16, 4);
+                tmem_st8(tmem + lanes + L::kColK + c * 8, lo);
+                tmem_st8(tmem + lanes + L::kColK + 16 + c * 8, hi);
+            }
+        } else if (TERMS == 2) {
+            unpack_v();
         }
         const bool vis = 2 * i + half < nloc && ct.sel[b0 + min(2 * i + half, nloc - 1)] * kQBlockTok + tok < ntok;
         const uint32_t kp = vis ? *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + tok * 4) : 0u;
@@ -447,55 +478,41 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             mma_commit(&ct.sbar);
         }
         __syncwarp();
-        // ---- V: this thread's dimension, 128 tokens of the two blocks
-        if (TERMS == 2 && i > 0) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // V(i - 1), P(i - 1) are read
-        if (TERMS == 3) wait_all(&ct.sbar, (uint32_t)i & 1u, abort_flag);                  // K(i) is read
-        {
-            uint32_t x[2][16];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint4 y = *reinterpret_cast<const uint4 *>(st + b * kQRec + kQOffV + c * 2048 + tid * 16);
-                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        x[b][4 * c + j] = w[j] & 0x0F0F0F0Fu;
-                        x[b][8 + 4 * c + j] = (w[j] >> 4) & 0x0F0F0F0Fu;
-                    }
-                }
-            tc_fence_after();
-            tmem_st16(tmem + lanes + L::kColV, x[0]);
-            tmem_st16(tmem + lanes + L::kColV + 16, x[1]);
-        }
         const float ks = QFmt<F16>::lo(kp), km = QFmt<F16>::hi(kp);
         const float vs = QFmt<F16>::lo(vp), vm = QFmt<F16>::hi(vp);
         const bool all_vis = __all_sync(kFull, vis);
-        if (TERMS == 2) wait_all(&ct.sbar, (uint32_t)i & 1u, abort_flag);
+        wait_all(&ct.sbar, (uint32_t)i & 1u, abort_flag);                 // S(i) is complete, K(i) read
+        if (wg == 0 && i > 0 && TERMS == 2) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // P(i - 1) is read
         tc_fence_after();
+        if (TERMS == 3 && wg == 1) unpack_v();
         // y = log2(e) s - m of this token, into e
         auto logits = [&]() {
-            uint32_t v[TERMS][16];
+            uint32_t v[TERMS][kH];
 #pragma unroll
-            for (int u = 0; u < TERMS; ++u) tmem_ld16_nowait(tmem + lanes + u * 16, v[u]);
+            for (int u = 0; u < TERMS; ++u) tmem_ld8_nowait(tmem + lanes + u * kG + h0, v[u]);
             tmem_wait_ld();
 #pragma unroll
             for (int u = 0; u < TERMS; ++u) reg_fence(v[u]);
             const f32x2 ks2 = pack2(ks, ks), km2 = pack2(km, km);
 #pragma unroll
-            for (int h = 0; h < kG / 2; ++h) {
-                const float2 m = reinterpret_cast<const float2 *>(ct.m)[h];
-                const f32x2 f = reinterpret_cast<const f32x2 *>(ct.f)[h], qs = reinterpret_cast<const f32x2 *>(ct.qs)[h];
-                f32x2 t = pack2(__uint_as_float(v[TERMS - 1][2 * h]), __uint_as_float(v[TERMS - 1][2 * h + 1]));
+            for (int h = 0; h < kH / 2; h += 2) {
+                const ulonglong2 nm = *reinterpret_cast<const ulonglong2 *>(ct.nm + h0 + 2 * h);
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(ct.f + h0 + 2 * h);
+                const ulonglong2 qs = *reinterpret_cast<const ulonglong2 *>(ct.qs + h0 + 2 * h);
 #pragma unroll
-                for (int u = TERMS - 2; u >= 0; --u)
-                    t = fma2(t, pack2(0.0625f, 0.0625f), pack2(__uint_as_float(v[u][2 * h]), __uint_as_float(v[u][2 * h + 1])));
-                t = fma2(mul2(t, f), ks2, fma2(km2, qs, pack2(-m.x, -m.y)));
-                unpack2(t, e[2 * h], e[2 * h + 1]);
+                for (int j = 0; j < 2; ++j) {
+                    const int x = 2 * (h + j);
+                    f32x2 t = pack2(__uint_as_float(v[TERMS - 1][x]), __uint_as_float(v[TERMS - 1][x + 1]));
+#pragma unroll
+                    for (int u = TERMS - 2; u >= 0; --u)
+                        t = fma2(t, pack2(0.0625f, 0.0625f), pack2(__uint_as_float(v[u][x]), __uint_as_float(v[u][x + 1])));
+                    t = fma2(mul2(t, j ? f.y : f.x), ks2, fma2(km2, j ? qs.y : qs.x, j ? nm.y : nm.x));
+                    unpack2(t, e[x], e[x + 1]);
+                }
             }
             if (!all_vis)
 #pragma unroll
-                for (int h = 0; h < kG; ++h) e[h] = vis ? e[h] : -INFINITY;
+                for (int h = 0; h < kH; ++h) e[h] = vis ? e[h] : -INFINITY;
         };
         bool renew = i == 0;
         while (true) {
@@ -505,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                 const float lv = vs == 0.0f ? -INFINITY : lg2(vs);
                 uint32_t mine[2] = {0u, 0u};
 #pragma unroll
-                for (int h = 0; h < kG; ++h) {
+                for (int h = 0; h < kH; ++h) {
                     const uint32_t y = __reduce_max_sync(kFull, score_key(e[h]));
                     const uint32_t r = __reduce_max_sync(kFull, score_key(e[h] + lv));
                     if (lane == h) {
@@ -513,128 +530,152 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                         mine[1] = r;
                     }
                 }
-                if (lane < kG) {
-                    ct.red[0][warp][lane] = mine[0];
-                    ct.red[1][warp][lane] = mine[1];
+                if (lane < kH) {
+                    ct.red[0][warp & 3][h0 + lane] = mine[0];
+                    ct.red[1][warp & 3][h0 + lane] = mine[1];
                 }
                 __syncthreads();
-                if (tid < kG) {
+                if (warp == 0) {
+                    const int h = lane & 15;
                     uint32_t y = 0u, r = 0u;
                     for (int w = 0; w < 4; ++w) {
-                        y = max(y, ct.red[0][w][tid]);
-                        r = max(r, ct.red[1][w][tid]);
+                        y = max(y, ct.red[0][w][h]);
+                        r = max(r, ct.red[1][w][h]);
                     }
-                    const float m0 = ct.m[tid], rise = key_float(y);
+                    const float m0 = -ct.nm[h], rise = key_float(y);
                     const float m1 = i == 0 ? rise : m0 + fmaxf(rise, 0.0f);
-                    const float top = fmaxf(ct.top[tid], m0 + key_float(r));
+                    const float top = fmaxf(ct.top[h], m0 + key_float(r));
                     // nothing but zero scales so far: any other one will pass the limit
                     const float eg = top == -INFINITY ? 60.0f : fminf(fmaxf(kTop - ceilf(top - m1), -126.0f), 126.0f);
                     const float fl = i == 0 ? 1.0f : exp2f(m0 - m1);
-                    ct.fl[tid] = fl;
-                    ct.fo[tid] = i == 0 ? 1.0f : fl * exp2f(fminf(fmaxf(eg - ct.eg[tid], -126.0f), 126.0f));
-                    ct.m[tid] = m1;
-                    ct.top[tid] = top;
-                    ct.eg[tid] = eg;
-                    ct.g[tid] = exp2f(eg);
+                    const float fo = i == 0 ? 1.0f : fl * exp2f(fminf(fmaxf(eg - ct.eg[h], -126.0f), 126.0f));
+                    float least = eg;
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, o));
+                    __syncwarp();
+                    if (lane < kG) {
+                        ct.fl[h] = fl;
+                        ct.fo[h] = fo;
+                        ct.nm[h] = -m1;
+                        ct.top[h] = top;
+                        ct.eg[h] = eg;
+                        ct.g[h] = exp2f(eg);
+                        if (lane == 0) ct.least_g = exp2f(least);
+                    }
                 }
                 __syncthreads();
                 if (i > 0) {   // what is summed so far, to the new references (O(i - 1) is complete)
 #pragma unroll
-                    for (int h = 0; h < kG / 2; ++h) {
-                        const f32x2 fl = reinterpret_cast<const f32x2 *>(ct.fl)[h];
+                    for (int h = 0; h < kH / 2; ++h) {
+                        const f32x2 fl = reinterpret_cast<const f32x2 *>(ct.fl + h0)[h];
+                        const float2 fo = reinterpret_cast<const float2 *>(ct.fo + h0)[h];
                         l[h] = mul2(l[h], fl);
                         mv[h] = mul2(mv[h], fl);
+                        if (TERMS == 2) left[h] = to_h2(h2_lo(left[h]) * fo.x, h2_hi(left[h]) * fo.y);
                     }
                     if (W)
                         for (int j = tid; j < 2 * i * kG; j += kThreads) (&ct.w[0][0])[j] *= ct.fl[j % kG];
-                    uint32_t o[16];
+                    uint32_t o[kH];
 #pragma unroll
                     for (int u = 0; u < TERMS; ++u) {
-                        tmem_ld16_nowait(tmem + lanes + L::kColO + u * 16, o);
+                        tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o);
                         tmem_wait_ld();
                         reg_fence(o);
 #pragma unroll
-                        for (int h = 0; h < kG; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * ct.fo[h]);
-                        tmem_st16(tmem + lanes + L::kColO + u * 16, o);
+                        for (int h = 0; h < kH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * ct.fo[h0 + h]);
+                        tmem_st8(tmem + lanes + L::kColO + u * kG + h0, o);
                     }
                 }
                 logits();
             }
-            // p = 2^y, the weights p vs g in terms to shared memory: row head (+ 16 per term), column token
-            float most = -INFINITY;
+            // p = 2^y, and the weights p vs g in terms to shared memory: [term][token][head]
+            bool over = false;
+            if (__any_sync(kFull, vis && vs * ct.least_g < kFaint)) {   // p may grow where the weights do not
 #pragma unroll
-            for (int h = 0; h < kG; ++h) most = fmaxf(most, e[h]);
-            uint32_t hmax = 0u;
+                for (int h = 0; h < kH; ++h) over |= e[h] > kMostY;
+            }
+            uint32_t hmax = 0u, word[TERMS][2];
+            uint32_t rest[kH / 2];
             const f32x2 vs2 = pack2(vs, vs);
 #pragma unroll
-            for (int h = 0; h < kG / 2; ++h) {
+            for (int h = 0; h < kH / 2; ++h) {
                 e[2 * h] = ex2(e[2 * h]);
                 e[2 * h + 1] = ex2(e[2 * h + 1]);
-                const f32x2 w2 = mul2(mul2(pack2(e[2 * h], e[2 * h + 1]), vs2), reinterpret_cast<const f32x2 *>(ct.g)[h]);
+                const f32x2 w2 = mul2(mul2(pack2(e[2 * h], e[2 * h + 1]), vs2), reinterpret_cast<const f32x2 *>(ct.g + h0)[h]);
                 float w0, w1;
                 unpack2(w2, w0, w1);
                 const uint32_t h2 = to_h2(w0, w1);
                 hmax = h2_max(hmax, h2);
                 uint16_t t[TERMS];
-                split_terms<TERMS>(w0, w1, h2, t);
-                uint8_t *r0 = sP + ((uint32_t)tid ^ (uint32_t)(((2 * h) & 7) << 4)) + (2 * h) * 128;
-                uint8_t *r1 = sP + ((uint32_t)tid ^ (uint32_t)(((2 * h + 1) & 7) << 4)) + (2 * h + 1) * 128;
+                rest[h] = split_terms<TERMS>(w0, w1, h2, t);
 #pragma unroll
                 for (int u = 0; u < TERMS; ++u) {
-                    r0[u * kG * 128] = (uint8_t)t[u];
-                    r1[u * kG * 128] = (uint8_t)(t[u] >> 8);
+                    if (h & 1) word[u][h >> 1] |= (uint32_t)t[u] << 16;
+                    else word[u][h >> 1] = t[u];
                 }
             }
-            const bool over = !renew && (most > kMostY || h2_lo(hmax) > kMostWeight || h2_hi(hmax) > kMostWeight);
+#pragma unroll
+            for (int u = 0; u < TERMS; ++u)
+                *reinterpret_cast<uint2 *>(sP + u * L::kTermP + row * kG + h0) = make_uint2(word[u][0], word[u][1]);
+            over = !renew && (over || h2_lo(hmax) > kMostWeight || h2_hi(hmax) > kMostWeight);
             fence_proxy_async();   // the weights are read by the tensor core
             tmem_wait_st();
             tc_fence_before();
-            if (!__syncthreads_or(over)) break;
+            if (!__syncthreads_or(over)) {
+                if (TERMS == 2)
+#pragma unroll
+                    for (int h = 0; h < kH / 2; ++h) left[h] = h2_add(left[h], rest[h]);
+                break;
+            }
             renew = true;
         }
-        if (tid == 0) {
+        if (tid == 128) {
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_f8_ta(tmem + L::kColO, tmem + L::kColV + kk * 8, sdesc(smem_u32(sP) + kk * 32), id,
-                          (i | kk) != 0 ? 1u : 0u);
+                mma_f8_ta(tmem + L::kColO, tmem + L::kColV + kk * 8, sdesc_mn(smem_u32(sP) + kk * 32 * kG, 8 * kG, L::kTermP),
+                          id | kIdescBMn, (i | kk) != 0 ? 1u : 0u);
             mma_commit(&ct.obar);
             if (i + kStages < tl) fetch(i + kStages);   // every thread has read this stage
         }
         __syncwarp();
         const f32x2 vm2 = pack2(vm, vm);
 #pragma unroll
-        for (int h = 0; h < kG / 2; ++h) {
+        for (int h = 0; h < kH / 2; ++h) {
             const f32x2 e2 = pack2(e[2 * h], e[2 * h + 1]);
             l[h] = add2(l[h], e2);
             mv[h] = fma2(e2, vm2, mv[h]);
         }
-        if (W) {   // two warps per block: their sum does not depend on which comes first
-            const float w = warp_sum16(e, lane);
-            if ((lane & 1) == 0 && 2 * i + half < nloc) atomicAdd(&ct.w[2 * i + half][lane >> 1], w);
+        if (W) {   // two warps per block and head half: their sum does not depend on which comes first
+            const float w = warp_sum8(e, lane);
+            if ((lane & 3) == 0 && 2 * i + half < nloc) atomicAdd(&ct.w[2 * i + half][h0 + (lane >> 2)], w);
         }
     }
 
     // ---- sums over the token lanes
     {
-        float x[kG];
+        float x[3][kH];
 #pragma unroll
-        for (int h = 0; h < kG / 2; ++h) unpack2(l[h], x[2 * h], x[2 * h + 1]);
-        const float ls = warp_sum16(x, lane);
-#pragma unroll
-        for (int h = 0; h < kG / 2; ++h) unpack2(mv[h], x[2 * h], x[2 * h + 1]);
-        const float ms = warp_sum16(x, lane);
+        for (int h = 0; h < kH / 2; ++h) {
+            unpack2(l[h], x[0][2 * h], x[0][2 * h + 1]);
+            unpack2(mv[h], x[1][2 * h], x[1][2 * h + 1]);
+            x[2][2 * h] = h2_lo(left[h]);
+            x[2][2 * h + 1] = h2_hi(left[h]);
+        }
         __syncthreads();   // every thread has read ct.red
-        if ((lane & 1) == 0) {
-            ct.red[0][warp][lane >> 1] = __float_as_uint(ls);
-            ct.red[1][warp][lane >> 1] = __float_as_uint(ms);
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            if (j == 2 && TERMS == 3) break;
+            const float sum = warp_sum8(x[j], lane);
+            if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = __float_as_uint(sum);
         }
         __syncthreads();
-        if (tid < 2 * kG) {
-            const int which = tid >> 4, h = tid & 15;
+        if (tid < 3 * kG) {
+            const int j = tid / kG, h = tid % kG;
             float sum = 0.0f;
-            for (int w = 0; w < 4; ++w) sum += __uint_as_float(ct.red[which][w][h]);
-            (which ? ct.mv : ct.l)[h] = sum;
+            if (j < 2 || TERMS == 2)
+                for (int w = 0; w < 4; ++w) sum += __uint_as_float(ct.red[j][w][h]);
+            ct.sum[j][h] = sum;
         }
         __syncthreads();
     }
@@ -648,25 +689,27 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     if (tl > 0) {
         wait_all(&ct.obar, (uint32_t)(tl - 1) & 1u, abort_flag);
         tc_fence_after();
-        uint32_t o[TERMS][16];
+        uint32_t o[TERMS][kH];
 #pragma unroll
-        for (int u = 0; u < TERMS; ++u) tmem_ld16_nowait(tmem + lanes + L::kColO + u * 16, o[u]);
+        for (int u = 0; u < TERMS; ++u) tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o[u]);
         tmem_wait_ld();
 #pragma unroll
         for (int u = 0; u < TERMS; ++u) reg_fence(o[u]);
-        // this thread's dimension of every head (a warp's stores for one head are 32 neighbours)
+        // this thread's dimension of its heads (a warp's stores for one head are 32 neighbours).  The codes'
+        // mean, 7.5, times what the rounding left of the weights takes most of its effect away.
 #pragma unroll
-        for (int h = 0; h < kG; ++h) {
-            float x = __uint_as_float(o[TERMS - 1][h]);
+        for (int j = 0; j < kH; ++j) {
+            const int h = h0 + j;
+            float x = __uint_as_float(o[TERMS - 1][j]);
 #pragma unroll
-            for (int u = TERMS - 2; u >= 0; --u) x = fmaf(x, 0.0625f, __uint_as_float(o[u][h]));
-            x = fmaf(x * 512.0f, exp2f(-ct.eg[h]), ct.mv[h]);
-            if (split > 1) part[h * kQDim + tid] = x;
-            else if (h < group) put(h, tid, x / ct.l[h]);
+            for (int u = TERMS - 2; u >= 0; --u) x = fmaf(x, 0.0625f, __uint_as_float(o[u][j]));
+            x = fmaf(fmaf(x, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), exp2f(-ct.eg[h]), ct.sum[1][h]);
+            if (split > 1) part[h * kQDim + row] = x;
+            else if (h < group) put(h, row, x / ct.sum[0][h]);
         }
         tc_fence_before();
     } else if (split == 1) {   // no visible token: o = 0
-        for (int h = 0; h < group; ++h) put(h, tid, 0.0f);
+        for (int h = h0; h < min(group, h0 + kH); ++h) put(h, row, 0.0f);
     }
     if (tid == 0 && ct.abort) {   // a wait gave up: let what is in flight land before the memory is freed
         for (int i = max(0, tl - kStages); i < tl; ++i) mbar_drain(&ct.full[i % kStages], (uint32_t)(i / kStages) & 1u);
@@ -676,10 +719,10 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     }
     if (split == 1) {
         if (a.lse && tid < group)
-            a.lse[head0 + tid] = tl > 0 ? (ct.m[tid] + log2f(ct.l[tid])) * 0.6931471805599453f : -INFINITY;
+            a.lse[head0 + tid] = tl > 0 ? (log2f(ct.sum[0][tid]) - ct.nm[tid]) * 0.6931471805599453f : -INFINITY;
         if (W && tid < nloc) {
             float w = 0.0f;
-            for (int h = 0; h < group; ++h) w += ct.w[tid][h] / ct.l[h];
+            for (int h = 0; h < group; ++h) w += ct.w[tid][h] / ct.sum[0][h];
             a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + ct.slot[tid]] = w;
         }
     }
@@ -704,10 +747,10 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             }
         for (int x = tid; x < kG * split; x += kThreads) {
             const int h = x % kG;
-            st_cluster(&ct.ml[rank][h], x / kG, make_float2(tl > 0 ? ct.m[h] : none, tl > 0 ? ct.l[h] : 0.0f));
+            st_cluster(&ct.ml[rank][h], x / kG, make_float2(tl > 0 ? -ct.nm[h] : none, tl > 0 ? ct.sum[0][h] : 0.0f));
         }
         cluster_sync();
-        for (int hh = 0; hh < nh; ++hh) {
+        for (int hh = wg; hh < nh; hh += 2) {
             const int h = rank * nh + hh;
             float M = -INFINITY, Lsum = 0.0f, acc = 0.0f;
             for (int r = 0; r < split; ++r)
@@ -717,12 +760,12 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                 if (v.y != 0.0f) {   // a CTA without tiles took no part
                     const float f = exp2f(v.x - M);
                     Lsum = fmaf(f, v.y, Lsum);
-                    acc = fmaf(f, recv[(r * nh + hh) * kQDim + tid], acc);
+                    acc = fmaf(f, recv[(r * nh + hh) * kQDim + row], acc);
                 }
             }
             if (h < group) {
-                put(h, tid, Lsum != 0.0f ? acc / Lsum : 0.0f);
-                if (a.lse && tid == 0) a.lse[head0 + h] = Lsum != 0.0f ? (M + log2f(Lsum)) * 0.6931471805599453f : -INFINITY;
+                put(h, row, Lsum != 0.0f ? acc / Lsum : 0.0f);
+                if (a.lse && row == 0) a.lse[head0 + h] = Lsum != 0.0f ? (M + log2f(Lsum)) * 0.6931471805599453f : -INFINITY;
             }
         }
         if (W) {
@@ -732,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                     if (ct.ml[r][tid].y != 0.0f) M = fmaxf(M, ct.ml[r][tid].x);
                 for (int r = 0; r < split; ++r)
                     if (ct.ml[r][tid].y != 0.0f) Lsum = fmaf(exp2f(ct.ml[r][tid].x - M), ct.ml[r][tid].y, Lsum);
-                ct.fl[tid] = tl > 0 ? exp2f(ct.m[tid] - M) / Lsum : 0.0f;
+                ct.fl[tid] = tl > 0 ? exp2f(-ct.nm[tid] - M) / Lsum : 0.0f;
             }
             __syncthreads();
             if (tid < nloc) {
