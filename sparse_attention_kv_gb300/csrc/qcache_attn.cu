@@ -51,8 +51,9 @@ namespace {
 constexpr int kG = 16;                    // head columns of a unit (heads past the group are zeros)
 constexpr int kH = 8;                     // heads of a thread: two warpgroups share the 16
 constexpr int kSel = QSA_ATTN_MAX_K;
-constexpr int kThreads = 256;
-constexpr int kStages = 2;
+constexpr int kThreads = 288;             // two warpgroups and the control warp
+constexpr int kWork = 256;
+constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kQRec;
 constexpr int kMaxSplit = 8;
 constexpr float kTop = 4.0f;              // log2 of the largest weight when the references are set
@@ -62,11 +63,11 @@ constexpr float kFaint = 0x1p-60f;        // V scales whose weights never reach 
 
 struct QCtrl {
     uint64_t full[kStages];
-    uint64_t sbar, obar;
+    uint64_t sbar[2], obar;
     uint32_t tmem_base;
     int abort;
     int nsel, ntok;
-    int32_t sel[kSel];                    // the distinct valid ids, in slot order
+    int32_t sel[kSel + 1];                // the distinct valid ids, in slot order, then one past every context
     int32_t slot[kSel];                   // and the slots they came from
     alignas(16) float f[kG];              // scale log2(e) 2^9 / (the head's power-of-two scaling of q)
     alignas(16) float qs[kG];             // scale log2(e) sum(q)
@@ -90,15 +91,12 @@ struct QLayout {
     static constexpr int kOffRing = kOffP + TERMS * kTermP;
     static constexpr int kOffCtrl = kOffRing + kStages * kStageBytes;
     static constexpr int kBytes = kOffCtrl + (int)sizeof(QCtrl) + 1024;   // + alignment slack
-    // tensor memory: S, O, the unpacked K tile and the unpacked V tile (fp16: one region for both)
-    static constexpr uint32_t kN = kG * TERMS;
-    static constexpr uint32_t kColO = kN;
-    static constexpr uint32_t kColK = TERMS == 2 ? 64 : 96;
-    static constexpr uint32_t kColV = 96;
-    static constexpr uint32_t kCols = 128;
+    // tensor memory: two tiles' S, O (two groups: the leading terms, and the others 16 times as
+    // large), the unpacked K tile and the unpacked V tile
+    static constexpr uint32_t kColS = 0, kColO = 32, kColK = 64, kColV = 96, kCols = 128;
 };
-// four CTAs (and 1 KB each that the system keeps) in an SM's 228 KB
-static_assert(4 * (QLayout<3>::kBytes + 1024) <= 228 * 1024, "four CTAs per SM");
+// three CTAs (and 1 KB each that the system keeps) in an SM's 228 KB
+static_assert(3 * (QLayout<3>::kBytes + 1024) <= 228 * 1024, "three CTAs per SM");
 // the combine's buffers fit the ring: outputs sent and received, 16 heads x 128 fp32 each
 static_assert(2 * kG * kQDim * 4 <= kStages * kStageBytes, "combine buffers");
 
@@ -184,10 +182,10 @@ __device__ __forceinline__ float h2_lo(uint32_t h) { return __half2float(__ushor
 __device__ __forceinline__ float h2_hi(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)(h >> 16))); }
 constexpr uint32_t kH16 = 0x4C004C00u, kHNeg16 = 0xCC00CC00u;   // (16, 16) and (-16, -16)
 
-// The e4m3 terms of two values, |v| <= 448: v = t0 + t1 / 16 + t2 / 256 + what is left.  Two terms: from
-// the fp16 pair h = (a, b), whose 11 bits are more than theirs; returns 16 x what is left (exact).
+// The e4m3 terms of two weights, at most 448: w = t0 + (t1 + t2) / 16 + what is left.  Two terms: from the
+// fp16 pair h = (a, b), whose 11 bits are more than theirs; returns 16 x what is left (exact).
 template <int TERMS>
-__device__ __forceinline__ uint32_t split_terms(float a, float b, uint32_t h, uint16_t (&t)[TERMS]) {
+__device__ __forceinline__ uint32_t split_weights(float a, float b, uint32_t h, uint16_t (&t)[TERMS]) {
     if constexpr (TERMS == 2) {
         t[0] = h2_to_e4m3(h);
         const uint32_t r = h2_fma(e4m3_to_h2(t[0]), kHNeg16, h2_mul(h, kH16));
@@ -198,8 +196,18 @@ __device__ __forceinline__ uint32_t split_terms(float a, float b, uint32_t h, ui
         const uint32_t h0 = e4m3_to_h2(t[0]);
         const uint32_t r = to_h2((a - h2_lo(h0)) * 16.0f, (b - h2_hi(h0)) * 16.0f);
         t[1] = h2_to_e4m3(r);
-        t[2] = h2_to_e4m3(h2_fma(e4m3_to_h2(t[1]), kHNeg16, h2_mul(r, kH16)));
+        t[2] = h2_to_e4m3(h2_sub(r, e4m3_to_h2(t[1])));
         return 0u;
+    }
+}
+// The e4m3 terms of two query values below 256 in an fp16 pair: v = t0 + t1 (+ t2), exact for the format's
+// significand down to 2^-10 (bf16) and 2^-7 (fp16) of the head's largest value, to 2^-18 of it below.
+template <int TERMS>
+__device__ __forceinline__ void split_query(uint32_t h, uint16_t (&t)[TERMS]) {
+#pragma unroll
+    for (int u = 0; u < TERMS; ++u) {
+        t[u] = h2_to_e4m3(h);
+        h = h2_sub(h, e4m3_to_h2(t[u]));
     }
 }
 
@@ -251,6 +259,19 @@ __device__ __forceinline__ void wait_all(uint64_t *bar, uint32_t parity, volatil
     __syncwarp();
 }
 
+// 2^x for an integer x in [-126, 127].
+__device__ __forceinline__ float pow2i(int x) { return __int_as_float((x + 127) << 23); }
+
+// Barriers beside __syncthreads: 1 among the two warpgroups, 2 from the first to the control warp.
+__device__ __forceinline__ void work_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void k_ready_arrive() { asm volatile("bar.arrive 2, 160;" ::: "memory"); }
+__device__ __forceinline__ void k_ready_wait() { asm volatile("bar.sync 2, 160;" ::: "memory"); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 struct QParams {
     QAttnArgs a;
     float scale_log2;
@@ -259,7 +280,7 @@ struct QParams {
 
 // F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted.
 template <bool F16, bool W>
-__global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constant__ QParams p) {
+__global__ void __launch_bounds__(kThreads, 3) qattn_kernel(const __grid_constant__ QParams p) {
     constexpr int TERMS = F16 ? 3 : 2;
     using L = QLayout<TERMS>;
     extern __shared__ uint8_t smem_raw[];
@@ -268,27 +289,34 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     QCtrl &ct = *reinterpret_cast<QCtrl *>(smem + L::kOffCtrl);
     volatile int *abort_flag = &ct.abort;
     const QAttnArgs &a = p.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const int split = p.split, rank = split > 1 ? (int)cluster_ctarank() : 0;
     const int unit = blockIdx.x / split;
     const int qi = unit / a.n_kv_heads, g = unit - qi * a.n_kv_heads;
     const int group = a.n_heads / a.n_kv_heads, nb_cap = a.capacity / kQBlockTok;
+    const uint8_t *head_cache = static_cast<const uint8_t *>(a.cache) + qrec_offset(g, nb_cap, 0);
+    // one thread: the records of tile i (blocks b0 + 2i, b0 + 2i + 1 of sel) into its stage
+    auto fetch = [&](int i, int b0, int nloc) {
+        const int n = min(2, nloc - 2 * i), s = i % kStages;
+        mbar_expect_tx(&ct.full[s], (uint32_t)(n * kQRec));
+        for (int j = 0; j < n; ++j)
+            bulk_load(ring + s * kStageBytes + j * kQRec, head_cache + (size_t)ct.sel[b0 + 2 * i + j] * kQRec, kQRec,
+                      &ct.full[s]);
+    };
 
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(&ct.full[s], 1);
-        mbar_init(&ct.sbar, 1);
-        mbar_init(&ct.obar, 1);
-        ct.abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
     // a programmatic dependent of the work before it: nothing is read, and no tensor memory taken,
     // before that work is complete
-    wait_prior_grid();
-    __syncwarp();
-    if (warp == 0) {
-        tmem_alloc(&ct.tmem_base, L::kCols);
-        tmem_relinquish();
-    } else if (warp == 1) {
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s) mbar_init(&ct.full[s], 1);
+            mbar_init(&ct.sbar[0], 1);
+            mbar_init(&ct.sbar[1], 1);
+            mbar_init(&ct.obar, 1);
+            ct.abort = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        wait_prior_grid();
         // the query's distinct ids inside its context, in slot order
         const int32_t *ids = a.ids + (size_t)qi * a.k;
         const int32_t r0 = lane < a.k ? ids[lane] : -1;
@@ -313,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
         const bool take0 = in0 && (same0 & below) == 0u;
         const bool take1 = in1 && (same1 & below) == 0u && !repeat;
         const unsigned m0 = __ballot_sync(kFull, take0), m1 = __ballot_sync(kFull, take1);
+        const int nsel = __popc(m0) + __popc(m1);
         if (take0) {
             const int at = __popc(m0 & below);
             ct.sel[at] = r0;
@@ -323,18 +352,30 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             ct.sel[at] = r1;
             ct.slot[at] = lane + 32;
         }
-        if (__any_sync(kFull, bad) && lane == 0 && g == 0 && rank == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_BAD_ID);
+        const bool any_bad = __any_sync(kFull, bad);
         if (lane == 0) {
-            ct.nsel = __popc(m0) + __popc(m1);
+            ct.sel[nsel] = QSA_MAX_BLOCKS;
+            ct.nsel = nsel;
             ct.ntok = ntok;
+            if (any_bad && g == 0 && rank == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_BAD_ID);
         }
+        __syncwarp();
+        if (lane == 0) {   // the first tiles, before anything else is ready
+            const int T = (nsel + 1) >> 1, p0 = rank * T / split, tl = (rank + 1) * T / split - p0;
+            for (int i = 0; i < kStages && i < tl; ++i) fetch(i, 2 * p0, min(nsel - 2 * p0, 2 * tl));
+        }
+        __syncwarp();
+        tmem_alloc(&ct.tmem_base, L::kCols);
+        tmem_relinquish();
         if (W && rank == 0) {   // slots that take no part
             float *w = a.weights + ((size_t)qi * a.n_kv_heads + g) * a.k;
             if (lane < a.k && !take0) w[lane] = 0.0f;
             if (lane + 32 < a.k && !take1) w[lane + 32] = 0.0f;
         }
-    }
-    {   // the group's queries: sixteen threads per head, 8 dimensions each
+    } else {   // the group's queries: sixteen threads per head, 8 dimensions each
+        if (W)
+            for (int i = tid; i < kSel * kG; i += kWork) (&ct.w[0][0])[i] = 0.0f;
+        wait_prior_grid();
         const int h = tid >> 4, part = tid & 15;
         float x[8];
 #pragma unroll
@@ -362,14 +403,14 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             sum += __shfl_xor_sync(kFull, sum, o);
         }
         const bool finite = big < 0x7F800000u;
-        // a power of two that puts the largest magnitude into [128, 256)
+        // a power of two that puts the largest magnitude into [128, 256), in two exact steps
         const int e = finite && big != 0u ? 7 - ilogbf(__uint_as_float(big)) : 0;
+        const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
         uint32_t out[TERMS][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float v0 = finite ? scalbnf(x[2 * i], e) : 0.0f, v1 = finite ? scalbnf(x[2 * i + 1], e) : 0.0f;
             uint16_t t[TERMS];
-            split_terms<TERMS>(v0, v1, to_h2(v0, v1), t);
+            split_query<TERMS>(finite ? to_h2(x[2 * i] * s0 * s1, x[2 * i + 1] * s0 * s1) : 0u, t);
 #pragma unroll
             for (int u = 0; u < TERMS; ++u) {
                 if (i & 1) out[u][i >> 1] |= (uint32_t)t[u] << 16;
@@ -387,8 +428,6 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             ct.top[h] = -INFINITY;
         }
     }
-    if (W)
-        for (int i = tid; i < kSel * kG; i += kThreads) (&ct.w[0][0])[i] = 0.0f;
     fence_proxy_async();   // the queries are read by the tensor core
     tc_fence_before();
     __syncthreads();
@@ -400,20 +439,8 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     const int T = (nsel + 1) >> 1;
     const int p0 = rank * T / split, tl = (rank + 1) * T / split - p0;
     const int b0 = 2 * p0, nloc = min(nsel - b0, 2 * tl);
-    const uint8_t *head_cache = static_cast<const uint8_t *>(a.cache) + qrec_offset(g, nb_cap, 0);
-    auto fetch = [&](int i) {   // one thread: the records of tile i into its stage
-        const int n = min(2, nloc - 2 * i), s = i % kStages;
-        mbar_expect_tx(&ct.full[s], (uint32_t)(n * kQRec));
-        for (int j = 0; j < n; ++j)
-            bulk_load(ring + s * kStageBytes + j * kQRec, head_cache + (size_t)ct.sel[b0 + 2 * i + j] * kQRec, kQRec,
-                      &ct.full[s]);
-    };
-    if (tid == 0)
-        for (int i = 0; i < kStages && i < tl; ++i) fetch(i);
-
     // Two warpgroups: both hold every token of a tile (and every dimension of O), one head half each.
     // The first unpacks K, the second V.
-    const uint32_t id = idesc(0, 128, L::kN);
     const int wg = tid >> 7, row = tid & 127, half = row >> 6, tok = row & 63;
     const int h0 = wg * kH;
     f32x2 l[kH / 2], mv[kH / 2];
@@ -425,74 +452,107 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     }
     float e[kH];
 
-    for (int i = 0; i < tl; ++i) {
-        const int s = i % kStages;
-        const uint8_t *st = ring + s * kStageBytes;
-        if (i > 0 && (TERMS == 3 || wg == 1)) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // V(i - 1) is read
-        wait_all(&ct.full[s], (uint32_t)(i / kStages) & 1u, abort_flag);
-        const uint8_t *rec = st + half * kQRec;
-        // 16 bytes of codes to 4 + 4 columns of a row of A
-        uint32_t lo[8], hi[8];
-        auto unpack = [&](const uint8_t *src, int at) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(src);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (warp == 8) {
+        // ---- control: S(i + 1) as soon as K(i + 1) is unpacked, O += P(i) V(i) when P(i) stands
+        const uint32_t id16 = idesc(0, 128, kG);
+        const uint64_t dq = sdesc(smem_u32(sQ)), dp = sdesc_mn(smem_u32(sP), 8 * kG, L::kTermP);
+        auto scores = [&](int i) {
+            k_ready_wait();
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo[at + j] = w[j] & 0x0F0F0F0Fu;
-                hi[at + j] = (w[j] >> 4) & 0x0F0F0F0Fu;
+                for (int u = 0; u < TERMS; ++u)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)   // descriptors count in units of 16 bytes
+                        mma_f8_ta(tmem + L::kColS + (i & 1) * kG, tmem + L::kColK + kk * 8, dq + u * (kG * 8) + kk * 2, id16,
+                                  (u | kk) != 0 ? 1u : 0u);
+                mma_commit(&ct.sbar[i & 1]);
             }
+            __syncwarp();
         };
-        auto unpack_v = [&]() {           // this thread's dimension, the tokens of the two blocks
+        if (tl > 0) scores(0);
+        for (int i = 0; i < tl; ++i) {
+            if (i + 1 < tl) scores(i + 1);
+            while (__syncthreads_or(0)) {}   // again while the references move
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+                for (int kk = 0; kk < 4; ++kk)   // both groups of columns
+                    mma_f8_ta(tmem + L::kColO, tmem + L::kColV + kk * 8, dp + kk * (2 * kG), idesc(0, 128, 2 * kG) | kIdescBMn,
+                              (i | kk) != 0 ? 1u : 0u);
+                if (TERMS == 3)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f8_ta(tmem + L::kColO + kG, tmem + L::kColV + kk * 8, dp + 2 * (L::kTermP / 16) + kk * (2 * kG),
+                                  id16 | kIdescBMn, 1u);
+                mma_commit(&ct.obar);
+                if (i + kStages < tl) fetch(i + kStages, b0, nloc);   // every thread has read this stage
+            }
+            __syncwarp();
+        }
+    } else {
+    auto wait_full = [&](int i) { wait_all(&ct.full[i % kStages], (uint32_t)(i / kStages) & 1u, abort_flag); };
+    // 16 bytes of codes to 4 + 4 columns of a row of A
+    uint32_t lo[8], hi[8];
+    auto unpack = [&](const uint8_t *src, int at) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(src);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            lo[at + j] = w[j] & 0x0F0F0F0Fu;
+            hi[at + j] = (w[j] >> 4) & 0x0F0F0F0Fu;
+        }
+    };
+    auto unpack_k = [&](int i) {              // this thread's token, its 128 dimensions
+        wait_full(i);
+        tc_fence_after();
+        const uint8_t *src = ring + (i % kStages) * kStageBytes + half * kQRec + tok * 16;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            unpack(src + (2 * c) * 1024, 0);
+            unpack(src + (2 * c + 1) * 1024, 4);
+            tmem_st8(tmem + lanes + L::kColK + c * 8, lo);
+            tmem_st8(tmem + lanes + L::kColK + 16 + c * 8, hi);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        k_ready_arrive();
+    };
+    if (wg == 0 && tl > 0) unpack_k(0);
+    for (int i = 0; i < tl; ++i) {
+        const uint8_t *st = ring + (i % kStages) * kStageBytes;
+        const uint8_t *rec = st + half * kQRec;
+        if (wg == 0) {
+            wait_all(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag);   // S(i) is complete, K(i) read
+            if (i + 1 < tl) unpack_k(i + 1);
+            if (i > 0) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // P(i - 1) is read
+        } else {
+            wait_full(i);
+            if (i > 0) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // V(i - 1), P(i - 1) are read
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {     // this thread's dimension, the tokens of the two blocks
                 const uint8_t *src = st + b * kQRec + kQOffV + row * 16;
                 unpack(src, 0);
                 unpack(src + 2048, 4);
                 tmem_st8(tmem + lanes + L::kColV + b * 16, lo);
                 tmem_st8(tmem + lanes + L::kColV + b * 16 + 8, hi);
             }
-        };
-        tc_fence_after();
-        if (wg == 0) {                    // this thread's token, its 128 dimensions
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                unpack(rec + (2 * c) * 1024 + tok * 16, 0);
-                unpack(rec + (2 * c + 1) * 1024 + tok * 16, 4);
-                tmem_st8(tmem + lanes + L::kColK + c * 8, lo);
-                tmem_st8(tmem + lanes + L::kColK + 16 + c * 8, hi);
-            }
-        } else if (TERMS == 2) {
-            unpack_v();
+            wait_all(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag);
         }
-        const bool vis = 2 * i + half < nloc && ct.sel[b0 + min(2 * i + half, nloc - 1)] * kQBlockTok + tok < ntok;
+        tc_fence_after();
+        const bool vis = ct.sel[b0 + 2 * i + half] * kQBlockTok + tok < ntok;
         const uint32_t kp = vis ? *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + tok * 4) : 0u;
         const uint32_t vp = vis ? *reinterpret_cast<const uint32_t *>(rec + kQOffVPair + tok * 4) : 0u;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_f8_ta(tmem, tmem + L::kColK + kk * 8, sdesc(smem_u32(sQ) + kk * 32), id, kk > 0 ? 1u : 0u);
-            mma_commit(&ct.sbar);
-        }
-        __syncwarp();
         const float ks = QFmt<F16>::lo(kp), km = QFmt<F16>::hi(kp);
         const float vs = QFmt<F16>::lo(vp), vm = QFmt<F16>::hi(vp);
         const bool all_vis = __all_sync(kFull, vis);
-        wait_all(&ct.sbar, (uint32_t)i & 1u, abort_flag);                 // S(i) is complete, K(i) read
-        if (wg == 0 && i > 0 && TERMS == 2) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // P(i - 1) is read
-        tc_fence_after();
-        if (TERMS == 3 && wg == 1) unpack_v();
         // y = log2(e) s - m of this token, into e
         auto logits = [&]() {
-            uint32_t v[TERMS][kH];
-#pragma unroll
-            for (int u = 0; u < TERMS; ++u) tmem_ld8_nowait(tmem + lanes + u * kG + h0, v[u]);
+            uint32_t v[kH];
+            tmem_ld8_nowait(tmem + lanes + L::kColS + (i & 1) * kG + h0, v);
             tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < TERMS; ++u) reg_fence(v[u]);
+            reg_fence(v);
             const f32x2 ks2 = pack2(ks, ks), km2 = pack2(km, km);
 #pragma unroll
             for (int h = 0; h < kH / 2; h += 2) {
@@ -502,10 +562,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int x = 2 * (h + j);
-                    f32x2 t = pack2(__uint_as_float(v[TERMS - 1][x]), __uint_as_float(v[TERMS - 1][x + 1]));
-#pragma unroll
-                    for (int u = TERMS - 2; u >= 0; --u)
-                        t = fma2(t, pack2(0.0625f, 0.0625f), pack2(__uint_as_float(v[u][x]), __uint_as_float(v[u][x + 1])));
+                    f32x2 t = pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
                     t = fma2(mul2(t, j ? f.y : f.x), ks2, fma2(km2, j ? qs.y : qs.x, j ? nm.y : nm.x));
                     unpack2(t, e[x], e[x + 1]);
                 }
@@ -534,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                     ct.red[0][warp & 3][h0 + lane] = mine[0];
                     ct.red[1][warp & 3][h0 + lane] = mine[1];
                 }
-                __syncthreads();
+                work_barrier();
                 if (warp == 0) {
                     const int h = lane & 15;
                     uint32_t y = 0u, r = 0u;
@@ -563,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                         if (lane == 0) ct.least_g = exp2f(least);
                     }
                 }
-                __syncthreads();
+                work_barrier();
                 if (i > 0) {   // what is summed so far, to the new references (O(i - 1) is complete)
 #pragma unroll
                     for (int h = 0; h < kH / 2; ++h) {
@@ -574,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                         if (TERMS == 2) left[h] = to_h2(h2_lo(left[h]) * fo.x, h2_hi(left[h]) * fo.y);
                     }
                     if (W)
-                        for (int j = tid; j < 2 * i * kG; j += kThreads) (&ct.w[0][0])[j] *= ct.fl[j % kG];
+                        for (int j = tid; j < 2 * i * kG; j += kWork) (&ct.w[0][0])[j] *= ct.fl[j % kG];
                     uint32_t o[kH];
 #pragma unroll
-                    for (int u = 0; u < TERMS; ++u) {
+                    for (int u = 0; u < 2; ++u) {
                         tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o);
                         tmem_wait_ld();
                         reg_fence(o);
@@ -607,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                 const uint32_t h2 = to_h2(w0, w1);
                 hmax = h2_max(hmax, h2);
                 uint16_t t[TERMS];
-                rest[h] = split_terms<TERMS>(w0, w1, h2, t);
+                rest[h] = split_weights<TERMS>(w0, w1, h2, t);
 #pragma unroll
                 for (int u = 0; u < TERMS; ++u) {
                     if (h & 1) word[u][h >> 1] |= (uint32_t)t[u] << 16;
@@ -629,16 +686,6 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             }
             renew = true;
         }
-        if (tid == 128) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_f8_ta(tmem + L::kColO, tmem + L::kColV + kk * 8, sdesc_mn(smem_u32(sP) + kk * 32 * kG, 8 * kG, L::kTermP),
-                          id | kIdescBMn, (i | kk) != 0 ? 1u : 0u);
-            mma_commit(&ct.obar);
-            if (i + kStages < tl) fetch(i + kStages);   // every thread has read this stage
-        }
-        __syncwarp();
         const f32x2 vm2 = pack2(vm, vm);
 #pragma unroll
         for (int h = 0; h < kH / 2; ++h) {
@@ -662,14 +709,14 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             x[2][2 * h] = h2_lo(left[h]);
             x[2][2 * h + 1] = h2_hi(left[h]);
         }
-        __syncthreads();   // every thread has read ct.red
+        work_barrier();   // every thread has read ct.red
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             if (j == 2 && TERMS == 3) break;
             const float sum = warp_sum8(x[j], lane);
             if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = __float_as_uint(sum);
         }
-        __syncthreads();
+        work_barrier();
         if (tid < 3 * kG) {
             const int j = tid / kG, h = tid % kG;
             float sum = 0.0f;
@@ -677,8 +724,9 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
                 for (int w = 0; w < 4; ++w) sum += __uint_as_float(ct.red[j][w][h]);
             ct.sum[j][h] = sum;
         }
-        __syncthreads();
     }
+    }
+    __syncthreads();
     const size_t head0 = (size_t)qi * a.n_heads + (size_t)g * group;
     auto put = [&](int h, int d, float x) {
         const size_t at = (head0 + h) * kQDim + d;
@@ -686,23 +734,22 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
         else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits(x);
     };
     float *part = reinterpret_cast<float *>(ring);   // split: this CTA's unnormalised output [16][128]
-    if (tl > 0) {
+    if (warp == 8) {
+    } else if (tl > 0) {
         wait_all(&ct.obar, (uint32_t)(tl - 1) & 1u, abort_flag);
         tc_fence_after();
-        uint32_t o[TERMS][kH];
+        uint32_t o[2][kH];
 #pragma unroll
-        for (int u = 0; u < TERMS; ++u) tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o[u]);
+        for (int u = 0; u < 2; ++u) tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o[u]);
         tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < TERMS; ++u) reg_fence(o[u]);
+        reg_fence(o[0]);
+        reg_fence(o[1]);
         // this thread's dimension of its heads (a warp's stores for one head are 32 neighbours).  The codes'
         // mean, 7.5, times what the rounding left of the weights takes most of its effect away.
 #pragma unroll
         for (int j = 0; j < kH; ++j) {
             const int h = h0 + j;
-            float x = __uint_as_float(o[TERMS - 1][j]);
-#pragma unroll
-            for (int u = TERMS - 2; u >= 0; --u) x = fmaf(x, 0.0625f, __uint_as_float(o[u][j]));
+            float x = fmaf(__uint_as_float(o[1][j]), 0.0625f, __uint_as_float(o[0][j]));
             x = fmaf(fmaf(x, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), exp2f(-ct.eg[h]), ct.sum[1][h]);
             if (split > 1) part[h * kQDim + row] = x;
             else if (h < group) put(h, row, x / ct.sum[0][h]);
@@ -713,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
     }
     if (tid == 0 && ct.abort) {   // a wait gave up: let what is in flight land before the memory is freed
         for (int i = max(0, tl - kStages); i < tl; ++i) mbar_drain(&ct.full[i % kStages], (uint32_t)(i / kStages) & 1u);
-        mbar_drain(&ct.sbar, (uint32_t)(tl - 1) & 1u);
+        for (int i = max(0, tl - 2); i < tl; ++i) mbar_drain(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u);
         mbar_drain(&ct.obar, (uint32_t)(tl - 1) & 1u);
         if (a.flags) atomicOr(a.flags, QSA_FLAG_WAIT_TIMEOUT);
     }
@@ -727,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
         }
     }
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 8) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, L::kCols);
@@ -750,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 4) qattn_kernel(const __grid_constan
             st_cluster(&ct.ml[rank][h], x / kG, make_float2(tl > 0 ? -ct.nm[h] : none, tl > 0 ? ct.sum[0][h] : 0.0f));
         }
         cluster_sync();
-        for (int hh = wg; hh < nh; hh += 2) {
+        for (int hh = wg; wg < 2 && hh < nh; hh += 2) {
             const int h = rank * nh + hh;
             float M = -INFINITY, Lsum = 0.0f, acc = 0.0f;
             for (int r = 0; r < split; ++r)
