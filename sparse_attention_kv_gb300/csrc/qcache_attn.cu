@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 3) qattn_kernel(const __grid_constan
     constexpr int TERMS = F16 ? 3 : 2;
     using L = QLayout<TERMS>;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // offset, not rounded as a number: the compiler keeps knowing that this is shared memory
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sQ = smem + L::kOffQ, *sP = smem + L::kOffP, *ring = smem + L::kOffRing;
     QCtrl &ct = *reinterpret_cast<QCtrl *>(smem + L::kOffCtrl);
     volatile int *abort_flag = &ct.abort;
