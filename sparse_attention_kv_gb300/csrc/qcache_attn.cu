@@ -18,22 +18,25 @@
 // number of terms (to 2^-8 of themselves beside bf16 rows, as a bf16 weight would be; 2^-12
 // beside fp16 ones), with steps of 2^-18 (2^-22) of the largest weight at the small end.
 //
-// One CTA (128 threads) per (query, KV head), four CTAs per SM; tiles of two blocks (128 tokens):
-//   1. a thread per token unpacks its K row from shared memory into tensor memory; S = K . Q^T with A
-//      from tensor memory (M = 128 tokens, N = 16 heads x terms, K = 128 dims);
-//   2. meanwhile a thread per dimension unpacks V^T the same way (the record holds V by dimension);
-//   3. a thread per token takes its row of S, p = exp2(y) against a running reference m per head, and
-//      writes the weights' terms to shared memory (rows = heads x terms, the swizzled K-major
-//      layout of B);
-//   4. O += V^T . P^T (M = 128 dims, N = 16 heads x terms, K = 128 tokens).
+// A CTA takes (query, KV head) units in turn, two CTAs per SM; a step of it is four blocks (two
+// tiles of 128 tokens).  Its warps:
+//   0-3   unpack K, a thread per token, from shared memory into tensor memory: S = K . Q^T with A from
+//         tensor memory (M = 128 tokens, N = 16 heads, K = 128 dims x terms);
+//   4-7   unpack V^T, a thread per dimension (the record holds V by dimension);
+//   0-7   two threads per token, eight heads each: p = exp2(y) against a running reference m per
+//         head, the weights' terms to shared memory (rows of 16 heads per token: B, MN-major);
+//   8     control: the record copies (two steps deep, across units), and the products: S of step t + 1
+//         as soon as its K is unpacked, then O += V^T . P^T of step t (M = 128 dims, K = 256 tokens);
+//   9     preparation of the next unit: its distinct ids, and its queries' terms and sums.
+// So K of the next step (of the next unit, too) unpacks and multiplies behind the softmax of this
+// one, and nothing of a unit's start waits for memory but the first unit's.
 // The references are lazy.  m[h] and the weights' scale g[h] (a power of two that puts the largest
-// p vs seen at 2^4) are taken from the first tile, and change only when a later tile's weight
-// would pass 2^8 or its y 30: the barrier before step 4 carries that vote, so an ordinary tile
-// has two barriers and no reduction across threads.  Sums of p (in fp32) stay per token
-// lane until the end.
+// p vs seen at 2^4) are taken from a unit's first step, and change only when a later weight
+// would pass 2^8 or its y 30: the barrier before O's product carries that vote, so an ordinary step
+// has one barrier and no reduction across threads.  Sums of p (in fp32) stay per token
+// lane until the unit's end.
 //
-// Records arrive by bulk copies, one per block, two tiles deep.  What bounds it: see the launcher.
-// When units are few, a cluster of 2, 4 or 8 CTAs splits a unit's tiles and combines the partial
+// When units are few, a cluster of 2, 4 or 8 CTAs splits a unit's blocks and combines the partial
 // outputs through distributed shared memory.  Every wait is bounded; on expiry the CTA raises
 // QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
@@ -51,54 +54,71 @@ namespace {
 constexpr int kG = 16;                    // head columns of a unit (heads past the group are zeros)
 constexpr int kH = 8;                     // heads of a thread: two warpgroups share the 16
 constexpr int kSel = QSA_ATTN_MAX_K;
-constexpr int kThreads = 288;             // two warpgroups and the control warp
-constexpr int kWork = 256;
-constexpr int kStages = 3;
-constexpr int kStageBytes = 2 * kQRec;
+constexpr int kWork = 256;                // threads of the two warpgroups
+constexpr int kThreads = 512;             // and a warpgroup that unpacks, and one of single warps
+constexpr int kUnpack = 8, kControl = 12, kPrepare = 13, kFetch = 14;   // first warps of the roles
+constexpr int kStep = 4;                  // blocks of a step
+constexpr int kKBytes = kQOffV, kVBytes = kQRec - kQOffV;  // a record's halves: K codes and all pairs, V codes
+constexpr int kVStages = 2;
 constexpr int kMaxSplit = 8;
 constexpr float kTop = 4.0f;              // log2 of the largest weight when the references are set
 constexpr float kMostWeight = 256.0f;     // a weight above this moves them (e4m3 holds 448)
 constexpr float kMostY = 30.0f;           // and a y above this
 constexpr float kFaint = 0x1p-60f;        // V scales whose weights never reach kMostWeight before p overflows
 
-struct QCtrl {
-    uint64_t full[kStages];
-    uint64_t sbar[2], obar;
-    uint32_t tmem_base;
-    int abort;
-    int nsel, ntok;
-    int32_t sel[kSel + 1];                // the distinct valid ids, in slot order, then one past every context
+// What the preparation warp leaves of a unit.
+struct QUnit {
+    int steps;                            // of this CTA's slice; 0: no visible token
+    int b0, nloc;                         // first entry and length of the slice of sel
+    int ntok;
+    int32_t sel[kSel + kStep];            // the distinct valid ids, in slot order, then ids past every context
     int32_t slot[kSel];                   // and the slots they came from
     alignas(16) float f[kG];              // scale log2(e) 2^9 / (the head's power-of-two scaling of q)
     alignas(16) float qs[kG];             // scale log2(e) sum(q)
+};
+
+struct QCtrl {
+    uint64_t k_full[2], k_free[2], v_full[kVStages], v_free[kVStages], sbar[2], obar;
+    uint64_t ids_ready[2], ready[2], done[2];
+    uint32_t tmem_base;
+    int abort;
+    QUnit unit[2];
+    alignas(16) float zero[kG];
     alignas(16) float nm[kG];             // minus the reference of the exponents (log2 units)
     alignas(16) float g[kG];              // power of two of the weights
     alignas(16) float fl[kG];             // rescaling of the sums and of the outputs
     alignas(16) float fo[kG];
+    alignas(16) float inv[kG];
     float top[kG], eg[kG];                // largest log2(p vs) + m seen, log2(g)
     float least_g;
     uint32_t red[3][4][kG];
     float sum[3][kG];                     // l, sum of p vm, 16 x what the weights' rounding took away
     float2 ml[kMaxSplit][kG];             // (m, l) of every CTA of a cluster
-    float w[kSel][kG];                    // sums of p over a slot's tokens
+    alignas(16) float w[kSel][kG];        // sums of p over a slot's tokens
 };
 
 template <int TERMS>
 struct QLayout {
-    static constexpr int kOffQ = 0;                              // heads x terms rows of 128 bytes, swizzled
-    static constexpr int kOffP = kOffQ + kG * TERMS * 128;       // per term [128 tokens][16 heads]
-    static constexpr int kTermP = 128 * kG;
-    static constexpr int kOffRing = kOffP + TERMS * kTermP;
-    static constexpr int kOffCtrl = kOffRing + kStages * kStageBytes;
+    static constexpr int kQBytes = kG * TERMS * 128;             // heads x terms rows of 128 bytes, swizzled
+    static constexpr int kTermP = 128 * kG;                      // [128 tokens][16 heads]
+    static constexpr int kTileP = TERMS * kTermP;
+    static constexpr int kOffQ = 0;                              // two units' queries
+    static constexpr int kOffP = kOffQ + 2 * kQBytes;
+    static constexpr int kStepP = 2 * kTileP;                    // the two tiles of a step
+    static constexpr int kPBufs = TERMS == 2 ? 2 : 1;            // what the shared memory of two CTAs holds
+    static constexpr int kKStages = 2;
+    static constexpr int kOffK = kOffP + kPBufs * kStepP;
+    static constexpr int kOffV = kOffK + kKStages * kStep * kKBytes;
+    static constexpr int kOffCtrl = kOffV + kVStages * kStep * kVBytes;
     static constexpr int kBytes = kOffCtrl + (int)sizeof(QCtrl) + 1024;   // + alignment slack
-    // tensor memory: two tiles' S, O (two groups: the leading terms, and the others 16 times as
-    // large), the unpacked K tile and the unpacked V tile
-    static constexpr uint32_t kColS = 0, kColO = 32, kColK = 64, kColV = 96, kCols = 128;
 };
-// three CTAs (and 1 KB each that the system keeps) in an SM's 228 KB
-static_assert(3 * (QLayout<3>::kBytes + 1024) <= 228 * 1024, "three CTAs per SM");
+// tensor memory: S (two steps of two tiles), O (two groups of columns: the leading terms, and the
+// others 16 times as large), the unpacked K tiles and the unpacked V tiles
+constexpr uint32_t kColS = 0, kColO = 64, kColK = 96, kColV = 160, kCols = 256;
+// two CTAs (and 1 KB each that the system keeps) in an SM's 228 KB
+static_assert(2 * (QLayout<2>::kBytes + 1024) <= 228 * 1024 && 2 * (QLayout<3>::kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
 // the combine's buffers fit the ring: outputs sent and received, 16 heads x 128 fp32 each
-static_assert(2 * kG * kQDim * 4 <= kStages * kStageBytes, "combine buffers");
+static_assert(2 * kG * kQDim * 4 <= 2 * kStep * kKBytes, "combine buffers");
 
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float a, float b) {
@@ -132,26 +152,32 @@ __device__ __forceinline__ float lg2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Two fp32 values to fp16 (b high), fp16 pairs to e4m3 pairs and back (exact).
+// Two fp32 values to fp16 (b high), two fp16 pairs (or four fp32 values) to four e4m3 and back (exact).
 __device__ __forceinline__ uint32_t to_h2(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ uint16_t h2_to_e4m3(uint32_t h) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-    return r;
-}
-__device__ __forceinline__ uint16_t f2_to_e4m3(float a, float b) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3_to_h2(uint16_t e) {
+__device__ __forceinline__ uint32_t h4_to_e4m3(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(e));
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
     return r;
+}
+__device__ __forceinline__ uint32_t f4_to_e4m3(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\t"
+        "mov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+__device__ __forceinline__ void e4m3_to_h4(uint32_t e, uint32_t &a, uint32_t &b) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(e));
 }
 __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
@@ -182,32 +208,41 @@ __device__ __forceinline__ float h2_lo(uint32_t h) { return __half2float(__ushor
 __device__ __forceinline__ float h2_hi(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)(h >> 16))); }
 constexpr uint32_t kH16 = 0x4C004C00u, kHNeg16 = 0xCC00CC00u;   // (16, 16) and (-16, -16)
 
-// The e4m3 terms of two weights, at most 448: w = t0 + (t1 + t2) / 16 + what is left.  Two terms: from the
-// fp16 pair h = (a, b), whose 11 bits are more than theirs; returns 16 x what is left (exact).
+// The e4m3 terms of four weights, at most 448: w = t0 + (t1 + t2) / 16 + what is left.  Two terms: from the
+// fp16 pairs h, whose 11 bits are more than theirs; what is left, 16 times as large, is added to `left` (exact).
 template <int TERMS>
-__device__ __forceinline__ uint32_t split_weights(float a, float b, uint32_t h, uint16_t (&t)[TERMS]) {
+__device__ __forceinline__ void split_weights(const float (&w)[4], const uint32_t (&h)[2], uint32_t (&t)[TERMS],
+                                              uint32_t (&left)[2]) {
+    uint32_t a, b;
     if constexpr (TERMS == 2) {
-        t[0] = h2_to_e4m3(h);
-        const uint32_t r = h2_fma(e4m3_to_h2(t[0]), kHNeg16, h2_mul(h, kH16));
-        t[1] = h2_to_e4m3(r);
-        return h2_sub(r, e4m3_to_h2(t[1]));
-    } else {   // the first remainder in fp32; it fits fp16 with bits to spare
-        t[0] = f2_to_e4m3(a, b);
-        const uint32_t h0 = e4m3_to_h2(t[0]);
-        const uint32_t r = to_h2((a - h2_lo(h0)) * 16.0f, (b - h2_hi(h0)) * 16.0f);
-        t[1] = h2_to_e4m3(r);
-        t[2] = h2_to_e4m3(h2_sub(r, e4m3_to_h2(t[1])));
-        return 0u;
+        t[0] = h4_to_e4m3(h[0], h[1]);
+        e4m3_to_h4(t[0], a, b);
+        const uint32_t r0 = h2_fma(a, kHNeg16, h2_mul(h[0], kH16)), r1 = h2_fma(b, kHNeg16, h2_mul(h[1], kH16));
+        t[1] = h4_to_e4m3(r0, r1);
+        e4m3_to_h4(t[1], a, b);
+        left[0] = h2_add(left[0], h2_sub(r0, a));
+        left[1] = h2_add(left[1], h2_sub(r1, b));
+    } else {   // the first remainders in fp32; they fit fp16 with bits to spare
+        t[0] = f4_to_e4m3(w[0], w[1], w[2], w[3]);
+        e4m3_to_h4(t[0], a, b);
+        const uint32_t r0 = to_h2((w[0] - h2_lo(a)) * 16.0f, (w[1] - h2_hi(a)) * 16.0f);
+        const uint32_t r1 = to_h2((w[2] - h2_lo(b)) * 16.0f, (w[3] - h2_hi(b)) * 16.0f);
+        t[1] = h4_to_e4m3(r0, r1);
+        e4m3_to_h4(t[1], a, b);
+        t[2] = h4_to_e4m3(h2_sub(r0, a), h2_sub(r1, b));
     }
 }
-// The e4m3 terms of two query values below 256 in an fp16 pair: v = t0 + t1 (+ t2), exact for the format's
-// significand down to 2^-10 (bf16) and 2^-7 (fp16) of the head's largest value, to 2^-18 of it below.
+// The e4m3 terms of four query values below 256: v = t0 + t1 (+ t2), exact for the format's significand down
+// to 2^-10 (bf16) and 2^-7 (fp16) of the head's largest value, to 2^-18 of it below.
 template <int TERMS>
-__device__ __forceinline__ void split_query(uint32_t h, uint16_t (&t)[TERMS]) {
+__device__ __forceinline__ void split_query(uint32_t h0, uint32_t h1, uint32_t (&t)[TERMS]) {
 #pragma unroll
     for (int u = 0; u < TERMS; ++u) {
-        t[u] = h2_to_e4m3(h);
-        h = h2_sub(h, e4m3_to_h2(t[u]));
+        uint32_t a, b;
+        t[u] = h4_to_e4m3(h0, h1);
+        e4m3_to_h4(t[u], a, b);
+        h0 = h2_sub(h0, a);
+        h1 = h2_sub(h1, b);
     }
 }
 
@@ -253,541 +288,733 @@ __device__ __forceinline__ float warp_sum8(const float (&x)[kH], int lane) {
     return c + __shfl_xor_sync(kFull, c, 1);
 }
 
-// Every thread waits; the warp is converged behind it (the tcgen05 loads and stores need that).
+
+// Every thread of the warp waits, a bounded number of tries (each suspends the thread for some
+// hundred cycles; the bound comes to seconds); after one has given up, waits return at once.  A
+// poll is four instructions: waiting warps share the issue slots with working ones.
+template <int SLEEP = 0>
 __device__ __forceinline__ void wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    mbar_wait(bar, parity, abort_flag);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (__all_sync(kFull, ok != 0)) return;   // the warp stays converged
+    const uint32_t most = *abort_flag ? 1u : 1u << 23;
+    if constexpr (SLEEP == 0)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+            "WAIT_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE_%=;\n\t"
+            "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, %3;\n\t@q bra WAIT_%=;\n\tDONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(most)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+            "WAIT_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE_%=;\n\t"
+            "nanosleep.u32 %4;\n\t"
+            "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, %3;\n\t@q bra WAIT_%=;\n\tDONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(most), "n"(SLEEP)
+            : "memory");
+    if (!ok) *abort_flag = 1;
     __syncwarp();
 }
 
-// 2^x for an integer x in [-126, 127].
-__device__ __forceinline__ float pow2i(int x) { return __int_as_float((x + 127) << 23); }
-
-// Barriers beside __syncthreads: 1 among the two warpgroups, 2 from the first to the control warp.
+// Barriers: 1 among the softmax warps, 2 and 4 from the unpacking warps to the control warp (K and V stand),
+// 3 with a vote among the softmax warps and the control warp.
 __device__ __forceinline__ void work_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void k_ready_arrive() { asm volatile("bar.arrive 2, 160;" ::: "memory"); }
 __device__ __forceinline__ void k_ready_wait() { asm volatile("bar.sync 2, 160;" ::: "memory"); }
+__device__ __forceinline__ void v_ready_arrive() { asm volatile("bar.arrive 4, 160;" ::: "memory"); }
+__device__ __forceinline__ void v_ready_wait() { asm volatile("bar.sync 4, 160;" ::: "memory"); }
+__device__ __forceinline__ bool vote_barrier(bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 3, 288, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((uint32_t)mine)
+        : "memory");
+    return any != 0;
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
     return ok != 0;
 }
+// 2^x for an integer x in [-126, 127].
+__device__ __forceinline__ float pow2i(int x) { return __int_as_float((x + 127) << 23); }
 
 struct QParams {
     QAttnArgs a;
     float scale_log2;
     int split;
+    int units;
 };
+
+// The preparation warp: a unit's distinct ids inside its context, in slot order, and this CTA's slice of them.
+template <bool W>
+__device__ __forceinline__ void prepare_ids(const QParams &p, int qi, int g, int rank, QUnit &u) {
+    const QAttnArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    const int32_t *ids = a.ids + (size_t)qi * a.k;
+    const int32_t r0 = lane < a.k ? ids[lane] : -1;
+    const int32_t r1 = lane + 32 < a.k ? ids[lane + 32] : -1;
+    int ntok = a.n_tokens[qi];
+    if (ntok < 0 || ntok > a.capacity) {
+        if (lane == 0 && g == 0 && rank == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+        ntok = ntok < 0 ? 0 : a.capacity;
+    }
+    const int nb = (ntok + kQBlockTok - 1) / kQBlockTok;
+    const unsigned below = (1u << lane) - 1u;
+    const bool in0 = r0 >= 0 && r0 < nb, in1 = r1 >= 0 && r1 < nb;
+    const bool bad = (r0 != -1 && !in0) || (r1 != -1 && !in1);
+    // every lane takes part in every exchange; the conditions come after it
+    const unsigned same0 = __match_any_sync(kFull, r0), same1 = __match_any_sync(kFull, r1);
+    bool repeat = false;
+    if (a.k > 32)
+        for (int i = 0; i < 32; ++i) {
+            const int32_t other = __shfl_sync(kFull, r0, i);
+            repeat |= other == r1;
+        }
+    const bool take0 = in0 && (same0 & below) == 0u;
+    const bool take1 = in1 && (same1 & below) == 0u && !repeat;
+    const unsigned m0 = __ballot_sync(kFull, take0), m1 = __ballot_sync(kFull, take1);
+    const int nsel = __popc(m0) + __popc(m1);
+    if (take0) {
+        const int at = __popc(m0 & below);
+        u.sel[at] = r0;
+        u.slot[at] = lane;
+    }
+    if (take1) {
+        const int at = __popc(m0) + __popc(m1 & below);
+        u.sel[at] = r1;
+        u.slot[at] = lane + 32;
+    }
+    if (lane < kStep) u.sel[nsel + lane] = QSA_MAX_BLOCKS;
+    const bool any_bad = __any_sync(kFull, bad);
+    if (lane == 0) {
+        const int T = (nsel + kStep - 1) / kStep, p0 = rank * T / p.split, p1 = (rank + 1) * T / p.split;   // slices of whole steps
+        u.b0 = kStep * p0;
+        u.nloc = min(nsel, kStep * p1) - kStep * p0;
+        u.steps = p1 - p0;
+        u.ntok = ntok;
+        if (any_bad && g == 0 && rank == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_BAD_ID);
+    }
+    if (W && rank == 0) {   // slots that take no part
+        float *w = a.weights + ((size_t)qi * a.n_kv_heads + g) * a.k;
+        if (lane < a.k && !take0) w[lane] = 0.0f;
+        if (lane + 32 < a.k && !take1) w[lane + 32] = 0.0f;
+    }
+}
+
+// The preparation warp: the group's queries as e4m3 terms (four dimensions of a head per lane).
+template <bool F16, int TERMS>
+__device__ __forceinline__ void prepare_queries(const QParams &p, int qi, int g, int group, QUnit &u, uint8_t *sQ) {
+    const QAttnArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    const uint16_t *q = static_cast<const uint16_t *>(a.qa) + qi * a.q_stride + (int64_t)(g * group) * a.q_head_stride + lane * 4;
+#pragma unroll 1
+    for (int hh = 0; hh < kG; hh += 8) {
+        uint2 raw[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            raw[j] = hh + j < group ? *reinterpret_cast<const uint2 *>(q + (hh + j) * a.q_head_stride) : make_uint2(0u, 0u);
+        float sums[8];
+        int es[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int h = hh + j;
+            const float x[4] = {QFmt<F16>::lo(raw[j].x), QFmt<F16>::hi(raw[j].x), QFmt<F16>::lo(raw[j].y), QFmt<F16>::hi(raw[j].y)};
+            uint32_t big = 0u;   // the bits of the largest magnitude (an infinity or a NaN stays the largest)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+            big = __reduce_max_sync(kFull, big);
+            sums[j] = (x[0] + x[1]) + (x[2] + x[3]);
+            const bool finite = big < 0x7F800000u;
+            // a power of two that puts the largest magnitude into [128, 256), in two exact steps
+            const int e = finite && big != 0u ? 7 - ilogbf(__uint_as_float(big)) : 0;
+            es[j] = finite ? e : 1024;
+            const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
+            uint32_t terms[TERMS];
+            split_query<TERMS>(finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u,
+                               finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u, terms);
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t)
+                *reinterpret_cast<uint32_t *>(sQ + (t * kG + h) * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) =
+                    terms[t];
+        }
+        const float sum = warp_sum8(sums, lane);
+        int e = es[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) e = (lane >> 2) == j ? es[j] : e;
+        if ((lane & 3) == 0) {
+            const int h = hh + (lane >> 2);
+            u.f[h] = e == 1024 ? __uint_as_float(0x7FC00000u) : scalbnf(p.scale_log2, 9 - e);
+            u.qs[h] = p.scale_log2 * sum;
+        }
+    }
+}
 
 // F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted.
 template <bool F16, bool W>
-__global__ void __launch_bounds__(kThreads, 3) qattn_kernel(const __grid_constant__ QParams p) {
+__global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constant__ QParams p) {
     constexpr int TERMS = F16 ? 3 : 2;
     using L = QLayout<TERMS>;
     extern __shared__ uint8_t smem_raw[];
-    // offset, not rounded as a number: the compiler keeps knowing that this is shared memory
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sQ = smem + L::kOffQ, *sP = smem + L::kOffP, *ring = smem + L::kOffRing;
+    uint8_t *sQ = smem + L::kOffQ, *sP = smem + L::kOffP, *sK = smem + L::kOffK, *sV = smem + L::kOffV;
     QCtrl &ct = *reinterpret_cast<QCtrl *>(smem + L::kOffCtrl);
     volatile int *abort_flag = &ct.abort;
     const QAttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const int split = p.split, rank = split > 1 ? (int)cluster_ctarank() : 0;
-    const int unit = blockIdx.x / split;
-    const int qi = unit / a.n_kv_heads, g = unit - qi * a.n_kv_heads;
+    const int u0 = blockIdx.x / split, ustep = gridDim.x / split;
     const int group = a.n_heads / a.n_kv_heads, nb_cap = a.capacity / kQBlockTok;
-    const uint8_t *head_cache = static_cast<const uint8_t *>(a.cache) + qrec_offset(g, nb_cap, 0);
-    // one thread: the records of tile i (blocks b0 + 2i, b0 + 2i + 1 of sel) into its stage
-    auto fetch = [&](int i, int b0, int nloc) {
-        const int n = min(2, nloc - 2 * i), s = i % kStages;
-        mbar_expect_tx(&ct.full[s], (uint32_t)(n * kQRec));
-        for (int j = 0; j < n; ++j)
-            bulk_load(ring + s * kStageBytes + j * kQRec, head_cache + (size_t)ct.sel[b0 + 2 * i + j] * kQRec, kQRec,
-                      &ct.full[s]);
-    };
 
+    for (int i = tid; i < (int)(sizeof(QCtrl) / 4); i += kThreads) reinterpret_cast<uint32_t *>(&ct)[i] = 0u;
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.k_full[i], 1);
+            mbar_init(&ct.k_free[i], 8);  // the softmax warps: they read the pairs behind S, and so behind K's unpacking
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&ct.v_full[i], 1);
+            mbar_init(&ct.v_free[i], 4);  // the unpacking warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.sbar[i], 1);
+            mbar_init(&ct.ids_ready[i], 1);
+            mbar_init(&ct.ready[i], 1);
+            mbar_init(&ct.done[i], 15);   // all warps but the preparing one
+        }
+        mbar_init(&ct.obar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
     // a programmatic dependent of the work before it: nothing is read, and no tensor memory taken,
     // before that work is complete
-    if (warp == 8) {
-        if (lane == 0) {
-            for (int s = 0; s < kStages; ++s) mbar_init(&ct.full[s], 1);
-            mbar_init(&ct.sbar[0], 1);
-            mbar_init(&ct.sbar[1], 1);
-            mbar_init(&ct.obar, 1);
-            ct.abort = 0;
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    wait_prior_grid();
+    __syncwarp();
+
+    // Every role walks the same units (n-th unit u, buffer n & 1) and the same steps (t-th step, stage t & 1).
+    if (warp >= kControl) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kPrepare) {
+        for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
+            if (n >= 2) wait_all<256>(&ct.done[n & 1], ((uint32_t)(n >> 1) - 1u) & 1u, abort_flag);
+            const int qi = u / a.n_kv_heads, g = u - qi * a.n_kv_heads;
+            prepare_ids<W>(p, qi, g, rank, ct.unit[n & 1]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ct.ids_ready[n & 1]);
+            prepare_queries<F16, TERMS>(p, qi, g, group, ct.unit[n & 1], sQ + (n & 1) * L::kQBytes);
+            fence_proxy_async();   // the queries are read by the tensor core
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ct.ready[n & 1]);
         }
-        __syncwarp();
-        wait_prior_grid();
-        // the query's distinct ids inside its context, in slot order
-        const int32_t *ids = a.ids + (size_t)qi * a.k;
-        const int32_t r0 = lane < a.k ? ids[lane] : -1;
-        const int32_t r1 = lane + 32 < a.k ? ids[lane + 32] : -1;
-        int ntok = a.n_tokens[qi];
-        if (ntok < 0 || ntok > a.capacity) {
-            if (lane == 0 && g == 0 && rank == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_NBLOCKS_CLAMPED);
-            ntok = ntok < 0 ? 0 : a.capacity;
-        }
-        const int nb = (ntok + kQBlockTok - 1) / kQBlockTok;
-        const unsigned below = (1u << lane) - 1u;
-        const bool in0 = r0 >= 0 && r0 < nb, in1 = r1 >= 0 && r1 < nb;
-        const bool bad = (r0 != -1 && !in0) || (r1 != -1 && !in1);
-        // every lane takes part in every exchange; the conditions come after it
-        const unsigned same0 = __match_any_sync(kFull, r0), same1 = __match_any_sync(kFull, r1);
-        bool repeat = false;
-        if (a.k > 32)
-            for (int i = 0; i < 32; ++i) {
-                const int32_t other = __shfl_sync(kFull, r0, i);
-                repeat |= other == r1;
+    } else if (warp >= kFetch) {
+        // copies, a lane per block: the first warp K and the pairs, the second V
+        const bool is_k = warp == kFetch;
+        const int stages = is_k ? L::kKStages : kVStages;
+        const uint32_t bytes = is_k ? kKBytes : kVBytes;
+        uint64_t *full = is_k ? ct.k_full : ct.v_full, *vacant = is_k ? ct.k_free : ct.v_free;
+        int s = 0;
+        uint32_t lap = 0;
+        for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
+            wait_all<64>(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            const QUnit &un = ct.unit[n & 1];
+            const int steps = un.steps, nloc = un.nloc;
+            const uint8_t *head = static_cast<const uint8_t *>(a.cache) + qrec_offset(u % a.n_kv_heads, nb_cap, 0) + (is_k ? 0 : kQOffV);
+            for (int i = 0; i < steps; ++i) {
+                const int m = min(kStep, nloc - kStep * i);
+                const uint8_t *src = head + (size_t)un.sel[un.b0 + kStep * i + min(lane, m - 1)] * kQRec;
+                if (lap > 0) wait_all<32>(&vacant[s], (lap - 1u) & 1u, abort_flag);
+                if (__any_sync(kFull, *abort_flag != 0)) break;   // the stage may still be in use
+                if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)m * bytes);
+                __syncwarp();
+                if (lane < m) bulk_load((is_k ? sK : sV) + (s * kStep + lane) * bytes, src, bytes, &full[s]);
+                __syncwarp();
+                if (++s == stages) {
+                    s = 0;
+                    ++lap;
+                }
             }
-        const bool take0 = in0 && (same0 & below) == 0u;
-        const bool take1 = in1 && (same1 & below) == 0u && !repeat;
-        const unsigned m0 = __ballot_sync(kFull, take0), m1 = __ballot_sync(kFull, take1);
-        const int nsel = __popc(m0) + __popc(m1);
-        if (take0) {
-            const int at = __popc(m0 & below);
-            ct.sel[at] = r0;
-            ct.slot[at] = lane;
+            if (lane == 0) mbar_arrive(&ct.done[n & 1]);
+            __syncwarp();
         }
-        if (take1) {
-            const int at = __popc(m0) + __popc(m1 & below);
-            ct.sel[at] = r1;
-            ct.slot[at] = lane + 32;
-        }
-        const bool any_bad = __any_sync(kFull, bad);
-        if (lane == 0) {
-            ct.sel[nsel] = QSA_MAX_BLOCKS;
-            ct.nsel = nsel;
-            ct.ntok = ntok;
-            if (any_bad && g == 0 && rank == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_BAD_ID);
-        }
+        if (*abort_flag)   // copies in flight land before the memory is given back
+            for (int i = 0; i < stages; ++i) {
+                if (lap > 0 || i < s) mbar_drain(&full[i], (i < s ? lap : lap - 1u) & 1u);
+            }
         __syncwarp();
-        if (lane == 0) {   // the first tiles, before anything else is ready
-            const int T = (nsel + 1) >> 1, p0 = rank * T / split, tl = (rank + 1) * T / split - p0;
-            for (int i = 0; i < kStages && i < tl; ++i) fetch(i, 2 * p0, min(nsel - 2 * p0, 2 * tl));
-        }
-        __syncwarp();
-        tmem_alloc(&ct.tmem_base, L::kCols);
+    } else if (warp == kControl) {
+        tmem_alloc(&ct.tmem_base, kCols);
         tmem_relinquish();
-        if (W && rank == 0) {   // slots that take no part
-            float *w = a.weights + ((size_t)qi * a.n_kv_heads + g) * a.k;
-            if (lane < a.k && !take0) w[lane] = 0.0f;
-            if (lane + 32 < a.k && !take1) w[lane + 32] = 0.0f;
-        }
-    } else {   // the group's queries: sixteen threads per head, 8 dimensions each
-        if (W)
-            for (int i = tid; i < kSel * kG; i += kWork) (&ct.w[0][0])[i] = 0.0f;
-        wait_prior_grid();
-        const int h = tid >> 4, part = tid & 15;
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-        if (h < group) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.qa) + qi * a.q_stride +
-                                                             (int64_t)(g * group + h) * a.q_head_stride + part * 8);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = QFmt<F16>::lo(w[j]);
-                x[2 * j + 1] = QFmt<F16>::hi(w[j]);
-            }
-        }
-        uint32_t big = 0u;   // the bits of the largest magnitude (an infinity or a NaN stays the largest)
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-            sum += x[i];
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) {
-            big = max(big, __shfl_xor_sync(kFull, big, o));
-            sum += __shfl_xor_sync(kFull, sum, o);
-        }
-        const bool finite = big < 0x7F800000u;
-        // a power of two that puts the largest magnitude into [128, 256), in two exact steps
-        const int e = finite && big != 0u ? 7 - ilogbf(__uint_as_float(big)) : 0;
-        const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
-        uint32_t out[TERMS][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint16_t t[TERMS];
-            split_query<TERMS>(finite ? to_h2(x[2 * i] * s0 * s1, x[2 * i + 1] * s0 * s1) : 0u, t);
-#pragma unroll
-            for (int u = 0; u < TERMS; ++u) {
-                if (i & 1) out[u][i >> 1] |= (uint32_t)t[u] << 16;
-                else out[u][i >> 1] = t[u];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < TERMS; ++u)
-            *reinterpret_cast<uint2 *>(sQ + (u * kG + h) * 128 + (((part >> 1) ^ (h & 7)) << 4) + (part & 1) * 8) =
-                make_uint2(out[u][0], out[u][1]);
-        if (part == 0) {
-            ct.f[h] = finite ? scalbnf(p.scale_log2, 9 - e) : __uint_as_float(0x7FC00000u);
-            ct.qs[h] = p.scale_log2 * sum;
-            ct.nm[h] = 0.0f;
-            ct.top[h] = -INFINITY;
-        }
     }
-    fence_proxy_async();   // the queries are read by the tensor core
+    if (warp <= kControl) {
     tc_fence_before();
-    __syncthreads();
+    asm volatile("bar.sync 3, 416;" ::: "memory");   // the softmax, unpacking and control warps
     tc_fence_after();
     const uint32_t tmem = ct.tmem_base;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int nsel = ct.nsel, ntok = ct.ntok;
-    // this CTA's tiles: all of them, or a slice of a cluster's split
-    const int T = (nsel + 1) >> 1;
-    const int p0 = rank * T / split, tl = (rank + 1) * T / split - p0;
-    const int b0 = 2 * p0, nloc = min(nsel - b0, 2 * tl);
-    // Two warpgroups: both hold every token of a tile (and every dimension of O), one head half each.
-    // The first unpacks K, the second V.
-    const int wg = tid >> 7, row = tid & 127, half = row >> 6, tok = row & 63;
-    const int h0 = wg * kH;
-    f32x2 l[kH / 2], mv[kH / 2];
-    uint32_t left[kH / 2];                // fp16 pairs: 16 x what the rounding of this token's weights left
-#pragma unroll
-    for (int h = 0; h < kH / 2; ++h) {
-        l[h] = mv[h] = 0ull;
-        left[h] = 0u;
-    }
-    float e[kH];
-
-    if (warp == 8) {
-        // ---- control: S(i + 1) as soon as K(i + 1) is unpacked, O += P(i) V(i) when P(i) stands
-        const uint32_t id16 = idesc(0, 128, kG);
+    if (warp == kControl) {
         const uint64_t dq = sdesc(smem_u32(sQ)), dp = sdesc_mn(smem_u32(sP), 8 * kG, L::kTermP);
-        auto scores = [&](int i) {
+        int scored = 0, summed = 0;
+        auto scores = [&](int n, int t) {   // step t, of unit n
+            wait_all(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             k_ready_wait();
             tc_fence_after();
             if (elect_one()) {
+                const uint64_t d = dq + (n & 1) * (L::kQBytes / 16);   // descriptors count in units of 16 bytes
+                for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                for (int u = 0; u < TERMS; ++u)
+                    for (int x = 0; x < TERMS; ++x)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)   // descriptors count in units of 16 bytes
-                        mma_f8_ta(tmem + L::kColS + (i & 1) * kG, tmem + L::kColK + kk * 8, dq + u * (kG * 8) + kk * 2, id16,
-                                  (u | kk) != 0 ? 1u : 0u);
-                mma_commit(&ct.sbar[i & 1]);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_f8_ta(tmem + kColS + (t & 1) * 2 * kG + sub * kG, tmem + kColK + sub * 32 + kk * 8,
+                                      d + x * (kG * 8) + kk * 2, idesc(0, 128, kG), (x | kk) != 0 ? 1u : 0u);
+                mma_commit(&ct.sbar[t & 1]);
             }
             __syncwarp();
+            ++scored;
         };
-        if (tl > 0) scores(0);
-        for (int i = 0; i < tl; ++i) {
-            if (i + 1 < tl) scores(i + 1);
-            while (__syncthreads_or(0)) {}   // again while the references move
-            tc_fence_after();
-            if (elect_one()) {
+        bool primed = false;
+        for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
+            wait_all(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            const int steps = ct.unit[n & 1].steps;
+            if (steps == 0) primed = false;
+            // i = -1: the first step's S, unless it was issued behind the last unit's last step
+            for (int i = -1; i < steps; ++i) {
+                int of = n;                                // the unit of the next S
+                bool next = i < 0 ? steps > 0 && !primed : i + 1 < steps;
+                if (i + 1 == steps && steps > 0 && u + ustep < p.units) {
+                    of = n + 1;
+                    wait_all(&ct.ready[of & 1], (uint32_t)(of >> 1) & 1u, abort_flag);
+                    next = ct.unit[of & 1].steps > 0;
+                }
+                if (i + 1 == steps) primed = next && of != n;
+                if (next) scores(of, t + (i >= 0 ? 1 : 0));
+                if (i < 0) continue;
+                v_ready_wait();
+                while (vote_barrier(false)) {}             // again while the references move
+                tc_fence_after();
+                if (elect_one()) {
+                    for (int sub = 0; sub < 2; ++sub) {
+                        const uint64_t d = dp + (t % L::kPBufs) * (L::kStepP / 16) + sub * (L::kTileP / 16);
+                        const uint32_t v = tmem + kColV + sub * 32;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)   // both groups of columns
-                    mma_f8_ta(tmem + L::kColO, tmem + L::kColV + kk * 8, dp + kk * (2 * kG), idesc(0, 128, 2 * kG) | kIdescBMn,
-                              (i | kk) != 0 ? 1u : 0u);
-                if (TERMS == 3)
+                        for (int kk = 0; kk < 4; ++kk)   // both groups of columns
+                            mma_f8_ta(tmem + kColO, v + kk * 8, d + kk * (2 * kG), idesc(0, 128, 2 * kG) | kIdescBMn,
+                                      (i | sub | kk) != 0 ? 1u : 0u);
+                        if (TERMS == 3)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_f8_ta(tmem + L::kColO + kG, tmem + L::kColV + kk * 8, dp + 2 * (L::kTermP / 16) + kk * (2 * kG),
-                                  id16 | kIdescBMn, 1u);
-                mma_commit(&ct.obar);
-                if (i + kStages < tl) fetch(i + kStages, b0, nloc);   // every thread has read this stage
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_f8_ta(tmem + kColO + kG, v + kk * 8, d + 2 * (L::kTermP / 16) + kk * (2 * kG),
+                                          idesc(0, 128, kG) | kIdescBMn, 1u);
+                    }
+                    mma_commit(&ct.obar);
+                }
+                __syncwarp();
+                ++summed;
+                ++t;
             }
+            if (lane == 0) mbar_arrive(&ct.done[n & 1]);
+            __syncwarp();
+        }
+        if (ct.abort) {   // a wait gave up: let what is in flight land before the memory is freed
+            for (int i = max(0, scored - 2); i < scored; ++i) mbar_drain(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u);
+            if (summed > 0) mbar_drain(&ct.obar, (uint32_t)(summed - 1) & 1u);
+            __syncwarp();
+            if (lane == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_WAIT_TIMEOUT);
+        }
+    } else if (warp >= kUnpack) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        // ---- unpacking: a row of A per thread, 32 bytes of codes at a time to 8 + 8 columns (low and high nibbles)
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int q = warp & 3, row = (q << 5) | lane;
+        auto unpack = [&](const uint8_t *a0, const uint8_t *a1, uint32_t lo_col, uint32_t hi_col) {
+            const uint4 x0 = *reinterpret_cast<const uint4 *>(a0), x1 = *reinterpret_cast<const uint4 *>(a1);
+            const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            uint32_t lo[8], hi[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                lo[j] = w[j] & 0x0F0F0F0Fu;
+                hi[j] = (w[j] >> 4) & 0x0F0F0F0Fu;
+            }
+            tmem_st8(tmem + lanes + lo_col, lo);
+            tmem_st8(tmem + lanes + hi_col, hi);
+        };
+        // K of a step: block q's tokens `lane` (tile 0) and 32 + `lane` (tile 1), their 128 dimensions
+        auto unpack_k = [&](int t) {
+            const int s = t % L::kKStages;
+            wait_all<32>(&ct.k_full[s], (uint32_t)(t / L::kKStages) & 1u, abort_flag);
+            tc_fence_after();
+            const uint8_t *src = sK + (s * kStep + q) * kKBytes + lane * 16;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                unpack(src + sub * 512, src + sub * 512 + 1024, kColK + sub * 32, kColK + sub * 32 + 16);
+                unpack(src + sub * 512 + 2048, src + sub * 512 + 3072, kColK + sub * 32 + 8, kColK + sub * 32 + 24);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            k_ready_arrive();
+        };
+        bool primed = false;
+        for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
+            wait_all(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            const int steps = ct.unit[n & 1].steps;
+            if (steps == 0) primed = false;
+            for (int i = -1; i < steps; ++i) {             // as the control warp walks
+                int of = n;
+                bool next = i < 0 ? steps > 0 && !primed : i + 1 < steps;
+                if (i + 1 == steps && steps > 0 && u + ustep < p.units) {
+                    of = n + 1;
+                    wait_all(&ct.ready[of & 1], (uint32_t)(of >> 1) & 1u, abort_flag);
+                    next = ct.unit[of & 1].steps > 0;
+                }
+                if (i + 1 == steps) primed = next && of != n;
+                if (i >= 0) wait_all<32>(&ct.sbar[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);   // K(t) is read
+                if (next) unpack_k(t + (i >= 0 ? 1 : 0));
+                if (i < 0) continue;
+                const int s = t % kVStages;
+                wait_all(&ct.v_full[s], (uint32_t)(t / kVStages) & 1u, abort_flag);
+                if (t > 0) wait_all<32>(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);   // V(t - 1) is read
+                tc_fence_after();
+                // V: this thread's dimension; the blocks' tokens 0..31 are the low nibbles (tile 0)
+                const uint8_t *src = sV + s * kStep * kVBytes + row * 16;
+#pragma unroll
+                for (int b = 0; b < kStep; ++b)
+                    unpack(src + b * kVBytes, src + b * kVBytes + 2048, kColV + b * 8, kColV + 32 + b * 8);
+                if (lane == 0) mbar_arrive(&ct.v_free[s]);   // the stores are fed from registers
+                __syncwarp();
+                tmem_wait_st();
+                tc_fence_before();
+                v_ready_arrive();
+                ++t;
+            }
+            if (lane == 0) mbar_arrive(&ct.done[n & 1]);
             __syncwarp();
         }
     } else {
-    auto wait_full = [&](int i) { wait_all(&ct.full[i % kStages], (uint32_t)(i / kStages) & 1u, abort_flag); };
-    // 16 bytes of codes to 4 + 4 columns of a row of A
-    uint32_t lo[8], hi[8];
-    auto unpack = [&](const uint8_t *src, int at) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(src);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+    // ---- softmax: two threads per token pair, eight heads each.  Rows 32q .. 32q + 31 of both tiles are block
+    // q's tokens 0..31 and 32..63, so a warp holds tokens of one block only.
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int wg = warp >> 2, q = warp & 3, row = tid & 127;
+    const int h0 = wg * kH;
+    for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
+        const QUnit &un = ct.unit[n & 1];
+        wait_all(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+        const int steps = un.steps, nloc = un.nloc, ntok = un.ntok;
+        const int32_t *sel = un.sel + un.b0 + q;
+        f32x2 l[kH / 2], mv[kH / 2];
+        uint32_t left[kH / 2];            // fp16 pairs: 16 x what the rounding of this thread's weights left
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            lo[at + j] = w[j] & 0x0F0F0F0Fu;
-            hi[at + j] = (w[j] >> 4) & 0x0F0F0F0Fu;
+        for (int h = 0; h < kH / 2; ++h) {
+            l[h] = mv[h] = 0ull;
+            left[h] = 0u;
         }
-    };
-    auto unpack_k = [&](int i) {              // this thread's token, its 128 dimensions
-        wait_full(i);
-        tc_fence_after();
-        const uint8_t *src = ring + (i % kStages) * kStageBytes + half * kQRec + tok * 16;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            unpack(src + (2 * c) * 1024, 0);
-            unpack(src + (2 * c + 1) * 1024, 4);
-            tmem_st8(tmem + lanes + L::kColK + c * 8, lo);
-            tmem_st8(tmem + lanes + L::kColK + 16 + c * 8, hi);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        k_ready_arrive();
-    };
-    if (wg == 0 && tl > 0) unpack_k(0);
-    for (int i = 0; i < tl; ++i) {
-        const uint8_t *st = ring + (i % kStages) * kStageBytes;
-        const uint8_t *rec = st + half * kQRec;
-        if (wg == 0) {
-            wait_all(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag);   // S(i) is complete, K(i) read
-            if (i + 1 < tl) unpack_k(i + 1);
-            if (i > 0) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // P(i - 1) is read
-        } else {
-            wait_full(i);
-            if (i > 0) wait_all(&ct.obar, (uint32_t)(i - 1) & 1u, abort_flag);   // V(i - 1), P(i - 1) are read
+        for (int i = 0; i < steps; ++i, ++t) {
+            const int ks_at = t % L::kKStages;
+            // S(t) is complete; so is, two steps back, O += P(t - 2) V(t - 2), which the control warp issued before
+            // it, and K(t) with its pairs has landed (the unpacking warps waited for it)
+            wait_all(&ct.sbar[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);
+            if (L::kPBufs == 1 && t > 0) wait_all(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);   // P(t - 1) is read
             tc_fence_after();
+            bool vis[2];
+            float ks[2], km[2], vs[2], vm[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {     // this thread's dimension, the tokens of the two blocks
-                const uint8_t *src = st + b * kQRec + kQOffV + row * 16;
-                unpack(src, 0);
-                unpack(src + 2048, 4);
-                tmem_st8(tmem + lanes + L::kColV + b * 16, lo);
-                tmem_st8(tmem + lanes + L::kColV + b * 16 + 8, hi);
+            for (int sub = 0; sub < 2; ++sub) {
+                const uint8_t *rec = sK + (ks_at * kStep + q) * kKBytes + (32 * sub + lane) * 4;
+                vis[sub] = sel[kStep * i] * kQBlockTok + 32 * sub + lane < ntok;
+                const uint32_t kp = vis[sub] ? *reinterpret_cast<const uint32_t *>(rec + kQOffKPair) : 0u;
+                const uint32_t vp = vis[sub] ? *reinterpret_cast<const uint32_t *>(rec + kQOffVPair) : 0u;
+                ks[sub] = QFmt<F16>::lo(kp), km[sub] = QFmt<F16>::hi(kp);
+                vs[sub] = QFmt<F16>::lo(vp), vm[sub] = QFmt<F16>::hi(vp);
             }
-            wait_all(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag);
+            const bool all_vis = __all_sync(kFull, vis[1]);   // and so vis[0]
+            if (lane == 0) mbar_arrive(&ct.k_free[ks_at]);
+            __syncwarp();
+            // y = log2(e) s - m of this thread's tokens, into e
+            float e[2][kH];
+            auto logits = [&](const float *nmp) {
+                uint32_t v[2][kH];
+                tmem_ld8_nowait(tmem + lanes + kColS + (t & 1) * 2 * kG + h0, v[0]);
+                tmem_ld8_nowait(tmem + lanes + kColS + (t & 1) * 2 * kG + kG + h0, v[1]);
+                tmem_wait_ld();
+                reg_fence(v[0]);
+                reg_fence(v[1]);
+#pragma unroll
+                for (int h = 0; h < kH / 2; h += 2) {
+                    const ulonglong2 nm = *reinterpret_cast<const ulonglong2 *>(nmp + h0 + 2 * h);
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(un.f + h0 + 2 * h);
+                    const ulonglong2 qs = *reinterpret_cast<const ulonglong2 *>(un.qs + h0 + 2 * h);
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub) {
+                        const f32x2 ks2 = pack2(ks[sub], ks[sub]), km2 = pack2(km[sub], km[sub]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int x = 2 * (h + j);
+                            const f32x2 s2 = pack2(__uint_as_float(v[sub][x]), __uint_as_float(v[sub][x + 1]));
+                            const f32x2 y = fma2(mul2(s2, j ? f.y : f.x), ks2, fma2(km2, j ? qs.y : qs.x, j ? nm.y : nm.x));
+                            unpack2(y, e[sub][x], e[sub][x + 1]);
+                        }
+                    }
+                }
+                if (!all_vis)
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                        for (int h = 0; h < kH; ++h) e[sub][h] = vis[sub] ? e[sub][h] : -INFINITY;
+            };
+            int renew = i == 0 ? 1 : 0;       // 1: the references move before the weights are made; 2: they have
+            while (true) {
+                logits(i == 0 && renew == 1 ? ct.zero : ct.nm);
+                if (renew == 1) {
+                    // new references: the largest exponent and the largest weight so far, per head
+                    const float lv0 = vs[0] == 0.0f ? -INFINITY : lg2(vs[0]), lv1 = vs[1] == 0.0f ? -INFINITY : lg2(vs[1]);
+                    uint32_t mine[2] = {0u, 0u};
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) {
+                        uint32_t y = score_key(e[0][h]), r = score_key(e[0][h] + lv0);
+                        y = max(y, score_key(e[1][h]));
+                        r = max(r, score_key(e[1][h] + lv1));
+                        y = __reduce_max_sync(kFull, y);
+                        r = __reduce_max_sync(kFull, r);
+                        if (lane == h) {
+                            mine[0] = y;
+                            mine[1] = r;
+                        }
+                    }
+                    if (lane < kH) {
+                        ct.red[0][warp & 3][h0 + lane] = mine[0];
+                        ct.red[1][warp & 3][h0 + lane] = mine[1];
+                    }
+                    work_barrier();
+                    if (warp == 0) {
+                        const int h = lane & 15;
+                        uint32_t y = 0u, r = 0u;
+                        for (int w = 0; w < 4; ++w) {
+                            y = max(y, ct.red[0][w][h]);
+                            r = max(r, ct.red[1][w][h]);
+                        }
+                        const float m0 = i == 0 ? 0.0f : -ct.nm[h], rise = key_float(y);
+                        const float m1 = i == 0 ? rise : m0 + fmaxf(rise, 0.0f);
+                        const float top = fmaxf(i == 0 ? -INFINITY : ct.top[h], m0 + key_float(r));
+                        // nothing but zero scales so far: any other one will pass the limit
+                        const float eg = top == -INFINITY ? 60.0f : fminf(fmaxf(kTop - ceilf(top - m1), -126.0f), 126.0f);
+                        const float fl = i == 0 ? 1.0f : exp2f(m0 - m1);
+                        const float fo = i == 0 ? 1.0f : fl * exp2f(fminf(fmaxf(eg - ct.eg[h], -126.0f), 126.0f));
+                        float least = eg;
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, o));
+                        __syncwarp();
+                        if (lane < kG) {
+                            ct.fl[h] = fl;
+                            ct.fo[h] = fo;
+                            ct.nm[h] = -m1;
+                            ct.top[h] = top;
+                            ct.eg[h] = eg;
+                            ct.g[h] = exp2f(eg);
+                            if (lane == 0) ct.least_g = exp2f(least);
+                        }
+                    }
+                    work_barrier();
+                    if (i > 0) {   // what is summed so far, to the new references
+                        wait_all(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);   // O(t - 1) is complete
+                        tc_fence_after();
+#pragma unroll
+                        for (int h = 0; h < kH / 2; ++h) {
+                            const f32x2 fl = reinterpret_cast<const f32x2 *>(ct.fl + h0)[h];
+                            const float2 fo = reinterpret_cast<const float2 *>(ct.fo + h0)[h];
+                            l[h] = mul2(l[h], fl);
+                            mv[h] = mul2(mv[h], fl);
+                            if (TERMS == 2) left[h] = to_h2(h2_lo(left[h]) * fo.x, h2_hi(left[h]) * fo.y);
+                        }
+                        if (W)
+                            for (int j = tid; j < kStep * i * kG; j += kWork) (&ct.w[0][0])[j] *= ct.fl[j % kG];
+                        uint32_t o[kH];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            tmem_ld8_nowait(tmem + lanes + kColO + x * kG + h0, o);
+                            tmem_wait_ld();
+                            reg_fence(o);
+#pragma unroll
+                            for (int h = 0; h < kH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * ct.fo[h0 + h]);
+                            tmem_st8(tmem + lanes + kColO + x * kG + h0, o);
+                        }
+                        tmem_wait_st();
+                    }
+                    renew = 2;
+                    continue;
+                }
+                // p = 2^y, and the weights p vs g in terms to shared memory: [tile][term][token][head]
+                bool over = false;
+                const float faint = fminf(vis[0] ? vs[0] : 1.0f, vis[1] ? vs[1] : 1.0f) * ct.least_g;
+                if (__any_sync(kFull, faint < kFaint)) {   // p may grow where the weights do not
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) over |= fmaxf(e[0][h], e[1][h]) > kMostY;
+                }
+                uint32_t hmax = 0u, rest[kH / 2];
+#pragma unroll
+                for (int h = 0; h < kH / 2; ++h) rest[h] = 0u;
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) {
+                    const f32x2 vs2 = pack2(vs[sub], vs[sub]);
+                    uint32_t word[2][TERMS];
+#pragma unroll
+                    for (int h = 0; h < kH; h += 4) {
+                        float w[4];
+                        uint32_t h2[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float &e0 = e[sub][h + 2 * j], &e1 = e[sub][h + 2 * j + 1];
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            const f32x2 w2 = mul2(mul2(pack2(e0, e1), vs2), reinterpret_cast<const f32x2 *>(ct.g + h0 + h)[j]);
+                            unpack2(w2, w[2 * j], w[2 * j + 1]);
+                            h2[j] = to_h2(w[2 * j], w[2 * j + 1]);
+                            hmax = h2_max(hmax, h2[j]);
+                        }
+                        uint32_t r[2] = {rest[h / 2], rest[h / 2 + 1]};
+                        split_weights<TERMS>(w, h2, word[h / 4], r);
+                        rest[h / 2] = r[0];
+                        rest[h / 2 + 1] = r[1];
+                    }
+#pragma unroll
+                    for (int y = 0; y < TERMS; ++y)
+                        *reinterpret_cast<uint2 *>(sP + (t % L::kPBufs) * L::kStepP + sub * L::kTileP + y * L::kTermP + row * kG + h0) =
+                            make_uint2(word[0][y], word[1][y]);
+                }
+                over = renew == 0 && (over || h2_lo(hmax) > kMostWeight || h2_hi(hmax) > kMostWeight);
+                fence_proxy_async();   // the weights are read by the tensor core
+                tc_fence_before();
+                if (!vote_barrier(over)) {
+                    if (TERMS == 2)
+#pragma unroll
+                        for (int h = 0; h < kH / 2; ++h) left[h] = h2_add(left[h], rest[h]);
+                    break;
+                }
+                renew = 1;
+            }
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const f32x2 vm2 = pack2(vm[sub], vm[sub]);
+#pragma unroll
+                for (int h = 0; h < kH / 2; ++h) {
+                    const f32x2 e2 = pack2(e[sub][2 * h], e[sub][2 * h + 1]);
+                    l[h] = add2(l[h], e2);
+                    mv[h] = fma2(e2, vm2, mv[h]);
+                }
+            }
+            if (W) {   // this block's sums: no other warp has this block and these heads
+                float x[kH];
+#pragma unroll
+                for (int h = 0; h < kH; ++h) x[h] = e[0][h] + e[1][h];
+                const float w = warp_sum8(x, lane);
+                if ((lane & 3) == 0) ct.w[kStep * i + q][h0 + (lane >> 2)] = w;
+            }
         }
-        tc_fence_after();
-        const bool vis = ct.sel[b0 + 2 * i + half] * kQBlockTok + tok < ntok;
-        const uint32_t kp = vis ? *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + tok * 4) : 0u;
-        const uint32_t vp = vis ? *reinterpret_cast<const uint32_t *>(rec + kQOffVPair + tok * 4) : 0u;
-        const float ks = QFmt<F16>::lo(kp), km = QFmt<F16>::hi(kp);
-        const float vs = QFmt<F16>::lo(vp), vm = QFmt<F16>::hi(vp);
-        const bool all_vis = __all_sync(kFull, vis);
-        // y = log2(e) s - m of this token, into e
-        auto logits = [&]() {
-            uint32_t v[kH];
-            tmem_ld8_nowait(tmem + lanes + L::kColS + (i & 1) * kG + h0, v);
-            tmem_wait_ld();
-            reg_fence(v);
-            const f32x2 ks2 = pack2(ks, ks), km2 = pack2(km, km);
-#pragma unroll
-            for (int h = 0; h < kH / 2; h += 2) {
-                const ulonglong2 nm = *reinterpret_cast<const ulonglong2 *>(ct.nm + h0 + 2 * h);
-                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(ct.f + h0 + 2 * h);
-                const ulonglong2 qs = *reinterpret_cast<const ulonglong2 *>(ct.qs + h0 + 2 * h);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int x = 2 * (h + j);
-                    f32x2 t = pack2(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-                    t = fma2(mul2(t, j ? f.y : f.x), ks2, fma2(km2, j ? qs.y : qs.x, j ? nm.y : nm.x));
-                    unpack2(t, e[x], e[x + 1]);
-                }
-            }
-            if (!all_vis)
-#pragma unroll
-                for (int h = 0; h < kH; ++h) e[h] = vis ? e[h] : -INFINITY;
-        };
-        bool renew = i == 0;
-        while (true) {
-            logits();
-            if (renew) {
-                // new references: the largest exponent and the largest weight so far, per head
-                const float lv = vs == 0.0f ? -INFINITY : lg2(vs);
-                uint32_t mine[2] = {0u, 0u};
-#pragma unroll
-                for (int h = 0; h < kH; ++h) {
-                    const uint32_t y = __reduce_max_sync(kFull, score_key(e[h]));
-                    const uint32_t r = __reduce_max_sync(kFull, score_key(e[h] + lv));
-                    if (lane == h) {
-                        mine[0] = y;
-                        mine[1] = r;
-                    }
-                }
-                if (lane < kH) {
-                    ct.red[0][warp & 3][h0 + lane] = mine[0];
-                    ct.red[1][warp & 3][h0 + lane] = mine[1];
-                }
-                work_barrier();
-                if (warp == 0) {
-                    const int h = lane & 15;
-                    uint32_t y = 0u, r = 0u;
-                    for (int w = 0; w < 4; ++w) {
-                        y = max(y, ct.red[0][w][h]);
-                        r = max(r, ct.red[1][w][h]);
-                    }
-                    const float m0 = -ct.nm[h], rise = key_float(y);
-                    const float m1 = i == 0 ? rise : m0 + fmaxf(rise, 0.0f);
-                    const float top = fmaxf(ct.top[h], m0 + key_float(r));
-                    // nothing but zero scales so far: any other one will pass the limit
-                    const float eg = top == -INFINITY ? 60.0f : fminf(fmaxf(kTop - ceilf(top - m1), -126.0f), 126.0f);
-                    const float fl = i == 0 ? 1.0f : exp2f(m0 - m1);
-                    const float fo = i == 0 ? 1.0f : fl * exp2f(fminf(fmaxf(eg - ct.eg[h], -126.0f), 126.0f));
-                    float least = eg;
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, o));
-                    __syncwarp();
-                    if (lane < kG) {
-                        ct.fl[h] = fl;
-                        ct.fo[h] = fo;
-                        ct.nm[h] = -m1;
-                        ct.top[h] = top;
-                        ct.eg[h] = eg;
-                        ct.g[h] = exp2f(eg);
-                        if (lane == 0) ct.least_g = exp2f(least);
-                    }
-                }
-                work_barrier();
-                if (i > 0) {   // what is summed so far, to the new references (O(i - 1) is complete)
-#pragma unroll
-                    for (int h = 0; h < kH / 2; ++h) {
-                        const f32x2 fl = reinterpret_cast<const f32x2 *>(ct.fl + h0)[h];
-                        const float2 fo = reinterpret_cast<const float2 *>(ct.fo + h0)[h];
-                        l[h] = mul2(l[h], fl);
-                        mv[h] = mul2(mv[h], fl);
-                        if (TERMS == 2) left[h] = to_h2(h2_lo(left[h]) * fo.x, h2_hi(left[h]) * fo.y);
-                    }
-                    if (W)
-                        for (int j = tid; j < 2 * i * kG; j += kWork) (&ct.w[0][0])[j] *= ct.fl[j % kG];
-                    uint32_t o[kH];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o);
-                        tmem_wait_ld();
-                        reg_fence(o);
-#pragma unroll
-                        for (int h = 0; h < kH; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * ct.fo[h0 + h]);
-                        tmem_st8(tmem + lanes + L::kColO + u * kG + h0, o);
-                    }
-                }
-                logits();
-            }
-            // p = 2^y, and the weights p vs g in terms to shared memory: [term][token][head]
-            bool over = false;
-            if (__any_sync(kFull, vis && vs * ct.least_g < kFaint)) {   // p may grow where the weights do not
-#pragma unroll
-                for (int h = 0; h < kH; ++h) over |= e[h] > kMostY;
-            }
-            uint32_t hmax = 0u, word[TERMS][2];
-            uint32_t rest[kH / 2];
-            const f32x2 vs2 = pack2(vs, vs);
-#pragma unroll
-            for (int h = 0; h < kH / 2; ++h) {
-                e[2 * h] = ex2(e[2 * h]);
-                e[2 * h + 1] = ex2(e[2 * h + 1]);
-                const f32x2 w2 = mul2(mul2(pack2(e[2 * h], e[2 * h + 1]), vs2), reinterpret_cast<const f32x2 *>(ct.g + h0)[h]);
-                float w0, w1;
-                unpack2(w2, w0, w1);
-                const uint32_t h2 = to_h2(w0, w1);
-                hmax = h2_max(hmax, h2);
-                uint16_t t[TERMS];
-                rest[h] = split_weights<TERMS>(w0, w1, h2, t);
-#pragma unroll
-                for (int u = 0; u < TERMS; ++u) {
-                    if (h & 1) word[u][h >> 1] |= (uint32_t)t[u] << 16;
-                    else word[u][h >> 1] = t[u];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < TERMS; ++u)
-                *reinterpret_cast<uint2 *>(sP + u * L::kTermP + row * kG + h0) = make_uint2(word[u][0], word[u][1]);
-            over = !renew && (over || h2_lo(hmax) > kMostWeight || h2_hi(hmax) > kMostWeight);
-            fence_proxy_async();   // the weights are read by the tensor core
-            tmem_wait_st();
-            tc_fence_before();
-            if (!__syncthreads_or(over)) {
-                if (TERMS == 2)
-#pragma unroll
-                    for (int h = 0; h < kH / 2; ++h) left[h] = h2_add(left[h], rest[h]);
-                break;
-            }
-            renew = true;
-        }
-        const f32x2 vm2 = pack2(vm, vm);
-#pragma unroll
-        for (int h = 0; h < kH / 2; ++h) {
-            const f32x2 e2 = pack2(e[2 * h], e[2 * h + 1]);
-            l[h] = add2(l[h], e2);
-            mv[h] = fma2(e2, vm2, mv[h]);
-        }
-        if (W) {   // two warps per block and head half: their sum does not depend on which comes first
-            const float w = warp_sum8(e, lane);
-            if ((lane & 3) == 0 && 2 * i + half < nloc) atomicAdd(&ct.w[2 * i + half][h0 + (lane >> 2)], w);
-        }
-    }
 
-    // ---- sums over the token lanes
-    {
-        float x[3][kH];
+        // ---- the unit's end: sums over the token lanes, outputs
+        const int qi = u / a.n_kv_heads, g = u - qi * a.n_kv_heads;
+        const size_t head0 = (size_t)qi * a.n_heads + (size_t)g * group;
+        auto put = [&](int h, float x) {   // a warp's stores for one head are 32 neighbours
+            const size_t at = (head0 + h) * kQDim + row;
+            if (a.out_dt == QSA_F32) static_cast<float *>(a.out)[at] = x;
+            else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits(x);
+        };
+        if (steps > 0) {
+            float x[kH];
 #pragma unroll
-        for (int h = 0; h < kH / 2; ++h) {
-            unpack2(l[h], x[0][2 * h], x[0][2 * h + 1]);
-            unpack2(mv[h], x[1][2 * h], x[1][2 * h + 1]);
-            x[2][2 * h] = h2_lo(left[h]);
-            x[2][2 * h + 1] = h2_hi(left[h]);
-        }
-        work_barrier();   // every thread has read ct.red
+            for (int j = 0; j < 3; ++j) {
+                if (j == 2 && TERMS == 3) break;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-            if (j == 2 && TERMS == 3) break;
-            const float sum = warp_sum8(x[j], lane);
-            if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = __float_as_uint(sum);
+                for (int h = 0; h < kH / 2; ++h) {
+                    if (j < 2) {
+                        unpack2(j ? mv[h] : l[h], x[2 * h], x[2 * h + 1]);
+                    } else {
+                        x[2 * h] = h2_lo(left[h]);
+                        x[2 * h + 1] = h2_hi(left[h]);
+                    }
+                }
+                const float sum = warp_sum8(x, lane);
+                if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = __float_as_uint(sum);
+            }
+            work_barrier();
+            if (tid < 3 * kG) {
+                const int j = tid / kG, h = tid % kG;
+                float sum = 0.0f;
+                if (j < 2 || TERMS == 2)
+                    for (int w = 0; w < 4; ++w) sum += __uint_as_float(ct.red[j][w][h]);
+                ct.sum[j][h] = sum;
+                if (j == 0) ct.inv[h] = 1.0f / sum;
+            }
+            work_barrier();
+            wait_all(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);
+            tc_fence_after();
+            uint32_t o[2][kH];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tmem_ld8_nowait(tmem + lanes + kColO + j * kG + h0, o[j]);
+            tmem_wait_ld();
+            reg_fence(o[0]);
+            reg_fence(o[1]);
+            tc_fence_before();
+            // this thread's dimension of its heads.  The codes' mean, 7.5, times what the rounding left of
+            // the weights takes most of its effect away.
+#pragma unroll
+            for (int j = 0; j < kH; ++j) {
+                const int h = h0 + j;
+                float y = fmaf(__uint_as_float(o[1][j]), 0.0625f, __uint_as_float(o[0][j]));
+                y = fmaf(fmaf(y, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), exp2f(-ct.eg[h]), ct.sum[1][h]);
+                if (split > 1) reinterpret_cast<float *>(sK)[h * kQDim + row] = y;
+                else if (h < group) put(h, y * ct.inv[h]);
+            }
+            if (split == 1) {
+                if (a.lse && tid < group) a.lse[head0 + tid] = (log2f(ct.sum[0][tid]) - ct.nm[tid]) * 0.6931471805599453f;
+                if (W && tid >= 64 && tid - 64 < nloc) {
+                    const float4 *w4 = reinterpret_cast<const float4 *>(ct.w[tid - 64]);
+                    const float4 *i4 = reinterpret_cast<const float4 *>(ct.inv);
+                    float w = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < kG / 4; ++j) {
+                        const float4 x4 = w4[j], y4 = i4[j];
+                        w += 4 * j < group ? x4.x * y4.x : 0.0f;
+                        w += 4 * j + 1 < group ? x4.y * y4.y : 0.0f;
+                        w += 4 * j + 2 < group ? x4.z * y4.z : 0.0f;
+                        w += 4 * j + 3 < group ? x4.w * y4.w : 0.0f;
+                    }
+                    a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + un.slot[tid - 64]] = w;
+                }
+            }
+        } else if (split == 1) {   // no visible token: o = 0
+            for (int h = h0; h < min(group, h0 + kH); ++h) put(h, 0.0f);
+            if (a.lse && tid < group) a.lse[head0 + tid] = -INFINITY;
         }
-        work_barrier();
-        if (tid < 3 * kG) {
-            const int j = tid / kG, h = tid % kG;
-            float sum = 0.0f;
-            if (j < 2 || TERMS == 2)
-                for (int w = 0; w < 4; ++w) sum += __uint_as_float(ct.red[j][w][h]);
-            ct.sum[j][h] = sum;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ct.done[n & 1]);
+    }
     }
     }
     __syncthreads();
-    const size_t head0 = (size_t)qi * a.n_heads + (size_t)g * group;
-    auto put = [&](int h, int d, float x) {
-        const size_t at = (head0 + h) * kQDim + d;
-        if (a.out_dt == QSA_F32) static_cast<float *>(a.out)[at] = x;
-        else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits(x);
-    };
-    float *part = reinterpret_cast<float *>(ring);   // split: this CTA's unnormalised output [16][128]
-    if (warp == 8) {
-    } else if (tl > 0) {
-        wait_all(&ct.obar, (uint32_t)(tl - 1) & 1u, abort_flag);
-        tc_fence_after();
-        uint32_t o[2][kH];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) tmem_ld8_nowait(tmem + lanes + L::kColO + u * kG + h0, o[u]);
-        tmem_wait_ld();
-        reg_fence(o[0]);
-        reg_fence(o[1]);
-        // this thread's dimension of its heads (a warp's stores for one head are 32 neighbours).  The codes'
-        // mean, 7.5, times what the rounding left of the weights takes most of its effect away.
-#pragma unroll
-        for (int j = 0; j < kH; ++j) {
-            const int h = h0 + j;
-            float x = fmaf(__uint_as_float(o[1][j]), 0.0625f, __uint_as_float(o[0][j]));
-            x = fmaf(fmaf(x, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), exp2f(-ct.eg[h]), ct.sum[1][h]);
-            if (split > 1) part[h * kQDim + row] = x;
-            else if (h < group) put(h, row, x / ct.sum[0][h]);
-        }
-        tc_fence_before();
-    } else if (split == 1) {   // no visible token: o = 0
-        for (int h = h0; h < min(group, h0 + kH); ++h) put(h, row, 0.0f);
-    }
-    if (tid == 0 && ct.abort) {   // a wait gave up: let what is in flight land before the memory is freed
-        for (int i = max(0, tl - kStages); i < tl; ++i) mbar_drain(&ct.full[i % kStages], (uint32_t)(i / kStages) & 1u);
-        for (int i = max(0, tl - 2); i < tl; ++i) mbar_drain(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u);
-        mbar_drain(&ct.obar, (uint32_t)(tl - 1) & 1u);
-        if (a.flags) atomicOr(a.flags, QSA_FLAG_WAIT_TIMEOUT);
-    }
-    if (split == 1) {
-        if (a.lse && tid < group)
-            a.lse[head0 + tid] = tl > 0 ? (log2f(ct.sum[0][tid]) - ct.nm[tid]) * 0.6931471805599453f : -INFINITY;
-        if (W && tid < nloc) {
-            float w = 0.0f;
-            for (int h = 0; h < group; ++h) w += ct.w[tid][h] / ct.sum[0][h];
-            a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + ct.slot[tid]] = w;
-        }
-    }
-    __syncthreads();
-    if (warp == 8) {
+    if (warp == kControl) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, L::kCols);
+        tmem_dealloc(ct.tmem_base, kCols);
     }
-    if (split > 1) {
+    if (split > 1) {   // one unit per cluster
         // every CTA sends each head's partial output to the CTA that combines that head, and its (m, l)
         // to all; after the barrier each combines from its own memory
+        const QUnit &un = ct.unit[0];
+        const int qi = u0 / a.n_kv_heads, g = u0 - qi * a.n_kv_heads;
+        const size_t head0 = (size_t)qi * a.n_heads + (size_t)g * group;
+        const bool some = un.steps > 0;
         const int nh = kG / split;
+        float *part = reinterpret_cast<float *>(sK);                 // this CTA's unnormalised output [16][128]
         float *recv = part + kG * kQDim;                             // [split][nh][128]
-        const float none = -INFINITY;
         cluster_sync();
-        if (tl > 0)
+        if (some)
             for (int x = tid; x < kG * 32; x += kThreads) {
                 const int h = x >> 5, d4 = x & 31;
                 st_cluster(reinterpret_cast<float4 *>(recv + (rank * nh + h % nh) * kQDim) + d4, h / nh,
@@ -795,25 +1022,28 @@ __global__ void __launch_bounds__(kThreads, 3) qattn_kernel(const __grid_constan
             }
         for (int x = tid; x < kG * split; x += kThreads) {
             const int h = x % kG;
-            st_cluster(&ct.ml[rank][h], x / kG, make_float2(tl > 0 ? -ct.nm[h] : none, tl > 0 ? ct.sum[0][h] : 0.0f));
+            st_cluster(&ct.ml[rank][h], x / kG, make_float2(some ? -ct.nm[h] : -INFINITY, some ? ct.sum[0][h] : 0.0f));
         }
         cluster_sync();
-        for (int hh = wg; wg < 2 && hh < nh; hh += 2) {
-            const int h = rank * nh + hh;
+        for (int x = tid; x < nh * kQDim; x += kThreads) {
+            const int hh = x >> 7, d = x & 127, h = rank * nh + hh;
             float M = -INFINITY, Lsum = 0.0f, acc = 0.0f;
             for (int r = 0; r < split; ++r)
                 if (ct.ml[r][h].y != 0.0f) M = fmaxf(M, ct.ml[r][h].x);
             for (int r = 0; r < split; ++r) {
                 const float2 v = ct.ml[r][h];
-                if (v.y != 0.0f) {   // a CTA without tiles took no part
+                if (v.y != 0.0f) {   // a CTA without tokens took no part
                     const float f = exp2f(v.x - M);
                     Lsum = fmaf(f, v.y, Lsum);
-                    acc = fmaf(f, recv[(r * nh + hh) * kQDim + row], acc);
+                    acc = fmaf(f, recv[(r * nh + hh) * kQDim + d], acc);
                 }
             }
             if (h < group) {
-                put(h, row, Lsum != 0.0f ? acc / Lsum : 0.0f);
-                if (a.lse && row == 0) a.lse[head0 + h] = Lsum != 0.0f ? (M + log2f(Lsum)) * 0.6931471805599453f : -INFINITY;
+                const size_t at = (head0 + h) * kQDim + d;
+                const float y = Lsum != 0.0f ? acc / Lsum : 0.0f;
+                if (a.out_dt == QSA_F32) static_cast<float *>(a.out)[at] = y;
+                else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits(y);
+                if (a.lse && d == 0) a.lse[head0 + h] = Lsum != 0.0f ? (M + log2f(Lsum)) * 0.6931471805599453f : -INFINITY;
             }
         }
         if (W) {
@@ -823,13 +1053,13 @@ __global__ void __launch_bounds__(kThreads, 3) qattn_kernel(const __grid_constan
                     if (ct.ml[r][tid].y != 0.0f) M = fmaxf(M, ct.ml[r][tid].x);
                 for (int r = 0; r < split; ++r)
                     if (ct.ml[r][tid].y != 0.0f) Lsum = fmaf(exp2f(ct.ml[r][tid].x - M), ct.ml[r][tid].y, Lsum);
-                ct.fl[tid] = tl > 0 ? exp2f(-ct.nm[tid] - M) / Lsum : 0.0f;
+                ct.fl[tid] = some ? exp2f(-ct.nm[tid] - M) / Lsum : 0.0f;
             }
             __syncthreads();
-            if (tid < nloc) {
+            if (tid < un.nloc) {
                 float w = 0.0f;
                 for (int h = 0; h < group; ++h) w = fmaf(ct.w[tid][h], ct.fl[h], w);
-                a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + ct.slot[b0 + tid]] = w;
+                a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + un.slot[un.b0 + tid]] = w;
             }
         }
     }
@@ -880,10 +1110,12 @@ qsa_status launch_qcache_attention(const QAttnArgs &a, cudaStream_t s) {
     // few units: split each unit's tiles over a cluster, doubling while the grid stays within two CTAs
     // per SM
     const long long units = (long long)a.nq * a.n_kv_heads;
-    const int tiles = (a.k + 1) / 2;
+    const int tiles = (a.k + kStep - 1) / kStep;
     p.split = 1;
     while (p.split < kMaxSplit && p.split * 2 <= tiles && units * p.split * 2 <= 2ll * num_sms()) p.split *= 2;
-    const int grid = (int)(units * p.split);
+    p.units = (int)units;
+    const long long most = p.split > 1 ? units : 2ll * num_sms();
+    const int grid = (int)(units < most ? units : most) * p.split;
     if (a.dt == QSA_F16) return a.weights ? launch_as<true, true>(p, grid, s) : launch_as<true, false>(p, grid, s);
     return a.weights ? launch_as<false, true>(p, grid, s) : launch_as<false, false>(p, grid, s);
 }
