@@ -358,7 +358,7 @@ qsa_status qsa_vcache_transpose(const void *v, void *vcache_t, int n_kv_heads, i
  *     x ~ scale * code + min,   min = min(x),   scale = least 16-bit number >= (max(x) - min(x)) / 15,
  *     code = (x - min) / scale rounded half to even (0 when scale is 0),
  * so |x - (scale * code + min)| <= scale / 2.  scale and min are held in the rows' own
- * 16-bit format (bf16 or fp16).  A row that holds an infinity or a NaN, or whose range
+ * 16-bit format (bf16 or fp16; a minimum of -0 as +0).  A row that holds an infinity or a NaN, or whose range
  * is not finite in fp32, is stored as scale = min = NaN and reads as NaN.
  *
  * Memory: cache [n_kv_heads][capacity / 64][QSA_QCACHE_BLOCK_BYTES], 16-byte aligned, one
@@ -405,8 +405,8 @@ qsa_status qsa_qcache_append(const void *k, int64_t k_token_stride, int64_t k_he
                              size_t ws_bytes, qsa_stream stream);
 
 /*
- * The rows of positions first .. first + n - 1 back in 16 bits (scale * code + min in fp32,
- * rounded once to `dt`), into k and v addressed as for qsa_qcache_append.
+ * The rows of positions first .. first + n - 1 back in 16 bits (scale * code + min rounded once
+ * to `dt`), into k and v addressed as for qsa_qcache_append.
  * Errors: as qsa_qcache_append's.
  */
 qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int head_dim, int capacity, int first,

@@ -42,7 +42,7 @@ def quantise(x: np.ndarray, fmt: str):
         lo, hi = x.min(-1), x.max(-1)
         wide = np.float64(np.finfo(np.float32).max)
         bad = ~(np.isfinite(x).all(-1)) | ~(hi - lo <= wide)
-    lo, rng = np.where(bad, 0.0, lo), np.where(bad, 0.0, hi - lo)
+    lo, rng = np.where(bad, 0.0, lo) + 0.0, np.where(bad, 0.0, hi - lo)
     scale = round_up(rng / 15, fmt)
     with np.errstate(invalid="ignore", divide="ignore"):
         y = np.where((scale > 0)[..., None], (np.where(bad[..., None], 0.0, x) - lo[..., None]) / scale[..., None], 0.0)

@@ -9,9 +9,10 @@
 // One CTA (256 threads) per (KV head, block of 64 tokens), four threads per token: thread
 // c of a token holds dimensions 16c .. 16c + 15 and 64 + 16c .. 64 + 16c + 15, which is
 // one 16-byte row of K plane c, so K goes from registers to the cache.  V is stored
-// dimension-major: its codes pass through shared memory once, and each thread writes
-// one 16-byte row of a V plane.  A CTA owns its whole block, so a partial block's other
-// tokens (the other nibbles of shared bytes) are merged without atomics.
+// dimension-major: its codes pass through shared memory as bytes, are transposed four by four
+// with byte permutes and exchanged among four lanes, and leave as whole 16-byte rows.  A CTA
+// owns its whole block, so a partial block's other tokens (the other nibbles of shared bytes)
+// are merged without atomics.
 #include <cfloat>
 
 #include "qcache.cuh"
@@ -21,7 +22,7 @@ namespace qsa {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int kPitch = 144;   // bytes per token of the staged V codes (16-byte rows, 4-bank steps)
+constexpr int kPitch = 136;   // bytes per token of the staged V codes: rows four apart start 8 banks apart
 
 struct RowPtr {
     const uint8_t *p;
@@ -60,37 +61,44 @@ __device__ __noinline__ int exact_code(float x, float lo, float scale) {
     return min(max((int)c, 0), 15);
 }
 
-// One thread's 32 values of a row (16 dimensions from 16c, 16 from 64 + 16c).
-template <bool F16>
-__device__ __forceinline__ void load_row(const uint8_t *row, int c, float (&x)[32]) {
+// One thread's 32 values of a row as 16 pairs (16 dimensions from 16c, 16 from 64 + 16c).
+__device__ __forceinline__ void load_row(const uint8_t *row, int c, uint32_t (&x)[16]) {
     const uint4 *r = reinterpret_cast<const uint4 *>(row);
     const uint4 a[4] = {r[2 * c], r[2 * c + 1], r[8 + 2 * c], r[8 + 2 * c + 1]};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = QFmt<F16>::lo(w[j]);
-            x[8 * i + 2 * j + 1] = QFmt<F16>::hi(w[j]);
-        }
+        x[4 * i] = a[i].x;
+        x[4 * i + 1] = a[i].y;
+        x[4 * i + 2] = a[i].z;
+        x[4 * i + 3] = a[i].w;
     }
 }
 
 // The row's codes (one nibble pair per byte: dimension 16c + j low, 64 + 16c + j high)
 // and its (scale, minimum) pair; the four threads of a token call it together.
+//
+// The quotient (x - min) / scale comes from the reciprocal and one correction, to half an fp32
+// step (2^-21 below 16).  Where x is 0 or at least kShort times the scale (and the minimum too),
+// 2 (x - min) - (2n + 1) scale is a multiple of 2^-20 of the scale, so a quotient is a half exactly
+// when its value is, and the rounding of the quotient is the exact one's; a row with a shorter x looks
+// whether any quotient lies near a half, and only then takes the exact comparison.
 template <bool F16>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[32], uint32_t (&packed)[4]) {
-    float lo = x[0], hi = x[0];
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[16], uint32_t (&packed)[4]) {
+    using Fmt = QFmt<F16>;
+    uint32_t mn2 = x[0], mx2 = x[0], ab2 = x[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 1; i < 32; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
+    for (int i = 1; i < 16; ++i) {
+        mn2 = Fmt::min2(mn2, x[i]);
+        mx2 = Fmt::max2(mx2, x[i]);
+        ab2 = Fmt::min2(ab2, x[i] & 0x7FFF7FFFu);
     }
+    float lo = min_nan(Fmt::lo(mn2), Fmt::hi(mn2)), hi = max_nan(Fmt::lo(mx2), Fmt::hi(mx2));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
         hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
     }
+    lo = __fadd_rn(lo, 0.0f);   // -0 is held as +0
     // upward at every step: the least 16-bit value >= the exact (max - min) / 15 (15 times a
     // 16-bit value is an fp32 value, so no rounding passes one)
     const float range = __fsub_ru(hi, lo);
@@ -98,35 +106,80 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[32], uint32_t (&pa
         packed[0] = packed[1] = packed[2] = packed[3] = 0u;
         return F16 ? 0x7E007E00u : 0x7FC07FC0u;
     }
-    const uint32_t sbits = QFmt<F16>::bits_up(__fdiv_ru(range, 15.0f));
-    const float scale = QFmt<F16>::lo(sbits);
-    // the approximate quotient is within 1e-5 of the exact one, so it decides the code
-    // unless it lies that near to a half; a subnormal scale has no finite reciprocal
-    const bool coarse = scale < 1e-30f;
-    const float inv = coarse ? 0.0f : __fdividef(1.0f, scale);
-    const float sure = coarse ? -1.0f : 0.4999f;
-    uint32_t codes[32];
+    const uint32_t sbits = Fmt::bits_up(__fdiv_ru(range, 15.0f));
+    const float scale = Fmt::lo(sbits);
+    bool exact = scale > 0.0f && scale < 1e-30f;   // no finite reciprocal, or a subnormal remainder
+    const float inv = scale < 1e-30f ? 0.0f : __frcp_rn(scale);
+    const float magic = 12582912.0f;               // 1.5 2^23: adding it rounds to an integer, half to even
+    auto quotient = [&](float v) {
+        const float d = v - lo, q0 = d * inv;
+        return fmaf(fmaf(-q0, scale, d), inv, q0);
+    };
+    const float least = scale * Fmt::kShort;
+    if (fminf(Fmt::lo(ab2), Fmt::hi(ab2)) < least || fabsf(lo) < least) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float q = (x[i] - lo) * inv;
-        const float t = rintf(q);
-        codes[i] = (uint32_t)(int)t;
-        if (fabsf(q - t) > sure) codes[i] = scale > 0.0f ? (uint32_t)exact_code(x[i], lo, scale) : 0u;
+        for (int i = 0; i < 16; ++i) {
+            const float q0 = quotient(Fmt::lo(x[i])), q1 = quotient(Fmt::hi(x[i]));
+            exact |= fabsf(q0 - ((q0 + magic) - magic)) > 0.498f || fabsf(q1 - ((q1 + magic) - magic)) > 0.498f;
+        }
+        exact = exact && scale > 0.0f;
     }
+    if (exact) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        packed[w] = 0u;
+        for (int w = 0; w < 4; ++w) {
+            packed[w] = 0u;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            packed[w] |= (codes[4 * w + j] | (codes[16 + 4 * w + j] << 4)) << (8 * j);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = x[2 * w + (j >> 1)], b = x[8 + 2 * w + (j >> 1)];
+                const int c0 = exact_code(j & 1 ? Fmt::hi(a) : Fmt::lo(a), lo, scale);
+                const int c1 = exact_code(j & 1 ? Fmt::hi(b) : Fmt::lo(b), lo, scale);
+                packed[w] |= (uint32_t)(c0 | (c1 << 4)) << (8 * j);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t byte[4];   // in the low bits of magic + low code + 16 x high code
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = x[2 * w + (j >> 1)], b = x[8 + 2 * w + (j >> 1)];
+                const float t0 = quotient(j & 1 ? Fmt::hi(a) : Fmt::lo(a)) + magic;
+                const float t1 = (quotient(j & 1 ? Fmt::hi(b) : Fmt::lo(b)) + magic) - magic;
+                byte[j] = __float_as_uint(fmaf(t1, 16.0f, t0));
+            }
+            packed[w] = __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
+        }
     }
-    return sbits | (QFmt<F16>::bits(lo) << 16);
+    return sbits | (Fmt::bits(lo) << 16);
+}
+
+// Words w[i] of four neighbouring lanes (q = lane & 3) as a 4 x 4 matrix, transposed: lane q gets word q of each.
+__device__ __forceinline__ void transpose_lanes(uint32_t (&w)[4], int q) {
+#pragma unroll
+    for (int step = 1; step < 4; step <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & step) continue;
+            const bool up = (q & step) != 0;
+            const uint32_t got = __shfl_xor_sync(kFull, up ? w[i] : w[i + step], step);
+            if (up) w[i] = got;
+            else w[i + step] = got;
+        }
+}
+// Bytes of four words as a 4 x 4 matrix, transposed.
+__device__ __forceinline__ void transpose_bytes(uint32_t (&w)[4]) {
+    const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+    const uint32_t c = __byte_perm(w[2], w[3], 0x5140), d = __byte_perm(w[2], w[3], 0x7362);
+    w[0] = __byte_perm(a, c, 0x5410);
+    w[1] = __byte_perm(a, c, 0x7632);
+    w[2] = __byte_perm(b, d, 0x5410);
+    w[3] = __byte_perm(b, d, 0x7632);
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kNT) append_kernel(const RowPtr k, const RowPtr v, int n, int first_host,
-                                                     const int32_t *first_dev, uint8_t *cache, int nb_cap,
-                                                     uint32_t *flags) {
+__global__ void __launch_bounds__(kNT, 3) append_kernel(const RowPtr k, const RowPtr v, int n, int first_host,
+                                                        const int32_t *first_dev, uint8_t *cache, int nb_cap,
+                                                        uint32_t *flags) {
     __shared__ __align__(16) uint8_t tile[kQBlockTok * kPitch];   // V codes, [token][dimension]
     const int tid = threadIdx.x, c = tid & 3, tok = tid >> 2;
     const int g = blockIdx.y;
@@ -137,64 +190,71 @@ __global__ void __launch_bounds__(kNT) append_kernel(const RowPtr k, const RowPt
     const long long b64 = (first >= 0 ? first / kQBlockTok : -((kQBlockTok - 1 - first) / kQBlockTok)) + blockIdx.x;
     if (b64 < 0 || b64 >= nb_cap) return;
     const int b = (int)b64;
-    const long long i = (long long)b * kQBlockTok + tok - first;   // the row this token takes
     if ((long long)b * kQBlockTok >= first + n) return;
+    const long long at = (long long)b * kQBlockTok - first;       // the row that the block's first token takes
+    const long long i = at + tok;
     const bool in = i >= 0 && i < n;
-    const bool whole = (long long)b * kQBlockTok >= first && (long long)(b + 1) * kQBlockTok <= first + n;
+    const bool whole = at >= 0 && at + kQBlockTok <= n;
     uint8_t *rec = cache + qrec_offset(g, nb_cap, b);
-    float x[32];
-    uint32_t packed[4];
-    // rows outside the range are read as zeros: the four threads of a token agree on it
+    uint32_t xk[16], xv[16], packed[4];
     if (in) {
-        load_row<F16>(k.p + i * k.token_bytes + g * k.head_bytes, c, x);
-    } else {
+        load_row(k.p + i * k.token_bytes + g * k.head_bytes, c, xk);
+        load_row(v.p + i * v.token_bytes + g * v.head_bytes, c, xv);
+    } else {   // a token outside the range: zeros, so that its four threads agree
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+        for (int j = 0; j < 16; ++j) xk[j] = xv[j] = 0u;
     }
-    const uint32_t kpair = quantise<F16>(x, packed);
+    const uint32_t kpair = quantise<F16>(xk, packed);
     if (in) {
         *reinterpret_cast<uint4 *>(rec + c * 1024 + tok * 16) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
         if (c == 0) *reinterpret_cast<uint32_t *>(rec + kQOffKPair + tok * 4) = kpair;
-        load_row<F16>(v.p + i * v.token_bytes + g * v.head_bytes, c, x);
     }
-    const uint32_t vpair = quantise<F16>(x, packed);
+    const uint32_t vpair = quantise<F16>(xv, packed);
     if (in && c == 0) *reinterpret_cast<uint32_t *>(rec + kQOffVPair + tok * 4) = vpair;
     // unpacked to bytes: the low nibbles are dimensions 16c .., the high ones 64 + 16c ..
-    uint4 *row = reinterpret_cast<uint4 *>(tile + tok * kPitch);
-    row[c] = make_uint4(packed[0] & 0x0F0F0F0Fu, packed[1] & 0x0F0F0F0Fu, packed[2] & 0x0F0F0F0Fu,
-                        packed[3] & 0x0F0F0F0Fu);
-    row[4 + c] = make_uint4((packed[0] >> 4) & 0x0F0F0F0Fu, (packed[1] >> 4) & 0x0F0F0F0Fu,
-                            (packed[2] >> 4) & 0x0F0F0F0Fu, (packed[3] >> 4) & 0x0F0F0F0Fu);
-    __syncthreads();
-    // V plane p, dimension d: byte j holds token 16p + j (low) and 32 + 16p + j (high)
-    const int p = tid >> 7, d = tid & 127;
-    uint4 *dst = reinterpret_cast<uint4 *>(rec + kQOffV + p * 2048 + d * 16);
-    uint32_t w[4], keep[4];
+    uint2 *row = reinterpret_cast<uint2 *>(tile + tok * kPitch);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        w[q] = keep[q] = 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int t0 = 16 * p + 4 * q + j;
-            w[q] |= (uint32_t)(tile[t0 * kPitch + d] | (tile[(t0 + 32) * kPitch + d] << 4)) << (8 * j);
-            const long long i0 = (long long)b * kQBlockTok + t0 - first;
-            if (i0 < 0 || i0 >= n) keep[q] |= 0x0Fu << (8 * j);
-            if (i0 + 32 < 0 || i0 + 32 >= n) keep[q] |= 0xF0u << (8 * j);
-        }
+    for (int j = 0; j < 2; ++j) {
+        row[2 * c + j] = make_uint2(packed[2 * j] & 0x0F0F0F0Fu, packed[2 * j + 1] & 0x0F0F0F0Fu);
+        row[8 + 2 * c + j] = make_uint2((packed[2 * j] >> 4) & 0x0F0F0F0Fu, (packed[2 * j + 1] >> 4) & 0x0F0F0F0Fu);
     }
-    if (!whole) {
+    __syncthreads();
+    // V plane p, dimensions 4 d4 .. 4 d4 + 3: this thread takes tokens 16p + 4q .. + 3 (low nibbles) and those 32
+    // further (high), then trades with its three neighbours for all 16 tokens of dimension 4 d4 + q
+    const int p = tid >> 7, d4 = (tid & 127) >> 2, q = tid & 3;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(tile + (16 * p + 4 * q + j) * kPitch) + d4;
+        w[j] = src[0] | (src[32 * kPitch / 4] << 4);
+    }
+    transpose_bytes(w);
+    transpose_lanes(w, q);
+    uint4 *dst = reinterpret_cast<uint4 *>(rec + kQOffV + p * 2048 + (4 * d4 + q) * 16);
+    if (!whole) {   // the other tokens' nibbles stay
         const uint4 old = *dst;
         const uint32_t o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = (w[q] & ~keep[q]) | (o[q] & keep[q]);
+        for (int x = 0; x < 4; ++x) {
+            uint32_t keep = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long i0 = at + 16 * p + 4 * x + j;
+                if (i0 < 0 || i0 >= n) keep |= 0x0Fu << (8 * j);
+                if (i0 + 32 < 0 || i0 + 32 >= n) keep |= 0xF0u << (8 * j);
+            }
+            w[x] = (w[x] & ~keep) | (o[x] & keep);
+        }
     }
     *dst = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 32 codes of a token (16 from dimension 16c, 16 from 64 + 16c) to 16-bit values: scale * code + min rounded once.
 template <bool F16>
 __device__ __forceinline__ void store_row(uint8_t *row, int c, const uint32_t (&lo)[4], const uint32_t (&hi)[4],
                                           uint32_t pair) {
-    const float scale = QFmt<F16>::lo(pair), mn = QFmt<F16>::hi(pair);
+    using Fmt = QFmt<F16>;
+    const uint32_t scale2 = __byte_perm(pair, 0u, 0x1010), min2 = __byte_perm(pair, 0u, 0x3232);
     uint4 *r = reinterpret_cast<uint4 *>(row);
 #pragma unroll
     for (int half = 0; half < 2; ++half)
@@ -202,10 +262,10 @@ __device__ __forceinline__ void store_row(uint8_t *row, int c, const uint32_t (&
         for (int i = 0; i < 2; ++i) {
             uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t w = (half ? hi : lo)[2 * i + (j >> 1)] >> (16 * (j & 1));
-                o[j] = QFmt<F16>::bits(fmaf(scale, (float)(w & 0xFFu), mn)) |
-                       (QFmt<F16>::bits(fmaf(scale, (float)((w >> 8) & 0xFFu), mn)) << 16);
+            for (int j = 0; j < 4; ++j) {   // a code's byte under the format's high byte is the base + code
+                const uint32_t w = (half ? hi : lo)[2 * i + (j >> 1)];
+                const uint32_t code2 = Fmt::fma2(__byte_perm(w, Fmt::kCodeHigh, j & 1 ? 0x4342 : 0x4140), Fmt::kOne2, Fmt::kMinusBase2);
+                o[j] = Fmt::fma2(scale2, code2, min2);
             }
             r[8 * half + 2 * c + i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -220,37 +280,47 @@ __global__ void __launch_bounds__(kNT) load_kernel(const uint8_t *cache, int nb_
     const uint8_t *rec = cache + qrec_offset(g, nb_cap, b);
     const long long i = (long long)b * kQBlockTok + tok - first;
     const bool in = i >= 0 && i < n;
-    uint32_t lo[4], hi[4];
-    auto unpack = [&](uint4 x) {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const int p = tid >> 7, d4 = (tid & 127) >> 2, q = tid & 3;
+    const uint4 x = *reinterpret_cast<const uint4 *>(rec + kQOffV + p * 2048 + (4 * d4 + q) * 16);
+    uint4 kx = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t kpair = 0u, vpair = 0u;
+    if (in) {
+        kx = *reinterpret_cast<const uint4 *>(rec + c * 1024 + tok * 16);
+        kpair = *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + tok * 4);
+        vpair = *reinterpret_cast<const uint32_t *>(rec + kQOffVPair + tok * 4);
+    }
+    {   // V codes to shared memory, token-major (the writer's steps backwards)
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        transpose_lanes(w, q);
+        transpose_bytes(w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t *dst = reinterpret_cast<uint32_t *>(tile + (16 * p + 4 * q + j) * kPitch) + d4;
+            dst[0] = w[j] & 0x0F0F0F0Fu;
+            dst[32 * kPitch / 4] = (w[j] >> 4) & 0x0F0F0F0Fu;
+        }
+    }
+    if (in) {
+        const uint32_t w[4] = {kx.x, kx.y, kx.z, kx.w};
+        uint32_t lo[4], hi[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             lo[j] = w[j] & 0x0F0F0F0Fu;
             hi[j] = (w[j] >> 4) & 0x0F0F0F0Fu;
         }
-    };
-    {   // V codes to shared memory, token-major
-        const int p = tid >> 7, d = tid & 127;
-        unpack(*reinterpret_cast<const uint4 *>(rec + kQOffV + p * 2048 + d * 16));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            tile[(16 * p + j) * kPitch + d] = (uint8_t)(lo[j >> 2] >> (8 * (j & 3)));
-            tile[(32 + 16 * p + j) * kPitch + d] = (uint8_t)(hi[j >> 2] >> (8 * (j & 3)));
-        }
-    }
-    if (in) {
-        unpack(*reinterpret_cast<const uint4 *>(rec + c * 1024 + tok * 16));
-        store_row<F16>(k.p + i * k.token_bytes + g * k.head_bytes, c, lo, hi,
-                       *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + tok * 4));
+        store_row<F16>(k.p + i * k.token_bytes + g * k.head_bytes, c, lo, hi, kpair);
     }
     __syncthreads();
     if (in) {
-        const uint4 a = reinterpret_cast<const uint4 *>(tile + tok * kPitch)[c];
-        const uint4 e = reinterpret_cast<const uint4 *>(tile + tok * kPitch)[4 + c];
-        lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w;
-        hi[0] = e.x, hi[1] = e.y, hi[2] = e.z, hi[3] = e.w;
-        store_row<F16>(v.p + i * v.token_bytes + g * v.head_bytes, c, lo, hi,
-                       *reinterpret_cast<const uint32_t *>(rec + kQOffVPair + tok * 4));
+        const uint2 *row = reinterpret_cast<const uint2 *>(tile + tok * kPitch);
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint2 a = row[2 * c + j], e = row[8 + 2 * c + j];
+            lo[2 * j] = a.x, lo[2 * j + 1] = a.y;
+            hi[2 * j] = e.x, hi[2 * j + 1] = e.y;
+        }
+        store_row<F16>(v.p + i * v.token_bytes + g * v.head_bytes, c, lo, hi, vpair);
     }
 }
 

@@ -42,6 +42,25 @@ struct QFmt<false> {
     static __device__ __forceinline__ uint32_t bits_up(float x) {
         return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(x));
     }
+    // of packed pairs; a NaN on either side wins
+    static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    // a code n in the low byte of kCodeHigh << 8 is the value kCodeBase + n; kMinusBase2 takes the base away
+    static constexpr uint32_t kCodeHigh = 0x43434343u, kOne2 = 0x3F803F80u, kMinusBase2 = 0xC300C300u;   // 128
+    static constexpr float kShort = 0x1p-12f;   // see quantise()
 };
 template <>
 struct QFmt<true> {
@@ -55,6 +74,23 @@ struct QFmt<true> {
     static __device__ __forceinline__ uint32_t bits_up(float x) {
         return (uint32_t)__half_as_ushort(__float2half_ru(x));
     }
+    static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+    static constexpr uint32_t kCodeHigh = 0x64646464u, kOne2 = 0x3C003C00u, kMinusBase2 = 0xE400E400u;   // 1024
+    static constexpr float kShort = 0x1p-9f;
 };
 
 }  // namespace qsa
