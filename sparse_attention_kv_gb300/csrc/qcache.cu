@@ -7,8 +7,9 @@
 // minimum is one of the row's values, so it is exact.
 //
 // One CTA (256 threads) per (KV head, block of 64 tokens), four threads per token: thread
-// c of a token holds dimensions 16c .. 16c + 15 and 64 + 16c .. 64 + 16c + 15, which is
-// one 16-byte row of K plane c, so K goes from registers to the cache.  V is stored
+// c of a token holds its 16-byte units c, c + 4, c + 8 and c + 12 (8 dimensions each), so the
+// four threads' accesses are neighbours, and units 8 apart are the low and the high nibbles
+// of the same 8 bytes of K, which go from registers to the cache.  V is stored
 // dimension-major: its codes pass through shared memory as bytes, are transposed four by four
 // with byte permutes and exchanged among four lanes, and leave as whole 16-byte rows.  A CTA
 // owns its whole block, so a partial block's other tokens (the other nibbles of shared bytes)
@@ -22,6 +23,7 @@ namespace qsa {
 namespace {
 
 constexpr int kNT = 256;
+constexpr float kNearHalf = 0.5f - 0x1p-18f;   // a quotient may be 2^-21 off
 constexpr int kPitch = 136;   // bytes per token of the staged V codes: rows four apart start 8 banks apart
 
 struct RowPtr {
@@ -47,7 +49,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // (x - lo) / scale rounded half to even, exactly: the difference as an unevaluated sum
 // a + e, a first quotient (at most one off), and the sign of the remainder against
 // half a step.  Each fp32 step before the last comparison is exact.
-__device__ __noinline__ int exact_code(float x, float lo, float scale) {
+__device__ __forceinline__ int exact_code(float x, float lo, float scale) {
     const float a = x - lo;
     const float bb = a - x;
     const float e = (x - (a - bb)) + (-lo - bb);
@@ -61,29 +63,45 @@ __device__ __noinline__ int exact_code(float x, float lo, float scale) {
     return min(max((int)c, 0), 15);
 }
 
-// One thread's 32 values of a row as 16 pairs (16 dimensions from 16c, 16 from 64 + 16c).
+// One thread's 32 values of a row as 16 pairs: its units c, c + 4, c + 8, c + 12.
 __device__ __forceinline__ void load_row(const uint8_t *row, int c, uint32_t (&x)[16]) {
     const uint4 *r = reinterpret_cast<const uint4 *>(row);
-    const uint4 a[4] = {r[2 * c], r[2 * c + 1], r[8 + 2 * c], r[8 + 2 * c + 1]};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[4 * i] = a[i].x;
-        x[4 * i + 1] = a[i].y;
-        x[4 * i + 2] = a[i].z;
-        x[4 * i + 3] = a[i].w;
+        const uint4 a = r[c + 4 * i];
+        x[4 * i] = a.x;
+        x[4 * i + 1] = a.y;
+        x[4 * i + 2] = a.z;
+        x[4 * i + 3] = a.w;
     }
 }
 
-// The row's codes (one nibble pair per byte: dimension 16c + j low, 64 + 16c + j high)
-// and its (scale, minimum) pair; the four threads of a token call it together.
+// Those units' codes by the exact comparison, from the row itself.  Rare, and out of line: it takes no registers
+// from the common path.
+template <bool F16>
+__device__ __noinline__ uint4 exact_row(const uint8_t *row, int c, float lo, float scale) {
+    uint32_t word[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(row) + 8 * (c + (w < 2 ? 0 : 4)) + 4 * (w & 1) + j;
+            const int c0 = exact_code(QFmt<F16>::lo(x[0]), lo, scale), c1 = exact_code(QFmt<F16>::lo(x[64]), lo, scale);
+            word[w] |= (uint32_t)(c0 | (c1 << 4)) << (8 * j);
+        }
+    return make_uint4(word[0], word[1], word[2], word[3]);
+}
+
+// The row's codes (a nibble pair per byte: words 0 and 1 units c low and c + 8 high, words 2 and 3 units
+// c + 4 and c + 12) and its (scale, minimum) pair; the four threads of a token call it together.
 //
 // The quotient (x - min) / scale comes from the reciprocal and one correction, to half an fp32
 // step (2^-21 below 16).  Where x is 0 or at least kShort times the scale (and the minimum too),
 // 2 (x - min) - (2n + 1) scale is a multiple of 2^-20 of the scale, so a quotient is a half exactly
 // when its value is, and the rounding of the quotient is the exact one's; a row with a shorter x looks
-// whether any quotient lies near a half, and only then takes the exact comparison.
+// whether such an x has its quotient near a half, and only then takes the exact comparison.
 template <bool F16>
-__device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[16], uint32_t (&packed)[4]) {
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[16], const uint8_t *row, int c, uint32_t (&packed)[4]) {
     using Fmt = QFmt<F16>;
     uint32_t mn2 = x[0], mx2 = x[0], ab2 = x[0] & 0x7FFF7FFFu;
 #pragma unroll
@@ -111,44 +129,45 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[16], uint32_t (
     bool exact = scale > 0.0f && scale < 1e-30f;   // no finite reciprocal, or a subnormal remainder
     const float inv = scale < 1e-30f ? 0.0f : __frcp_rn(scale);
     const float magic = 12582912.0f;               // 1.5 2^23: adding it rounds to an integer, half to even
-    auto quotient = [&](float v) {
-        const float d = v - lo, q0 = d * inv;
-        return fmaf(fmaf(-q0, scale, d), inv, q0);
+    const f32x2 nlo2 = pack2(-lo, -lo), inv2 = pack2(inv, inv), nscale2 = pack2(-scale, -scale);
+    const f32x2 magic2 = pack2(magic, magic), nmagic2 = pack2(-magic, -magic), sixteen2 = pack2(16.0f, 16.0f);
+    auto quotients = [&](uint32_t pair) {
+        const f32x2 d = add2(pack2(Fmt::lo(pair), Fmt::hi(pair)), nlo2), q0 = mul2(d, inv2);
+        return fma2(fma2(q0, nscale2, d), inv2, q0);
     };
     const float least = scale * Fmt::kShort;
-    if (fminf(Fmt::lo(ab2), Fmt::hi(ab2)) < least || fabsf(lo) < least) {
+    const bool lo_short = fabsf(lo) < least;
+    if (fminf(Fmt::lo(ab2), Fmt::hi(ab2)) < least || lo_short) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float q0 = quotient(Fmt::lo(x[i])), q1 = quotient(Fmt::hi(x[i]));
-            exact |= fabsf(q0 - ((q0 + magic) - magic)) > 0.498f || fabsf(q1 - ((q1 + magic) - magic)) > 0.498f;
+            const f32x2 q = quotients(x[i]);
+            float f0, f1;
+            unpack2(fma2(add2(add2(q, magic2), nmagic2), pack2(-1.0f, -1.0f), q), f0, f1);
+            exact |= fabsf(f0) > kNearHalf && (lo_short || fabsf(Fmt::lo(x[i])) < least);
+            exact |= fabsf(f1) > kNearHalf && (lo_short || fabsf(Fmt::hi(x[i])) < least);
         }
         exact = exact && scale > 0.0f;
     }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t byte[4];   // in the low bits of magic + low code + 16 x high code
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x2 t0 = add2(quotients(x[2 * w + j]), magic2);
+            const f32x2 t1 = add2(add2(quotients(x[8 + 2 * w + j]), magic2), nmagic2);
+            float b0, b1;
+            unpack2(fma2(t1, sixteen2, t0), b0, b1);
+            byte[2 * j] = __float_as_uint(b0);
+            byte[2 * j + 1] = __float_as_uint(b1);
+        }
+        packed[w] = __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
+    }
     if (exact) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            packed[w] = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = x[2 * w + (j >> 1)], b = x[8 + 2 * w + (j >> 1)];
-                const int c0 = exact_code(j & 1 ? Fmt::hi(a) : Fmt::lo(a), lo, scale);
-                const int c1 = exact_code(j & 1 ? Fmt::hi(b) : Fmt::lo(b), lo, scale);
-                packed[w] |= (uint32_t)(c0 | (c1 << 4)) << (8 * j);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t byte[4];   // in the low bits of magic + low code + 16 x high code
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a = x[2 * w + (j >> 1)], b = x[8 + 2 * w + (j >> 1)];
-                const float t0 = quotient(j & 1 ? Fmt::hi(a) : Fmt::lo(a)) + magic;
-                const float t1 = (quotient(j & 1 ? Fmt::hi(b) : Fmt::lo(b)) + magic) - magic;
-                byte[j] = __float_as_uint(fmaf(t1, 16.0f, t0));
-            }
-            packed[w] = __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
-        }
+        const uint4 all = exact_row<F16>(row, c, lo, scale);
+        packed[0] = all.x;
+        packed[1] = all.y;
+        packed[2] = all.z;
+        packed[3] = all.w;
     }
     return sbits | (Fmt::bits(lo) << 16);
 }
@@ -177,7 +196,7 @@ __device__ __forceinline__ void transpose_bytes(uint32_t (&w)[4]) {
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kNT, 3) append_kernel(const RowPtr k, const RowPtr v, int n, int first_host,
+__global__ void __launch_bounds__(kNT, 4) append_kernel(const RowPtr k, const RowPtr v, int n, int first_host,
                                                         const int32_t *first_dev, uint8_t *cache, int nb_cap,
                                                         uint32_t *flags) {
     __shared__ __align__(16) uint8_t tile[kQBlockTok * kPitch];   // V codes, [token][dimension]
@@ -197,26 +216,30 @@ __global__ void __launch_bounds__(kNT, 3) append_kernel(const RowPtr k, const Ro
     const bool whole = at >= 0 && at + kQBlockTok <= n;
     uint8_t *rec = cache + qrec_offset(g, nb_cap, b);
     uint32_t xk[16], xv[16], packed[4];
+    const uint8_t *krow = k.p + i * k.token_bytes + g * k.head_bytes;
+    const uint8_t *vrow = v.p + i * v.token_bytes + g * v.head_bytes;
     if (in) {
-        load_row(k.p + i * k.token_bytes + g * k.head_bytes, c, xk);
-        load_row(v.p + i * v.token_bytes + g * v.head_bytes, c, xv);
+        load_row(krow, c, xk);
+        load_row(vrow, c, xv);
     } else {   // a token outside the range: zeros, so that its four threads agree
 #pragma unroll
         for (int j = 0; j < 16; ++j) xk[j] = xv[j] = 0u;
     }
-    const uint32_t kpair = quantise<F16>(xk, packed);
+    const uint32_t kpair = quantise<F16>(xk, krow, c, packed);
     if (in) {
-        *reinterpret_cast<uint4 *>(rec + c * 1024 + tok * 16) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        uint2 *dst = reinterpret_cast<uint2 *>(rec + (c >> 1) * 1024 + tok * 16) + (c & 1);
+        dst[0] = make_uint2(packed[0], packed[1]);
+        dst[2 * 1024 / 8] = make_uint2(packed[2], packed[3]);
         if (c == 0) *reinterpret_cast<uint32_t *>(rec + kQOffKPair + tok * 4) = kpair;
     }
-    const uint32_t vpair = quantise<F16>(xv, packed);
+    const uint32_t vpair = quantise<F16>(xv, vrow, c, packed);
     if (in && c == 0) *reinterpret_cast<uint32_t *>(rec + kQOffVPair + tok * 4) = vpair;
-    // unpacked to bytes: the low nibbles are dimensions 16c .., the high ones 64 + 16c ..
+    // unpacked to bytes
     uint2 *row = reinterpret_cast<uint2 *>(tile + tok * kPitch);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        row[2 * c + j] = make_uint2(packed[2 * j] & 0x0F0F0F0Fu, packed[2 * j + 1] & 0x0F0F0F0Fu);
-        row[8 + 2 * c + j] = make_uint2((packed[2 * j] >> 4) & 0x0F0F0F0Fu, (packed[2 * j + 1] >> 4) & 0x0F0F0F0Fu);
+        row[c + 4 * j] = make_uint2(packed[2 * j] & 0x0F0F0F0Fu, packed[2 * j + 1] & 0x0F0F0F0Fu);
+        row[8 + c + 4 * j] = make_uint2((packed[2 * j] >> 4) & 0x0F0F0F0Fu, (packed[2 * j + 1] >> 4) & 0x0F0F0F0Fu);
     }
     __syncthreads();
     // V plane p, dimensions 4 d4 .. 4 d4 + 3: this thread takes tokens 16p + 4q .. + 3 (low nibbles) and those 32
@@ -249,7 +272,8 @@ __global__ void __launch_bounds__(kNT, 3) append_kernel(const RowPtr k, const Ro
     *dst = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 32 codes of a token (16 from dimension 16c, 16 from 64 + 16c) to 16-bit values: scale * code + min rounded once.
+// 32 codes of a token (units c and c + 4 in lo, c + 8 and c + 12 in hi) to 16-bit values: scale * code + min
+// rounded once.
 template <bool F16>
 __device__ __forceinline__ void store_row(uint8_t *row, int c, const uint32_t (&lo)[4], const uint32_t (&hi)[4],
                                           uint32_t pair) {
@@ -257,18 +281,16 @@ __device__ __forceinline__ void store_row(uint8_t *row, int c, const uint32_t (&
     const uint32_t scale2 = __byte_perm(pair, 0u, 0x1010), min2 = __byte_perm(pair, 0u, 0x3232);
     uint4 *r = reinterpret_cast<uint4 *>(row);
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {   // a code's byte under the format's high byte is the base + code
-                const uint32_t w = (half ? hi : lo)[2 * i + (j >> 1)];
-                const uint32_t code2 = Fmt::fma2(__byte_perm(w, Fmt::kCodeHigh, j & 1 ? 0x4342 : 0x4140), Fmt::kOne2, Fmt::kMinusBase2);
-                o[j] = Fmt::fma2(scale2, code2, min2);
-            }
-            r[8 * half + 2 * c + i] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; ++j) {   // a code's byte under the format's high byte is the base + code
+            const uint32_t w = (i < 2 ? lo : hi)[2 * (i & 1) + (j >> 1)];
+            const uint32_t code2 = Fmt::fma2(__byte_perm(w, Fmt::kCodeHigh, j & 1 ? 0x4342 : 0x4140), Fmt::kOne2, Fmt::kMinusBase2);
+            o[j] = Fmt::fma2(scale2, code2, min2);
         }
+        r[c + 4 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
 }
 
 template <bool F16>
@@ -282,10 +304,12 @@ __global__ void __launch_bounds__(kNT) load_kernel(const uint8_t *cache, int nb_
     const bool in = i >= 0 && i < n;
     const int p = tid >> 7, d4 = (tid & 127) >> 2, q = tid & 3;
     const uint4 x = *reinterpret_cast<const uint4 *>(rec + kQOffV + p * 2048 + (4 * d4 + q) * 16);
-    uint4 kx = make_uint4(0u, 0u, 0u, 0u);
+    uint2 kx[2] = {};
     uint32_t kpair = 0u, vpair = 0u;
     if (in) {
-        kx = *reinterpret_cast<const uint4 *>(rec + c * 1024 + tok * 16);
+        const uint2 *src = reinterpret_cast<const uint2 *>(rec + (c >> 1) * 1024 + tok * 16) + (c & 1);
+        kx[0] = src[0];
+        kx[1] = src[2 * 1024 / 8];
         kpair = *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + tok * 4);
         vpair = *reinterpret_cast<const uint32_t *>(rec + kQOffVPair + tok * 4);
     }
@@ -301,7 +325,7 @@ __global__ void __launch_bounds__(kNT) load_kernel(const uint8_t *cache, int nb_
         }
     }
     if (in) {
-        const uint32_t w[4] = {kx.x, kx.y, kx.z, kx.w};
+        const uint32_t w[4] = {kx[0].x, kx[0].y, kx[1].x, kx[1].y};
         uint32_t lo[4], hi[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -316,7 +340,7 @@ __global__ void __launch_bounds__(kNT) load_kernel(const uint8_t *cache, int nb_
         uint32_t lo[4], hi[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint2 a = row[2 * c + j], e = row[8 + 2 * c + j];
+            const uint2 a = row[c + 4 * j], e = row[8 + c + 4 * j];
             lo[2 * j] = a.x, lo[2 * j + 1] = a.y;
             hi[2 * j] = e.x, hi[2 * j + 1] = e.y;
         }
