@@ -1,15 +1,19 @@
 // evict.cu -- eviction of KV blocks by accumulated attention weight: the selected
 // blocks' weights added up per block, the blocks to keep, and the move of what is kept.
 //
-// 1. weights_add_kernel: acc[b] = decay * prev[b] + sum of the weights of the slots that
-//    selected b.  Each CTA owns a range of blocks, reads every id, and adds the weights of
-//    its own blocks in shared memory as 64-bit integers in units of 2^-36, so the result
-//    does not depend on the order in which threads arrive.
-// 2. evict_plan_kernel: one CTA per row finds the weight of the last block that stays by a
-//    radix select over order-preserving keys (8 bits a pass), then emits the kept ids in
-//    ascending order, ties to the lower id.
-// 3. gather_blocks_kernel: one warp per (array, row, kept block) copies a block.
+// 1. acc[b] = decay * prev[b] + sum of the weights of the slots that selected b, added in shared
+//    memory as 64-bit integers in units of 2^-36, so the result does not depend on the order in
+//    which threads arrive.  Few entries: every CTA owns a range of blocks, reads all ids and takes its
+//    own (weights_scan_kernel).  Many: the CTAs of one cluster share the blocks out, read an eighth
+//    of the entries each and add to the owner's memory (weights_cluster_kernel).
+// 2. evict_plan_kernel: one CTA per row holds the weights' order-preserving keys in registers, a
+//    run of neighbouring blocks per thread, and finds the last key that stays bit by bit (a count
+//    and a barrier each; two bits at a time took 13 us instead of 5 at 8,125 blocks); one scan
+//    then emits the kept ids in ascending order, ties to the lower id.  Rows past 16,384 blocks re-read their weights instead
+//    (evict_plan_long_kernel, a radix select of 8 bits a pass).
+// 3. gather_blocks_kernel: a warp copies 2 KB of a record, or as many small records as its lanes hold.
 #include <climits>
+#include <mutex>
 
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
@@ -22,10 +26,30 @@ constexpr float kMaxWeight = QSA_MAX_BLOCK_WEIGHT;
 constexpr int kAddThreads = 512;
 constexpr int kAddBlocks = 512;           // blocks owned by a CTA
 
-__global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const float *__restrict__ weights,
-                                                                  const int32_t *__restrict__ ids, int n_entries,
-                                                                  int n_kv, int k, float decay, const float *prev,
-                                                                  float *acc, int max_blocks, uint32_t *flags) {
+// The integer sum of an entry's weights over the KV heads.
+__device__ __forceinline__ unsigned long long entry_sum(const float *__restrict__ weights, int e, int n_kv, int k,
+                                                        uint32_t &bad) {
+    const int q = e / k, j = e - q * k;
+    const float *w = weights + (size_t)q * n_kv * k + j;
+    unsigned long long add = 0ull;
+#pragma unroll 4
+    for (int g = 0; g < n_kv; ++g) {
+        const float x = w[(size_t)g * k];
+        if (!(x >= 0.0f && x <= kMaxWeight)) bad |= QSA_FLAG_BAD_WEIGHT;
+        add += (unsigned long long)__float2ll_rn(fminf(fmaxf(x, 0.0f), kMaxWeight) * kUnit);   // NaN counts as 0
+    }
+    return add;
+}
+// One block's result: the sum in two halves, each exact in fp64 once scaled; fp32 once at the end.
+__device__ __forceinline__ float block_sum(unsigned long long sum, float decay, const float *prev, int b) {
+    const double s = (double)(uint32_t)(sum >> 32) * 0.0625 + (double)(uint32_t)sum * (1.0 / 68719476736.0);
+    return (float)((prev ? (double)decay * (double)prev[b] : 0.0) + s);
+}
+
+__global__ void __launch_bounds__(kAddThreads) weights_scan_kernel(const float *__restrict__ weights,
+                                                                   const int32_t *__restrict__ ids, int n_entries,
+                                                                   int n_kv, int k, float decay, const float *prev,
+                                                                   float *acc, int max_blocks, uint32_t *flags) {
     __shared__ unsigned long long sum[kAddBlocks];
     const int b0 = blockIdx.x * kAddBlocks;
     for (int i = threadIdx.x; i < kAddBlocks; i += kAddThreads) sum[i] = 0ull;
@@ -35,24 +59,44 @@ __global__ void __launch_bounds__(kAddThreads) weights_add_kernel(const float *_
         const int b = ids[e];
         if (blockIdx.x == 0 && b != -1 && (b < 0 || b >= max_blocks)) bad |= QSA_FLAG_BAD_ID;
         if (b < b0 || b >= b0 + kAddBlocks || b >= max_blocks) continue;
-        const int q = e / k, j = e - q * k;
-        const float *w = weights + (size_t)q * n_kv * k + j;
-        unsigned long long add = 0ull;
-        for (int g = 0; g < n_kv; ++g) {
-            const float x = w[(size_t)g * k];
-            if (!(x >= 0.0f && x <= kMaxWeight)) bad |= QSA_FLAG_BAD_WEIGHT;
-            add += (unsigned long long)__float2ll_rn(fminf(fmaxf(x, 0.0f), kMaxWeight) * kUnit);   // NaN counts as 0
-        }
-        atomicAdd(&sum[b - b0], add);
+        atomicAdd(&sum[b - b0], entry_sum(weights, e, n_kv, k, bad));
     }
     if (bad && flags) atomicOr(flags, bad);
     __syncthreads();
-    for (int i = threadIdx.x; i < kAddBlocks && b0 + i < max_blocks; i += kAddThreads) {
-        // the sum in two halves, each exact in fp64 once scaled; fp32 once at the end
-        const double s = (double)(sum[i] >> 32) * 0.0625 + (double)(uint32_t)sum[i] * (1.0 / 68719476736.0);
-        const double p = prev ? (double)decay * (double)prev[b0 + i] : 0.0;
-        acc[b0 + i] = (float)(p + s);
+    for (int i = threadIdx.x; i < kAddBlocks && b0 + i < max_blocks; i += kAddThreads)
+        acc[b0 + i] = block_sum(sum[i], decay, prev, b0 + i);
+}
+
+constexpr int kAddCluster = 8;
+constexpr int kAddClusterThreads = 1024;
+constexpr int kAddClusterBlocks = 28672;   // 8 bytes each in a CTA's shared memory
+
+__global__ void __cluster_dims__(kAddCluster, 1, 1) __launch_bounds__(kAddClusterThreads)
+    weights_cluster_kernel(const float *__restrict__ weights, const int32_t *__restrict__ ids, int n_entries, int n_kv,
+                           int k, float decay, const float *prev, float *acc, int max_blocks, int per_cta,
+                           uint32_t *flags) {
+    extern __shared__ unsigned long long sums[];   // this CTA's blocks: blockIdx.x * per_cta ..
+    for (int i = threadIdx.x; i < per_cta; i += kAddClusterThreads) sums[i] = 0ull;
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(sums));
+    uint32_t bad = 0u;
+    for (int e = blockIdx.x * kAddClusterThreads + threadIdx.x; e < n_entries; e += kAddCluster * kAddClusterThreads) {
+        const int b = ids[e];
+        if (b < 0 || b >= max_blocks) {
+            if (b != -1) bad |= QSA_FLAG_BAD_ID;
+            continue;
+        }
+        const unsigned long long add = entry_sum(weights, e, n_kv, k, bad);
+        const int owner = b / per_cta;
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + (uint32_t)(b - owner * per_cta) * 8u), "r"(owner));
+        asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(at), "l"(add) : "memory");
     }
+    if (bad && flags) atomicOr(flags, bad);
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const int b0 = blockIdx.x * per_cta;
+    for (int i = threadIdx.x; i < per_cta && b0 + i < max_blocks; i += kAddClusterThreads)
+        acc[b0 + i] = block_sum(sums[i], decay, prev, b0 + i);
 }
 
 constexpr int kPlanThreads = 1024;
@@ -63,25 +107,98 @@ __device__ __forceinline__ uint32_t plan_key(float w, int b, int nb, int n_first
     return w == w ? score_key(w) : 0u;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const float *__restrict__ weights, int64_t stride,
+// What every plan kernel starts with: the row's blocks; all of them kept: the answer at once.
+template <int NT>
+__device__ __forceinline__ int plan_blocks(const int32_t *__restrict__ n_tokens, int row, int max_blocks, int n_keep,
+                                           int32_t *out, int32_t *new_tokens, uint32_t *flags) {
+    int nt = n_tokens[row];
+    if (nt < 0 || (long long)nt > 64ll * max_blocks) {
+        if (threadIdx.x == 0 && flags) atomicOr(flags, QSA_FLAG_NBLOCKS_CLAMPED);
+        nt = nt < 0 ? 0 : 64 * max_blocks;
+    }
+    const int nb = (int)(((long long)nt + 63) / 64);
+    if (threadIdx.x == 0) new_tokens[row] = nt - 64 * max(nb - n_keep, 0);
+    if (nb <= n_keep)
+        for (int i = threadIdx.x; i < n_keep; i += NT) out[i] = i < nb ? i : -1;
+    return nb;
+}
+
+// E keys per thread, NT threads: rows of up to NT * E blocks.
+template <int NT, int E>
+__global__ void __launch_bounds__(NT) evict_plan_kernel(const float *__restrict__ weights, int64_t stride,
+                                                        const int32_t *__restrict__ n_tokens, int max_blocks,
+                                                        int n_keep, int n_first, int n_last, int32_t *keep,
+                                                        int32_t *new_tokens, uint32_t *flags) {
+    constexpr int NW = NT / 32;
+    __shared__ int part[2][32];
+    __shared__ BlockScratch sm;
+    allow_dependent_launch();   // the move that follows may line up
+    wait_prior_grid();
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float *w = weights + (size_t)row * stride;
+    int32_t *out = keep + (size_t)row * n_keep;
+    const int nb = plan_blocks<NT>(n_tokens, row, max_blocks, n_keep, out, new_tokens, flags);
+    if (nb <= n_keep) return;
+    uint32_t key[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int b = tid * E + e;
+        key[e] = b < nb ? plan_key(w[b], b, nb, n_first, n_last) : 0u;
+    }
+    // the largest T with at least n_keep keys >= T, bit by bit, until a count meets n_keep.  Keys past the row are
+    // 0: a T above 0 does not count them, and T stays 0 only when fewer than n_keep keys are above 0.
+    uint32_t T = 0u;
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t M = T | (1u << bit);
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) mine += key[e] >= M ? 1 : 0;
+        mine = __reduce_add_sync(kFull, mine);
+        int *p = part[bit & 1];
+        if (lane == 0) p[warp] = mine;
+        __syncthreads();
+        const int all = __reduce_add_sync(kFull, lane < NW ? p[lane] : 0);
+        if (all >= n_keep) T = M;
+        if (all == n_keep) {   // exactly these: the keys above M - 1
+            T = M - 1u;
+            break;
+        }
+    }
+    // ascending emit: keys above T, and the first of those equal to it
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const bool in = tid * E + e < nb;
+        above += in && key[e] > T ? 1 : 0;
+        equal += in && key[e] == T ? 1 : 0;
+    }
+    int total = 0;   // both counts in one scan: rows have at most 2^14 blocks
+    const uint32_t before = (uint32_t)block_excl_scan<NT>(above | (equal << 16), sm, total);
+    const int want = n_keep - (total & 0xFFFF);
+    int at = (int)(before & 0xFFFFu), eq = (int)(before >> 16);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int b = tid * E + e;
+        if (b >= nb) continue;
+        if (key[e] > T) out[min(eq, want) + at++] = b;
+        if (key[e] == T) {
+            if (eq < want) out[eq + at] = b;
+            ++eq;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) evict_plan_long_kernel(const float *__restrict__ weights, int64_t stride,
                                                                   const int32_t *__restrict__ n_tokens, int max_blocks,
                                                                   int n_keep, int n_first, int n_last, int32_t *keep,
                                                                   int32_t *new_tokens, uint32_t *flags) {
     __shared__ BlockScratch sm;
+    wait_prior_grid();
     const int row = blockIdx.x, tid = threadIdx.x;
     const float *w = weights + (size_t)row * stride;
     int32_t *out = keep + (size_t)row * n_keep;
-    int nt = n_tokens[row];
-    if (nt < 0 || (long long)nt > 64ll * max_blocks) {
-        if (tid == 0 && flags) atomicOr(flags, QSA_FLAG_NBLOCKS_CLAMPED);
-        nt = nt < 0 ? 0 : 64 * max_blocks;
-    }
-    const int nb = (int)(((long long)nt + 63) / 64);
-    if (tid == 0) new_tokens[row] = nt - 64 * max(nb - n_keep, 0);
-    if (nb <= n_keep) {
-        for (int i = tid; i < n_keep; i += kPlanThreads) out[i] = i < nb ? i : -1;
-        return;
-    }
+    const int nb = plan_blocks<kPlanThreads>(n_tokens, row, max_blocks, n_keep, out, new_tokens, flags);
+    if (nb <= n_keep) return;
     // the n_keep-th largest key, 8 bits a pass
     uint32_t prefix = 0u, mask = 0u;
     int want = n_keep;
@@ -123,8 +240,20 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const float *_
 }
 
 constexpr int kGatherThreads = 256;
+constexpr int kBatch = 4;   // 16-byte (or 4-byte) units per lane in flight
+// How an array's records are dealt to warps: `lanes` lanes per record (a power of two) and so 32 / lanes records
+// per warp, or, for records of more than 32 units, `pieces` warps per record.
+struct GatherArray {
+    const uint8_t *src;
+    uint8_t *dst;
+    uint32_t units;          // per record, of 16 bytes (wide) or 4
+    int wide;
+    int lanes, pieces;
+    uint32_t groups;         // per row: groups of 32 / lanes records
+    int src_blocks, dst_blocks;
+};
 struct GatherParams {
-    qsa_block_array a[QSA_GATHER_MAX_ARRAYS];
+    GatherArray a[QSA_GATHER_MAX_ARRAYS];
     long long first[QSA_GATHER_MAX_ARRAYS + 1];   // first warp of each array
     int n_arrays;
     int n_keep;
@@ -132,48 +261,109 @@ struct GatherParams {
     uint32_t *flags;
 };
 
+template <typename T>
+__device__ __forceinline__ void copy_units(const uint8_t *src, uint8_t *dst, uint32_t at, uint32_t end, uint32_t step) {
+    const T *s = reinterpret_cast<const T *>(src);
+    T *d = reinterpret_cast<T *>(dst);
+    T x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        if (at + i * step < end) x[i] = __ldcs(s + at + i * step);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+        if (at + i * step < end) __stcs(d + at + i * step, x[i]);
+}
+
 __global__ void __launch_bounds__(kGatherThreads) gather_blocks_kernel(const __grid_constant__ GatherParams p) {
     const int lane = threadIdx.x & 31;
-    const long long n_warps = (long long)gridDim.x * (kGatherThreads / 32);
-    for (long long w = (long long)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5); w < p.first[p.n_arrays];
-         w += n_warps) {
+    const long long n_warps = (long long)gridDim.x * (kGatherThreads / 32), all = p.first[p.n_arrays];
+    wait_prior_grid();
+    for (long long w = (long long)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5); w < all; w += n_warps) {
         int a = 0;
         while (w >= p.first[a + 1]) ++a;
-        const qsa_block_array &x = p.a[a];
-        const long long at = w - p.first[a];
-        const int row = (int)(at / p.n_keep), i = (int)(at % p.n_keep);
+        const GatherArray &x = p.a[a];
+        const uint64_t at = (uint64_t)(w - p.first[a]);
+        const uint32_t group = (uint32_t)(at / (uint32_t)x.pieces), piece = (uint32_t)(at - (uint64_t)group * x.pieces);
+        const uint32_t row = group / x.groups;
+        const uint32_t i = (group - row * x.groups) * (32u / x.lanes) + lane / x.lanes;
+        if (i >= (uint32_t)p.n_keep) continue;
         const int b = p.keep[i];
         if (b < 0 || b >= x.src_blocks) {
-            if (b != -1 && lane == 0 && p.flags) atomicOr(p.flags, QSA_FLAG_BAD_ID);
+            if (b != -1 && lane % x.lanes == 0 && p.flags) atomicOr(p.flags, QSA_FLAG_BAD_ID);
             continue;
         }
-        const uint8_t *src = static_cast<const uint8_t *>(x.src) + ((size_t)row * x.src_blocks + b) * x.block_bytes;
-        uint8_t *dst = static_cast<uint8_t *>(x.dst) + ((size_t)row * x.dst_blocks + i) * x.block_bytes;
-        if (((reinterpret_cast<uintptr_t>(x.src) | reinterpret_cast<uintptr_t>(x.dst) | (uintptr_t)x.block_bytes) & 15u) == 0u) {
-            const int n = (int)(x.block_bytes >> 4);
-#pragma unroll 4
-            for (int j = lane; j < n; j += 32) reinterpret_cast<uint4 *>(dst)[j] = reinterpret_cast<const uint4 *>(src)[j];
-        } else {
-            const int n = (int)(x.block_bytes >> 2);
-            for (int j = lane; j < n; j += 32)
-                reinterpret_cast<uint32_t *>(dst)[j] = reinterpret_cast<const uint32_t *>(src)[j];
-        }
+        const size_t bytes = (size_t)x.units * (x.wide ? 16 : 4);
+        const uint8_t *src = x.src + ((size_t)row * x.src_blocks + b) * bytes;
+        uint8_t *dst = x.dst + ((size_t)row * x.dst_blocks + i) * bytes;
+        const uint32_t from = piece * (32u * kBatch) + lane % x.lanes;
+        if (x.wide) copy_units<uint4>(src, dst, from, x.units, (uint32_t)x.lanes);
+        else copy_units<uint32_t>(src, dst, from, x.units, (uint32_t)x.lanes);
     }
 }
 
 }  // namespace
 
+// Launch as a programmatic dependent of the work before it on the stream: the kernel waits for it at entry.
+template <typename... Params, typename... Args>
+static qsa_status launch_dependent(const char *what, void (*kern)(Params...), int grid, int threads, size_t smem,
+                                   cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...), what);
+}
+
+// Above this many entries the cluster form is the faster one (see its comment).
+constexpr int kScanEntries = 2048;
+
 qsa_status launch_weights_add(const WeightsAddArgs &a, cudaStream_t s) {
+    const int entries = a.nq * a.k;
+    const int per_cta = (a.max_blocks + kAddCluster - 1) / kAddCluster;
+    if (entries > kScanEntries && per_cta <= kAddClusterBlocks) {
+        static std::mutex mu;
+        static bool opted_in[64] = {false};
+        int dev = 0;
+        qsa_status st = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
+        if (st != QSA_OK) return st;
+        if (dev < 0 || dev >= 64) return fail(QSA_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+        {
+            std::lock_guard<std::mutex> lock(mu);
+            if (!opted_in[dev]) {
+                st = check_cuda(cudaFuncSetAttribute(weights_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kAddClusterBlocks * 8),
+                                "cudaFuncSetAttribute(block weights)");
+                if (st != QSA_OK) return st;
+                opted_in[dev] = true;
+            }
+        }
+        weights_cluster_kernel<<<kAddCluster, kAddClusterThreads, (size_t)per_cta * 8, s>>>(
+            a.weights, a.ids, entries, a.n_kv_heads, a.k, a.decay, a.prev, a.acc, a.max_blocks, per_cta, a.flags);
+        return check_cuda(cudaGetLastError(), "weights_cluster_kernel launch");
+    }
     const int grid = (a.max_blocks + kAddBlocks - 1) / kAddBlocks;
-    weights_add_kernel<<<grid, kAddThreads, 0, s>>>(a.weights, a.ids, a.nq * a.k, a.n_kv_heads, a.k, a.decay, a.prev,
-                                                    a.acc, a.max_blocks, a.flags);
-    return check_cuda(cudaGetLastError(), "weights_add_kernel launch");
+    weights_scan_kernel<<<grid, kAddThreads, 0, s>>>(a.weights, a.ids, entries, a.n_kv_heads, a.k, a.decay, a.prev, a.acc,
+                                                     a.max_blocks, a.flags);
+    return check_cuda(cudaGetLastError(), "weights_scan_kernel launch");
 }
 
 qsa_status launch_evict_plan(const EvictPlanArgs &a, cudaStream_t s) {
-    evict_plan_kernel<<<a.n_rows, kPlanThreads, 0, s>>>(a.weights, a.stride, a.n_tokens, a.max_blocks, a.n_keep,
-                                                        a.n_first, a.n_last, a.keep, a.new_tokens, a.flags);
-    return check_cuda(cudaGetLastError(), "evict_plan_kernel launch");
+    auto run = [&](auto *kern, int threads) {
+        return launch_dependent("evict_plan_kernel launch", kern, a.n_rows, threads, 0, s, a.weights, a.stride, a.n_tokens,
+                                a.max_blocks, a.n_keep, a.n_first, a.n_last, a.keep, a.new_tokens, a.flags);
+    };
+    // the fewest threads that hold a row: a step's barrier is cheaper among fewer warps
+    if (a.max_blocks <= 1024) return run(evict_plan_kernel<256, 4>, 256);
+    if (a.max_blocks <= 4096) return run(evict_plan_kernel<512, 8>, 512);
+    if (a.max_blocks <= 8192) return run(evict_plan_kernel<1024, 8>, 1024);
+    if (a.max_blocks <= 16384) return run(evict_plan_kernel<1024, 16>, 1024);
+    return run(evict_plan_long_kernel, kPlanThreads);
 }
 
 qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, int n_keep,
@@ -184,14 +374,25 @@ qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, con
     p.keep = keep;
     p.flags = flags;
     for (int i = 0; i < n_arrays; ++i) {
-        p.a[i] = arrays[i];
-        p.first[i + 1] = p.first[i] + (long long)arrays[i].n_rows * n_keep;
+        const qsa_block_array &x = arrays[i];
+        GatherArray &y = p.a[i];
+        y.src = static_cast<const uint8_t *>(x.src);
+        y.dst = static_cast<uint8_t *>(x.dst);
+        y.wide = ((reinterpret_cast<uintptr_t>(x.src) | reinterpret_cast<uintptr_t>(x.dst) | (uintptr_t)x.block_bytes) & 15u) == 0u;
+        y.units = (uint32_t)(x.block_bytes >> (y.wide ? 4 : 2));
+        y.lanes = 1;
+        while (y.lanes < 32 && (uint32_t)y.lanes < y.units) y.lanes *= 2;
+        y.pieces = (int)((y.units + 32u * kBatch - 1) / (32u * kBatch));
+        y.groups = (uint32_t)((n_keep + 32 / y.lanes - 1) / (32 / y.lanes));
+        y.src_blocks = x.src_blocks;
+        y.dst_blocks = x.dst_blocks;
+        p.first[i + 1] = p.first[i] + (long long)x.n_rows * y.groups * y.pieces;
     }
     const long long warps = p.first[n_arrays];
     const long long ctas = (warps + kGatherThreads / 32 - 1) / (kGatherThreads / 32);
     const long long most = 8ll * num_sms();
-    gather_blocks_kernel<<<(unsigned)(ctas < most ? ctas : most), kGatherThreads, 0, s>>>(p);
-    return check_cuda(cudaGetLastError(), "gather_blocks_kernel launch");
+    return launch_dependent("gather_blocks_kernel launch", gather_blocks_kernel, (int)(ctas < most ? ctas : most),
+                            kGatherThreads, 0, s, p);
 }
 
 }  // namespace qsa
