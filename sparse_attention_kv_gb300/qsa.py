@@ -9,7 +9,9 @@ to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -55,6 +57,10 @@ class BlockArray(ctypes.Structure):
     """qsa_block_array: an array of one record per block, moved by qsa_gather_blocks."""
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("block_bytes", ctypes.c_int64),
                 ("n_rows", ctypes.c_int32), ("src_blocks", ctypes.c_int32), ("dst_blocks", ctypes.c_int32)]
+
+
+_PACK_BLOCK_ARRAY = struct.Struct("@PPqiii4x").pack   # a qsa_block_array as bytes
+assert struct.calcsize("@PPqiii4x") == ctypes.sizeof(BlockArray)
 
 
 _lib = None
@@ -106,7 +112,7 @@ def load() -> ctypes.CDLL:
     lib.qsa_block_weights_add.restype = i32
     lib.qsa_evict_plan.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     lib.qsa_evict_plan.restype = i32
-    lib.qsa_gather_blocks.argtypes = [ctypes.POINTER(BlockArray), i32, vp, i32, vp, sz, vp]
+    lib.qsa_gather_blocks.argtypes = [vp, i32, vp, i32, vp, sz, vp]
     lib.qsa_gather_blocks.restype = i32
     lib.qsa_read_flags.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), i32, vp]
     lib.qsa_read_flags.restype = i32
@@ -348,39 +354,50 @@ def vcache_transpose(v: torch.Tensor, vcache_t: torch.Tensor, first_block: int =
     return vcache_t
 
 
-def _on_current_device(tensors) -> int:
-    """The current stream, for tensors that all lie on the current CUDA device; raises otherwise."""
-    dev = torch.cuda.current_device()
-    for t, name in tensors:
+def _stream_of(stream, dev: int, **tensors) -> int:
+    """The stream's handle (the current one by default), once every tensor is found on the current device."""
+    for name, t in tensors.items():
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on the current device {dev} (it is on {t.device})")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+_QDTYPES = {torch.bfloat16: BF16, torch.float16: F16}
 
 
 def _qdtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float16:
-        return F16
-    raise ValueError(f"{name} must be bfloat16 or float16 (got {t.dtype})")
+    code = _QDTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16 (got {t.dtype})")
+    return code
 
 
 def _qcache_dims(cache: torch.Tensor) -> tuple[int, int]:
-    if cache.dtype != torch.uint8 or cache.dim() != 3 or cache.shape[2] != QCACHE_BLOCK_BYTES or \
-            not cache.is_contiguous():
+    shape = cache.shape
+    if cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != QCACHE_BLOCK_BYTES or not cache.is_contiguous():
         raise ValueError(f"cache must be a contiguous uint8 tensor [n_kv_heads, blocks, {QCACHE_BLOCK_BYTES}]")
-    return cache.shape[0], cache.shape[1] * 64
+    return shape[0], shape[1] * 64
 
 
-def _qrows(t: torch.Tensor, name: str, kv: int) -> tuple[int, int]:
-    """(token stride, head stride) of rows [n, n_kv_heads, 128]."""
-    if t.dim() != 3 or t.shape[1] != kv or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [n, {kv}, {HEAD_DIM}] with unit inner stride (got {tuple(t.shape)})")
-    return t.stride(0), t.stride(1)
+def _qrows(k: torch.Tensor, v: torch.Tensor, kv: int) -> tuple[int, int, int, int, int]:
+    """(n, token and head stride of k, of v) of rows [n, n_kv_heads, 128]."""
+    shape = tuple(k.shape)
+    if v.dtype != k.dtype or tuple(v.shape) != shape:
+        raise ValueError("v must match k's shape and dtype")
+    if len(shape) != 3 or shape[1] != kv or shape[2] != HEAD_DIM:
+        raise ValueError(f"k and v must be [n, {kv}, {HEAD_DIM}] (got {shape})")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("k and v must have unit inner stride")
+    return shape[0], ks[0], ks[1], vs[0], vs[1]
 
 
 def _ws_args(ws: torch.Tensor | None) -> tuple[int | None, int]:
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def qcache_bytes(n_kv_heads: int, capacity: int) -> int:
@@ -402,18 +419,16 @@ def qcache_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, first, 
     lib = load()
     kv, cap = _qcache_dims(cache)
     dt = _qdtype(k, "k")
-    if v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError("v must match k's shape and dtype")
-    ks, vs = _qrows(k, "k", kv), _qrows(v, "v", kv)
-    dev_first = first if isinstance(first, torch.Tensor) else None
-    if dev_first is not None and (dev_first.dtype != torch.int32 or dev_first.numel() != 1):
+    n, kt, kh, vt, vh = _qrows(k, v, kv)
+    on_device = isinstance(first, torch.Tensor)
+    if on_device and (first.dtype != torch.int32 or first.numel() != 1):
         raise ValueError("first must be an int or an int32 tensor of one element")
-    cur = _on_current_device(((k, "k"), (v, "v"), (cache, "cache"), (dev_first, "first"), (ws, "ws")))
-    st = lib.qsa_qcache_append(k.data_ptr(), *ks, v.data_ptr(), *vs, dt, k.shape[0], kv, HEAD_DIM,
-                               0 if dev_first is not None else int(first),
-                               None if dev_first is None else dev_first.data_ptr(), cache.data_ptr(), cap,
-                               *_ws_args(ws), cur if stream is None else _stream(stream)) if k.shape[0] else OK
-    _check("qsa_qcache_append", st)
+    on = _stream_of(stream, torch.cuda.current_device(), k=k, v=v, cache=cache, first=first if on_device else None, ws=ws)
+    if n:
+        wp, wn = _ws_args(ws)
+        _check("qsa_qcache_append", lib.qsa_qcache_append(
+            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, n, kv, HEAD_DIM, 0 if on_device else int(first),
+            first.data_ptr() if on_device else None, cache.data_ptr(), cap, wp, wn, on))
     return cache
 
 
@@ -422,13 +437,11 @@ def qcache_load(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, first: in
     lib = load()
     kv, cap = _qcache_dims(cache)
     dt = _qdtype(k, "k")
-    if v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError("v must match k's shape and dtype")
-    ks, vs = _qrows(k, "k", kv), _qrows(v, "v", kv)
-    cur = _on_current_device(((cache, "cache"), (k, "k"), (v, "v")))
-    st = lib.qsa_qcache_load(cache.data_ptr(), dt, kv, HEAD_DIM, cap, int(first), k.shape[0], k.data_ptr(), *ks,
-                             v.data_ptr(), *vs, cur if stream is None else _stream(stream)) if k.shape[0] else OK
-    _check("qsa_qcache_load", st)
+    n, kt, kh, vt, vh = _qrows(k, v, kv)
+    on = _stream_of(stream, torch.cuda.current_device(), cache=cache, k=k, v=v)
+    if n:
+        _check("qsa_qcache_load", lib.qsa_qcache_load(cache.data_ptr(), dt, kv, HEAD_DIM, cap, int(first), n, k.data_ptr(),
+                                                      kt, kh, v.data_ptr(), vt, vh, on))
 
 
 def select_attention_qcache(qa: torch.Tensor, cache: torch.Tensor, ids: torch.Tensor, n_tokens: torch.Tensor,
@@ -441,29 +454,29 @@ def select_attention_qcache(qa: torch.Tensor, cache: torch.Tensor, ids: torch.Te
     lib = load()
     kv, cap = _qcache_dims(cache)
     dt = _qdtype(qa, "qa")
-    if qa.dim() != 3 or qa.stride(2) != 1:
+    shape, strides, picks = tuple(qa.shape), qa.stride(), tuple(ids.shape)
+    if len(shape) != 3 or strides[2] != 1:
         raise ValueError("qa must be [nq, n_heads, 128] with unit inner stride")
-    nq, H, D = qa.shape
-    if ids.dtype != torch.int32 or ids.dim() != 2 or ids.shape[0] != nq or not ids.is_contiguous():
+    nq, H, D = shape
+    if ids.dtype != torch.int32 or len(picks) != 2 or picks[0] != nq or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 tensor [nq, k]")
     if n_tokens.dtype != torch.int32 or n_tokens.numel() != nq or not n_tokens.is_contiguous():
         raise ValueError("n_tokens must be a contiguous int32 tensor [nq]")
-    if out.shape != qa.shape or not out.is_contiguous() or (out.dtype != torch.float32 and out.dtype != qa.dtype):
+    out_dt = F32 if out.dtype == torch.float32 else dt
+    if tuple(out.shape) != shape or not out.is_contiguous() or (out_dt == dt and out.dtype != qa.dtype):
         raise ValueError("out must be a contiguous tensor [nq, n_heads, 128], fp32 or of qa's dtype")
-    k = ids.shape[1]
+    k = picks[1]
     if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (nq, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor [nq, n_heads]")
     if weights is not None and (weights.dtype != torch.float32 or tuple(weights.shape) != (nq, kv, k) or
                                 not weights.is_contiguous()):
         raise ValueError("weights must be a contiguous fp32 tensor [nq, n_kv_heads, k]")
-    cur = _on_current_device(((qa, "qa"), (cache, "cache"), (ids, "ids"), (n_tokens, "n_tokens"), (out, "out"),
-                              (lse, "lse"), (weights, "weights"), (ws, "ws")))
-    st = lib.qsa_select_attention_qcache(
-        qa.data_ptr(), qa.stride(0), qa.stride(1), dt, cache.data_ptr(), ids.data_ptr(), k, n_tokens.data_ptr(), nq, H,
-        kv, D, cap, D ** -0.5 if scale is None else float(scale), out.data_ptr(),
-        F32 if out.dtype == torch.float32 else dt, None if lse is None else lse.data_ptr(),
-        None if weights is None else weights.data_ptr(), *_ws_args(ws), cur if stream is None else _stream(stream))
-    _check("qsa_select_attention_qcache", st)
+    on = _stream_of(stream, torch.cuda.current_device(), qa=qa, cache=cache, ids=ids, n_tokens=n_tokens, out=out, lse=lse,
+                    weights=weights, ws=ws)
+    wp, wn = _ws_args(ws)
+    _check("qsa_select_attention_qcache", lib.qsa_select_attention_qcache(
+        qa.data_ptr(), strides[0], strides[1], dt, cache.data_ptr(), ids.data_ptr(), k, n_tokens.data_ptr(), nq, H, kv, D,
+        cap, D ** -0.5 if scale is None else float(scale), out.data_ptr(), out_dt, _ptr(lse), _ptr(weights), wp, wn, on))
     return out
 
 
@@ -477,18 +490,17 @@ def block_weights_add(weights: torch.Tensor, ids: torch.Tensor, acc: torch.Tenso
     nq, kv, k = weights.shape
     if ids.dtype != torch.int32 or tuple(ids.shape) != (nq, k) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 tensor [nq, k]")
+    n = acc.numel()
     for t, name in ((acc, "acc"), (prev, "prev")):
-        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous() or
-                              t.numel() != acc.numel()):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous() or t.numel() != n):
             raise ValueError(f"{name} must be a contiguous fp32 tensor [max_blocks]")
-    cur = _on_current_device(((weights, "weights"), (ids, "ids"), (acc, "acc"), (prev, "prev"), (ws, "ws")))
-    if prev is not None and prev.data_ptr() != acc.data_ptr() and \
-            abs(prev.data_ptr() - acc.data_ptr()) < 4 * acc.numel():
+    on = _stream_of(stream, torch.cuda.current_device(), weights=weights, ids=ids, acc=acc, prev=prev, ws=ws)
+    at, before = acc.data_ptr(), _ptr(prev)
+    if before is not None and before != at and abs(before - at) < 4 * n:
         raise ValueError("prev must be acc itself or not overlap it")
-    st = lib.qsa_block_weights_add(weights.data_ptr(), ids.data_ptr(), nq, kv, k, float(decay),
-                                   None if prev is None else prev.data_ptr(), acc.data_ptr(), acc.numel(),
-                                   *_ws_args(ws), cur if stream is None else _stream(stream))
-    _check("qsa_block_weights_add", st)
+    wp, wn = _ws_args(ws)
+    _check("qsa_block_weights_add", lib.qsa_block_weights_add(weights.data_ptr(), ids.data_ptr(), nq, kv, k, float(decay),
+                                                              before, at, n, wp, wn, on))
     return acc
 
 
@@ -506,29 +518,27 @@ def evict_plan(weights: torch.Tensor, n_tokens: torch.Tensor, keep: torch.Tensor
     for t, name in ((n_tokens, "n_tokens"), (new_tokens, "new_tokens")):
         if t.dtype != torch.int32 or t.numel() != n_rows or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor [n_rows]")
-    cur = _on_current_device(((weights, "weights"), (n_tokens, "n_tokens"), (keep, "keep"),
-                              (new_tokens, "new_tokens"), (ws, "ws")))
+    on = _stream_of(stream, torch.cuda.current_device(), weights=weights, n_tokens=n_tokens, keep=keep,
+                    new_tokens=new_tokens, ws=ws)
     # a single row's stride is never used and may be anything in torch
-    stride = max(weights.stride(0), max_blocks) if n_rows == 1 else weights.stride(0)
-    st = lib.qsa_evict_plan(weights.data_ptr(), stride, n_tokens.data_ptr(), n_rows, max_blocks,
-                            keep.shape[1], n_first, n_last, keep.data_ptr(), new_tokens.data_ptr(), *_ws_args(ws),
-                            cur if stream is None else _stream(stream))
-    _check("qsa_evict_plan", st)
+    stride = max_blocks if n_rows == 1 else weights.stride(0)
+    wp, wn = _ws_args(ws)
+    _check("qsa_evict_plan", lib.qsa_evict_plan(weights.data_ptr(), stride, n_tokens.data_ptr(), n_rows, max_blocks,
+                                                keep.shape[1], n_first, n_last, keep.data_ptr(), new_tokens.data_ptr(), wp,
+                                                wn, on))
     return keep
 
 
-def _block_array(src: torch.Tensor, dst: torch.Tensor) -> BlockArray:
-    """src, dst as [rows, blocks, ...], or [blocks, ...] for one row, with 1 or 2 dimensions."""
-    if src.dtype != dst.dtype or src.dim() != dst.dim() or not src.is_contiguous() or not dst.is_contiguous():
+def _block_array(src: torch.Tensor, dst: torch.Tensor) -> bytes:
+    """A qsa_block_array of src, dst: [rows, blocks, ...], or [blocks, ...] for one row, with 1 or 2 dimensions."""
+    a, b = tuple(src.shape), tuple(dst.shape)
+    if src.dtype != dst.dtype or len(a) != len(b) or not a or not src.is_contiguous() or not dst.is_contiguous():
         raise ValueError("src and dst must be contiguous tensors of one dtype and as many dimensions")
-    at = 1 if src.dim() >= 3 else 0
-    if src.shape[:at] != dst.shape[:at] or src.shape[at + 1:] != dst.shape[at + 1:]:
+    at = 1 if len(a) >= 3 else 0
+    if a[:at] != b[:at] or a[at + 1:] != b[at + 1:]:
         raise ValueError("src and dst may differ in their number of blocks only")
-    rows = src.shape[0] if at else 1
-    per = src.element_size()
-    for n in src.shape[at + 1:]:
-        per *= n
-    return BlockArray(src.data_ptr(), dst.data_ptr(), per, rows, src.shape[at], dst.shape[at])
+    return _PACK_BLOCK_ARRAY(src.data_ptr(), dst.data_ptr(), math.prod(a[at + 1:]) * src.element_size(), a[0] if at else 1,
+                             a[at], b[at])
 
 
 def gather_blocks(arrays, keep: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> None:
@@ -542,11 +552,15 @@ def gather_blocks(arrays, keep: torch.Tensor, ws: torch.Tensor | None = None, st
         raise ValueError("keep must be a contiguous int32 tensor [n_keep]")
     if not 1 <= len(arrays) <= GATHER_MAX_ARRAYS:
         raise ValueError(f"1 to {GATHER_MAX_ARRAYS} arrays (got {len(arrays)})")
-    cur = _on_current_device([(keep, "keep"), (ws, "ws")] + [(t, "arrays") for pair in arrays for t in pair])
-    packed = (BlockArray * len(arrays))(*(_block_array(src, dst) for src, dst in arrays))
-    st = lib.qsa_gather_blocks(packed, len(arrays), keep.data_ptr(), keep.numel(), *_ws_args(ws),
-                               cur if stream is None else _stream(stream))
-    _check("qsa_gather_blocks", st)
+    dev = torch.cuda.current_device()
+    on = _stream_of(stream, dev, keep=keep, ws=ws)
+    for pair in arrays:
+        for t in pair:
+            if t.get_device() != dev:
+                raise ValueError(f"arrays must lie on the current device {dev} (one is on {t.device})")
+    wp, wn = _ws_args(ws)
+    _check("qsa_gather_blocks", lib.qsa_gather_blocks(b"".join([_block_array(src, dst) for src, dst in arrays]),
+                                                      len(arrays), keep.data_ptr(), keep.numel(), wp, wn, on))
 
 
 def read_flags(ws: torch.Tensor, clear: bool = True, stream=None) -> int:
