@@ -169,6 +169,10 @@ qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int n
     if (max_blocks < 1 || max_blocks > QSA_MAX_BLOCKS)
         return fail(QSA_ERR_INVALID_ARG, "max_blocks must be in [1, %d] (got %d)", QSA_MAX_BLOCKS, max_blocks);
     if (!(decay >= 0.0f) || !(decay <= 3.4e38f)) return fail(QSA_ERR_INVALID_ARG, "decay must be finite and >= 0");
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(acc), p0 = reinterpret_cast<uintptr_t>(prev);
+    const size_t acc_bytes = (size_t)max_blocks * sizeof(float);
+    if (prev && prev != acc && a0 < p0 + acc_bytes && p0 < a0 + acc_bytes)
+        return fail(QSA_ERR_INVALID_ARG, "prev must be acc itself or not overlap it");
     qsa_status st = check_flags_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
     WeightsAddArgs a{};

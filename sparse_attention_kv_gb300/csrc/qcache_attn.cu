@@ -62,9 +62,9 @@ constexpr int kKBytes = kQOffV, kVBytes = kQRec - kQOffV;  // a record's halves:
 constexpr int kVStages = 2;
 constexpr int kMaxSplit = 8;
 constexpr float kTop = 4.0f;              // log2 of the largest weight when the references are set
-constexpr float kMostWeight = 256.0f;     // a weight above this moves them (e4m3 holds 448)
+// (a weight whose leading term is 256 or more moves them; e4m3 holds 448)
 constexpr float kMostY = 30.0f;           // and a y above this
-constexpr float kFaint = 0x1p-60f;        // V scales whose weights never reach kMostWeight before p overflows
+constexpr float kFaint = 0x1p-60f;        // V scales whose weights may stay small until p overflows
 
 // What the preparation warp leaves of a unit.
 struct QUnit {
@@ -83,6 +83,9 @@ struct QCtrl {
     uint32_t tmem_base;
     int abort;
     QUnit unit[2];
+    // a step's pairs (K, V) by tile and row; a V scale of -1: not seen.  Three steps: those of t + 1 are written while
+    // a slow warp may still read those of t - 1
+    alignas(16) uint2 token[3][kStep * kQBlockTok];
     alignas(16) float zero[kG];
     alignas(16) float nm[kG];             // minus the reference of the exponents (log2 units)
     alignas(16) float g[kG];              // power of two of the weights
@@ -90,8 +93,9 @@ struct QCtrl {
     alignas(16) float fo[kG];
     alignas(16) float inv[kG];
     float top[kG], eg[kG];                // largest log2(p vs) + m seen, log2(g)
+    float ig[kG];                         // 1 / g
     float least_g;
-    uint32_t red[3][4][kG];
+    float red[3][4][kG];
     float sum[3][kG];                     // l, sum of p vm, 16 x what the weights' rounding took away
     float2 ml[kMaxSplit][kG];             // (m, l) of every CTA of a cluster
     alignas(16) float w[kSel][kG];        // sums of p over a slot's tokens
@@ -177,9 +181,10 @@ __device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t h2_max(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+// The warp's largest value (a NaN counts as none).
+__device__ __forceinline__ float warp_fmax(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ float h2_lo(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu))); }
@@ -268,9 +273,11 @@ __device__ __forceinline__ float warp_sum8(const float (&x)[kH], int lane) {
 
 
 // Every thread of the warp waits, a bounded number of tries (each suspends the thread for some
-// hundred cycles; the bound comes to seconds); after one has given up, waits return at once.  A
-// poll is four instructions: waiting warps share the issue slots with working ones.
-template <int SLEEP = 0>
+// hundred cycles; the bound comes to seconds).  After one has given up, waits for copies and
+// products return at once, and the CTA runs through its remaining steps without their results.
+// Waits for what another warp does (HANDSHAKE) keep their patience: every warp still makes its steps, and
+// all of them read the same number of steps, so that the barriers meet.
+template <int SLEEP = 0, bool HANDSHAKE = false>
 __device__ __forceinline__ void wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     uint32_t ok;
     asm volatile(
@@ -279,7 +286,7 @@ __device__ __forceinline__ void wait_all(uint64_t *bar, uint32_t parity, volatil
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     if (__all_sync(kFull, ok != 0)) return;   // the warp stays converged
-    const uint32_t most = *abort_flag ? 1u : 1u << 23;
+    const uint32_t most = !HANDSHAKE && *abort_flag ? 1u : 1u << 23;
     if constexpr (SLEEP == 0)
         asm volatile(
             "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
@@ -436,8 +443,10 @@ __device__ __forceinline__ void prepare_queries(const QParams &p, int qi, int g,
     }
 }
 
-// F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted.
-template <bool F16, bool W>
+// F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted; HALF: groups
+// of at most eight heads, whose second half is not computed (61 queries x 8 KV heads x 8: 30.8 -> 24.7 us; as a
+// branch of the one kernel it cost groups of 16 1.5 us of 67).
+template <bool F16, bool W, bool HALF>
 __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constant__ QParams p) {
     constexpr int TERMS = F16 ? 3 : 2;
     using L = QLayout<TERMS>;
@@ -457,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.k_full[i], 1);
-            mbar_init(&ct.k_free[i], 8);  // the softmax warps: they read the pairs behind S, and so behind K's unpacking
+            mbar_init(&ct.k_free[i], 4);  // the unpacking warps
         }
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&ct.v_full[i], 1);
             mbar_init(&ct.v_free[i], 4);  // the unpacking warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ct.sbar[i], 1);
+            mbar_init(&ct.sbar[i], 5);    // S is complete, and the unpacking warps' pairs stand
             mbar_init(&ct.ids_ready[i], 1);
             mbar_init(&ct.ready[i], 1);
             mbar_init(&ct.done[i], 15);   // all warps but the preparing one
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     if (warp >= kControl) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kPrepare) {
         for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
-            if (n >= 2) wait_all<256>(&ct.done[n & 1], ((uint32_t)(n >> 1) - 1u) & 1u, abort_flag);
+            if (n >= 2) wait_all<256, true>(&ct.done[n & 1], ((uint32_t)(n >> 1) - 1u) & 1u, abort_flag);
             const int qi = u / a.n_kv_heads, g = u - qi * a.n_kv_heads;
             prepare_ids<W>(p, qi, g, rank, ct.unit[n & 1]);
             __syncwarp();
@@ -501,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
         int s = 0;
         uint32_t lap = 0;
         for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
-            wait_all<64>(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            wait_all<64, true>(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             const QUnit &un = ct.unit[n & 1];
             const int steps = un.steps, nloc = un.nloc;
             const uint8_t *head = static_cast<const uint8_t *>(a.cache) + qrec_offset(u % a.n_kv_heads, nb_cap, 0) + (is_k ? 0 : kQOffV);
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
         const uint64_t dq = sdesc(smem_u32(sQ)), dp = sdesc_mn(smem_u32(sP), 8 * kG, L::kTermP);
         int scored = 0, summed = 0;
         auto scores = [&](int n, int t) {   // step t, of unit n
-            wait_all(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             k_ready_wait();
             tc_fence_after();
             if (elect_one()) {
@@ -559,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
         };
         bool primed = false;
         for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
-            wait_all(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            wait_all<0, true>(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             const int steps = ct.unit[n & 1].steps;
             if (steps == 0) primed = false;
             // i = -1: the first step's S, unless it was issued behind the last unit's last step
@@ -568,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 bool next = i < 0 ? steps > 0 && !primed : i + 1 < steps;
                 if (i + 1 == steps && steps > 0 && u + ustep < p.units) {
                     of = n + 1;
-                    wait_all(&ct.ready[of & 1], (uint32_t)(of >> 1) & 1u, abort_flag);
+                    wait_all<0, true>(&ct.ready[of & 1], (uint32_t)(of >> 1) & 1u, abort_flag);
                     next = ct.unit[of & 1].steps > 0;
                 }
                 if (i + 1 == steps) primed = next && of != n;
@@ -623,24 +632,39 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             tmem_st8(tmem + lanes + lo_col, lo);
             tmem_st8(tmem + lanes + hi_col, hi);
         };
-        // K of a step: block q's tokens `lane` (tile 0) and 32 + `lane` (tile 1), their 128 dimensions
-        auto unpack_k = [&](int t) {
+        // K of step t, step i of unit un: block q's tokens `lane` (tile 0) and 32 + `lane` (tile 1), their 128
+        // dimensions and their pairs
+        auto unpack_k = [&](int t, const QUnit &un, int i) {
             const int s = t % L::kKStages;
             wait_all<32>(&ct.k_full[s], (uint32_t)(t / L::kKStages) & 1u, abort_flag);
             tc_fence_after();
-            const uint8_t *src = sK + (s * kStep + q) * kKBytes + lane * 16;
+            const uint8_t *rec = sK + (s * kStep + q) * kKBytes;
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                unpack(src + sub * 512, src + sub * 512 + 1024, kColK + sub * 32, kColK + sub * 32 + 16);
-                unpack(src + sub * 512 + 2048, src + sub * 512 + 3072, kColK + sub * 32 + 8, kColK + sub * 32 + 24);
+                const uint8_t *src = rec + (32 * sub + lane) * 16;
+                unpack(src, src + 1024, kColK + sub * 32, kColK + sub * 32 + 16);
+                unpack(src + 2048, src + 3072, kColK + sub * 32 + 8, kColK + sub * 32 + 24);
             }
+            const int left = un.ntok - un.sel[un.b0 + kStep * i + q] * kQBlockTok;   // tokens of this block below the context's end
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const uint32_t kp = *reinterpret_cast<const uint32_t *>(rec + kQOffKPair + (32 * sub + lane) * 4);
+                const uint32_t vp = *reinterpret_cast<const uint32_t *>(rec + kQOffVPair + (32 * sub + lane) * 4);
+                ct.token[t % 3][sub * 128 + row] = 32 * sub + lane < left ? make_uint2(kp, vp) : make_uint2(0u, F16 ? 0xBC00u : 0xBF80u);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ct.k_free[s]);   // the stores to tensor memory are fed from registers
+                mbar_arrive(&ct.sbar[t & 1]);
+            }
+            __syncwarp();
             tmem_wait_st();
             tc_fence_before();
             k_ready_arrive();
         };
         bool primed = false;
         for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
-            wait_all(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             const int steps = ct.unit[n & 1].steps;
             if (steps == 0) primed = false;
             for (int i = -1; i < steps; ++i) {             // as the control warp walks
@@ -648,12 +672,12 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 bool next = i < 0 ? steps > 0 && !primed : i + 1 < steps;
                 if (i + 1 == steps && steps > 0 && u + ustep < p.units) {
                     of = n + 1;
-                    wait_all(&ct.ready[of & 1], (uint32_t)(of >> 1) & 1u, abort_flag);
+                    wait_all<0, true>(&ct.ready[of & 1], (uint32_t)(of >> 1) & 1u, abort_flag);
                     next = ct.unit[of & 1].steps > 0;
                 }
                 if (i + 1 == steps) primed = next && of != n;
                 if (i >= 0) wait_all<32>(&ct.sbar[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);   // K(t) is read
-                if (next) unpack_k(t + (i >= 0 ? 1 : 0));
+                if (next) unpack_k(t + (i >= 0 ? 1 : 0), ct.unit[of & 1], of == n ? i + 1 : 0);
                 if (i < 0) continue;
                 const int s = t % kVStages;
                 wait_all(&ct.v_full[s], (uint32_t)(t / kVStages) & 1u, abort_flag);
@@ -681,11 +705,35 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int wg = warp >> 2, q = warp & 3, row = tid & 127;
     const int h0 = wg * kH;
+    if (HALF && wg == 1) {   // no heads in this half: its weights stay 0, and its warps only keep step
+        for (int i = 0; i < L::kPBufs * 2 * TERMS; ++i)
+            *reinterpret_cast<uint2 *>(sP + i * L::kTermP + row * kG + h0) = make_uint2(0u, 0u);
+        fence_proxy_async();
+        for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
+            wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+            const int steps = ct.unit[n & 1].steps;
+            for (int i = 0; i < steps; ++i) {
+                bool renew = i == 0;
+                do {
+                    if (renew) {
+                        work_barrier();
+                        work_barrier();
+                    }
+                    renew = vote_barrier(false);
+                } while (renew);
+            }
+            if (steps > 0) {   // the unit's end
+                work_barrier();
+                work_barrier();
+            }
+            if (lane == 0) mbar_arrive(&ct.done[n & 1]);
+            __syncwarp();
+        }
+    } else
     for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
         const QUnit &un = ct.unit[n & 1];
-        wait_all(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
-        const int steps = un.steps, nloc = un.nloc, ntok = un.ntok;
-        const int32_t *sel = un.sel + un.b0 + q;
+        wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
+        const int steps = un.steps, nloc = un.nloc;
         f32x2 l[kH / 2], mv[kH / 2];
         uint32_t left[kH / 2];            // fp16 pairs: 16 x what the rounding of this thread's weights left
 #pragma unroll
@@ -694,26 +742,18 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             left[h] = 0u;
         }
         for (int i = 0; i < steps; ++i, ++t) {
-            const int ks_at = t % L::kKStages;
-            // S(t) is complete; so is, two steps back, O += P(t - 2) V(t - 2), which the control warp issued before
-            // it, and K(t) with its pairs has landed (the unpacking warps waited for it)
+            // S(t) is complete; so is, two steps back, O += P(t - 2) V(t - 2), which the control warp issued before it
             wait_all(&ct.sbar[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);
             if (L::kPBufs == 1 && t > 0) wait_all(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);   // P(t - 1) is read
             tc_fence_after();
-            bool vis[2];
             float ks[2], km[2], vs[2], vm[2];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                const uint8_t *rec = sK + (ks_at * kStep + q) * kKBytes + (32 * sub + lane) * 4;
-                vis[sub] = sel[kStep * i] * kQBlockTok + 32 * sub + lane < ntok;
-                const uint32_t kp = vis[sub] ? *reinterpret_cast<const uint32_t *>(rec + kQOffKPair) : 0u;
-                const uint32_t vp = vis[sub] ? *reinterpret_cast<const uint32_t *>(rec + kQOffVPair) : 0u;
-                ks[sub] = QFmt<F16>::lo(kp), km[sub] = QFmt<F16>::hi(kp);
-                vs[sub] = QFmt<F16>::lo(vp), vm[sub] = QFmt<F16>::hi(vp);
+                const uint2 x = ct.token[t % 3][sub * 128 + row];
+                ks[sub] = QFmt<F16>::lo(x.x), km[sub] = QFmt<F16>::hi(x.x);
+                vs[sub] = QFmt<F16>::lo(x.y), vm[sub] = QFmt<F16>::hi(x.y);
             }
-            const bool all_vis = __all_sync(kFull, vis[1]);   // and so vis[0]
-            if (lane == 0) mbar_arrive(&ct.k_free[ks_at]);
-            __syncwarp();
+            const bool all_vis = __all_sync(kFull, !(vs[1] < 0.0f));   // and so the first tile's
             // y = log2(e) s - m of this thread's tokens, into e
             float e[2][kH];
             auto logits = [&](const float *nmp) {
@@ -744,22 +784,19 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
 #pragma unroll
                     for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                        for (int h = 0; h < kH; ++h) e[sub][h] = vis[sub] ? e[sub][h] : -INFINITY;
+                        for (int h = 0; h < kH; ++h) e[sub][h] = vs[sub] < 0.0f ? -INFINITY : e[sub][h];
             };
             int renew = i == 0 ? 1 : 0;       // 1: the references move before the weights are made; 2: they have
             while (true) {
                 logits(i == 0 && renew == 1 ? ct.zero : ct.nm);
                 if (renew == 1) {
                     // new references: the largest exponent and the largest weight so far, per head
-                    const float lv0 = vs[0] == 0.0f ? -INFINITY : lg2(vs[0]), lv1 = vs[1] == 0.0f ? -INFINITY : lg2(vs[1]);
-                    uint32_t mine[2] = {0u, 0u};
+                    const float lv0 = vs[0] > 0.0f ? lg2(vs[0]) : -INFINITY, lv1 = vs[1] > 0.0f ? lg2(vs[1]) : -INFINITY;
+                    float mine[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int h = 0; h < kH; ++h) {
-                        uint32_t y = score_key(e[0][h]), r = score_key(e[0][h] + lv0);
-                        y = max(y, score_key(e[1][h]));
-                        r = max(r, score_key(e[1][h] + lv1));
-                        y = __reduce_max_sync(kFull, y);
-                        r = __reduce_max_sync(kFull, r);
+                        const float y = warp_fmax(fmaxf(e[0][h], e[1][h]));
+                        const float r = warp_fmax(fmaxf(e[0][h] + lv0, e[1][h] + lv1));
                         if (lane == h) {
                             mine[0] = y;
                             mine[1] = r;
@@ -772,14 +809,14 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     work_barrier();
                     if (warp == 0) {
                         const int h = lane & 15;
-                        uint32_t y = 0u, r = 0u;
+                        float y = -INFINITY, r = -INFINITY;
                         for (int w = 0; w < 4; ++w) {
-                            y = max(y, ct.red[0][w][h]);
-                            r = max(r, ct.red[1][w][h]);
+                            y = fmaxf(y, ct.red[0][w][h]);
+                            r = fmaxf(r, ct.red[1][w][h]);
                         }
-                        const float m0 = i == 0 ? 0.0f : -ct.nm[h], rise = key_float(y);
+                        const float m0 = i == 0 ? 0.0f : -ct.nm[h], rise = y;
                         const float m1 = i == 0 ? rise : m0 + fmaxf(rise, 0.0f);
-                        const float top = fmaxf(i == 0 ? -INFINITY : ct.top[h], m0 + key_float(r));
+                        const float top = fmaxf(i == 0 ? -INFINITY : ct.top[h], m0 + r);
                         // nothing but zero scales so far: any other one will pass the limit
                         const float eg = top == -INFINITY ? 60.0f : fminf(fmaxf(kTop - ceilf(top - m1), -126.0f), 126.0f);
                         const float fl = i == 0 ? 1.0f : exp2f(m0 - m1);
@@ -795,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                             ct.top[h] = top;
                             ct.eg[h] = eg;
                             ct.g[h] = exp2f(eg);
+                            ct.ig[h] = exp2f(-eg);
                             if (lane == 0) ct.least_g = exp2f(least);
                         }
                     }
@@ -829,17 +867,18 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 }
                 // p = 2^y, and the weights p vs g in terms to shared memory: [tile][term][token][head]
                 bool over = false;
-                const float faint = fminf(vis[0] ? vs[0] : 1.0f, vis[1] ? vs[1] : 1.0f) * ct.least_g;
+                const float faint = fminf(vs[0] < 0.0f ? 1.0f : vs[0], vs[1] < 0.0f ? 1.0f : vs[1]) * ct.least_g;
                 if (__any_sync(kFull, faint < kFaint)) {   // p may grow where the weights do not
 #pragma unroll
                     for (int h = 0; h < kH; ++h) over |= fmaxf(e[0][h], e[1][h]) > kMostY;
                 }
-                uint32_t hmax = 0u, rest[kH / 2];
+                uint32_t high = 0u, rest[kH / 2];
 #pragma unroll
                 for (int h = 0; h < kH / 2; ++h) rest[h] = 0u;
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub) {
-                    const f32x2 vs2 = pack2(vs[sub], vs[sub]);
+                    const float seen = vs[sub] < 0.0f ? 0.0f : vs[sub];   // no weight of -0: its sign would count as a high one
+                    const f32x2 vs2 = pack2(seen, seen);
                     uint32_t word[2][TERMS];
 #pragma unroll
                     for (int h = 0; h < kH; h += 4) {
@@ -853,19 +892,19 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                             const f32x2 w2 = mul2(mul2(pack2(e0, e1), vs2), reinterpret_cast<const f32x2 *>(ct.g + h0 + h)[j]);
                             unpack2(w2, w[2 * j], w[2 * j + 1]);
                             h2[j] = to_h2(w[2 * j], w[2 * j + 1]);
-                            hmax = h2_max(hmax, h2[j]);
                         }
                         uint32_t r[2] = {rest[h / 2], rest[h / 2 + 1]};
                         split_weights<TERMS>(w, h2, word[h / 4], r);
                         rest[h / 2] = r[0];
                         rest[h / 2 + 1] = r[1];
+                        high |= word[h / 4][0] + 0x08080808u;   // a leading term of 256 or more reaches bit 7
                     }
 #pragma unroll
                     for (int y = 0; y < TERMS; ++y)
                         *reinterpret_cast<uint2 *>(sP + (t % L::kPBufs) * L::kStepP + sub * L::kTileP + y * L::kTermP + row * kG + h0) =
                             make_uint2(word[0][y], word[1][y]);
                 }
-                over = renew == 0 && (over || h2_lo(hmax) > kMostWeight || h2_hi(hmax) > kMostWeight);
+                over = renew == 0 && (over || (high & 0x80808080u) != 0u);
                 fence_proxy_async();   // the weights are read by the tensor core
                 tc_fence_before();
                 if (!vote_barrier(over)) {
@@ -918,14 +957,14 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     }
                 }
                 const float sum = warp_sum8(x, lane);
-                if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = __float_as_uint(sum);
+                if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = sum;
             }
             work_barrier();
             if (tid < 3 * kG) {
                 const int j = tid / kG, h = tid % kG;
                 float sum = 0.0f;
                 if (j < 2 || TERMS == 2)
-                    for (int w = 0; w < 4; ++w) sum += __uint_as_float(ct.red[j][w][h]);
+                    for (int w = 0; w < 4; ++w) sum += ct.red[j][w][h];
                 ct.sum[j][h] = sum;
                 if (j == 0) ct.inv[h] = 1.0f / sum;
             }
@@ -945,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             for (int j = 0; j < kH; ++j) {
                 const int h = h0 + j;
                 float y = fmaf(__uint_as_float(o[1][j]), 0.0625f, __uint_as_float(o[0][j]));
-                y = fmaf(fmaf(y, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), exp2f(-ct.eg[h]), ct.sum[1][h]);
+                y = fmaf(fmaf(y, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), ct.ig[h], ct.sum[1][h]);
                 if (split > 1) reinterpret_cast<float *>(sK)[h * kQDim + row] = y;
                 else if (h < group) put(h, y * ct.inv[h]);
             }
@@ -1043,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     }
 }
 
-template <bool F16, bool W>
+template <bool F16, bool W, bool HALF>
 qsa_status launch_as(const QParams &p, int grid, cudaStream_t s) {
     constexpr int kBytes = QLayout<F16 ? 3 : 2>::kBytes;
     static std::mutex mu;
@@ -1055,7 +1094,7 @@ qsa_status launch_as(const QParams &p, int grid, cudaStream_t s) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!opted_in[dev]) {
-            st = check_cuda(cudaFuncSetAttribute(qattn_kernel<F16, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
+            st = check_cuda(cudaFuncSetAttribute(qattn_kernel<F16, W, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
                             "cudaFuncSetAttribute(4-bit selection attention)");
             if (st != QSA_OK) return st;
             opted_in[dev] = true;
@@ -1076,7 +1115,7 @@ qsa_status launch_as(const QParams &p, int grid, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.split > 1 ? 2 : 1;
-    return check_cuda(cudaLaunchKernelEx(&cfg, qattn_kernel<F16, W>, p), "qattn_kernel launch");
+    return check_cuda(cudaLaunchKernelEx(&cfg, qattn_kernel<F16, W, HALF>, p), "qattn_kernel launch");
 }
 
 }  // namespace
@@ -1094,8 +1133,12 @@ qsa_status launch_qcache_attention(const QAttnArgs &a, cudaStream_t s) {
     p.units = (int)units;
     const long long most = p.split > 1 ? units : 2ll * num_sms();
     const int grid = (int)(units < most ? units : most) * p.split;
-    if (a.dt == QSA_F16) return a.weights ? launch_as<true, true>(p, grid, s) : launch_as<true, false>(p, grid, s);
-    return a.weights ? launch_as<false, true>(p, grid, s) : launch_as<false, false>(p, grid, s);
+    const bool half = a.n_heads / a.n_kv_heads <= kH;
+    auto run = a.dt == QSA_F16 ? (a.weights ? (half ? launch_as<true, true, true> : launch_as<true, true, false>)
+                                            : (half ? launch_as<true, false, true> : launch_as<true, false, false>))
+                               : (a.weights ? (half ? launch_as<false, true, true> : launch_as<false, true, false>)
+                                            : (half ? launch_as<false, false, true> : launch_as<false, false, false>));
+    return run(p, grid, s);
 }
 
 }  // namespace qsa

@@ -495,12 +495,9 @@ def block_weights_add(weights: torch.Tensor, ids: torch.Tensor, acc: torch.Tenso
         if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous() or t.numel() != n):
             raise ValueError(f"{name} must be a contiguous fp32 tensor [max_blocks]")
     on = _stream_of(stream, torch.cuda.current_device(), weights=weights, ids=ids, acc=acc, prev=prev, ws=ws)
-    at, before = acc.data_ptr(), _ptr(prev)
-    if before is not None and before != at and abs(before - at) < 4 * n:
-        raise ValueError("prev must be acc itself or not overlap it")
     wp, wn = _ws_args(ws)
     _check("qsa_block_weights_add", lib.qsa_block_weights_add(weights.data_ptr(), ids.data_ptr(), nq, kv, k, float(decay),
-                                                              before, at, n, wp, wn, on))
+                                                              _ptr(prev), acc.data_ptr(), n, wp, wn, on))
     return acc
 
 

@@ -149,11 +149,12 @@ def test_attention_rejects_bad_arguments_before_launch(lib, case, status):
     (dict(k=0), "ARG"), (dict(nq=1 << 20), "ARG"), (dict(nq=1 << 30, kv=1 << 30), "ARG"), (dict(n=0), "ARG"),
     (dict(n=(1 << 24) + 1), "ARG"), (dict(decay=-0.5), "ARG"), (dict(decay=float("nan")), "ARG"),
     (dict(decay=float("inf")), "ARG"), (dict(ws=FAKE + 8), "WS"), (dict(ws_bytes=255), "WS"),
+    (dict(prev=FAKE + 396), "ARG"), (dict(prev=FAKE - 4), "ARG"),   # overlaps acc without being it
 ])
 def test_weights_add_rejects_bad_arguments_before_launch(lib, case, status):
-    a = dict(w=FAKE, ids=FAKE, nq=4, kv=4, k=32, decay=1.0, acc=FAKE, n=100, ws=FAKE, ws_bytes=256)
+    a = dict(w=FAKE, ids=FAKE, nq=4, kv=4, k=32, decay=1.0, prev=None, acc=FAKE, n=100, ws=FAKE, ws_bytes=256)
     a.update(case)
-    st = lib.qsa_block_weights_add(a["w"], a["ids"], a["nq"], a["kv"], a["k"], a["decay"], None, a["acc"], a["n"], a["ws"],
+    st = lib.qsa_block_weights_add(a["w"], a["ids"], a["nq"], a["kv"], a["k"], a["decay"], a["prev"], a["acc"], a["n"], a["ws"],
                                    a["ws_bytes"], None)
     assert st == STATUS[status]
     assert lib.qsa_last_error().decode()
