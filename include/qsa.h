@@ -430,7 +430,11 @@ qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int 
  *             weights add up to its heads, or to 0 when it sees no token
  *
  * Arithmetic: products of codes with the queries exact, accumulated in fp32; softmax
- * statistics, lse and weights in fp32.
+ * statistics, lse and weights in fp32; the weights of the P.V product are rounded to 8
+ * significant bits beside bf16 rows and 12 beside fp16 ones, and to 2^-18 of the largest
+ * weight times the largest V scale where they are smaller.
+ * Launch: as a programmatic dependent of the work before it on `stream`, as
+ * qsa_select_attention.
  * Errors: as qsa_select_attention's, with n_heads a multiple of n_kv_heads of at most 16
  * times it, the cache sizes as qsa_qcache_bytes() has them, nq * n_kv_heads < 2^28, and
  * out_dt other than QSA_F32 or dt.
@@ -470,8 +474,8 @@ qsa_status qsa_select_attention_qcache(const void *qa, int64_t q_stride, int64_t
  * The weights are summed as integers in units of 2^-36, so the result does not depend on
  * the order of the work.
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, nq, n_kv_heads or k < 1, nq * n_kv_heads * k >
- * 2^22, max_blocks outside [1, QSA_MAX_BLOCKS], a decay not finite or < 0;
- * QSA_ERR_WORKSPACE as above.
+ * 2^22, max_blocks outside [1, QSA_MAX_BLOCKS], a decay not finite or < 0, a prev that
+ * overlaps acc without being it; QSA_ERR_WORKSPACE as above.
  */
 qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, float decay,
                                  const float *prev, float *acc, int max_blocks, void *ws, size_t ws_bytes,
@@ -491,6 +495,8 @@ qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int n
  *               block stays last, so a partial one stays valid
  *   ws          a workspace of at least 256 bytes (its flags word is used), or NULL
  *
+ * Launch: as a programmatic dependent of the work before it, and a qsa_gather_blocks behind it
+ * may line up while it runs (both wait before they read anything).
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, 2^20], max_blocks outside
  * [1, QSA_MAX_BLOCKS], weights_stride < max_blocks, n_keep outside [1, max_blocks],
  * n_first < 0, n_last < 1, n_first + n_last > n_keep; QSA_ERR_WORKSPACE as above.

@@ -12,6 +12,11 @@
 //    then emits the kept ids in ascending order, ties to the lower id.  Rows past 16,384 blocks re-read their weights instead
 //    (evict_plan_long_kernel, a radix select of 8 bits a pass).
 // 3. gather_blocks_kernel: a warp copies 2 KB of a record, or as many small records as its lanes hold.
+//
+// Measured (warm graph): 1. 3.4 us for 3 queries x 4 KV heads x 32 slots over 4,032 blocks, 6.6 us for 256
+// queries over 8,125 (every CTA reading all ids took 17.5); launches and one chain of loads.  2 and 3 together:
+// 5.3 us to keep 128 of 257 blocks of one KV head; 55 us to keep 4,096 of 8,125 blocks of 4 (287 MB, of which
+// the move takes 42 us, 6.9 TB/s: the copy rate).
 #include <climits>
 #include <mutex>
 
@@ -320,8 +325,10 @@ static qsa_status launch_dependent(const char *what, void (*kern)(Params...), in
     return check_cuda(cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...), what);
 }
 
-// Above this many entries the cluster form is the faster one (see its comment).
-constexpr int kScanEntries = 2048;
+// Up to this many entries every CTA scans them all, two per thread.  Scan / cluster, us, 8,125 blocks: 3.7 / 4.9 at
+// 256 entries, 5.0 / 6.1 at 1,024, 6.8 / 6.1 at 2,048, 17.5 / 6.6 at 8,192; 2,048 blocks: 3.6 / 3.6, 4.8 / 4.4,
+// 7.1 / 4.9, 18.4 / 5.5.
+constexpr int kScanEntries = 1024;
 
 qsa_status launch_weights_add(const WeightsAddArgs &a, cudaStream_t s) {
     const int entries = a.nq * a.k;
@@ -358,7 +365,8 @@ qsa_status launch_evict_plan(const EvictPlanArgs &a, cudaStream_t s) {
         return launch_dependent("evict_plan_kernel launch", kern, a.n_rows, threads, 0, s, a.weights, a.stride, a.n_tokens,
                                 a.max_blocks, a.n_keep, a.n_first, a.n_last, a.keep, a.new_tokens, a.flags);
     };
-    // the fewest threads that hold a row: a step's barrier is cheaper among fewer warps
+    // the fewest threads that hold a row: a step's barrier is cheaper among fewer warps (257 blocks 3.4 us with 256
+    // threads and 6.4 with 1,024, 4,000 blocks 6.2 with 512 and 8.0 with 1,024)
     if (a.max_blocks <= 1024) return run(evict_plan_kernel<256, 4>, 256);
     if (a.max_blocks <= 4096) return run(evict_plan_kernel<512, 8>, 512);
     if (a.max_blocks <= 8192) return run(evict_plan_kernel<1024, 8>, 1024);

@@ -14,6 +14,12 @@
 // with byte permutes and exchanged among four lanes, and leave as whole 16-byte rows.  A CTA
 // owns its whole block, so a partial block's other tokens (the other nibbles of shared bytes)
 // are merged without atomics.
+//
+// Measured, 131,072 tokens x 4 KV heads, bf16: the reader moves its 336 MB in 51 us (6.65 TB/s, the
+// copy rate); the writer's 336 MB take 78 us: it issues 0.70 instructions a cycle and scheduler (15
+// a value, half of them the quotient and its rounding), against 50 us at the copy rate.  Units dealt as
+// 32 consecutive bytes per thread instead of one 16-byte unit in four took 65 us (reader);
+// codes by divisions and byte-wise transposes 203 us (writer).
 #include <cfloat>
 
 #include "qcache.cuh"

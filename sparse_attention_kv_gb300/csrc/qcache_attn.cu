@@ -12,33 +12,50 @@
 //   o    = sum_t (p_t vs_t) vc_t + sum_t p_t vm_t.
 // A code n in a byte of its own, 0x00..0x0F, is the e4m3 number n 2^-9 (subnormal up to 7, then one
 // binade of eight steps), so unpacking 8 codes takes two masks and a shift, and the products with
-// them are exact.  The other operands are split into e4m3 terms of 4 significant bits, each
-// 2^-4 of the one before, in accumulator columns of their own: two terms hold a bf16 query (8
-// bits) exactly, three an fp16 one (11 bits); the weights p_t vs_t of P.V are rounded to the same
-// number of terms (to 2^-8 of themselves beside bf16 rows, as a bf16 weight would be; 2^-12
-// beside fp16 ones), with steps of 2^-18 (2^-22) of the largest weight at the small end.
+// them are exact.  The other operands are split into e4m3 terms of 4 significant bits:
+//   queries, scaled by a power of two per head: t0 + t1 (+ t2), stacked along K into one accumulator: two
+//     terms hold a bf16 query (8 bits) exactly, three an fp16 one (11 bits);
+//   weights w = p vs g: t0 + (t1 + t2) / 16 with the second group in accumulator columns of its own,
+//     two terms beside bf16 rows (2^-8 of the weight, as a bf16 weight would be), three beside fp16
+//     (2^-12), with steps of 2^-18 of the largest weight at the small end.  The codes are not
+//     centred, so a weight's rounding would count 7.5 steps too often: what the rounding leaves is
+//     summed per head (exactly, in fp16) and goes back times the mean code at the end.  Error of the
+//     output against fp64, 256 queries x 520,000 tokens: 0.0019 of its norm with it, 0.0025 without,
+//     0.0017 from rounding the output to bf16 alone.
 //
-// A CTA takes (query, KV head) units in turn, two CTAs per SM; a step of it is four blocks (two
-// tiles of 128 tokens).  Its warps:
-//   0-3   unpack K, a thread per token, from shared memory into tensor memory: S = K . Q^T with A from
-//         tensor memory (M = 128 tokens, N = 16 heads, K = 128 dims x terms);
-//   4-7   unpack V^T, a thread per dimension (the record holds V by dimension);
-//   0-7   two threads per token, eight heads each: p = exp2(y) against a running reference m per
-//         head, the weights' terms to shared memory (rows of 16 heads per token: B, MN-major);
-//   8     control: the record copies (two steps deep, across units), and the products: S of step t + 1
-//         as soon as its K is unpacked, then O += V^T . P^T of step t (M = 128 dims, K = 256 tokens);
-//   9     preparation of the next unit: its distinct ids, and its queries' terms and sums.
+// A CTA takes (query, KV head) units in turn, two CTAs per SM; a step of it is four blocks, as two
+// tiles of 128 rows: row 32q + r of tile s is block q's token 32s + r, so a thread's two tokens
+// belong to one block.  Its warps:
+//   0-7    softmax, two threads per row, eight heads each: y = log2(e) s - m from S, p = 2^y, the weights'
+//          terms to shared memory (16 heads in a row per token: B, MN-major), a block's sums of p;
+//   8-11   unpacking, a row per thread: K's tokens and V^T's dimensions (the record holds V by
+//          dimension) from shared into tensor memory, and the tokens' pairs to where the softmax reads them;
+//   12     control: S = K . Q^T of step t + 1 as soon as its K is unpacked (M = 128 tokens, N = 16 heads, K = 128
+//          dims x terms, A from tensor memory), then O += V^T . P^T of step t (M = 128 dims, K = 256 tokens);
+//   13     preparation of the next unit: its distinct ids, and its queries' terms and sums;
+//   14, 15 the record halves' copies, two steps deep, across units: K and all pairs, V.
 // So K of the next step (of the next unit, too) unpacks and multiplies behind the softmax of this
 // one, and nothing of a unit's start waits for memory but the first unit's.
 // The references are lazy.  m[h] and the weights' scale g[h] (a power of two that puts the largest
 // p vs seen at 2^4) are taken from a unit's first step, and change only when a later weight
 // would pass 2^8 or its y 30: the barrier before O's product carries that vote, so an ordinary step
-// has one barrier and no reduction across threads.  Sums of p (in fp32) stay per token
-// lane until the unit's end.
+// has one wait and one barrier and no reduction across threads.  Sums of p (in fp32) stay per
+// token lane until the unit's end.
 //
-// When units are few, a cluster of 2, 4 or 8 CTAs splits a unit's blocks and combines the partial
+// When units are few, a cluster of 2, 4 or 8 CTAs splits a unit's steps and combines the partial
 // outputs through distributed shared memory.  Every wait is bounded; on expiry the CTA raises
 // QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
+//
+// Measured (device time in a graph of back-to-back calls, 256 queries x 64 heads in 4 groups x 520,000 tokens,
+// k = 32, weights wanted): 67.5 us, where one read of each selected block by each query is 285 MB (42 us
+// at the copy rate) and DRAM moves 214 MB; the 16-bit attention of the same selection takes 164 us.  It is
+// bound by the softmax warps' instructions (one CTA per SM alone takes 1,590 cycles a step, two
+// 3,600), not by memory, tensor cores (10% busy) or the copies.  Forms on the way, same call: one warpgroup
+// doing everything 105 us; two sharing the heads, four CTAs per SM, 99; a control warp and S in two
+// buffers, three CTAs per SM, 90; shared memory addressed as such 78.5; this form 70; pairs through shared
+// memory, float reductions 67.5.  Not kept: reading S before the step's pairs or before the last step's
+// end (74 and 79: outstanding tensor-memory loads hold up what follows), the unit's end in the
+// unpacking warps (72), longer sleeps in the waits (no change), 88 registers for the softmax (no change).
 #include <cuda.h>
 
 #include <cmath>
@@ -46,7 +63,7 @@
 
 #include "qcache.cuh"
 #include "qsa_device.cuh"
-#include "tc_ptx.cuh"
+#include "tc_ptx_tmem.cuh"
 
 namespace qsa {
 namespace {
@@ -1124,12 +1141,13 @@ qsa_status launch_qcache_attention(const QAttnArgs &a, cudaStream_t s) {
     QParams p{};
     p.a = a;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-    // few units: split each unit's tiles over a cluster, doubling while the grid stays within two CTAs
-    // per SM
+    // few units: split each unit's steps over a cluster, doubling while every CTA has an SM of its own.  Split 1 /
+    // 2 / 4 / 8 at k = 32, us: 4 units 14.0 / 12.5 / 10.5 / 10.0, 32 units 14.3 / 12.7 / 11.4 / 13.8, 76 units
+    // 14.6 / 13.4 / 21.6 / 30.8, 152 units 15.1 / 17.5 / 33 / 53
     const long long units = (long long)a.nq * a.n_kv_heads;
-    const int tiles = (a.k + kStep - 1) / kStep;
+    const int steps = (a.k + kStep - 1) / kStep;
     p.split = 1;
-    while (p.split < kMaxSplit && p.split * 2 <= tiles && units * p.split * 2 <= 2ll * num_sms()) p.split *= 2;
+    while (p.split < kMaxSplit && p.split * 2 <= steps && units * p.split * 2 <= num_sms()) p.split *= 2;
     p.units = (int)units;
     const long long most = p.split > 1 ? units : 2ll * num_sms();
     const int grid = (int)(units < most ? units : most) * p.split;

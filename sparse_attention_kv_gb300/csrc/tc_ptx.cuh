@@ -81,13 +81,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
         : "memory");
 }
-// One contiguous copy; both addresses 16-byte aligned, bytes a multiple of 16.
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols) {
@@ -126,14 +119,6 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t adesc, uint64_t bdesc, 
             : "memory");
     }
 }
-// The same with A in tensor memory (`a`: row i of A in lane i, 4 bytes of its K axis per column).
-__device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
-        : "memory");
-}
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
@@ -162,18 +147,6 @@ __device__ __forceinline__ void tmem_ld64_nowait(uint32_t taddr, uint32_t (&v)[4
           "=r"(v[3][8]), "=r"(v[3][9]), "=r"(v[3][10]), "=r"(v[3][11]), "=r"(v[3][12]), "=r"(v[3][13]), "=r"(v[3][14]), "=r"(v[3][15])
         : "r"(taddr));
 }
-// 8 consecutive columns of this warp's 32 TMEM lanes, one row of 8 values per thread.
-__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Ties loaded registers to a point after tcgen05.wait::ld, so that no use of
 // them is scheduled before the wait.
@@ -182,11 +155,6 @@ __device__ __forceinline__ void reg_fence(uint32_t (&v)[16]) {
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                    "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
                    "+r"(v[15]));
-}
-
-__device__ __forceinline__ void reg_fence(uint32_t (&v)[8]) {
-    asm volatile(""
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]));
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -202,18 +170,6 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
     d |= (uint64_t)2 << 61;
     return d;
 }
-// Shared-memory matrix descriptor: MN-major operand without swizzle.  16 bytes of the M or N axis
-// are contiguous, 8 steps of the K axis lie 16 bytes apart, groups of 8 steps `k_bytes` apart and
-// the next 16 bytes of the M or N axis `mn_bytes` apart.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t k_bytes, uint32_t mn_bytes) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(k_bytes >> 4) << 16;
-    d |= (uint64_t)(mn_bytes >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    return d;
-}
-constexpr uint32_t kIdescBMn = 1u << 16;   // instruction descriptor: B is MN-major
 // Instruction descriptor: fp32 accumulator, A/B format `fmt` (kind::f16: 1 = bf16;
 // kind::tf32: 2; kind::f8f6f4: 0 = e4m3), both K-major, M x N.
 __host__ __device__ constexpr uint32_t idesc(uint32_t fmt, int M, int N) {
