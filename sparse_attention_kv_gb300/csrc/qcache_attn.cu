@@ -26,7 +26,7 @@
 // A CTA takes (query, KV head) units in turn, two CTAs per SM; a step of it is four blocks, as two
 // tiles of 128 rows: row 32q + r of tile s is block q's token 32s + r, so a thread's two tokens
 // belong to one block.  Its warps:
-//   0-7    softmax, two threads per row, eight heads each: y = log2(e) s - m from S, p = 2^y, the weights'
+//   0-7    softmax, two threads per row, eight heads each (or one, in groups of up to eight heads): y = log2(e) s - m from S, p = 2^y, the weights'
 //          terms to shared memory (16 heads in a row per token: B, MN-major), a block's sums of p;
 //   8-11   unpacking, a row per thread: K's tokens and V^T's dimensions (the record holds V by
 //          dimension) from shared into tensor memory, and the tokens' pairs to where the softmax reads them;
@@ -461,8 +461,9 @@ __device__ __forceinline__ void prepare_queries(const QParams &p, int qi, int g,
 }
 
 // F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted; HALF: groups
-// of at most eight heads, whose second half is not computed (61 queries x 8 KV heads x 8: 30.8 -> 24.7 us; as a
-// branch of the one kernel it cost groups of 16 1.5 us of 67).
+// of at most eight heads, whose softmax threads take one token and eight heads each instead of two tokens and half
+// of sixteen heads (256 queries x 8 KV heads x 8 heads, k = 32: 101 us, by the form for sixteen 124; in fp16 142
+// and 181; one query 10.0 and 10.3.  One warpgroup for eight heads and the other idle: 115 and 179).
 template <bool F16, bool W, bool HALF>
 __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constant__ QParams p) {
     constexpr int TERMS = F16 ? 3 : 2;
@@ -721,32 +722,16 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     // q's tokens 0..31 and 32..63, so a warp holds tokens of one block only.
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int wg = warp >> 2, q = warp & 3, row = tid & 127;
-    const int h0 = wg * kH;
-    if (HALF && wg == 1) {   // no heads in this half: its weights stay 0, and its warps only keep step
+    // HALF: each warpgroup takes one tile's tokens and all (at most eight) heads, and sums of theirs go to columns
+    // of its own; the weights of heads 8..15 stay 0
+    constexpr int SUBS = HALF ? 1 : 2;
+    constexpr int kHO = HALF ? kH / 2 : kH;                          // heads of a thread's outputs
+    const int c0 = wg * kH, h0 = HALF ? 0 : c0, ho = HALF ? wg * kHO : c0, sub0 = HALF ? wg : 0;
+    if (HALF && wg == 1) {
         for (int i = 0; i < L::kPBufs * 2 * TERMS; ++i)
-            *reinterpret_cast<uint2 *>(sP + i * L::kTermP + row * kG + h0) = make_uint2(0u, 0u);
+            *reinterpret_cast<uint2 *>(sP + i * L::kTermP + row * kG + kH) = make_uint2(0u, 0u);
         fence_proxy_async();
-        for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
-            wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
-            const int steps = ct.unit[n & 1].steps;
-            for (int i = 0; i < steps; ++i) {
-                bool renew = i == 0;
-                do {
-                    if (renew) {
-                        work_barrier();
-                        work_barrier();
-                    }
-                    renew = vote_barrier(false);
-                } while (renew);
-            }
-            if (steps > 0) {   // the unit's end
-                work_barrier();
-                work_barrier();
-            }
-            if (lane == 0) mbar_arrive(&ct.done[n & 1]);
-            __syncwarp();
-        }
-    } else
+    }
     for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
         const QUnit &un = ct.unit[n & 1];
         wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
@@ -763,30 +748,31 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             wait_all(&ct.sbar[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag);
             if (L::kPBufs == 1 && t > 0) wait_all(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);   // P(t - 1) is read
             tc_fence_after();
-            float ks[2], km[2], vs[2], vm[2];
+            float ks[SUBS], km[SUBS], vs[SUBS], vm[SUBS];
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                const uint2 x = ct.token[t % 3][sub * 128 + row];
+            for (int sub = 0; sub < SUBS; ++sub) {
+                const uint2 x = ct.token[t % 3][(sub0 + sub) * 128 + row];
                 ks[sub] = QFmt<F16>::lo(x.x), km[sub] = QFmt<F16>::hi(x.x);
                 vs[sub] = QFmt<F16>::lo(x.y), vm[sub] = QFmt<F16>::hi(x.y);
             }
-            const bool all_vis = __all_sync(kFull, !(vs[1] < 0.0f));   // and so the first tile's
+            const bool all_vis = __all_sync(kFull, !(vs[SUBS - 1] < 0.0f));   // and so the first tile's
             // y = log2(e) s - m of this thread's tokens, into e
-            float e[2][kH];
+            float e[SUBS][kH];
             auto logits = [&](const float *nmp) {
-                uint32_t v[2][kH];
-                tmem_ld8_nowait(tmem + lanes + kColS + (t & 1) * 2 * kG + h0, v[0]);
-                tmem_ld8_nowait(tmem + lanes + kColS + (t & 1) * 2 * kG + kG + h0, v[1]);
+                uint32_t v[SUBS][kH];
+#pragma unroll
+                for (int sub = 0; sub < SUBS; ++sub)
+                    tmem_ld8_nowait(tmem + lanes + kColS + ((t & 1) * 2 + sub0 + sub) * kG + h0, v[sub]);
                 tmem_wait_ld();
-                reg_fence(v[0]);
-                reg_fence(v[1]);
+#pragma unroll
+                for (int sub = 0; sub < SUBS; ++sub) reg_fence(v[sub]);
 #pragma unroll
                 for (int h = 0; h < kH / 2; h += 2) {
                     const ulonglong2 nm = *reinterpret_cast<const ulonglong2 *>(nmp + h0 + 2 * h);
                     const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(un.f + h0 + 2 * h);
                     const ulonglong2 qs = *reinterpret_cast<const ulonglong2 *>(un.qs + h0 + 2 * h);
 #pragma unroll
-                    for (int sub = 0; sub < 2; ++sub) {
+                    for (int sub = 0; sub < SUBS; ++sub) {
                         const f32x2 ks2 = pack2(ks[sub], ks[sub]), km2 = pack2(km[sub], km[sub]);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -799,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 }
                 if (!all_vis)
 #pragma unroll
-                    for (int sub = 0; sub < 2; ++sub)
+                    for (int sub = 0; sub < SUBS; ++sub)
 #pragma unroll
                         for (int h = 0; h < kH; ++h) e[sub][h] = vs[sub] < 0.0f ? -INFINITY : e[sub][h];
             };
@@ -808,20 +794,22 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 logits(i == 0 && renew == 1 ? ct.zero : ct.nm);
                 if (renew == 1) {
                     // new references: the largest exponent and the largest weight so far, per head
-                    const float lv0 = vs[0] > 0.0f ? lg2(vs[0]) : -INFINITY, lv1 = vs[1] > 0.0f ? lg2(vs[1]) : -INFINITY;
+                    float lv[SUBS];
+#pragma unroll
+                    for (int sub = 0; sub < SUBS; ++sub) lv[sub] = vs[sub] > 0.0f ? lg2(vs[sub]) : -INFINITY;
                     float mine[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int h = 0; h < kH; ++h) {
-                        const float y = warp_fmax(fmaxf(e[0][h], e[1][h]));
-                        const float r = warp_fmax(fmaxf(e[0][h] + lv0, e[1][h] + lv1));
+                        const float y = warp_fmax(HALF ? e[0][h] : fmaxf(e[0][h], e[SUBS - 1][h]));
+                        const float r = warp_fmax(HALF ? e[0][h] + lv[0] : fmaxf(e[0][h] + lv[0], e[SUBS - 1][h] + lv[SUBS - 1]));
                         if (lane == h) {
                             mine[0] = y;
                             mine[1] = r;
                         }
                     }
                     if (lane < kH) {
-                        ct.red[0][warp & 3][h0 + lane] = mine[0];
-                        ct.red[1][warp & 3][h0 + lane] = mine[1];
+                        ct.red[0][warp & 3][c0 + lane] = mine[0];
+                        ct.red[1][warp & 3][c0 + lane] = mine[1];
                     }
                     work_barrier();
                     if (warp == 0) {
@@ -830,6 +818,10 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                         for (int w = 0; w < 4; ++w) {
                             y = fmaxf(y, ct.red[0][w][h]);
                             r = fmaxf(r, ct.red[1][w][h]);
+                        }
+                        if (HALF) {   // both tiles' tokens
+                            y = fmaxf(y, __shfl_xor_sync(kFull, y, kH));
+                            r = fmaxf(r, __shfl_xor_sync(kFull, r, kH));
                         }
                         const float m0 = i == 0 ? 0.0f : -ct.nm[h], rise = y;
                         const float m1 = i == 0 ? rise : m0 + fmaxf(rise, 0.0f);
@@ -869,7 +861,8 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                             for (int j = tid; j < kStep * i * kG; j += kWork) (&ct.w[0][0])[j] *= ct.fl[j % kG];
                         uint32_t o[kH];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
+                        for (int y = 0; y < SUBS; ++y) {
+                            const int x = sub0 + y;          // columns of the leading terms, of the others
                             tmem_ld8_nowait(tmem + lanes + kColO + x * kG + h0, o);
                             tmem_wait_ld();
                             reg_fence(o);
@@ -884,16 +877,18 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 }
                 // p = 2^y, and the weights p vs g in terms to shared memory: [tile][term][token][head]
                 bool over = false;
-                const float faint = fminf(vs[0] < 0.0f ? 1.0f : vs[0], vs[1] < 0.0f ? 1.0f : vs[1]) * ct.least_g;
+                float faint = vs[0] < 0.0f ? 1.0f : vs[0];
+                if (!HALF) faint = fminf(faint, vs[SUBS - 1] < 0.0f ? 1.0f : vs[SUBS - 1]);
+                faint *= ct.least_g;
                 if (__any_sync(kFull, faint < kFaint)) {   // p may grow where the weights do not
 #pragma unroll
-                    for (int h = 0; h < kH; ++h) over |= fmaxf(e[0][h], e[1][h]) > kMostY;
+                    for (int h = 0; h < kH; ++h) over |= fmaxf(e[0][h], e[SUBS - 1][h]) > kMostY;
                 }
                 uint32_t high = 0u, rest[kH / 2];
 #pragma unroll
                 for (int h = 0; h < kH / 2; ++h) rest[h] = 0u;
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub) {
+                for (int sub = 0; sub < SUBS; ++sub) {
                     const float seen = vs[sub] < 0.0f ? 0.0f : vs[sub];   // no weight of -0: its sign would count as a high one
                     const f32x2 vs2 = pack2(seen, seen);
                     uint32_t word[2][TERMS];
@@ -918,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     }
 #pragma unroll
                     for (int y = 0; y < TERMS; ++y)
-                        *reinterpret_cast<uint2 *>(sP + (t % L::kPBufs) * L::kStepP + sub * L::kTileP + y * L::kTermP + row * kG + h0) =
+                        *reinterpret_cast<uint2 *>(sP + (t % L::kPBufs) * L::kStepP + (sub0 + sub) * L::kTileP + y * L::kTermP + row * kG + h0) =
                             make_uint2(word[0][y], word[1][y]);
                 }
                 over = renew == 0 && (over || (high & 0x80808080u) != 0u);
@@ -933,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 renew = 1;
             }
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+            for (int sub = 0; sub < SUBS; ++sub) {
                 const f32x2 vm2 = pack2(vm[sub], vm[sub]);
 #pragma unroll
                 for (int h = 0; h < kH / 2; ++h) {
@@ -942,12 +937,12 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     mv[h] = fma2(e2, vm2, mv[h]);
                 }
             }
-            if (W) {   // this block's sums: no other warp has this block and these heads
+            if (W) {   // this block's sums: no other warp has this block and these columns
                 float x[kH];
 #pragma unroll
-                for (int h = 0; h < kH; ++h) x[h] = e[0][h] + e[1][h];
+                for (int h = 0; h < kH; ++h) x[h] = HALF ? e[0][h] : e[0][h] + e[SUBS - 1][h];
                 const float w = warp_sum8(x, lane);
-                if ((lane & 3) == 0) ct.w[kStep * i + q][h0 + (lane >> 2)] = w;
+                if ((lane & 3) == 0) ct.w[kStep * i + q][c0 + (lane >> 2)] = w;
             }
         }
 
@@ -974,14 +969,14 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     }
                 }
                 const float sum = warp_sum8(x, lane);
-                if ((lane & 3) == 0) ct.red[j][warp & 3][h0 + (lane >> 2)] = sum;
+                if ((lane & 3) == 0) ct.red[j][warp & 3][c0 + (lane >> 2)] = sum;
             }
             work_barrier();
             if (tid < 3 * kG) {
                 const int j = tid / kG, h = tid % kG;
                 float sum = 0.0f;
                 if (j < 2 || TERMS == 2)
-                    for (int w = 0; w < 4; ++w) sum += ct.red[j][w][h];
+                    for (int w = 0; w < 4; ++w) sum += HALF ? ct.red[j][w][h] + ct.red[j][w][h ^ kH] : ct.red[j][w][h];
                 ct.sum[j][h] = sum;
                 if (j == 0) ct.inv[h] = 1.0f / sum;
             }
@@ -990,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             tc_fence_after();
             uint32_t o[2][kH];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) tmem_ld8_nowait(tmem + lanes + kColO + j * kG + h0, o[j]);
+            for (int j = 0; j < 2; ++j) tmem_ld8_nowait(tmem + lanes + kColO + j * kG + ho, o[j]);
             tmem_wait_ld();
             reg_fence(o[0]);
             reg_fence(o[1]);
@@ -998,8 +993,8 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             // this thread's dimension of its heads.  The codes' mean, 7.5, times what the rounding left of
             // the weights takes most of its effect away.
 #pragma unroll
-            for (int j = 0; j < kH; ++j) {
-                const int h = h0 + j;
+            for (int j = 0; j < kHO; ++j) {
+                const int h = ho + j;
                 float y = fmaf(__uint_as_float(o[1][j]), 0.0625f, __uint_as_float(o[0][j]));
                 y = fmaf(fmaf(y, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), ct.ig[h], ct.sum[1][h]);
                 if (split > 1) reinterpret_cast<float *>(sK)[h * kQDim + row] = y;
@@ -1014,16 +1009,17 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
 #pragma unroll
                     for (int j = 0; j < kG / 4; ++j) {
                         const float4 x4 = w4[j], y4 = i4[j];
-                        w += 4 * j < group ? x4.x * y4.x : 0.0f;
-                        w += 4 * j + 1 < group ? x4.y * y4.y : 0.0f;
-                        w += 4 * j + 2 < group ? x4.z * y4.z : 0.0f;
-                        w += 4 * j + 3 < group ? x4.w * y4.w : 0.0f;
+                        const int h = HALF ? 4 * j % kH : 4 * j;
+                        w += h < group ? x4.x * y4.x : 0.0f;
+                        w += h + 1 < group ? x4.y * y4.y : 0.0f;
+                        w += h + 2 < group ? x4.z * y4.z : 0.0f;
+                        w += h + 3 < group ? x4.w * y4.w : 0.0f;
                     }
                     a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + un.slot[tid - 64]] = w;
                 }
             }
         } else if (split == 1) {   // no visible token: o = 0
-            for (int h = h0; h < min(group, h0 + kH); ++h) put(h, 0.0f);
+            for (int h = ho; h < min(group, ho + kHO); ++h) put(h, 0.0f);
             if (a.lse && tid < group) a.lse[head0 + tid] = -INFINITY;
         }
         __syncwarp();
@@ -1092,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             __syncthreads();
             if (tid < un.nloc) {
                 float w = 0.0f;
-                for (int h = 0; h < group; ++h) w = fmaf(ct.w[tid][h], ct.fl[h], w);
+                for (int h = 0; h < group; ++h) w = fmaf(HALF ? ct.w[tid][h] + ct.w[tid][h + kH] : ct.w[tid][h], ct.fl[h], w);
                 a.weights[((size_t)qi * a.n_kv_heads + g) * a.k + un.slot[un.b0 + tid]] = w;
             }
         }

@@ -363,6 +363,25 @@ def test_attention_on_unusual_values(kind, fmt):
         check_attention(_attend(qt, cache, ids, nt, fmt, f32=True), want, fmt, out_f32=True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group", [5, 8, 16])
+@pytest.mark.parametrize("kind", ["rising", "v growing", "one"])
+def test_attention_on_unusual_values_in_units_of_many_steps(kind, group, fmt):
+    """As many units as leave each to one CTA, whose running maxima move in its later steps, too."""
+    nq, n = 160, 20 * 64 - 13
+    k, v, q = _special(40, fmt, kind)
+    kt, _ = to16(k[:n], fmt)
+    vt, _ = to16(v[:n], fmt)
+    cache = qsa.alloc_qcache(1, 20 * 64)
+    qsa.qcache_append(kt, vt, cache, 0)
+    qt, qd = to16(np.concatenate([q[:1], q[:1] * 0.5, q[1:]])[np.arange(nq) % 3][:, :group], fmt)
+    ids = np.repeat(np.arange(20, dtype=np.int32)[None], nq, 0)
+    nt = n - np.arange(nq) // 3
+    want = oq.attention(qd, cache.cpu().numpy(), ids, nt, float(np.float32(128 ** -0.5)), fmt)
+    check_attention(_attend(qt, cache, ids, nt, fmt), want, fmt)
+    check_attention(_attend(qt, cache, ids, nt, fmt, f32=True), want, fmt, out_f32=True)
+
+
 def test_attention_other_scales():
     fmt = oq.BF16
     host = random_cache(15, 1, 9, fmt)
