@@ -26,8 +26,9 @@
 // A CTA takes (query, KV head) units in turn, two CTAs per SM; a step of it is four blocks, as two
 // tiles of 128 rows: row 32q + r of tile s is block q's token 32s + r, so a thread's two tokens
 // belong to one block.  Its warps:
-//   0-7    softmax, two threads per row, eight heads each (or one, in groups of up to eight heads): y = log2(e) s - m from S, p = 2^y, the weights'
-//          terms to shared memory (16 heads in a row per token: B, MN-major), a block's sums of p;
+//   0-7    softmax, two threads per row, eight heads each (in groups of up to eight heads one thread per row):
+//          y = log2(e) s - m from S, p = 2^y, the weights' terms to shared memory (16 heads in a row per
+//          token: B, MN-major), a block's sums of p;
 //   8-11   unpacking, a row per thread: K's tokens and V^T's dimensions (the record holds V by
 //          dimension) from shared into tensor memory, and the tokens' pairs to where the softmax reads them;
 //   12     control: S = K . Q^T of step t + 1 as soon as its K is unpacked (M = 128 tokens, N = 16 heads, K = 128

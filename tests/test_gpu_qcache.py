@@ -192,6 +192,8 @@ CASES = [
     (80, 4, 16, 48, None, 32, None),      # more units than fit at once
     (61, 8, 5, 20, None, 17, "random"),
     (200, 4, 16, 12, None, 4, None),
+    (90, 4, 16, 70, None, 64, "random"),  # the largest selections, several units per CTA
+    (160, 2, 8, 70, 4477, 64, None),
 ]
 
 
@@ -365,10 +367,11 @@ def test_attention_on_unusual_values(kind, fmt):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("group", [5, 8, 16])
+@pytest.mark.parametrize("nq", [3, 160])
 @pytest.mark.parametrize("kind", ["rising", "v growing", "one"])
-def test_attention_on_unusual_values_in_units_of_many_steps(kind, group, fmt):
-    """As many units as leave each to one CTA, whose running maxima move in its later steps, too."""
-    nq, n = 160, 20 * 64 - 13
+def test_attention_on_unusual_values_in_units_of_many_steps(kind, nq, group, fmt):
+    """Units split over a cluster, and so many that each is one CTA's, whose running maxima move in its later steps, too."""
+    n = 20 * 64 - 13
     k, v, q = _special(40, fmt, kind)
     kt, _ = to16(k[:n], fmt)
     vt, _ = to16(v[:n], fmt)
