@@ -33,7 +33,8 @@
 //          dimension) from shared into tensor memory, and the tokens' pairs to where the softmax reads them;
 //   12     control: S = K . Q^T of step t + 1 as soon as its K is unpacked (M = 128 tokens, N = 16 heads, K = 128
 //          dims x terms, A from tensor memory), then O += V^T . P^T of step t (M = 128 dims, K = 256 tokens);
-//   13     preparation of the next unit: its distinct ids, and its queries' terms and sums;
+//   13     preparation of the next unit: its distinct ids, and its queries' terms and sums (the first unit's
+//          queries are shared out among the softmax warps: one warp takes 3 us for them);
 //   14, 15 the record halves' copies, two steps deep, across units: K and all pairs, V.
 // So K of the next step (of the next unit, too) unpacks and multiplies behind the softmax of this
 // one, and nothing of a unit's start waits for memory but the first unit's.
@@ -413,51 +414,60 @@ __device__ __forceinline__ void prepare_ids(const QParams &p, int qi, int g, int
     }
 }
 
-// The preparation warp: the group's queries as e4m3 terms (four dimensions of a head per lane).
-template <bool F16, int TERMS>
-__device__ __forceinline__ void prepare_queries(const QParams &p, int qi, int g, int group, QUnit &u, uint8_t *sQ) {
+// One warp: N (2 or 8) of the group's queries from head hh, as e4m3 terms (four dimensions of a head per lane).
+template <bool F16, int TERMS, int N>
+__device__ __forceinline__ void prepare_queries(const QParams &p, int u_at, int group, int hh, QUnit &u, uint8_t *sQ) {
     const QAttnArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, qi = u_at / a.n_kv_heads, g = u_at - qi * a.n_kv_heads;
     const uint16_t *q = static_cast<const uint16_t *>(a.qa) + qi * a.q_stride + (int64_t)(g * group) * a.q_head_stride + lane * 4;
-#pragma unroll 1
-    for (int hh = 0; hh < kG; hh += 8) {
-        uint2 raw[8];
+    uint2 raw[N];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            raw[j] = hh + j < group ? *reinterpret_cast<const uint2 *>(q + (hh + j) * a.q_head_stride) : make_uint2(0u, 0u);
-        float sums[8];
-        int es[8];
+    for (int j = 0; j < N; ++j)
+        raw[j] = hh + j < group ? *reinterpret_cast<const uint2 *>(q + (hh + j) * a.q_head_stride) : make_uint2(0u, 0u);
+    float sums[N];
+    int es[N];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int h = hh + j;
-            const float x[4] = {QFmt<F16>::lo(raw[j].x), QFmt<F16>::hi(raw[j].x), QFmt<F16>::lo(raw[j].y), QFmt<F16>::hi(raw[j].y)};
-            uint32_t big = 0u;   // the bits of the largest magnitude (an infinity or a NaN stays the largest)
+    for (int j = 0; j < N; ++j) {
+        const int h = hh + j;
+        const float x[4] = {QFmt<F16>::lo(raw[j].x), QFmt<F16>::hi(raw[j].x), QFmt<F16>::lo(raw[j].y), QFmt<F16>::hi(raw[j].y)};
+        uint32_t big = 0u;   // the bits of the largest magnitude (an infinity or a NaN stays the largest)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-            big = __reduce_max_sync(kFull, big);
-            sums[j] = (x[0] + x[1]) + (x[2] + x[3]);
-            const bool finite = big < 0x7F800000u;
-            // a power of two that puts the largest magnitude into [128, 256), in two exact steps
-            const int e = finite && big != 0u ? 7 - ilogbf(__uint_as_float(big)) : 0;
-            es[j] = finite ? e : 1024;
-            const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
-            uint32_t terms[TERMS];
-            split_query<TERMS>(finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u,
-                               finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u, terms);
+        for (int i = 0; i < 4; ++i) big = max(big, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+        big = __reduce_max_sync(kFull, big);
+        sums[j] = (x[0] + x[1]) + (x[2] + x[3]);
+        const bool finite = big < 0x7F800000u;
+        // a power of two that puts the largest magnitude into [128, 256), in two exact steps
+        const int lg = big >= 0x00800000u ? (int)(big >> 23) - 127 : -118 - __clz((int)big);
+        const int e = finite && big != 0u ? 7 - lg : 0;
+        es[j] = finite ? e : 1024;
+        const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
+        uint32_t terms[TERMS];
+        split_query<TERMS>(finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u,
+                           finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u, terms);
 #pragma unroll
-            for (int t = 0; t < TERMS; ++t)
-                *reinterpret_cast<uint32_t *>(sQ + (t * kG + h) * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) =
-                    terms[t];
+        for (int t = 0; t < TERMS; ++t)
+            *reinterpret_cast<uint32_t *>(sQ + (t * kG + h) * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) = terms[t];
+    }
+    constexpr int kPer = 32 / N;   // lanes that hold a head's sum
+    float sum;
+    if constexpr (N == 8) {
+        sum = warp_sum8(sums, lane);
+    } else {                       // the same pairs in the same order
+        static_assert(N == 2, "two or eight heads");
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sums[0] += __shfl_xor_sync(kFull, sums[0], o);
+            sums[1] += __shfl_xor_sync(kFull, sums[1], o);
         }
-        const float sum = warp_sum8(sums, lane);
-        int e = es[0];
+        sum = lane < kPer ? sums[0] : sums[1];
+    }
+    int e = es[0];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) e = (lane >> 2) == j ? es[j] : e;
-        if ((lane & 3) == 0) {
-            const int h = hh + (lane >> 2);
-            u.f[h] = e == 1024 ? __uint_as_float(0x7FC00000u) : scalbnf(p.scale_log2, 9 - e);
-            u.qs[h] = p.scale_log2 * sum;
-        }
+    for (int j = 1; j < N; ++j) e = lane / kPer == j ? es[j] : e;
+    if (lane % kPer == 0) {
+        const int h = hh + lane / kPer;
+        u.f[h] = e == 1024 ? __uint_as_float(0x7FC00000u) : scalbnf(p.scale_log2, 9 - e);
+        u.qs[h] = p.scale_log2 * sum;
     }
 }
 
@@ -494,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.sbar[i], 5);    // S is complete, and the unpacking warps' pairs stand
             mbar_init(&ct.ids_ready[i], 1);
-            mbar_init(&ct.ready[i], 1);
+            mbar_init(&ct.ready[i], 2);   // the ids, the queries
             mbar_init(&ct.done[i], 15);   // all warps but the preparing one
         }
         mbar_init(&ct.obar, 1);
@@ -515,10 +525,13 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             prepare_ids<W>(p, qi, g, rank, ct.unit[n & 1]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&ct.ids_ready[n & 1]);
-            prepare_queries<F16, TERMS>(p, qi, g, group, ct.unit[n & 1], sQ + (n & 1) * L::kQBytes);
+            if (n > 0)   // the first unit's queries come from the softmax warps
+#pragma unroll 1
+                for (int hh = 0; hh < kG; hh += 8)
+                    prepare_queries<F16, TERMS, 8>(p, u, group, hh, ct.unit[n & 1], sQ + (n & 1) * L::kQBytes);
             fence_proxy_async();   // the queries are read by the tensor core
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ct.ready[n & 1]);
+            if (lane < (n > 0 ? 2 : 1)) mbar_arrive(&ct.ready[n & 1]);
         }
     } else if (warp >= kFetch) {
         // copies, a lane per block: the first warp K and the pairs, the second V
@@ -558,6 +571,13 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     } else if (warp == kControl) {
         tmem_alloc(&ct.tmem_base, kCols);
         tmem_relinquish();
+    }
+    if (warp < kUnpack) {   // nothing to do yet: two heads of the first unit's queries each
+        prepare_queries<F16, TERMS, 2>(p, u0, group, 2 * warp, ct.unit[0], sQ);
+        fence_proxy_async();
+        work_barrier();
+        if (tid == 0) mbar_arrive(&ct.ready[0]);
+        __syncwarp();
     }
     if (warp <= kControl) {
     tc_fence_before();
