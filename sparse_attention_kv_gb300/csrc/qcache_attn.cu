@@ -110,12 +110,13 @@ struct QCtrl {
     alignas(16) float g[kG];              // power of two of the weights
     alignas(16) float fl[kG];             // rescaling of the sums and of the outputs
     alignas(16) float fo[kG];
-    alignas(16) float inv[kG];
     float top[kG], eg[kG];                // largest log2(p vs) + m seen, log2(g)
     float ig[kG];                         // 1 / g
     float least_g;
-    float red[3][4][kG];
-    float sum[3][kG];                     // l, sum of p vm, 16 x what the weights' rounding took away
+    float red[2][4][kG];                  // maxima by warp
+    float part[3][4][kG];                 // a unit's sums by warp: l, sum of p vm, 16 x what the weights' rounding took away
+    alignas(16) float fin[8][4][kG];      // a warp's copy of the heads' factors of the outputs, and 1 / l
+    float sum[kG];                        // l
     float2 ml[kMaxSplit][kG];             // (m, l) of every CTA of a cluster
     alignas(16) float w[kSel][kG];        // sums of p over a slot's tokens
 };
@@ -990,18 +991,35 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     }
                 }
                 const float sum = warp_sum8(x, lane);
-                if ((lane & 3) == 0) ct.red[j][warp & 3][c0 + (lane >> 2)] = sum;
+                if ((lane & 3) == 0) ct.part[j][warp & 3][c0 + (lane >> 2)] = sum;
             }
             work_barrier();
-            if (tid < 3 * kG) {
-                const int j = tid / kG, h = tid % kG;
-                float sum = 0.0f;
-                if (j < 2 || TERMS == 2)
-                    for (int w = 0; w < 4; ++w) sum += HALF ? ct.red[j][w][h] + ct.red[j][w][h ^ kH] : ct.red[j][w][h];
-                ct.sum[j][h] = sum;
-                if (j == 0) ct.inv[h] = 1.0f / sum;
+            // o = (512 O ig + mean part ig + sum of p vm) / l: every warp makes all heads' factors for itself
+            float *fin = ct.fin[warp][0];
+            {
+                const int h = lane & 15, w = lane >> 4;
+                float tot[3];
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    tot[j] = 0.0f;
+                    if (j == 2 && TERMS == 3) break;
+                    tot[j] = ct.part[j][w][h] + ct.part[j][w + 2][h];
+                    tot[j] += __shfl_xor_sync(kFull, tot[j], 16);
+                    if (HALF) tot[j] += __shfl_xor_sync(kFull, tot[j], kH);   // both tiles' tokens
+                }
+                const float inv = 1.0f / tot[0], norm = split == 1 ? inv : 1.0f, ig = ct.ig[h];
+                if (w == 0) {
+                    fin[h] = ig;
+                    fin[kG + h] = 512.0f * norm;
+                    fin[3 * kG + h] = inv;
+                    fin[2 * kG + h] = fmaf((7.5f / 16.0f) * tot[2], ig, tot[1]) * norm;
+                    if (warp == 0) {
+                        ct.sum[h] = tot[0];
+                        if (split == 1 && a.lse && h < group) a.lse[head0 + h] = (log2f(tot[0]) - ct.nm[h]) * 0.6931471805599453f;
+                    }
+                }
+                __syncwarp();
             }
-            work_barrier();
             wait_all(&ct.obar, (uint32_t)(t - 1) & 1u, abort_flag);
             tc_fence_after();
             uint32_t o[2][kH];
@@ -1014,18 +1032,22 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             // this thread's dimension of its heads.  The codes' mean, 7.5, times what the rounding left of
             // the weights takes most of its effect away.
 #pragma unroll
-            for (int j = 0; j < kHO; ++j) {
-                const int h = ho + j;
-                float y = fmaf(__uint_as_float(o[1][j]), 0.0625f, __uint_as_float(o[0][j]));
-                y = fmaf(fmaf(y, 512.0f, (7.5f / 16.0f) * ct.sum[2][h]), ct.ig[h], ct.sum[1][h]);
-                if (split > 1) reinterpret_cast<float *>(sK)[h * kQDim + row] = y;
-                else if (h < group) put(h, y * ct.inv[h]);
+            for (int j = 0; j < kHO; j += 4) {
+                const float4 ig = *reinterpret_cast<const float4 *>(fin + ho + j), up = *reinterpret_cast<const float4 *>(fin + kG + ho + j);
+                const float4 add = *reinterpret_cast<const float4 *>(fin + 2 * kG + ho + j);
+                const float igs[4] = {ig.x, ig.y, ig.z, ig.w}, ups[4] = {up.x, up.y, up.z, up.w}, adds[4] = {add.x, add.y, add.z, add.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int h = ho + j + x;
+                    const float y = fmaf(fmaf(__uint_as_float(o[1][j + x]), 0.0625f, __uint_as_float(o[0][j + x])) * ups[x], igs[x], adds[x]);
+                    if (split > 1) reinterpret_cast<float *>(sK)[h * kQDim + row] = y;
+                    else if (h < group) put(h, y);
+                }
             }
             if (split == 1) {
-                if (a.lse && tid < group) a.lse[head0 + tid] = (log2f(ct.sum[0][tid]) - ct.nm[tid]) * 0.6931471805599453f;
                 if (W && tid >= 64 && tid - 64 < nloc) {
                     const float4 *w4 = reinterpret_cast<const float4 *>(ct.w[tid - 64]);
-                    const float4 *i4 = reinterpret_cast<const float4 *>(ct.inv);
+                    const float4 *i4 = reinterpret_cast<const float4 *>(fin + 3 * kG);
                     float w = 0.0f;
 #pragma unroll
                     for (int j = 0; j < kG / 4; ++j) {
@@ -1073,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             }
         for (int x = tid; x < kG * split; x += kThreads) {
             const int h = x % kG;
-            st_cluster(&ct.ml[rank][h], x / kG, make_float2(some ? -ct.nm[h] : -INFINITY, some ? ct.sum[0][h] : 0.0f));
+            st_cluster(&ct.ml[rank][h], x / kG, make_float2(some ? -ct.nm[h] : -INFINITY, some ? ct.sum[h] : 0.0f));
         }
         cluster_sync();
         for (int x = tid; x < nh * kQDim; x += kThreads) {
