@@ -429,10 +429,11 @@ qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int 
  *             context, or a repeat of an earlier slot gets 0); a (query, KV head)'s
  *             weights add up to its heads, or to 0 when it sees no token
  *
- * Arithmetic: products of codes with the queries exact, accumulated in fp32; softmax
- * statistics, lse and weights in fp32; the weights of the P.V product are rounded to 8
- * significant bits beside bf16 rows and 12 beside fp16 ones, and to 2^-18 of the largest
- * weight times the largest V scale where they are smaller.
+ * Arithmetic: products of codes with the queries exact (queries to 2^-18 of their head's
+ * largest value), accumulated in fp32; softmax statistics, lse and weights in fp32; the
+ * weights of the P.V product are rounded to 8 significant bits beside bf16 rows and 12 beside
+ * fp16 ones, and to 2^-18 of the largest weight times the largest V scale where they are
+ * smaller.
  * Launch: as a programmatic dependent of the work before it on `stream`, as
  * qsa_select_attention.
  * Errors: as qsa_select_attention's, with n_heads a multiple of n_kv_heads of at most 16

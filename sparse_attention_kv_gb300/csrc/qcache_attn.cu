@@ -14,7 +14,9 @@
 // binade of eight steps), so unpacking 8 codes takes two masks and a shift, and the products with
 // them are exact.  The other operands are split into e4m3 terms of 4 significant bits:
 //   queries, scaled by a power of two per head: t0 + t1 (+ t2), stacked along K into one accumulator: two
-//     terms hold a bf16 query (8 bits) exactly, three an fp16 one (11 bits);
+//     terms hold a bf16 query (8 bits) exactly, three an fp16 one (11 bits), but for what lies below 2^-18 of
+//     the head's largest value; in fp16, where that is more of them, its sum goes back times the mean code
+//     (error of lse over single blocks 1.7e-6 of its norm without);
 //   weights w = p vs g: t0 + (t1 + t2) / 16 with the second group in accumulator columns of its own,
 //     two terms beside bf16 rows (2^-8 of the weight, as a bf16 weight would be), three beside fp16
 //     (2^-12), with steps of 2^-18 of the largest weight at the small end.  The codes are not
@@ -49,15 +51,18 @@
 // QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 //
 // Measured (device time in a graph of back-to-back calls, 256 queries x 64 heads in 4 groups x 520,000 tokens,
-// k = 32, weights wanted): 67.5 us, where one read of each selected block by each query is 285 MB (42 us
-// at the copy rate) and DRAM moves 214 MB; the 16-bit attention of the same selection takes 164 us.  It is
-// bound by the softmax warps' instructions (one CTA per SM alone takes 1,590 cycles a step, two
-// 3,600), not by memory, tensor cores (10% busy) or the copies.  Forms on the way, same call: one warpgroup
-// doing everything 105 us; two sharing the heads, four CTAs per SM, 99; a control warp and S in two
-// buffers, three CTAs per SM, 90; shared memory addressed as such 78.5; this form 70; pairs through shared
-// memory, float reductions 67.5.  Not kept: reading S before the step's pairs or before the last step's
-// end (74 and 79: outstanding tensor-memory loads hold up what follows), the unit's end in the
-// unpacking warps (72), longer sleeps in the waits (no change), 88 registers for the softmax (no change).
+// k = 32, weights wanted): 63.5 us, where one read of each selected block by each query is 285 MB (42 us
+// at the copy rate) and DRAM moves 218 MB; the 16-bit attention of the same selection takes 164 us.  It is
+// bound by the softmax warps' chain of instructions (of a unit's 36,000 cycles, in a build that reads the clock:
+// 1,800 until it stands prepared, 6,300 for the first step with its maxima, 3,400 for each other one, 4,200
+// for the end; one CTA per SM takes 83 us), not by memory, tensor cores (12% busy) or the copies.  Without the
+// weights 54-56 us.  Forms on the way, same call: one warpgroup doing everything 105 us; two sharing the heads,
+// four CTAs per SM, 99; a control warp and S in two buffers, three CTAs per SM, 90; shared memory addressed as
+// such 78.5; this division of labour 70; pairs through shared memory, float reductions 67.5; the first unit's
+// queries shared out 64.  Not kept: reading S before the step's pairs or before the last step's end (74 and 79:
+// outstanding tensor-memory loads hold up what follows), the unit's end in the unpacking warps (72), longer sleeps
+// in the waits (no change), 88 registers for the softmax (no change), references made by every warp for itself
+// (-2% in bf16, +2% in fp16 and in groups of eight).
 #include <cuda.h>
 
 #include <cmath>
@@ -94,6 +99,7 @@ struct QUnit {
     int32_t slot[kSel];                   // and the slots they came from
     alignas(16) float f[kG];              // scale log2(e) 2^9 / (the head's power-of-two scaling of q)
     alignas(16) float qs[kG];             // scale log2(e) sum(q)
+    alignas(16) float fc[kG];             // f times what the terms left of the queries times the codes' mean, 7.5 (fp16)
 };
 
 struct QCtrl {
@@ -237,8 +243,9 @@ __device__ __forceinline__ void split_weights(const float (&w)[4], const uint32_
 }
 // The e4m3 terms of four query values below 256: v = t0 + t1 (+ t2), exact for the format's significand down
 // to 2^-10 (bf16) and 2^-7 (fp16) of the head's largest value, to 2^-18 of it below.
+// What is left stays in h0 and h1.
 template <int TERMS>
-__device__ __forceinline__ void split_query(uint32_t h0, uint32_t h1, uint32_t (&t)[TERMS]) {
+__device__ __forceinline__ void split_query(uint32_t &h0, uint32_t &h1, uint32_t (&t)[TERMS]) {
 #pragma unroll
     for (int u = 0; u < TERMS; ++u) {
         uint32_t a, b;
@@ -425,7 +432,7 @@ __device__ __forceinline__ void prepare_queries(const QParams &p, int u_at, int 
 #pragma unroll
     for (int j = 0; j < N; ++j)
         raw[j] = hh + j < group ? *reinterpret_cast<const uint2 *>(q + (hh + j) * a.q_head_stride) : make_uint2(0u, 0u);
-    float sums[N];
+    float sums[N], lefts[N];
     int es[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -443,39 +450,44 @@ __device__ __forceinline__ void prepare_queries(const QParams &p, int u_at, int 
         es[j] = finite ? e : 1024;
         const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
         uint32_t terms[TERMS];
-        split_query<TERMS>(finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u,
-                           finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u, terms);
+        uint32_t h0 = finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u, h1 = finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u;
+        split_query<TERMS>(h0, h1, terms);
+        if (F16) lefts[j] = (h2_lo(h0) + h2_hi(h0)) + (h2_lo(h1) + h2_hi(h1));
 #pragma unroll
         for (int t = 0; t < TERMS; ++t)
             *reinterpret_cast<uint32_t *>(sQ + (t * kG + h) * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) = terms[t];
     }
     constexpr int kPer = 32 / N;   // lanes that hold a head's sum
-    float sum;
-    if constexpr (N == 8) {
-        sum = warp_sum8(sums, lane);
-    } else {                       // the same pairs in the same order
-        static_assert(N == 2, "two or eight heads");
+    auto over_lanes = [&](float (&x)[N]) {
+        if constexpr (N == 8) {
+            return warp_sum8(x, lane);
+        } else {                   // the same pairs in the same order
+            static_assert(N == 2, "two or eight heads");
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            sums[0] += __shfl_xor_sync(kFull, sums[0], o);
-            sums[1] += __shfl_xor_sync(kFull, sums[1], o);
+            for (int o = 16; o > 0; o >>= 1) {
+                x[0] += __shfl_xor_sync(kFull, x[0], o);
+                x[1] += __shfl_xor_sync(kFull, x[1], o);
+            }
+            return lane < kPer ? x[0] : x[1];
         }
-        sum = lane < kPer ? sums[0] : sums[1];
-    }
+    };
+    const float sum = over_lanes(sums), left = F16 ? over_lanes(lefts) : 0.0f;
     int e = es[0];
 #pragma unroll
     for (int j = 1; j < N; ++j) e = lane / kPer == j ? es[j] : e;
     if (lane % kPer == 0) {
         const int h = hh + lane / kPer;
-        u.f[h] = e == 1024 ? __uint_as_float(0x7FC00000u) : scalbnf(p.scale_log2, 9 - e);
+        const float f = e == 1024 ? __uint_as_float(0x7FC00000u) : scalbnf(p.scale_log2, 9 - e);
+        u.f[h] = f;
+        if (F16) u.fc[h] = f * (left * (7.5f / 512.0f));
         u.qs[h] = p.scale_log2 * sum;
     }
 }
 
 // F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted; HALF: groups
 // of at most eight heads, whose softmax threads take one token and eight heads each instead of two tokens and half
-// of sixteen heads (256 queries x 8 KV heads x 8 heads, k = 32: 101 us, by the form for sixteen 124; in fp16 142
-// and 181; one query 10.0 and 10.3.  One warpgroup for eight heads and the other idle: 115 and 179).
+// of sixteen heads (256 queries x 8 KV heads x 8 heads, k = 32: 98 us, by the form for sixteen 120; in fp16 145
+// and 192; one query 8.5 and 8.8.  One warpgroup for eight heads and the other idle took 115 where this took 101).
 template <bool F16, bool W, bool HALF>
 __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constant__ QParams p) {
     constexpr int TERMS = F16 ? 3 : 2;
@@ -793,6 +805,8 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     const ulonglong2 nm = *reinterpret_cast<const ulonglong2 *>(nmp + h0 + 2 * h);
                     const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(un.f + h0 + 2 * h);
                     const ulonglong2 qs = *reinterpret_cast<const ulonglong2 *>(un.qs + h0 + 2 * h);
+                    ulonglong2 fc = make_ulonglong2(0ull, 0ull);
+                    if (F16) fc = *reinterpret_cast<const ulonglong2 *>(un.fc + h0 + 2 * h);
 #pragma unroll
                     for (int sub = 0; sub < SUBS; ++sub) {
                         const f32x2 ks2 = pack2(ks[sub], ks[sub]), km2 = pack2(km[sub], km[sub]);
@@ -800,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                         for (int j = 0; j < 2; ++j) {
                             const int x = 2 * (h + j);
                             const f32x2 s2 = pack2(__uint_as_float(v[sub][x]), __uint_as_float(v[sub][x + 1]));
-                            const f32x2 y = fma2(mul2(s2, j ? f.y : f.x), ks2, fma2(km2, j ? qs.y : qs.x, j ? nm.y : nm.x));
+                            const f32x2 sf = F16 ? fma2(s2, j ? f.y : f.x, j ? fc.y : fc.x) : mul2(s2, j ? f.y : f.x);
+                            const f32x2 y = fma2(sf, ks2, fma2(km2, j ? qs.y : qs.x, j ? nm.y : nm.x));
                             unpack2(y, e[sub][x], e[sub][x + 1]);
                         }
                     }
@@ -1181,8 +1196,8 @@ qsa_status launch_qcache_attention(const QAttnArgs &a, cudaStream_t s) {
     p.a = a;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
     // few units: split each unit's steps over a cluster, doubling while every CTA has an SM of its own.  Split 1 /
-    // 2 / 4 / 8 at k = 32, us: 4 units 14.0 / 12.5 / 10.5 / 10.0, 32 units 14.3 / 12.7 / 11.4 / 13.8, 76 units
-    // 14.6 / 13.4 / 21.6 / 30.8, 152 units 15.1 / 17.5 / 33 / 53
+    // 2 / 4 / 8 at k = 32, us: 4 units 11.8 / 10.6 / 8.6 / 8.0, 32 units 12.1 / 10.8 / 9.4 / 11.8, 76 units
+    // 12.3 / 11.5 / 17.8 / 25.3, 152 units 12.6 / 15.6 / 27.6 / 43.6
     const long long units = (long long)a.nq * a.n_kv_heads;
     const int steps = (a.k + kStep - 1) / kStep;
     p.split = 1;

@@ -385,6 +385,25 @@ def test_attention_on_unusual_values_in_units_of_many_steps(kind, nq, group, fmt
     check_attention(_attend(qt, cache, ids, nt, fmt, f32=True), want, fmt, out_f32=True)
 
 
+def test_attention_fp16_lse_has_no_common_shift():
+    """What three e4m3 terms leave of a query is at most 2^-10 of 128..256 in the few dimensions below 2^-7 of the
+    largest one: 4 of 128 and 2^-10 / sqrt(3) each.  Times the codes' mean, 7.5, it shifts every logit of a head alike:
+    1e-3 * 7.5 * scale * (K scale, 0.35) / (128 / 3) = 6e-6, 1.5e-6 of an lse of 4.  With the mean taken back there
+    remain the codes' deviations (2.8, and 1 / sqrt(64) of it over a block's tokens): 0.1e-6, beside fp32 sums."""
+    fmt, nq = oq.F16, 64
+    rng = np.random.default_rng(50)
+    kt, _ = to16(rng.normal(size=(640, 2, 128)), fmt)
+    vt, _ = to16(rng.normal(size=(640, 2, 128)), fmt)
+    cache = qsa.alloc_qcache(2, 640)
+    qsa.qcache_append(kt, vt, cache, 0)
+    q, qd = to16(rng.normal(size=(nq, 16, 128)), fmt)
+    ids = rng.integers(0, 10, size=(nq, 1)).astype(np.int32)
+    nt = np.full(nq, 640)
+    want = oq.attention(qd, cache.cpu().numpy(), ids, nt, float(np.float32(128 ** -0.5)), fmt)[1]
+    got = _attend(q, cache, ids, nt, fmt)[1]
+    assert np.linalg.norm(got - want) <= 0.6e-6 * np.linalg.norm(want)
+
+
 def test_attention_other_scales():
     fmt = oq.BF16
     host = random_cache(15, 1, 9, fmt)
