@@ -450,7 +450,8 @@ __device__ __forceinline__ void prepare_queries(const QParams &p, int u_at, int 
         es[j] = finite ? e : 1024;
         const float s0 = pow2i(e >> 1), s1 = pow2i(e - (e >> 1));
         uint32_t terms[TERMS];
-        uint32_t h0 = finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u, h1 = finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u;
+        uint32_t h0 = finite ? to_h2(x[0] * s0 * s1, x[1] * s0 * s1) : 0u;
+        uint32_t h1 = finite ? to_h2(x[2] * s0 * s1, x[3] * s0 * s1) : 0u;
         split_query<TERMS>(h0, h1, terms);
         if (F16) lefts[j] = (h2_lo(h0) + h2_hi(h0)) + (h2_lo(h1) + h2_hi(h1));
 #pragma unroll
@@ -693,9 +694,10 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             const uint8_t *rec = sK + (s * kStep + q) * kKBytes;
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
+                constexpr int kPlane = kQBlockTok * 16;
                 const uint8_t *src = rec + (32 * sub + lane) * 16;
-                unpack(src, src + 1024, kColK + sub * 32, kColK + sub * 32 + 16);
-                unpack(src + 2048, src + 3072, kColK + sub * 32 + 8, kColK + sub * 32 + 24);
+                unpack(src, src + kPlane, kColK + sub * 32, kColK + sub * 32 + 16);
+                unpack(src + 2 * kPlane, src + 3 * kPlane, kColK + sub * 32 + 8, kColK + sub * 32 + 24);
             }
             const int left = un.ntok - un.sel[un.b0 + kStep * i + q] * kQBlockTok;   // tokens of this block below the context's end
 #pragma unroll
@@ -950,8 +952,8 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     }
 #pragma unroll
                     for (int y = 0; y < TERMS; ++y)
-                        *reinterpret_cast<uint2 *>(sP + (t % L::kPBufs) * L::kStepP + (sub0 + sub) * L::kTileP + y * L::kTermP + row * kG + h0) =
-                            make_uint2(word[0][y], word[1][y]);
+                        *reinterpret_cast<uint2 *>(sP + (t % L::kPBufs) * L::kStepP + (sub0 + sub) * L::kTileP +
+                                                   y * L::kTermP + row * kG + h0) = make_uint2(word[0][y], word[1][y]);
                 }
                 over = renew == 0 && (over || (high & 0x80808080u) != 0u);
                 fence_proxy_async();   // the weights are read by the tensor core
@@ -1048,13 +1050,16 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             // the weights takes most of its effect away.
 #pragma unroll
             for (int j = 0; j < kHO; j += 4) {
-                const float4 ig = *reinterpret_cast<const float4 *>(fin + ho + j), up = *reinterpret_cast<const float4 *>(fin + kG + ho + j);
+                const float4 ig = *reinterpret_cast<const float4 *>(fin + ho + j);
+                const float4 up = *reinterpret_cast<const float4 *>(fin + kG + ho + j);
                 const float4 add = *reinterpret_cast<const float4 *>(fin + 2 * kG + ho + j);
-                const float igs[4] = {ig.x, ig.y, ig.z, ig.w}, ups[4] = {up.x, up.y, up.z, up.w}, adds[4] = {add.x, add.y, add.z, add.w};
+                const float igs[4] = {ig.x, ig.y, ig.z, ig.w}, ups[4] = {up.x, up.y, up.z, up.w};
+                const float adds[4] = {add.x, add.y, add.z, add.w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int h = ho + j + x;
-                    const float y = fmaf(fmaf(__uint_as_float(o[1][j + x]), 0.0625f, __uint_as_float(o[0][j + x])) * ups[x], igs[x], adds[x]);
+                    const float sum = fmaf(__uint_as_float(o[1][j + x]), 0.0625f, __uint_as_float(o[0][j + x]));
+                    const float y = fmaf(sum * ups[x], igs[x], adds[x]);
                     if (split > 1) reinterpret_cast<float *>(sK)[h * kQDim + row] = y;
                     else if (h < group) put(h, y);
                 }
