@@ -365,9 +365,11 @@ qsa_status launch_evict_plan(const EvictPlanArgs &a, cudaStream_t s) {
         return launch_dependent("evict_plan_kernel launch", kern, a.n_rows, threads, 0, s, a.weights, a.stride, a.n_tokens,
                                 a.max_blocks, a.n_keep, a.n_first, a.n_last, a.keep, a.new_tokens, a.flags);
     };
-    // the fewest threads that hold a row: a step's barrier is cheaper among fewer warps (257 blocks 3.4 us with 256
-    // threads and 6.4 with 1,024, 4,000 blocks 6.2 with 512 and 8.0 with 1,024)
+    // Few keys per thread and few warps: a step's barrier is cheaper among fewer, its compares among more.  us with
+    // 256 / 512 / 1,024 threads: 257 blocks 3.6 / 4.1 / 5.3, 1,000 blocks 3.6 / 4.0 / 5.0, 2,048 blocks 4.4 / 4.0 / 5.0,
+    // 4,000 blocks 7.2 / 6.1 / 6.0, 8,125 blocks 13.5 / 9.9 / 8.6
     if (a.max_blocks <= 1024) return run(evict_plan_kernel<256, 4>, 256);
+    if (a.max_blocks <= 2048) return run(evict_plan_kernel<512, 4>, 512);
     if (a.max_blocks <= 4096) return run(evict_plan_kernel<512, 8>, 512);
     if (a.max_blocks <= 8192) return run(evict_plan_kernel<1024, 8>, 1024);
     if (a.max_blocks <= 16384) return run(evict_plan_kernel<1024, 16>, 1024);

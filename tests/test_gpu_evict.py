@@ -87,7 +87,9 @@ def test_weights_add_largest_sum():
 
 @pytest.mark.parametrize("n,keep,first,last", [(1, 1, 0, 1), (64, 16, 1, 1), (257, 128, 1, 8), (1024, 1023, 0, 1),
                                                (1025, 5, 4, 1), (8125, 4096, 4, 64), (8192, 1, 0, 1), (40_000, 20_001, 10, 300),
-                                               (300, 300, 5, 7), (5000, 4999, 2500, 2499)])
+                                               (300, 300, 5, 7), (5000, 4999, 2500, 2499),
+                                               (2048, 777, 2, 3), (2049, 2000, 2, 3), (4096, 4000, 1, 1), (4097, 17, 4, 4),
+                                               (8193, 8000, 1, 1), (16_384, 9_999, 3, 50), (16_385, 100, 0, 1)])
 @pytest.mark.parametrize("kind", ["random", "levels", "equal", "special"])
 def test_plan_matches_the_oracle(n, keep, first, last, kind):
     rng = np.random.default_rng(n + keep)
