@@ -493,14 +493,16 @@ qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int n
  *               QSA_FLAG_NBLOCKS_CLAMPED)
  *   keep        [n_rows][n_keep] int32 out: the kept ids in ascending order, -1 behind them
  *   new_tokens  [n_rows] int32 out: tokens left, n_tokens - 64 * (blocks evicted): the last
- *               block stays last, so a partial one stays valid
+ *               block stays last, so a partial one stays valid.  May be n_tokens itself (lengths
+ *               updated in place); otherwise keep and new_tokens overlap nothing
  *   ws          a workspace of at least 256 bytes (its flags word is used), or NULL
  *
  * Launch: as a programmatic dependent of the work before it, and a qsa_gather_blocks behind it
  * may line up while it runs (both wait before they read anything).
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, 2^20], max_blocks outside
  * [1, QSA_MAX_BLOCKS], weights_stride < max_blocks, n_keep outside [1, max_blocks],
- * n_first < 0, n_last < 1, n_first + n_last > n_keep; QSA_ERR_WORKSPACE as above.
+ * n_first < 0, n_last < 1, n_first + n_last > n_keep, an output that overlaps an input or the
+ * other output (but for new_tokens == n_tokens); QSA_ERR_WORKSPACE as above.
  */
 qsa_status qsa_evict_plan(const float *weights, int64_t weights_stride, const int32_t *n_tokens, int n_rows,
                           int max_blocks, int n_keep, int n_first, int n_last, int32_t *keep, int32_t *new_tokens,

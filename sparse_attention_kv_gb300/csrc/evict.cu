@@ -112,26 +112,30 @@ __device__ __forceinline__ uint32_t plan_key(float w, int b, int nb, int n_first
     return w == w ? score_key(w) : 0u;
 }
 
-// What every plan kernel starts with: the row's blocks; all of them kept: the answer at once.
+// What every plan kernel starts with: the row's tokens nt and its blocks; all of them kept: the answer at once.
+// new_tokens may be n_tokens: every thread reads the old length before a barrier, and thread 0 stores the new one
+// behind it (here, or at the kernel's end where fewer blocks are kept).
 template <int NT>
-__device__ __forceinline__ int plan_blocks(const int32_t *__restrict__ n_tokens, int row, int max_blocks, int n_keep,
-                                           int32_t *out, int32_t *new_tokens, uint32_t *flags) {
-    int nt = n_tokens[row];
+__device__ __forceinline__ int plan_blocks(const int32_t *n_tokens, int row, int max_blocks, int n_keep, int32_t *out,
+                                           int32_t *new_tokens, uint32_t *flags, int &nt) {
+    nt = n_tokens[row];
     if (nt < 0 || (long long)nt > 64ll * max_blocks) {
         if (threadIdx.x == 0 && flags) atomicOr(flags, QSA_FLAG_NBLOCKS_CLAMPED);
         nt = nt < 0 ? 0 : 64 * max_blocks;
     }
     const int nb = (int)(((long long)nt + 63) / 64);
-    if (threadIdx.x == 0) new_tokens[row] = nt - 64 * max(nb - n_keep, 0);
-    if (nb <= n_keep)
+    if (nb <= n_keep) {
+        __syncthreads();   // every thread takes this way: nb is the block's
+        if (threadIdx.x == 0) new_tokens[row] = nt;
         for (int i = threadIdx.x; i < n_keep; i += NT) out[i] = i < nb ? i : -1;
+    }
     return nb;
 }
 
 // E keys per thread, NT threads: rows of up to NT * E blocks.
 template <int NT, int E>
 __global__ void __launch_bounds__(NT) evict_plan_kernel(const float *__restrict__ weights, int64_t stride,
-                                                        const int32_t *__restrict__ n_tokens, int max_blocks,
+                                                        const int32_t *n_tokens, int max_blocks,
                                                         int n_keep, int n_first, int n_last, int32_t *keep,
                                                         int32_t *new_tokens, uint32_t *flags) {
     constexpr int NW = NT / 32;
@@ -142,7 +146,8 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const float *__restrict_
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float *w = weights + (size_t)row * stride;
     int32_t *out = keep + (size_t)row * n_keep;
-    const int nb = plan_blocks<NT>(n_tokens, row, max_blocks, n_keep, out, new_tokens, flags);
+    int nt;
+    const int nb = plan_blocks<NT>(n_tokens, row, max_blocks, n_keep, out, new_tokens, flags, nt);
     if (nb <= n_keep) return;
     uint32_t key[E];
 #pragma unroll
@@ -177,6 +182,7 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const float *__restrict_
         above += in && key[e] > T ? 1 : 0;
         equal += in && key[e] == T ? 1 : 0;
     }
+    if (tid == 0) new_tokens[row] = nt - 64 * (nb - n_keep);   // barriers lie behind: every thread has read n_tokens
     int total = 0;   // both counts in one scan: rows have at most 2^14 blocks
     const uint32_t before = (uint32_t)block_excl_scan<NT>(above | (equal << 16), sm, total);
     const int want = n_keep - (total & 0xFFFF);
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(NT) evict_plan_kernel(const float *__restrict_
 }
 
 __global__ void __launch_bounds__(kPlanThreads) evict_plan_long_kernel(const float *__restrict__ weights, int64_t stride,
-                                                                  const int32_t *__restrict__ n_tokens, int max_blocks,
+                                                                  const int32_t *n_tokens, int max_blocks,
                                                                   int n_keep, int n_first, int n_last, int32_t *keep,
                                                                   int32_t *new_tokens, uint32_t *flags) {
     __shared__ BlockScratch sm;
@@ -202,7 +208,8 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_long_kernel(const flo
     const int row = blockIdx.x, tid = threadIdx.x;
     const float *w = weights + (size_t)row * stride;
     int32_t *out = keep + (size_t)row * n_keep;
-    const int nb = plan_blocks<kPlanThreads>(n_tokens, row, max_blocks, n_keep, out, new_tokens, flags);
+    int nt;
+    const int nb = plan_blocks<kPlanThreads>(n_tokens, row, max_blocks, n_keep, out, new_tokens, flags, nt);
     if (nb <= n_keep) return;
     // the n_keep-th largest key, 8 bits a pass
     uint32_t prefix = 0u, mask = 0u;
@@ -227,6 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_long_kernel(const flo
         want = sm.misc[1];
         __syncthreads();
     }
+    if (tid == 0) new_tokens[row] = nt - 64 * (nb - n_keep);   // barriers lie behind: every thread has read n_tokens
     // ascending emit: keys above the threshold, and the first `want` equal to it
     int kept = 0, equal = 0;
     for (int b0 = 0; b0 < nb; b0 += kPlanThreads) {

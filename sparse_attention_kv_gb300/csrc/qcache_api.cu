@@ -44,6 +44,12 @@ qsa_status check_rows(const void *k, int64_t kt, int64_t kh, const void *v, int6
     return QSA_OK;
 }
 
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + bn && b0 < a0 + an;
+}
+
 uint32_t *flags_of(void *ws) { return static_cast<uint32_t *>(ws); }
 
 }  // namespace
@@ -207,6 +213,13 @@ qsa_status qsa_evict_plan(const float *weights, int64_t weights_stride, const in
                     n_last, n_keep);
     qsa_status st = check_flags_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
+    const size_t rows = (size_t)n_rows * sizeof(int32_t), keep_bytes = rows * (size_t)n_keep;
+    const size_t weight_bytes = ((size_t)(n_rows - 1) * (size_t)weights_stride + (size_t)max_blocks) * sizeof(float);
+    if (overlap(keep, keep_bytes, weights, weight_bytes) || overlap(keep, keep_bytes, n_tokens, rows) ||
+        overlap(keep, keep_bytes, new_tokens, rows) || overlap(new_tokens, rows, weights, weight_bytes))
+        return fail(QSA_ERR_INVALID_ARG, "keep and new_tokens must overlap neither each other nor an input");
+    if (new_tokens != n_tokens && overlap(new_tokens, rows, n_tokens, rows))
+        return fail(QSA_ERR_INVALID_ARG, "new_tokens must be n_tokens itself or not overlap it");
     EvictPlanArgs a{};
     a.weights = weights;
     a.stride = weights_stride;

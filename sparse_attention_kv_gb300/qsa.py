@@ -505,7 +505,7 @@ def evict_plan(weights: torch.Tensor, n_tokens: torch.Tensor, keep: torch.Tensor
                n_first: int = 1, n_last: int = 1, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """keep [n_rows, n_keep] int32: the blocks of each row that stay (the first n_first, the last
     n_last, and the others of largest weights [n_rows, max_blocks]), ascending, -1 behind them;
-    new_tokens [n_rows] int32: the tokens left of n_tokens [n_rows]."""
+    new_tokens [n_rows] int32: the tokens left of n_tokens [n_rows] (may be n_tokens itself)."""
     lib = load()
     if weights.dtype != torch.float32 or weights.dim() != 2 or weights.stride(1) != 1:
         raise ValueError("weights must be a 2-D fp32 tensor with unit inner stride")

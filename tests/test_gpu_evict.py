@@ -320,3 +320,27 @@ def test_captured_loop_with_eviction_shares_one_workspace():
         for n in x:
             assert torch.equal(s[n], x[n]), n
     assert qsa.read_flags(ws) == 0
+
+
+@pytest.mark.parametrize("n,keep", [(257, 128), (1024, 500), (2000, 1999), (4096, 100), (8125, 4096), (12_000, 5000), (17_000, 6000)])
+def test_plan_updates_the_lengths_in_place(n, keep):
+    """new_tokens is n_tokens, row after row, for every kernel of the plan: ids and lengths as out of place."""
+    rng = np.random.default_rng(n)
+    rows = 300
+    w = torch.rand(rows, n, device="cuda")
+    tokens = rng.integers(0, 64 * n + 1, size=rows).astype(np.int32)
+    tokens[::3] = 64 * keep + rng.integers(-64, 129, size=len(tokens[::3]))   # just all of them kept, or just not
+    tokens = np.minimum(tokens, 64 * n)
+    nt = _cuda(tokens)
+    keeps = [torch.empty(rows, keep, dtype=torch.int32, device="cuda") for _ in range(2)]
+    left = torch.empty(rows, dtype=torch.int32, device="cuda")
+    qsa.evict_plan(w, nt, keeps[0], left, 3, 10)
+    for _ in range(5):
+        there = nt.clone()
+        keeps[1].fill_(-7)
+        qsa.evict_plan(w, there, keeps[1], there, 3, 10)
+        assert torch.equal(there, left) and torch.equal(keeps[0], keeps[1])
+    for r in range(0, rows, 37):
+        kept, want = oq.evict_plan(w[r].cpu().numpy(), int(tokens[r]), keep, 3, 10)
+        np.testing.assert_array_equal(keeps[1][r].cpu().numpy(), kept)
+        assert there[r].item() == want

@@ -254,3 +254,17 @@ def test_binding_checks_shapes_before_devices(lib, monkeypatch):
 def test_alloc_rejects_bad_sizes(lib):
     with pytest.raises(ValueError):
         qsa.alloc_qcache(1, 100)
+
+
+@pytest.mark.parametrize("case", [
+    dict(new=FAKE + 4), dict(new=FAKE - 4),                # overlaps n_tokens without being it
+    dict(keep=FAKE + 4), dict(keep=FAKE - 4 * 99),         # overlaps n_tokens
+    dict(new=FAR + 4 * 99), dict(keep=FAR),                # overlaps the weights' second row
+    dict(keep=FAR, w=3 * FAR, new=FAR + 4 * 99), dict(keep=FAR + 4 * 199),
+])
+def test_plan_rejects_overlapping_arrays(lib, case):
+    a = dict(w=FAR, nt=FAKE, keep=2 * FAR, new=FAKE)
+    a.update(case)
+    st = lib.qsa_evict_plan(a["w"], 100, a["nt"], 2, 100, 50, 1, 2, a["keep"], a["new"], None, 0, None)
+    assert st == qsa.ERR_INVALID_ARG
+    assert "overlap" in lib.qsa_last_error().decode()
