@@ -104,7 +104,7 @@ struct QUnit {
 
 struct QCtrl {
     uint64_t k_full[2], k_free[2], v_full[kVStages], v_free[kVStages], sbar[2], obar;
-    uint64_t ids_ready[2], ready[2], done[2];
+    uint64_t ids_ready[2], ready[2], done[2], drained;
     uint32_t tmem_base;
     int abort;
     QUnit unit[2];
@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             mbar_init(&ct.done[i], 15);   // all warps but the preparing one
         }
         mbar_init(&ct.obar, 1);
+        mbar_init(&ct.drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -531,6 +532,8 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     __syncwarp();
 
     // Every role walks the same units (n-th unit u, buffer n & 1) and the same steps (t-th step, stage t & 1).
+    int stage = 0;                        // a copying warp's next stage, and how often it has filled the last one
+    uint32_t lap = 0;
     if (warp >= kControl) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kPrepare) {
         for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
@@ -550,11 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     } else if (warp >= kFetch) {
         // copies, a lane per block: the first warp K and the pairs, the second V
         const bool is_k = warp == kFetch;
-        const int stages = is_k ? L::kKStages : kVStages;
+        static_assert(L::kKStages == 2 && kVStages == 2, "two stages each");
         const uint32_t bytes = is_k ? kKBytes : kVBytes;
         uint64_t *full = is_k ? ct.k_full : ct.v_full, *vacant = is_k ? ct.k_free : ct.v_free;
-        int s = 0;
-        uint32_t lap = 0;
         for (int u = u0, n = 0; u < p.units; u += ustep, ++n) {
             wait_all<64, true>(&ct.ids_ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             const QUnit &un = ct.unit[n & 1];
@@ -563,25 +564,20 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
             for (int i = 0; i < steps; ++i) {
                 const int m = min(kStep, nloc - kStep * i);
                 const uint8_t *src = head + (size_t)un.sel[un.b0 + kStep * i + min(lane, m - 1)] * kQRec;
-                if (lap > 0) wait_all<32>(&vacant[s], (lap - 1u) & 1u, abort_flag);
+                if (lap > 0) wait_all<32>(&vacant[stage], (lap - 1u) & 1u, abort_flag);
                 if (__any_sync(kFull, *abort_flag != 0)) break;   // the stage may still be in use
-                if (lane == 0) mbar_expect_tx(&full[s], (uint32_t)m * bytes);
+                if (lane == 0) mbar_expect_tx(&full[stage], (uint32_t)m * bytes);
                 __syncwarp();
-                if (lane < m) bulk_load((is_k ? sK : sV) + (s * kStep + lane) * bytes, src, bytes, &full[s]);
+                if (lane < m) bulk_load((is_k ? sK : sV) + (stage * kStep + lane) * bytes, src, bytes, &full[stage]);
                 __syncwarp();
-                if (++s == stages) {
-                    s = 0;
+                if (++stage == 2) {
+                    stage = 0;
                     ++lap;
                 }
             }
             if (lane == 0) mbar_arrive(&ct.done[n & 1]);
             __syncwarp();
         }
-        if (*abort_flag)   // copies in flight land before the memory is given back
-            for (int i = 0; i < stages; ++i) {
-                if (lap > 0 || i < s) mbar_drain(&full[i], (i < s ? lap : lap - 1u) & 1u);
-            }
-        __syncwarp();
     } else if (warp == kControl) {
         tmem_alloc(&ct.tmem_base, kCols);
         tmem_relinquish();
@@ -600,7 +596,6 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     const uint32_t tmem = ct.tmem_base;
     if (warp == kControl) {
         const uint64_t dq = sdesc(smem_u32(sQ)), dp = sdesc_mn(smem_u32(sP), 8 * kG, L::kTermP);
-        int scored = 0, summed = 0;
         auto scores = [&](int n, int t) {   // step t, of unit n
             wait_all<0, true>(&ct.ready[n & 1], (uint32_t)(n >> 1) & 1u, abort_flag);
             k_ready_wait();
@@ -617,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 mma_commit(&ct.sbar[t & 1]);
             }
             __syncwarp();
-            ++scored;
         };
         bool primed = false;
         for (int u = u0, n = 0, t = 0; u < p.units; u += ustep, ++n) {
@@ -656,17 +650,10 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                     mma_commit(&ct.obar);
                 }
                 __syncwarp();
-                ++summed;
                 ++t;
             }
             if (lane == 0) mbar_arrive(&ct.done[n & 1]);
             __syncwarp();
-        }
-        if (ct.abort) {   // a wait gave up: let what is in flight land before the memory is freed
-            for (int i = max(0, scored - 2); i < scored; ++i) mbar_drain(&ct.sbar[i & 1], (uint32_t)(i >> 1) & 1u);
-            if (summed > 0) mbar_drain(&ct.obar, (uint32_t)(summed - 1) & 1u);
-            __syncwarp();
-            if (lane == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_WAIT_TIMEOUT);
         }
     } else if (warp >= kUnpack) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -1091,6 +1078,19 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
     }
     }
     __syncthreads();
+    if (ct.abort) {   // a wait of some role gave up: what is in flight lands before any of the memory is used again
+        if (warp >= kFetch) {      // each stage's last fill
+            uint64_t *full = warp == kFetch ? ct.k_full : ct.v_full;
+            for (int i = 0; i < 2; ++i)
+                if (lap > 0 || i < stage) mbar_drain(&full[i], (i < stage ? lap : lap - 1u) & 1u);
+        } else if (warp == kControl) {   // one more commit completes behind every product issued
+            if (elect_one()) mma_commit(&ct.drained);
+            __syncwarp();
+            mbar_drain(&ct.drained, 0);
+        }
+        if (tid == 0 && a.flags) atomicOr(a.flags, QSA_FLAG_WAIT_TIMEOUT);
+        __syncthreads();
+    }
     if (warp == kControl) {
         __syncwarp();
         tc_fence_after();
