@@ -299,11 +299,13 @@ __device__ __forceinline__ float warp_sum8(const float (&x)[kH], int lane) {
 }
 
 
-// Every thread of the warp waits, a bounded number of tries (each suspends the thread for some
-// hundred cycles; the bound comes to seconds).  After one has given up, waits for copies and
-// products return at once, and the CTA runs through its remaining steps without their results.
-// Waits for what another warp does (HANDSHAKE) keep their patience: every warp still makes its steps, and
-// all of them read the same number of steps, so that the barriers meet.
+// Every thread of the warp waits, a bounded number of tries: one that fails suspends the thread for 3.9 us (measured on
+// a barrier that nobody arrives at, with and without the sleeps), so 2^18 come to a second.  After one wait has given
+// up, waits for copies and products return at once, and the CTA runs through its remaining steps without their results.
+// Waits for what another warp does (HANDSHAKE) go on and have four times as many, so that one that began before the wait
+// that gave up does not run out while the other warp still waits: every warp makes its steps, and all of them read
+// the same number of steps, so that the barriers meet.  (A look at the clock in the loop, as the other kernels' waits
+// take, made the deep prompt's call 5% slower: the waits' code stands in the loop of every role.)
 template <int SLEEP = 0, bool HANDSHAKE = false>
 __device__ __forceinline__ void wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     uint32_t ok;
@@ -313,7 +315,7 @@ __device__ __forceinline__ void wait_all(uint64_t *bar, uint32_t parity, volatil
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     if (__all_sync(kFull, ok != 0)) return;   // the warp stays converged
-    const uint32_t most = !HANDSHAKE && *abort_flag ? 1u : 1u << 23;
+    const uint32_t most = HANDSHAKE ? 1u << 20 : *abort_flag ? 1u : 1u << 18;
     if constexpr (SLEEP == 0)
         asm volatile(
             "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
