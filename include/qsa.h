@@ -391,7 +391,8 @@ size_t qsa_qcache_bytes(int n_kv_heads, int capacity);
  *               captured decode step appends wherever it says).  Tokens whose position lies
  *               outside [0, capacity) are dropped and set QSA_FLAG_NBLOCKS_CLAMPED
  *   cache       see above; other positions, those of a shared byte among them, keep
- *               their values
+ *               their values, whatever else writes them meanwhile: appends to different
+ *               positions may run at the same time, also in one block
  *   ws          a workspace of at least 256 bytes (its flags word is used), or NULL
  *
  * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides not multiples of 8,

@@ -11,9 +11,9 @@
 // four threads' accesses are neighbours, and units 8 apart are the low and the high nibbles
 // of the same 8 bytes of K, which go from registers to the cache.  V is stored
 // dimension-major: its codes pass through shared memory as bytes, are transposed four by four
-// with byte permutes and exchanged among four lanes, and leave as whole 16-byte rows.  A CTA
-// owns its whole block, so a partial block's other tokens (the other nibbles of shared bytes)
-// are merged without atomics.
+// with byte permutes and exchanged among four lanes, and leave as whole 16-byte rows.  In a
+// partial block only the call's own nibbles change, one atomic exclusive-or per word, so that two
+// appends may fill one block at the same time.
 //
 // Measured, 131,072 tokens x 4 KV heads, bf16: the reader moves its 336 MB in 51 us (6.65 TB/s, the
 // copy rate); the writer's 336 MB take 78 us: it issues 0.70 instructions a cycle and scheduler (15
@@ -218,8 +218,9 @@ __global__ void __launch_bounds__(kNT, 4) append_kernel(const RowPtr k, const Ro
     if ((long long)b * kQBlockTok >= first + n) return;
     const long long at = (long long)b * kQBlockTok - first;       // the row that the block's first token takes
     const long long i = at + tok;
-    const bool in = i >= 0 && i < n;
-    const bool whole = at >= 0 && at + kQBlockTok <= n;
+    // the block's tokens t0 .. t1 - 1 are the call's
+    const int t0 = at < 0 ? (int)min(-at, (long long)kQBlockTok) : 0, t1 = (int)min((long long)n - at, (long long)kQBlockTok);
+    const bool in = tok >= t0 && tok < t1;
     uint8_t *rec = cache + qrec_offset(g, nb_cap, b);
     uint32_t xk[16], xv[16], packed[4];
     const uint8_t *krow = k.p + i * k.token_bytes + g * k.head_bytes;
@@ -260,22 +261,24 @@ __global__ void __launch_bounds__(kNT, 4) append_kernel(const RowPtr k, const Ro
     transpose_bytes(w);
     transpose_lanes(w, q);
     uint4 *dst = reinterpret_cast<uint4 *>(rec + kQOffV + p * 2048 + (4 * d4 + q) * 16);
-    if (!whole) {   // the other tokens' nibbles stay
-        const uint4 old = *dst;
-        const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            uint32_t keep = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const long long i0 = at + 16 * p + 4 * x + j;
-                if (i0 < 0 || i0 >= n) keep |= 0x0Fu << (8 * j);
-                if (i0 + 32 < 0 || i0 + 32 >= n) keep |= 0xF0u << (8 * j);
-            }
-            w[x] = (w[x] & ~keep) | (o[x] & keep);
-        }
+    if (t1 - t0 == kQBlockTok) {
+        *dst = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
     }
-    *dst = make_uint4(w[0], w[1], w[2], w[3]);
+    // the other tokens' nibbles stay, also while another append writes them: what changes of this call's own nibbles is
+    // flipped (nobody else writes those), a word at a time
+    uint32_t *word = reinterpret_cast<uint32_t *>(dst);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        uint32_t mine = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = 16 * p + 4 * x + j;
+            if (t >= t0 && t < t1) mine |= 0x0Fu << (8 * j);
+            if (t + 32 >= t0 && t + 32 < t1) mine |= 0xF0u << (8 * j);
+        }
+        if (mine) atomicXor(word + x, (w[x] ^ __ldcg(word + x)) & mine);
+    }
 }
 
 // 32 codes of a token (units c and c + 4 in lo, c + 8 and c + 12 in hi) to 16-bit values: scale * code + min

@@ -512,3 +512,24 @@ def test_two_streams_at_once():
         for got in o:
             for a, b in zip(got, want):
                 np.testing.assert_array_equal(a.double().cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_appends_on_two_streams_share_a_block(fmt):
+    """Two streams fill one block's tokens in turn, token by token (tokens r and r + 32 share V's bytes): every
+    position holds its own row, whatever the streams' order."""
+    kv, n = 3, 64
+    k, _ = to16(_rows(70, n, kv), fmt)
+    v, _ = to16(_rows(71, n, kv), fmt)
+    want = qsa.alloc_qcache(kv, 64)
+    qsa.qcache_append(k, v, want, 0)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for split in (lambda t: t >= 32, lambda t: t % 2, lambda t: (t // 4) % 2):
+        cache = torch.randint(0, 256, tuple(want.shape), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for t in range(32):
+            for u in (t, t + 32):
+                with torch.cuda.stream(streams[int(split(u))]):
+                    qsa.qcache_append(k[u:u + 1], v[u:u + 1], cache, u)
+        torch.cuda.synchronize()
+        assert torch.equal(cache, want)
