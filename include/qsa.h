@@ -407,7 +407,8 @@ qsa_status qsa_qcache_append(const void *k, int64_t k_token_stride, int64_t k_he
 
 /*
  * The rows of positions first .. first + n - 1 back in 16 bits (scale * code + min rounded once
- * to `dt`), into k and v addressed as for qsa_qcache_append.
+ * to `dt`; what that puts past dt's largest finite value, by scale / 2 at most, reads as that
+ * value), into k and v addressed as for qsa_qcache_append.
  * Errors: as qsa_qcache_append's.
  */
 qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int head_dim, int capacity, int first,
@@ -423,7 +424,8 @@ qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int 
  *             `dt` (strides in elements, multiples of 8), 16-byte aligned
  *   cache     of the same dt
  *   ids, k, n_tokens, capacity, scale, ws   as for qsa_select_attention
- *   out       [nq][n_heads][128] of dtype out_dt: QSA_F32, or dt
+ *   out       [nq][n_heads][128] of dtype out_dt: QSA_F32, or dt (what passes dt's range becomes
+ *             its largest finite value)
  *   lse       [nq][n_heads] fp32 out, or NULL
  *   weights   [nq][n_kv_heads][k] fp32 out, or NULL: the softmax weight that the group's heads
  *             together give to slot j's tokens (a slot with id -1, an id outside the

@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kNT, 4) append_kernel(const RowPtr k, const Ro
 }
 
 // 32 codes of a token (units c and c + 4 in lo, c + 8 and c + 12 in hi) to 16-bit values: scale * code + min
-// rounded once.
+// rounded once.  The scale is rounded up, so the top level may pass the format's largest value, by half a step at
+// most where a code stands for a finite value: then that value is what is read.
 template <bool F16>
 __device__ __forceinline__ void store_row(uint8_t *row, int c, const uint32_t (&lo)[4], const uint32_t (&hi)[4],
                                           uint32_t pair) {
@@ -296,7 +297,7 @@ __device__ __forceinline__ void store_row(uint8_t *row, int c, const uint32_t (&
         for (int j = 0; j < 4; ++j) {   // a code's byte under the format's high byte is the base + code
             const uint32_t w = (i < 2 ? lo : hi)[2 * (i & 1) + (j >> 1)];
             const uint32_t code2 = Fmt::fma2(__byte_perm(w, Fmt::kCodeHigh, j & 1 ? 0x4342 : 0x4140), Fmt::kOne2, Fmt::kMinusBase2);
-            o[j] = Fmt::fma2(scale2, code2, min2);
+            o[j] = Fmt::min2(Fmt::fma2(scale2, code2, min2), Fmt::kMax2);   // min is finite: nothing passes below
         }
         r[c + 4 * i] = make_uint4(o[0], o[1], o[2], o[3]);
     }

@@ -63,6 +63,13 @@ struct QFmt<false> {
     static __device__ __forceinline__ uint32_t bits(float x) {
         return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
     }
+    // what passes the format's range becomes its largest value; a NaN stays one
+    static __device__ __forceinline__ uint32_t bits_sat(float x) {
+        uint32_t r;
+        asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.bf16.f32 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(r) : "f"(x));
+        return r;
+    }
+    static constexpr uint32_t kMax2 = 0x7F7F7F7Fu;   // a pair of the largest finite value
     static __device__ __forceinline__ uint32_t bits_up(float x) {
         return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_ru(x));
     }
@@ -95,6 +102,12 @@ struct QFmt<true> {
         return __half2float(__ushort_as_half((unsigned short)(w >> 16)));
     }
     static __device__ __forceinline__ uint32_t bits(float x) { return (uint32_t)__half_as_ushort(__float2half_rn(x)); }
+    static __device__ __forceinline__ uint32_t bits_sat(float x) {
+        uint32_t r;
+        asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.f16.f32 h, %1;\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(r) : "f"(x));
+        return r;
+    }
+    static constexpr uint32_t kMax2 = 0x7BFF7BFFu;
     static __device__ __forceinline__ uint32_t bits_up(float x) {
         return (uint32_t)__half_as_ushort(__float2half_ru(x));
     }

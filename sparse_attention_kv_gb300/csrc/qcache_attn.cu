@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
         auto put = [&](int h, float x) {   // a warp's stores for one head are 32 neighbours
             const size_t at = (head0 + h) * kQDim + row;
             if (a.out_dt == QSA_F32) static_cast<float *>(a.out)[at] = x;
-            else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits(x);
+            else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits_sat(x);   // values may pass the range, see store_row()
         };
         if (steps > 0) {
             float x[kH];
@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constan
                 const size_t at = (head0 + h) * kQDim + d;
                 const float y = Lsum != 0.0f ? acc / Lsum : 0.0f;
                 if (a.out_dt == QSA_F32) static_cast<float *>(a.out)[at] = y;
-                else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits(y);
+                else static_cast<uint16_t *>(a.out)[at] = (uint16_t)QFmt<F16>::bits_sat(y);
                 if (a.lse && d == 0) a.lse[head0 + h] = Lsum != 0.0f ? (M + log2f(Lsum)) * 0.6931471805599453f : -INFINITY;
             }
         }

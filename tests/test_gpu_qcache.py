@@ -533,3 +533,51 @@ def test_appends_on_two_streams_share_a_block(fmt):
                     qsa.qcache_append(k[u:u + 1], v[u:u + 1], cache, u)
         torch.cuda.synchronize()
         assert torch.equal(cache, want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_near_the_largest_value_read_as_finite(fmt):
+    """The scale is rounded up, so the top level may lie past the format: it reads as the largest finite value, and every
+    value within scale / 2 and a rounding of its own."""
+    rng = np.random.default_rng(72)
+    big = float(torch.finfo(DT[fmt]).max)
+    rows = [np.where(rng.random(128) < 0.5, big, 0.0), rng.uniform(0, 1, 128) * big, np.where(np.arange(128) == 3, big, -big / 512),
+            np.where(rng.random(128) < 0.5, -big, 0.0), np.full(128, big), np.full(128, -big),
+            np.where(np.arange(128) % 2, np.inf, big)]
+    rows[1][5] = big
+    if fmt == oq.F16:   # a range that fp32 holds
+        rows += [np.where(rng.random(128) < 0.5, -big, big), rng.uniform(-1, 1, 128) * big]
+        rows[-1][:2] = -big, big
+    k, kd = to16(np.stack(rows)[:, None], fmt)
+    cache = qsa.alloc_qcache(1, 64)
+    qsa.qcache_append(k, k.flip(0), cache, 0)
+    ko, vo = torch.empty_like(k), torch.empty_like(k)
+    qsa.qcache_load(cache, ko, vo, 0)
+    with np.errstate(invalid="ignore"):
+        _, scale, _ = oq.quantise(kd, fmt)
+        want = np.minimum(oq.rows(cache.cpu().numpy(), 0, len(rows), fmt)[0], big)   # NaN stays NaN
+    assert np.isnan(want[6]).all() and torch.isnan(ko[6]).all() and torch.isnan(vo[-7]).all()
+    ok = np.arange(len(rows)) != 6
+    got = ko.double().cpu().numpy()
+    np.testing.assert_array_equal(got[ok], torch.from_numpy(want[ok]).to(DT[fmt]).double().numpy())
+    assert np.isfinite(got[ok]).all()
+    half = float(torch.finfo(DT[fmt]).eps) / 2
+    assert (np.abs(got - kd)[ok] <= (scale[..., None] / 2 * (1 + 1e-12) + half * np.abs(got))[ok]).all()
+    assert torch.equal(vo.flip(0)[ok.tolist()], ko[ok.tolist()])
+
+
+@pytest.mark.parametrize("nq", [2, 100])
+def test_attention_over_the_largest_values_is_finite(nq):
+    """fp16 rows of +-65504: their top level is 65536, which the fp32 output shows and the fp16 output holds at 65504."""
+    fmt = oq.F16
+    sign = np.where(np.arange(128) % 2, 1.0, -1.0)
+    kt, _ = to16(np.random.default_rng(73).normal(size=(300, 1, 128)), fmt)
+    vt, _ = to16(np.broadcast_to(65504.0 * sign, (300, 1, 128)), fmt)
+    cache = qsa.alloc_qcache(1, 320)
+    qsa.qcache_append(kt, vt, cache, 0)
+    q, _ = to16(np.random.default_rng(74).normal(size=(nq, 16, 128)), fmt)
+    ids = np.repeat(np.arange(5, dtype=np.int32)[None], nq, 0)
+    out = _attend(q, cache, ids, np.full(nq, 300), fmt)[0]
+    assert (out[..., 1::2] == 65504).all() and (np.abs(out[..., ::2] + 65504) <= 65536 * 2.0 ** -9).all()
+    wide = _attend(q, cache, ids, np.full(nq, 300), fmt, f32=True)[0]
+    assert (np.abs(wide[..., 1::2] - 65536) <= 65536 * 2.0 ** -9).all()
