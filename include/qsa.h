@@ -470,7 +470,8 @@ qsa_status qsa_select_attention_qcache(const void *qa, int64_t q_stride, int64_t
  *             and set QSA_FLAG_BAD_WEIGHT)
  *   ids       [nq][k] int32; -1 is skipped, other ids outside [0, max_blocks) too (with
  *             QSA_FLAG_BAD_ID); the same id may appear any number of times
- *   decay     host float, finite and >= 0
+ *   decay     host double, finite and >= 0; the product with prev and the sum are formed in 64 bits
+ *             and rounded to fp32 once
  *   prev      [max_blocks] fp32, or NULL (zeros); may be acc itself
  *   acc       [max_blocks] fp32 out
  *   ws        a workspace of at least 256 bytes (its flags word is used), or NULL
@@ -481,7 +482,7 @@ qsa_status qsa_select_attention_qcache(const void *qa, int64_t q_stride, int64_t
  * 2^22, max_blocks outside [1, QSA_MAX_BLOCKS], a decay not finite or < 0, a prev that
  * overlaps acc without being it; QSA_ERR_WORKSPACE as above.
  */
-qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, float decay,
+qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, double decay,
                                  const float *prev, float *acc, int max_blocks, void *ws, size_t ws_bytes,
                                  qsa_stream stream);
 

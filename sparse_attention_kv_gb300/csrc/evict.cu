@@ -46,14 +46,14 @@ __device__ __forceinline__ unsigned long long entry_sum(const float *__restrict_
     return add;
 }
 // One block's result: the sum in two halves, each exact in fp64 once scaled; fp32 once at the end.
-__device__ __forceinline__ float block_sum(unsigned long long sum, float decay, const float *prev, int b) {
+__device__ __forceinline__ float block_sum(unsigned long long sum, double decay, const float *prev, int b) {
     const double s = (double)(uint32_t)(sum >> 32) * 0.0625 + (double)(uint32_t)sum * (1.0 / 68719476736.0);
-    return (float)((prev ? (double)decay * (double)prev[b] : 0.0) + s);
+    return (float)((prev ? decay * (double)prev[b] : 0.0) + s);
 }
 
 __global__ void __launch_bounds__(kAddThreads) weights_scan_kernel(const float *__restrict__ weights,
                                                                    const int32_t *__restrict__ ids, int n_entries,
-                                                                   int n_kv, int k, float decay, const float *prev,
+                                                                   int n_kv, int k, double decay, const float *prev,
                                                                    float *acc, int max_blocks, uint32_t *flags) {
     __shared__ unsigned long long sum[kAddBlocks];
     const int b0 = blockIdx.x * kAddBlocks;
@@ -78,7 +78,7 @@ constexpr int kAddClusterBlocks = 28672;   // 8 bytes each in a CTA's shared mem
 
 __global__ void __cluster_dims__(kAddCluster, 1, 1) __launch_bounds__(kAddClusterThreads)
     weights_cluster_kernel(const float *__restrict__ weights, const int32_t *__restrict__ ids, int n_entries, int n_kv,
-                           int k, float decay, const float *prev, float *acc, int max_blocks, int per_cta,
+                           int k, double decay, const float *prev, float *acc, int max_blocks, int per_cta,
                            uint32_t *flags) {
     extern __shared__ unsigned long long sums[];   // this CTA's blocks: blockIdx.x * per_cta ..
     for (int i = threadIdx.x; i < per_cta; i += kAddClusterThreads) sums[i] = 0ull;

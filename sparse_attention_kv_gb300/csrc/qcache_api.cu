@@ -1,4 +1,6 @@
 // qcache_api.cu -- the C ABI of the 4-bit KV cache and of the eviction: argument checks.
+#include <cfloat>
+
 #include "qsa_internal.h"
 
 namespace qsa {
@@ -163,7 +165,7 @@ qsa_status qsa_select_attention_qcache(const void *qa, int64_t q_stride, int64_t
     return launch_qcache_attention(a, static_cast<cudaStream_t>(stream));
 }
 
-qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, float decay,
+qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, double decay,
                                  const float *prev, float *acc, int max_blocks, void *ws, size_t ws_bytes,
                                  qsa_stream stream) {
     if (!weights || !ids || !acc) return fail(QSA_ERR_INVALID_ARG, "NULL weights, ids or acc");
@@ -174,7 +176,7 @@ qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int n
         return fail(QSA_ERR_INVALID_ARG, "nq * n_kv_heads * k too large (at most %d)", 1 << 22);
     if (max_blocks < 1 || max_blocks > QSA_MAX_BLOCKS)
         return fail(QSA_ERR_INVALID_ARG, "max_blocks must be in [1, %d] (got %d)", QSA_MAX_BLOCKS, max_blocks);
-    if (!(decay >= 0.0f) || !(decay <= 3.4e38f)) return fail(QSA_ERR_INVALID_ARG, "decay must be finite and >= 0");
+    if (!(decay >= 0.0) || !(decay <= DBL_MAX)) return fail(QSA_ERR_INVALID_ARG, "decay must be finite and >= 0");
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(acc), p0 = reinterpret_cast<uintptr_t>(prev);
     const size_t acc_bytes = (size_t)max_blocks * sizeof(float);
     if (prev && prev != acc && a0 < p0 + acc_bytes && p0 < a0 + acc_bytes)

@@ -195,7 +195,7 @@ struct WeightsAddArgs {
     int nq;
     int n_kv_heads;
     int k;
-    float decay;
+    double decay;
     const float *prev;   // may be null (zeros) or acc
     float *acc;
     int max_blocks;

@@ -98,7 +98,7 @@ def load() -> ctypes.CDLL:
     lib.qsa_select_attention.restype = i32
     lib.qsa_vcache_transpose.argtypes = [vp, vp, i32, i32, i32, i32, vp]
     lib.qsa_vcache_transpose.restype = i32
-    f32 = ctypes.c_float
+    f32, f64 = ctypes.c_float, ctypes.c_double
     lib.qsa_qcache_bytes.argtypes = [i32, i32]
     lib.qsa_qcache_bytes.restype = sz
     lib.qsa_qcache_append.argtypes = [vp, i64, i64, vp, i64, i64, i32, i32, i32, i32, i32, vp, vp, i32, vp, sz, vp]
@@ -108,7 +108,7 @@ def load() -> ctypes.CDLL:
     lib.qsa_select_attention_qcache.argtypes = [vp, i64, i64, i32, vp, vp, i32, vp, i32, i32, i32, i32, i32, f32, vp,
                                                 i32, vp, vp, vp, sz, vp]
     lib.qsa_select_attention_qcache.restype = i32
-    lib.qsa_block_weights_add.argtypes = [vp, vp, i32, i32, i32, f32, vp, vp, i32, vp, sz, vp]
+    lib.qsa_block_weights_add.argtypes = [vp, vp, i32, i32, i32, f64, vp, vp, i32, vp, sz, vp]
     lib.qsa_block_weights_add.restype = i32
     lib.qsa_evict_plan.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp]
     lib.qsa_evict_plan.restype = i32

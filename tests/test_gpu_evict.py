@@ -344,3 +344,24 @@ def test_plan_updates_the_lengths_in_place(n, keep):
         kept, want = oq.evict_plan(w[r].cpu().numpy(), int(tokens[r]), keep, 3, 10)
         np.testing.assert_array_equal(keeps[1][r].cpu().numpy(), kept)
         assert there[r].item() == want
+
+
+@pytest.mark.parametrize("nq", [3, 100])
+@pytest.mark.parametrize("decay", [0.98, 0.9, 1 / 3])
+def test_weights_add_keeps_the_decay_in_64_bits(decay, nq):
+    """A decay that fp32 does not hold: decay * prev + sum in 64 bits, rounded once (the weights are whole numbers, so
+    their sum is exact, and numpy forms the same two roundings)."""
+    rng = np.random.default_rng(int(decay * 100))
+    n = 5000
+    prev = (rng.random(n) * 50).astype(np.float32)
+    ids = rng.integers(0, n, size=(nq, 16)).astype(np.int32)
+    w = rng.integers(0, 17, size=(nq, 2, 16)).astype(np.float32)
+    add = np.zeros(n)
+    np.add.at(add, ids.reshape(-1), w.sum(1, dtype=np.float64).reshape(-1))
+    acc = torch.empty(n, device="cuda")
+    qsa.block_weights_add(_cuda(w), _cuda(ids), acc, prev=_cuda(prev), decay=decay)
+    double = decay * prev.astype(np.float64) + add
+    got = acc.cpu().numpy()
+    # one rounding to fp32 of a double that is at most one step of 2^-53 off (a product and a sum, or both in one)
+    assert (np.abs(got - double) <= np.abs(double) * (2.0 ** -24 + 2.0 ** -52)).all()
+    assert (got == double.astype(np.float32)).mean() > 0.999

@@ -268,3 +268,13 @@ def test_plan_rejects_overlapping_arrays(lib, case):
     st = lib.qsa_evict_plan(a["w"], 100, a["nt"], 2, 100, 50, 1, 2, a["keep"], a["new"], None, 0, None)
     assert st == qsa.ERR_INVALID_ARG
     assert "overlap" in lib.qsa_last_error().decode()
+
+
+def test_decay_crosses_the_boundary_in_64_bits(lib):
+    import ctypes
+    import os
+    import re
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "qsa.h")).read()
+    declared = re.search(r"qsa_block_weights_add\((.*?)\);", header, flags=re.S).group(1).split(",")
+    at = next(i for i, x in enumerate(declared) if x.split()[-1] == "decay")
+    assert declared[at].split()[0] == "double" and lib.qsa_block_weights_add.argtypes[at] is ctypes.c_double
