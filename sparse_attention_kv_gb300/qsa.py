@@ -389,7 +389,12 @@ def _qrows(k: torch.Tensor, v: torch.Tensor, kv: int) -> tuple[int, int, int, in
     ks, vs = k.stride(), v.stride()
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("k and v must have unit inner stride")
-    return shape[0], ks[0], ks[1], vs[0], vs[1]
+    return shape[0], *_used(shape, ks), *_used(shape, vs)
+
+
+def _used(shape: tuple, strides: tuple) -> tuple[int, int]:
+    """The first two strides; one along a dimension of a single entry is never used and may be anything in torch."""
+    return strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0
 
 
 def _ws_args(ws: torch.Tensor | None) -> tuple[int | None, int]:
@@ -458,6 +463,7 @@ def select_attention_qcache(qa: torch.Tensor, cache: torch.Tensor, ids: torch.Te
     if len(shape) != 3 or strides[2] != 1:
         raise ValueError("qa must be [nq, n_heads, 128] with unit inner stride")
     nq, H, D = shape
+    qs, hs = _used(shape, strides)
     if ids.dtype != torch.int32 or len(picks) != 2 or picks[0] != nq or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 tensor [nq, k]")
     if n_tokens.dtype != torch.int32 or n_tokens.numel() != nq or not n_tokens.is_contiguous():
@@ -475,7 +481,7 @@ def select_attention_qcache(qa: torch.Tensor, cache: torch.Tensor, ids: torch.Te
                     weights=weights, ws=ws)
     wp, wn = _ws_args(ws)
     _check("qsa_select_attention_qcache", lib.qsa_select_attention_qcache(
-        qa.data_ptr(), strides[0], strides[1], dt, cache.data_ptr(), ids.data_ptr(), k, n_tokens.data_ptr(), nq, H, kv, D,
+        qa.data_ptr(), qs, hs, dt, cache.data_ptr(), ids.data_ptr(), k, n_tokens.data_ptr(), nq, H, kv, D,
         cap, D ** -0.5 if scale is None else float(scale), out.data_ptr(), out_dt, _ptr(lse), _ptr(weights), wp, wn, on))
     return out
 

@@ -581,3 +581,33 @@ def test_attention_over_the_largest_values_is_finite(nq):
     assert (out[..., 1::2] == 65504).all() and (np.abs(out[..., ::2] + 65504) <= 65536 * 2.0 ** -9).all()
     wide = _attend(q, cache, ids, np.full(nq, 300), fmt, f32=True)[0]
     assert (np.abs(wide[..., 1::2] - 65536) <= 65536 * 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_strides_that_no_element_uses(fmt):
+    """One token, one query or one head: its stride is never used, whatever torch has it at."""
+    x, _ = to16(np.random.default_rng(75).normal(size=(3, 16 * 128 + 4)), fmt)   # rows of a projection, no multiple of 8 long
+    row = x[:1].as_strided((1, 16, 128), (x.stride(0), 128, 1))
+    assert row.stride(0) % 8 == 4
+    a, b = qsa.alloc_qcache(2, 64), qsa.alloc_qcache(2, 64)
+    qsa.qcache_append(row[:, 2:4], row[:, 6:8], a, 9)
+    qsa.qcache_append(row[:, 2:4].contiguous(), row[:, 6:8].clone(memory_format=torch.contiguous_format), b, 9)
+    assert torch.equal(a, b)
+    out, _ = to16(np.zeros((1, 4 * 128 + 4)), fmt)
+    ko, vo = out.as_strided((1, 2, 128), (516, 128, 1)), out.as_strided((1, 2, 128), (516, 128, 1), 256)
+    qsa.qcache_load(a, ko, vo, 9)
+    kc, vc = torch.empty(1, 2, 128, dtype=DT[fmt], device="cuda"), torch.empty(1, 2, 128, dtype=DT[fmt], device="cuda")
+    qsa.qcache_load(a, kc, vc, 9)
+    assert torch.equal(ko, kc) and torch.equal(vo, vc) and not out[:, 512:].any()
+    cache = torch.from_numpy(random_cache(76, 1, 4, fmt)).cuda()
+    ids = np.array([[0, 2, 3]], dtype=np.int32)
+    for view in (row[:, :5], row[:, 3:4], x.as_strided((3, 1, 128), (128, 129, 1))):   # one query; one head of one; one head of three
+        n = view.shape[0]
+        want = _attend(view.clone(memory_format=torch.contiguous_format), cache, ids.repeat(n, 0), [250] * n, fmt)
+        for got, ref in zip(_attend(view, cache, ids.repeat(n, 0), [250] * n, fmt), want):
+            np.testing.assert_array_equal(got, ref)
+    one = x.as_strided((3, 1, 128), (128, 129, 1))
+    c, d = qsa.alloc_qcache(1, 64), qsa.alloc_qcache(1, 64)
+    qsa.qcache_append(one, one, c, 5)
+    qsa.qcache_append(one.clone(memory_format=torch.contiguous_format), one.clone(memory_format=torch.contiguous_format), d, 5)
+    assert torch.equal(c, d)
