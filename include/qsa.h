@@ -33,6 +33,8 @@
  *    returns a one-line reason.
  *  - One workspace must not be used by two calls that can run concurrently
  *    (e.g. on two streams); give each stream its own workspace.
+ *  - An output overlaps neither an input nor another output, unless its call says
+ *    that it may.
  */
 #ifndef QSA_H
 #define QSA_H
@@ -480,7 +482,7 @@ qsa_status qsa_select_attention_qcache(const void *qa, int64_t q_stride, int64_t
  * the order of the work.
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, nq, n_kv_heads or k < 1, nq * n_kv_heads * k >
  * 2^22, max_blocks outside [1, QSA_MAX_BLOCKS], a decay not finite or < 0, a prev that
- * overlaps acc without being it; QSA_ERR_WORKSPACE as above.
+ * overlaps acc without being it, weights or ids that overlap acc; QSA_ERR_WORKSPACE as above.
  */
 qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int nq, int n_kv_heads, int k, double decay,
                                  const float *prev, float *acc, int max_blocks, void *ws, size_t ws_bytes,
@@ -533,7 +535,7 @@ typedef struct {
  *          [0, src_blocks) (QSA_FLAG_BAD_ID), dst[row][i] is left as it was
  *   ws     a workspace of at least 256 bytes (its flags word is used), or NULL
  *
- * Out of place: a dst may overlap no src and no other dst.
+ * Out of place: a dst may overlap no src, no other dst and not keep.
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_arrays or n_keep out of range, sizes < 1,
  * dst_blocks < n_keep, block_bytes not a multiple of 4 or above 2^30, pointers not 4-byte
  * aligned, a dst that overlaps; QSA_ERR_WORKSPACE as above.

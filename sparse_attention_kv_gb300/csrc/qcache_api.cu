@@ -177,12 +177,14 @@ qsa_status qsa_block_weights_add(const float *weights, const int32_t *ids, int n
     if (max_blocks < 1 || max_blocks > QSA_MAX_BLOCKS)
         return fail(QSA_ERR_INVALID_ARG, "max_blocks must be in [1, %d] (got %d)", QSA_MAX_BLOCKS, max_blocks);
     if (!(decay >= 0.0) || !(decay <= DBL_MAX)) return fail(QSA_ERR_INVALID_ARG, "decay must be finite and >= 0");
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(acc), p0 = reinterpret_cast<uintptr_t>(prev);
-    const size_t acc_bytes = (size_t)max_blocks * sizeof(float);
-    if (prev && prev != acc && a0 < p0 + acc_bytes && p0 < a0 + acc_bytes)
+    const size_t acc_bytes = (size_t)max_blocks * sizeof(float), entries = (size_t)nq * k;
+    if (prev && prev != acc && overlap(acc, acc_bytes, prev, acc_bytes))
         return fail(QSA_ERR_INVALID_ARG, "prev must be acc itself or not overlap it");
     qsa_status st = check_flags_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
+    if (overlap(acc, acc_bytes, weights, entries * n_kv_heads * sizeof(float)) ||
+        overlap(acc, acc_bytes, ids, entries * sizeof(int32_t)))
+        return fail(QSA_ERR_INVALID_ARG, "acc must not overlap weights or ids");
     WeightsAddArgs a{};
     a.weights = weights;
     a.ids = ids;
@@ -262,16 +264,18 @@ qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const 
             for (int other = 0; other < 2; ++other) {   // dst i against src j, and against another dst j
                 if (other && i == j) continue;
                 const qsa_block_array &x = arrays[i], &y = arrays[j];
-                const uintptr_t a0 = reinterpret_cast<uintptr_t>(x.dst);
-                const uintptr_t b0 = reinterpret_cast<uintptr_t>(other ? (const void *)y.dst : y.src);
                 const size_t an = (size_t)x.n_rows * x.dst_blocks * x.block_bytes;
                 const size_t bn = (size_t)y.n_rows * (other ? y.dst_blocks : y.src_blocks) * y.block_bytes;
-                if (a0 < b0 + bn && b0 < a0 + an)
+                if (overlap(x.dst, an, other ? y.dst : y.src, bn))
                     return fail(QSA_ERR_INVALID_ARG, "array %d: dst overlaps the %s of array %d", i,
                                 other ? "dst" : "src", j);
             }
     qsa_status st = check_flags_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
+    for (int i = 0; i < n_arrays; ++i)
+        if (overlap(arrays[i].dst, (size_t)arrays[i].n_rows * arrays[i].dst_blocks * arrays[i].block_bytes, keep,
+                    (size_t)n_keep * sizeof(int32_t)))
+            return fail(QSA_ERR_INVALID_ARG, "array %d: dst overlaps keep", i);
     return launch_gather_blocks(arrays, n_arrays, keep, n_keep, flags_of(ws), static_cast<cudaStream_t>(stream));
 }
 

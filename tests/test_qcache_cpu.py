@@ -278,3 +278,19 @@ def test_decay_crosses_the_boundary_in_64_bits(lib):
     declared = re.search(r"qsa_block_weights_add\((.*?)\);", header, flags=re.S).group(1).split(",")
     at = next(i for i, x in enumerate(declared) if x.split()[-1] == "decay")
     assert declared[at].split()[0] == "double" and lib.qsa_block_weights_add.argtypes[at] is ctypes.c_double
+
+
+@pytest.mark.parametrize("case", [dict(acc=FAKE + 4 * (4 * 4 * 32) - 4), dict(acc=FAKE - 4 * 99), dict(ids=FAR + 4 * 99),
+                                  dict(ids=FAR - 4 * (4 * 32 - 1))])
+def test_weights_add_rejects_an_acc_that_overlaps_its_inputs(lib, case):
+    a = dict(w=FAKE, ids=2 * FAR, acc=FAR)
+    a.update(case)
+    st = lib.qsa_block_weights_add(a["w"], a["ids"], 4, 4, 32, 1.0, None, a["acc"], 100, None, 0, None)
+    assert st == qsa.ERR_INVALID_ARG and "overlap" in lib.qsa_last_error().decode()
+
+
+@pytest.mark.parametrize("keep", [FAR + 64 * 8 - 4, FAR - 12, FAR + 64])
+def test_gather_rejects_a_keep_inside_a_destination(lib, keep):
+    one = (qsa.BlockArray * 1)(qsa.BlockArray(FAKE, FAR, 64, 1, 8, 8))
+    assert lib.qsa_gather_blocks(one, 1, keep, 4, None, 0, None) == qsa.ERR_INVALID_ARG
+    assert "keep" in lib.qsa_last_error().decode()
