@@ -611,3 +611,10 @@ def test_strides_that_no_element_uses(fmt):
     qsa.qcache_append(one, one, c, 5)
     qsa.qcache_append(one.clone(memory_format=torch.contiguous_format), one.clone(memory_format=torch.contiguous_format), d, 5)
     assert torch.equal(c, d)
+
+
+def test_current_stream_is_the_public_one():
+    side = torch.cuda.Stream()
+    for s in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(s):
+            assert qsa._current_stream(torch.cuda.current_device()) == s.cuda_stream

@@ -294,3 +294,11 @@ def test_gather_rejects_a_keep_inside_a_destination(lib, keep):
     one = (qsa.BlockArray * 1)(qsa.BlockArray(FAKE, FAR, 64, 1, 8, 8))
     assert lib.qsa_gather_blocks(one, 1, keep, 4, None, 0, None) == qsa.ERR_INVALID_ARG
     assert "keep" in lib.qsa_last_error().decode()
+
+
+def test_current_stream_needs_no_internal_name(monkeypatch):
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream())
+    assert qsa._current_stream(0) == 77
