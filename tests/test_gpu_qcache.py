@@ -618,3 +618,95 @@ def test_current_stream_is_the_public_one():
     for s in (torch.cuda.current_stream(), side):
         with torch.cuda.stream(s):
             assert qsa._current_stream(torch.cuda.current_device()) == s.cuda_stream
+
+
+def _coherent(kind, nq, group):
+    """(K, V, q) whose P.V weights round alike over thousands of tokens, so that what the rounding leaves adds up.
+
+    K rows are constant (scale 0), so a block's tokens have one logit, u[block] times the head's factor: 0, or 0.25 in
+    every fourth block, which sets the reference.  A head's factor makes 2^y of the others, relative to that, an odd
+    number of 1024ths in 0.70 .. 0.80: 10 significant bits, which a weight's fp16 form holds and two e4m3 terms (8 bits)
+    do not.  V rows lie between -0.9375 and 0.9375 (scale 1/8 exactly) with 126 dimensions near 0, so at codes 7 and 8.
+    rising: the last block's logit moves the references late (by 5 to 8 powers of two); v growing: its scale does (2^5)."""
+    rng = np.random.default_rng(60)
+    block = np.arange(64 * 64 - 13) // 64
+    u, a = np.where(np.arange(64) % 4 == 0, 0.25, 0.0), np.ones(64)
+    if kind == "rising":
+        u[63] = 4.25
+    elif kind == "v growing":
+        a[63] = 32
+    v = rng.uniform(-0.02, 0.02, (len(block), 128))
+    v[:, 0], v[:, 1] = -0.9375, 0.9375
+    p = (2 * rng.integers(359, 410, size=(nq, group)) + 1) / 1024
+    rest = -np.log(p) * 128 ** 0.5 / 0.25
+    hold = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).bfloat16().double().numpy()  # noqa: E731
+    q = hold(rng.normal(size=(nq, group, 128)) * 0.05)
+    q[..., :4] = 0
+    rest -= q.sum(-1)
+    for i in range(4):                                  # the sum to 32 bits
+        q[..., i] = hold(rest)
+        rest -= q[..., i]
+    return np.repeat(u[block][:, None, None], 128, 2), (v * a[block][:, None])[:, None], q
+
+
+@pytest.mark.parametrize("group", [5, 16])
+@pytest.mark.parametrize("nq", [3, 80])
+@pytest.mark.parametrize("kind", ["even", "rising", "v growing"])
+def test_attention_returns_what_the_weights_rounding_leaves(kind, nq, group):
+    """bf16, split over a cluster (3 queries) and not (80), half groups and whole ones.  What the rounding leaves of a weight w,
+    at most 2^-8 of it, is returned at the mean code, 7.5, so a code c keeps 2^-8 w |c - 7.5|; the codes of a
+    dimension are 7 or 8 at random, so those add up as a random walk: 1.5 of its deviation bounds the norm over 126
+    dimensions.  To that the fp32 arithmetic: 128 additions of a product (2^-17) at most truncated (2^-16), a logit
+    below 16 (2^-20) and its power, 40 additions of the sum of weights (2^-18.7): 2^-15 of the sum of magnitudes
+    in all.  Without the return the error is 3 ("rising") to 11 times this bound by the same arithmetic, with
+    what is left not moved along with the references hundreds of times."""
+    fmt = oq.BF16
+    k, v, q = _coherent(kind, nq, group)
+    n = len(k)
+    kt, _ = to16(k, fmt)
+    vt, _ = to16(v, fmt)
+    qt, qd = to16(q, fmt)
+    cache = qsa.alloc_qcache(1, 64 * 64)
+    qsa.qcache_append(kt, vt, cache, 0)
+    chosen = np.r_[0:60, 63]
+    ids = np.repeat(chosen.astype(np.int32)[None], nq, 0)
+    got = _attend(qt, cache, ids, np.full(nq, n), fmt, f32=True)[0]
+    host = cache.cpu().numpy()
+    codes, pairs = zip(*(oq.read_block(host[0, b], fmt)[1:] for b in chosen))
+    seen = (64 * chosen[:, None] + np.arange(64) < n).reshape(-1)
+    codes = np.concatenate(codes)[seen]
+    ks, km, vs, vm = (np.concatenate([x[w, :, j] for x in pairs])[seen] for w in (0, 1) for j in (0, 1))
+    assert not ks.any() and (np.abs(codes[:, 2:] - 7.5) == 0.5).all()
+    s = float(np.float32(128 ** -0.5)) * qd.sum(-1)[..., None] * km
+    p = np.exp(s - s.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    w = p * vs
+    want = w @ codes + (p @ vm)[..., None]
+    bound = 1.5 * 2.0 ** -8 * np.sqrt(w ** 2 @ (codes - 7.5) ** 2) + 2.0 ** -15 * (w @ codes + (p @ np.abs(vm))[..., None])
+    assert np.linalg.norm((got - want)[..., 2:]) <= np.linalg.norm(bound[..., 2:])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_head_major_views(fmt):
+    """Rows kept head by head in memory: the append, the reader and the attention take them as they lie."""
+    kv, n = 3, 70
+    x, _ = to16(_rows(77, kv, n), fmt)                     # [kv, n, 128] in memory
+    y, _ = to16(_rows(78, kv, 2 * n), fmt)
+    k, v = x.transpose(0, 1), y[:, ::2].transpose(0, 1)    # [n, kv, 128]
+    assert not k.is_contiguous() and k.stride(1) > k.stride(0)
+    a, b = qsa.alloc_qcache(kv, 128), qsa.alloc_qcache(kv, 128)
+    qsa.qcache_append(k, v, a, 31)
+    qsa.qcache_append(k.contiguous(), v.contiguous(), b, 31)
+    assert torch.equal(a, b)
+    ko, vo = torch.zeros_like(x), torch.zeros_like(y)
+    qsa.qcache_load(a, ko.transpose(0, 1), vo[:, ::2].transpose(0, 1), 31)
+    kc, vc = torch.empty(n, kv, 128, dtype=DT[fmt], device="cuda"), torch.empty(n, kv, 128, dtype=DT[fmt], device="cuda")
+    qsa.qcache_load(a, kc, vc, 31)
+    assert torch.equal(ko.transpose(0, 1), kc) and torch.equal(vo[:, ::2].transpose(0, 1), vc) and not vo[:, 1::2].any()
+    cache = torch.from_numpy(random_cache(79, 2, 10, fmt)).cuda()
+    heads, _ = to16(np.random.default_rng(80).normal(size=(32, 6, 128)), fmt)   # [heads, nq, 128] in memory
+    nt = np.full(6, 640)
+    ids = random_ids(81, 6, 5, nt)
+    view = heads.transpose(0, 1)
+    for got, ref in zip(_attend(view, cache, ids, nt, fmt), _attend(view.contiguous(), cache, ids, nt, fmt)):
+        np.testing.assert_array_equal(got, ref)
