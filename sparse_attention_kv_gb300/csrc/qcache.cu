@@ -54,7 +54,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // (x - lo) / scale rounded half to even, exactly: the difference as an unevaluated sum
 // a + e, a first quotient (at most one off), and the sign of the remainder against
-// half a step.  Each fp32 step before the last comparison is exact.
+// half a step.  Each fp32 step before the last comparison is exact (a + e is the two-sum of O. Moller and
+// D. E. Knuth).
 __device__ __forceinline__ int exact_code(float x, float lo, float scale) {
     const float a = x - lo;
     const float bb = a - x;
@@ -101,11 +102,12 @@ __device__ __noinline__ uint4 exact_row(const uint8_t *row, int c, float lo, flo
 // The row's codes (a nibble pair per byte: words 0 and 1 units c low and c + 8 high, words 2 and 3 units
 // c + 4 and c + 12) and its (scale, minimum) pair; the four threads of a token call it together.
 //
-// The quotient (x - min) / scale comes from the reciprocal and one correction, to half an fp32
-// step (2^-21 below 16).  Where x is 0 or at least kShort times the scale (and the minimum too),
-// 2 (x - min) - (2n + 1) scale is a multiple of 2^-20 of the scale, so a quotient is a half exactly
-// when its value is, and the rounding of the quotient is the exact one's; a row with a shorter x looks
-// whether such an x has its quotient near a half, and only then takes the exact comparison.
+// The quotient (x - min) / scale comes from the reciprocal and one correction by its remainder (P. Markstein, IBM
+// Journal of Research and Development 34, 1990), to half an fp32 step (2^-21 below 16).  Where x
+// is 0 or at least kShort times the scale (and the minimum too), 2 (x - min) - (2n + 1) scale is a
+// multiple of 2^-20 of the scale, so a quotient is a half exactly when its value is, and the
+// rounding of the quotient is the exact one's; a row with a shorter x looks whether such an x has
+// its quotient near a half, and only then takes the exact comparison.
 template <bool F16>
 __device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[16], const uint8_t *row, int c, uint32_t (&packed)[4]) {
     using Fmt = QFmt<F16>;
@@ -219,7 +221,8 @@ __global__ void __launch_bounds__(kNT, 4) append_kernel(const RowPtr k, const Ro
     const long long at = (long long)b * kQBlockTok - first;       // the row that the block's first token takes
     const long long i = at + tok;
     // the block's tokens t0 .. t1 - 1 are the call's
-    const int t0 = at < 0 ? (int)min(-at, (long long)kQBlockTok) : 0, t1 = (int)min((long long)n - at, (long long)kQBlockTok);
+    const int t0 = at < 0 ? (int)min(-at, (long long)kQBlockTok) : 0;
+    const int t1 = (int)min((long long)n - at, (long long)kQBlockTok);
     const bool in = tok >= t0 && tok < t1;
     uint8_t *rec = cache + qrec_offset(g, nb_cap, b);
     uint32_t xk[16], xv[16], packed[4];
