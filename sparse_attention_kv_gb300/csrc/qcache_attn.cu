@@ -492,8 +492,8 @@ __device__ __forceinline__ void prepare_queries(const QParams &p, int u_at, int 
 
 // F16: rows and queries in fp16 (three terms), otherwise bf16 (two); W: the slots' weights are wanted; HALF: groups
 // of at most eight heads, whose softmax threads take one token and eight heads each instead of two tokens and half
-// of sixteen heads (256 queries x 8 KV heads x 8 heads, k = 32: 98 us, by the form for sixteen 120; in fp16 145
-// and 192; one query 8.5 and 8.8.  One warpgroup for eight heads and the other idle took 115 where this took 101).
+// of sixteen heads (256 queries x 8 KV heads x 8 heads, k = 32: 100 us, by the form for sixteen 122; in fp16 107
+// and 134; one query 7.8 and 8.1.  One warpgroup for eight heads and the other idle took 115 where this took 101).
 template <bool F16, bool W, bool HALF>
 __global__ void __launch_bounds__(kThreads, 2) qattn_kernel(const __grid_constant__ QParams p) {
     constexpr int TERMS = F16 ? 3 : 2;
