@@ -438,7 +438,8 @@ qsa_status qsa_qcache_load(const void *cache, qsa_dtype dt, int n_kv_heads, int 
  * largest value), accumulated in fp32; softmax statistics, lse and weights in fp32; the
  * weights of the P.V product are rounded to 8 significant bits beside bf16 rows and 12 beside
  * fp16 ones, and to 2^-18 of the largest weight times the largest V scale where they are
- * smaller.
+ * smaller.  Sums over the tokens are formed in fp32 before they are divided by the weights' sum:
+ * bf16 rows of V above 2^80 in magnitude may overflow.
  * Launch: as a programmatic dependent of the work before it on `stream`, as
  * qsa_select_attention.
  * Errors: as qsa_select_attention's, with n_heads a multiple of n_kv_heads of at most 16

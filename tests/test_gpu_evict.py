@@ -365,3 +365,53 @@ def test_weights_add_keeps_the_decay_in_64_bits(decay, nq):
     # one rounding to fp32 of a double that is at most one step of 2^-53 off (a product and a sum, or both in one)
     assert (np.abs(got - double) <= np.abs(double) * (2.0 ** -24 + 2.0 ** -52)).all()
     assert (got == double.astype(np.float32)).mean() > 0.999
+
+
+def test_captured_on_several_streams():
+    """One captured graph that forks: the append on one stream, attention and weights on another behind it, the plan on
+    a third, and the move behind all of them; replays give what eager calls give."""
+    fmt, kv, blocks, k, n_keep = oq.BF16, 2, 40, 8, 16
+    start = torch.from_numpy(random_cache(8, kv, blocks, fmt)).cuda()
+    rng = np.random.default_rng(9)
+    rows = [to16(rng.normal(size=(3, kv, 128)), fmt)[0] for _ in "kv"]
+    q, _ = to16(rng.normal(size=(2, 32, 128)), fmt)
+    ids = _cuda(random_ids(9, 2, k, np.full(2, 64 * blocks - 70)))
+    src = torch.rand(blocks, device="cuda")
+
+    def buffers():
+        return dict(cache=start.clone(), n=torch.tensor([64 * blocks - 70] * 2, dtype=torch.int32, device="cuda"),
+                    out=torch.zeros_like(q), w=torch.zeros(2, kv, k, device="cuda"), acc=torch.zeros(blocks, device="cuda"),
+                    keep=torch.zeros(1, n_keep, dtype=torch.int32, device="cuda"), left=torch.zeros(1, dtype=torch.int32, device="cuda"),
+                    dst=torch.zeros(kv, n_keep, oq.REC, dtype=torch.uint8, device="cuda"), low=torch.zeros(n_keep, device="cuda"))
+
+    def step(b, side, third):
+        main = torch.cuda.current_stream()
+        qsa.qcache_append(*rows, b["cache"], b["n"][:1])
+        b["n"] += 3
+        side.wait_stream(main)
+        third.wait_stream(main)
+        with torch.cuda.stream(third):                     # the plan by weights at hand, beside the attention
+            qsa.evict_plan(src[None], b["n"][:1], b["keep"], b["left"], 1, 2)
+        with torch.cuda.stream(side):
+            qsa.select_attention_qcache(q, b["cache"], ids, b["n"], b["out"], None, b["w"])
+            qsa.block_weights_add(b["w"], ids, b["acc"], prev=b["acc"], decay=0.75)
+        main.wait_stream(side)
+        main.wait_stream(third)
+        qsa.gather_blocks([(b["cache"], b["dst"]), (b["acc"], b["low"])], b["keep"][0])
+
+    want, got = buffers(), buffers()
+    s = torch.cuda.current_stream()
+    for _ in range(3):
+        step(want, s, s)
+    side, third = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(got, side, third)
+    for name, x in buffers().items():
+        got[name].copy_(x)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
