@@ -13,7 +13,7 @@
 //    (evict_plan_long_kernel, a radix select of 8 bits a pass).
 // 3. gather_blocks_kernel: a warp copies 2 KB of a record, or as many small records as its lanes hold.
 //
-// Measured (warm graph): 1. 3.4 us for 3 queries x 4 KV heads x 32 slots over 4,032 blocks, 6.6 us for 256
+// Measured (warm graph): 1. 3.4 us for 3 queries x 4 KV heads x 32 slots over 4,032 blocks, 6.9 us for 256
 // queries over 8,125 (every CTA reading all ids took 17.5); launches and one chain of loads.  2 and 3 together:
 // 5.3 us to keep 128 of 257 blocks of one KV head; 55 us to keep 4,096 of 8,125 blocks of 4 (287 MB, of which
 // the move takes 42 us, 6.9 TB/s: the copy rate).

@@ -15,8 +15,8 @@
 // partial block only the call's own nibbles change, by an atomic exclusive-or of each word that
 // holds others too, so that two appends may fill one block at the same time.
 //
-// Measured, 131,072 tokens x 4 KV heads, bf16: the reader moves its 336 MB in 51 us (6.65 TB/s, the
-// copy rate); the writer's 336 MB take 78 us: it issues 0.70 instructions a cycle and scheduler (15
+// Measured, 131,072 tokens x 4 KV heads, bf16: the reader moves its 340 MB in 52 us (6.5 TB/s, near
+// the copy rate); the writer's 340 MB take 76 us: it issues 0.70 instructions a cycle and scheduler (15
 // a value, half of them the quotient and its rounding), against 50 us at the copy rate.  Units dealt as
 // 32 consecutive bytes per thread instead of one 16-byte unit in four took 65 us (reader);
 // codes by divisions and byte-wise transposes 203 us (writer).

@@ -52,12 +52,12 @@
 // QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
 //
 // Measured (device time in a graph of back-to-back calls, 256 queries x 64 heads in 4 groups x 520,000 tokens,
-// k = 32, weights wanted): 63.5 us, where one read of each selected block by each query is 285 MB (42 us
+// k = 32, weights wanted): 62.6 us (fp16 69), where one read of each selected block by each query is 285 MB (42 us
 // at the copy rate) and DRAM moves 218 MB; the 16-bit attention of the same selection takes 164 us.  It is
 // bound by the softmax warps' chain of instructions (of a unit's 36,000 cycles, in a build that reads the clock:
 // 1,800 until it stands prepared, 6,300 for the first step with its maxima, 3,400 for each other one, 4,200
 // for the end; one CTA per SM takes 83 us), not by memory, tensor cores (12% busy) or the copies.  Without the
-// weights 54-56 us.  Forms on the way, same call: one warpgroup doing everything 105 us; two sharing the heads,
+// weights 56 us (fp16 63).  Forms on the way, same call: one warpgroup doing everything 105 us; two sharing the heads,
 // four CTAs per SM, 99; a control warp and S in two buffers, three CTAs per SM, 90; shared memory addressed as
 // such 78.5; this division of labour 70; pairs through shared memory, float reductions 67.5; the first unit's
 // queries shared out 64.  Not kept: reading S before the step's pairs or before the last step's end (74 and 79:
