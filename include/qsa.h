@@ -545,6 +545,232 @@ qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const 
                              size_t ws_bytes, qsa_stream stream);
 
 /*
+ * ---- The paged 16-bit cache ------------------------------------------------------
+ *
+ * A pool of pages that many sequences share.  A page is a 64-token block of the 16-bit cache in
+ * the layout of qsa_select_attention, for every KV head: page p holds the K rows
+ * kcache[g][64 p .. 64 p + 63][128] and the V block vcache_t[g][p][128][64] (and, in other arrays
+ * of one record per block, whatever else belongs to it, e.g. its indexer key).  Its state:
+ *
+ *     table    [n_rows][table_stride] int32: the pages of sequence (row) s in order, page
+ *              table[s][j] holding its tokens 64 j .. 64 j + 63; -1 behind the last one
+ *     n_tokens [n_rows] int32: tokens of each sequence (its row may hold more pages than they fill)
+ *     refs     [n_pages] int32: how many entries of the table hold each page; 0 = free
+ *
+ * all on the DEVICE.  A step of generation: qsa_pages_reserve makes room behind the sequences,
+ * qsa_pages_copy copies the pages that were shared and are about to be written,
+ * qsa_pages_append writes the rows; qsa_pages_fork lets a sequence begin with another's pages,
+ * qsa_pages_release gives pages back, qsa_pages_compact moves the live pages together.  The
+ * attention of a prompt (qsa_prompt_attention) and of drafted tokens over the pages
+ * (qsa_tree_attention) stand beside them.  No passage of the source pages defines these
+ * calls.  One call at a time may change a table, its lengths and its refs.
+ */
+
+/* Some row of qsa_pages_reserve got no pages: too few are free. */
+#define QSA_FLAG_NO_PAGES 0x40u
+
+/* Largest number of pages of a pool, and of rows of a table. */
+#define QSA_MAX_PAGES (1 << 20)
+#define QSA_MAX_TABLE_ROWS 4096
+
+/* Workspace of qsa_pages_reserve and qsa_pages_compact, in bytes; 0 for sizes out of range. */
+size_t qsa_pages_workspace_bytes(int n_rows, int n_pages);
+
+/*
+ * Fork: for each i < n the row dst[i] becomes a copy of row src[i]: the same pages for its
+ * n_tokens[src[i]] tokens (pages reserved behind them are not taken), -1 behind them, the same
+ * n_tokens, and one more reference on each page.
+ *
+ *   table, table_stride, max_pages, n_rows   max_pages <= table_stride entries of a row are used
+ *   src, dst  [n] int32 on the DEVICE
+ *   ws        a workspace of at least 256 bytes (its flags word is used), or NULL
+ *
+ * Entry i is skipped, with QSA_FLAG_BAD_ID, when src[i] or dst[i] is no row, when dst[i] is an
+ * earlier dst or any src of the call, or when it still has tokens (release it first).  An
+ * entry with src[i] = -1 and dst[i] = -1 is skipped without a flag.  Pages that the row dst[i] reserved
+ * without tokens are released.
+ * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, QSA_MAX_TABLE_ROWS],
+ * n_pages outside [1, QSA_MAX_PAGES], max_pages outside [1, QSA_MAX_PAGES], table_stride <
+ * max_pages, n outside [0, n_rows], arrays that overlap; QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not
+ * 256-byte aligned.
+ */
+qsa_status qsa_pages_fork(int32_t *table, int64_t table_stride, int max_pages, int32_t *n_tokens, int n_rows,
+                          int32_t *refs, int n_pages, const int32_t *src, const int32_t *dst, int n, void *ws,
+                          size_t ws_bytes, qsa_stream stream);
+
+/*
+ * Release: row s keeps the pages of its first keep[s] tokens and gives the others back (-1 in the
+ * table, one reference less each); n_tokens[s] = min(n_tokens[s], keep[s]).  keep[s] = 0 frees the
+ * row, keep[s] < 0 leaves it as it is.
+ *
+ *   keep  [n_rows] int32 on the DEVICE; may be n_tokens itself (reserved pages are given back)
+ * Entries of the table that are no page, and references that are 0 already, are left (with
+ * QSA_FLAG_BAD_ID).  Errors: as qsa_pages_fork's.
+ */
+qsa_status qsa_pages_release(int32_t *table, int64_t table_stride, int max_pages, int32_t *n_tokens, int n_rows,
+                             int32_t *refs, int n_pages, const int32_t *keep, void *ws, size_t ws_bytes,
+                             qsa_stream stream);
+
+/*
+ * Reserve: room for add[s] tokens behind the n_tokens[s] of every row s.  A row gets the pages
+ * that its table lacks for them, and, when add[s] > 0 and its last page is partial and has other
+ * references too, a page of its own in place of that one.  Pages are given in ascending order, the
+ * lowest free ones first, to the rows in order and within a row by position.  Of several rows that share their last
+ * page and write, the last one keeps it when no other row refers to it.
+ *
+ *   add         [n_rows] int32 on the DEVICE (negative: as 0, with QSA_FLAG_NBLOCKS_CLAMPED)
+ *   new_tokens  [n_rows] int32 out: n_tokens + add; n_tokens itself where the row could not be
+ *               served: too few pages are free for it and the rows before it
+ *               (QSA_FLAG_NO_PAGES), or it would pass max_pages entries (QSA_FLAG_NBLOCKS_CLAMPED).  Such a
+ *               row is left as it was.  The pages such rows ask for count for the rows behind them
+ *               that need any; a row that passes max_pages asks for none.
+ *   copy_src, copy_dst [n_rows] int32 out: the page that row s shared and the one it has in
+ *               its place, or -1 twice; qsa_pages_copy brings the contents over
+ *   ws          a workspace of at least qsa_pages_workspace_bytes(n_rows, n_pages) bytes
+ * Errors: as qsa_pages_fork's; ws may not be NULL.
+ */
+qsa_status qsa_pages_reserve(int32_t *table, int64_t table_stride, int max_pages, const int32_t *n_tokens, int n_rows,
+                             int32_t *refs, int n_pages, const int32_t *add, int32_t *new_tokens, int32_t *copy_src,
+                             int32_t *copy_dst, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/*
+ * Compact: the live pages (refs > 0) move to the front of the pool.  With L of them, the i-th live
+ * page at or behind L, in ascending order, moves to the i-th free page below L; the others stay.
+ *
+ *   table_out  [n_rows][table_stride] int32 out: the table with the new pages (its first max_pages
+ *              entries a row; entries that are no page become -1, with QSA_FLAG_BAD_ID but for -1); may be table itself
+ *   refs_out   [n_pages] int32 out: the references with the new pages; may be refs itself
+ *   copy_src, copy_dst [n_pages / 2] int32 out: the moves, -1 behind them (a pool of one page: none, they may
+ *              be NULL); qsa_pages_copy carries them out
+ *   ws         as for qsa_pages_reserve
+ * Errors: as qsa_pages_reserve's.
+ */
+qsa_status qsa_pages_compact(const int32_t *table, int64_t table_stride, int max_pages, int n_rows, const int32_t *refs,
+                             int n_pages, int32_t *table_out, int32_t *refs_out, int32_t *copy_src, int32_t *copy_dst,
+                             void *ws, size_t ws_bytes, qsa_stream stream);
+
+/*
+ * Copy pages within their pool: x[row][dst_ids[i]] = x[row][src_ids[i]] for every row and i < n,
+ * for each of n_arrays (host array, 1 .. QSA_GATHER_MAX_ARRAYS) arrays, one launch in all.  In an
+ * array src == dst and src_blocks == dst_blocks (the pool).
+ *
+ *   src_ids, dst_ids [n] int32 on the DEVICE: -1 twice is skipped, an id outside the pool too
+ *             (with QSA_FLAG_BAD_ID).  No dst id may be a src id or another dst id of the call (the lists of
+ *             qsa_pages_reserve and qsa_pages_compact are so); a src id may repeat
+ *   ws        a workspace of at least 256 bytes (its flags word is used), or NULL
+ * Errors: as qsa_gather_blocks's, n outside [0, QSA_MAX_PAGES], an array whose src is not its dst,
+ * arrays that overlap each other or the ids.
+ */
+qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int32_t *src_ids, const int32_t *dst_ids,
+                          int n, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/*
+ * Append: K and V rows into the pages.  Row s takes cu_rows[s + 1] - cu_rows[s] rows, at positions
+ * first[s], first[s] + 1, ...: entry e (cu_rows[s] <= e < cu_rows[s + 1]) is row rows[e] of k and v
+ * (row e itself when rows is NULL) and goes to page table[s][pos / 64].
+ *
+ *   k, v      row r of KV head g at k + r * k_token_stride + g * k_head_stride, 128 values of `dt`
+ *             (QSA_BF16 or QSA_F16; strides in elements, multiples of 8), 16-byte aligned
+ *   n_source  rows of k and v; an entry of rows outside [0, n_source) is skipped (with
+ *             QSA_FLAG_BAD_ID, but for -1) and its position left as it was
+ *   rows      [n] int32 on the DEVICE, e.g. the accepted nodes of a draft; or NULL
+ *   n         entries in all, an upper bound on cu_rows (n = n_source when rows is NULL)
+ *   cu_rows   [n_rows + 1] int32 on the DEVICE, ascending, clamped to [0, n] (and a descent to no
+ *             rows; either sets QSA_FLAG_NBLOCKS_CLAMPED)
+ *   first     [n_rows] int32 on the DEVICE (n_tokens before the step); a position below 0 or at or past
+ *             64 max_pages is dropped (QSA_FLAG_NBLOCKS_CLAMPED), one whose table entry is no page too
+ *             (QSA_FLAG_BAD_ID)
+ *   kcache, vcache_t, capacity   the pool: capacity = 64 n_pages, 16-byte aligned.  Other positions keep their
+ *             values, whatever else writes them meanwhile
+ * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides not multiples of 8,
+ * head_dim != 128, n_kv_heads outside [1, 65535], capacity not a positive multiple of 64 or above 64 *
+ * QSA_MAX_PAGES, n_rows, max_pages or table_stride as above, n or n_source outside [0, 2^28],
+ * rows NULL and n != n_source, a pool that overlaps an input; QSA_ERR_UNSUPPORTED for another dtype; QSA_ERR_WORKSPACE as
+ * above.
+ */
+qsa_status qsa_pages_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                            int64_t v_token_stride, int64_t v_head_stride, qsa_dtype dt, int n_source,
+                            const int32_t *rows, int n, const int32_t *cu_rows, const int32_t *first,
+                            const int32_t *table, int64_t table_stride, int max_pages, int n_rows, int n_kv_heads,
+                            int head_dim, void *kcache, void *vcache_t, int capacity, void *ws, size_t ws_bytes,
+                            qsa_stream stream);
+
+/* Workspace of the two attentions below for `rows` query rows (tokens) in all, in bytes; 0 for invalid sizes. */
+size_t qsa_attention_workspace_bytes(int rows, int n_heads, int n_kv_heads);
+
+/*
+ * Causal attention of whole prompts, packed: sequence s has the queries cu_q[s] .. cu_q[s + 1] - 1 and
+ * the keys cu_k[s] .. cu_k[s + 1] - 1.  With lq and lk of them, query i (0 <= i < lq) sees the
+ * first lk - lq + i + 1 keys (a whole prompt has lk = lq; a chunk of one has the earlier tokens' keys
+ * before its own).  For head h, with KV head g = h / (n_heads / n_kv_heads):
+ *
+ *   o[i][h] = sum_t exp(scale (s_t - m)) v[t][g] / sum_t exp(scale (s_t - m)),  s_t = q[i][h] . k[t][g]
+ *   lse[i][h] = scale m + log(sum_t exp(scale (s_t - m))),  m = max_t s_t
+ *
+ * over the keys it sees; o = 0 and lse = -inf when it sees none.
+ *
+ *   q         [total_q][n_heads][128] of `dt`, k and v [total_k][n_kv_heads][128], addressed by token and
+ *             head strides in elements, multiples of 8 (slices of a fused projection's rows are taken as
+ *             they lie), 16-byte aligned; those of k and v >= 128 along an axis of more than one entry
+ *   cu_q, cu_k [n_seqs + 1] int32 on the DEVICE, ascending from >= 0 to <= total_q and total_k; a
+ *             value outside is clamped and a descent makes an empty sequence (either sets QSA_FLAG_NBLOCKS_CLAMPED)
+ *   out       [total_q][n_heads][128] of out_dt: QSA_F32, or dt; 16-byte aligned
+ *   lse       [total_q][n_heads] fp32 out, or NULL
+ *   scale     softmax scale (host float), finite and > 0
+ *   ws        a workspace of at least qsa_attention_workspace_bytes(total_q, n_heads, n_kv_heads) bytes
+ *
+ * Rows of out and lse that belong to no sequence are left as they were; keys and values that a query does not see do
+ * not touch it, whatever they hold.  Arithmetic: products on the tensor cores with fp32 sums, softmax
+ * statistics in fp32, the weights of the product with v rounded to `dt`.
+ * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides as above, head_dim != 128, n_heads not 1 to
+ * 16 times n_kv_heads, n_kv_heads outside [1, 65535], n_seqs outside [1, 65535], total_q < 0 or total_q *
+ * n_heads >= 2^30, total_k < 0 or total_k >= 2^30, a scale not finite or <= 0, out_dt other than QSA_F32 or dt, an
+ * out or lse that overlaps an input or each other;
+ * QSA_ERR_UNSUPPORTED for a dtype other than QSA_BF16 or QSA_F16; QSA_ERR_WORKSPACE for a ws that is NULL, smaller or
+ * not 256-byte aligned.
+ */
+qsa_status qsa_prompt_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                                int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                                int64_t v_head_stride, qsa_dtype dt, const int32_t *cu_q, const int32_t *cu_k, int n_seqs,
+                                int total_q, int total_k, int n_heads, int n_kv_heads, int head_dim, float scale,
+                                void *out, qsa_dtype out_dt, float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/* Largest tree of qsa_tree_attention. */
+#define QSA_TREE_MAX_NODES 64
+
+/*
+ * Attention of drafted tokens over the paged cache: sequence s has n_tokens[s] tokens in its
+ * pages and a tree of the drafted tokens cu_nodes[s] .. cu_nodes[s + 1] - 1 (nodes, in an order
+ * that puts a parent before its children).  A node sees every token of the sequence, its
+ * ancestors and itself; formulas as for qsa_prompt_attention.  One node per sequence is an ordinary
+ * decode step.  The nodes' K and V rows come with the call and are not in the pages yet
+ * (qsa_pages_append writes those that are accepted).
+ *
+ *   q, k, v   as for qsa_prompt_attention, [total_nodes] rows
+ *   parents   [total_nodes] int32 on the DEVICE: the parent's place in its tree (0 for its first node), or
+ *             -1: the node follows the context.  A parent that is not before its node is taken as -1
+ *             (QSA_FLAG_BAD_ID)
+ *   cu_nodes  [n_seqs + 1] int32 on the DEVICE, ascending from >= 0 to <= total_nodes, clamped as cu_q above; a tree of
+ *             more than max_nodes nodes loses the last ones (QSA_FLAG_NBLOCKS_CLAMPED): their rows are left as they were
+ *   max_nodes host int, 1 .. QSA_TREE_MAX_NODES: an upper bound on the trees' nodes
+ *   kcache, vcache_t, capacity  the pool: capacity = 64 n_pages tokens per KV head, 16-byte aligned
+ *   table, table_stride, max_pages  [n_seqs] rows as above; a page outside the pool is skipped (QSA_FLAG_BAD_ID)
+ *   n_tokens  [n_seqs] int32 on the DEVICE, clamped to [0, 64 max_pages] (QSA_FLAG_NBLOCKS_CLAMPED)
+ *   out, out_dt, lse, scale, ws   as for qsa_prompt_attention, with total_nodes rows
+ *
+ * Positions at or past n_tokens take no part, whatever the pages hold there, nor do nodes that are no ancestors.
+ * Errors: as qsa_prompt_attention's, max_nodes out of range, capacity < 64, not a multiple of 64 or above 64 *
+ * QSA_MAX_PAGES, n_kv_heads * capacity >= 2^30, max_pages outside [1, QSA_MAX_PAGES], table_stride < max_pages.
+ */
+qsa_status qsa_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                              int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                              int64_t v_head_stride, qsa_dtype dt, const int32_t *parents, const int32_t *cu_nodes,
+                              int n_seqs, int total_nodes, int max_nodes, const void *kcache, const void *vcache_t,
+                              int capacity, const int32_t *table, int64_t table_stride, int max_pages,
+                              const int32_t *n_tokens, int n_heads, int n_kv_heads, int head_dim, float scale,
+                              void *out, qsa_dtype out_dt, float *lse, void *ws, size_t ws_bytes, qsa_stream stream);
+
+/*
  * Copy the workspace flags word (QSA_FLAG_* bits) to host `*flags`, waiting for
  * `stream` to finish; clear it on the device when `clear` is nonzero.
  */

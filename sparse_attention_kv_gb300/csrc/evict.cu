@@ -11,7 +11,8 @@
 //    and a barrier each, 8.6 us at 8,125 blocks; two bits at a time took 13); one scan
 //    then emits the kept ids in ascending order, ties to the lower id.  Rows past 16,384 blocks re-read their weights instead
 //    (evict_plan_long_kernel, a radix select of 8 bits a pass).
-// 3. gather_blocks_kernel: a warp copies 2 KB of a record, or as many small records as its lanes hold.
+// 3. gather_blocks_kernel: a warp copies 2 KB of a record, or as many small records as its lanes hold.  With a list of
+//    places it copies pages within their pool.
 //
 // Measured (warm graph): 1. 3.4 us for 3 queries x 4 KV heads x 32 slots over 4,032 blocks, 6.9 us for 256
 // queries over 8,125 (every CTA reading all ids took 17.5); launches and one chain of loads.  2 and 3 together:
@@ -20,6 +21,7 @@
 #include <climits>
 #include <mutex>
 
+#include "launch.h"
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
 
@@ -271,6 +273,7 @@ struct GatherParams {
     int n_arrays;
     int n_keep;
     const int32_t *keep;
+    const int32_t *to;       // null: record i goes to place i
     uint32_t *flags;
 };
 
@@ -301,13 +304,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_blocks_kernel(const __g
         const uint32_t i = (group - row * x.groups) * (32u / x.lanes) + lane / x.lanes;
         if (i >= (uint32_t)p.n_keep) continue;
         const int b = p.keep[i];
-        if (b < 0 || b >= x.src_blocks) {
-            if (b != -1 && lane % x.lanes == 0 && p.flags) atomicOr(p.flags, QSA_FLAG_BAD_ID);
+        const int place = p.to ? p.to[i] : (int)i;
+        if (b < 0 || b >= x.src_blocks || place < 0 || place >= x.dst_blocks) {
+            if ((b != -1 || place < -1 || (p.to && place != -1)) && lane % x.lanes == 0 && p.flags)
+                atomicOr(p.flags, QSA_FLAG_BAD_ID);
             continue;
         }
         const size_t bytes = (size_t)x.units * (x.wide ? 16 : 4);
         const uint8_t *src = x.src + ((size_t)row * x.src_blocks + b) * bytes;
-        uint8_t *dst = x.dst + ((size_t)row * x.dst_blocks + i) * bytes;
+        uint8_t *dst = x.dst + ((size_t)row * x.dst_blocks + place) * bytes;
         const uint32_t from = piece * (32u * kBatch) + lane % x.lanes;
         if (x.wide) copy_units<uint4>(src, dst, from, x.units, (uint32_t)x.lanes);
         else copy_units<uint32_t>(src, dst, from, x.units, (uint32_t)x.lanes);
@@ -315,23 +320,6 @@ __global__ void __launch_bounds__(kGatherThreads) gather_blocks_kernel(const __g
 }
 
 }  // namespace
-
-// Launch as a programmatic dependent of the work before it on the stream: the kernel waits for it at entry.
-template <typename... Params, typename... Args>
-static qsa_status launch_dependent(const char *what, void (*kern)(Params...), int grid, int threads, size_t smem,
-                                   cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return check_cuda(cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...), what);
-}
 
 // Up to this many entries every CTA scans them all, two per thread.  Scan / cluster, us, 8,125 blocks: 3.7 / 4.9 at
 // 256 entries, 5.0 / 6.1 at 1,024, 6.8 / 6.1 at 2,048, 17.5 / 6.6 at 8,192; 2,048 blocks: 3.6 / 3.6, 4.8 / 4.4,
@@ -384,12 +372,13 @@ qsa_status launch_evict_plan(const EvictPlanArgs &a, cudaStream_t s) {
     return run(evict_plan_long_kernel, kPlanThreads);
 }
 
-qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, int n_keep,
-                                uint32_t *flags, cudaStream_t s) {
+qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, const int32_t *to,
+                                int n_keep, uint32_t *flags, cudaStream_t s) {
     GatherParams p{};
     p.n_arrays = n_arrays;
     p.n_keep = n_keep;
     p.keep = keep;
+    p.to = to;
     p.flags = flags;
     for (int i = 0; i < n_arrays; ++i) {
         const qsa_block_array &x = arrays[i];

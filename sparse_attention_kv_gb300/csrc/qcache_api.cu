@@ -276,7 +276,7 @@ qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const 
         if (overlap(arrays[i].dst, (size_t)arrays[i].n_rows * arrays[i].dst_blocks * arrays[i].block_bytes, keep,
                     (size_t)n_keep * sizeof(int32_t)))
             return fail(QSA_ERR_INVALID_ARG, "array %d: dst overlaps keep", i);
-    return launch_gather_blocks(arrays, n_arrays, keep, n_keep, flags_of(ws), static_cast<cudaStream_t>(stream));
+    return launch_gather_blocks(arrays, n_arrays, keep, nullptr, n_keep, flags_of(ws), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -215,7 +215,74 @@ struct EvictPlanArgs {
     uint32_t *flags;
 };
 qsa_status launch_evict_plan(const EvictPlanArgs &a, cudaStream_t s);
-qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, int n_keep,
-                                uint32_t *flags, cudaStream_t s);
+// to == nullptr: record i goes to place i, else to to[i]
+qsa_status launch_gather_blocks(const qsa_block_array *arrays, int n_arrays, const int32_t *keep, const int32_t *to,
+                                int n_keep, uint32_t *flags, cudaStream_t s);
+
+// The paged 16-bit cache: tables of pages, their lengths and references.
+struct PageTable {
+    int32_t *table;
+    int64_t stride;
+    int max_pages;
+    int n_rows;
+    int n_pages;
+    uint32_t *flags;
+};
+// Workspace of reserve and compact, in 32-bit words behind the first 256 bytes.
+struct PagesWs {
+    int32_t *need;    // [2 n_rows] reserve: pages a row asks for; those that it and the rows before it ask for
+    int32_t *list;    // [n_pages]  reserve: free pages in order; compact: where a page goes
+    int32_t *live;    // [1]        compact: number of live pages
+};
+qsa_status launch_pages_fork(const PageTable &t, int32_t *n_tokens, int32_t *refs, const int32_t *src, const int32_t *dst,
+                             int n, cudaStream_t s);
+qsa_status launch_pages_release(const PageTable &t, int32_t *n_tokens, int32_t *refs, const int32_t *keep, cudaStream_t s);
+qsa_status launch_pages_reserve(const PageTable &t, const int32_t *n_tokens, int32_t *refs, const int32_t *add,
+                                int32_t *new_tokens, int32_t *copy_src, int32_t *copy_dst, const PagesWs &ws,
+                                cudaStream_t s);
+qsa_status launch_pages_compact(const PageTable &t, const int32_t *refs, int32_t *table_out, int32_t *refs_out,
+                                int32_t *copy_src, int32_t *copy_dst, const PagesWs &ws, cudaStream_t s);
+
+// Rows of 128 16-bit values, addressed by token and head strides in elements.
+struct Rows16 {
+    const void *p;
+    int64_t token, head;
+};
+struct PagesAppendArgs {
+    Rows16 k, v;
+    int n_source;
+    const int32_t *rows;   // or null
+    int n;
+    const int32_t *cu_rows, *first;
+    int n_kv_heads;
+    void *kcache, *vcache_t;
+};
+qsa_status launch_pages_append(const PageTable &t, const PagesAppendArgs &a, cudaStream_t s);
+
+// Dense attention: causal over packed rows, or a tree of drafts over pages.
+struct DenseArgs {
+    qsa_dtype dt;          // QSA_BF16 or QSA_F16
+    Rows16 q, k, v;
+    const int32_t *cu_q;
+    const int32_t *cu_k;   // prompts
+    int n_seqs;
+    int total_q, total_k;
+    int n_heads, n_kv_heads;
+    float scale;
+    void *out;
+    qsa_dtype out_dt;      // QSA_F32 or dt
+    float *lse;            // or null
+    // trees
+    const int32_t *parents;
+    int max_nodes;
+    const void *kcache, *vcache_t;
+    PageTable table;
+    const int32_t *n_tokens;
+    void *ws;
+    uint32_t *flags;
+};
+qsa_status launch_prompt_attention(const DenseArgs &a, cudaStream_t s);
+qsa_status launch_tree_attention(const DenseArgs &a, cudaStream_t s);
+size_t attention_ws_bytes(int rows, int n_heads, int n_kv_heads);
 
 }  // namespace qsa

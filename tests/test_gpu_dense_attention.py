@@ -1,0 +1,299 @@
+"""Prompt attention and tree attention on the GPU against their definition in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from oracle import paged  # noqa: E402
+from sparse_attention_kv_gb300 import qsa  # noqa: E402
+
+from .paged_cases import check_attention, cu, i32, normal, random_parents, random_pool, random_table  # noqa: E402
+
+BF16, F16 = torch.bfloat16, torch.float16
+SCALE = 128 ** -0.5
+
+
+def _prompt(q, k, v, lq, lk, out_dt=None, lse=True, scale=None, ws=None, cu_q=None, cu_k=None):
+    out = torch.full(q.shape, float("nan"), dtype=out_dt or q.dtype, device="cuda")
+    ls = torch.full(q.shape[:2], float("nan"), device="cuda") if lse else None
+    ws = qsa.alloc_attention_workspace(max(1, q.shape[0]), q.shape[1], k.shape[1]) if ws is None else ws
+    qsa.prompt_attention(q, k, v, i32(cu(lq)) if cu_q is None else cu_q, i32(cu(lk)) if cu_k is None else cu_k, out, ls, ws=ws,
+                         scale=scale)
+    return out, ls, ws
+
+
+def _check_prompt(lq, lk, kv, group, dt, seed=1, **kw):
+    q, k, v = (normal(seed + i, n, h, 128, dt=dt, mean=m) for i, (n, h, m) in
+               enumerate(((sum(lq), kv * group, 0.0), (sum(lk), kv, 0.0), (sum(lk), kv, 0.25))))
+    out, lse, ws = _prompt(q, k, v, lq, lk, **kw)
+    want = paged.prompt(q.double(), k.double(), v.double(), lq, lk, kw.get("scale") or SCALE)
+    check_attention(out, lse, want, dt)
+    assert qsa.read_flags(ws) == 0
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("kv,group", [(4, 16), (2, 7), (1, 1), (3, 2), (1, 16)])
+@pytest.mark.parametrize("lq,lk", [([1], [1]), ([5], [5]), ([64], [64]), ([65, 1, 130], [65, 1, 130]), ([300, 17], [300, 17]),
+                                   ([3], [500]), ([128, 129], [1000, 129])])
+def test_prompt_matches_the_definition(lq, lk, kv, group, dt):
+    _check_prompt(lq, lk, kv, group, dt)
+
+
+@pytest.mark.parametrize("lq,lk", [([1021, 333, 1, 777], [1021, 850, 2001, 840]), ([2500], [2500]), ([16, 4000], [16, 4000]),
+                                   ([1] * 40, list(range(1, 400, 10))), ([7], [9001])])
+@pytest.mark.parametrize("kv,group,dt", [(2, 7, F16), (1, 16, BF16), (2, 1, BF16)])
+def test_prompt_longer_and_ragged(lq, lk, kv, group, dt):
+    _check_prompt(lq, lk, kv, group, dt, seed=11)
+
+
+def test_prompt_rows_without_keys_are_zero():
+    """More queries than keys, and no keys at all: the first rows see nothing."""
+    lq, lk = [200, 3, 5, 1], [70, 3, 0, 1]
+    _check_prompt(lq, lk, 2, 4, BF16, seed=3)
+    q, k, v = normal(1, 4, 8, 128, dt=F16), *(torch.empty(0, 2, 128, dtype=F16, device="cuda") for _ in "kv")
+    out, lse, ws = _prompt(q, k, v, [4], [0])
+    assert (out == 0).all() and torch.isneginf(lse).all() and qsa.read_flags(ws) == 0
+
+
+def test_prompt_fp32_output_no_lse_and_scale():
+    _check_prompt([130, 9], [140, 9], 2, 3, F16, out_dt=torch.float32)
+    _check_prompt([130, 9], [140, 9], 2, 3, BF16, out_dt=torch.float32, lse=False, scale=0.3)
+    _check_prompt([130, 9], [140, 9], 2, 3, BF16, scale=2.0)
+
+
+def test_prompt_strided_inputs():
+    """Slices of a fused projection, head-major tensors, a broadcast query row."""
+    row = normal(5, 150, 20 + 2 * 4, 128, dt=BF16)
+    q, k, v = row[:, :20], row[:, 20:24], row[:, 24:]
+    want = paged.prompt(q.double(), k.double(), v.double(), [100, 50], [100, 50], SCALE)
+    out, lse, _ = _prompt(q, k, v, [100, 50], [100, 50])
+    check_attention(out, lse, want, BF16)
+    qh, kh, vh = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v))   # head-major
+    again, lse2, _ = _prompt(qh, kh, vh, [100, 50], [100, 50])
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    one = q[:1].expand(150, -1, -1)
+    out, lse, _ = _prompt(one, k, v, [100, 50], [100, 50])
+    want = paged.prompt(one.double(), k.double(), v.double(), [100, 50], [100, 50], SCALE)
+    check_attention(out, lse, want, BF16)
+
+
+@pytest.mark.parametrize("group", [1, 7, 16])
+def test_prompt_unseen_rows_do_not_touch_it(group):
+    """NaN and infinities in keys and values that no query, or only later queries, see."""
+    lq, lk, kv = [70, 130], [70, 300], 2
+    q, k, v = normal(1, 210, kv * group, 128, dt=BF16), normal(2, 380, kv, 128, dt=BF16), normal(3, 380, kv, 128, dt=BF16)
+    good, lse, _ = _prompt(q, k, v, lq, lk)
+    cq, ck = [5, 75, 205], [5, 75, 375]          # rows before the first and behind the last sequence
+    qq = torch.cat((normal(4, 5, kv * group, 128, dt=BF16), q[:200], normal(5, 5, kv * group, 128, dt=BF16)))
+    kk, vv = (torch.full((380, kv, 128), float("nan"), dtype=BF16, device="cuda") for _ in "kv")
+    kk[5:375], vv[5:375] = k[:370], v[:370]
+    vv[375:] = float("inf")
+    out, ls, ws = _prompt(qq, kk, vv, None, None, cu_q=i32(cq), cu_k=i32(ck))
+    assert torch.equal(out[5:205], good[:200]) and torch.equal(ls[5:205], lse[:200])
+    assert torch.isnan(out[:5]).all() and torch.isnan(out[205:]).all() and torch.isnan(ls[:5]).all()   # left as they were
+    assert qsa.read_flags(ws) == 0
+    # keys of the second sequence's last tokens: only the queries at and behind them change
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        k2, v2 = k.clone(), v.clone()
+        k2[70 + 290] = bad
+        v2[70 + 280, :, 5] = bad                 # seen by queries 110 ..
+        out, ls, _ = _prompt(q, k2, v2, lq, lk)
+        assert torch.equal(out[:70 + 110], good[:70 + 110]) and torch.equal(ls[:70 + 110], lse[:70 + 110])
+        mid = out[70 + 110:70 + 120]             # the value's dimension, and no other
+        assert not torch.isfinite(mid[..., 5]).any()
+        if not math.isnan(bad):
+            assert (mid[..., 5] == bad).all()
+        keep = [d for d in range(128) if d != 5]
+        assert torch.equal(mid[..., keep], good[70 + 110:70 + 120][..., keep])
+        if math.isnan(bad):
+            assert torch.isnan(out[70 + 120:]).all() and torch.isnan(ls[70 + 120:]).all()
+
+
+def test_prompt_bad_ranges_are_flagged():
+    q, k, v = normal(1, 40, 4, 128, dt=BF16), normal(2, 40, 2, 128, dt=BF16), normal(3, 40, 2, 128, dt=BF16)
+    good, lse, _ = _prompt(q, k, v, [40], [40])
+    out, ls, ws = _prompt(q, k, v, None, None, cu_q=i32([0, 99]), cu_k=i32([-3, 40]))
+    assert torch.equal(out, good) and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+    out, ls, ws = _prompt(q, k, v, None, None, cu_q=i32([0, 40, 7]), cu_k=i32([0, 40, 40]))
+    assert torch.equal(out, good) and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+
+
+def test_prompt_large_logits_and_late_rises():
+    """Logits in the hundreds, and a maximum that rises in every tile."""
+    for dt in (BF16, F16):
+        q, k, v = normal(1, 600, 4, 128, dt=dt), normal(2, 600, 2, 128, dt=dt), normal(3, 600, 2, 128, dt=dt)
+        rise = torch.linspace(0.1, 6.0, 600, device="cuda")[:, None, None]
+        k2 = (k.float() * rise).to(dt)
+        out, lse, _ = _prompt(q, k2, v, [600], [600])
+        check_attention(out, lse, paged.prompt(q.double(), k2.double(), v.double(), [600], [600], SCALE), dt)
+        k2[:, :, :] = (q[:, :1] * rise).to(dt)      # aligned keys: each later key dominates by far
+        out, lse, _ = _prompt(q, k2, v, [600], [600])
+        check_attention(out, lse, paged.prompt(q.double(), k2.double(), v.double(), [600], [600], SCALE), dt)
+
+
+def test_prompt_is_the_same_every_time_and_in_any_batch():
+    q, k, v = normal(1, 900, 8, 128, dt=BF16), normal(2, 900, 2, 128, dt=BF16), normal(3, 900, 2, 128, dt=BF16)
+    ws = qsa.alloc_attention_workspace(900, 8, 2)
+    first, l1, _ = _prompt(q, k, v, [500, 400], [500, 400], ws=ws)
+    for _ in range(3):
+        out, ls, _ = _prompt(q, k, v, [500, 400], [500, 400], ws=ws)
+        assert torch.equal(out, first) and torch.equal(ls, l1)
+
+
+# ------------------------------------------------------------------ trees
+
+def _tree_inputs(seed, n_tokens, nodes, kv, group, dt, spare=3):
+    total = sum(nodes)
+    q, k, v = normal(seed, total, kv * group, 128, dt=dt), normal(seed + 1, total, kv, 128, dt=dt), \
+        normal(seed + 2, total, kv, 128, dt=dt, mean=0.25)
+    pages = sum((n + 63) // 64 for n in n_tokens) + spare
+    kc, vc = random_pool(seed + 3, kv, pages, dt)
+    width = max((n + 63) // 64 for n in n_tokens) + 2
+    return q, k, v, random_parents(seed, nodes), kc, vc, random_table(seed, n_tokens, pages, width)
+
+
+def _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens, out_dt=None, max_nodes=None, lse=True, scale=None):
+    out = torch.full(q.shape, float("nan"), dtype=out_dt or q.dtype, device="cuda")
+    ls = torch.full(q.shape[:2], float("nan"), device="cuda") if lse else None
+    ws = qsa.alloc_attention_workspace(q.shape[0], q.shape[1], k.shape[1])
+    qsa.tree_attention(q, k, v, i32(parents), i32(cu(nodes)), max_nodes or max(nodes), kc, vc, i32(table), i32(n_tokens), out, ls,
+                       ws=ws, scale=scale)
+    return out, ls, ws
+
+
+def _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens, scale=SCALE):
+    return paged.tree(q.double(), k.double(), v.double(), parents, nodes, kc.double(), vc.double(), table, n_tokens, scale)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("kv,group", [(4, 16), (2, 7), (1, 1), (2, 8)])
+@pytest.mark.parametrize("n_tokens,nodes", [([0], [1]), ([1], [1]), ([63, 64, 65], [3, 1, 2]), ([500], [64]), ([0, 130, 1000], [5, 17, 33]),
+                                            ([128], [16]), ([2000, 7], [1, 1])])
+def test_tree_matches_the_definition(n_tokens, nodes, kv, group, dt):
+    x = _tree_inputs(7, n_tokens, nodes, kv, group, dt)
+    q, k, v, parents, kc, vc, table = x
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens), dt)
+    assert qsa.read_flags(ws) == 0
+
+
+@pytest.mark.parametrize("n_tokens,nodes,kv,group,dt", [
+    ([9000], [1], 4, 16, BF16), ([12_345, 3, 700], [9, 64, 30], 2, 16, F16), ([100 * i for i in range(50)], [1 + i % 8 for i in range(50)], 2, 8, BF16),
+    ([5000, 5000], [64, 64], 1, 16, BF16), ([3001], [61], 1, 13, F16)])
+def test_tree_longer_and_ragged(n_tokens, nodes, kv, group, dt):
+    q, k, v, parents, kc, vc, table = _tree_inputs(17, n_tokens, nodes, kv, group, dt)
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens), dt)
+    assert qsa.read_flags(ws) == 0
+
+
+def test_tree_empty_trees_fp32_output_and_a_loose_bound():
+    n_tokens, nodes = [100, 50, 0, 300], [0, 4, 0, 2]
+    q, k, v, parents, kc, vc, table = _tree_inputs(23, n_tokens, nodes, 2, 4, F16)
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens, out_dt=torch.float32, max_nodes=64, scale=0.2)
+    check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens, 0.2), F16)
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens, lse=False)
+    check_attention(out, None, _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens), F16)
+
+
+@pytest.mark.parametrize("group", [1, 16])
+def test_tree_unseen_rows_do_not_touch_it(group):
+    """Page places behind the tokens, pages of others, and nodes that are no ancestors hold NaN or infinities."""
+    n_tokens, nodes, kv = [100, 250], [6, 5], 2
+    q, k, v, _, kc, vc, table = _tree_inputs(29, n_tokens, nodes, kv, group, BF16)
+    parents = [-1, 0, 0, 1, 1, 2, -1, 0, 1, 2, 3]
+    good, lse, _ = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    for bad in (float("nan"), float("inf")):
+        kc2, vc2 = torch.full_like(kc, bad), torch.full_like(vc, bad)
+        for s, n in enumerate(n_tokens):
+            for t in range(n):
+                p = table[s][t // 64]
+                kc2[:, 64 * p + t % 64], vc2[:, p, :, t % 64] = kc[:, 64 * p + t % 64], vc[:, p, :, t % 64]
+        out, ls, ws = _tree(q, k, v, parents, nodes, kc2, vc2, table, n_tokens)
+        assert torch.equal(out, good) and torch.equal(ls, lse) and qsa.read_flags(ws) == 0
+        v2, k2 = v.clone(), k.clone()
+        v2[2, :, 9] = bad          # node 2: its child 5 sees it, the others do not
+        k2[4] = bad                # node 4: nobody but itself
+        out, ls, _ = _tree(q, k2, v2, parents, nodes, kc, vc, table, n_tokens)
+        for i in (0, 1, 3, 6, 7, 8, 9, 10):
+            assert torch.equal(out[i], good[i]) and torch.equal(ls[i], lse[i])
+        for i in (2, 5):
+            assert not torch.isfinite(out[i, :, 9]).any()
+            keep = [d for d in range(128) if d != 9]
+            assert torch.equal(out[i][:, keep], good[i][:, keep])
+        if math.isnan(bad):
+            assert torch.isnan(out[4]).all()
+
+
+def test_tree_bad_pages_parents_and_lengths_are_flagged():
+    n_tokens, nodes, kv, group = [200, 300], [4, 3], 2, 4
+    q, k, v, parents, kc, vc, table = _tree_inputs(31, n_tokens, nodes, kv, group, BF16)
+    for bad in (-1, len(vc[0]), 2 ** 31 - 1, -2 ** 31):
+        t2 = [list(r) for r in table]
+        t2[0][1] = bad
+        out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, t2, n_tokens)
+        check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, t2, n_tokens), BF16)
+        assert qsa.read_flags(ws) == qsa.FLAG_BAD_ID
+    p2 = list(parents)
+    p2[2], p2[5] = 2, 64
+    out, lse, ws = _tree(q, k, v, p2, nodes, kc, vc, table, n_tokens)
+    check_attention(out, lse, _want_tree(q, k, v, p2, nodes, kc, vc, table, n_tokens), BF16)
+    assert qsa.read_flags(ws) == qsa.FLAG_BAD_ID
+    good, _, _ = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens, max_nodes=3)
+    assert torch.equal(out[:3], good[:3]) and torch.isnan(out[3]).all() and torch.equal(out[4:], good[4:])
+    assert qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+    wide = 64 * len(table[0])
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, [-5, wide + 1])   # as 0 and the row's width
+    assert qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED | qsa.FLAG_BAD_ID
+    check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, table, [0, wide]), BF16)
+
+
+def test_tree_of_one_node_is_the_last_row_of_a_prompt():
+    """A decode step over pages against prompt attention with all the keys in rows."""
+    n = 777
+    q, k, v, parents, kc, vc, table = _tree_inputs(37, [n], [1], 2, 8, BF16)
+    out, lse, _ = _tree(q, k, v, parents, [1], kc, vc, table, [n])
+    pk, pv, _ = paged.paged_rows(kc, vc, table[0], n)
+    out2, lse2, _ = _prompt(q, torch.cat((pk, k)), torch.cat((pv, v)), [1], [n + 1])
+    want = _want_tree(q, k, v, parents, [1], kc, vc, table, [n])
+    check_attention(out, lse, want, BF16)
+    check_attention(out2, lse2, want, BF16)
+
+
+def test_captured_calls_follow_their_inputs():
+    """Captured once, replayed on new lengths, tables and values; on a stream of its own."""
+    n_tokens, nodes, kv, group = [300, 90], [4, 3], 2, 8
+    q, k, v, parents, kc, vc, table = _tree_inputs(41, n_tokens, nodes, kv, group, BF16)
+    ws = qsa.alloc_attention_workspace(7, kv * group, kv)
+    d = dict(parents=i32(parents), cu_nodes=i32(cu(nodes)), table=i32(table), n_tokens=i32(n_tokens))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    pout, plse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    cq, ck = i32([0, 4, 7]), i32([0, 4, 7])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        def step():
+            qsa.tree_attention(q, k, v, d["parents"], d["cu_nodes"], 64, kc, vc, d["table"], d["n_tokens"], out, lse, ws=ws)
+            qsa.prompt_attention(q, k, v, cq, ck, pout, plse, ws=ws)
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step()
+        for turn in range(3):
+            nt, nn = ([300, 90], [64 + turn, 1])[turn % 2], ([4, 3], [2, 5])[turn % 2]
+            par = random_parents(turn, nn)
+            q.copy_(normal(50 + turn, *q.shape, dt=BF16))
+            d["n_tokens"].copy_(i32(nt)), d["cu_nodes"].copy_(i32(cu(nn))), d["parents"].copy_(i32(par))
+            ck.copy_(i32(cu(nn))), cq.copy_(i32(cu(nn)))
+            g.replay()
+            side.synchronize()
+            check_attention(out, lse, _want_tree(q, k, v, par, nn, kc, vc, table, nt), BF16)
+            check_attention(pout, plse, paged.prompt(q.double(), k.double(), v.double(), nn, nn, SCALE), BF16)
+    assert qsa.read_flags(ws, stream=side) == 0
