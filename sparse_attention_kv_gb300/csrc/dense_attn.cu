@@ -1,151 +1,1038 @@
 // dense_attn.cu -- attention of whole prompts over packed rows, and of drafted token trees over pages.
 //
-// The simplest form: a warp per (query, head).  32 keys at a time, a lane per key forms its logit; the softmax keeps a
-// running maximum and sum; then a lane per four dimensions adds the keys' values up.  It reads K and V once per head.
+//   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale (s_t - m)),  s_t = q . k_t,
+//
+// over the keys t that a row (a query token under one head) sees: causal ones of packed rows, or the pages of a
+// sequence and the row's ancestors among the drafts.  One pass over the keys, 128 a step, with a running reference m:
+//   S = Q K^T   tcgen05, M = 128 rows, N = 128 keys, into tensor memory
+//   P = exp2    one thread per row reads its 128 logits, writes the weights in 16 bits over them in tensor memory
+//   O += P V    tcgen05 with A = P from tensor memory, M = 128 rows, N = 128 dimensions
+// The rows of a tile are (token, head of the group) pairs, token-major, so every group size fills it, all rows of a
+// tile share one KV head's K and V, and a tile of 256 rows spans few tokens (16 at groups of 16): little of a causal
+// tile is masked, and one token's 16 heads already read a page once.  A CTA works on two streams of 128 rows in turn (the
+// tensor cores multiply for one while the other's softmax runs), which take the same K and V from shared memory.  m
+// moves only when a row's maximum has risen by more than 2^8 of weight (then l and O are scaled in place), since
+// any reference gives the same quotient: sums stay below 2^8 x keys, weights keep their relative precision.
+//
+// Work: every (sequence, KV head, tile) is a run of steps; the CTAs of a persistent grid take equal shares of all runs laid
+// end to end, so one long context fills the GPU as well as many short ones.  A run that crosses a border is
+// joined by combine_kernel from the CTAs' partial (O, m, l).
+//
+// Roles: warps 0-3 and 4-7 softmax and epilogue of a stream, warp 8 TMA (a ring of 32 KB slots, K and V in turn), warp 9
+// the MMAs.  V of packed rows is an MN-major operand, V of a page a K-major one (its dimension comes before its token).
+// Values at places that a row does not see must not reach it as 0 x NaN: in steps that hold such places one stream's
+// warps clear what lies past the last row's view and any value that is not finite; the latter is added to the
+// rows that do see it at the end.
+//
+// Every wait is bounded; on expiry the CTA raises QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees its tensor memory and exits.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <mutex>
 
 #include "launch.h"
 #include "qsa_device.cuh"
 #include "qsa_internal.h"
+#include "tc_ptx_tmem.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 320;
+constexpr int kRows = 128;            // rows of a stream (TMEM lanes)
+constexpr int kKeys = 128;            // keys of a step
+constexpr int kTileRows = 2 * kRows;
+constexpr int kSlots = 5;
+constexpr int kSlotBytes = kKeys * 128 * 2;
+constexpr int kQBytes = kRows * 128 * 2;
+constexpr int kInfo = 8;              // steps whose page limits are held: more than the ring holds
+constexpr int kMaxCtas = 152;
+constexpr int kWhole = 4;             // runs of so few steps are not split
+constexpr int kMinShare = 4;          // fewest steps (and run beginnings) a CTA is started for
+constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
+constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+struct Params {
+    Rows16 q, v;
+    const int32_t *cu_q, *cu_k;
+    int n_seqs, total_q, total_k;
+    int n_heads, n_kv, group;
+    float scale, scale_log2;
+    void *out;
+    int out_f32;
+    float *lse;
+    const int32_t *parents;
+    int max_nodes;
+    const int32_t *table;
+    int64_t table_stride;
+    int max_pages, n_pages;
+    const int32_t *n_tokens;
+    int row_tiles;        // trees: CTAs side by side that take a tile of rows each
+    int shares;           // CTAs (or groups of row_tiles) that take a share
+    int rows_cap;         // rows of a partial
+    float4 *part;         // [grid][2][32][rows_cap]: O, four dimensions of a row at a time
+    float2 *ml;           // [grid][2][rows_cap]: (m scale log2 e, l)
+    int4 *desc;           // [grid][2]: see describe()
+    uint32_t *flags;
+};
 
-template <typename T, bool TREE>
-__global__ void __launch_bounds__(32 * kWarps) dense_kernel(DenseArgs a) {
-    __shared__ float qs[kWarps][128];
-    wait_prior_grid();
-    const int s = blockIdx.x, h = blockIdx.y, g = h / (a.n_heads / a.n_kv_heads);
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    auto range = [&](const int32_t *cu, int most, int &c0, int &c1) {
-        c0 = cu[s];
-        c1 = cu[s + 1];
-        if ((c0 < 0 || c1 < c0 || c1 > most) && threadIdx.x == 0) atomicOr(a.flags, QSA_FLAG_NBLOCKS_CLAMPED);
-        c0 = min(max(c0, 0), most);
-        c1 = min(max(c1, c0), most);
-    };
-    int q0, q1, k0 = 0, k1 = 0;
-    range(a.cu_q, a.total_q, q0, q1);
-    int past = 0;
-    const int32_t *table = nullptr;
-    if constexpr (TREE) {
-        if (q1 - q0 > a.max_nodes) {
-            q1 = q0 + a.max_nodes;
-            if (threadIdx.x == 0) atomicOr(a.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+struct Ctrl {
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t qready[2], sfull[2], pready[2], ofull[2];
+    uint64_t drain;
+    long long x0, x1, at;   // this CTA's share and the beginning of the run it starts in
+    int s, g, t;            // that run
+    uint32_t tmem;
+    int abort;
+    int bad[2];             // number + 1 of the last piece in which a value was not finite, by its parity
+    int info[kInfo][2];     // valid tokens in each page of a step
+};
+constexpr int kOffQ = 0;
+constexpr int kOffRing = 2 * kQBytes;
+constexpr int kOffCtrl = kOffRing + kSlots * kSlotBytes;
+constexpr int kSmem = 1024 + kOffCtrl + (int)sizeof(Ctrl);
+static_assert(kSmem <= 232448, "shared memory");
+
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = now_ns();
+    while (true) {
+        if (__all_sync(~0u, mbar_try_wait_sleep(bar, parity))) return true;
+        if (__any_sync(~0u, *abort_flag != 0)) return false;
+        if (__any_sync(~0u, now_ns() - t0 > kWaitNs)) {
+            *abort_flag = 1;
+            return false;
         }
-        past = a.n_tokens[s];
-        const int most = 64 * a.table.max_pages;
-        if ((past < 0 || past > most) && threadIdx.x == 0) atomicOr(a.flags, QSA_FLAG_NBLOCKS_CLAMPED);
-        past = min(max(past, 0), most);
-        table = a.table.table + (size_t)s * a.table.stride;
-    } else {
-        range(a.cu_k, a.total_k, k0, k1);
     }
-    const T *K = static_cast<const T *>(a.k.p) + g * a.k.head, *V = static_cast<const T *>(a.v.p) + g * a.v.head;
-    const T *KC = static_cast<const T *>(a.kcache), *VC = static_cast<const T *>(a.vcache_t);
-    for (int row = q0 + blockIdx.z * kWarps + wid; row < q1; row += gridDim.z * kWarps) {
-        const int i = row - q0;
-        unsigned long long sees = 0ull;
-        int seen = 0;
+}
+
+// ------------------------------------------------------------------ the runs and the shares
+
+template <bool TREE>
+struct Seq {
+    int q0, lq, k0, lk, tiles;   // trees: lk = tokens in the pages
+    long long e;                 // see cum()
+
+    __device__ __forceinline__ void load(const Params &p, int s, bool tell) {
+        range(p, p.cu_q, s, p.total_q, tell, q0, lq);
         if constexpr (TREE) {
-            for (int n = i; n >= 0;) {
-                sees |= 1ull << n;
-                int p = a.parents[q0 + n];
-                if (p < -1 || p >= n) {
-                    p = -1;
-                    if (lane == 0) atomicOr(a.flags, QSA_FLAG_BAD_ID);
-                }
-                n = p;
+            if (lq > p.max_nodes) {
+                lq = p.max_nodes;
+                if (tell) atomicOr(p.flags, QSA_FLAG_NBLOCKS_CLAMPED);
             }
-            seen = past + i + 1;
+            const int n = p.n_tokens[s], most = 64 * p.max_pages;
+            lk = min(max(n, 0), most);
+            if (tell && lk != n) atomicOr(p.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+            k0 = 0;
+            tiles = lq > 0 ? 1 : 0;   // each CTA of a group has its own tile of rows
         } else {
-            seen = max(0, (k1 - k0) - (q1 - q0) + i + 1);
+            range(p, p.cu_k, s, p.total_k, tell, k0, lk);
+            const long long rows = (long long)lq * p.group;
+            tiles = (int)((rows + kTileRows - 1) / kTileRows);
+            const long long c = kTileRows - 1 + (long long)p.group * (lk - lq + kKeys);
+            e = c >= 0 ? c / kKeys : -((-c + kKeys - 1) / kKeys);
         }
-        const T *q = static_cast<const T *>(a.q.p) + (int64_t)row * a.q.token + (int64_t)h * a.q.head;
-        __syncwarp();
-        for (int d = lane; d < 128; d += 32) qs[wid][d] = to_f32(q[d]);
-        __syncwarp();
-        float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int t0 = 0; t0 < seen; t0 += 32) {
-            const int t = t0 + lane;
-            // where key t lies: row of K and V, or page and place
-            bool ok = t < seen;
-            int page = -1;
-            if (TREE && ok) {
-                if (t < past) {
-                    page = table[t >> 6];
-                    if (page < 0 || page >= a.table.n_pages) {
-                        ok = false;
-                        atomicOr(a.flags, QSA_FLAG_BAD_ID);
-                    }
-                } else {
-                    ok = sees >> (t - past) & 1ull;
-                }
-            }
-            float x = -INFINITY;
-            if (ok) {
-                const T *kr = page >= 0 ? KC + (((size_t)g * a.table.n_pages + page) * 64 + (t & 63)) * 128
-                                        : K + (int64_t)(TREE ? q0 + t - past : k0 + t) * a.k.token;
-                float dot = 0.0f;
-                for (int d = 0; d < 128; ++d) dot += qs[wid][d] * to_f32(kr[d]);
-                x = dot * a.scale;
-            }
-            float top = x;
-            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            const float m1 = fmaxf(m, top), ref = m1 == -INFINITY ? 0.0f : m1;
-            const float turn = expf(m - ref), p = expf(x - ref);
-            float sum = ok ? p : 0.0f;
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-            l = l * turn + sum;
-            m = m1;
-            for (int e = 0; e < 4; ++e) o[e] *= turn;
-            for (int j = 0; j < 32 && t0 + j < seen; ++j) {
-                const float w = __shfl_sync(~0u, p, j);
-                const bool use = __shfl_sync(~0u, ok ? 1 : 0, j);
-                const int pg = __shfl_sync(~0u, page, j), tj = t0 + j;
-                if (!use) continue;
-                for (int e = 0; e < 4; ++e) {
-                    const int d = lane * 4 + e;
-                    const T v = pg >= 0 ? VC[(((size_t)g * a.table.n_pages + pg) * 128 + d) * 64 + (tj & 63)]
-                                        : V[(int64_t)(TREE ? q0 + tj - past : k0 + tj) * a.v.token + d];
-                    o[e] += w * to_f32(v);
-                }
-            }
-        }
-        const size_t at = (size_t)row * a.n_heads + h;
-        for (int e = 0; e < 4; ++e) {
-            const float x = m == -INFINITY && l == 0.0f ? 0.0f : o[e] / l;
-            const size_t to = at * 128 + lane * 4 + e;
-            if (a.out_dt == QSA_F32) static_cast<float *>(a.out)[to] = x;
-            else if (a.out_dt == QSA_BF16) static_cast<__nv_bfloat16 *>(a.out)[to] = __float2bfloat16(x);
-            else static_cast<__half *>(a.out)[to] = __float2half(x);
-        }
-        if (lane == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : m + logf(l);
     }
+    static __device__ __forceinline__ void range(const Params &p, const int32_t *cu, int s, int most, bool tell, int &c0,
+                                                 int &len) {
+        const int a = cu[s], b = cu[s + 1];
+        if (tell && (a < 0 || b < a || b > most)) atomicOr(p.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+        c0 = min(max(a, 0), most);
+        len = min(max(b, c0), most) - c0;
+    }
+    // Keys that row r of the sequence's rows sees.
+    __device__ __forceinline__ int limit(const Params &p, int r) const {
+        return min(max(lk - lq + r / p.group + 1, 0), lk);
+    }
+    __device__ __forceinline__ int steps(const Params &p, int t) const {
+        if constexpr (TREE) return (lk + kKeys - 1) / kKeys + 1;   // the pages, then the drafts
+        const long long rows = (long long)lq * p.group, end = (long long)(t + 1) * kTileRows;
+        return (limit(p, (int)((end < rows ? end : rows) - 1)) + kKeys - 1) / kKeys;
+    }
+    // Lengths of the runs of tiles 0 .. T - 1, each its steps and one more for its beginning and end.  A full
+    // tile t has max(0, floor((2 t + e) / G)) steps: its last row is row 256 t + 255, whose limit is lk - lq +
+    // floor((256 t + 255) / G) + 1, and floors nest.  The last tile ends at lk.
+    __device__ __forceinline__ long long cum(const Params &p, int T) const {
+        if constexpr (TREE) return T ? steps(p, 0) + 1 : 0;
+        long long sum = T;
+        if (T == tiles && T > 0) {
+            sum += (max(lk, 0) + kKeys - 1) / kKeys;
+            --T;
+        }
+        const long long t0 = e < 0 ? (-e + 1) / 2 : 0;
+        const long long U = T - t0;
+        if (U <= 0) return sum;
+        const int G = p.group;
+        const long long e1 = e + 2 * t0, q = e1 / G;
+        const int rem = (int)(e1 - q * G), a = (G - rem + 1) / 2, b = (2 * G - rem + 1) / 2;
+        const long long A = U / G;
+        const int m = (int)(U - A * G);
+        const long long per = max(0, G - a) + max(0, G - b), rest = max(0, m - a) + max(0, m - b);
+        return sum + U * q + G * A * (A - 1) + A * per + 2 * A * m + rest;
+    }
+};
+
+struct Piece {
+    int s, g;
+    int q0, lq, k0, lk;
+    int row0, rows;       // rows of the sequence, of this tile
+    int s0, s1, n;        // steps of this piece, of the run
+    int e[2];             // where each stream's steps end (<= s1; s0: none)
+};
+
+// A CTA's pieces one after another; every role walks by itself.
+template <bool TREE>
+struct Walk {
+    Seq<TREE> q;
+    long long at, x0, x1;
+    int s, g, t, tile;
+
+    __device__ __forceinline__ Walk(const Params &p, const Ctrl &c) {
+        x0 = c.x0;
+        x1 = c.x1;
+        at = c.at;
+        s = c.s;
+        g = c.g;
+        t = c.t;
+        tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
+        if (at < x1 && s < p.n_seqs) q.load(p, s, false);
+    }
+    __device__ __forceinline__ bool next(const Params &p, Piece &pc) {
+        while (at < x1 && s < p.n_seqs) {
+            const int n = q.steps(p, t);
+            const long long from = at;
+            int s0 = 0, s1 = n;
+            bool take = from >= x0;
+            if (n > kWhole) {
+                const long long a = x0 - from - 1, b = x1 - from - 1;
+                s0 = a > 0 ? (int)(a < n ? a : n) : 0;
+                s1 = b < n ? (int)(b > 0 ? b : 0) : n;
+                take = s1 > s0;
+            }
+            pc.s = s;
+            pc.g = g;
+            pc.q0 = q.q0;
+            pc.lq = q.lq;
+            pc.k0 = q.k0;
+            pc.lk = q.lk;
+            pc.row0 = (TREE ? tile : t) * kTileRows;
+            pc.rows = min(q.lq * p.group - pc.row0, kTileRows);
+            pc.s0 = s0;
+            pc.s1 = s1;
+            pc.n = n;
+            if (pc.rows <= 0) take = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int mine = min(pc.rows - i * kRows, kRows);
+                int end = s0;
+                if (take && mine > 0) {
+                    end = n;
+                    if constexpr (!TREE) end = (q.limit(p, pc.row0 + i * kRows + mine - 1) + kKeys - 1) / kKeys;
+                    end = max(min(end, s1), s0);
+                }
+                pc.e[i] = end;
+            }
+            at += n + 1;
+            if (++t >= q.tiles) {
+                t = 0;
+                if (++g >= p.n_kv) {
+                    g = 0;
+                    do {
+                        if (++s >= p.n_seqs) break;
+                        q.load(p, s, false);
+                    } while (q.tiles == 0);
+                }
+            }
+            if (take) return true;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    return v;
+}
+
+// This CTA's share of all runs, and the run it begins in (one warp).
+template <bool TREE>
+__device__ void find_share(const Params &p, Ctrl &c) {
+    const int lane = threadIdx.x & 31;
+    const int share = blockIdx.x / p.row_tiles;
+    const bool tell = blockIdx.x == 0;
+    Seq<TREE> q;
+    auto weight = [&](int s, bool say) -> long long {
+        if (s >= p.n_seqs) return 0;
+        q.load(p, s, say);
+        return p.n_kv * q.cum(p, q.tiles);
+    };
+    long long total = 0, first = 0;   // first: the weights of sequences 0 .. 31
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+        const long long w = weight(s0 + lane, tell);
+        if (s0 == 0) first = w;
+        total += warp_sum(w);
+    }
+    long long used = (total + kMinShare - 1) / kMinShare;
+    used = used < 1 ? 1 : used > p.shares ? p.shares : used;
+    const long long x0 = share < used ? share * total / used : total;
+    const long long x1 = share < used ? (share + 1) * total / used : total;
+    long long before = 0, at = x0;
+    int s = p.n_seqs, g = 0, t = 0;
+    for (int s0 = 0; s0 < p.n_seqs && x0 < x1; s0 += 32) {
+        const long long w = s0 == 0 ? first : weight(s0 + lane, false);
+        long long incl = w;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const long long y = __shfl_up_sync(~0u, incl, d);
+            if (lane >= d) incl += y;
+        }
+        const unsigned past = __ballot_sync(~0u, before + incl > x0);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            s = s0 + l;
+            before += __shfl_sync(~0u, incl - w, l);
+            break;
+        }
+        before += __shfl_sync(~0u, incl, 31);
+    }
+    if (s < p.n_seqs) {
+        q.load(p, s, false);
+        const long long per = q.cum(p, q.tiles);
+        g = (int)((x0 - before) / per);
+        before += g * per;
+        int lo = 0, hi = q.tiles;   // cum(lo) <= x0 - before < cum(hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, mid = min(lo + (lane + 1) * step, hi);
+            const unsigned over = __ballot_sync(~0u, q.cum(p, mid) > x0 - before);   // lane 31 reaches hi
+            const int l = __ffs(over) - 1;
+            const int new_hi = min(lo + (l + 1) * step, hi);
+            lo += l * step;
+            hi = new_hi;
+        }
+        t = lo;
+        at = before + q.cum(p, t);
+    }
+    if (lane == 0) {
+        c.x0 = x0;
+        c.x1 = x1;
+        c.at = at;
+        c.s = s;
+        c.g = g;
+        c.t = t;
+    }
+}
+
+// ------------------------------------------------------------------ arithmetic
+
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t r;
+    if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ float widen(uint32_t half) {
+    if constexpr (F16) return __half2float(__ushort_as_half((unsigned short)half));
+    else return __uint_as_float(half << 16);
+}
+// Bits of a pair of 16-bit values whose exponents are all ones: 0xFFFF where a value is not finite.
+template <bool F16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
+    constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
+    return ((pair & e) == e ? 0xFFFFu : 0u) | ((pair & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
+}
+template <bool F16>
+__device__ __forceinline__ bool any_not_finite(const uint4 &x) {
+    return (not_finite<F16>(x.x) | not_finite<F16>(x.y) | not_finite<F16>(x.z) | not_finite<F16>(x.w)) != 0u;
+}
+
+// The nodes a tree's row sees (one warp; every lane gets its own row's): bit j of the mask is node j.
+__device__ unsigned long long ancestors(const Params &p, const Piece &pc, int node) {
+    const int lane = threadIdx.x & 31;
+    unsigned long long mask[2];
+    int up[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        int a = i < pc.lq ? p.parents[pc.q0 + i] : -1;
+        if (a < -1 || a >= i) {
+            atomicOr(p.flags, QSA_FLAG_BAD_ID);
+            a = -1;
+        }
+        up[h] = a;
+        mask[h] = 1ull << i;
+    }
+    auto of = [&](const unsigned long long (&m)[2], int i) {
+        const unsigned long long a = __shfl_sync(~0u, m[0], i & 31), b = __shfl_sync(~0u, m[1], i & 31);
+        return i & 32 ? b : a;
+    };
+#pragma unroll 1
+    for (int round = 0; round < 6; ++round) {   // each node's mask covers 2^round nodes of its path
+        unsigned long long add[2];
+        int far[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = max(up[h], 0);
+            add[h] = of(mask, i);
+            const int a = __shfl_sync(~0u, up[0], i & 31), b = __shfl_sync(~0u, up[1], i & 31);
+            far[h] = i & 32 ? b : a;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (up[h] >= 0) {
+                mask[h] |= add[h];
+                up[h] = far[h];
+            }
+    }
+    return of(mask, node);
+}
+
+// ------------------------------------------------------------------ the kernel
+
+// What a CTA left in its partials.  desc[0]: (1 = the piece ends its run, 2 = it does not, 0 = none) for a piece that began
+// in an earlier CTA; desc[1]: (1, s, g, row0) for a run that begins here and does not end here.
+__device__ __forceinline__ void describe(const Params &p, const Piece &pc) {
+    int4 *d = p.desc + 2 * (size_t)blockIdx.x;
+    if (pc.s0 > 0) d[0] = make_int4(pc.s1 == pc.n ? 1 : 2, 0, 0, 0);
+    else if (pc.s1 < pc.n) d[1] = make_int4(1, pc.s, pc.g, pc.row0);
+}
+
+// Four values of a row of out, at element `at`.
+template <bool F16>
+__device__ __forceinline__ void store4(const Params &p, size_t at, float a, float b, float c, float d) {
+    if (p.out_f32) *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(a, b, c, d);
+    else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(pack16<F16>(a, b), pack16<F16>(c, d));
+}
+
+template <bool F16, bool TREE>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
+                 const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring = smem + kOffRing;
+    Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + kOffCtrl);
+    volatile int *abort_flag = &ct.abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&ct.full[i], 1);
+            mbar_init(&ct.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.qready[i], 4);   // one arrival per warp of the stream
+            mbar_init(&ct.sfull[i], 1);
+            mbar_init(&ct.pready[i], 4);
+            mbar_init(&ct.ofull[i], 1);
+            ct.bad[i] = 0;
+        }
+        mbar_init(&ct.drain, 1);
+        ct.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_prior_grid();   // nothing the caller wrote is read, and no tensor memory taken, before this
+    allow_dependent_launch();
+    if (warp == 9) {
+        tmem_alloc(&ct.tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 8) find_share<TREE>(p, ct);
+    if (tid == 0) {
+        p.desc[2 * (size_t)blockIdx.x] = make_int4(0, 0, 0, 0);
+        p.desc[2 * (size_t)blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ct.tmem;
+
+    int it = 0;   // slots of the ring used so far
+    if (warp == 8) {
+        Walk<TREE> walk(p, ct);
+        Piece pc;
+        // ---------------- copies: K and V of each step, K first
+        int step = 0;
+        bool ok = true;
+        while (ok && walk.next(p, pc)) {
+            int pages = 0, ahead = 0;   // 32 entries of the table, a lane each, and the 32 after them
+            const int nb = TREE ? (pc.lk + 63) >> 6 : 0;
+            auto entries = [&](int chunk) {
+                const int i = chunk * 32 + lane;
+                return i < nb ? p.table[(size_t)pc.s * p.table_stride + i] : -1;
+            };
+            for (int j = pc.s0; j < pc.s1; ++j, ++step) {
+                const bool paged = TREE && j < pc.n - 1;
+                int page[2] = {0, 0};
+                if (paged) {
+                    if (j == pc.s0) {
+                        pages = entries(j >> 4);
+                        ahead = entries((j >> 4) + 1);
+                    } else if ((j & 15) == 0) {
+                        pages = ahead;
+                        ahead = entries((j >> 4) + 1);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        page[h] = __shfl_sync(~0u, pages, 2 * (j & 15) + h);
+                        int valid = min(max(pc.lk - j * kKeys - h * 64, 0), 64);
+                        if (page[h] < 0 || page[h] >= p.n_pages) {
+                            if (valid > 0 && lane == 0) atomicOr(p.flags, QSA_FLAG_BAD_ID);
+                            page[h] = 0;   // anything that can be read; none of it is seen
+                            valid = 0;
+                        }
+                        if (lane == 0) ct.info[step % kInfo][h] = valid;
+                    }
+                }
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const int slot = it % kSlots;
+                    if (!(ok = wait_all(&ct.empty[slot], ((uint32_t)(it / kSlots) & 1u) ^ 1u, abort_flag))) break;
+                    if (lane != 0) continue;
+                    uint8_t *to = ring + slot * kSlotBytes;
+                    uint64_t *bar = &ct.full[slot];
+                    mbar_expect_tx(bar, kSlotBytes);
+                    if (!paged) {
+                        const int row = TREE ? pc.q0 : pc.k0 + j * kKeys;
+                        const CUtensorMap *m = kv ? &tm_v : &tm_k;
+                        tma_load_3d(to, m, bar, 0, row, pc.g);
+                        tma_load_3d(to + kSlotBytes / 2, m, bar, 64, row, pc.g);
+                    } else if (kv == 0) {   // two halves of 64 dimensions, each 128 token rows
+                        for (int h = 0; h < 2; ++h) {
+                            const int row = (pc.g * p.n_pages + page[h]) * 64;
+                            tma_load_2d(to + h * 8192, &tm_kc, bar, 0, row);
+                            tma_load_2d(to + kSlotBytes / 2 + h * 8192, &tm_kc, bar, 64, row);
+                        }
+                    } else {                // two pages of 128 dimension rows
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_2d(to + h * 16384, &tm_vc, bar, 0, (pc.g * p.n_pages + page[h]) * 128);
+                    }
+                }
+                if (!ok) break;
+            }
+            if (lane == 0 && ok) describe(p, pc);
+        }
+    } else if (warp == 9) {
+        // ---------------- products, issued by one lane
+        if (lane == 0) {
+            constexpr uint32_t kDesc = idesc(F16 ? 0 : 1, kRows, 128);
+            const uint32_t ring0 = smem_u32(ring), q0 = smem_u32(smem + kOffQ);
+            Walk<TREE> walk(p, ct);
+            Piece pc;
+            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+            bool ok = true;
+            auto logits = [&](int i, int kit) {
+                const uint32_t a = q0 + i * kQBytes, b = ring0 + (kit % kSlots) * kSlotBytes;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
+                    mma<MmaKind::f16>(tmem + kColS + i * 128, sdesc(a + off), sdesc(b + off), kDesc, k > 0);
+                }
+                mma_commit(&ct.sfull[i]);
+            };
+            while (ok && walk.next(p, pc)) {
+                if (pc.s1 == pc.s0) continue;
+                const int last = pc.e[1] > pc.s0 ? 1 : 0;   // the stream that uses a slot last
+                if (!(ok = mbar_wait(&ct.full[it % kSlots], (uint32_t)(it / kSlots) & 1u, abort_flag))) break;
+                for (int i = 0; i < 2 && ok; ++i) {
+                    if (pc.e[i] <= pc.s0) continue;
+                    if (!(ok = mbar_wait(&ct.qready[i], nq[i]++ & 1u, abort_flag))) break;
+                    tc_fence_after();
+                    logits(i, it);
+                }
+                if (!ok) break;
+                mma_commit(&ct.empty[it % kSlots]);
+                for (int j = pc.s0; ok && j < pc.s1; ++j, it += 2) {
+                    const int vit = it + 1, kit = it + 2;
+                    const bool paged = TREE && j < pc.n - 1;
+                    const uint32_t v = ring0 + (vit % kSlots) * kSlotBytes;
+                    if (!(ok = mbar_wait(&ct.full[vit % kSlots], (uint32_t)(vit / kSlots) & 1u, abort_flag))) break;
+                    bool have_k = false;
+                    for (int i = 0; i < 2; ++i) {
+                        if (j >= pc.e[i]) continue;
+                        if (!(ok = mbar_wait(&ct.pready[i], np[i]++ & 1u, abort_flag))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint64_t b = paged ? sdesc(v + (k >> 2) * 16384 + (k & 3) * 32)
+                                                     : sdesc_mn128(v + k * 2048, 16384);
+                            mma_f16_ta(tmem + kColO + i * 128, tmem + kColS + i * 128 + k * 8, b,
+                                       paged ? kDesc : kDesc | kIdescBMn, j > pc.s0 || k > 0);
+                        }
+                        if (i == last) mma_commit(&ct.empty[vit % kSlots]);
+                        if (j + 1 < pc.e[i]) {
+                            if (!have_k && !(ok = mbar_wait(&ct.full[kit % kSlots], (uint32_t)(kit / kSlots) & 1u, abort_flag)))
+                                break;
+                            have_k = true;
+                            logits(i, kit);
+                            if (i == last) mma_commit(&ct.empty[kit % kSlots]);
+                        } else {
+                            mma_commit(&ct.ofull[i]);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- softmax and epilogue of a stream, a thread per row
+        Walk<TREE> walk(p, ct);
+        Piece pc;
+        const int st = warp >> 2, r = tid & 127, G = p.group;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
+        uint8_t *sq = smem + kOffQ + st * kQBytes;
+        const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
+        int base = 0, step0 = 0, seq_no = 0;
+        uint32_t ns = 0, no = 0;
+        bool ok = true;
+        while (ok && walk.next(p, pc)) {
+            const int mine = min(pc.rows - st * kRows, kRows), row = pc.row0 + st * kRows + r;
+            const int end = pc.e[st];
+            ++seq_no;
+            if (end > pc.s0) {
+                // the stream's rows into shared memory, zeros behind the last (their logits are read by no one)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4 x[8];
+                    const int ch = r & 15;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int a = (r >> 4) + 8 * (8 * h + i), qr = pc.row0 + st * kRows + a;
+                        x[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (a < mine) {
+                            const int tok = qr / G, hd = pc.g * G + qr - tok * G;
+                            x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q.p) +
+                                                                    (int64_t)(pc.q0 + tok) * p.q.token +
+                                                                    (int64_t)hd * p.q.head + 8 * ch);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int a = (r >> 4) + 8 * (8 * h + i);
+                        *reinterpret_cast<uint4 *>(sq + (ch >> 3) * 16384 + a * 128 + (((ch & 7) ^ (a & 7)) << 4)) = x[i];
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ct.qready[st]);
+            }
+            // what this row sees
+            int lim = 0, low = 0, high = 0;             // prompts: keys of this row, of the tile's first and last row
+            int low_st = 0;                             // and of the stream's first
+            unsigned long long nodes = 0ull;            // trees: of the drafts
+            if constexpr (TREE) {
+                if (end == pc.n && end > pc.s0) nodes = ancestors(p, pc, min(row / G, pc.lq - 1));
+            } else {
+                Seq<TREE> q;
+                q.lk = pc.lk;
+                q.lq = pc.lq;
+                lim = q.limit(p, min(row, pc.row0 + pc.rows - 1));
+                low = q.limit(p, pc.row0);
+                low_st = q.limit(p, min(pc.row0 + st * kRows, pc.row0 + pc.rows - 1));
+                high = q.limit(p, pc.row0 + pc.rows - 1);
+            }
+            float m = -INFINITY, l = 0.0f;
+            for (int j = pc.s0; j < end; ++j) {
+                if (!(ok = wait_all(&ct.sfull[st], ns++ & 1u, abort_flag))) break;
+                tc_fence_after();
+                const bool paged = TREE && j < pc.n - 1;
+                int va = 0, vb = 0;
+                if (paged) {
+                    va = ct.info[(step0 + j - pc.s0) % kInfo][0];
+                    vb = ct.info[(step0 + j - pc.s0) % kInfo][1];
+                }
+                // the lowest stream at work clears V where not every row sees all of it
+                const bool partial = TREE ? !paged || va < 64 || vb < 64 : (j + 1) * kKeys > low;
+                const bool cleans = partial && (st == 0 || j >= pc.e[0]);
+                if (cleans) {
+                    const int vit = base + 2 * (j - pc.s0) + 1;
+                    if (!(ok = wait_all(&ct.full[vit % kSlots], (uint32_t)(vit / kSlots) & 1u, abort_flag))) break;
+                    uint8_t *v = ring + (vit % kSlots) * kSlotBytes;
+                    if (!paged) {   // this thread's token
+                        const bool gone = TREE ? r >= pc.lq : j * kKeys + r >= high;
+                        bool bad = false;
+#pragma unroll 4
+                        for (int ch = 0; ch < 16; ++ch) {
+                            uint4 *x = reinterpret_cast<uint4 *>(v + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                            if (gone) {
+                                *x = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                uint4 y = *x;
+                                if (any_not_finite<F16>(y)) {
+                                    bad = true;
+                                    y.x &= ~not_finite<F16>(y.x);
+                                    y.y &= ~not_finite<F16>(y.y);
+                                    y.z &= ~not_finite<F16>(y.z);
+                                    y.w &= ~not_finite<F16>(y.w);
+                                    *x = y;
+                                }
+                            }
+                        }
+                        if (bad) ct.bad[seq_no & 1] = seq_no + 1;
+                    } else {        // this thread's dimension: every row sees the tokens that are there
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int valid = h ? vb : va;
+                            for (int ch = valid >> 3; ch < 8; ++ch) {
+                                uint8_t *x = v + h * 16384 + r * 128 + ((ch ^ (r & 7)) << 4);
+                                if (8 * ch >= valid) {
+                                    *reinterpret_cast<uint4 *>(x) = make_uint4(0u, 0u, 0u, 0u);
+                                } else {
+                                    uint16_t *e = reinterpret_cast<uint16_t *>(x);
+                                    for (int t = valid - 8 * ch; t < 8; ++t) e[t] = 0;
+                                }
+                            }
+                        }
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+                uint32_t v0[4][16], v1[4][16];
+                tmem_ld64_nowait(tS, v0);
+                tmem_ld64_nowait(tS + 64, v1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    reg_fence(v0[i]);
+                    reg_fence(v1[i]);
+                }
+                if (TREE ? partial : (j + 1) * kKeys > low_st) {
+                    uint32_t see[4];
+                    if constexpr (TREE) {
+                        const unsigned long long a = paged ? (va >= 64 ? ~0ull : (1ull << va) - 1ull) : nodes;
+                        const unsigned long long b = paged ? (vb >= 64 ? ~0ull : (1ull << vb) - 1ull) : 0ull;
+                        see[0] = (uint32_t)a;
+                        see[1] = (uint32_t)(a >> 32);
+                        see[2] = (uint32_t)b;
+                        see[3] = (uint32_t)(b >> 32);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int left = lim - j * kKeys - 32 * w;
+                            see[w] = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        if (!(see[i >> 5] >> (i & 31) & 1u)) v0[i >> 4][i & 15] = 0xFF800000u;
+                        if (!(see[2 + (i >> 5)] >> (i & 31) & 1u)) v1[i >> 4][i & 15] = 0xFF800000u;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(__uint_as_float(v0[i >> 4][i & 15]),
+                                                                       __uint_as_float(v0[i >> 4][(i & 15) + 1])));
+                    top[2 + ((i >> 1) & 1)] = fmaxf(top[2 + ((i >> 1) & 1)], fmaxf(__uint_as_float(v1[i >> 4][i & 15]),
+                                                                                   __uint_as_float(v1[i >> 4][(i & 15) + 1])));
+                }
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (j == pc.s0) {
+                    m = now;
+                } else {
+                    const bool risen = now > m + rise;
+                    if (__any_sync(~0u, risen)) {
+                        // S of this step is complete, so every product before it is: O may be scaled in place
+                        const float f = risen ? ex2((m - now) * c) : 1.0f;
+                        if (risen) m = now;
+                        l *= f;
+#pragma unroll 1
+                        for (int d = 0; d < 128; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_nowait(tO + d, o);
+                            tmem_wait_ld();
+                            reg_fence(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(tO + d, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.0f : m * c;
+                const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+                f32x2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {   // 32 keys a round
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int k = 32 * q + 2 * i;
+                        const uint32_t a = k < 64 ? v0[(k & 63) >> 4][k & 15] : v1[(k & 63) >> 4][k & 15];
+                        const uint32_t b = k < 64 ? v0[(k & 63) >> 4][(k & 15) + 1] : v1[(k & 63) >> 4][(k & 15) + 1];
+                        float y0, y1;
+                        unpack2(fma2(pack2(__uint_as_float(a), __uint_as_float(b)), c2, nm2), y0, y1);
+                        y0 = ex2(y0);
+                        y1 = ex2(y1);
+                        sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
+                        w[i] = pack16<F16>(y0, y1);
+                    }
+                    tmem_st16(tS + 16 * q, w);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ct.pready[st]);
+                float a, b;
+                unpack2(add2(sum[0], sum[1]), a, b);
+                l += a + b;
+            }
+            if (!ok) break;
+            if (mine > 0) {
+                if (end > pc.s0) {
+                    if (!(ok = wait_all(&ct.ofull[st], no++ & 1u, abort_flag))) break;
+                    tc_fence_after();
+                }
+                const bool whole = pc.s0 == 0 && pc.s1 == pc.n;
+                const bool fix = ct.bad[seq_no & 1] == seq_no + 1;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int tok = row / G;
+                const size_t at = (size_t)(pc.q0 + tok) * p.n_heads + pc.g * G + (row - tok * G);
+                const size_t slot = 2 * (size_t)blockIdx.x + (pc.s0 > 0 ? 0 : 1);
+                const int in_tile = st * kRows + r;
+#pragma unroll 1
+                for (int d = 0; d < 128; d += 16) {
+                    uint32_t o[16];
+                    __syncwarp();
+                    if (end > pc.s0) {
+                        tmem_ld16_nowait(tO + d, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = 0u;
+                    }
+                    if (r >= mine) continue;
+                    if (fix) {   // values that are not finite, where this row sees them
+                        const int t0 = TREE ? 0 : max(low / kKeys, pc.s0) * kKeys, t1 = TREE ? pc.lq : min(lim, pc.s1 * kKeys);
+                        for (int t = t0; t < t1; ++t) {
+                            if (TREE && !(nodes >> t & 1ull)) continue;
+                            const uint16_t *v = static_cast<const uint16_t *>(p.v.p) +
+                                                (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token + (int64_t)pc.g * p.v.head + d;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (not_finite<F16>(v[i]) & 0xFFFFu) o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<F16>(v[i]));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float x[4] = {__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                            __uint_as_float(o[i + 3])};
+                        if (whole) store4<F16>(p, at * 128 + d + i, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+                        else p.part[(slot * 32 + (d + i) / 4) * p.rows_cap + in_tile] = make_float4(x[0], x[1], x[2], x[3]);
+                    }
+                }
+                __syncwarp();
+                tc_fence_before();
+                if (r < mine) {
+                    if (!whole) p.ml[slot * p.rows_cap + in_tile] = make_float2(m * c, l);
+                    else if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
+                }
+            }
+            base += 2 * (pc.s1 - pc.s0);
+            step0 += pc.s1 - pc.s0;
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (ct.abort && lane == 0) {   // copies and products in flight end before their memory goes
+        if (warp == 8)
+            for (int i = max(0, it - kSlots); i < it; ++i) mbar_drain(&ct.full[i % kSlots], (uint32_t)(i / kSlots) & 1u);
+        if (warp == 9) {
+            mma_commit(&ct.drain);
+            mbar_drain(&ct.drain, 0);
+        }
+    }
+    __syncwarp();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && ct.abort) atomicOr(p.flags, QSA_FLAG_WAIT_TIMEOUT);
+}
+
+// Runs that several CTAs worked on: a CTA per (share that a run begins in and does not end in, 32 rows), a lane per row.
+// The partials O_c of the shares from there to the run's end are weighted 2^(m_c - M).
+constexpr int kJoinThreads = 256;
+
+template <bool F16, bool TREE>
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ Params p, int grid) {
+    wait_prior_grid();
+    allow_dependent_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = p.row_tiles;
+    const int4 d = p.desc[2 * (size_t)blockIdx.x + 1];
+    if (d.x == 0) return;
+    Seq<TREE> q;
+    q.load(p, d.y, false);
+    const int rows = min(q.lq * p.group - d.w, kTileRows), in_tile = blockIdx.y * 32 + lane;
+    if ((int)blockIdx.y * 32 >= rows) return;
+    int parts = 0;   // shares behind this one
+    for (int c0 = 1;; c0 += 32) {
+        const long long c = blockIdx.x + (long long)(c0 + lane) * step;
+        const int kind = c < grid ? p.desc[2 * c].x : 1;
+        const unsigned ends = __ballot_sync(~0u, kind != 2);
+        if (ends) {
+            parts = c0 + __ffs(ends) - 1;
+            break;
+        }
+    }
+    const bool mine = in_tile < rows;
+    auto slot = [&](int i) { return 2 * ((size_t)blockIdx.x + (size_t)i * step) + (i == 0 ? 1 : 0); };
+    float M = -INFINITY, L = 0.0f;
+    if (mine) {
+#pragma unroll 8
+        for (int i = 0; i <= parts; ++i) {
+            const float2 x = p.ml[slot(i) * p.rows_cap + in_tile];
+            M = fmaxf(M, x.y == 0.0f ? -INFINITY : x.x);
+        }
+        float4 o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = 0; i <= parts; ++i) {
+            const float2 x = p.ml[slot(i) * p.rows_cap + in_tile];
+            if (x.y == 0.0f) continue;   // saw nothing
+            const float f = ex2(x.x - M);
+            L = fmaf(f, x.y, L);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 y = p.part[(slot(i) * 32 + warp + 8 * e) * p.rows_cap + in_tile];
+                o[e].x = fmaf(f, y.x, o[e].x);
+                o[e].y = fmaf(f, y.y, o[e].y);
+                o[e].z = fmaf(f, y.z, o[e].z);
+                o[e].w = fmaf(f, y.w, o[e].w);
+            }
+        }
+        const int row = d.w + in_tile, tok = row / p.group;
+        const size_t at = (size_t)(q.q0 + tok) * p.n_heads + d.z * p.group + (row - tok * p.group);
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            store4<F16>(p, at * 128 + 4 * (warp + 8 * e), o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv);
+        if (warp == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    }
+}
+
+int rows_cap(long long rows) {
+    return rows >= kTileRows ? kTileRows : (int)((rows + 31) / 32 * 32);
+}
+
+template <bool F16, bool TREE>
+qsa_status launch_typed(const CUtensorMap (&m)[4], const Params &p, int grid, bool split, cudaStream_t s) {
+    static std::mutex mu;
+    static bool opted_in[64] = {false};
+    int dev = 0;
+    qsa_status st = check_cuda(cudaGetDevice(&dev), "cudaGetDevice");
+    if (st != QSA_OK) return st;
+    if (dev < 0 || dev >= 64) return fail(QSA_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted_in[dev]) {
+            st = check_cuda(cudaFuncSetAttribute(dense_kernel<F16, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+                            "cudaFuncSetAttribute(dense attention)");
+            if (st != QSA_OK) return st;
+            opted_in[dev] = true;
+        }
+    }
+    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3], p);
+    if (st != QSA_OK || !split) return st;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return check_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<F16, TREE>, p, grid), "combine_kernel launch");
 }
 
 template <bool TREE>
 qsa_status launch(const DenseArgs &a, cudaStream_t s) {
-    const long long rows = TREE ? a.max_nodes : a.total_q;
-    const dim3 grid((unsigned)a.n_seqs, (unsigned)a.n_heads, (unsigned)((rows + kWarps - 1) / kWarps < 64 ? (rows + kWarps - 1) / kWarps : 64));
-    if (a.dt == QSA_BF16) dense_kernel<__nv_bfloat16, TREE><<<grid, 32 * kWarps, 0, s>>>(a);
-    else dense_kernel<__half, TREE><<<grid, 32 * kWarps, 0, s>>>(a);
-    return check_cuda(cudaGetLastError(), "dense_kernel launch");
+    Params p{};
+    p.q = a.q;
+    p.v = a.v;
+    p.cu_q = a.cu_q;
+    p.cu_k = a.cu_k;
+    p.n_seqs = a.n_seqs;
+    p.total_q = a.total_q;
+    p.total_k = a.total_k;
+    p.n_heads = a.n_heads;
+    p.n_kv = a.n_kv_heads;
+    p.group = a.n_heads / a.n_kv_heads;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.out = a.out;
+    p.out_f32 = a.out_dt == QSA_F32;
+    p.lse = a.lse;
+    p.parents = a.parents;
+    p.max_nodes = a.max_nodes;
+    p.table = a.table.table;
+    p.table_stride = a.table.stride;
+    p.max_pages = a.table.max_pages;
+    p.n_pages = a.table.n_pages;
+    p.n_tokens = a.n_tokens;
+    p.flags = a.flags;
+    p.rows_cap = rows_cap((long long)a.total_q * p.group);
+    char *ws = static_cast<char *>(a.ws) + 256;
+    p.desc = reinterpret_cast<int4 *>(ws);
+    p.ml = reinterpret_cast<float2 *>(ws + kMaxCtas * 2 * sizeof(int4));
+    p.part = reinterpret_cast<float4 *>(ws + kMaxCtas * 2 * (sizeof(int4) + (size_t)p.rows_cap * sizeof(float2)));
+    const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
+    p.row_tiles = TREE ? (a.max_nodes * p.group + kTileRows - 1) / kTileRows : 1;
+    p.shares = ctas / p.row_tiles;
+    const int grid = p.shares * p.row_tiles;
+    // the longest run that the sizes allow
+    const bool split = (TREE ? 64ll * a.table.max_pages + kKeys : (long long)a.total_k) > kWhole * kKeys;
+    CUtensorMap m[4];
+    const Rows16 &k = a.total_k > 0 ? a.k : a.q, &v = a.total_k > 0 ? a.v : a.q;   // without keys nothing is loaded
+    const int rows = a.total_k > 0 ? a.total_k : 1, heads = a.total_k > 0 ? a.n_kv_heads : 1;
+    qsa_status st;
+    if ((st = get_rows_map(&m[0], k, rows, heads, kKeys)) != QSA_OK || (st = get_rows_map(&m[1], v, rows, heads, kKeys)) != QSA_OK)
+        return st;
+    m[2] = m[0];
+    m[3] = m[1];
+    if (TREE) {
+        const uint64_t pages = (uint64_t)a.n_kv_heads * a.table.n_pages;
+        if ((st = get_map(&m[2], a.kcache, 2, 128, pages * 64, 64)) != QSA_OK ||
+            (st = get_map(&m[3], a.vcache_t, 2, 64, pages * 128, 128)) != QSA_OK)
+            return st;
+    }
+    return a.dt == QSA_F16 ? launch_typed<true, TREE>(m, p, grid, split, s) : launch_typed<false, TREE>(m, p, grid, split, s);
 }
 
 }  // namespace
 
-size_t attention_ws_bytes(int, int, int) { return 256; }
+size_t attention_ws_bytes(int rows, int n_heads, int n_kv_heads) {
+    const int cap = rows_cap((long long)rows * (n_heads / n_kv_heads));
+    return 256 + (size_t)kMaxCtas * 2 * (sizeof(int4) + (size_t)cap * (sizeof(float2) + 32 * sizeof(float4)));
+}
 qsa_status launch_prompt_attention(const DenseArgs &a, cudaStream_t s) { return launch<false>(a, s); }
 qsa_status launch_tree_attention(const DenseArgs &a, cudaStream_t s) { return launch<true>(a, s); }
 

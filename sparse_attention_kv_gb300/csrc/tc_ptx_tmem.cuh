@@ -1,12 +1,19 @@
 // tc_ptx_tmem.cuh -- inline-PTX wrappers beside those of tc_ptx.cuh for kernels that write tensor
-// memory from registers: 8-column loads and stores, the 8-bit MMA with A in tensor memory, the
-// MN-major operand without swizzle, and the untiled bulk copy.
+// memory from registers: 8-column loads and stores, the MMAs with A in tensor memory,
+// the MN-major operands, the 3-D tensor load and the untiled bulk copy.
 #pragma once
 
 #include "tc_ptx.cuh"
 
 namespace qsa {
 
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
 // One contiguous copy; both addresses 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -22,6 +29,14 @@ __device__ __forceinline__ void mma_f8_ta(uint32_t d, uint32_t a, uint64_t bdesc
         "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
         : "memory");
 }
+// kind::f16 with A in tensor memory (two 16-bit values of its K axis per column, the lower one first).
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
 // 8 consecutive columns of this warp's 32 TMEM lanes, one row of 8 values per thread.
 __device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&v)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -32,6 +47,15 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
                  : "memory");
+}
+// 16 consecutive columns, as tmem_ld16_nowait reads them.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // As tc_ptx.cuh's, for 8 registers.
@@ -48,6 +72,18 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t k_bytes, u
     d |= (uint64_t)(k_bytes >> 4) << 16;
     d |= (uint64_t)(mn_bytes >> 4) << 32;
     d |= (uint64_t)1 << 46;
+    return d;
+}
+// MN-major operand of 16-bit values under the 128-byte swizzle: 64 steps of the M or N axis are a 128-byte row, 8
+// steps of the K axis lie 128 bytes apart, groups of 8 steps 1024 bytes apart (SBO) and the next 64 of the M or N
+// axis `mn_bytes` apart (LBO).
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t mn_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(mn_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
     return d;
 }
 constexpr uint32_t kIdescBMn = 1u << 16;   // instruction descriptor: B is MN-major
