@@ -39,13 +39,14 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kRows = 128;            // rows of a stream (TMEM lanes)
 constexpr int kKeys = 128;            // keys of a step
-constexpr int kTileRows = 2 * kRows;
-constexpr int kSlots = 5;
+constexpr int kSlots = 4;
 constexpr int kSlotBytes = kKeys * 128 * 2;
 constexpr int kQBytes = kRows * 128 * 2;
+constexpr int kStageBytes = 4096;     // per softmax warp: 32 rows of 128 bytes on their way out
+constexpr int kPieces = 4;            // pieces that are published ahead
 constexpr int kInfo = 8;              // steps whose page limits are held: more than the ring holds
 constexpr int kMaxCtas = 152;
 constexpr int kWhole = 4;             // runs of so few steps are not split
@@ -54,10 +55,12 @@ constexpr float kRise = 8.0f;         // log2 of the largest weight before the r
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
 
 struct Params {
-    Rows16 q, v;
+    Rows16 v;
     const int32_t *cu_q, *cu_k;
     int n_seqs, total_q, total_k;
     int n_heads, n_kv, group;
+    int toks;             // tokens of a stream: 128 / group, so that a stream begins with a token
+    uint32_t by_group;    // ceil(2^16 / group): x / group = x * by_group >> 16 for x < 128
     float scale, scale_log2;
     void *out;
     int out_f32;
@@ -77,20 +80,32 @@ struct Params {
     uint32_t *flags;
 };
 
+// What a CTA works on at a time: steps s0 .. s1 - 1 of a run's n, for a tile of two streams.
+struct Piece {
+    int stop;             // no piece: the CTA is done
+    int bad;              // a value in a step that not every row sees whole was not finite
+    int s, g;
+    int q0, lq, k0, lk;
+    int tok0;             // the tile's first token in its sequence
+    int s0, s1, n;
+    int rows[2];          // rows of each stream
+    int e[2];             // where each stream's steps end (<= s1; s0: none)
+};
+
 struct Ctrl {
-    uint64_t full[kSlots], empty[kSlots];
-    uint64_t qready[2], sfull[2], pready[2], ofull[2];
+    uint64_t full[kSlots], empty[kSlots], dirty, clean;
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2], ofull[2];
+    uint64_t pfull[kPieces], pempty[kPieces];
     uint64_t drain;
-    long long x0, x1, at;   // this CTA's share and the beginning of the run it starts in
-    int s, g, t;            // that run
+    Piece pieces[kPieces];
     uint32_t tmem;
     int abort;
-    int bad[2];             // number + 1 of the last piece in which a value was not finite, by its parity
-    int info[kInfo][2];     // valid tokens in each page of a step
+    int info[kInfo][2];   // valid tokens in each page of a step
 };
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQBytes;
-constexpr int kOffCtrl = kOffRing + kSlots * kSlotBytes;
+constexpr int kOffStage = kOffRing + kSlots * kSlotBytes;
+constexpr int kOffCtrl = kOffStage + 8 * kStageBytes;
 constexpr int kSmem = 1024 + kOffCtrl + (int)sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory");
 
@@ -109,10 +124,31 @@ __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatil
 
 // ------------------------------------------------------------------ the runs and the shares
 
+// sum of floor((a t + b) / m) over t < n, by the Euclidean steps of counting lattice points under a line
+__device__ __forceinline__ long long floor_sum(unsigned long long n, unsigned m, unsigned a, unsigned long long b) {
+    unsigned long long sum = 0;
+    while (true) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const unsigned long long top = a * n + b;
+        if (top < m) return (long long)sum;
+        n = top / m;
+        b = top % m;
+        const unsigned x = m;
+        m = a;
+        a = x;
+    }
+}
+
 template <bool TREE>
 struct Seq {
     int q0, lq, k0, lk, tiles;   // trees: lk = tokens in the pages
-    long long e;                 // see cum()
 
     __device__ __forceinline__ void load(const Params &p, int s, bool tell) {
         range(p, p.cu_q, s, p.total_q, tell, q0, lq);
@@ -128,10 +164,7 @@ struct Seq {
             tiles = lq > 0 ? 1 : 0;   // each CTA of a group has its own tile of rows
         } else {
             range(p, p.cu_k, s, p.total_k, tell, k0, lk);
-            const long long rows = (long long)lq * p.group;
-            tiles = (int)((rows + kTileRows - 1) / kTileRows);
-            const long long c = kTileRows - 1 + (long long)p.group * (lk - lq + kKeys);
-            e = c >= 0 ? c / kKeys : -((-c + kKeys - 1) / kKeys);
+            tiles = (lq + 2 * p.toks - 1) / (2 * p.toks);
         }
     }
     static __device__ __forceinline__ void range(const Params &p, const int32_t *cu, int s, int most, bool tell, int &c0,
@@ -141,18 +174,12 @@ struct Seq {
         c0 = min(max(a, 0), most);
         len = min(max(b, c0), most) - c0;
     }
-    // Keys that row r of the sequence's rows sees.
-    __device__ __forceinline__ int limit(const Params &p, int r) const {
-        return min(max(lk - lq + r / p.group + 1, 0), lk);
-    }
     __device__ __forceinline__ int steps(const Params &p, int t) const {
         if constexpr (TREE) return (lk + kKeys - 1) / kKeys + 1;   // the pages, then the drafts
-        const long long rows = (long long)lq * p.group, end = (long long)(t + 1) * kTileRows;
-        return (limit(p, (int)((end < rows ? end : rows) - 1)) + kKeys - 1) / kKeys;
+        return (keys_of(lq, lk, min((t + 1) * 2 * p.toks, lq) - 1) + kKeys - 1) / kKeys;
     }
-    // Lengths of the runs of tiles 0 .. T - 1, each its steps and one more for its beginning and end.  A full
-    // tile t has max(0, floor((2 t + e) / G)) steps: its last row is row 256 t + 255, whose limit is lk - lq +
-    // floor((256 t + 255) / G) + 1, and floors nest.  The last tile ends at lk.
+    // Lengths of the runs of tiles 0 .. T - 1, each its steps and one more for its beginning and end.  With W tokens a
+    // tile, a full tile t has max(0, floor((W t + c) / 128)) steps, c = lk - lq + W + 127; the last tile ends at lk.
     __device__ __forceinline__ long long cum(const Params &p, int T) const {
         if constexpr (TREE) return T ? steps(p, 0) + 1 : 0;
         long long sum = T;
@@ -160,44 +187,21 @@ struct Seq {
             sum += (max(lk, 0) + kKeys - 1) / kKeys;
             --T;
         }
-        const long long t0 = e < 0 ? (-e + 1) / 2 : 0;
-        const long long U = T - t0;
-        if (U <= 0) return sum;
-        const int G = p.group;
-        const long long e1 = e + 2 * t0, q = e1 / G;
-        const int rem = (int)(e1 - q * G), a = (G - rem + 1) / 2, b = (2 * G - rem + 1) / 2;
-        const long long A = U / G;
-        const int m = (int)(U - A * G);
-        const long long per = max(0, G - a) + max(0, G - b), rest = max(0, m - a) + max(0, m - b);
-        return sum + U * q + G * A * (A - 1) + A * per + 2 * A * m + rest;
+        const int W = 2 * p.toks;
+        const long long c = (long long)lk - lq + W + kKeys - 1, t0 = c < 0 ? (-c + W - 1) / W : 0;
+        return T > t0 ? sum + floor_sum(T - t0, kKeys, W, c + t0 * W) : sum;
     }
+    // Keys that token i of lq sees.
+    static __device__ __forceinline__ int keys_of(int lq, int lk, int i) { return min(max(lk - lq + i + 1, 0), lk); }
 };
 
-struct Piece {
-    int s, g;
-    int q0, lq, k0, lk;
-    int row0, rows;       // rows of the sequence, of this tile
-    int s0, s1, n;        // steps of this piece, of the run
-    int e[2];             // where each stream's steps end (<= s1; s0: none)
-};
-
-// A CTA's pieces one after another; every role walks by itself.
+// A CTA's pieces one after another.
 template <bool TREE>
 struct Walk {
     Seq<TREE> q;
-    long long at, x0, x1;
+    long long at, x0, x1;   // the beginning of the next run, and the CTA's share of all runs
     int s, g, t, tile;
 
-    __device__ __forceinline__ Walk(const Params &p, const Ctrl &c) {
-        x0 = c.x0;
-        x1 = c.x1;
-        at = c.at;
-        s = c.s;
-        g = c.g;
-        t = c.t;
-        tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
-        if (at < x1 && s < p.n_seqs) q.load(p, s, false);
-    }
     __device__ __forceinline__ bool next(const Params &p, Piece &pc) {
         while (at < x1 && s < p.n_seqs) {
             const int n = q.steps(p, t);
@@ -216,19 +220,18 @@ struct Walk {
             pc.lq = q.lq;
             pc.k0 = q.k0;
             pc.lk = q.lk;
-            pc.row0 = (TREE ? tile : t) * kTileRows;
-            pc.rows = min(q.lq * p.group - pc.row0, kTileRows);
+            pc.tok0 = (TREE ? tile : t) * 2 * p.toks;
             pc.s0 = s0;
             pc.s1 = s1;
             pc.n = n;
-            if (pc.rows <= 0) take = false;
+            if (pc.tok0 >= q.lq) take = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int mine = min(pc.rows - i * kRows, kRows);
+                const int first = pc.tok0 + i * p.toks, toks = min(max(q.lq - first, 0), p.toks);
+                pc.rows[i] = toks * p.group;
                 int end = s0;
-                if (take && mine > 0) {
-                    end = n;
-                    if constexpr (!TREE) end = (q.limit(p, pc.row0 + i * kRows + mine - 1) + kKeys - 1) / kKeys;
+                if (toks > 0) {
+                    end = TREE ? n : (q.keys_of(q.lq, q.lk, first + toks - 1) + kKeys - 1) / kKeys;
                     end = max(min(end, s1), s0);
                 }
                 pc.e[i] = end;
@@ -256,13 +259,13 @@ __device__ __forceinline__ long long warp_sum(long long v) {
     return v;
 }
 
-// This CTA's share of all runs, and the run it begins in (one warp).
+// This CTA's share of all runs, and the run it begins in (one warp; every lane gets it).
 template <bool TREE>
-__device__ void find_share(const Params &p, Ctrl &c) {
+__device__ void find_share(const Params &p, Walk<TREE> &w) {
     const int lane = threadIdx.x & 31;
     const int share = blockIdx.x / p.row_tiles;
     const bool tell = blockIdx.x == 0;
-    Seq<TREE> q;
+    Seq<TREE> &q = w.q;
     auto weight = [&](int s, bool say) -> long long {
         if (s >= p.n_seqs) return 0;
         q.load(p, s, say);
@@ -270,57 +273,52 @@ __device__ void find_share(const Params &p, Ctrl &c) {
     };
     long long total = 0, first = 0;   // first: the weights of sequences 0 .. 31
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        const long long w = weight(s0 + lane, tell);
-        if (s0 == 0) first = w;
-        total += warp_sum(w);
+        const long long x = weight(s0 + lane, tell);
+        if (s0 == 0) first = x;
+        total += warp_sum(x);
     }
     long long used = (total + kMinShare - 1) / kMinShare;
     used = used < 1 ? 1 : used > p.shares ? p.shares : used;
-    const long long x0 = share < used ? share * total / used : total;
-    const long long x1 = share < used ? (share + 1) * total / used : total;
-    long long before = 0, at = x0;
-    int s = p.n_seqs, g = 0, t = 0;
-    for (int s0 = 0; s0 < p.n_seqs && x0 < x1; s0 += 32) {
-        const long long w = s0 == 0 ? first : weight(s0 + lane, false);
-        long long incl = w;
+    w.x0 = share < used ? share * total / used : total;
+    w.x1 = share < used ? (share + 1) * total / used : total;
+    w.tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
+    long long before = 0;
+    w.at = w.x0;
+    w.s = p.n_seqs;
+    w.g = w.t = 0;
+    for (int s0 = 0; s0 < p.n_seqs && w.x0 < w.x1; s0 += 32) {
+        const long long x = s0 == 0 ? first : weight(s0 + lane, false);
+        long long incl = x;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const long long y = __shfl_up_sync(~0u, incl, d);
             if (lane >= d) incl += y;
         }
-        const unsigned past = __ballot_sync(~0u, before + incl > x0);
+        const unsigned past = __ballot_sync(~0u, before + incl > w.x0);
         if (past) {
             const int l = __ffs(past) - 1;
-            s = s0 + l;
-            before += __shfl_sync(~0u, incl - w, l);
+            w.s = s0 + l;
+            before += __shfl_sync(~0u, incl - x, l);
             break;
         }
         before += __shfl_sync(~0u, incl, 31);
     }
-    if (s < p.n_seqs) {
-        q.load(p, s, false);
+    if (w.s < p.n_seqs) {
+        q.load(p, w.s, false);
         const long long per = q.cum(p, q.tiles);
-        g = (int)((x0 - before) / per);
-        before += g * per;
+        w.g = (int)((w.x0 - before) / per);
+        before += w.g * per;
         int lo = 0, hi = q.tiles;   // cum(lo) <= x0 - before < cum(hi)
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32, mid = min(lo + (lane + 1) * step, hi);
-            const unsigned over = __ballot_sync(~0u, q.cum(p, mid) > x0 - before);   // lane 31 reaches hi
+            const unsigned over = __ballot_sync(~0u, q.cum(p, mid) > w.x0 - before);   // lane 31 reaches hi
             const int l = __ffs(over) - 1;
             const int new_hi = min(lo + (l + 1) * step, hi);
             lo += l * step;
             hi = new_hi;
         }
-        t = lo;
-        at = before + q.cum(p, t);
-    }
-    if (lane == 0) {
-        c.x0 = x0;
-        c.x1 = x1;
-        c.at = at;
-        c.s = s;
-        c.g = g;
-        c.t = t;
+        w.t = lo;
+        w.at = before + q.cum(p, lo);
     }
 }
 
@@ -372,14 +370,14 @@ __device__ __forceinline__ bool any_not_finite(const uint4 &x) {
 }
 
 // The nodes a tree's row sees (one warp; every lane gets its own row's): bit j of the mask is node j.
-__device__ unsigned long long ancestors(const Params &p, const Piece &pc, int node) {
+__device__ unsigned long long ancestors(const Params &p, int q0, int lq, int node) {
     const int lane = threadIdx.x & 31;
     unsigned long long mask[2];
     int up[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = lane + 32 * h;
-        int a = i < pc.lq ? p.parents[pc.q0 + i] : -1;
+        int a = i < lq ? p.parents[q0 + i] : -1;
         if (a < -1 || a >= i) {
             atomicOr(p.flags, QSA_FLAG_BAD_ID);
             a = -1;
@@ -415,11 +413,11 @@ __device__ unsigned long long ancestors(const Params &p, const Piece &pc, int no
 // ------------------------------------------------------------------ the kernel
 
 // What a CTA left in its partials.  desc[0]: (1 = the piece ends its run, 2 = it does not, 0 = none) for a piece that began
-// in an earlier CTA; desc[1]: (1, s, g, row0) for a run that begins here and does not end here.
+// in an earlier CTA; desc[1]: (1, s, g, tok0) for a run that begins here and does not end here.
 __device__ __forceinline__ void describe(const Params &p, const Piece &pc) {
     int4 *d = p.desc + 2 * (size_t)blockIdx.x;
     if (pc.s0 > 0) d[0] = make_int4(pc.s1 == pc.n ? 1 : 2, 0, 0, 0);
-    else if (pc.s1 < pc.n) d[1] = make_int4(1, pc.s, pc.g, pc.row0);
+    else if (pc.s1 < pc.n) d[1] = make_int4(1, pc.s, pc.g, pc.tok0);
 }
 
 // Four values of a row of out, at element `at`.
@@ -429,11 +427,115 @@ __device__ __forceinline__ void store4(const Params &p, size_t at, float a, floa
     else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(pack16<F16>(a, b), pack16<F16>(c, d));
 }
 
+// The end of a piece for one warp's rows (a lane each): the output normalised, in whole 128-byte rows through `stage`, or the
+// partial as it is.  have: there is an O in tensor memory.
+template <bool F16, bool TREE>
+__device__ __forceinline__ void finish(const Params &p, const Piece &pc, bool have, uint32_t tO, uint8_t *stage, float m, float l,
+                                       int lim, int low, unsigned long long nodes, int my_tok, int rows) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = warp >> 2, r = threadIdx.x & 127, G = p.group;
+    const bool whole = pc.s0 == 0 && pc.s1 == pc.n, mine = r < rows, fix = pc.bad != 0;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const size_t slot = 2 * (size_t)blockIdx.x + (pc.s0 > 0 ? 0 : 1);
+    const int in_tile = st * kRows + r;
+    // values that are not finite are added where this row sees them: in the drafts, or from the first step that was cleared
+    const int f0 = TREE ? 0 : max(Seq<TREE>::keys_of(pc.lq, pc.lk, pc.tok0) / kKeys, pc.s0) * kKeys;
+    const int f1 = TREE ? (pc.s1 == pc.n ? pc.lq : 0) : min(lim, pc.s1 * kKeys);
+    const int wide = p.out_f32 ? 32 : 64;   // dimensions of a row's 128 staged bytes
+#pragma unroll 1
+    for (int d = 0; d < 128; d += 16) {
+        uint32_t o[16];
+        __syncwarp();
+        if (have) {
+            tmem_ld16_nowait(tO + d, o);
+            tmem_wait_ld();
+            reg_fence(o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0u;
+        }
+        if (fix && mine) {
+            for (int t = f0; t < f1; ++t) {
+                if (TREE && !(nodes >> t & 1ull)) continue;
+                const uint16_t *v = static_cast<const uint16_t *>(p.v.p) + (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token +
+                                    (int64_t)pc.g * p.v.head + d;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (not_finite<F16>(v[i]) & 0xFFFFu) o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<F16>(v[i]));
+            }
+        }
+        if (!whole) {
+            if (mine)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    p.part[(slot * 32 + (d + i) / 4) * p.rows_cap + in_tile] =
+                        make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+            continue;
+        }
+        // this row's 16-byte units, rotated by the row so that neither way meets a bank twice
+        if (p.out_f32) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 x = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
+                                             __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                *reinterpret_cast<float4 *>(stage + lane * 128 + (((((d & 31) + i) >> 2) ^ (lane & 7)) << 4)) = x;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    w[x] = pack16<F16>(__uint_as_float(o[i + 2 * x]) * inv, __uint_as_float(o[i + 2 * x + 1]) * inv);
+                *reinterpret_cast<uint4 *>(stage + lane * 128 + (((((d & 63) + i) >> 3) ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (((d + 16) & (wide - 1)) == 0) {   // 128 bytes of each row: eight lanes write a row's
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), row = (warp & 3) * 32 + rr;
+                const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                if (row < rows) {
+                    const int tok = (int)(row * p.by_group >> 16);
+                    const size_t at = (size_t)(pc.q0 + pc.tok0 + st * p.toks + tok) * p.n_heads + pc.g * G + (row - tok * G);
+                    uint8_t *out = static_cast<uint8_t *>(p.out) + (at * 128 + (d + 16 - wide)) * (p.out_f32 ? 4 : 2);
+                    *reinterpret_cast<uint4 *>(out + 16 * (lane & 7)) = x;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (mine) {
+        if (!whole) {
+            p.ml[slot * p.rows_cap + in_tile] = make_float2(m * p.scale_log2, l);
+        } else if (p.lse) {
+            const int tok = my_tok - st * p.toks;
+            const size_t at = (size_t)(pc.q0 + pc.tok0 + my_tok) * p.n_heads + pc.g * G + (r - tok * G);
+            p.lse[at] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
+        }
+    }
+}
+
+// The next published piece (a warp); false when the wait ran out.  A reader gives it back with done().
+struct Pieces {
+    Ctrl &ct;
+    int no = 0;   // pieces taken
+
+    __device__ __forceinline__ bool next(volatile int *abort_flag, const Piece *&pc) {
+        pc = &ct.pieces[no % kPieces];
+        return wait_all(&ct.pfull[no % kPieces], (uint32_t)(no / kPieces) & 1u, abort_flag);
+    }
+    __device__ __forceinline__ void done() {   // lane 0, once the warp has read all it needs
+        mbar_arrive(&ct.pempty[no++ % kPieces]);
+    }
+};
+
 template <bool F16, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
-    dense_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                 const __grid_constant__ CUtensorMap tm_kc, const __grid_constant__ CUtensorMap tm_vc,
-                 const __grid_constant__ Params p) {
+    dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
+                 const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t *ring = smem + kOffRing;
@@ -447,12 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ct.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ct.qready[i], 4);   // one arrival per warp of the stream
+            mbar_init(&ct.qfull[i], 1);
+            mbar_init(&ct.qempty[i], 1);
             mbar_init(&ct.sfull[i], 1);
-            mbar_init(&ct.pready[i], 4);
+            mbar_init(&ct.pready[i], 4);   // one arrival per warp of the stream
             mbar_init(&ct.ofull[i], 1);
-            ct.bad[i] = 0;
         }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(&ct.pfull[i], 1);
+            mbar_init(&ct.pempty[i], 11);  // every warp but the one that publishes
+        }
+        mbar_init(&ct.dirty, 1);
+        mbar_init(&ct.clean, 2);           // warps 10 and 11
         mbar_init(&ct.drain, 1);
         ct.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -463,11 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 8) find_share<TREE>(p, ct);
-    if (tid == 0) {
-        p.desc[2 * (size_t)blockIdx.x] = make_int4(0, 0, 0, 0);
-        p.desc[2 * (size_t)blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -475,19 +578,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     int it = 0;   // slots of the ring used so far
     if (warp == 8) {
-        Walk<TREE> walk(p, ct);
+        // ---------------- pieces and copies: Q, K and V of each step, K first
+        if (lane == 0) {
+            p.desc[2 * (size_t)blockIdx.x] = make_int4(0, 0, 0, 0);
+            p.desc[2 * (size_t)blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+        }
+        Walk<TREE> walk;
+        find_share<TREE>(p, walk);
         Piece pc;
-        // ---------------- copies: K and V of each step, K first
-        int step = 0;
+        int step = 0, no = 0;
+        uint32_t nq[2] = {0, 0};
         bool ok = true;
-        while (ok && walk.next(p, pc)) {
+        const uint32_t qbytes = (uint32_t)(p.toks * p.group * 256);
+        auto load_q = [&]() {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || pc.e[i] <= pc.s0) continue;
+                if (!(ok = wait_all(&ct.qempty[i], (nq[i]++ & 1u) ^ 1u, abort_flag)) || lane != 0) continue;
+                uint8_t *to = smem + kOffQ + i * kQBytes;
+                mbar_expect_tx(&ct.qfull[i], qbytes);
+                const int row = pc.q0 + pc.tok0 + i * p.toks;
+                tma_load_3d(to, &tm_q, &ct.qfull[i], 0, pc.g * p.group, row);
+                tma_load_3d(to + kQBytes / 2, &tm_q, &ct.qfull[i], 64, pc.g * p.group, row);
+            }
+        };
+        while (ok) {
+            const bool more = walk.next(p, pc);
+            pc.stop = !more;
+            pc.bad = 0;
+            if (!(ok = wait_all(&ct.pempty[no % kPieces], ((uint32_t)(no / kPieces) & 1u) ^ 1u, abort_flag))) break;
+            if (lane == 0) {
+                ct.pieces[no % kPieces] = pc;
+                mbar_arrive(&ct.pfull[no % kPieces]);
+            }
+            ++no;
+            if (!more) break;
             int pages = 0, ahead = 0;   // 32 entries of the table, a lane each, and the 32 after them
             const int nb = TREE ? (pc.lk + 63) >> 6 : 0;
             auto entries = [&](int chunk) {
                 const int i = chunk * 32 + lane;
                 return i < nb ? p.table[(size_t)pc.s * p.table_stride + i] : -1;
             };
-            for (int j = pc.s0; j < pc.s1; ++j, ++step) {
+            for (int j = pc.s0; ok && j < pc.s1; ++j, ++step) {
                 const bool paged = TREE && j < pc.n - 1;
                 int page[2] = {0, 0};
                 if (paged) {
@@ -504,8 +636,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         int valid = min(max(pc.lk - j * kKeys - h * 64, 0), 64);
                         if (page[h] < 0 || page[h] >= p.n_pages) {
                             if (valid > 0 && lane == 0) atomicOr(p.flags, QSA_FLAG_BAD_ID);
-                            page[h] = 0;   // anything that can be read; none of it is seen
+                            page[h] = p.n_kv * p.n_pages;   // behind the pool: the copy fills in zeros
                             valid = 0;
+                        } else {
+                            page[h] += pc.g * p.n_pages;
                         }
                         if (lane == 0) ct.info[step % kInfo][h] = valid;
                     }
@@ -513,171 +647,148 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kv = 0; kv < 2; ++kv, ++it) {
                     const int slot = it % kSlots;
                     if (!(ok = wait_all(&ct.empty[slot], ((uint32_t)(it / kSlots) & 1u) ^ 1u, abort_flag))) break;
-                    if (lane != 0) continue;
-                    uint8_t *to = ring + slot * kSlotBytes;
-                    uint64_t *bar = &ct.full[slot];
-                    mbar_expect_tx(bar, kSlotBytes);
-                    if (!paged) {
-                        const int row = TREE ? pc.q0 : pc.k0 + j * kKeys;
-                        const CUtensorMap *m = kv ? &tm_v : &tm_k;
-                        tma_load_3d(to, m, bar, 0, row, pc.g);
-                        tma_load_3d(to + kSlotBytes / 2, m, bar, 64, row, pc.g);
-                    } else if (kv == 0) {   // two halves of 64 dimensions, each 128 token rows
-                        for (int h = 0; h < 2; ++h) {
-                            const int row = (pc.g * p.n_pages + page[h]) * 64;
-                            tma_load_2d(to + h * 8192, &tm_kc, bar, 0, row);
-                            tma_load_2d(to + kSlotBytes / 2 + h * 8192, &tm_kc, bar, 64, row);
+                    if (lane == 0) {
+                        uint8_t *to = ring + slot * kSlotBytes;
+                        uint64_t *bar = &ct.full[slot];
+                        mbar_expect_tx(bar, kSlotBytes);
+                        if (!paged) {
+                            const int row = TREE ? pc.q0 : pc.k0 + j * kKeys;
+                            const CUtensorMap *m = kv ? &tm_v : &tm_k;
+                            tma_load_3d(to, m, bar, 0, row, pc.g);
+                            tma_load_3d(to + kSlotBytes / 2, m, bar, 64, row, pc.g);
+                        } else if (kv == 0) {   // two halves of 64 dimensions, each 128 token rows
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int row = page[h] * 64;
+                                tma_load_2d(to + h * 8192, &tm_kc, bar, 0, row);
+                                tma_load_2d(to + kSlotBytes / 2 + h * 8192, &tm_kc, bar, 64, row);
+                            }
+                        } else {                // two pages of 128 dimension rows
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_2d(to + h * 16384, &tm_vc, bar, 0, page[h] * 128);
                         }
-                    } else {                // two pages of 128 dimension rows
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_2d(to + h * 16384, &tm_vc, bar, 0, (pc.g * p.n_pages + page[h]) * 128);
+                    }
+                    if (kv == 0 && j == pc.s0) load_q();   // behind the first K: the last piece may still read Q
+                    if (!ok) {
+                        ++it;
+                        break;
                     }
                 }
-                if (!ok) break;
             }
             if (lane == 0 && ok) describe(p, pc);
         }
     } else if (warp == 9) {
         // ---------------- products, issued by one lane
-        if (lane == 0) {
-            constexpr uint32_t kDesc = idesc(F16 ? 0 : 1, kRows, 128);
-            const uint32_t ring0 = smem_u32(ring), q0 = smem_u32(smem + kOffQ);
-            Walk<TREE> walk(p, ct);
-            Piece pc;
-            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-            bool ok = true;
-            auto logits = [&](int i, int kit) {
-                const uint32_t a = q0 + i * kQBytes, b = ring0 + (kit % kSlots) * kSlotBytes;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-                    mma<MmaKind::f16>(tmem + kColS + i * 128, sdesc(a + off), sdesc(b + off), kDesc, k > 0);
-                }
-                mma_commit(&ct.sfull[i]);
-            };
-            while (ok && walk.next(p, pc)) {
-                if (pc.s1 == pc.s0) continue;
-                const int last = pc.e[1] > pc.s0 ? 1 : 0;   // the stream that uses a slot last
-                if (!(ok = mbar_wait(&ct.full[it % kSlots], (uint32_t)(it / kSlots) & 1u, abort_flag))) break;
-                for (int i = 0; i < 2 && ok; ++i) {
-                    if (pc.e[i] <= pc.s0) continue;
-                    if (!(ok = mbar_wait(&ct.qready[i], nq[i]++ & 1u, abort_flag))) break;
-                    tc_fence_after();
-                    logits(i, it);
-                }
-                if (!ok) break;
-                mma_commit(&ct.empty[it % kSlots]);
-                for (int j = pc.s0; ok && j < pc.s1; ++j, it += 2) {
-                    const int vit = it + 1, kit = it + 2;
-                    const bool paged = TREE && j < pc.n - 1;
-                    const uint32_t v = ring0 + (vit % kSlots) * kSlotBytes;
-                    if (!(ok = mbar_wait(&ct.full[vit % kSlots], (uint32_t)(vit / kSlots) & 1u, abort_flag))) break;
-                    bool have_k = false;
-                    for (int i = 0; i < 2; ++i) {
-                        if (j >= pc.e[i]) continue;
-                        if (!(ok = mbar_wait(&ct.pready[i], np[i]++ & 1u, abort_flag))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint64_t b = paged ? sdesc(v + (k >> 2) * 16384 + (k & 3) * 32)
-                                                     : sdesc_mn128(v + k * 2048, 16384);
-                            mma_f16_ta(tmem + kColO + i * 128, tmem + kColS + i * 128 + k * 8, b,
-                                       paged ? kDesc : kDesc | kIdescBMn, j > pc.s0 || k > 0);
-                        }
-                        if (i == last) mma_commit(&ct.empty[vit % kSlots]);
-                        if (j + 1 < pc.e[i]) {
-                            if (!have_k && !(ok = mbar_wait(&ct.full[kit % kSlots], (uint32_t)(kit / kSlots) & 1u, abort_flag)))
-                                break;
-                            have_k = true;
-                            logits(i, kit);
-                            if (i == last) mma_commit(&ct.empty[kit % kSlots]);
-                        } else {
-                            mma_commit(&ct.ofull[i]);
-                        }
-                    }
-                }
-            }
-        }
-        __syncwarp();
-    } else {
-        // ---------------- softmax and epilogue of a stream, a thread per row
-        Walk<TREE> walk(p, ct);
-        Piece pc;
-        const int st = warp >> 2, r = tid & 127, G = p.group;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
-        uint8_t *sq = smem + kOffQ + st * kQBytes;
-        const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
-        int base = 0, step0 = 0, seq_no = 0;
-        uint32_t ns = 0, no = 0;
+        constexpr uint32_t kDesc = idesc(F16 ? 0 : 1, kRows, 128);
+        const uint64_t q_desc = sdesc(smem_u32(smem + kOffQ)), k_desc = sdesc(smem_u32(ring));
+        const uint64_t v_desc = sdesc_mn128(smem_u32(ring), 16384);
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, cleaned = 0;
         bool ok = true;
-        while (ok && walk.next(p, pc)) {
-            const int mine = min(pc.rows - st * kRows, kRows), row = pc.row0 + st * kRows + r;
-            const int end = pc.e[st];
-            ++seq_no;
-            if (end > pc.s0) {
-                // the stream's rows into shared memory, zeros behind the last (their logits are read by no one)
+        Pieces pieces{ct};
+        const Piece *pp;
+        auto logits = [&](int i, int kit) {
+            const uint64_t a = q_desc + (uint64_t)(i * (kQBytes >> 4)), b = k_desc + (uint64_t)((kit % kSlots) * (kSlotBytes >> 4));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 x[8];
-                    const int ch = r & 15;
+            for (int k = 0; k < 8; ++k) {
+                const int off = (k >> 2) * 1024 + (k & 3) * 2;
+                mma<MmaKind::f16>(tmem + kColS + i * 128, a + off, b + off, kDesc, k > 0);
+            }
+            mma_commit(&ct.sfull[i]);
+        };
+        while (ok) {
+            if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
+            if (lane == 0) {
+                const int s0 = pp->s0, s1 = pp->s1, e0 = pp->e[0], e1 = pp->e[1], n = pp->n, lk = pp->lk;
+                const int low = TREE ? 0 : Seq<TREE>::keys_of(pp->lq, lk, pp->tok0);
+                if (s1 > s0) {
+                    const int last = e1 > s0 ? 1 : 0;   // the stream that uses a slot last
+                    ok = mbar_wait(&ct.full[it % kSlots], (uint32_t)(it / kSlots) & 1u, abort_flag);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int a = (r >> 4) + 8 * (8 * h + i), qr = pc.row0 + st * kRows + a;
-                        x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (a < mine) {
-                            const int tok = qr / G, hd = pc.g * G + qr - tok * G;
-                            x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q.p) +
-                                                                    (int64_t)(pc.q0 + tok) * p.q.token +
-                                                                    (int64_t)hd * p.q.head + 8 * ch);
+                    for (int i = 0; i < 2; ++i) {
+                        const int e = i ? e1 : e0;
+                        if (!ok || e <= s0) continue;
+                        if (!(ok = mbar_wait(&ct.qfull[i], nq[i]++ & 1u, abort_flag))) continue;
+                        tc_fence_after();
+                        logits(i, it);
+                        if (e == s0 + 1) mma_commit(&ct.qempty[i]);
+                    }
+                    if (ok) mma_commit(&ct.empty[it % kSlots]);
+                    for (int j = s0; ok && j < s1; ++j, it += 2) {
+                        const int vslot = (it + 1) % kSlots, kit = it + 2;
+                        const bool paged = TREE && j < n - 1;
+                        if (!(ok = mbar_wait(&ct.full[vslot], (uint32_t)((it + 1) / kSlots) & 1u, abort_flag))) break;
+                        if (TREE ? !paged || (j + 1) * kKeys > lk : (j + 1) * kKeys > low) {
+                            mbar_arrive(&ct.dirty);   // V has landed: warps 10 and 11 clear what must not be read
+                            if (!(ok = mbar_wait(&ct.clean, cleaned++ & 1u, abort_flag))) break;
+                        }
+                        bool have_k = false;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int e = i ? e1 : e0;
+                            if (!ok || j >= e) continue;
+                            if (!(ok = mbar_wait(&ct.pready[i], np[i]++ & 1u, abort_flag))) continue;
+                            tc_fence_after();
+                            const uint32_t o = tmem + kColO + i * 128, w = tmem + kColS + i * 128;
+                            if (paged) {
+                                const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_f16_ta(o, w + k * 8, b + (k >> 2) * 1024 + (k & 3) * 2, kDesc, k > 0 || j > s0);
+                            } else {
+                                const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) mma_f16_ta(o, w + k * 8, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
+                            }
+                            if (i == last) mma_commit(&ct.empty[vslot]);
+                            if (j + 1 < e) {
+                                if (!have_k) {
+                                    ok = mbar_wait(&ct.full[kit % kSlots], (uint32_t)(kit / kSlots) & 1u, abort_flag);
+                                    if (!ok) continue;
+                                    have_k = true;
+                                }
+                                logits(i, kit);
+                                if (i == last) mma_commit(&ct.empty[kit % kSlots]);
+                                if (e == j + 2) mma_commit(&ct.qempty[i]);
+                            } else {
+                                mma_commit(&ct.ofull[i]);
+                            }
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int a = (r >> 4) + 8 * (8 * h + i);
-                        *reinterpret_cast<uint4 *>(sq + (ch >> 3) * 16384 + a * 128 + (((ch & 7) ^ (a & 7)) << 4)) = x[i];
-                    }
                 }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ct.qready[st]);
-            }
-            // what this row sees
-            int lim = 0, low = 0, high = 0;             // prompts: keys of this row, of the tile's first and last row
-            int low_st = 0;                             // and of the stream's first
-            unsigned long long nodes = 0ull;            // trees: of the drafts
-            if constexpr (TREE) {
-                if (end == pc.n && end > pc.s0) nodes = ancestors(p, pc, min(row / G, pc.lq - 1));
+                pieces.done();
             } else {
-                Seq<TREE> q;
-                q.lk = pc.lk;
-                q.lq = pc.lq;
-                lim = q.limit(p, min(row, pc.row0 + pc.rows - 1));
-                low = q.limit(p, pc.row0);
-                low_st = q.limit(p, min(pc.row0 + st * kRows, pc.row0 + pc.rows - 1));
-                high = q.limit(p, pc.row0 + pc.rows - 1);
+                ++pieces.no;
             }
-            float m = -INFINITY, l = 0.0f;
-            for (int j = pc.s0; j < end; ++j) {
-                if (!(ok = wait_all(&ct.sfull[st], ns++ & 1u, abort_flag))) break;
-                tc_fence_after();
-                const bool paged = TREE && j < pc.n - 1;
-                int va = 0, vb = 0;
-                if (paged) {
-                    va = ct.info[(step0 + j - pc.s0) % kInfo][0];
-                    vb = ct.info[(step0 + j - pc.s0) % kInfo][1];
-                }
-                // the lowest stream at work clears V where not every row sees all of it
-                const bool partial = TREE ? !paged || va < 64 || vb < 64 : (j + 1) * kKeys > low;
-                const bool cleans = partial && (st == 0 || j >= pc.e[0]);
-                if (cleans) {
-                    const int vit = base + 2 * (j - pc.s0) + 1;
-                    if (!(ok = wait_all(&ct.full[vit % kSlots], (uint32_t)(vit / kSlots) & 1u, abort_flag))) break;
-                    uint8_t *v = ring + (vit % kSlots) * kSlotBytes;
-                    if (!paged) {   // this thread's token
-                        const bool gone = TREE ? r >= pc.lq : j * kKeys + r >= high;
-                        bool bad = false;
-#pragma unroll 4
+            ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
+        }
+    } else if (warp >= 10) {
+        // ---------------- values at places that not every row sees: cleared before the product reads them
+        Pieces pieces{ct};
+        const Piece *pp;
+        bool ok = true;
+        int base = 0;
+        uint32_t nd = 0;
+        const int t64 = tid - 320;
+        while (ok) {
+            if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
+            const int s0 = pp->s0, s1 = pp->s1, n = pp->n, lq = pp->lq, lk = pp->lk;
+            const int low = TREE ? 0 : Seq<TREE>::keys_of(lq, lk, pp->tok0);
+            const int high = TREE ? lq : Seq<TREE>::keys_of(lq, lk, min(pp->tok0 + 2 * p.toks, lq) - 1);
+            // only a run's last steps can hold such places
+            for (int j = TREE ? max(s0, lk / kKeys) : max(s0, low / kKeys); ok && j < s1; ++j) {
+                const bool paged = TREE && j < n - 1;
+                const int vit = base + 2 * (j - s0) + 1, vslot = vit % kSlots;
+                if (!(ok = wait_all(&ct.dirty, nd++ & 1u, abort_flag) &&
+                           wait_all(&ct.full[vslot], (uint32_t)(vit / kSlots) & 1u, abort_flag)))
+                    break;
+                uint8_t *v = ring + vslot * kSlotBytes;
+                bool bad = false;
+#pragma unroll 1
+                for (int r = t64; r < 128; r += 64) {
+                    if (!paged) {   // a token
+                        const bool gone = (TREE ? r : j * kKeys + r) >= high;
+#pragma unroll 8
                         for (int ch = 0; ch < 16; ++ch) {
                             uint4 *x = reinterpret_cast<uint4 *>(v + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
                             if (gone) {
@@ -694,11 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
                         }
-                        if (bad) ct.bad[seq_no & 1] = seq_no + 1;
-                    } else {        // this thread's dimension: every row sees the tokens that are there
+                    } else {        // a dimension: every row sees the tokens that are there
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const int valid = h ? vb : va;
+                            const int valid = min(max(lk - j * kKeys - 64 * h, 0), 64);
                             for (int ch = valid >> 3; ch < 8; ++ch) {
                                 uint8_t *x = v + h * 16384 + r * 128 + ((ch ^ (r & 7)) << 4);
                                 if (8 * ch >= valid) {
@@ -710,9 +820,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    fence_proxy_async();
-                    __syncwarp();
                 }
+                if (bad) ct.pieces[pieces.no % kPieces].bad = 1;
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ct.clean);
+            }
+            base += 2 * (s1 - s0);
+            __syncwarp();
+            if (lane == 0) pieces.done();
+            else ++pieces.no;
+        }
+    } else {
+        // ---------------- softmax and epilogue of a stream, a thread per row
+        const int st = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
+        uint8_t *stage = smem + kOffStage + warp * kStageBytes;
+        const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
+        const int my_tok = st * p.toks + (int)(r * p.by_group >> 16);   // this row's token in a tile
+        Pieces pieces{ct};
+        const Piece *pp;
+        int step0 = 0;
+        uint32_t ns = 0, no = 0;
+        bool ok = true;
+        while (ok) {
+            if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
+            const int s0 = pp->s0, end = pp->e[st], n = pp->n;
+            // what this row sees
+            int lim = 0, low = 0;                       // prompts: keys of this row, of the stream's first one
+            unsigned long long nodes = 0ull;            // trees: of the drafts
+            if constexpr (TREE) {
+                if (end == n && end > s0) nodes = ancestors(p, pp->q0, pp->lq, min(pp->tok0 + my_tok, pp->lq - 1));
+            } else {
+                lim = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + my_tok, pp->lq - 1));
+                low = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + st * p.toks, pp->lq - 1));
+            }
+            float m = -INFINITY, l = 0.0f;
+            for (int j = s0; j < end; ++j) {
+                if (!(ok = wait_all(&ct.sfull[st], ns++ & 1u, abort_flag))) break;
+                tc_fence_after();
                 uint32_t v0[4][16], v1[4][16];
                 tmem_ld64_nowait(tS, v0);
                 tmem_ld64_nowait(tS + 64, v1);
@@ -722,26 +869,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     reg_fence(v0[i]);
                     reg_fence(v1[i]);
                 }
-                if (TREE ? partial : (j + 1) * kKeys > low_st) {
-                    uint32_t see[4];
-                    if constexpr (TREE) {
+                if constexpr (TREE) {
+                    const bool paged = j < n - 1;
+                    const int va = paged ? ct.info[(step0 + j - s0) % kInfo][0] : 0;
+                    const int vb = paged ? ct.info[(step0 + j - s0) % kInfo][1] : 0;
+                    if (va < 64 || vb < 64) {
                         const unsigned long long a = paged ? (va >= 64 ? ~0ull : (1ull << va) - 1ull) : nodes;
                         const unsigned long long b = paged ? (vb >= 64 ? ~0ull : (1ull << vb) - 1ull) : 0ull;
-                        see[0] = (uint32_t)a;
-                        see[1] = (uint32_t)(a >> 32);
-                        see[2] = (uint32_t)b;
-                        see[3] = (uint32_t)(b >> 32);
-                    } else {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int left = lim - j * kKeys - 32 * w;
-                            see[w] = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                        for (int i = 0; i < 64; ++i) {
+                            const uint32_t wa = i < 32 ? (uint32_t)a : (uint32_t)(a >> 32), wb = i < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
+                            if (!(wa & 1u << (i & 31))) v0[i >> 4][i & 15] = 0xFF800000u;
+                            if (!(wb & 1u << (i & 31))) v1[i >> 4][i & 15] = 0xFF800000u;
                         }
                     }
+                } else if ((j + 1) * kKeys > low) {
+                    const int left = lim - j * kKeys;
 #pragma unroll
                     for (int i = 0; i < 64; ++i) {
-                        if (!(see[i >> 5] >> (i & 31) & 1u)) v0[i >> 4][i & 15] = 0xFF800000u;
-                        if (!(see[2 + (i >> 5)] >> (i & 31) & 1u)) v1[i >> 4][i & 15] = 0xFF800000u;
+                        if (i >= left) v0[i >> 4][i & 15] = 0xFF800000u;
+                        if (64 + i >= left) v1[i >> 4][i & 15] = 0xFF800000u;
                     }
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -753,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                                    __uint_as_float(v1[i >> 4][(i & 15) + 1])));
                 }
                 const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                if (j == pc.s0) {
+                if (j == s0) {
                     m = now;
                 } else {
                     const bool risen = now > m + rise;
@@ -803,59 +950,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += a + b;
             }
             if (!ok) break;
-            if (mine > 0) {
-                if (end > pc.s0) {
+            const int rows = pp->rows[st];
+            if (rows > (warp & 3) * 32 || end > s0) {
+                if (end > s0) {
                     if (!(ok = wait_all(&ct.ofull[st], no++ & 1u, abort_flag))) break;
                     tc_fence_after();
                 }
-                const bool whole = pc.s0 == 0 && pc.s1 == pc.n;
-                const bool fix = ct.bad[seq_no & 1] == seq_no + 1;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                const int tok = row / G;
-                const size_t at = (size_t)(pc.q0 + tok) * p.n_heads + pc.g * G + (row - tok * G);
-                const size_t slot = 2 * (size_t)blockIdx.x + (pc.s0 > 0 ? 0 : 1);
-                const int in_tile = st * kRows + r;
-#pragma unroll 1
-                for (int d = 0; d < 128; d += 16) {
-                    uint32_t o[16];
-                    __syncwarp();
-                    if (end > pc.s0) {
-                        tmem_ld16_nowait(tO + d, o);
-                        tmem_wait_ld();
-                        reg_fence(o);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = 0u;
-                    }
-                    if (r >= mine) continue;
-                    if (fix) {   // values that are not finite, where this row sees them
-                        const int t0 = TREE ? 0 : max(low / kKeys, pc.s0) * kKeys, t1 = TREE ? pc.lq : min(lim, pc.s1 * kKeys);
-                        for (int t = t0; t < t1; ++t) {
-                            if (TREE && !(nodes >> t & 1ull)) continue;
-                            const uint16_t *v = static_cast<const uint16_t *>(p.v.p) +
-                                                (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token + (int64_t)pc.g * p.v.head + d;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (not_finite<F16>(v[i]) & 0xFFFFu) o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<F16>(v[i]));
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float x[4] = {__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                            __uint_as_float(o[i + 3])};
-                        if (whole) store4<F16>(p, at * 128 + d + i, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-                        else p.part[(slot * 32 + (d + i) / 4) * p.rows_cap + in_tile] = make_float4(x[0], x[1], x[2], x[3]);
-                    }
-                }
-                __syncwarp();
+                finish<F16, TREE>(p, *pp, end > s0, tO, stage, m, l, lim, low, nodes, my_tok, rows);
                 tc_fence_before();
-                if (r < mine) {
-                    if (!whole) p.ml[slot * p.rows_cap + in_tile] = make_float2(m * c, l);
-                    else if (p.lse) p.lse[at] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
-                }
             }
-            base += 2 * (pc.s1 - pc.s0);
-            step0 += pc.s1 - pc.s0;
+            step0 += pp->s1 - s0;
+            __syncwarp();
+            if (lane == 0) pieces.done();
+            else ++pieces.no;
         }
         tc_fence_before();
     }
@@ -889,8 +996,10 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     if (d.x == 0) return;
     Seq<TREE> q;
     q.load(p, d.y, false);
-    const int rows = min(q.lq * p.group - d.w, kTileRows), in_tile = blockIdx.y * 32 + lane;
-    if ((int)blockIdx.y * 32 >= rows) return;
+    const int in_tile = blockIdx.y * 32 + lane, st = blockIdx.y >> 2, r = in_tile & (kRows - 1);
+    const int tok = (int)(r * p.by_group >> 16), token = d.w + st * p.toks + tok;
+    const bool mine = tok < p.toks && token < q.lq;
+    if (!__syncthreads_or(mine)) return;
     int parts = 0;   // shares behind this one
     for (int c0 = 1;; c0 += 32) {
         const long long c = blockIdx.x + (long long)(c0 + lane) * step;
@@ -901,7 +1010,6 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
             break;
         }
     }
-    const bool mine = in_tile < rows;
     auto slot = [&](int i) { return 2 * ((size_t)blockIdx.x + (size_t)i * step) + (i == 0 ? 1 : 0); };
     float M = -INFINITY, L = 0.0f;
     if (mine) {
@@ -928,8 +1036,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
                 o[e].w = fmaf(f, y.w, o[e].w);
             }
         }
-        const int row = d.w + in_tile, tok = row / p.group;
-        const size_t at = (size_t)(q.q0 + tok) * p.n_heads + d.z * p.group + (row - tok * p.group);
+        const size_t at = (size_t)(q.q0 + token) * p.n_heads + d.z * p.group + (r - tok * p.group);
         const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -938,12 +1045,13 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
     }
 }
 
-int rows_cap(long long rows) {
-    return rows >= kTileRows ? kTileRows : (int)((rows + 31) / 32 * 32);
+// Rows of a tile that `tokens` tokens can fill.
+int rows_cap(int tokens, int group) {
+    return tokens > kRows / group ? 2 * kRows : (tokens * group + 31) / 32 * 32;
 }
 
 template <bool F16, bool TREE>
-qsa_status launch_typed(const CUtensorMap (&m)[4], const Params &p, int grid, bool split, cudaStream_t s) {
+qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bool split, cudaStream_t s) {
     static std::mutex mu;
     static bool opted_in[64] = {false};
     int dev = 0;
@@ -959,7 +1067,8 @@ qsa_status launch_typed(const CUtensorMap (&m)[4], const Params &p, int grid, bo
             opted_in[dev] = true;
         }
     }
-    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3], p);
+    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3],
+                          m[4], p);
     if (st != QSA_OK || !split) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32));
@@ -976,7 +1085,6 @@ qsa_status launch_typed(const CUtensorMap (&m)[4], const Params &p, int grid, bo
 template <bool TREE>
 qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     Params p{};
-    p.q = a.q;
     p.v = a.v;
     p.cu_q = a.cu_q;
     p.cu_k = a.cu_k;
@@ -986,6 +1094,8 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.n_heads = a.n_heads;
     p.n_kv = a.n_kv_heads;
     p.group = a.n_heads / a.n_kv_heads;
+    p.toks = kRows / p.group;
+    p.by_group = (65536u + (uint32_t)p.group - 1u) / (uint32_t)p.group;
     p.scale = a.scale;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.out = a.out;
@@ -999,29 +1109,31 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.n_pages = a.table.n_pages;
     p.n_tokens = a.n_tokens;
     p.flags = a.flags;
-    p.rows_cap = rows_cap((long long)a.total_q * p.group);
+    p.rows_cap = rows_cap(a.total_q, p.group);
     char *ws = static_cast<char *>(a.ws) + 256;
     p.desc = reinterpret_cast<int4 *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + kMaxCtas * 2 * sizeof(int4));
     p.part = reinterpret_cast<float4 *>(ws + kMaxCtas * 2 * (sizeof(int4) + (size_t)p.rows_cap * sizeof(float2)));
     const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
-    p.row_tiles = TREE ? (a.max_nodes * p.group + kTileRows - 1) / kTileRows : 1;
+    p.row_tiles = TREE ? (a.max_nodes + 2 * p.toks - 1) / (2 * p.toks) : 1;
     p.shares = ctas / p.row_tiles;
     const int grid = p.shares * p.row_tiles;
     // the longest run that the sizes allow
     const bool split = (TREE ? 64ll * a.table.max_pages + kKeys : (long long)a.total_k) > kWhole * kKeys;
-    CUtensorMap m[4];
+    CUtensorMap m[5];
     const Rows16 &k = a.total_k > 0 ? a.k : a.q, &v = a.total_k > 0 ? a.v : a.q;   // without keys nothing is loaded
     const int rows = a.total_k > 0 ? a.total_k : 1, heads = a.total_k > 0 ? a.n_kv_heads : 1;
     qsa_status st;
-    if ((st = get_rows_map(&m[0], k, rows, heads, kKeys)) != QSA_OK || (st = get_rows_map(&m[1], v, rows, heads, kKeys)) != QSA_OK)
+    if ((st = get_rows_map(&m[0], a.q, a.total_q, a.n_heads, true, p.toks, p.group)) != QSA_OK ||
+        (st = get_rows_map(&m[1], k, rows, heads, false, kKeys, 1)) != QSA_OK ||
+        (st = get_rows_map(&m[2], v, rows, heads, false, kKeys, 1)) != QSA_OK)
         return st;
-    m[2] = m[0];
     m[3] = m[1];
+    m[4] = m[2];
     if (TREE) {
         const uint64_t pages = (uint64_t)a.n_kv_heads * a.table.n_pages;
-        if ((st = get_map(&m[2], a.kcache, 2, 128, pages * 64, 64)) != QSA_OK ||
-            (st = get_map(&m[3], a.vcache_t, 2, 64, pages * 128, 128)) != QSA_OK)
+        if ((st = get_map(&m[3], a.kcache, 2, 128, pages * 64, 64)) != QSA_OK ||
+            (st = get_map(&m[4], a.vcache_t, 2, 64, pages * 128, 128)) != QSA_OK)
             return st;
     }
     return a.dt == QSA_F16 ? launch_typed<true, TREE>(m, p, grid, split, s) : launch_typed<false, TREE>(m, p, grid, split, s);
@@ -1030,7 +1142,7 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t attention_ws_bytes(int rows, int n_heads, int n_kv_heads) {
-    const int cap = rows_cap((long long)rows * (n_heads / n_kv_heads));
+    const int cap = rows_cap(rows, n_heads / n_kv_heads);
     return 256 + (size_t)kMaxCtas * 2 * (sizeof(int4) + (size_t)cap * (sizeof(float2) + 32 * sizeof(float4)));
 }
 qsa_status launch_prompt_attention(const DenseArgs &a, cudaStream_t s) { return launch<false>(a, s); }

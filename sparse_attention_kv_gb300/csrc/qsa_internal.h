@@ -257,7 +257,8 @@ struct PagesAppendArgs {
     int n_kv_heads;
     void *kcache, *vcache_t;
 };
-qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads, uint32_t box_tokens);
+qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads, bool heads_inner, uint32_t box_tokens,
+                        uint32_t box_heads);
 qsa_status launch_pages_append(const PageTable &t, const PagesAppendArgs &a, cudaStream_t s);
 
 // Dense attention: causal over packed rows, or a tree of drafts over pages.

@@ -85,15 +85,23 @@ qsa_status get_map(CUtensorMap *out, const void *ptr, int esize, uint32_t inner,
     return QSA_OK;
 }
 
-// Rows of 128 16-bit values as [heads][tokens][128] with any strides: boxes of 64 values x box_tokens of one head.
-// Not cached: a call's rows are new.
-qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads, uint32_t box_tokens) {
+// Rows of 128 16-bit values with any strides, as [heads][tokens][128] or, heads_inner, [tokens][heads][128]: boxes of
+// 64 values x box_tokens x box_heads.  Not cached: a call's rows are new.
+qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads, bool heads_inner, uint32_t box_tokens,
+                        uint32_t box_heads) {
     auto fn = encode_fn();
     if (!fn) return fail(QSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t dims[3] = {128, (cuuint64_t)tokens, (cuuint64_t)heads};
-    // a stride along a single entry is never used; the encoder still wants a multiple of 16 bytes
-    const cuuint64_t strides[2] = {tokens > 1 ? (cuuint64_t)x.token * 2 : 256, heads > 1 ? (cuuint64_t)x.head * 2 : 256};
-    const cuuint32_t box[3] = {64, box_tokens, 1}, estr[3] = {1, 1, 1};
+    const int t = heads_inner ? 2 : 1, h = 3 - t;
+    cuuint64_t dims[3] = {128, 0, 0}, strides[2];
+    cuuint32_t box[3] = {64, 0, 0};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    dims[t] = (cuuint64_t)tokens;
+    dims[h] = (cuuint64_t)heads;
+    box[t] = box_tokens;
+    box[h] = box_heads;
+    // a stride along a single entry is never used
+    strides[t - 1] = tokens > 1 ? (cuuint64_t)x.token * 2 : 256;
+    strides[h - 1] = heads > 1 ? (cuuint64_t)x.head * 2 : 256;
     const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x.p), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
