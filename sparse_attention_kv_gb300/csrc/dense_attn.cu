@@ -39,18 +39,20 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kSoftWarps = 16;        // two threads a row, each with half of a step's keys and of the output's dimensions
 constexpr int kRows = 128;            // rows of a stream (TMEM lanes)
 constexpr int kKeys = 128;            // keys of a step
 constexpr int kSlots = 4;
 constexpr int kSlotBytes = kKeys * 128 * 2;
 constexpr int kQBytes = kRows * 128 * 2;
-constexpr int kStageBytes = 4096;     // per softmax warp: 32 rows of 128 bytes on their way out
+constexpr int kStageBytes = 2048;     // per softmax warp: 32 rows of 64 bytes on their way out
 constexpr int kPieces = 4;            // pieces that are published ahead
 constexpr int kInfo = 8;              // steps whose page limits are held: more than the ring holds
 constexpr int kMaxCtas = 152;
 constexpr int kWhole = 4;             // runs of so few steps are not split
-constexpr int kMinShare = 4;          // fewest steps (and run beginnings) a CTA is started for
+constexpr int kRunKeys = 256;         // what a run's beginning and end cost, in keys
+constexpr int kMinShare = 512;        // least work, in keys, that a CTA is started for
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
 
@@ -93,20 +95,21 @@ struct Piece {
 };
 
 struct Ctrl {
-    uint64_t full[kSlots], empty[kSlots], dirty, clean;
+    uint64_t full[kSlots], empty[kSlots], dirty, clean, turn[2];
     uint64_t qfull[2], qempty[2], sfull[2], pready[2], ofull[2];
     uint64_t pfull[kPieces], pempty[kPieces];
-    uint64_t drain;
+    uint64_t drain[2];
     Piece pieces[kPieces];
     uint32_t tmem;
     int abort;
     int info[kInfo][2];   // valid tokens in each page of a step
+    float swap[2][2][kRows];   // what the two threads of a row tell each other, by stream and half
 };
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQBytes;
 constexpr int kOffStage = kOffRing + kSlots * kSlotBytes;
-constexpr int kOffCtrl = kOffStage + 8 * kStageBytes;
-constexpr int kSmem = 1024 + kOffCtrl + (int)sizeof(Ctrl);
+constexpr int kOffCtrl = kOffStage + kSoftWarps * kStageBytes;
+constexpr int kSmem = kOffCtrl + (int)sizeof(Ctrl);
 static_assert(kSmem <= 232448, "shared memory");
 
 __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
@@ -122,28 +125,32 @@ __device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t parity, volatil
     }
 }
 
+// The same value in every lane, so that the compiler may hold it (and what follows from it) once per warp: the descriptors of
+// the products are taken from uniform registers, and moving them there for each one takes longer than forming it.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
+}
+// The 64 threads of a pair of warps, which share their rows.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    int any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"((int)x), "r"(id)
+        : "memory");
+    return any != 0;
+}
+
 // ------------------------------------------------------------------ the runs and the shares
 
-// sum of floor((a t + b) / m) over t < n, by the Euclidean steps of counting lattice points under a line
-__device__ __forceinline__ long long floor_sum(unsigned long long n, unsigned m, unsigned a, unsigned long long b) {
-    unsigned long long sum = 0;
-    while (true) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const unsigned long long top = a * n + b;
-        if (top < m) return (long long)sum;
-        n = top / m;
-        b = top % m;
-        const unsigned x = m;
-        m = a;
-        a = x;
-    }
+// a b / c: by 32-bit division where the sizes allow
+__device__ __forceinline__ long long mul_div(unsigned a, long long b, unsigned c) {
+    return b < (1 << 24) ? (long long)(a * (unsigned)b / c) : (long long)a * b / c;   // a, c <= 152
 }
 
 template <bool TREE>
@@ -178,18 +185,22 @@ struct Seq {
         if constexpr (TREE) return (lk + kKeys - 1) / kKeys + 1;   // the pages, then the drafts
         return (keys_of(lq, lk, min((t + 1) * 2 * p.toks, lq) - 1) + kKeys - 1) / kKeys;
     }
-    // Lengths of the runs of tiles 0 .. T - 1, each its steps and one more for its beginning and end.  With W tokens a
-    // tile, a full tile t has max(0, floor((W t + c) / 128)) steps, c = lk - lq + W + 127; the last tile ends at lk.
+    // The work of tiles 0 .. T - 1, in keys: what each tile's last token sees, and kRunKeys.  With W tokens a tile, that is
+    // max(0, lk - lq + (t + 1) W) for a full tile t; the last one's is lk.
     __device__ __forceinline__ long long cum(const Params &p, int T) const {
-        if constexpr (TREE) return T ? steps(p, 0) + 1 : 0;
-        long long sum = T;
+        if constexpr (TREE) return T ? lk + kKeys + kRunKeys : 0;
+        long long sum = (long long)T * kRunKeys;
         if (T == tiles && T > 0) {
-            sum += (max(lk, 0) + kKeys - 1) / kKeys;
+            sum += lk;
             --T;
         }
-        const int W = 2 * p.toks;
-        const long long c = (long long)lk - lq + W + kKeys - 1, t0 = c < 0 ? (-c + W - 1) / W : 0;
-        return T > t0 ? sum + floor_sum(T - t0, kKeys, W, c + t0 * W) : sum;
+        const int W = 2 * p.toks, c = lk - lq + W, t0 = c < 0 ? min((-c + W - 1) / W, T) : 0;
+        const long long n = T - t0;
+        return sum + n * (c + (long long)t0 * W) + W * (n * (n - 1) / 2);
+    }
+    __device__ __forceinline__ int work(const Params &p, int t) const {   // cum(t + 1) - cum(t)
+        if constexpr (TREE) return lk + kKeys + kRunKeys;
+        return keys_of(lq, lk, min((t + 1) * 2 * p.toks, lq) - 1) + kRunKeys;
     }
     // Keys that token i of lq sees.
     static __device__ __forceinline__ int keys_of(int lq, int lk, int i) { return min(max(lk - lq + i + 1, 0), lk); }
@@ -204,14 +215,14 @@ struct Walk {
 
     __device__ __forceinline__ bool next(const Params &p, Piece &pc) {
         while (at < x1 && s < p.n_seqs) {
-            const int n = q.steps(p, t);
+            const int n = q.steps(p, t), work = q.work(p, t);
             const long long from = at;
             int s0 = 0, s1 = n;
             bool take = from >= x0;
-            if (n > kWhole) {
-                const long long a = x0 - from - 1, b = x1 - from - 1;
-                s0 = a > 0 ? (int)(a < n ? a : n) : 0;
-                s1 = b < n ? (int)(b > 0 ? b : 0) : n;
+            if (n > kWhole) {   // the step that begins nearest to a border; both sides of it compute the same
+                const long long a = (x0 - from - kRunKeys + kKeys / 2) / kKeys, b = (x1 - from - kRunKeys + kKeys / 2) / kKeys;
+                s0 = x0 <= from || a <= 0 ? 0 : (int)(a < n ? a : n);
+                s1 = b <= 0 ? 0 : b < n && x1 < from + work ? (int)b : n;
                 take = s1 > s0;
             }
             pc.s = s;
@@ -236,7 +247,7 @@ struct Walk {
                 }
                 pc.e[i] = end;
             }
-            at += n + 1;
+            at += work;
             if (++t >= q.tiles) {
                 t = 0;
                 if (++g >= p.n_kv) {
@@ -263,7 +274,7 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 template <bool TREE>
 __device__ void find_share(const Params &p, Walk<TREE> &w) {
     const int lane = threadIdx.x & 31;
-    const int share = blockIdx.x / p.row_tiles;
+    const unsigned share = blockIdx.x / (unsigned)p.row_tiles;
     const bool tell = blockIdx.x == 0;
     Seq<TREE> &q = w.q;
     auto weight = [&](int s, bool say) -> long long {
@@ -279,8 +290,8 @@ __device__ void find_share(const Params &p, Walk<TREE> &w) {
     }
     long long used = (total + kMinShare - 1) / kMinShare;
     used = used < 1 ? 1 : used > p.shares ? p.shares : used;
-    w.x0 = share < used ? share * total / used : total;
-    w.x1 = share < used ? (share + 1) * total / used : total;
+    w.x0 = share < used ? mul_div(share, total, (unsigned)used) : total;
+    w.x1 = share < used ? mul_div(share + 1, total, (unsigned)used) : total;
     w.tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
     long long before = 0;
     w.at = w.x0;
@@ -305,8 +316,8 @@ __device__ void find_share(const Params &p, Walk<TREE> &w) {
     }
     if (w.s < p.n_seqs) {
         q.load(p, w.s, false);
-        const long long per = q.cum(p, q.tiles);
-        w.g = (int)((w.x0 - before) / per);
+        const long long per = q.cum(p, q.tiles), in_seq = w.x0 - before;
+        w.g = in_seq < (1ll << 31) && per < (1ll << 31) ? (int)((unsigned)in_seq / (unsigned)per) : (int)(in_seq / per);
         before += w.g * per;
         int lo = 0, hi = q.tiles;   // cum(lo) <= x0 - before < cum(hi)
         while (hi - lo > 1) {
@@ -364,9 +375,12 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
     constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
     return ((pair & e) == e ? 0xFFFFu : 0u) | ((pair & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
 }
+// acc + 0 x: NaN in a half once a value there is not finite
 template <bool F16>
-__device__ __forceinline__ bool any_not_finite(const uint4 &x) {
-    return (not_finite<F16>(x.x) | not_finite<F16>(x.y) | not_finite<F16>(x.z) | not_finite<F16>(x.w)) != 0u;
+__device__ __forceinline__ uint32_t probe(uint32_t x, uint32_t acc) {
+    if constexpr (F16) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
 }
 
 // The nodes a tree's row sees (one warp; every lane gets its own row's): bit j of the mask is node j.
@@ -427,12 +441,13 @@ __device__ __forceinline__ void store4(const Params &p, size_t at, float a, floa
     else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(pack16<F16>(a, b), pack16<F16>(c, d));
 }
 
-// The end of a piece for one warp's rows (a lane each): the output normalised, in whole 128-byte rows through `stage`, or the
-// partial as it is.  have: there is an O in tensor memory.
+// The end of a piece for a warp's 32 rows and 64 dimensions: the output normalised, through `stage` so that a row's bytes
+// are written together, or the partial as it is.  have: there is an O in tensor memory.
 template <bool F16, bool TREE>
 __device__ __forceinline__ void finish(const Params &p, const Piece &pc, bool have, uint32_t tO, uint8_t *stage, float m, float l,
-                                       int lim, int low, unsigned long long nodes, int my_tok, int rows) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = warp >> 2, r = threadIdx.x & 127, G = p.group;
+                                       int lim, unsigned long long nodes, int rows) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, G = p.group;
+    const int r = (warp & 3) * 32 + lane, d = half * 64;
     const bool whole = pc.s0 == 0 && pc.s1 == pc.n, mine = r < rows, fix = pc.bad != 0;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const size_t slot = 2 * (size_t)blockIdx.x + (pc.s0 > 0 ? 0 : 1);
@@ -440,81 +455,77 @@ __device__ __forceinline__ void finish(const Params &p, const Piece &pc, bool ha
     // values that are not finite are added where this row sees them: in the drafts, or from the first step that was cleared
     const int f0 = TREE ? 0 : max(Seq<TREE>::keys_of(pc.lq, pc.lk, pc.tok0) / kKeys, pc.s0) * kKeys;
     const int f1 = TREE ? (pc.s1 == pc.n ? pc.lq : 0) : min(lim, pc.s1 * kKeys);
-    const int wide = p.out_f32 ? 32 : 64;   // dimensions of a row's 128 staged bytes
-#pragma unroll 1
-    for (int d = 0; d < 128; d += 16) {
-        uint32_t o[16];
+    const size_t out0 = (size_t)(pc.q0 + pc.tok0 + st * p.toks) * p.n_heads + pc.g * G;
+    auto output = [&](int row) {   // the row of out that a row of the stream is
+        const int tok = (int)(row * p.by_group >> 16);
+        return out0 + (size_t)tok * p.n_heads + (row - tok * G);
+    };
+    uint32_t o[4][16];
+    if (have) {
+        tmem_ld64_nowait(tO, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reg_fence(o[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) o[i >> 4][i & 15] = 0u;
+    }
+    if (fix && mine) {
+        for (int t = f0; t < f1; ++t) {
+            if (TREE && !(nodes >> t & 1ull)) continue;
+            const uint16_t *v = static_cast<const uint16_t *>(p.v.p) + (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token +
+                                (int64_t)pc.g * p.v.head + d;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (not_finite<F16>(v[i]) & 0xFFFFu)
+                    o[i >> 4][i & 15] = __float_as_uint(__uint_as_float(o[i >> 4][i & 15]) + widen<F16>(v[i]));
+        }
+    }
+    auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
+    if (!whole) {
+        if (!mine) return;
+        float4 *part = p.part + (slot * 32 + d / 4) * p.rows_cap + in_tile;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) part[(i / 4) * p.rows_cap] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+        if (half == 0) p.ml[slot * p.rows_cap + in_tile] = make_float2(m * p.scale_log2, l);
+        return;
+    }
+    // 64 bytes of each row at a time; its 16-byte units are rotated by the row so that neither way meets a bank twice
+    uint8_t *line = stage + lane * 64;
+    const int turn = (lane >> 1) & 3;
+    auto drain = [&](int at) {   // four lanes write a row's 64 bytes, which begin at its byte `at`
         __syncwarp();
-        if (have) {
-            tmem_ld16_nowait(tO + d, o);
-            tmem_wait_ld();
-            reg_fence(o);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = 0u;
+        for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), row = (warp & 3) * 32 + rr;
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+            if (row < rows)
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + output(row) * (p.out_f32 ? 512 : 256) + at +
+                                           16 * (lane & 3)) = x;
         }
-        if (fix && mine) {
-            for (int t = f0; t < f1; ++t) {
-                if (TREE && !(nodes >> t & 1ull)) continue;
-                const uint16_t *v = static_cast<const uint16_t *>(p.v.p) + (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token +
-                                    (int64_t)pc.g * p.v.head + d;
+        __syncwarp();
+    };
+    if (p.out_f32) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (not_finite<F16>(v[i]) & 0xFFFFu) o[i] = __float_as_uint(__uint_as_float(o[i]) + widen<F16>(v[i]));
-            }
+        for (int h = 0; h < 64; h += 16) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4 *>(line + (((i >> 2) ^ turn) << 4)) =
+                    make_float4(val(h + i) * inv, val(h + i + 1) * inv, val(h + i + 2) * inv, val(h + i + 3) * inv);
+            drain(4 * (d + h));
         }
-        if (!whole) {
-            if (mine)
+    } else {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    p.part[(slot * 32 + (d + i) / 4) * p.rows_cap + in_tile] =
-                        make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-            continue;
-        }
-        // this row's 16-byte units, rotated by the row so that neither way meets a bank twice
-        if (p.out_f32) {
+        for (int h = 0; h < 64; h += 32) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const float4 x = make_float4(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv,
-                                             __uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                *reinterpret_cast<float4 *>(stage + lane * 128 + (((((d & 31) + i) >> 2) ^ (lane & 7)) << 4)) = x;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    w[x] = pack16<F16>(__uint_as_float(o[i + 2 * x]) * inv, __uint_as_float(o[i + 2 * x + 1]) * inv);
-                *reinterpret_cast<uint4 *>(stage + lane * 128 + (((((d & 63) + i) >> 3) ^ (lane & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-        if (((d + 16) & (wide - 1)) == 0) {   // 128 bytes of each row: eight lanes write a row's
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int rr = 4 * i + (lane >> 3), row = (warp & 3) * 32 + rr;
-                const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                if (row < rows) {
-                    const int tok = (int)(row * p.by_group >> 16);
-                    const size_t at = (size_t)(pc.q0 + pc.tok0 + st * p.toks + tok) * p.n_heads + pc.g * G + (row - tok * G);
-                    uint8_t *out = static_cast<uint8_t *>(p.out) + (at * 128 + (d + 16 - wide)) * (p.out_f32 ? 4 : 2);
-                    *reinterpret_cast<uint4 *>(out + 16 * (lane & 7)) = x;
-                }
-            }
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(line + (((i >> 3) ^ turn) << 4)) = make_uint4(
+                    pack16<F16>(val(h + i) * inv, val(h + i + 1) * inv), pack16<F16>(val(h + i + 2) * inv, val(h + i + 3) * inv),
+                    pack16<F16>(val(h + i + 4) * inv, val(h + i + 5) * inv), pack16<F16>(val(h + i + 6) * inv, val(h + i + 7) * inv));
+            drain(2 * (d + h));
         }
     }
-    __syncwarp();
-    if (mine) {
-        if (!whole) {
-            p.ml[slot * p.rows_cap + in_tile] = make_float2(m * p.scale_log2, l);
-        } else if (p.lse) {
-            const int tok = my_tok - st * p.toks;
-            const size_t at = (size_t)(pc.q0 + pc.tok0 + my_tok) * p.n_heads + pc.g * G + (r - tok * G);
-            p.lse[at] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
-        }
-    }
+    if (mine && half == 0 && p.lse) p.lse[output(r)] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
 }
 
 // The next published piece (a warp); false when the wait ran out.  A reader gives it back with done().
@@ -536,48 +547,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
                  const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem + kOffRing;
     Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + kOffCtrl);
     volatile int *abort_flag = &ct.abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&ct.full[i], 1);
-            mbar_init(&ct.empty[i], 1);
+            mbar_init(&ct.empty[i], 2);        // both streams
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.qfull[i], 1);
             mbar_init(&ct.qempty[i], 1);
             mbar_init(&ct.sfull[i], 1);
-            mbar_init(&ct.pready[i], 4);   // one arrival per warp of the stream
+            mbar_init(&ct.pready[i], 8);   // one arrival per warp of the stream
             mbar_init(&ct.ofull[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&ct.pfull[i], 1);
-            mbar_init(&ct.pempty[i], 11);  // every warp but the one that publishes
+            mbar_init(&ct.pempty[i], 19);  // every warp but the one that publishes
         }
-        mbar_init(&ct.dirty, 1);
-        mbar_init(&ct.clean, 2);           // warps 10 and 11
-        mbar_init(&ct.drain, 1);
+        mbar_init(&ct.turn[0], 1);
+        mbar_init(&ct.turn[1], 1);
+        mbar_init(&ct.dirty, 2);
+        mbar_init(&ct.clean, 1);
+        mbar_init(&ct.drain[0], 1);
+        mbar_init(&ct.drain[1], 1);
         ct.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     wait_prior_grid();   // nothing the caller wrote is read, and no tensor memory taken, before this
     allow_dependent_launch();
-    if (warp == 9) {
+    if (warp == 1) {
         tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ct.tmem;
+    const uint32_t tmem = (uint32_t)uniform((int)ct.tmem);
 
     int it = 0;   // slots of the ring used so far
-    if (warp == 8) {
+    if (warp == 0) {
         // ---------------- pieces and copies: Q, K and V of each step, K first
         if (lane == 0) {
             p.desc[2 * (size_t)blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -678,98 +691,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0 && ok) describe(p, pc);
         }
-    } else if (warp == 9) {
-        // ---------------- products, issued by one lane
+    } else if (warp == 1 || warp == 2) {
+        // ---------------- products of a stream, issued by one lane.  The streams take turns (a stream's 16 MMAs of a step
+        // run back to back while the other one's softmax does), and each waits for all it needs before its turn, so that
+        // its waits lie behind the other one's products.  An MMA takes 47 cycles to issue and 64 to form: one warp alone, with
+        // the waits between, issues both streams' more slowly than the tensor cores form them.
+        const int st = warp - 1;
         constexpr uint32_t kDesc = idesc(F16 ? 0 : 1, kRows, 128);
-        const uint64_t q_desc = sdesc(smem_u32(smem + kOffQ)), k_desc = sdesc(smem_u32(ring));
-        const uint64_t v_desc = sdesc_mn128(smem_u32(ring), 16384);
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0}, cleaned = 0;
+        const uint32_t smem0 = (uint32_t)uniform((int)smem_u32(smem));
+        const uint64_t q_desc = sdesc(smem0 + kOffQ + st * kQBytes), k_desc = sdesc(smem0 + kOffRing);
+        const uint64_t v_desc = sdesc_mn128(smem0 + kOffRing, 16384);
+        const uint32_t tS = tmem + kColS + st * 128, tO = tmem + kColO + st * 128;
+        uint32_t nq = 0, np = 0, cleaned = 0, turns = 0;
         bool ok = true;
         Pieces pieces{ct};
         const Piece *pp;
-        auto logits = [&](int i, int kit) {
-            const uint64_t a = q_desc + (uint64_t)(i * (kQBytes >> 4)), b = k_desc + (uint64_t)((kit % kSlots) * (kSlotBytes >> 4));
+        auto slot_full = [&](int i) { return wait_all(&ct.full[i % kSlots], (uint32_t)(i / kSlots) & 1u, abort_flag); };
+        auto my_turn = [&]() { return wait_all(&ct.turn[st], (turns++ & 1u) ^ (st == 0 ? 1u : 0u), abort_flag); };
+        auto logits = [&](int kit, bool last) {   // one lane
+            const uint64_t b = k_desc + (uint64_t)((kit % kSlots) * (kSlotBytes >> 4));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int off = (k >> 2) * 1024 + (k & 3) * 2;
-                mma<MmaKind::f16>(tmem + kColS + i * 128, a + off, b + off, kDesc, k > 0);
+                mma<MmaKind::f16>(tS, q_desc + off, b + off, kDesc, k > 0);
             }
-            mma_commit(&ct.sfull[i]);
+            mma_commit(&ct.sfull[st]);
+            mma_commit(&ct.empty[kit % kSlots]);
+            if (last) mma_commit(&ct.qempty[st]);
         };
         while (ok) {
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
-            if (lane == 0) {
-                const int s0 = pp->s0, s1 = pp->s1, e0 = pp->e[0], e1 = pp->e[1], n = pp->n, lk = pp->lk;
-                const int low = TREE ? 0 : Seq<TREE>::keys_of(pp->lq, lk, pp->tok0);
-                if (s1 > s0) {
-                    const int last = e1 > s0 ? 1 : 0;   // the stream that uses a slot last
-                    ok = mbar_wait(&ct.full[it % kSlots], (uint32_t)(it / kSlots) & 1u, abort_flag);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int e = i ? e1 : e0;
-                        if (!ok || e <= s0) continue;
-                        if (!(ok = mbar_wait(&ct.qfull[i], nq[i]++ & 1u, abort_flag))) continue;
-                        tc_fence_after();
-                        logits(i, it);
-                        if (e == s0 + 1) mma_commit(&ct.qempty[i]);
+            // a stream that is done with its steps still takes its turns and gives the other one's slots back
+            const int s0 = uniform(pp->s0), s1 = uniform(pp->s1), e = uniform(pp->e[st]), n = uniform(pp->n), lk = uniform(pp->lk);
+            const int low = TREE ? lk : uniform(Seq<TREE>::keys_of(pp->lq, lk, pp->tok0));
+            if (s1 > s0) {
+                ok = slot_full(it) && (e <= s0 || wait_all(&ct.qfull[st], nq++ & 1u, abort_flag)) && my_turn();
+                if (ok) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (e > s0) logits(it, e == s0 + 1);
+                        else mbar_arrive(&ct.empty[it % kSlots]);
+                        mbar_arrive(&ct.turn[st ^ 1]);
                     }
-                    if (ok) mma_commit(&ct.empty[it % kSlots]);
-                    for (int j = s0; ok && j < s1; ++j, it += 2) {
-                        const int vslot = (it + 1) % kSlots, kit = it + 2;
-                        const bool paged = TREE && j < n - 1;
-                        if (!(ok = mbar_wait(&ct.full[vslot], (uint32_t)((it + 1) / kSlots) & 1u, abort_flag))) break;
-                        if (TREE ? !paged || (j + 1) * kKeys > lk : (j + 1) * kKeys > low) {
-                            mbar_arrive(&ct.dirty);   // V has landed: warps 10 and 11 clear what must not be read
-                            if (!(ok = mbar_wait(&ct.clean, cleaned++ & 1u, abort_flag))) break;
-                        }
-                        bool have_k = false;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int e = i ? e1 : e0;
-                            if (!ok || j >= e) continue;
-                            if (!(ok = mbar_wait(&ct.pready[i], np[i]++ & 1u, abort_flag))) continue;
-                            tc_fence_after();
-                            const uint32_t o = tmem + kColO + i * 128, w = tmem + kColS + i * 128;
-                            if (paged) {
-                                const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_f16_ta(o, w + k * 8, b + (k >> 2) * 1024 + (k & 3) * 2, kDesc, k > 0 || j > s0);
-                            } else {
-                                const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) mma_f16_ta(o, w + k * 8, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
-                            }
-                            if (i == last) mma_commit(&ct.empty[vslot]);
-                            if (j + 1 < e) {
-                                if (!have_k) {
-                                    ok = mbar_wait(&ct.full[kit % kSlots], (uint32_t)(kit / kSlots) & 1u, abort_flag);
-                                    if (!ok) continue;
-                                    have_k = true;
-                                }
-                                logits(i, kit);
-                                if (i == last) mma_commit(&ct.empty[kit % kSlots]);
-                                if (e == j + 2) mma_commit(&ct.qempty[i]);
-                            } else {
-                                mma_commit(&ct.ofull[i]);
-                            }
-                        }
-                    }
+                    __syncwarp();
                 }
-                pieces.done();
-            } else {
-                ++pieces.no;
             }
-            ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
+            for (int j = s0; ok && j < s1; ++j, it += 2) {
+                const int vslot = (it + 1) % kSlots;
+                const bool paged = TREE && j < n - 1, more = j + 1 < s1;
+                if (!(ok = slot_full(it + 1))) break;
+                if ((j + 1) * kKeys > low || (TREE && !paged)) {
+                    if (lane == 0) mbar_arrive(&ct.dirty);   // V has landed: warp 3 clears what must not be read
+                    __syncwarp();
+                    if (!(ok = wait_all(&ct.clean, cleaned++ & 1u, abort_flag))) break;
+                }
+                if (!(ok = (!more || slot_full(it + 2)) && (j >= e || wait_all(&ct.pready[st], np++ & 1u, abort_flag)) && my_turn()))
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (j < e) {
+                        if (paged) {
+                            const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_f16_ta(tO, tS + k * 8, b + (k >> 2) * 1024 + (k & 3) * 2, kDesc, k > 0 || j > s0);
+                        } else {
+                            const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) mma_f16_ta(tO, tS + k * 8, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
+                        }
+                        if (j + 1 == e) mma_commit(&ct.ofull[st]);
+                        mma_commit(&ct.empty[vslot]);
+                    } else {
+                        mbar_arrive(&ct.empty[vslot]);
+                    }
+                    if (j + 1 < e) logits(it + 2, e == j + 2);
+                    else if (more) mbar_arrive(&ct.empty[(it + 2) % kSlots]);
+                    mbar_arrive(&ct.turn[st ^ 1]);
+                }
+                __syncwarp();
+            }
+            if (lane == 0) pieces.done();
+            else ++pieces.no;
         }
-    } else if (warp >= 10) {
+    } else if (warp == 3) {
         // ---------------- values at places that not every row sees: cleared before the product reads them
         Pieces pieces{ct};
         const Piece *pp;
         bool ok = true;
         int base = 0;
         uint32_t nd = 0;
-        const int t64 = tid - 320;
         while (ok) {
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
             const int s0 = pp->s0, s1 = pp->s1, n = pp->n, lq = pp->lq, lk = pp->lk;
@@ -785,23 +796,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *v = ring + vslot * kSlotBytes;
                 bool bad = false;
 #pragma unroll 1
-                for (int r = t64; r < 128; r += 64) {
+                for (int r = lane; r < kKeys; r += 32) {
                     if (!paged) {   // a token
-                        const bool gone = (TREE ? r : j * kKeys + r) >= high;
-#pragma unroll 8
-                        for (int ch = 0; ch < 16; ++ch) {
-                            uint4 *x = reinterpret_cast<uint4 *>(v + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                            if (gone) {
-                                *x = make_uint4(0u, 0u, 0u, 0u);
-                            } else {
-                                uint4 y = *x;
-                                if (any_not_finite<F16>(y)) {
-                                    bad = true;
-                                    y.x &= ~not_finite<F16>(y.x);
-                                    y.y &= ~not_finite<F16>(y.y);
-                                    y.z &= ~not_finite<F16>(y.z);
-                                    y.w &= ~not_finite<F16>(y.w);
-                                    *x = y;
+                        const int t = TREE ? r : j * kKeys + r;
+                        uint8_t *row = v + r * 128;
+                        if (t >= high) {
+#pragma unroll
+                            for (int ch = 0; ch < 16; ++ch)
+                                *reinterpret_cast<uint4 *>(row + (ch >> 3) * 16384 + ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (t >= low) {   // seen by some of the rows
+                            uint32_t acc[2] = {0u, 0u};
+#pragma unroll
+                            for (int ch = 0; ch < 16; ++ch) {   // in any order: the swizzle moves units within the row
+                                const uint4 x = *reinterpret_cast<const uint4 *>(row + (ch >> 3) * 16384 + (((ch ^ r) & 7) << 4));
+                                acc[0] = probe<F16>(x.x, acc[0]);
+                                acc[1] = probe<F16>(x.y, acc[1]);
+                                acc[0] = probe<F16>(x.z, acc[0]);
+                                acc[1] = probe<F16>(x.w, acc[1]);
+                            }
+                            if (not_finite<F16>(acc[0]) | not_finite<F16>(acc[1])) {
+                                bad = true;
+#pragma unroll 1
+                                for (int e = 0; e < 64; ++e) {
+                                    uint32_t *x = reinterpret_cast<uint32_t *>(row + (e >> 5) * 16384) + (e & 31);
+                                    *x &= ~not_finite<F16>(*x);
                                 }
                             }
                         }
@@ -832,11 +850,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             else ++pieces.no;
         }
     } else {
-        // ---------------- softmax and epilogue of a stream, a thread per row
-        const int st = warp >> 2, r = tid & 127;
+        // ---------------- softmax and epilogue of a stream, two threads a row
+        const int st = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
-        uint8_t *stage = smem + kOffStage + warp * kStageBytes;
+        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128 + half * 64;
+        const int pair = 1 + st * 4 + (warp & 3);   // barrier of the two warps of these rows
+        float *tell = &ct.swap[st][half][r], *hear = &ct.swap[st][half ^ 1][r];
         const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
         const int my_tok = st * p.toks + (int)(r * p.by_group >> 16);   // this row's token in a tile
         Pieces pieces{ct};
@@ -860,57 +879,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = s0; j < end; ++j) {
                 if (!(ok = wait_all(&ct.sfull[st], ns++ & 1u, abort_flag))) break;
                 tc_fence_after();
-                uint32_t v0[4][16], v1[4][16];
-                tmem_ld64_nowait(tS, v0);
-                tmem_ld64_nowait(tS + 64, v1);
+                uint32_t v[4][16];
+                tmem_ld64_nowait(tS + half * 64, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    reg_fence(v0[i]);
-                    reg_fence(v1[i]);
-                }
+                for (int i = 0; i < 4; ++i) reg_fence(v[i]);
                 if constexpr (TREE) {
                     const bool paged = j < n - 1;
-                    const int va = paged ? ct.info[(step0 + j - s0) % kInfo][0] : 0;
-                    const int vb = paged ? ct.info[(step0 + j - s0) % kInfo][1] : 0;
-                    if (va < 64 || vb < 64) {
-                        const unsigned long long a = paged ? (va >= 64 ? ~0ull : (1ull << va) - 1ull) : nodes;
-                        const unsigned long long b = paged ? (vb >= 64 ? ~0ull : (1ull << vb) - 1ull) : 0ull;
+                    const int valid = paged ? ct.info[(step0 + j - s0) % kInfo][half] : 0;
+                    if (valid < 64) {
+                        const unsigned long long see = paged ? (1ull << valid) - 1ull : half ? 0ull : nodes;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) {
-                            const uint32_t wa = i < 32 ? (uint32_t)a : (uint32_t)(a >> 32), wb = i < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
-                            if (!(wa & 1u << (i & 31))) v0[i >> 4][i & 15] = 0xFF800000u;
-                            if (!(wb & 1u << (i & 31))) v1[i >> 4][i & 15] = 0xFF800000u;
-                        }
+                        for (int i = 0; i < 64; ++i)
+                            if (!((i < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) & 1u << (i & 31))) v[i >> 4][i & 15] = 0xFF800000u;
                     }
                 } else if ((j + 1) * kKeys > low) {
-                    const int left = lim - j * kKeys;
+                    const int left = lim - j * kKeys - half * 64;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        if (i >= left) v0[i >> 4][i & 15] = 0xFF800000u;
-                        if (64 + i >= left) v1[i >> 4][i & 15] = 0xFF800000u;
-                    }
+                    for (int i = 0; i < 64; ++i)
+                        if (i >= left) v[i >> 4][i & 15] = 0xFF800000u;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], fmaxf(__uint_as_float(v0[i >> 4][i & 15]),
-                                                                       __uint_as_float(v0[i >> 4][(i & 15) + 1])));
-                    top[2 + ((i >> 1) & 1)] = fmaxf(top[2 + ((i >> 1) & 1)], fmaxf(__uint_as_float(v1[i >> 4][i & 15]),
-                                                                                   __uint_as_float(v1[i >> 4][(i & 15) + 1])));
-                }
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                if (j == s0) {
-                    m = now;
-                } else {
-                    const bool risen = now > m + rise;
-                    if (__any_sync(~0u, risen)) {
+                for (int i = 0; i < 64; i += 2)
+                    top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(v[i >> 4][i & 15]),
+                                                                       __uint_as_float(v[i >> 4][(i & 15) + 1])));
+                float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // Both threads of a row go by one reference.  The barrier also has both warps' logits in registers before
+                // either one's weights overwrite them.
+                if (j == s0 || pair_any(pair, now > m + rise)) {
+                    *tell = now;
+                    pair_sync(pair);
+                    now = fmaxf(now, *hear);
+                    if (j == s0) {
+                        m = now;
+                    } else {
                         // S of this step is complete, so every product before it is: O may be scaled in place
+                        const bool risen = now > m + rise;
                         const float f = risen ? ex2((m - now) * c) : 1.0f;
                         if (risen) m = now;
                         l *= f;
 #pragma unroll 1
-                        for (int d = 0; d < 128; d += 16) {
+                        for (int d = 0; d < 64; d += 16) {
                             uint32_t o[16];
                             tmem_ld16_nowait(tO + d, o);
                             tmem_wait_ld();
@@ -925,21 +935,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
                 f32x2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {   // 32 keys a round
+                for (int q = 0; q < 2; ++q) {   // 32 keys a round
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int k = 32 * q + 2 * i;
-                        const uint32_t a = k < 64 ? v0[(k & 63) >> 4][k & 15] : v1[(k & 63) >> 4][k & 15];
-                        const uint32_t b = k < 64 ? v0[(k & 63) >> 4][(k & 15) + 1] : v1[(k & 63) >> 4][(k & 15) + 1];
                         float y0, y1;
-                        unpack2(fma2(pack2(__uint_as_float(a), __uint_as_float(b)), c2, nm2), y0, y1);
+                        unpack2(fma2(pack2(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1])), c2, nm2), y0,
+                                y1);
                         y0 = ex2(y0);
                         y1 = ex2(y1);
                         sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
                         w[i] = pack16<F16>(y0, y1);
                     }
-                    tmem_st16(tS + 16 * q, w);
+                    tmem_st16(tS + 32 * half + 16 * q, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -952,12 +961,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const int rows = pp->rows[st];
             if (rows > (warp & 3) * 32 || end > s0) {
+                pair_sync(pair);   // the other thread has read what it was told last
+                *tell = l;
+                pair_sync(pair);
+                l += *hear;
                 if (end > s0) {
                     if (!(ok = wait_all(&ct.ofull[st], no++ & 1u, abort_flag))) break;
                     tc_fence_after();
                 }
-                finish<F16, TREE>(p, *pp, end > s0, tO, stage, m, l, lim, low, nodes, my_tok, rows);
+                finish<F16, TREE>(p, *pp, end > s0, tO, smem + kOffStage + (warp - 4) * kStageBytes, m, l, lim, nodes, rows);
                 tc_fence_before();
+                pair_sync(pair);
             }
             step0 += pp->s1 - s0;
             __syncwarp();
@@ -968,15 +982,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (ct.abort && lane == 0) {   // copies and products in flight end before their memory goes
-        if (warp == 8)
+        if (warp == 0)
             for (int i = max(0, it - kSlots); i < it; ++i) mbar_drain(&ct.full[i % kSlots], (uint32_t)(i / kSlots) & 1u);
-        if (warp == 9) {
-            mma_commit(&ct.drain);
-            mbar_drain(&ct.drain, 0);
+        if (warp == 1 || warp == 2) {
+            mma_commit(&ct.drain[warp - 1]);
+            mbar_drain(&ct.drain[warp - 1], 0);
         }
     }
-    __syncwarp();
-    if (warp == 9) {
+    __syncthreads();
+    if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
