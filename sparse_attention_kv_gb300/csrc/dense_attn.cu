@@ -62,6 +62,7 @@ struct Params {
     int n_seqs, total_q, total_k;
     int n_heads, n_kv, group;
     int toks;             // tokens of a stream: 128 / group, so that a stream begins with a token
+    int tile;             // tokens of a tile: two streams', or one's where both take the same
     uint32_t by_group;    // ceil(2^16 / group): x / group = x * by_group >> 16 for x < 128
     float scale, scale_log2;
     void *out;
@@ -135,16 +136,18 @@ __device__ __forceinline__ bool elect_one() {
 }
 // The 64 threads of a pair of warps, which share their rows.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool pair_any(int id, bool x) {
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
     int any;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 64, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        "bar.red.or.pred q, %2, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(any)
-        : "r"((int)x), "r"(id)
+        : "r"((int)x), "r"(id), "r"(threads)
         : "memory");
     return any != 0;
 }
+// All softmax warps.
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 9, 512;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the runs and the shares
 
@@ -171,7 +174,7 @@ struct Seq {
             tiles = lq > 0 ? 1 : 0;   // each CTA of a group has its own tile of rows
         } else {
             range(p, p.cu_k, s, p.total_k, tell, k0, lk);
-            tiles = (lq + 2 * p.toks - 1) / (2 * p.toks);
+            tiles = (lq + p.tile - 1) / p.tile;
         }
     }
     static __device__ __forceinline__ void range(const Params &p, const int32_t *cu, int s, int most, bool tell, int &c0,
@@ -183,7 +186,7 @@ struct Seq {
     }
     __device__ __forceinline__ int steps(const Params &p, int t) const {
         if constexpr (TREE) return (lk + kKeys - 1) / kKeys + 1;   // the pages, then the drafts
-        return (keys_of(lq, lk, min((t + 1) * 2 * p.toks, lq) - 1) + kKeys - 1) / kKeys;
+        return (keys_of(lq, lk, min((t + 1) * p.tile, lq) - 1) + kKeys - 1) / kKeys;
     }
     // The work of tiles 0 .. T - 1, in keys: what each tile's last token sees, and kRunKeys.  With W tokens a tile, that is
     // max(0, lk - lq + (t + 1) W) for a full tile t; the last one's is lk.
@@ -194,20 +197,20 @@ struct Seq {
             sum += lk;
             --T;
         }
-        const int W = 2 * p.toks, c = lk - lq + W, t0 = c < 0 ? min((-c + W - 1) / W, T) : 0;
+        const int W = p.tile, c = lk - lq + W, t0 = c < 0 ? min((-c + W - 1) / W, T) : 0;
         const long long n = T - t0;
         return sum + n * (c + (long long)t0 * W) + W * (n * (n - 1) / 2);
     }
     __device__ __forceinline__ int work(const Params &p, int t) const {   // cum(t + 1) - cum(t)
         if constexpr (TREE) return lk + kKeys + kRunKeys;
-        return keys_of(lq, lk, min((t + 1) * 2 * p.toks, lq) - 1) + kRunKeys;
+        return keys_of(lq, lk, min((t + 1) * p.tile, lq) - 1) + kRunKeys;
     }
     // Keys that token i of lq sees.
     static __device__ __forceinline__ int keys_of(int lq, int lk, int i) { return min(max(lk - lq + i + 1, 0), lk); }
 };
 
 // A CTA's pieces one after another.
-template <bool TREE>
+template <bool TREE, bool HALVES>
 struct Walk {
     Seq<TREE> q;
     long long at, x0, x1;   // the beginning of the next run, and the CTA's share of all runs
@@ -231,14 +234,14 @@ struct Walk {
             pc.lq = q.lq;
             pc.k0 = q.k0;
             pc.lk = q.lk;
-            pc.tok0 = (TREE ? tile : t) * 2 * p.toks;
+            pc.tok0 = (TREE ? tile : t) * p.tile;
             pc.s0 = s0;
             pc.s1 = s1;
             pc.n = n;
             if (pc.tok0 >= q.lq) take = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int first = pc.tok0 + i * p.toks, toks = min(max(q.lq - first, 0), p.toks);
+                const int first = pc.tok0 + (HALVES ? 0 : i * p.toks), toks = min(max(q.lq - first, 0), p.toks);
                 pc.rows[i] = toks * p.group;
                 int end = s0;
                 if (toks > 0) {
@@ -271,8 +274,8 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 }
 
 // This CTA's share of all runs, and the run it begins in (one warp; every lane gets it).
-template <bool TREE>
-__device__ void find_share(const Params &p, Walk<TREE> &w) {
+template <bool TREE, bool HALVES>
+__device__ void find_share(const Params &p, Walk<TREE, HALVES> &w) {
     const int lane = threadIdx.x & 31;
     const unsigned share = blockIdx.x / (unsigned)p.row_tiles;
     const bool tell = blockIdx.x == 0;
@@ -443,19 +446,19 @@ __device__ __forceinline__ void store4(const Params &p, size_t at, float a, floa
 
 // The end of a piece for a warp's 32 rows and 64 dimensions: the output normalised, through `stage` so that a row's bytes
 // are written together, or the partial as it is.  have: there is an O in tensor memory.
-template <bool F16, bool TREE>
-__device__ __forceinline__ void finish(const Params &p, const Piece &pc, bool have, uint32_t tO, uint8_t *stage, float m, float l,
-                                       int lim, unsigned long long nodes, int rows) {
+// HALVES: stream 1 hands what it has to stream 0 through `box` (32 KB), and stream 0 goes on.
+template <bool F16, bool TREE, bool HALVES>
+__device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &pc, bool have, uint32_t tO, uint8_t *stage, float4 *box,
+                                       float m, float l, int lim, unsigned long long nodes, int rows) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, G = p.group;
     const int r = (warp & 3) * 32 + lane, d = half * 64;
     const bool whole = pc.s0 == 0 && pc.s1 == pc.n, mine = r < rows, fix = pc.bad != 0;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const size_t slot = 2 * (size_t)blockIdx.x + (pc.s0 > 0 ? 0 : 1);
     const int in_tile = st * kRows + r;
     // values that are not finite are added where this row sees them: in the drafts, or from the first step that was cleared
     const int f0 = TREE ? 0 : max(Seq<TREE>::keys_of(pc.lq, pc.lk, pc.tok0) / kKeys, pc.s0) * kKeys;
     const int f1 = TREE ? (pc.s1 == pc.n ? pc.lq : 0) : min(lim, pc.s1 * kKeys);
-    const size_t out0 = (size_t)(pc.q0 + pc.tok0 + st * p.toks) * p.n_heads + pc.g * G;
+    const size_t out0 = (size_t)(pc.q0 + pc.tok0 + (HALVES ? 0 : st * p.toks)) * p.n_heads + pc.g * G;
     auto output = [&](int row) {   // the row of out that a row of the stream is
         const int tok = (int)(row * p.by_group >> 16);
         return out0 + (size_t)tok * p.n_heads + (row - tok * G);
@@ -470,6 +473,50 @@ __device__ __forceinline__ void finish(const Params &p, const Piece &pc, bool ha
 #pragma unroll
         for (int i = 0; i < 64; ++i) o[i >> 4][i & 15] = 0u;
     }
+    auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
+    if constexpr (HALVES) {
+        if (have) {   // the same for all
+            const int at = (int)threadIdx.x - 128 - st * 256;
+            if (st == 1) {   // both threads of a row have read the other's sum
+                pair_sync(1 + st * 4 + (warp & 3));
+                ct.swap[1][half][r] = half ? l : m;
+            }
+            float f0 = 1.0f, f1 = 1.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {   // 32 dimensions at a time
+                if (st == 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        box[i * 256 + at] = make_float4(val(32 * h + 4 * i), val(32 * h + 4 * i + 1), val(32 * h + 4 * i + 2),
+                                                        val(32 * h + 4 * i + 3));
+                soft_sync();
+                if (st == 0) {
+                    if (h == 0) {
+                        const float m1 = ct.swap[1][0][r], l1 = ct.swap[1][1][r];
+                        const float top = l == 0.0f ? m1 : l1 == 0.0f ? m : fmaxf(m, m1);   // of those that saw something
+                        f0 = l == 0.0f ? 0.0f : ex2((m - top) * p.scale_log2);
+                        f1 = l1 == 0.0f ? 0.0f : ex2((m1 - top) * p.scale_log2);
+                        m = top;
+                        l = f0 * l + f1 * l1;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 x = box[i * 256 + at];
+                        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t &to = o[(32 * h + 4 * i + e) >> 4][(4 * i + e) & 15];
+                            to = __float_as_uint(__uint_as_float(to) * f0 + y[e] * f1);
+                        }
+                    }
+                }
+                if (h == 1) fence_proxy_async();   // the box is Q's memory again
+                soft_sync();
+            }
+        }
+        if (st == 1) return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (fix && mine) {
         for (int t = f0; t < f1; ++t) {
             if (TREE && !(nodes >> t & 1ull)) continue;
@@ -481,7 +528,6 @@ __device__ __forceinline__ void finish(const Params &p, const Piece &pc, bool ha
                     o[i >> 4][i & 15] = __float_as_uint(__uint_as_float(o[i >> 4][i & 15]) + widen<F16>(v[i]));
         }
     }
-    auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
     if (!whole) {
         if (!mine) return;
         float4 *part = p.part + (slot * 32 + d / 4) * p.rows_cap + in_tile;
@@ -542,7 +588,8 @@ struct Pieces {
     }
 };
 
-template <bool F16, bool TREE>
+// HALVES: every tile has at most one stream's rows; both streams take them, each with half of a step's keys.
+template <bool F16, bool TREE, bool HALVES>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
@@ -596,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.desc[2 * (size_t)blockIdx.x] = make_int4(0, 0, 0, 0);
             p.desc[2 * (size_t)blockIdx.x + 1] = make_int4(0, 0, 0, 0);
         }
-        Walk<TREE> walk;
-        find_share<TREE>(p, walk);
+        Walk<TREE, HALVES> walk;
+        find_share(p, walk);
         Piece pc;
         int step = 0, no = 0;
         uint32_t nq[2] = {0, 0};
@@ -610,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait_all(&ct.qempty[i], (nq[i]++ & 1u) ^ 1u, abort_flag)) || lane != 0) continue;
                 uint8_t *to = smem + kOffQ + i * kQBytes;
                 mbar_expect_tx(&ct.qfull[i], qbytes);
-                const int row = pc.q0 + pc.tok0 + i * p.toks;
+                const int row = pc.q0 + pc.tok0 + (HALVES ? 0 : i * p.toks);
                 tma_load_3d(to, &tm_q, &ct.qfull[i], 0, pc.g * p.group, row);
                 tma_load_3d(to + kQBytes / 2, &tm_q, &ct.qfull[i], 64, pc.g * p.group, row);
             }
@@ -697,7 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // its waits lie behind the other one's products.  An MMA takes 47 cycles to issue and 64 to form: one warp alone, with
         // the waits between, issues both streams' more slowly than the tensor cores form them.
         const int st = warp - 1;
-        constexpr uint32_t kDesc = idesc(F16 ? 0 : 1, kRows, 128);
+        constexpr uint32_t kDescS = idesc(F16 ? 0 : 1, kRows, HALVES ? 64 : 128), kDesc = idesc(F16 ? 0 : 1, kRows, 128);
+        constexpr int kSteps = HALVES ? 4 : 8;   // of 16 keys
         const uint32_t smem0 = (uint32_t)uniform((int)smem_u32(smem));
         const uint64_t q_desc = sdesc(smem0 + kOffQ + st * kQBytes), k_desc = sdesc(smem0 + kOffRing);
         const uint64_t v_desc = sdesc_mn128(smem0 + kOffRing, 16384);
@@ -709,15 +757,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto slot_full = [&](int i) { return wait_all(&ct.full[i % kSlots], (uint32_t)(i / kSlots) & 1u, abort_flag); };
         auto my_turn = [&]() { return wait_all(&ct.turn[st], (turns++ & 1u) ^ (st == 0 ? 1u : 0u), abort_flag); };
         auto logits = [&](int kit, bool last) {   // one lane
-            const uint64_t b = k_desc + (uint64_t)((kit % kSlots) * (kSlotBytes >> 4));
+            const uint64_t b = k_desc + (uint64_t)((kit % kSlots) * (kSlotBytes >> 4) + (HALVES ? st * 512 : 0));
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int off = (k >> 2) * 1024 + (k & 3) * 2;
-                mma<MmaKind::f16>(tS, q_desc + off, b + off, kDesc, k > 0);
+                mma<MmaKind::f16>(tS, q_desc + off, b + off, kDescS, k > 0);
             }
             mma_commit(&ct.sfull[st]);
             mma_commit(&ct.empty[kit % kSlots]);
-            if (last) mma_commit(&ct.qempty[st]);
+            if (last && !(HALVES && st == 1)) mma_commit(&ct.qempty[st]);   // there, Q's memory is used once more
         };
         while (ok) {
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
@@ -751,14 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_one()) {
                     if (j < e) {
                         if (paged) {
-                            const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
+                            const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4) + (HALVES ? st * 1024 : 0));
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
+                            for (int k = 0; k < kSteps; ++k)
                                 mma_f16_ta(tO, tS + k * 8, b + (k >> 2) * 1024 + (k & 3) * 2, kDesc, k > 0 || j > s0);
                         } else {
-                            const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4));
+                            const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4) + (HALVES ? st * 512 : 0));
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) mma_f16_ta(tO, tS + k * 8, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
+                            for (int k = 0; k < kSteps; ++k) mma_f16_ta(tO, tS + k * 8, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
                         }
                         if (j + 1 == e) mma_commit(&ct.ofull[st]);
                         mma_commit(&ct.empty[vslot]);
@@ -785,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
             const int s0 = pp->s0, s1 = pp->s1, n = pp->n, lq = pp->lq, lk = pp->lk;
             const int low = TREE ? 0 : Seq<TREE>::keys_of(lq, lk, pp->tok0);
-            const int high = TREE ? lq : Seq<TREE>::keys_of(lq, lk, min(pp->tok0 + 2 * p.toks, lq) - 1);
+            const int high = TREE ? lq : Seq<TREE>::keys_of(lq, lk, min(pp->tok0 + p.tile, lq) - 1);
             // only a run's last steps can hold such places
             for (int j = TREE ? max(s0, lk / kKeys) : max(s0, low / kKeys); ok && j < s1; ++j) {
                 const bool paged = TREE && j < n - 1;
@@ -857,14 +905,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pair = 1 + st * 4 + (warp & 3);   // barrier of the two warps of these rows
         float *tell = &ct.swap[st][half][r], *hear = &ct.swap[st][half ^ 1][r];
         const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
-        const int my_tok = st * p.toks + (int)(r * p.by_group >> 16);   // this row's token in a tile
+        const int first_tok = HALVES ? 0 : st * p.toks;                     // of the stream, in a tile
+        const int my_tok = first_tok + (int)(r * p.by_group >> 16);        // this row's
+        constexpr int kCols = HALVES ? 32 : 64;                            // keys of a thread
+        const int col0 = HALVES ? st * 64 + half * 32 : half * 64;         // the first of them in a step
         Pieces pieces{ct};
         const Piece *pp;
         int step0 = 0;
         uint32_t ns = 0, no = 0;
         bool ok = true;
-        while (ok) {
-            if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
+        // These warps meet at named barriers, which know no limit, so none may leave alone: one whose wait ran out goes
+        // on without waiting, and all of a stream (HALVES: of both) leave together before the next piece.
+        while (true) {
+            ok = pieces.next(abort_flag, pp) && ok;
+            if (any_of(HALVES ? 9 : 9 + st, HALVES ? 512 : 256, !ok) || pp->stop) break;
             const int s0 = pp->s0, end = pp->e[st], n = pp->n;
             // what this row sees
             int lim = 0, low = 0;                       // prompts: keys of this row, of the stream's first one
@@ -873,41 +927,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (end == n && end > s0) nodes = ancestors(p, pp->q0, pp->lq, min(pp->tok0 + my_tok, pp->lq - 1));
             } else {
                 lim = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + my_tok, pp->lq - 1));
-                low = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + st * p.toks, pp->lq - 1));
+                low = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + first_tok, pp->lq - 1));
             }
             float m = -INFINITY, l = 0.0f;
             for (int j = s0; j < end; ++j) {
-                if (!(ok = wait_all(&ct.sfull[st], ns++ & 1u, abort_flag))) break;
+                ok = ok && wait_all(&ct.sfull[st], ns++ & 1u, abort_flag);
                 tc_fence_after();
-                uint32_t v[4][16];
-                tmem_ld64_nowait(tS + half * 64, v);
+                uint32_t v[kCols / 16][16];
+                if constexpr (HALVES) {
+                    tmem_ld16_nowait(tS + half * 32, v[0]);
+                    tmem_ld16_nowait(tS + half * 32 + 16, v[1]);
+                } else {
+                    tmem_ld64_nowait(tS + half * 64, v);
+                }
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) reg_fence(v[i]);
+                for (int i = 0; i < kCols / 16; ++i) reg_fence(v[i]);
                 if constexpr (TREE) {
                     const bool paged = j < n - 1;
-                    const int valid = paged ? ct.info[(step0 + j - s0) % kInfo][half] : 0;
+                    const int valid = paged ? ct.info[(step0 + j - s0) % kInfo][col0 >> 6] : 0;
                     if (valid < 64) {
-                        const unsigned long long see = paged ? (1ull << valid) - 1ull : half ? 0ull : nodes;
+                        unsigned long long see = paged ? (1ull << valid) - 1ull : col0 >= 64 ? 0ull : nodes;
+                        see >>= col0 & 63;
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < kCols; ++i)
                             if (!((i < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) & 1u << (i & 31))) v[i >> 4][i & 15] = 0xFF800000u;
                     }
                 } else if ((j + 1) * kKeys > low) {
-                    const int left = lim - j * kKeys - half * 64;
+                    const int left = lim - j * kKeys - col0;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
+                    for (int i = 0; i < kCols; ++i)
                         if (i >= left) v[i >> 4][i & 15] = 0xFF800000u;
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 64; i += 2)
+                for (int i = 0; i < kCols; i += 2)
                     top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(v[i >> 4][i & 15]),
                                                                        __uint_as_float(v[i >> 4][(i & 15) + 1])));
                 float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 // Both threads of a row go by one reference.  The barrier also has both warps' logits in registers before
                 // either one's weights overwrite them.
-                if (j == s0 || pair_any(pair, now > m + rise)) {
+                if (j == s0 || any_of(pair, 64, now > m + rise)) {
                     *tell = now;
                     pair_sync(pair);
                     now = fmaxf(now, *hear);
@@ -935,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
                 f32x2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {   // 32 keys a round
+                for (int q = 0; q < kCols / 32; ++q) {   // 32 keys a round
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -948,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
                         w[i] = pack16<F16>(y0, y1);
                     }
-                    tmem_st16(tS + 32 * half + 16 * q, w);
+                    tmem_st16(tS + half * (kCols / 2) + 16 * q, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -958,20 +1018,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 unpack2(add2(sum[0], sum[1]), a, b);
                 l += a + b;
             }
-            if (!ok) break;
             const int rows = pp->rows[st];
-            if (rows > (warp & 3) * 32 || end > s0) {
+            if (HALVES || rows > (warp & 3) * 32 || end > s0) {
                 pair_sync(pair);   // the other thread has read what it was told last
                 *tell = l;
                 pair_sync(pair);
                 l += *hear;
                 if (end > s0) {
-                    if (!(ok = wait_all(&ct.ofull[st], no++ & 1u, abort_flag))) break;
+                    ok = ok && wait_all(&ct.ofull[st], no++ & 1u, abort_flag);
                     tc_fence_after();
                 }
-                finish<F16, TREE>(p, *pp, end > s0, tO, smem + kOffStage + (warp - 4) * kStageBytes, m, l, lim, nodes, rows);
+                finish<F16, TREE, HALVES>(p, ct, *pp, end > s0, tO, smem + kOffStage + (warp - 4) * kStageBytes,
+                                          reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, lim, nodes, rows);
                 tc_fence_before();
                 pair_sync(pair);
+                if (HALVES && tid == 128 && end > s0) mbar_arrive(&ct.qempty[1]);
             }
             step0 += pp->s1 - s0;
             __syncwarp();
@@ -1064,7 +1125,7 @@ int rows_cap(int tokens, int group) {
     return tokens > kRows / group ? 2 * kRows : (tokens * group + 31) / 32 * 32;
 }
 
-template <bool F16, bool TREE>
+template <bool F16, bool TREE, bool HALVES>
 qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bool split, cudaStream_t s) {
     static std::mutex mu;
     static bool opted_in[64] = {false};
@@ -1075,13 +1136,13 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bo
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!opted_in[dev]) {
-            st = check_cuda(cudaFuncSetAttribute(dense_kernel<F16, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+            st = check_cuda(cudaFuncSetAttribute(dense_kernel<F16, TREE, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                             "cudaFuncSetAttribute(dense attention)");
             if (st != QSA_OK) return st;
             opted_in[dev] = true;
         }
     }
-    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3],
+    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE, HALVES>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3],
                           m[4], p);
     if (st != QSA_OK || !split) return st;
     cudaLaunchConfig_t cfg{};
@@ -1109,6 +1170,10 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.n_kv = a.n_kv_heads;
     p.group = a.n_heads / a.n_kv_heads;
     p.toks = kRows / p.group;
+    const bool halves = (TREE ? a.max_nodes : a.total_q) <= p.toks;   // no tile holds a second stream's rows
+    p.tile = halves ? p.toks : 2 * p.toks;
+    const int most = TREE && a.max_nodes < a.total_q ? a.max_nodes : a.total_q;   // tokens of a sequence
+    p.rows_cap = rows_cap(most, p.group);
     p.by_group = (65536u + (uint32_t)p.group - 1u) / (uint32_t)p.group;
     p.scale = a.scale;
     p.scale_log2 = a.scale * 1.4426950408889634f;
@@ -1123,13 +1188,12 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.n_pages = a.table.n_pages;
     p.n_tokens = a.n_tokens;
     p.flags = a.flags;
-    p.rows_cap = rows_cap(a.total_q, p.group);
     char *ws = static_cast<char *>(a.ws) + 256;
     p.desc = reinterpret_cast<int4 *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + kMaxCtas * 2 * sizeof(int4));
     p.part = reinterpret_cast<float4 *>(ws + kMaxCtas * 2 * (sizeof(int4) + (size_t)p.rows_cap * sizeof(float2)));
     const int ctas = num_sms() < kMaxCtas ? num_sms() : kMaxCtas;
-    p.row_tiles = TREE ? (a.max_nodes + 2 * p.toks - 1) / (2 * p.toks) : 1;
+    p.row_tiles = TREE ? (a.max_nodes + p.tile - 1) / p.tile : 1;
     p.shares = ctas / p.row_tiles;
     const int grid = p.shares * p.row_tiles;
     // the longest run that the sizes allow
@@ -1150,7 +1214,9 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
             (st = get_map(&m[4], a.vcache_t, 2, 64, pages * 128, 128)) != QSA_OK)
             return st;
     }
-    return a.dt == QSA_F16 ? launch_typed<true, TREE>(m, p, grid, split, s) : launch_typed<false, TREE>(m, p, grid, split, s);
+    if (halves)
+        return a.dt == QSA_F16 ? launch_typed<true, TREE, true>(m, p, grid, split, s) : launch_typed<false, TREE, true>(m, p, grid, split, s);
+    return a.dt == QSA_F16 ? launch_typed<true, TREE, false>(m, p, grid, split, s) : launch_typed<false, TREE, false>(m, p, grid, split, s);
 }
 
 }  // namespace
