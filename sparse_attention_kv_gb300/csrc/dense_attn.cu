@@ -39,20 +39,20 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kSoftWarps = 16;        // two threads a row, each with half of a step's keys and of the output's dimensions
+constexpr int kThreads = 384;
+constexpr int kSoftWarps = 8;         // a thread a row
 constexpr int kRows = 128;            // rows of a stream (TMEM lanes)
 constexpr int kKeys = 128;            // keys of a step
 constexpr int kSlots = 4;
 constexpr int kSlotBytes = kKeys * 128 * 2;
 constexpr int kQBytes = kRows * 128 * 2;
-constexpr int kStageBytes = 2048;     // per softmax warp: 32 rows of 64 bytes on their way out
+constexpr int kStageBytes = 4096;     // per softmax warp: 32 rows of 128 bytes on their way out
 constexpr int kPieces = 4;            // pieces that are published ahead
 constexpr int kInfo = 8;              // steps whose page limits are held: more than the ring holds
 constexpr int kMaxCtas = 152;
 constexpr int kWhole = 4;             // runs of so few steps are not split
 constexpr int kRunKeys = 256;         // what a run's beginning and end cost, in keys
-constexpr int kMinShare = 512;        // least work, in keys, that a CTA is started for
+constexpr int kMinShare = 384;        // least work, in keys, that a CTA is started for
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
 
@@ -96,15 +96,15 @@ struct Piece {
 };
 
 struct Ctrl {
-    uint64_t full[kSlots], empty[kSlots], dirty, clean, turn[2];
-    uint64_t qfull[2], qempty[2], sfull[2], pready[2], ofull[2];
+    uint64_t full[kSlots], empty[kSlots], clean[kSlots / 2], turn[2];
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], ofull[2];
     uint64_t pfull[kPieces], pempty[kPieces];
     uint64_t drain[2];
     Piece pieces[kPieces];
     uint32_t tmem;
     int abort;
     int info[kInfo][2];   // valid tokens in each page of a step
-    float swap[2][2][kRows];   // what the two threads of a row tell each other, by stream and half
+    float2 other[kRows];  // HALVES: stream 1's (m, l)
 };
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQBytes;
@@ -134,8 +134,7 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
     return is != 0;
 }
-// The 64 threads of a pair of warps, which share their rows.
-__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+// Whether x holds in any of `threads` threads, which meet at barrier `id`.
 __device__ __forceinline__ bool any_of(int id, int threads, bool x) {
     int any;
     asm volatile(
@@ -147,7 +146,7 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool x) {
     return any != 0;
 }
 // All softmax warps.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 9, 512;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
 
 // ------------------------------------------------------------------ the runs and the shares
 
@@ -183,6 +182,14 @@ struct Seq {
         if (tell && (a < 0 || b < a || b > most)) atomicOr(p.flags, QSA_FLAG_NBLOCKS_CLAMPED);
         c0 = min(max(a, 0), most);
         len = min(max(b, c0), most) - c0;
+    }
+    // What lane l of the warp has loaded.
+    __device__ __forceinline__ void take(int l) {
+        q0 = __shfl_sync(~0u, q0, l);
+        lq = __shfl_sync(~0u, lq, l);
+        k0 = __shfl_sync(~0u, k0, l);
+        lk = __shfl_sync(~0u, lk, l);
+        tiles = __shfl_sync(~0u, tiles, l);
     }
     __device__ __forceinline__ int steps(const Params &p, int t) const {
         if constexpr (TREE) return (lk + kKeys - 1) / kKeys + 1;   // the pages, then the drafts
@@ -301,7 +308,7 @@ __device__ void find_share(const Params &p, Walk<TREE, HALVES> &w) {
     w.s = p.n_seqs;
     w.g = w.t = 0;
     for (int s0 = 0; s0 < p.n_seqs && w.x0 < w.x1; s0 += 32) {
-        const long long x = s0 == 0 ? first : weight(s0 + lane, false);
+        const long long x = s0 == 0 && p.n_seqs <= 32 ? first : weight(s0 + lane, false);
         long long incl = x;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -318,7 +325,7 @@ __device__ void find_share(const Params &p, Walk<TREE, HALVES> &w) {
         before += __shfl_sync(~0u, incl, 31);
     }
     if (w.s < p.n_seqs) {
-        q.load(p, w.s, false);
+        q.take(w.s & 31);
         const long long per = q.cum(p, q.tiles), in_seq = w.x0 - before;
         w.g = in_seq < (1ll << 31) && per < (1ll << 31) ? (int)((unsigned)in_seq / (unsigned)per) : (int)(in_seq / per);
         before += w.g * per;
@@ -444,14 +451,14 @@ __device__ __forceinline__ void store4(const Params &p, size_t at, float a, floa
     else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(pack16<F16>(a, b), pack16<F16>(c, d));
 }
 
-// The end of a piece for a warp's 32 rows and 64 dimensions: the output normalised, through `stage` so that a row's bytes
-// are written together, or the partial as it is.  have: there is an O in tensor memory.
+// The end of a piece for a warp's 32 rows: the output normalised, through `stage` so that a row's bytes are written
+// together, or the partial as it is.  have: there is an O in tensor memory.
 // HALVES: stream 1 hands what it has to stream 0 through `box` (32 KB), and stream 0 goes on.
 template <bool F16, bool TREE, bool HALVES>
 __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &pc, bool have, uint32_t tO, uint8_t *stage, float4 *box,
                                        float m, float l, int lim, unsigned long long nodes, int rows) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, G = p.group;
-    const int r = (warp & 3) * 32 + lane, d = half * 64;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = (warp - 4) >> 2, G = p.group;
+    const int r = (warp & 3) * 32 + lane;
     const bool whole = pc.s0 == 0 && pc.s1 == pc.n, mine = r < rows, fix = pc.bad != 0;
     const size_t slot = 2 * (size_t)blockIdx.x + (pc.s0 > 0 ? 0 : 1);
     const int in_tile = st * kRows + r;
@@ -463,115 +470,109 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
         const int tok = (int)(row * p.by_group >> 16);
         return out0 + (size_t)tok * p.n_heads + (row - tok * G);
     };
-    uint32_t o[4][16];
-    if (have) {
-        tmem_ld64_nowait(tO, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reg_fence(o[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) o[i >> 4][i & 15] = 0u;
-    }
-    auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
+    float keep = 1.0f, add = 0.0f;   // HALVES: factors of this stream's and of the other's
     if constexpr (HALVES) {
         if (have) {   // the same for all
-            const int at = (int)threadIdx.x - 128 - st * 256;
-            if (st == 1) {   // both threads of a row have read the other's sum
-                pair_sync(1 + st * 4 + (warp & 3));
-                ct.swap[1][half][r] = half ? l : m;
-            }
-            float f0 = 1.0f, f1 = 1.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {   // 32 dimensions at a time
-                if (st == 1)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        box[i * 256 + at] = make_float4(val(32 * h + 4 * i), val(32 * h + 4 * i + 1), val(32 * h + 4 * i + 2),
-                                                        val(32 * h + 4 * i + 3));
-                soft_sync();
-                if (st == 0) {
-                    if (h == 0) {
-                        const float m1 = ct.swap[1][0][r], l1 = ct.swap[1][1][r];
-                        const float top = l == 0.0f ? m1 : l1 == 0.0f ? m : fmaxf(m, m1);   // of those that saw something
-                        f0 = l == 0.0f ? 0.0f : ex2((m - top) * p.scale_log2);
-                        f1 = l1 == 0.0f ? 0.0f : ex2((m1 - top) * p.scale_log2);
-                        m = top;
-                        l = f0 * l + f1 * l1;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 x = box[i * 256 + at];
-                        const float y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t &to = o[(32 * h + 4 * i + e) >> 4][(4 * i + e) & 15];
-                            to = __float_as_uint(__uint_as_float(to) * f0 + y[e] * f1);
-                        }
-                    }
-                }
-                if (h == 1) fence_proxy_async();   // the box is Q's memory again
-                soft_sync();
+            if (st == 1) ct.other[r] = make_float2(m, l);
+            soft_sync();
+            if (st == 0) {
+                const float2 x = ct.other[r];
+                const float top = l == 0.0f ? x.x : x.y == 0.0f ? m : fmaxf(m, x.x);   // of those that saw something
+                keep = l == 0.0f ? 0.0f : ex2((m - top) * p.scale_log2);
+                add = x.y == 0.0f ? 0.0f : ex2((x.x - top) * p.scale_log2);
+                m = top;
+                l = keep * l + add * x.y;
             }
         }
-        if (st == 1) return;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    if (fix && mine) {
-        for (int t = f0; t < f1; ++t) {
-            if (TREE && !(nodes >> t & 1ull)) continue;
-            const uint16_t *v = static_cast<const uint16_t *>(p.v.p) + (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token +
-                                (int64_t)pc.g * p.v.head + d;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (not_finite<F16>(v[i]) & 0xFFFFu)
-                    o[i >> 4][i & 15] = __float_as_uint(__uint_as_float(o[i >> 4][i & 15]) + widen<F16>(v[i]));
-        }
-    }
-    if (!whole) {
-        if (!mine) return;
-        float4 *part = p.part + (slot * 32 + d / 4) * p.rows_cap + in_tile;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) part[(i / 4) * p.rows_cap] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
-        if (half == 0) p.ml[slot * p.rows_cap + in_tile] = make_float2(m * p.scale_log2, l);
-        return;
-    }
-    // 64 bytes of each row at a time; its 16-byte units are rotated by the row so that neither way meets a bank twice
-    uint8_t *line = stage + lane * 64;
-    const int turn = (lane >> 1) & 3;
-    auto drain = [&](int at) {   // four lanes write a row's 64 bytes, which begin at its byte `at`
+    uint8_t *line = stage + lane * 128;
+#pragma unroll 1
+    for (int d = 0; d < 128; d += 64) {
+        uint32_t o[4][16];
+        auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
         __syncwarp();
+        if (have) {
+            tmem_ld64_nowait(tO + d, o);
+            tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), row = (warp & 3) * 32 + rr;
-            const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-            if (row < rows)
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + output(row) * (p.out_f32 ? 512 : 256) + at +
-                                           16 * (lane & 3)) = x;
+            for (int i = 0; i < 4; ++i) reg_fence(o[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) o[i >> 4][i & 15] = 0u;
         }
-        __syncwarp();
-    };
-    if (p.out_f32) {
+        if constexpr (HALVES) {
+            if (have) {
+                if (st == 1)
 #pragma unroll
-        for (int h = 0; h < 64; h += 16) {
+                    for (int i = 0; i < 64; i += 4) box[(i / 4) * kRows + r] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+                soft_sync();
+                if (st == 0)
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4 *>(line + (((i >> 2) ^ turn) << 4)) =
-                    make_float4(val(h + i) * inv, val(h + i + 1) * inv, val(h + i + 2) * inv, val(h + i + 3) * inv);
-            drain(4 * (d + h));
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 x = box[(i / 4) * kRows + r];
+                        const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[(i + e) >> 4][(i + e) & 15] = __float_as_uint(val(i + e) * keep + y[e] * add);
+                    }
+                if (d == 64) fence_proxy_async();   // the box is Q's memory again
+                soft_sync();
+            }
+            if (st == 1) continue;
         }
-    } else {
+        if (fix && mine) {
+            for (int t = f0; t < f1; ++t) {
+                if (TREE && !(nodes >> t & 1ull)) continue;
+                const uint16_t *v = static_cast<const uint16_t *>(p.v.p) + (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token +
+                                    (int64_t)pc.g * p.v.head + d;
 #pragma unroll
-        for (int h = 0; h < 64; h += 32) {
+                for (int i = 0; i < 64; ++i)
+                    if (not_finite<F16>(v[i]) & 0xFFFFu) o[i >> 4][i & 15] = __float_as_uint(val(i) + widen<F16>(v[i]));
+            }
+        }
+        if (!whole) {
+            if (mine) {
+                float4 *part = p.part + (slot * 32 + d / 4) * p.rows_cap + in_tile;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4 *>(line + (((i >> 3) ^ turn) << 4)) = make_uint4(
-                    pack16<F16>(val(h + i) * inv, val(h + i + 1) * inv), pack16<F16>(val(h + i + 2) * inv, val(h + i + 3) * inv),
-                    pack16<F16>(val(h + i + 4) * inv, val(h + i + 5) * inv), pack16<F16>(val(h + i + 6) * inv, val(h + i + 7) * inv));
-            drain(2 * (d + h));
+                for (int i = 0; i < 64; i += 4) part[(i / 4) * p.rows_cap] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+            }
+            continue;
+        }
+        // 128 bytes of each row at a time; its 16-byte units are rotated by the row so that neither way meets a bank twice
+        auto drain = [&](int at) {   // eight lanes write a row's 128 bytes, which begin at its byte `at`
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), row = (warp & 3) * 32 + rr;
+                const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                if (row < rows)
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + output(row) * (p.out_f32 ? 512 : 256) + at +
+                                               16 * (lane & 7)) = x;
+            }
+            __syncwarp();
+        };
+        if (p.out_f32) {
+#pragma unroll
+            for (int h = 0; h < 64; h += 32) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4 *>(line + (((i >> 2) ^ (lane & 7)) << 4)) =
+                        make_float4(val(h + i) * inv, val(h + i + 1) * inv, val(h + i + 2) * inv, val(h + i + 3) * inv);
+                drain(4 * (d + h));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; i += 8)
+                *reinterpret_cast<uint4 *>(line + (((i >> 3) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack16<F16>(val(i) * inv, val(i + 1) * inv), pack16<F16>(val(i + 2) * inv, val(i + 3) * inv),
+                               pack16<F16>(val(i + 4) * inv, val(i + 5) * inv), pack16<F16>(val(i + 6) * inv, val(i + 7) * inv));
+            drain(2 * d);
         }
     }
-    if (mine && half == 0 && p.lse) p.lse[output(r)] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
+    __syncwarp();
+    if (!mine || (HALVES && st == 1)) return;
+    if (!whole) p.ml[slot * p.rows_cap + in_tile] = make_float2(m * p.scale_log2, l);
+    else if (p.lse) p.lse[output(r)] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
 }
 
 // The next published piece (a warp); false when the wait ran out.  A reader gives it back with done().
@@ -603,27 +604,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&ct.full[i], 1);
-            mbar_init(&ct.empty[i], 2);        // both streams
+            mbar_init(&ct.empty[i], 2 + (i & 1));   // both streams, and for V (in the odd slots) warp 3
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.qfull[i], 1);
             mbar_init(&ct.qempty[i], 1);
             mbar_init(&ct.sfull[i], 1);
-            mbar_init(&ct.pready[i], 8);   // one arrival per warp of the stream
+            for (int h = 0; h < 2; ++h) mbar_init(&ct.pready[i][h], 4);   // one arrival per warp of the stream
             mbar_init(&ct.ofull[i], 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(&ct.pfull[i], 1);
-            mbar_init(&ct.pempty[i], 19);  // every warp but the one that publishes
+            mbar_init(&ct.pempty[i], 11);  // every warp but the one that publishes
         }
         mbar_init(&ct.turn[0], 1);
         mbar_init(&ct.turn[1], 1);
-        mbar_init(&ct.dirty, 2);
-        mbar_init(&ct.clean, 1);
+        for (int i = 0; i < kSlots / 2; ++i) mbar_init(&ct.clean[i], 1);
         mbar_init(&ct.drain[0], 1);
         mbar_init(&ct.drain[1], 1);
         ct.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane < 5) {
+        const CUtensorMap *m = lane == 0 ? &tm_q : lane == 1 ? &tm_k : lane == 2 ? &tm_v : lane == 3 ? &tm_kc : &tm_vc;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
     wait_prior_grid();   // nothing the caller wrote is read, and no tensor memory taken, before this
     allow_dependent_launch();
@@ -789,25 +793,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool paged = TREE && j < n - 1, more = j + 1 < s1;
                 if (!(ok = slot_full(it + 1))) break;
                 if ((j + 1) * kKeys > low || (TREE && !paged)) {
-                    if (lane == 0) mbar_arrive(&ct.dirty);   // V has landed: warp 3 clears what must not be read
-                    __syncwarp();
-                    if (!(ok = wait_all(&ct.clean, cleaned++ & 1u, abort_flag))) break;
+                    const int i = vslot >> 1;   // warp 3 clears what must not be read
+                    if (!(ok = wait_all(&ct.clean[i], cleaned >> i & 1u, abort_flag))) break;
+                    cleaned ^= 1u << i;
                 }
-                if (!(ok = (!more || slot_full(it + 2)) && (j >= e || wait_all(&ct.pready[st], np++ & 1u, abort_flag)) && my_turn()))
+                if (!(ok = (!more || slot_full(it + 2)) && (j >= e || wait_all(&ct.pready[st][0], np & 1u, abort_flag)) && my_turn()))
                     break;
                 tc_fence_after();
+                if (j < e) {   // the weights come in two parts: the first one's products run while the second is formed
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1) {
+                            if (!(ok = wait_all(&ct.pready[st][1], np++ & 1u, abort_flag))) break;
+                            tc_fence_after();
+                        }
+                        if (elect_one()) {
+                            if (paged) {
+                                const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4) + (HALVES ? st * 1024 : 0));
+#pragma unroll
+                                for (int k = h * kSteps / 2; k < (h + 1) * kSteps / 2; ++k)
+                                    mma_f16_ta(tO, tS + 8 * k, b + (k >> 2) * 1024 + (k & 3) * 2, kDesc, k > 0 || j > s0);
+                            } else {
+                                const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4) + (HALVES ? st * 512 : 0));
+#pragma unroll
+                                for (int k = h * kSteps / 2; k < (h + 1) * kSteps / 2; ++k)
+                                    mma_f16_ta(tO, tS + 8 * k, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
                 if (elect_one()) {
                     if (j < e) {
-                        if (paged) {
-                            const uint64_t b = k_desc + (uint64_t)(vslot * (kSlotBytes >> 4) + (HALVES ? st * 1024 : 0));
-#pragma unroll
-                            for (int k = 0; k < kSteps; ++k)
-                                mma_f16_ta(tO, tS + k * 8, b + (k >> 2) * 1024 + (k & 3) * 2, kDesc, k > 0 || j > s0);
-                        } else {
-                            const uint64_t b = v_desc + (uint64_t)(vslot * (kSlotBytes >> 4) + (HALVES ? st * 512 : 0));
-#pragma unroll
-                            for (int k = 0; k < kSteps; ++k) mma_f16_ta(tO, tS + k * 8, b + k * 128, kDesc | kIdescBMn, k > 0 || j > s0);
-                        }
                         if (j + 1 == e) mma_commit(&ct.ofull[st]);
                         mma_commit(&ct.empty[vslot]);
                     } else {
@@ -828,19 +846,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Piece *pp;
         bool ok = true;
         int base = 0;
-        uint32_t nd = 0;
         while (ok) {
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
             const int s0 = pp->s0, s1 = pp->s1, n = pp->n, lq = pp->lq, lk = pp->lk;
             const int low = TREE ? 0 : Seq<TREE>::keys_of(lq, lk, pp->tok0);
             const int high = TREE ? lq : Seq<TREE>::keys_of(lq, lk, min(pp->tok0 + p.tile, lq) - 1);
-            // only a run's last steps can hold such places
-            for (int j = TREE ? max(s0, lk / kKeys) : max(s0, low / kKeys); ok && j < s1; ++j) {
+            for (int j = s0; ok && j < s1; ++j) {
                 const bool paged = TREE && j < n - 1;
                 const int vit = base + 2 * (j - s0) + 1, vslot = vit % kSlots;
-                if (!(ok = wait_all(&ct.dirty, nd++ & 1u, abort_flag) &&
-                           wait_all(&ct.full[vslot], (uint32_t)(vit / kSlots) & 1u, abort_flag)))
-                    break;
+                if (!(ok = wait_all(&ct.full[vslot], (uint32_t)(vit / kSlots) & 1u, abort_flag))) break;
+                // only a run's last steps hold such places
+                if (TREE ? paged && (j + 1) * kKeys <= lk : (j + 1) * kKeys <= low) {
+                    if (lane == 0) mbar_arrive(&ct.empty[vslot]);
+                    continue;
+                }
                 uint8_t *v = ring + vslot * kSlotBytes;
                 bool bad = false;
 #pragma unroll 1
@@ -890,7 +909,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (bad) ct.pieces[pieces.no % kPieces].bad = 1;
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ct.clean);
+                if (lane == 0) {
+                    mbar_arrive(&ct.clean[vslot >> 1]);
+                    mbar_arrive(&ct.empty[vslot]);
+                }
             }
             base += 2 * (s1 - s0);
             __syncwarp();
@@ -898,27 +920,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             else ++pieces.no;
         }
     } else {
-        // ---------------- softmax and epilogue of a stream, two threads a row
-        const int st = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, r = (warp & 3) * 32 + lane;
+        // ---------------- softmax and epilogue of a stream, a thread a row
+        const int st = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128 + half * 64;
-        const int pair = 1 + st * 4 + (warp & 3);   // barrier of the two warps of these rows
-        float *tell = &ct.swap[st][half][r], *hear = &ct.swap[st][half ^ 1][r];
+        const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
         const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
         const int first_tok = HALVES ? 0 : st * p.toks;                     // of the stream, in a tile
         const int my_tok = first_tok + (int)(r * p.by_group >> 16);        // this row's
-        constexpr int kCols = HALVES ? 32 : 64;                            // keys of a thread
-        const int col0 = HALVES ? st * 64 + half * 32 : half * 64;         // the first of them in a step
+        constexpr int kCols = HALVES ? 64 : 128;                           // keys of a stream in a step
         Pieces pieces{ct};
         const Piece *pp;
         int step0 = 0;
         uint32_t ns = 0, no = 0;
         bool ok = true;
-        // These warps meet at named barriers, which know no limit, so none may leave alone: one whose wait ran out goes
-        // on without waiting, and all of a stream (HALVES: of both) leave together before the next piece.
+        // HALVES: the streams meet at named barriers, which know no limit, so no warp may leave alone: one whose wait ran
+        // out goes on without waiting, and all leave together before the next piece.
         while (true) {
             ok = pieces.next(abort_flag, pp) && ok;
-            if (any_of(HALVES ? 9 : 9 + st, HALVES ? 512 : 256, !ok) || pp->stop) break;
+            if ((HALVES ? any_of(3, 256, !ok) : !ok) || pp->stop) break;
             const int s0 = pp->s0, end = pp->e[st], n = pp->n;
             // what this row sees
             int lim = 0, low = 0;                       // prompts: keys of this row, of the stream's first one
@@ -932,29 +951,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.0f;
             for (int j = s0; j < end; ++j) {
                 ok = ok && wait_all(&ct.sfull[st], ns++ & 1u, abort_flag);
+                if (!HALVES && !ok) break;
                 tc_fence_after();
                 uint32_t v[kCols / 16][16];
-                if constexpr (HALVES) {
-                    tmem_ld16_nowait(tS + half * 32, v[0]);
-                    tmem_ld16_nowait(tS + half * 32 + 16, v[1]);
-                } else {
-                    tmem_ld64_nowait(tS + half * 64, v);
-                }
+#pragma unroll
+                for (int h = 0; h < kCols / 64; ++h) tmem_ld64_nowait(tS + 64 * h, reinterpret_cast<uint32_t(&)[4][16]>(v[4 * h]));
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < kCols / 16; ++i) reg_fence(v[i]);
                 if constexpr (TREE) {
                     const bool paged = j < n - 1;
-                    const int valid = paged ? ct.info[(step0 + j - s0) % kInfo][col0 >> 6] : 0;
-                    if (valid < 64) {
-                        unsigned long long see = paged ? (1ull << valid) - 1ull : col0 >= 64 ? 0ull : nodes;
-                        see >>= col0 & 63;
 #pragma unroll
-                        for (int i = 0; i < kCols; ++i)
-                            if (!((i < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) & 1u << (i & 31))) v[i >> 4][i & 15] = 0xFF800000u;
+                    for (int h = 0; h < kCols / 64; ++h) {   // the keys of a page
+                        const int page = HALVES ? st : h;
+                        const int valid = paged ? ct.info[(step0 + j - s0) % kInfo][page] : 0;
+                        if (valid < 64) {
+                            const unsigned long long see = paged ? (1ull << valid) - 1ull : page ? 0ull : nodes;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (!((i < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) & 1u << (i & 31)))
+                                    v[4 * h + (i >> 4)][i & 15] = 0xFF800000u;
+                        }
                     }
                 } else if ((j + 1) * kKeys > low) {
-                    const int left = lim - j * kKeys - col0;
+                    const int left = lim - j * kKeys - (HALVES ? 64 * st : 0);
 #pragma unroll
                     for (int i = 0; i < kCols; ++i)
                         if (i >= left) v[i >> 4][i & 15] = 0xFF800000u;
@@ -964,23 +984,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kCols; i += 2)
                     top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(v[i >> 4][i & 15]),
                                                                        __uint_as_float(v[i >> 4][(i & 15) + 1])));
-                float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                // Both threads of a row go by one reference.  The barrier also has both warps' logits in registers before
-                // either one's weights overwrite them.
-                if (j == s0 || any_of(pair, 64, now > m + rise)) {
-                    *tell = now;
-                    pair_sync(pair);
-                    now = fmaxf(now, *hear);
-                    if (j == s0) {
-                        m = now;
-                    } else {
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (j == s0) {
+                    m = now;
+                } else {
+                    const bool risen = now > m + rise;
+                    if (__any_sync(~0u, risen)) {
                         // S of this step is complete, so every product before it is: O may be scaled in place
-                        const bool risen = now > m + rise;
                         const float f = risen ? ex2((m - now) * c) : 1.0f;
                         if (risen) m = now;
                         l *= f;
 #pragma unroll 1
-                        for (int d = 0; d < 64; d += 16) {
+                        for (int d = 0; d < 128; d += 16) {
                             uint32_t o[16];
                             tmem_ld16_nowait(tO + d, o);
                             tmem_wait_ld();
@@ -995,43 +1010,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
                 f32x2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
-                for (int q = 0; q < kCols / 32; ++q) {   // 32 keys a round
-                    uint32_t w[16];
+                for (int h = 0; h < 2; ++h) {   // a part of the weights is passed on as soon as it is there
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int k = 32 * q + 2 * i;
-                        float y0, y1;
-                        unpack2(fma2(pack2(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1])), c2, nm2), y0,
-                                y1);
-                        y0 = ex2(y0);
-                        y1 = ex2(y1);
-                        sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
-                        w[i] = pack16<F16>(y0, y1);
+                    for (int q = 0; q < kCols / 64; ++q) {   // 32 keys
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int k = h * (kCols / 2) + 32 * q + 2 * i;
+                            float y0, y1;
+                            unpack2(fma2(pack2(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1])), c2, nm2),
+                                    y0, y1);
+                            y0 = ex2(y0);
+                            y1 = ex2(y1);
+                            sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
+                            w[i] = pack16<F16>(y0, y1);
+                        }
+                        tmem_st16(tS + h * (kCols / 4) + 16 * q, w);
                     }
-                    tmem_st16(tS + half * (kCols / 2) + 16 * q, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ct.pready[st][h]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ct.pready[st]);
                 float a, b;
                 unpack2(add2(sum[0], sum[1]), a, b);
                 l += a + b;
             }
+            if (!HALVES && !ok) break;
             const int rows = pp->rows[st];
             if (HALVES || rows > (warp & 3) * 32 || end > s0) {
-                pair_sync(pair);   // the other thread has read what it was told last
-                *tell = l;
-                pair_sync(pair);
-                l += *hear;
                 if (end > s0) {
                     ok = ok && wait_all(&ct.ofull[st], no++ & 1u, abort_flag);
+                    if (!HALVES && !ok) break;
                     tc_fence_after();
                 }
                 finish<F16, TREE, HALVES>(p, ct, *pp, end > s0, tO, smem + kOffStage + (warp - 4) * kStageBytes,
                                           reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, lim, nodes, rows);
                 tc_fence_before();
-                pair_sync(pair);
                 if (HALVES && tid == 128 && end > s0) mbar_arrive(&ct.qempty[1]);
             }
             step0 += pp->s1 - s0;
@@ -1060,21 +1075,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Runs that several CTAs worked on: a CTA per (share that a run begins in and does not end in, 32 rows), a lane per row.
 // The partials O_c of the shares from there to the run's end are weighted 2^(m_c - M).
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinParts = kMaxCtas;
 
 template <bool F16, bool TREE>
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_constant__ Params p, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_constant__ Params p, int grid) {
+    __shared__ float weight[kJoinParts][32];   // of a part, by row
+    __shared__ float top[kJoinWarps][32], sums[kJoinWarps][32];
     wait_prior_grid();
     allow_dependent_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = p.row_tiles;
     const int4 d = p.desc[2 * (size_t)blockIdx.x + 1];
     if (d.x == 0) return;
-    Seq<TREE> q;
-    q.load(p, d.y, false);
-    const int in_tile = blockIdx.y * 32 + lane, st = blockIdx.y >> 2, r = in_tile & (kRows - 1);
-    const int tok = (int)(r * p.by_group >> 16), token = d.w + st * p.toks + tok;
-    const bool mine = tok < p.toks && token < q.lq;
-    if (!__syncthreads_or(mine)) return;
     int parts = 0;   // shares behind this one
     for (int c0 = 1;; c0 += 32) {
         const long long c = blockIdx.x + (long long)(c0 + lane) * step;
@@ -1085,39 +1097,54 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const __grid_cons
             break;
         }
     }
+    Seq<TREE> q;
+    q.load(p, d.y, false);
+    const int in_tile = blockIdx.y * 32 + lane, st = blockIdx.y >> 2, r = in_tile & (kRows - 1);
+    const int tok = (int)(r * p.by_group >> 16), token = d.w + st * p.toks + tok;
+    const bool mine = tok < p.toks && token < q.lq;
+    if (!__syncthreads_or(mine)) return;
     auto slot = [&](int i) { return 2 * ((size_t)blockIdx.x + (size_t)i * step) + (i == 0 ? 1 : 0); };
-    float M = -INFINITY, L = 0.0f;
-    if (mine) {
-#pragma unroll 8
-        for (int i = 0; i <= parts; ++i) {
-            const float2 x = p.ml[slot(i) * p.rows_cap + in_tile];
-            M = fmaxf(M, x.y == 0.0f ? -INFINITY : x.x);
-        }
-        float4 o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int i = 0; i <= parts; ++i) {
-            const float2 x = p.ml[slot(i) * p.rows_cap + in_tile];
-            if (x.y == 0.0f) continue;   // saw nothing
-            const float f = ex2(x.x - M);
-            L = fmaf(f, x.y, L);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 y = p.part[(slot(i) * 32 + warp + 8 * e) * p.rows_cap + in_tile];
-                o[e].x = fmaf(f, y.x, o[e].x);
-                o[e].y = fmaf(f, y.y, o[e].y);
-                o[e].z = fmaf(f, y.z, o[e].z);
-                o[e].w = fmaf(f, y.w, o[e].w);
-            }
-        }
-        const size_t at = (size_t)(q.q0 + token) * p.n_heads + d.z * p.group + (r - tok * p.group);
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            store4<F16>(p, at * 128 + 4 * (warp + 8 * e), o[e].x * inv, o[e].y * inv, o[e].z * inv, o[e].w * inv);
-        if (warp == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    // each warp a part in eight: maxima, then weights and their sum
+    float M = -INFINITY;
+    for (int i = warp; i <= parts; i += kJoinWarps) {
+        const float2 x = mine ? p.ml[slot(i) * p.rows_cap + in_tile] : make_float2(0.0f, 0.0f);
+        weight[i][lane] = x.y == 0.0f ? -INFINITY : x.x;   // -inf: saw nothing
+        M = fmaxf(M, weight[i][lane]);
     }
+    top[warp][lane] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, top[w][lane]);
+    float L = 0.0f;
+    for (int i = warp; i <= parts; i += kJoinWarps) {
+        const float l = mine ? p.ml[slot(i) * p.rows_cap + in_tile].y : 0.0f;
+        const float f = l == 0.0f ? 0.0f : ex2(weight[i][lane] - M);
+        weight[i][lane] = f;
+        L = fmaf(f, l, L);
+    }
+    sums[warp][lane] = L;
+    __syncthreads();
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) L += sums[w][lane];
+    if (!mine) return;
+    // four dimensions a thread
+    const int d4 = blockIdx.z * kJoinWarps + warp;
+    const float4 *part = p.part + (size_t)d4 * p.rows_cap + in_tile;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = 0; i <= parts; ++i) {
+        const float f = weight[i][lane];
+        const float4 y = part[slot(i) * 32 * p.rows_cap];
+        o.x = f == 0.0f ? o.x : fmaf(f, y.x, o.x);
+        o.y = f == 0.0f ? o.y : fmaf(f, y.y, o.y);
+        o.z = f == 0.0f ? o.z : fmaf(f, y.z, o.z);
+        o.w = f == 0.0f ? o.w : fmaf(f, y.w, o.w);
+    }
+    const size_t at = (size_t)(q.q0 + token) * p.n_heads + d.z * p.group + (r - tok * p.group);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    store4<F16>(p, at * 128 + 4 * d4, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (d4 == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // Rows of a tile that `tokens` tokens can fill.
@@ -1146,8 +1173,8 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bo
                           m[4], p);
     if (st != QSA_OK || !split) return st;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32));
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32), 32 / kJoinWarps);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
