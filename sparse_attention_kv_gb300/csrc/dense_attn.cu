@@ -50,8 +50,8 @@ constexpr int kStageBytes = 4096;     // per softmax warp: 32 rows of 128 bytes 
 constexpr int kPieces = 4;            // pieces that are published ahead
 constexpr int kInfo = 8;              // steps whose page limits are held: more than the ring holds
 constexpr int kMaxCtas = 152;
-constexpr int kWhole = 4;             // runs of so few steps are not split
-constexpr int kRunKeys = 256;         // what a run's beginning and end cost, in keys
+constexpr int kWhole = 8;             // runs of so few steps are not split
+constexpr int kRunKeys = 512;         // what a run's beginning and end cost, in keys
 constexpr int kMinShare = 384;        // least work, in keys, that a CTA is started for
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
@@ -487,36 +487,42 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint8_t *line = stage + lane * 128;
+    const int unit = p.out_f32 ? 4 : 2;
+    // 32 dimensions a round: in 16 bits two rounds make 128 bytes of each row, in 32 bits one
 #pragma unroll 1
-    for (int d = 0; d < 128; d += 64) {
-        uint32_t o[4][16];
+    for (int d = 0; d < 128; d += 32) {
+        uint32_t o[2][16];
         auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
         __syncwarp();
         if (have) {
-            tmem_ld64_nowait(tO + d, o);
+            tmem_ld16_nowait(tO + d, o[0]);
+            tmem_ld16_nowait(tO + d + 16, o[1]);
             tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) reg_fence(o[i]);
+            reg_fence(o[0]);
+            reg_fence(o[1]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) o[i >> 4][i & 15] = 0u;
+            for (int i = 0; i < 32; ++i) o[i >> 4][i & 15] = 0u;
         }
         if constexpr (HALVES) {
             if (have) {
+                float4 *at = box + (d & 32) / 4 * kRows + r;   // the box holds two rounds
                 if (st == 1)
 #pragma unroll
-                    for (int i = 0; i < 64; i += 4) box[(i / 4) * kRows + r] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+                    for (int i = 0; i < 32; i += 4) at[(i / 4) * kRows] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
                 soft_sync();
                 if (st == 0)
 #pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 x = box[(i / 4) * kRows + r];
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 x = at[(i / 4) * kRows];
                         const float y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[(i + e) >> 4][(i + e) & 15] = __float_as_uint(val(i + e) * keep + y[e] * add);
                     }
-                if (d == 64) fence_proxy_async();   // the box is Q's memory again
-                soft_sync();
+                if (d == 96) {
+                    fence_proxy_async();   // the box is Q's memory again
+                    soft_sync();
+                }
             }
             if (st == 1) continue;
         }
@@ -526,7 +532,7 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
                 const uint16_t *v = static_cast<const uint16_t *>(p.v.p) + (int64_t)((TREE ? pc.q0 : pc.k0) + t) * p.v.token +
                                     (int64_t)pc.g * p.v.head + d;
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
+                for (int i = 0; i < 32; ++i)
                     if (not_finite<F16>(v[i]) & 0xFFFFu) o[i >> 4][i & 15] = __float_as_uint(val(i) + widen<F16>(v[i]));
             }
         }
@@ -534,39 +540,31 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
             if (mine) {
                 float4 *part = p.part + (slot * 32 + d / 4) * p.rows_cap + in_tile;
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) part[(i / 4) * p.rows_cap] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
+                for (int i = 0; i < 32; i += 4) part[(i / 4) * p.rows_cap] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
             }
             continue;
         }
-        // 128 bytes of each row at a time; its 16-byte units are rotated by the row so that neither way meets a bank twice
-        auto drain = [&](int at) {   // eight lanes write a row's 128 bytes, which begin at its byte `at`
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int rr = 4 * i + (lane >> 3), row = (warp & 3) * 32 + rr;
-                const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                if (row < rows)
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + output(row) * (p.out_f32 ? 512 : 256) + at +
-                                               16 * (lane & 7)) = x;
-            }
-            __syncwarp();
-        };
+        // the row's 16-byte units are rotated by the row so that neither way meets a bank twice
         if (p.out_f32) {
 #pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(line + (((i >> 2) ^ (lane & 7)) << 4)) =
-                        make_float4(val(h + i) * inv, val(h + i + 1) * inv, val(h + i + 2) * inv, val(h + i + 3) * inv);
-                drain(4 * (d + h));
-            }
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(line + (((i >> 2) ^ (lane & 7)) << 4)) =
+                    make_float4(val(i) * inv, val(i + 1) * inv, val(i + 2) * inv, val(i + 3) * inv);
         } else {
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
-                *reinterpret_cast<uint4 *>(line + (((i >> 3) ^ (lane & 7)) << 4)) =
+            for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4 *>(line + (((((d & 32) + i) >> 3) ^ (lane & 7)) << 4)) =
                     make_uint4(pack16<F16>(val(i) * inv, val(i + 1) * inv), pack16<F16>(val(i + 2) * inv, val(i + 3) * inv),
                                pack16<F16>(val(i + 4) * inv, val(i + 5) * inv), pack16<F16>(val(i + 6) * inv, val(i + 7) * inv));
-            drain(2 * d);
+            if ((d & 32) == 0) continue;
+        }
+        __syncwarp();   // eight lanes write a row's 128 bytes
+        const int at = (d + 32) * unit - 128 + 16 * (lane & 7);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int rr = 4 * i + (lane >> 3), row = (warp & 3) * 32 + rr;
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (row < rows) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + output(row) * (128 * unit) + at) = x;
         }
     }
     __syncwarp();
@@ -953,84 +951,123 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = ok && wait_all(&ct.sfull[st], ns++ & 1u, abort_flag);
                 if (!HALVES && !ok) break;
                 tc_fence_after();
-                uint32_t v[kCols / 16][16];
-#pragma unroll
-                for (int h = 0; h < kCols / 64; ++h) tmem_ld64_nowait(tS + 64 * h, reinterpret_cast<uint32_t(&)[4][16]>(v[4 * h]));
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < kCols / 16; ++i) reg_fence(v[i]);
-                if constexpr (TREE) {
-                    const bool paged = j < n - 1;
-#pragma unroll
-                    for (int h = 0; h < kCols / 64; ++h) {   // the keys of a page
-                        const int page = HALVES ? st : h;
-                        const int valid = paged ? ct.info[(step0 + j - s0) % kInfo][page] : 0;
-                        if (valid < 64) {
-                            const unsigned long long see = paged ? (1ull << valid) - 1ull : page ? 0ull : nodes;
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (!((i < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) & 1u << (i & 31)))
-                                    v[4 * h + (i >> 4)][i & 15] = 0xFF800000u;
-                        }
-                    }
-                } else if ((j + 1) * kKeys > low) {
-                    const int left = lim - j * kKeys - (HALVES ? 64 * st : 0);
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        if (i >= left) v[i >> 4][i & 15] = 0xFF800000u;
+                // which keys this row sees, 32 a word; all of them in most steps
+                const bool paged = TREE && j < n - 1;
+                int valid[2] = {0, 0};
+                if (paged) {
+                    valid[0] = ct.info[(step0 + j - s0) % kInfo][0];
+                    valid[1] = ct.info[(step0 + j - s0) % kInfo][1];
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < kCols; i += 2)
-                    top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(v[i >> 4][i & 15]),
-                                                                       __uint_as_float(v[i >> 4][(i & 15) + 1])));
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                if (j == s0) {
-                    m = now;
-                } else {
+                const bool some = TREE ? (HALVES ? valid[st] : min(valid[0], valid[1])) < 64 : (j + 1) * kKeys > low;
+                auto sees = [&](int q) -> uint32_t {
+                    const int at = (HALVES ? 64 * st : 0) + 32 * q;   // the word's first key in the step
+                    if (TREE && !paged) return at == 0 ? (uint32_t)nodes : at == 32 ? (uint32_t)(nodes >> 32) : 0u;
+                    const int left = TREE ? valid[at >> 6] - (at & 63) : lim - j * kKeys - at;
+                    return left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1u;
+                };
+                // the row's reference, given the step's largest logit
+                auto settle = [&](float now) {
+                    if (j == s0) {
+                        m = now;
+                        return;
+                    }
                     const bool risen = now > m + rise;
-                    if (__any_sync(~0u, risen)) {
-                        // S of this step is complete, so every product before it is: O may be scaled in place
-                        const float f = risen ? ex2((m - now) * c) : 1.0f;
-                        if (risen) m = now;
-                        l *= f;
+                    if (!__any_sync(~0u, risen)) return;
+                    // S of this step is complete, so every product before it is: O may be scaled in place
+                    const float f = risen ? ex2((m - now) * c) : 1.0f;
+                    if (risen) m = now;
+                    l *= f;
 #pragma unroll 1
-                        for (int d = 0; d < 128; d += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_nowait(tO + d, o);
-                            tmem_wait_ld();
-                            reg_fence(o);
+                    for (int d = 0; d < 128; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld16_nowait(tO + d, o);
+                        tmem_wait_ld();
+                        reg_fence(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st16(tO + d, o);
-                        }
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(tO + d, o);
                     }
-                }
-                const float mc = m == -INFINITY ? 0.0f : m * c;
-                const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+                };
                 f32x2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {   // a part of the weights is passed on as soon as it is there
-#pragma unroll
-                    for (int q = 0; q < kCols / 64; ++q) {   // 32 keys
-                        uint32_t w[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int k = h * (kCols / 2) + 32 * q + 2 * i;
-                            float y0, y1;
-                            unpack2(fma2(pack2(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1])), c2, nm2),
-                                    y0, y1);
-                            y0 = ex2(y0);
-                            y1 = ex2(y1);
-                            sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
-                            w[i] = pack16<F16>(y0, y1);
-                        }
-                        tmem_st16(tS + h * (kCols / 4) + 16 * q, w);
-                    }
+                auto weigh = [&](float s0, float s1, f32x2 c2, f32x2 nm2, int i) -> uint32_t {
+                    float y0, y1;
+                    unpack2(fma2(pack2(s0, s1), c2, nm2), y0, y1);
+                    y0 = ex2(y0);
+                    y1 = ex2(y1);
+                    sum[i & 1] = add2(sum[i & 1], pack2(y0, y1));
+                    return pack16<F16>(y0, y1);
+                };
+                auto pass_on = [&](int h) {   // a part of the weights goes on as soon as it is there
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ct.pready[st][h]);
+                };
+                if (!some) {
+                    uint32_t v[kCols / 16][16];
+#pragma unroll
+                    for (int h = 0; h < kCols / 64; ++h) tmem_ld64_nowait(tS + 64 * h, reinterpret_cast<uint32_t(&)[4][16]>(v[4 * h]));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < kCols / 16; ++i) reg_fence(v[i]);
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kCols; i += 2)
+                        top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(v[i >> 4][i & 15]),
+                                                                           __uint_as_float(v[i >> 4][(i & 15) + 1])));
+                    settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int q = 0; q < kCols / 64; ++q) {   // 32 keys
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = h * (kCols / 2) + 32 * q + 2 * i;
+                                w[i] = weigh(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1]), c2, nm2, i);
+                            }
+                            tmem_st16(tS + h * (kCols / 4) + 16 * q, w);
+                        }
+                        pass_on(h);
+                    }
+                } else {
+                    // 32 keys a round, read twice, in little code: short runs spend their time in steps like this one, and on
+                    // fetching instructions
+                    auto logits_of = [&](int q, uint32_t (&x)[2][16]) {
+                        tmem_ld16_nowait(tS + 32 * q, x[0]);
+                        tmem_ld16_nowait(tS + 32 * q + 16, x[1]);
+                        const uint32_t word = sees(q);
+                        tmem_wait_ld();
+                        reg_fence(x[0]);
+                        reg_fence(x[1]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(word & 1u << i)) x[i >> 4][i & 15] = 0xFF800000u;
+                    };
+                    float now = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < kCols / 32; ++q) {
+                        uint32_t x[2][16];
+                        logits_of(q, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) now = fmaxf(now, fmaxf(__uint_as_float(x[0][i]), __uint_as_float(x[1][i])));
+                    }
+                    settle(now);
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
+#pragma unroll 1
+                    for (int q = 0; q < kCols / 32; ++q) {
+                        uint32_t x[2][16], w[16];
+                        logits_of(q, x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = weigh(__uint_as_float(x[i >> 3][2 * (i & 7)]), __uint_as_float(x[i >> 3][2 * (i & 7) + 1]), c2, nm2, i);
+                        tmem_st16(tS + 16 * q, w);   // over logits that have been read
+                        if (q == kCols / 64 - 1) pass_on(0);
+                    }
+                    pass_on(1);
                 }
                 float a, b;
                 unpack2(add2(sum[0], sum[1]), a, b);
