@@ -52,6 +52,9 @@ constexpr int kInfo = 8;              // steps whose page limits are held: more 
 constexpr int kMaxCtas = 152;
 constexpr int kWhole = 8;             // runs of so few steps are not split
 constexpr int kRunKeys = 512;         // what a run's beginning and end cost, in keys
+constexpr int kTable = 256;           // sequences whose runs are counted in shared memory
+constexpr int kSlack = 8;             // steps that pieces of one length may lie above an even share
+constexpr int kShortRun = 16;         // steps of runs that are dealt out as they are, however few the shares hold
 constexpr int kMinShare = 384;        // least work, in keys, that a CTA is started for
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
@@ -80,6 +83,7 @@ struct Params {
     float4 *part;         // [grid][2][32][rows_cap]: O, four dimensions of a row at a time
     float2 *ml;           // [grid][2][rows_cap]: (m scale log2 e, l)
     int4 *desc;           // [grid][2]: see describe()
+    unsigned *dealt;      // runs dealt out so far, and CTAs that are done; both 0 between calls
     uint32_t *flags;
 };
 
@@ -105,6 +109,8 @@ struct Ctrl {
     int abort;
     int info[kInfo][2];   // valid tokens in each page of a step
     float2 other[kRows];  // HALVES: stream 1's (m, l)
+    int runs[kTable + 1]; // runs of the sequences before each one
+    int dealing;          // the CTAs take runs as they come free
 };
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQBytes;
@@ -216,47 +222,107 @@ struct Seq {
     static __device__ __forceinline__ int keys_of(int lq, int lk, int i) { return min(max(lk - lq + i + 1, 0), lk); }
 };
 
-// A CTA's pieces one after another.
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    return v;
+}
+__device__ __forceinline__ int warp_scan(int v) {   // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int x = __shfl_up_sync(~0u, v, d);
+        if ((int)(threadIdx.x & 31) >= d) v += x;
+    }
+    return v;
+}
+
+// A CTA's pieces one after another (one warp).  Which they are goes by one of three rules, the same in every CTA:
+//  kEven   no more runs than shares: each run in equal pieces, a share each, where that costs little against an even split
+//  kDealt  many runs, short against a share: whole, longest first within a (sequence, KV head), each to the next CTA that is free
+//  kBorder otherwise: all runs laid end to end and cut at equal distances
+// Measured, us, kEven / kBorder: 5 trees over 900 tokens 23 / 28; kDealt / kBorder: 1,024 tokens 33 / 42, 16,384 tokens 2,450 / 2,560.
+enum Rule { kEven, kDealt, kBorder };
+
 template <bool TREE, bool HALVES>
 struct Walk {
     Seq<TREE> q;
-    long long at, x0, x1;   // the beginning of the next run, and the CTA's share of all runs
+    Rule rule;
     int s, g, t, tile;
+    long long at, x0, x1;   // kBorder: the beginning of the next run, and the CTA's share of all runs
+    int run, runs;          // kDealt: the next run
+    unsigned ahead;         // and the one after it, by count behind the first ones
+    int s0, s1;             // kEven: the piece's steps; s0 < 0: no piece (any more)
 
-    __device__ __forceinline__ bool next(const Params &p, Piece &pc) {
+    // The piece s0 .. s1 - 1 of the run (s, g, t); false when this CTA has no rows in it.
+    __device__ __forceinline__ bool fill(const Params &p, Piece &pc, int from, int to, int n) const {
+        pc.s = s;
+        pc.g = g;
+        pc.q0 = q.q0;
+        pc.lq = q.lq;
+        pc.k0 = q.k0;
+        pc.lk = q.lk;
+        pc.tok0 = (TREE ? tile : t) * p.tile;
+        pc.s0 = from;
+        pc.s1 = to;
+        pc.n = n;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int first = pc.tok0 + (HALVES ? 0 : i * p.toks), toks = min(max(q.lq - first, 0), p.toks);
+            pc.rows[i] = toks * p.group;
+            int end = from;
+            if (toks > 0) {
+                end = TREE ? n : (q.keys_of(q.lq, q.lk, first + toks - 1) + kKeys - 1) / kKeys;
+                end = max(min(end, to), from);
+            }
+            pc.e[i] = end;
+        }
+        return pc.tok0 < q.lq;
+    }
+    // Run i of all: by sequence, KV head, tiles from the last one on.
+    __device__ __forceinline__ void locate(const Params &p, const Ctrl &ct, int i) {
+        int lo = 0, hi = p.n_seqs;   // runs[lo] <= i < runs[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (ct.runs[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        if (lo != s) {
+            s = lo;
+            q.load(p, s, false);
+        }
+        const int local = i - ct.runs[lo];
+        g = local / q.tiles;
+        t = q.tiles - 1 - (local - g * q.tiles);
+    }
+    __device__ __forceinline__ bool next(const Params &p, const Ctrl &ct, Piece &pc) {
+        if (rule == kEven) {
+            if (s0 < 0) return false;
+            const int from = s0;
+            s0 = -1;
+            return fill(p, pc, from, s1, q.steps(p, t));
+        }
+        if (rule == kDealt) {
+            while (run < runs) {
+                locate(p, ct, run);
+                run = (int)(gridDim.x / (unsigned)p.row_tiles + __shfl_sync(~0u, ahead, 0));
+                if ((threadIdx.x & 31) == 0 && run < runs) ahead = atomicAdd(p.dealt + 2 * tile, 1u);
+                const int n = q.steps(p, t);
+                if (fill(p, pc, 0, n, n)) return true;
+            }
+            return false;
+        }
         while (at < x1 && s < p.n_seqs) {
             const int n = q.steps(p, t), work = q.work(p, t);
             const long long from = at;
-            int s0 = 0, s1 = n;
+            int a0 = 0, a1 = n;
             bool take = from >= x0;
             if (n > kWhole) {   // the step that begins nearest to a border; both sides of it compute the same
                 const long long a = (x0 - from - kRunKeys + kKeys / 2) / kKeys, b = (x1 - from - kRunKeys + kKeys / 2) / kKeys;
-                s0 = x0 <= from || a <= 0 ? 0 : (int)(a < n ? a : n);
-                s1 = b <= 0 ? 0 : b < n && x1 < from + work ? (int)b : n;
-                take = s1 > s0;
+                a0 = x0 <= from || a <= 0 ? 0 : (int)(a < n ? a : n);
+                a1 = b <= 0 ? 0 : b < n && x1 < from + work ? (int)b : n;
+                take = a1 > a0;
             }
-            pc.s = s;
-            pc.g = g;
-            pc.q0 = q.q0;
-            pc.lq = q.lq;
-            pc.k0 = q.k0;
-            pc.lk = q.lk;
-            pc.tok0 = (TREE ? tile : t) * p.tile;
-            pc.s0 = s0;
-            pc.s1 = s1;
-            pc.n = n;
-            if (pc.tok0 >= q.lq) take = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int first = pc.tok0 + (HALVES ? 0 : i * p.toks), toks = min(max(q.lq - first, 0), p.toks);
-                pc.rows[i] = toks * p.group;
-                int end = s0;
-                if (toks > 0) {
-                    end = TREE ? n : (q.keys_of(q.lq, q.lk, first + toks - 1) + kKeys - 1) / kKeys;
-                    end = max(min(end, s1), s0);
-                }
-                pc.e[i] = end;
-            }
+            take = fill(p, pc, a0, a1, n) && take;
             at += work;
             if (++t >= q.tiles) {
                 t = 0;
@@ -274,18 +340,12 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    return v;
-}
-
-// This CTA's share of all runs, and the run it begins in (one warp; every lane gets it).
+// The rule, and where this CTA begins (one warp).
 template <bool TREE, bool HALVES>
-__device__ void find_share(const Params &p, Walk<TREE, HALVES> &w) {
+__device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     const int lane = threadIdx.x & 31;
     const unsigned share = blockIdx.x / (unsigned)p.row_tiles;
-    const bool tell = blockIdx.x == 0;
+    const bool tell = blockIdx.x == 0, counted = p.n_seqs <= kTable;
     Seq<TREE> &q = w.q;
     auto weight = [&](int s, bool say) -> long long {
         if (s >= p.n_seqs) return 0;
@@ -293,22 +353,90 @@ __device__ void find_share(const Params &p, Walk<TREE, HALVES> &w) {
         return p.n_kv * q.cum(p, q.tiles);
     };
     long long total = 0, first = 0;   // first: the weights of sequences 0 .. 31
+    int runs = 0, longest = 0;
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
         const long long x = weight(s0 + lane, tell);
         if (s0 == 0) first = x;
         total += warp_sum(x);
+        const bool in = s0 + lane < p.n_seqs;
+        longest = max(longest, in && q.tiles > 0 ? q.work(p, q.tiles - 1) : 0);
+        if (counted) {
+            const int mine = in ? p.n_kv * q.tiles : 0, incl = warp_scan(mine);
+            if (in) ct.runs[s0 + lane + 1] = runs + incl;
+            runs += __shfl_sync(~0u, incl, 31);
+        }
+    }
+    longest = __reduce_max_sync(~0u, longest);
+    if (lane == 0) ct.runs[0] = 0;
+    __syncwarp();
+    w.tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
+    w.rule = kBorder;
+    w.s = -1;
+    if (counted && runs <= p.shares) {
+        constexpr int kTurns = (kMaxCtas + 31) / 32;
+        int n[kTurns], steps = 0;
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            const int i = lane + 32 * k;
+            n[k] = 0;
+            if (i < runs) {
+                w.locate(p, ct, i);
+                n[k] = max(q.steps(p, w.t), 1);
+            }
+            steps += n[k];
+        }
+        steps = __reduce_add_sync(~0u, min(steps, 1 << 24));
+        const int even = (steps + p.shares - 1) / p.shares;
+        int len = max(even, kWhole);   // of a piece, at most
+        while (len <= even + kSlack) {
+            int pieces = 0;
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) pieces += (n[k] + len - 1) / len;
+            if (__reduce_add_sync(~0u, pieces) <= p.shares) break;
+            ++len;
+        }
+        if (len <= even + kSlack || len == kWhole) {
+            w.rule = kEven;
+            w.s0 = -1;
+            int before = 0;
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                const int c = (n[k] + len - 1) / len, incl = warp_scan(c);
+                const int part = (int)share - (before + incl - c);
+                const unsigned mine = __ballot_sync(~0u, part >= 0 && part < c);
+                if (mine) {
+                    const int l = __ffs(mine) - 1, parts = __shfl_sync(~0u, c, l), of = __shfl_sync(~0u, part, l);
+                    w.s = -1;
+                    w.locate(p, ct, l + 32 * k);
+                    const int all = q.steps(p, w.t);
+                    w.s0 = (int)((long long)of * all / parts);
+                    w.s1 = (int)((long long)(of + 1) * all / parts);
+                    break;
+                }
+                before += __shfl_sync(~0u, incl, 31);
+            }
+            return;
+        }
+    }
+    if (counted && runs > p.shares && longest <= max(total / p.shares / 4, (long long)kShortRun * kKeys + kRunKeys)) {
+        w.rule = kDealt;
+        w.run = (int)share;
+        w.runs = runs;
+        w.s = -1;
+        w.ahead = 0;
+        if (lane == 0 && w.run < runs) w.ahead = atomicAdd(p.dealt + 2 * w.tile, 1u);
+        return;
     }
     long long used = (total + kMinShare - 1) / kMinShare;
     used = used < 1 ? 1 : used > p.shares ? p.shares : used;
     w.x0 = share < used ? mul_div(share, total, (unsigned)used) : total;
     w.x1 = share < used ? mul_div(share + 1, total, (unsigned)used) : total;
-    w.tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
     long long before = 0;
     w.at = w.x0;
     w.s = p.n_seqs;
     w.g = w.t = 0;
     for (int s0 = 0; s0 < p.n_seqs && w.x0 < w.x1; s0 += 32) {
-        const long long x = s0 == 0 && p.n_seqs <= 32 ? first : weight(s0 + lane, false);
+        const long long x = s0 == 0 && p.n_seqs <= 32 && runs > p.shares ? first : weight(s0 + lane, false);
         long long incl = x;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -492,7 +620,6 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
 #pragma unroll 1
     for (int d = 0; d < 128; d += 32) {
         uint32_t o[2][16];
-        auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
         __syncwarp();
         if (have) {
             tmem_ld16_nowait(tO + d, o[0]);
@@ -504,6 +631,7 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i >> 4][i & 15] = 0u;
         }
+        auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
         if constexpr (HALVES) {
             if (have) {
                 float4 *at = box + (d & 32) / 4 * kRows + r;   // the box holds two rounds
@@ -646,7 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.desc[2 * (size_t)blockIdx.x + 1] = make_int4(0, 0, 0, 0);
         }
         Walk<TREE, HALVES> walk;
-        find_share(p, walk);
+        find_share(p, ct, walk);
+        if (lane == 0) ct.dealing = walk.rule == kDealt;
         Piece pc;
         int step = 0, no = 0;
         uint32_t nq[2] = {0, 0};
@@ -665,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         while (ok) {
-            const bool more = walk.next(p, pc);
+            const bool more = walk.next(p, ct, pc);
             pc.stop = !more;
             pc.bad = 0;
             if (!(ok = wait_all(&ct.pempty[no % kPieces], ((uint32_t)(no / kPieces) & 1u) ^ 1u, abort_flag))) break;
@@ -1107,18 +1236,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (tid == 0 && ct.abort) atomicOr(p.flags, QSA_FLAG_WAIT_TIMEOUT);
+    if (tid == 0) {
+        if (ct.abort) atomicOr(p.flags, QSA_FLAG_WAIT_TIMEOUT);
+        if (ct.dealing) {   // the last CTA leaves the counts at 0
+            unsigned *dealt = p.dealt + 2 * (blockIdx.x % (unsigned)p.row_tiles);
+            if (atomicAdd(dealt + 1, 1u) + 1u == (unsigned)p.shares) dealt[0] = dealt[1] = 0u;
+        }
+    }
 }
 
 // Runs that several CTAs worked on: a CTA per (share that a run begins in and does not end in, 32 rows), a lane per row.
 // The partials O_c of the shares from there to the run's end are weighted 2^(m_c - M).
 constexpr int kJoinWarps = 8;
-constexpr int kJoinParts = kMaxCtas;
+constexpr int kJoinDims = 4;   // groups of four dimensions a CTA joins where parts may be many
+constexpr int kJoinTurns = (kMaxCtas + kJoinWarps - 1) / kJoinWarps;
 
-template <bool F16, bool TREE>
+// MANY: few rows (a decode step), so a run may lie in many parts: the warps share them out and meet in shared memory.
+// Otherwise a warp takes four dimensions of all parts.
+template <bool F16, bool TREE, bool MANY>
 __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_constant__ Params p, int grid) {
-    __shared__ float weight[kJoinParts][32];   // of a part, by row
-    __shared__ float top[kJoinWarps][32], sums[kJoinWarps][32];
     wait_prior_grid();
     allow_dependent_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = p.row_tiles;
@@ -1141,46 +1277,75 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
     const bool mine = tok < p.toks && token < q.lq;
     if (!__syncthreads_or(mine)) return;
     auto slot = [&](int i) { return 2 * ((size_t)blockIdx.x + (size_t)i * step) + (i == 0 ? 1 : 0); };
-    // each warp a part in eight: maxima, then weights and their sum
-    float M = -INFINITY;
-    for (int i = warp; i <= parts; i += kJoinWarps) {
-        const float2 x = mine ? p.ml[slot(i) * p.rows_cap + in_tile] : make_float2(0.0f, 0.0f);
-        weight[i][lane] = x.y == 0.0f ? -INFINITY : x.x;   // -inf: saw nothing
-        M = fmaxf(M, weight[i][lane]);
-    }
-    top[warp][lane] = M;
-    __syncthreads();
+    auto sums_of = [&](int i) { return p.ml[slot(i) * p.rows_cap + in_tile]; };   // a sum of 0: saw nothing
+    auto part_of = [&](int i, int d4) { return p.part[(slot(i) * 32 + d4) * p.rows_cap + in_tile]; };
+    auto add = [](float4 &o, float f, const float4 &y) {
+        o.x = fmaf(f, y.x, o.x);
+        o.y = fmaf(f, y.y, o.y);
+        o.z = fmaf(f, y.z, o.z);
+        o.w = fmaf(f, y.w, o.w);
+    };
+    float M = -INFINITY, L = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int d4 = blockIdx.z * kJoinWarps + warp;
+    if constexpr (MANY) {
+        __shared__ float top[kJoinWarps][32], sums[kJoinWarps][32];
+        __shared__ float4 joined[kJoinWarps][kJoinDims][32];
+        float2 ml[kJoinTurns];
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, top[w][lane]);
-    float L = 0.0f;
-    for (int i = warp; i <= parts; i += kJoinWarps) {
-        const float l = mine ? p.ml[slot(i) * p.rows_cap + in_tile].y : 0.0f;
-        const float f = l == 0.0f ? 0.0f : ex2(weight[i][lane] - M);
-        weight[i][lane] = f;
-        L = fmaf(f, l, L);
-    }
-    sums[warp][lane] = L;
-    __syncthreads();
-    L = 0.0f;
+        for (int k = 0; k < kJoinTurns; ++k) {
+            const int i = warp + k * kJoinWarps;
+            ml[k] = mine && i <= parts ? sums_of(i) : make_float2(-INFINITY, 0.0f);
+        }
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) L += sums[w][lane];
-    if (!mine) return;
-    // four dimensions a thread
-    const int d4 = blockIdx.z * kJoinWarps + warp;
-    const float4 *part = p.part + (size_t)d4 * p.rows_cap + in_tile;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int i = 0; i <= parts; ++i) {
-        const float f = weight[i][lane];
-        const float4 y = part[slot(i) * 32 * p.rows_cap];
-        o.x = f == 0.0f ? o.x : fmaf(f, y.x, o.x);
-        o.y = f == 0.0f ? o.y : fmaf(f, y.y, o.y);
-        o.z = f == 0.0f ? o.z : fmaf(f, y.z, o.z);
-        o.w = f == 0.0f ? o.w : fmaf(f, y.w, o.w);
+        for (int k = 0; k < kJoinTurns; ++k)
+            if (ml[k].y != 0.0f) M = fmaxf(M, ml[k].x);
+        top[warp][lane] = M;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, top[w][lane]);
+        float4 o[kJoinDims];
+#pragma unroll
+        for (int e = 0; e < kJoinDims; ++e) o[e] = x;
+#pragma unroll
+        for (int k = 0; k < kJoinTurns; ++k) {
+            const float f = ml[k].y == 0.0f ? 0.0f : ex2(ml[k].x - M);
+            L = fmaf(f, ml[k].y, L);
+            if (f == 0.0f) continue;
+#pragma unroll
+            for (int e = 0; e < kJoinDims; ++e) add(o[e], f, part_of(warp + k * kJoinWarps, blockIdx.z * kJoinDims + e));
+        }
+        sums[warp][lane] = L;
+#pragma unroll
+        for (int e = 0; e < kJoinDims; ++e) joined[warp][e][lane] = o[e];
+        __syncthreads();
+        if (warp >= kJoinDims || !mine) return;
+        L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            add(x, 1.0f, joined[w][warp][lane]);
+            L += sums[w][lane];
+        }
+        d4 = blockIdx.z * kJoinDims + warp;
+    } else {
+        if (!mine) return;
+#pragma unroll 4
+        for (int i = 0; i <= parts; ++i) {
+            const float2 ml = sums_of(i);
+            M = fmaxf(M, ml.y == 0.0f ? -INFINITY : ml.x);
+        }
+#pragma unroll 4
+        for (int i = 0; i <= parts; ++i) {
+            const float2 ml = sums_of(i);
+            const float4 y = part_of(i, d4);
+            const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
+            L = fmaf(f, ml.y, L);
+            if (f != 0.0f) add(x, f, y);
+        }
     }
     const size_t at = (size_t)(q.q0 + token) * p.n_heads + d.z * p.group + (r - tok * p.group);
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    store4<F16>(p, at * 128 + 4 * d4, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    store4<F16>(p, at * 128 + 4 * d4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     if (d4 == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
@@ -1209,8 +1374,9 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bo
     st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE, HALVES>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3],
                           m[4], p);
     if (st != QSA_OK || !split) return st;
+    const bool many = p.rows_cap <= 64;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32), 32 / kJoinWarps);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32), 32 / (many ? kJoinDims : kJoinWarps));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
@@ -1218,7 +1384,9 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bo
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return check_cuda(cudaLaunchKernelEx(&cfg, combine_kernel<F16, TREE>, p, grid), "combine_kernel launch");
+    return check_cuda(many ? cudaLaunchKernelEx(&cfg, combine_kernel<F16, TREE, true>, p, grid)
+                           : cudaLaunchKernelEx(&cfg, combine_kernel<F16, TREE, false>, p, grid),
+                      "combine_kernel launch");
 }
 
 template <bool TREE>
@@ -1252,6 +1420,7 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.n_pages = a.table.n_pages;
     p.n_tokens = a.n_tokens;
     p.flags = a.flags;
+    p.dealt = static_cast<unsigned *>(a.ws) + 16;   // in the first 256 bytes, behind the flags word; two counts for each tile of rows
     char *ws = static_cast<char *>(a.ws) + 256;
     p.desc = reinterpret_cast<int4 *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + kMaxCtas * 2 * sizeof(int4));
