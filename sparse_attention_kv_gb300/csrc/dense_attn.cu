@@ -190,12 +190,12 @@ struct Seq {
         len = min(max(b, c0), most) - c0;
     }
     // What lane l of the warp has loaded.
-    __device__ __forceinline__ void take(int l) {
-        q0 = __shfl_sync(~0u, q0, l);
-        lq = __shfl_sync(~0u, lq, l);
-        k0 = __shfl_sync(~0u, k0, l);
-        lk = __shfl_sync(~0u, lk, l);
-        tiles = __shfl_sync(~0u, tiles, l);
+    __device__ __forceinline__ void take(const Seq &x, int l) {
+        q0 = __shfl_sync(~0u, x.q0, l);
+        lq = __shfl_sync(~0u, x.lq, l);
+        k0 = __shfl_sync(~0u, x.k0, l);
+        lk = __shfl_sync(~0u, x.lk, l);
+        tiles = __shfl_sync(~0u, x.tiles, l);
     }
     __device__ __forceinline__ int steps(const Params &p, int t) const {
         if constexpr (TREE) return (lk + kKeys - 1) / kKeys + 1;   // the pages, then the drafts
@@ -250,7 +250,8 @@ struct Walk {
     int s, g, t, tile;
     long long at, x0, x1;   // kBorder: the beginning of the next run, and the CTA's share of all runs
     int run, runs;          // kDealt: the next run
-    unsigned ahead;         // and the one after it, by count behind the first ones
+    bool begun;
+    Seq<TREE> mine;         // up to 32 sequences: a lane each
     int s0, s1;             // kEven: the piece's steps; s0 < 0: no piece (any more)
 
     // The piece s0 .. s1 - 1 of the run (s, g, t); false when this CTA has no rows in it.
@@ -278,7 +279,7 @@ struct Walk {
         }
         return pc.tok0 < q.lq;
     }
-    // Run i of all: by sequence, KV head, tiles from the last one on.
+    // Run i of all: by sequence, KV head, tiles from the last one on.  Every lane calls, for a run of its own.
     __device__ __forceinline__ void locate(const Params &p, const Ctrl &ct, int i) {
         int lo = 0, hi = p.n_seqs;   // runs[lo] <= i < runs[hi]
         while (hi - lo > 1) {
@@ -286,13 +287,13 @@ struct Walk {
             if (ct.runs[mid] <= i) lo = mid;
             else hi = mid;
         }
-        if (lo != s) {
-            s = lo;
-            q.load(p, s, false);
-        }
-        const int local = i - ct.runs[lo];
-        g = local / q.tiles;
-        t = q.tiles - 1 - (local - g * q.tiles);
+        s = lo;
+        __syncwarp();
+        if (p.n_seqs <= 32) q.take(mine, lo);
+        else q.load(p, lo, false);
+        const int local = i - ct.runs[lo], tiles = max(q.tiles, 1);
+        g = local / tiles;
+        t = tiles - 1 - (local - g * tiles);
     }
     __device__ __forceinline__ bool next(const Params &p, const Ctrl &ct, Piece &pc) {
         if (rule == kEven) {
@@ -303,9 +304,14 @@ struct Walk {
         }
         if (rule == kDealt) {
             while (run < runs) {
+                if (begun) {   // the copies of the run before are on their way
+                    unsigned i = 0;
+                    if ((threadIdx.x & 31) == 0) i = atomicAdd(p.dealt + 2 * tile, 1u);
+                    run = p.shares + (int)__shfl_sync(~0u, i, 0);
+                    if (run >= runs) break;
+                }
+                begun = true;
                 locate(p, ct, run);
-                run = (int)(gridDim.x / (unsigned)p.row_tiles + __shfl_sync(~0u, ahead, 0));
-                if ((threadIdx.x & 31) == 0 && run < runs) ahead = atomicAdd(p.dealt + 2 * tile, 1u);
                 const int n = q.steps(p, t);
                 if (fill(p, pc, 0, n, n)) return true;
             }
@@ -348,7 +354,10 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     const bool tell = blockIdx.x == 0, counted = p.n_seqs <= kTable;
     Seq<TREE> &q = w.q;
     auto weight = [&](int s, bool say) -> long long {
-        if (s >= p.n_seqs) return 0;
+        if (s >= p.n_seqs) {
+            q = Seq<TREE>{};
+            return 0;
+        }
         q.load(p, s, say);
         return p.n_kv * q.cum(p, q.tiles);
     };
@@ -356,7 +365,10 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     int runs = 0, longest = 0;
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
         const long long x = weight(s0 + lane, tell);
-        if (s0 == 0) first = x;
+        if (s0 == 0) {
+            first = x;
+            w.mine = q;
+        }
         total += warp_sum(x);
         const bool in = s0 + lane < p.n_seqs;
         longest = max(longest, in && q.tiles > 0 ? q.work(p, q.tiles - 1) : 0);
@@ -371,7 +383,6 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     __syncwarp();
     w.tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
     w.rule = kBorder;
-    w.s = -1;
     if (counted && runs <= p.shares) {
         constexpr int kTurns = (kMaxCtas + 31) / 32;
         int n[kTurns], steps = 0;
@@ -379,9 +390,9 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
         for (int k = 0; k < kTurns; ++k) {
             const int i = lane + 32 * k;
             n[k] = 0;
-            if (i < runs) {
-                w.locate(p, ct, i);
-                n[k] = max(q.steps(p, w.t), 1);
+            if (32 * k < runs) {
+                w.locate(p, ct, min(i, runs - 1));
+                if (i < runs) n[k] = max(q.steps(p, w.t), 1);
             }
             steps += n[k];
         }
@@ -406,7 +417,6 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
                 const unsigned mine = __ballot_sync(~0u, part >= 0 && part < c);
                 if (mine) {
                     const int l = __ffs(mine) - 1, parts = __shfl_sync(~0u, c, l), of = __shfl_sync(~0u, part, l);
-                    w.s = -1;
                     w.locate(p, ct, l + 32 * k);
                     const int all = q.steps(p, w.t);
                     w.s0 = (int)((long long)of * all / parts);
@@ -422,9 +432,7 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
         w.rule = kDealt;
         w.run = (int)share;
         w.runs = runs;
-        w.s = -1;
-        w.ahead = 0;
-        if (lane == 0 && w.run < runs) w.ahead = atomicAdd(p.dealt + 2 * w.tile, 1u);
+        w.begun = false;
         return;
     }
     long long used = (total + kMinShare - 1) / kMinShare;
@@ -453,7 +461,7 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
         before += __shfl_sync(~0u, incl, 31);
     }
     if (w.s < p.n_seqs) {
-        q.take(w.s & 31);
+        q.take(q, w.s & 31);
         const long long per = q.cum(p, q.tiles), in_seq = w.x0 - before;
         w.g = in_seq < (1ll << 31) && per < (1ll << 31) ? (int)((unsigned)in_seq / (unsigned)per) : (int)(in_seq / per);
         before += w.g * per;
