@@ -151,8 +151,8 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool x) {
         : "memory");
     return any != 0;
 }
-// All softmax warps.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+// HALVES: the two warps that hold a row's halves, one of each stream.
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync %0, 64;" ::"r"(4 + (threadIdx.x >> 5 & 3)) : "memory"); }
 
 // ------------------------------------------------------------------ the runs and the shares
 
@@ -573,11 +573,12 @@ __device__ unsigned long long ancestors(const Params &p, int q0, int lq, int nod
 // ------------------------------------------------------------------ the kernel
 
 // What a CTA left in its partials.  desc[0]: (1 = the piece ends its run, 2 = it does not, 0 = none) for a piece that began
-// in an earlier CTA; desc[1]: (1, s, g, tok0) for a run that begins here and does not end here.
+// in an earlier CTA; desc[1]: (1, KV head, the tile's first token among all, the tokens from there to the sequence's end)
+// for a run that begins here and does not end here.
 __device__ __forceinline__ void describe(const Params &p, const Piece &pc) {
     int4 *d = p.desc + 2 * (size_t)blockIdx.x;
     if (pc.s0 > 0) d[0] = make_int4(pc.s1 == pc.n ? 1 : 2, 0, 0, 0);
-    else if (pc.s1 < pc.n) d[1] = make_int4(1, pc.s, pc.g, pc.tok0);
+    else if (pc.s1 < pc.n) d[1] = make_int4(1, pc.g, pc.q0 + pc.tok0, pc.lq - pc.tok0);
 }
 
 // Four values of a row of out, at element `at`.
@@ -608,9 +609,9 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
     };
     float keep = 1.0f, add = 0.0f;   // HALVES: factors of this stream's and of the other's
     if constexpr (HALVES) {
-        if (have) {   // the same for all
+        if (have && rows > (warp & 3) * 32) {   // the same for both warps
             if (st == 1) ct.other[r] = make_float2(m, l);
-            soft_sync();
+            rows_sync();
             if (st == 0) {
                 const float2 x = ct.other[r];
                 const float top = l == 0.0f ? x.x : x.y == 0.0f ? m : fmaxf(m, x.x);   // of those that saw something
@@ -641,12 +642,13 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
         }
         auto val = [&](int i) { return __uint_as_float(o[i >> 4][i & 15]); };
         if constexpr (HALVES) {
-            if (have) {
-                float4 *at = box + (d & 32) / 4 * kRows + r;   // the box holds two rounds
+            if (have && rows > (warp & 3) * 32) {
+                float4 *at = box + (d & 32) / 4 * kRows + r;   // the box holds two rounds: what a round overwrites was read before the barrier of the last one
                 if (st == 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) at[(i / 4) * kRows] = make_float4(val(i), val(i + 1), val(i + 2), val(i + 3));
-                soft_sync();
+                if (d == 96) fence_proxy_async();   // the box is Q's memory again
+                rows_sync();
                 if (st == 0)
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
@@ -655,10 +657,7 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[(i + e) >> 4][(i + e) & 15] = __float_as_uint(val(i + e) * keep + y[e] * add);
                     }
-                if (d == 96) {
-                    fence_proxy_async();   // the box is Q's memory again
-                    soft_sync();
-                }
+                if (d == 96) fence_proxy_async();
             }
             if (st == 1) continue;
         }
@@ -742,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.qfull[i], 1);
-            mbar_init(&ct.qempty[i], 1);
+            mbar_init(&ct.qempty[i], HALVES && i == 1 ? 4 : 1);   // there, a warp of stream 0 each
             mbar_init(&ct.sfull[i], 1);
             for (int h = 0; h < 2; ++h) mbar_init(&ct.pready[i][h], 4);   // one arrival per warp of the stream
             mbar_init(&ct.ofull[i], 1);
@@ -1221,7 +1220,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 finish<F16, TREE, HALVES>(p, ct, *pp, end > s0, tO, smem + kOffStage + (warp - 4) * kStageBytes,
                                           reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, lim, nodes, rows);
                 tc_fence_before();
-                if (HALVES && tid == 128 && end > s0) mbar_arrive(&ct.qempty[1]);
+                if (HALVES && st == 0 && end > s0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ct.qempty[1]);
+                }
             }
             step0 += pp->s1 - s0;
             __syncwarp();
@@ -1261,14 +1263,18 @@ constexpr int kJoinTurns = (kMaxCtas + kJoinWarps - 1) / kJoinWarps;
 
 // MANY: few rows (a decode step), so a run may lie in many parts: the warps share them out and meet in shared memory.
 // Otherwise a warp takes four dimensions of all parts.
-template <bool F16, bool TREE, bool MANY>
+template <bool F16, bool MANY>
 __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_constant__ Params p, int grid) {
     wait_prior_grid();
     allow_dependent_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = p.row_tiles;
     const int4 d = p.desc[2 * (size_t)blockIdx.x + 1];
     if (d.x == 0) return;
-    int parts = 0;   // shares behind this one
+    const int in_tile = blockIdx.y * 32 + lane, st = blockIdx.y >> 2, r = in_tile & (kRows - 1);
+    const int tok = (int)(r * p.by_group >> 16), token = st * p.toks + tok;
+    const bool mine = tok < p.toks && token < d.w;
+    if (!__any_sync(~0u, mine)) return;   // the same in every warp
+    int parts = 0;   // shares behind this one that hold a part
     for (int c0 = 1;; c0 += 32) {
         const long long c = blockIdx.x + (long long)(c0 + lane) * step;
         const int kind = c < grid ? p.desc[2 * c].x : 1;
@@ -1278,12 +1284,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
             break;
         }
     }
-    Seq<TREE> q;
-    q.load(p, d.y, false);
-    const int in_tile = blockIdx.y * 32 + lane, st = blockIdx.y >> 2, r = in_tile & (kRows - 1);
-    const int tok = (int)(r * p.by_group >> 16), token = d.w + st * p.toks + tok;
-    const bool mine = tok < p.toks && token < q.lq;
-    if (!__syncthreads_or(mine)) return;
     auto slot = [&](int i) { return 2 * ((size_t)blockIdx.x + (size_t)i * step) + (i == 0 ? 1 : 0); };
     auto sums_of = [&](int i) { return p.ml[slot(i) * p.rows_cap + in_tile]; };   // a sum of 0: saw nothing
     auto part_of = [&](int i, int d4) { return p.part[(slot(i) * 32 + d4) * p.rows_cap + in_tile]; };
@@ -1351,7 +1351,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
             if (f != 0.0f) add(x, f, y);
         }
     }
-    const size_t at = (size_t)(q.q0 + token) * p.n_heads + d.z * p.group + (r - tok * p.group);
+    const size_t at = (size_t)(d.z + token) * p.n_heads + d.y * p.group + (r - tok * p.group);
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     store4<F16>(p, at * 128 + 4 * d4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     if (d4 == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
@@ -1392,8 +1392,8 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bo
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return check_cuda(many ? cudaLaunchKernelEx(&cfg, combine_kernel<F16, TREE, true>, p, grid)
-                           : cudaLaunchKernelEx(&cfg, combine_kernel<F16, TREE, false>, p, grid),
+    return check_cuda(many ? cudaLaunchKernelEx(&cfg, combine_kernel<F16, true>, p, grid)
+                           : cudaLaunchKernelEx(&cfg, combine_kernel<F16, false>, p, grid),
                       "combine_kernel launch");
 }
 
