@@ -77,12 +77,12 @@ PageTable page_table(const int32_t *table, int64_t stride, int max_pages, int n_
 }
 
 size_t pages_ws_bytes(int n_rows, int n_pages) {
-    return 256 + ((size_t)2 * n_rows + (size_t)n_pages + 1 + 63) / 64 * 256;
+    return 256 + ((size_t)n_rows + (size_t)n_pages + 1 + 63) / 64 * 256;
 }
 PagesWs pages_ws(void *ws, int n_rows, int n_pages) {
     PagesWs w{};
-    w.need = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + 256);
-    w.list = w.need + 2 * (size_t)n_rows;
+    w.upto = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + 256);
+    w.list = w.upto + n_rows;
     w.live = w.list + n_pages;
     return w;
 }

@@ -4,9 +4,9 @@
 // What a page's entry in a table says is in qsa.h.  The bookkeeping reads and writes a few KB, so its time is a launch
 // and a chain of loads; what there is to choose is the number of steps in that chain.
 //  - fork, release: one CTA per row, references by atomics (integers: any order gives the same).
-//  - reserve: one CTA.  A warp counts what a row lacks; shared last pages are settled by rank among the rows that write
+//  - reserve: one CTA.  A thread, a warp or the whole CTA counts what a row lacks, by the entries it looks at; shared last pages are settled by rank among the rows that write
 //    (a row copies when more references than rows before it remain); one scan gives each row its part of the ascending list of
-//    free pages, and a warp fills the row's entries from it.  The list is written no further than it is needed.
+//    free pages, from which its entries are filled.  The list is written no further than it is needed.
 //  - compact: one CTA lists the free pages below the number of live ones and the live pages behind it, both in order,
 //    and pairs them; a second grid rewrites the table.
 //  - append: one CTA per (page touched, KV head): K rows as they are, V through shared memory into its dimension-major block.
@@ -21,6 +21,9 @@ namespace {
 
 constexpr int kRowThreads = 256;    // fork, release, append
 constexpr int kOneThreads = 1024;   // reserve, compact
+constexpr int kBatch = 4;           // table entries of a thread under way
+constexpr int kFew = 2;             // reserve: entries of a row that one thread looks at; a warp beyond,
+constexpr int kMany = 512;          // and the whole CTA beyond this
 
 __device__ __forceinline__ void raise(uint32_t *flags, uint32_t bit) {
     if (flags) atomicOr(flags, bit);
@@ -34,11 +37,10 @@ __device__ __forceinline__ int row_tokens(int n, int max_pages, uint32_t *flags)
     }
     return n;
 }
-__device__ __forceinline__ void give_back(int32_t *refs, int page, uint32_t *flags) {
-    if (atomicSub(refs + page, 1) <= 0) {   // nothing refers to it: as before
-        atomicAdd(refs + page, 1);
-        raise(flags, QSA_FLAG_BAD_ID);
-    }
+// A page that nothing referred to when a reference was given back: as before.
+__device__ __forceinline__ void restore(int32_t *refs, int page, uint32_t *flags) {
+    atomicAdd(refs + page, 1);
+    raise(flags, QSA_FLAG_BAD_ID);
 }
 
 __global__ void __launch_bounds__(kRowThreads) pages_fork_kernel(PageTable t, int32_t *n_tokens, int32_t *refs,
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(kRowThreads) pages_fork_kernel(PageTable t, in
             page = -1;
         }
         if (page >= 0) atomicAdd(refs + page, 1);
-        if (had >= 0 && had < t.n_pages) give_back(refs, had, t.flags);
+        if (had >= 0 && had < t.n_pages && atomicSub(refs + had, 1) <= 0) restore(refs, had, t.flags);
         if (had != page) b[j] = page;
     }
     __syncthreads();   // every thread has read n_tokens[to]
@@ -81,15 +83,26 @@ __global__ void __launch_bounds__(kRowThreads) pages_release_kernel(PageTable t,
     const int row = blockIdx.x, tid = threadIdx.x, left = keep[row], n = n_tokens[row];
     if (left < 0) return;
     int32_t *a = t.table + (size_t)row * t.stride;
-    for (int j = (int)(((unsigned)left + 63u) >> 6) + tid; j < t.max_pages; j += kRowThreads) {
-        const int page = a[j];
-        if (page == -1) continue;
-        if (page < 0 || page >= t.n_pages) {
-            raise(t.flags, QSA_FLAG_BAD_ID);
-            continue;
+    for (int j0 = (int)(((unsigned)left + 63u) >> 6) + tid; j0 < t.max_pages; j0 += kBatch * kRowThreads) {
+        int page[kBatch], held[kBatch];   // loads and atomics of a batch under way together
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = j0 + i * kRowThreads;
+            page[i] = j < t.max_pages ? a[j] : -1;
         }
-        give_back(refs, page, t.flags);
-        a[j] = -1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            held[i] = page[i] >= 0 && page[i] < t.n_pages ? atomicSub(refs + page[i], 1) : 1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (page[i] == -1) continue;
+            if (page[i] < 0 || page[i] >= t.n_pages) {
+                raise(t.flags, QSA_FLAG_BAD_ID);
+                continue;
+            }
+            if (held[i] <= 0) restore(refs, page[i], t.flags);
+            a[j0 + i * kRowThreads] = -1;
+        }
     }
     __syncthreads();   // keep may be n_tokens: every thread has read it
     if (tid == 0 && left < n) n_tokens[row] = left;
@@ -120,64 +133,116 @@ __device__ __forceinline__ unsigned long long scan_all(unsigned long long v, uns
 // What a row of reserve does with its last page.
 enum : uint8_t { kWhole = 0, kCopies = 1, kKeeps = 2, kPast = 3 };
 
+// The entries that a row's new tokens need, [b0, b1), and whether it has any.
+struct Wants {
+    int n, more, b0, b1;
+    bool past;
+};
+__device__ __forceinline__ Wants wants_of(const PageTable &t, const int32_t *n_tokens, const int32_t *add, int row, bool tell) {
+    Wants w;
+    w.n = n_tokens[row];
+    w.more = add[row];
+    if (w.more < 0) {
+        if (tell) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+        w.more = 0;
+    }
+    w.past = w.n < 0 || (long long)w.n + w.more > 64ll * t.max_pages;
+    w.b0 = w.b1 = 0;
+    if (!w.past && w.more > 0) {
+        w.b0 = (w.n + 63) >> 6;
+        w.b1 = (int)(((long long)w.n + w.more + 63) >> 6);
+    }
+    return w;
+}
+__device__ __forceinline__ bool is_page(const PageTable &t, int p) { return p >= 0 && p < t.n_pages; }
+
 __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t, const int32_t *n_tokens, int32_t *refs,
                                                                     const int32_t *add, int32_t *new_tokens,
                                                                     int32_t *copy_src, int32_t *copy_dst, PagesWs ws) {
     __shared__ int32_t last[QSA_MAX_TABLE_ROWS];   // the page a row is about to write into, or -1
+    __shared__ int32_t needs[QSA_MAX_TABLE_ROWS];  // pages it asks for
     __shared__ uint8_t what[QSA_MAX_TABLE_ROWS];
     __shared__ unsigned long long sums[kOneThreads / 32];
     __shared__ int counts[kOneThreads / 32];
     wait_prior_grid();
     allow_dependent_launch();
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const long long most = 64ll * t.max_pages;
-    // what each row lacks
-    for (int row = wid; row < t.n_rows; row += kOneThreads / 32) {
-        const int n = n_tokens[row];
-        int more = add[row];
-        if (more < 0) {
-            if (lane == 0) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
-            more = 0;
-        }
-        const bool past = n < 0 || (long long)n + more > most;
+    int held[4];   // references of the pool's first pages, on their way meanwhile
+#pragma unroll
+    for (int e = 0; e < 4; ++e) held[e] = tid * 4 + e < t.n_pages ? refs[tid * 4 + e] : 1;
+    // what each row lacks: entries that are no page (a bad one counts as none)
+    bool any_warp = false, any_all = false;
+    for (int row = tid; row < t.n_rows; row += kOneThreads) {
+        const Wants w = wants_of(t, n_tokens, add, row, true);
+        const int32_t *a = t.table + (size_t)row * t.stride;
         int lacks = 0, page = -1;
-        if (!past && more > 0) {
+        if (w.past) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+        if (w.b1 - w.b0 <= kFew) {
+            int p[kFew];
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) p[i] = w.b0 + i < w.b1 ? a[w.b0 + i] : 0;
+            if (w.b1 > 0 && (w.n & 63)) page = a[w.n >> 6];
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                lacks += w.b0 + i < w.b1 && !is_page(t, p[i]);
+                if (p[i] < -1 || p[i] >= t.n_pages) raise(t.flags, QSA_FLAG_BAD_ID);
+            }
+        } else {
+            if (w.n & 63) page = a[w.n >> 6];
+            any_warp = any_warp || w.b1 - w.b0 <= kMany;
+            any_all = any_all || w.b1 - w.b0 > kMany;
+        }
+        if (w.b1 > 0 && (w.n & 63) && !is_page(t, page)) {   // a page that the tokens should have lain in
+            raise(t.flags, QSA_FLAG_BAD_ID);
+            page = -1;
+            ++lacks;
+        }
+        last[row] = page;
+        what[row] = w.past ? kPast : kWhole;
+        needs[row] = lacks;
+    }
+    if (__syncthreads_or(any_warp))
+        for (int row = wid; row < t.n_rows; row += kOneThreads / 32) {
+            const Wants w = wants_of(t, n_tokens, add, row, false);
+            if (w.b1 - w.b0 <= kFew || w.b1 - w.b0 > kMany) continue;
             const int32_t *a = t.table + (size_t)row * t.stride;
-            const int b0 = (n + 63) >> 6, b1 = (int)(((long long)n + more + 63) >> 6);
-            for (int b = b0 + lane; b < b1; b += 32) {
+            int lacks = 0;
+#pragma unroll 4
+            for (int b = w.b0 + lane; b < w.b1; b += 32) {
                 const int p = a[b];
-                if (p >= t.n_pages || p < -1) raise(t.flags, QSA_FLAG_BAD_ID);
-                lacks += p < 0 || p >= t.n_pages;
+                lacks += !is_page(t, p);
+                if (p < -1 || p >= t.n_pages) raise(t.flags, QSA_FLAG_BAD_ID);
             }
             lacks = __reduce_add_sync(~0u, lacks);
-            if (n & 63) {
-                page = a[n >> 6];
-                if (page < 0 || page >= t.n_pages) {   // a page that the tokens should have lain in
-                    if (lane == 0) raise(t.flags, QSA_FLAG_BAD_ID);
-                    page = -1;
-                    ++lacks;
-                }
+            if (lane == 0) needs[row] += lacks;
+        }
+    if (__syncthreads_or(any_all))
+        for (int row = 0; row < t.n_rows; ++row) {
+            const Wants w = wants_of(t, n_tokens, add, row, false);
+            if (w.b1 - w.b0 <= kMany) continue;
+            const int32_t *a = t.table + (size_t)row * t.stride;
+            int lacks = 0;
+#pragma unroll 4
+            for (int b = w.b0 + tid; b < w.b1; b += kOneThreads) {
+                const int p = a[b];
+                lacks += !is_page(t, p);
+                if (p < -1 || p >= t.n_pages) raise(t.flags, QSA_FLAG_BAD_ID);
             }
+            lacks = __reduce_add_sync(~0u, lacks);
+            if (lane == 0) atomicAdd(&needs[row], lacks);
         }
-        if (lane == 0) {
-            if (past) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
-            last[row] = page;
-            what[row] = past ? kPast : kWhole;
-            ws.need[row] = lacks;
-        }
-    }
     __syncthreads();
     // rows that share their last page: the k-th of them to write copies while more than k references remain
     for (int row = tid; row < t.n_rows; row += kOneThreads) {
         const int page = last[row];
         if (page < 0) continue;
-        const int held = refs[page];
-        if (held <= 1) continue;
+        const int all = refs[page];
+        if (all <= 1) continue;
         int earlier = 0;
         for (int j = 0; j < row; ++j) earlier += last[j] == page;
-        const bool copies = held - earlier > 1;
+        const bool copies = all - earlier > 1;
         what[row] = copies ? kCopies : kKeeps;
-        if (copies) ws.need[row] += 1;
+        if (copies) needs[row] += 1;
     }
     __syncthreads();
     // pages that a row and those before it ask for
@@ -185,10 +250,10 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
     for (int r0 = 0; r0 < t.n_rows; r0 += kOneThreads) {
         const int row = r0 + tid;
         unsigned long long total;
-        const unsigned long long incl = scan_all(row < t.n_rows ? (unsigned long long)ws.need[row] : 0ull, sums, total);
+        const unsigned long long incl = scan_all(row < t.n_rows ? (unsigned long long)needs[row] : 0ull, sums, total);
         if (row < t.n_rows) {   // more than a pool holds is more than is free
             const unsigned long long upto = asked + incl;
-            ws.need[t.n_rows + row] = (int)(upto < (1ull << 30) ? upto : (1ull << 30));
+            ws.upto[row] = (int)(upto < (1ull << 30) ? upto : (1ull << 30));
         }
         asked += total;
     }
@@ -196,14 +261,14 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
     // the first free pages in order, as many as are asked for
     int free_pages = 0;
     for (int p0 = 0; p0 < t.n_pages && free_pages < want; p0 += 4 * kOneThreads) {
-        int mine[4], k = 0;
+        int k = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int p = p0 + tid * 4 + e;
-            mine[e] = p < t.n_pages ? refs[p] : 1;
+            if (p0 > 0) held[e] = p < t.n_pages ? refs[p] : 1;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) k += mine[e] == 0;
+        for (int e = 0; e < 4; ++e) k += held[e] == 0;
         const int incl = warp_incl_scan(k);
         __syncthreads();
         if (lane == 31) counts[wid] = incl;
@@ -216,37 +281,62 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (mine[e] == 0) {
+            if (held[e] == 0) {
                 if (at < want) ws.list[at] = p0 + tid * 4 + e;
                 ++at;
             }
     }
     __syncthreads();   // the list and the rows' needs lie in global memory, read by other threads of this CTA
-    for (int row = wid; row < t.n_rows; row += kOneThreads / 32) {
-        const int n = n_tokens[row], more = max(add[row], 0), need = ws.need[row], upto = ws.need[t.n_rows + row];
+    // the page under a row's last tokens comes first, then the others; a row's first page for them
+    auto served = [&](int row, int &need) {
+        need = needs[row];
         const uint8_t does = what[row];
-        const bool served = does != kPast && (upto <= free_pages || (need == 0 && does != kKeeps));
-        int from = -1, to = -1;
-        if (served && need > 0) {
+        return does != kPast && (ws.upto[row] <= free_pages || (need == 0 && does != kKeeps));
+    };
+    auto first_of = [&](int row, int need, const Wants &w) {
+        return ws.upto[row] - need + ((w.n & 63) && (what[row] == kCopies || last[row] < 0) ? 1 : 0);
+    };
+    for (int row = tid; row < t.n_rows; row += kOneThreads) {
+        const Wants w = wants_of(t, n_tokens, add, row, false);
+        int need, from = -1, to = -1;
+        const bool ok = served(row, need);
+        if (ok && need > 0) {
             int32_t *a = t.table + (size_t)row * t.stride;
-            int at = upto - need;
-            int b = (n + 63) >> 6;
-            const int b1 = (int)(((long long)n + more + 63) >> 6);
-            if ((n & 63) && (does == kCopies || last[row] < 0)) {   // the page under the last tokens comes first
-                to = ws.list[at];
-                if (does == kCopies) from = last[row];
-                if (lane == 0) {
-                    a[n >> 6] = to;
-                    refs[to] = 1;
-                    if (from >= 0) atomicSub(refs + from, 1);
+            int at = first_of(row, need, w);
+            if (at > ws.upto[row] - need) {
+                to = ws.list[at - 1];
+                a[w.n >> 6] = to;
+                refs[to] = 1;
+                if (what[row] == kCopies) {
+                    from = last[row];
+                    atomicSub(refs + from, 1);
+                } else {
+                    to = -1;   // nothing to copy
                 }
-                if (from < 0) to = -1;   // nothing to copy
-                ++at;
             }
-            for (; b < b1; b += 32) {
-                const bool in = b + lane < b1;
-                const int p = in ? a[b + lane] : 0;
-                const bool lacks = in && (p < 0 || p >= t.n_pages);
+            if (w.b1 - w.b0 <= kFew)
+#pragma unroll
+                for (int i = 0; i < kFew; ++i)
+                    if (w.b0 + i < w.b1 && !is_page(t, a[w.b0 + i])) {
+                        const int page = ws.list[at++];
+                        a[w.b0 + i] = page;
+                        refs[page] = 1;
+                    }
+        }
+        if (!ok && what[row] != kPast) raise(t.flags, QSA_FLAG_NO_PAGES);
+        new_tokens[row] = ok ? w.n + w.more : w.n;
+        copy_src[row] = from;
+        copy_dst[row] = to;
+    }
+    if (__syncthreads_or(any_warp))
+        for (int row = wid; row < t.n_rows; row += kOneThreads / 32) {
+            const Wants w = wants_of(t, n_tokens, add, row, false);
+            int need;
+            if (w.b1 - w.b0 <= kFew || w.b1 - w.b0 > kMany || !served(row, need) || need == 0) continue;
+            int32_t *a = t.table + (size_t)row * t.stride;
+            int at = first_of(row, need, w);
+            for (int b = w.b0; b < w.b1; b += 32) {
+                const bool lacks = b + lane < w.b1 && !is_page(t, a[b + lane]);
                 const unsigned who = __ballot_sync(~0u, lacks);
                 if (lacks) {
                     const int page = ws.list[at + __popc(who & ((1u << lane) - 1u))];
@@ -256,13 +346,25 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
                 at += __popc(who);
             }
         }
-        if (lane == 0) {
-            if (!served && does != kPast) raise(t.flags, QSA_FLAG_NO_PAGES);
-            new_tokens[row] = served ? n + more : n;
-            copy_src[row] = from;
-            copy_dst[row] = to;
+    if (__syncthreads_or(any_all))
+        for (int row = 0; row < t.n_rows; ++row) {
+            const Wants w = wants_of(t, n_tokens, add, row, false);
+            int need;
+            if (w.b1 - w.b0 <= kMany || !served(row, need) || need == 0) continue;
+            int32_t *a = t.table + (size_t)row * t.stride;
+            int at = first_of(row, need, w);
+            for (int b = w.b0; b < w.b1; b += kOneThreads) {
+                const bool lacks = b + tid < w.b1 && !is_page(t, a[b + tid]);
+                unsigned long long total;
+                const int rank = (int)scan_all(lacks ? 1ull : 0ull, sums, total) - 1;
+                if (lacks) {
+                    const int page = ws.list[at + rank];
+                    a[b + tid] = page;
+                    refs[page] = 1;
+                }
+                at += (int)total;
+            }
         }
-    }
 }
 
 __global__ void __launch_bounds__(kOneThreads) pages_compact_kernel(const int32_t *refs, int n_pages, int32_t *refs_out,
@@ -381,17 +483,19 @@ __device__ __forceinline__ int pages_of(const Span &s) { return s.hi > s.lo ? (i
 __global__ void __launch_bounds__(kRowThreads) pages_append_kernel(PageTable t, PagesAppendArgs a) {
     __shared__ BlockScratch sm;
     __shared__ Unit unit;
-    __shared__ __align__(16) uint16_t tile[64][136];   // V rows; 272 bytes a row: 16-byte aligned
+    // V rows of a page, 16 units of 16 bytes each: unit u of token i lies at u ^ (i / 8), so that neither the rows coming in
+    // nor eight tokens of a dimension going out meet a bank twice
+    __shared__ uint4 tile[64][16];
     __shared__ int source[64];
     wait_prior_grid();
     allow_dependent_launch();
-    const int tid = threadIdx.x, g = blockIdx.y;
+    const int tid = threadIdx.x;
     if (tid == 0) unit.row = -1;
     __syncthreads();
     int before = 0;
     for (int r0 = 0; r0 < t.n_rows && before <= (int)blockIdx.x; r0 += kRowThreads) {
         const int row = r0 + tid;
-        const int np = row < t.n_rows ? pages_of(span_of(t, a, row, blockIdx.x == 0 && g == 0)) : 0;
+        const int np = row < t.n_rows ? pages_of(span_of(t, a, row, blockIdx.x == 0 && blockIdx.y == 0)) : 0;
         int total;
         const int at = before + block_excl_scan<kRowThreads>(np, sm, total);
         if ((int)blockIdx.x >= at && (int)blockIdx.x < at + np) {
@@ -417,54 +521,62 @@ __global__ void __launch_bounds__(kRowThreads) pages_append_kernel(PageTable t, 
             const int e = s.e0 + (int)(pos - s.first);
             r = a.rows ? a.rows[e] : e;
             if (r < 0 || r >= a.n_source) {
-                if (r != -1 && g == 0) raise(t.flags, QSA_FLAG_BAD_ID);
+                if (r != -1 && blockIdx.y == 0) raise(t.flags, QSA_FLAG_BAD_ID);
                 r = -1;
             }
         }
         source[tid] = r;
     }
     __syncthreads();
-    const uint16_t *k = static_cast<const uint16_t *>(a.k.p) + (size_t)g * a.k.head;
-    const uint16_t *v = static_cast<const uint16_t *>(a.v.p) + (size_t)g * a.v.head;
-    uint16_t *kc = static_cast<uint16_t *>(a.kcache) + ((size_t)g * t.n_pages + page) * (64 * 128);
-    uint16_t *vc = static_cast<uint16_t *>(a.vcache_t) + ((size_t)g * t.n_pages + page) * (64 * 128);
-    const int c = tid & 15;
-    uint4 kx[4], vx[4];
+    const int u = tid & 15, c = tid & 7;
+    uint32_t there = 0u;   // of the eight tokens that this thread writes
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = source[(tid >> 4) + 16 * i];
-        kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= 0) {
-            kx[i] = *reinterpret_cast<const uint4 *>(k + (int64_t)r * a.k.token + 8 * c);
-            vx[i] = *reinterpret_cast<const uint4 *>(v + (int64_t)r * a.v.token + 8 * c);
+    for (int j = 0; j < 8; ++j) there |= (source[8 * c + j] >= 0 ? 1u : 0u) << j;
+    for (int g = blockIdx.y; g < a.n_kv_heads; g += gridDim.y) {
+        const uint16_t *k = static_cast<const uint16_t *>(a.k.p) + (size_t)g * a.k.head;
+        const uint16_t *v = static_cast<const uint16_t *>(a.v.p) + (size_t)g * a.v.head;
+        uint16_t *kc = static_cast<uint16_t *>(a.kcache) + ((size_t)g * t.n_pages + page) * (64 * 128);
+        uint16_t *vc = static_cast<uint16_t *>(a.vcache_t) + ((size_t)g * t.n_pages + page) * (64 * 128);
+        uint4 kx[4], vx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = source[(tid >> 4) + 16 * i];
+            kx[i] = vx[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r >= 0) {
+                kx[i] = *reinterpret_cast<const uint4 *>(k + (int64_t)r * a.k.token + 8 * u);
+                vx[i] = *reinterpret_cast<const uint4 *>(v + (int64_t)r * a.v.token + 8 * u);
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = (tid >> 4) + 16 * i;
-        if (source[at] >= 0) *reinterpret_cast<uint4 *>(kc + at * 128 + 8 * c) = kx[i];
-        *reinterpret_cast<uint4 *>(&tile[at][8 * c]) = vx[i];
-    }
-    __syncthreads();
-    // dimension d, eight tokens a thread; 8 lanes write a dimension's 128 bytes
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = (tid >> 3) + 32 * i, t0 = (tid & 7) * 8;
-        uint16_t x[8];
-        bool all = true;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = tile[t0 + j][d];
-            all = all && source[t0 + j] >= 0;
+        for (int i = 0; i < 4; ++i) {
+            const int at = (tid >> 4) + 16 * i;
+            if (source[at] >= 0) *reinterpret_cast<uint4 *>(kc + at * 128 + 8 * u) = kx[i];
+            tile[at][u ^ (at >> 3)] = vx[i];
         }
-        if (all) {
-            *reinterpret_cast<uint4 *>(vc + d * 64 + t0) =
-                make_uint4(x[0] | (uint32_t)x[1] << 16, x[2] | (uint32_t)x[3] << 16, x[4] | (uint32_t)x[5] << 16,
-                           x[6] | (uint32_t)x[7] << 16);
-        } else {
+        __syncthreads();
+        // two dimensions and eight tokens a turn; 8 lanes write a dimension's 128 bytes
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int pair = (tid >> 3) + 32 * i;   // dimensions 2 pair and 2 pair + 1
+            uint32_t x[8];
+#pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (source[t0 + j] >= 0) vc[d * 64 + t0 + j] = x[j];
+                x[j] = reinterpret_cast<const uint32_t *>(&tile[8 * c + j][(pair >> 2) ^ c])[pair & 3];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint16_t *to = vc + (2 * pair + h) * 64 + 8 * c;
+                const uint32_t pick = h ? 0x7632u : 0x5410u;   // a half of two words
+                if (there == 0xFFu) {
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(__byte_perm(x[0], x[1], pick), __byte_perm(x[2], x[3], pick),
+                                                                __byte_perm(x[4], x[5], pick), __byte_perm(x[6], x[7], pick));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (there >> j & 1u) to[j] = (uint16_t)(h ? x[j] >> 16 : x[j]);
+                }
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -498,7 +610,9 @@ qsa_status launch_pages_append(const PageTable &t, const PagesAppendArgs &a, cud
     long long units = a.n / 64 + 2ll * t.n_rows;
     if (units > a.n) units = a.n;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)units, (unsigned)a.n_kv_heads);
+    // a CTA looks its page up once for all heads, unless the GPU would stay empty
+    const long long spread = 8ll * num_sms() / units;
+    cfg.gridDim = dim3((unsigned)units, (unsigned)(spread < 1 ? 1 : spread < a.n_kv_heads ? spread : a.n_kv_heads));
     cfg.blockDim = dim3(kRowThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr{};

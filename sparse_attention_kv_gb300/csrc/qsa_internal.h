@@ -230,7 +230,7 @@ struct PageTable {
 };
 // Workspace of reserve and compact, in 32-bit words behind the first 256 bytes.
 struct PagesWs {
-    int32_t *need;    // [2 n_rows] reserve: pages a row asks for; those that it and the rows before it ask for
+    int32_t *upto;    // [n_rows]   reserve: pages that a row and those before it ask for
     int32_t *list;    // [n_pages]  reserve: free pages in order; compact: where a page goes
     int32_t *live;    // [1]        compact: number of live pages
 };
