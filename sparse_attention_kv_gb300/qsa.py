@@ -631,52 +631,78 @@ def alloc_pages(n_rows: int, max_pages: int, n_pages: int, n_kv_heads: int, dtyp
             torch.zeros(n_rows, dtype=torch.int32, device=dev), torch.zeros(n_pages, dtype=torch.int32, device=dev))
 
 
-def _i32(t: torch.Tensor, name: str, n: int | None = None) -> int:
-    """The entries of a contiguous int32 tensor of one dimension (n of them, when given)."""
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous int32 tensor [{'n' if n is None else n}]")
-    return t.shape[0]
+_INT = torch.int32
 
 
-def _table(table: torch.Tensor) -> tuple[int, int, int]:
+def _elsewhere(name: str, t: torch.Tensor, dev: int) -> ValueError:
+    return ValueError(f"{name} must be a CUDA tensor on the current device {dev} (it is on {t.device})")
+
+
+def _vectors(n: int, dev: int, *named) -> None:
+    """Each (name, tensor) must be a contiguous int32 tensor [n] on the current device."""
+    size = (n,)
+    for name, t in named:
+        if t.dtype is not _INT or t.shape != size or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{n}]")
+        if t.get_device() != dev:
+            raise _elsewhere(name, t, dev)
+
+
+def _length(name: str, t: torch.Tensor, dev: int) -> int:
+    """The entries of a contiguous int32 tensor [n] on the current device."""
+    n = t.numel()
+    _vectors(n, dev, (name, t))
+    return n
+
+
+def _table(table: torch.Tensor, dev: int, name: str = "table") -> tuple[int, int, int]:
     """(rows, entries of a row, row stride) of a table of pages."""
-    shape = table.shape
-    if table.dtype != torch.int32 or len(shape) != 2 or (shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("table must be an int32 tensor [n_rows, max_pages] with unit inner stride")
+    shape, strides = table.shape, table.stride()
+    if table.dtype is not _INT or len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be an int32 tensor [n_rows, max_pages] with unit inner stride")
+    if table.get_device() != dev:
+        raise _elsewhere(name, table, dev)
+    rows, width = shape
     # a single row's stride is never used and may be anything in torch
-    return shape[0], shape[1], table.stride(0) if shape[0] > 1 else shape[1]
+    return rows, width, strides[0] if rows > 1 else width
+
+
+def _workspace(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev:
+        raise _elsewhere("ws", ws, dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def pages_fork(table: torch.Tensor, n_tokens: torch.Tensor, refs: torch.Tensor, src: torch.Tensor, dst: torch.Tensor,
                ws: torch.Tensor | None = None, stream=None) -> None:
     """Rows dst[i] of table [n_rows, max_pages] become copies of rows src[i], sharing their pages
     (n_tokens [n_rows], refs [n_pages], src and dst [n]; all int32, changed in place)."""
-    lib = load()
-    rows, width, stride = _table(table)
-    _i32(n_tokens, "n_tokens", rows)
-    pages, n = _i32(refs, "refs"), _i32(src, "src")
-    _i32(dst, "dst", n)
-    on = _stream_of(stream, torch.cuda.current_device(), table=table, n_tokens=n_tokens, refs=refs, src=src, dst=dst, ws=ws)
-    if n == 0:
-        return
-    wp, wn = _ws_args(ws)
-    _check("qsa_pages_fork", lib.qsa_pages_fork(table.data_ptr(), stride, width, n_tokens.data_ptr(), rows, refs.data_ptr(),
-                                                pages, src.data_ptr(), dst.data_ptr(), n, wp, wn, on))
+    lib, dev = load(), torch.cuda.current_device()
+    rows, width, stride = _table(table, dev)
+    pages, n = _length("refs", refs, dev), src.numel()
+    _vectors(rows, dev, ("n_tokens", n_tokens))
+    _vectors(n, dev, ("src", src), ("dst", dst))
+    wp, wn = _workspace(ws, dev)
+    if n:
+        _check("qsa_pages_fork", lib.qsa_pages_fork(
+            table.data_ptr(), stride, width, n_tokens.data_ptr(), rows, refs.data_ptr(), pages, src.data_ptr(),
+            dst.data_ptr(), n, wp, wn, _current_stream(dev) if stream is None else _stream(stream)))
 
 
 def pages_release(table: torch.Tensor, n_tokens: torch.Tensor, refs: torch.Tensor, keep: torch.Tensor,
                   ws: torch.Tensor | None = None, stream=None) -> None:
     """Row s keeps the pages of its first keep[s] tokens (0: none; negative: the row stays as it is)
     and gives the others back; keep [n_rows] int32 may be n_tokens itself."""
-    lib = load()
-    rows, width, stride = _table(table)
-    _i32(n_tokens, "n_tokens", rows)
-    _i32(keep, "keep", rows)
-    pages = _i32(refs, "refs")
-    on = _stream_of(stream, torch.cuda.current_device(), table=table, n_tokens=n_tokens, refs=refs, keep=keep, ws=ws)
-    wp, wn = _ws_args(ws)
-    _check("qsa_pages_release", lib.qsa_pages_release(table.data_ptr(), stride, width, n_tokens.data_ptr(), rows,
-                                                      refs.data_ptr(), pages, keep.data_ptr(), wp, wn, on))
+    lib, dev = load(), torch.cuda.current_device()
+    rows, width, stride = _table(table, dev)
+    pages = _length("refs", refs, dev)
+    _vectors(rows, dev, ("n_tokens", n_tokens), ("keep", keep))
+    wp, wn = _workspace(ws, dev)
+    _check("qsa_pages_release", lib.qsa_pages_release(
+        table.data_ptr(), stride, width, n_tokens.data_ptr(), rows, refs.data_ptr(), pages, keep.data_ptr(), wp, wn,
+        _current_stream(dev) if stream is None else _stream(stream)))
 
 
 def pages_reserve(table: torch.Tensor, n_tokens: torch.Tensor, refs: torch.Tensor, add: torch.Tensor,
@@ -686,18 +712,16 @@ def pages_reserve(table: torch.Tensor, n_tokens: torch.Tensor, refs: torch.Tenso
     shared last page is replaced by one of the row's own (copy_src[s] -> copy_dst[s], for pages_copy;
     -1 where there is none).  new_tokens[s] = n_tokens[s] + add[s], or n_tokens[s] where pages ran
     out (FLAG_NO_PAGES); every array [n_rows] int32."""
-    lib = load()
-    rows, width, stride = _table(table)
-    for t, name in ((n_tokens, "n_tokens"), (add, "add"), (new_tokens, "new_tokens"), (copy_src, "copy_src"),
-                    (copy_dst, "copy_dst")):
-        _i32(t, name, rows)
-    pages = _i32(refs, "refs")
-    on = _stream_of(stream, torch.cuda.current_device(), table=table, n_tokens=n_tokens, refs=refs, add=add,
-                    new_tokens=new_tokens, copy_src=copy_src, copy_dst=copy_dst, ws=ws)
-    wp, wn = _ws_args(ws)
+    lib, dev = load(), torch.cuda.current_device()
+    rows, width, stride = _table(table, dev)
+    pages = _length("refs", refs, dev)
+    _vectors(rows, dev, ("n_tokens", n_tokens), ("add", add), ("new_tokens", new_tokens), ("copy_src", copy_src),
+             ("copy_dst", copy_dst))
+    wp, wn = _workspace(ws, dev)
     _check("qsa_pages_reserve", lib.qsa_pages_reserve(
         table.data_ptr(), stride, width, n_tokens.data_ptr(), rows, refs.data_ptr(), pages, add.data_ptr(),
-        new_tokens.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), wp, wn, on))
+        new_tokens.data_ptr(), copy_src.data_ptr(), copy_dst.data_ptr(), wp, wn,
+        _current_stream(dev) if stream is None else _stream(stream)))
 
 
 def pages_compact(table: torch.Tensor, refs: torch.Tensor, table_out: torch.Tensor, refs_out: torch.Tensor,
@@ -705,61 +729,64 @@ def pages_compact(table: torch.Tensor, refs: torch.Tensor, table_out: torch.Tens
     """The live pages move to the front of the pool: table_out and refs_out (may be table and refs
     themselves) name the new pages, copy_src -> copy_dst [n_pages // 2] int32 the moves (-1 behind
     them), for pages_copy."""
-    lib = load()
-    rows, width, stride = _table(table)
-    if _table(table_out) != (rows, width, stride):
+    lib, dev = load(), torch.cuda.current_device()
+    rows, width, stride = _table(table, dev)
+    if _table(table_out, dev, "table_out") != (rows, width, stride):
         raise ValueError("table_out must have table's shape and strides")
-    pages = _i32(refs, "refs")
-    _i32(refs_out, "refs_out", pages)
-    _i32(copy_src, "copy_src", pages // 2)
-    _i32(copy_dst, "copy_dst", pages // 2)
-    on = _stream_of(stream, torch.cuda.current_device(), table=table, refs=refs, table_out=table_out, refs_out=refs_out,
-                    copy_src=copy_src, copy_dst=copy_dst, ws=ws)
-    wp, wn = _ws_args(ws)
+    pages = _length("refs", refs, dev)
+    _vectors(pages, dev, ("refs_out", refs_out))
+    _vectors(pages // 2, dev, ("copy_src", copy_src), ("copy_dst", copy_dst))
+    wp, wn = _workspace(ws, dev)
     _check("qsa_pages_compact", lib.qsa_pages_compact(
         table.data_ptr(), stride, width, rows, refs.data_ptr(), pages, table_out.data_ptr(), refs_out.data_ptr(),
-        copy_src.data_ptr() or None, copy_dst.data_ptr() or None, wp, wn, on))
+        copy_src.data_ptr() or None, copy_dst.data_ptr() or None, wp, wn,
+        _current_stream(dev) if stream is None else _stream(stream)))
 
 
 def pages_copy(arrays, copy_src: torch.Tensor, copy_dst: torch.Tensor, ws: torch.Tensor | None = None, stream=None) -> None:
     """x[row, copy_dst[i]] = x[row, copy_src[i]] for each pool x of arrays (at most 8), in one launch; shapes as for
     gather_blocks, and a 16-bit K cache [Hkv, 64 n_pages, 128] as kcache.view(Hkv, -1, 64, 128).
     Entries of -1 are skipped; no page of copy_dst may be in copy_src or twice in copy_dst."""
-    lib = load()
-    n = _i32(copy_src, "copy_src")
-    _i32(copy_dst, "copy_dst", n)
+    lib, dev = load(), torch.cuda.current_device()
+    n = _length("copy_src", copy_src, dev)
+    _vectors(n, dev, ("copy_dst", copy_dst))
     if not 1 <= len(arrays) <= GATHER_MAX_ARRAYS:
         raise ValueError(f"1 to {GATHER_MAX_ARRAYS} arrays (got {len(arrays)})")
-    dev = torch.cuda.current_device()
-    on = _stream_of(stream, dev, copy_src=copy_src, copy_dst=copy_dst, ws=ws)
     for t in arrays:
         if t.get_device() != dev:
             raise ValueError(f"arrays must lie on the current device {dev} (one is on {t.device})")
+    wp, wn = _workspace(ws, dev)
     packed = b"".join([_block_array(t, t) for t in arrays])
-    if n == 0:
-        return
-    wp, wn = _ws_args(ws)
-    _check("qsa_pages_copy", lib.qsa_pages_copy(packed, len(arrays), copy_src.data_ptr(), copy_dst.data_ptr(), n, wp, wn, on))
+    if n:
+        _check("qsa_pages_copy", lib.qsa_pages_copy(packed, len(arrays), copy_src.data_ptr(), copy_dst.data_ptr(), n, wp, wn,
+                                                    _current_stream(dev) if stream is None else _stream(stream)))
 
 
-def _rows16(t: torch.Tensor, name: str, heads: int | None = None) -> tuple[int, int, int, int]:
-    """(rows, heads, token stride, head stride) of rows [n, heads, 128] of 16-bit values."""
-    shape = tuple(t.shape)
-    if len(shape) != 3 or shape[2] != HEAD_DIM or (heads is not None and shape[1] != heads) or t.stride(2) != 1:
+def _rows16(t: torch.Tensor, name: str, dev: int, heads: int | None = None) -> tuple[int, int, int, int]:
+    """(rows, heads, token stride, head stride) of rows [n, heads, 128] of 16-bit values on the current device."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or (heads is not None and shape[1] != heads) or strides[2] != 1:
         raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {HEAD_DIM}] with unit inner stride "
-                         f"(got {shape})")
-    return shape[0], shape[1], *_used(shape, t.stride())
+                         f"(got {tuple(shape)})")
+    if t.get_device() != dev:
+        raise _elsewhere(name, t, dev)
+    n, h, _ = shape
+    # a stride along a single entry is never used and may be anything in torch
+    return n, h, strides[0] if n > 1 else 0, strides[1] if h > 1 else 0
 
 
-def _pool(kcache: torch.Tensor, vcache_t: torch.Tensor, dtype) -> tuple[int, int]:
+def _pool(kcache: torch.Tensor, vcache_t: torch.Tensor, dtype, dev: int) -> tuple[int, int]:
     """(KV heads, capacity) of a pool of 16-bit pages."""
-    a, b = tuple(kcache.shape), tuple(vcache_t.shape)
-    if kcache.dtype != dtype or vcache_t.dtype != dtype:
+    a, b = kcache.shape, vcache_t.shape
+    if kcache.dtype is not dtype or vcache_t.dtype is not dtype:
         raise ValueError("kcache and vcache_t must have the rows' dtype")
     if len(a) != 3 or a[1] % 64 or a[2] != HEAD_DIM or b != (a[0], a[1] // 64, HEAD_DIM, 64) or \
             not kcache.is_contiguous() or not vcache_t.is_contiguous():
         raise ValueError("kcache and vcache_t must be contiguous [n_kv_heads, 64 n_pages, 128] and "
                          "[n_kv_heads, n_pages, 128, 64]")
+    for name, t in (("kcache", kcache), ("vcache_t", vcache_t)):
+        if t.get_device() != dev:
+            raise _elsewhere(name, t, dev)
     return a[0], a[1]
 
 
@@ -769,25 +796,23 @@ def pages_append(k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, first: t
     """K and V rows [n, n_kv_heads, 128] into the pages of table [n_rows, max_pages] at positions
     first[s], first[s] + 1, ...: entries cu_rows[s] .. cu_rows[s + 1] - 1 are row s's, and name the
     rows of k and v (rows int32, e.g. the accepted drafts) or are them (rows None)."""
-    lib = load()
+    lib, dev = load(), torch.cuda.current_device()
     dt = _qdtype(k, "k")
-    if v.dtype != k.dtype or v.shape != k.shape:
+    if v.dtype is not k.dtype or v.shape != k.shape:
         raise ValueError("v must match k's shape and dtype")
-    kv, cap = _pool(kcache, vcache_t, k.dtype)
-    n, _, kt, kh = _rows16(k, "k", kv)
-    _, _, vt, vh = _rows16(v, "v", kv)
-    n_rows, width, stride = _table(table)
-    _i32(first, "first", n_rows)
-    _i32(cu_rows, "cu_rows", n_rows + 1)
-    entries = n if rows is None else _i32(rows, "rows")
-    on = _stream_of(stream, torch.cuda.current_device(), k=k, v=v, table=table, first=first, cu_rows=cu_rows, kcache=kcache,
-                    vcache_t=vcache_t, rows=rows, ws=ws)
-    if entries == 0 or n == 0:
-        return
-    wp, wn = _ws_args(ws)
-    _check("qsa_pages_append", lib.qsa_pages_append(
-        k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, n, _ptr(rows), entries, cu_rows.data_ptr(), first.data_ptr(),
-        table.data_ptr(), stride, width, n_rows, kv, HEAD_DIM, kcache.data_ptr(), vcache_t.data_ptr(), cap, wp, wn, on))
+    kv, cap = _pool(kcache, vcache_t, k.dtype, dev)
+    n, _, kt, kh = _rows16(k, "k", dev, kv)
+    _, _, vt, vh = _rows16(v, "v", dev, kv)
+    n_rows, width, stride = _table(table, dev)
+    _vectors(n_rows, dev, ("first", first))
+    _vectors(n_rows + 1, dev, ("cu_rows", cu_rows))
+    entries = n if rows is None else _length("rows", rows, dev)
+    wp, wn = _workspace(ws, dev)
+    if entries and n:
+        _check("qsa_pages_append", lib.qsa_pages_append(
+            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, n, _ptr(rows), entries, cu_rows.data_ptr(), first.data_ptr(),
+            table.data_ptr(), stride, width, n_rows, kv, HEAD_DIM, kcache.data_ptr(), vcache_t.data_ptr(), cap, wp, wn,
+            _current_stream(dev) if stream is None else _stream(stream)))
 
 
 def attention_workspace_bytes(rows: int, n_heads: int, n_kv_heads: int) -> int:
@@ -802,20 +827,26 @@ def alloc_attention_workspace(rows: int, n_heads: int, n_kv_heads: int, device=N
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _dense_args(q, k, v, out, lse):
-    """What both dense attentions check of their rows: (dtype, q's, k's and v's rows and strides, the output's dtype)."""
+def _dense_args(q, k, v, out, lse, dev):
+    """What both dense attentions check of their rows: (dtype, rows and heads of q and of k, their strides, out's dtype)."""
+    dtype = q.dtype
     dt = _qdtype(q, "q")
-    if k.dtype != q.dtype or v.dtype != q.dtype or v.shape != k.shape:
+    if k.dtype is not dtype or v.dtype is not dtype or v.shape != k.shape:
         raise ValueError("k and v must match each other's shape and q's dtype")
-    qn, heads, qt, qh = _rows16(q, "q")
-    kn, kv, kt, kh = _rows16(k, "k")
-    _, _, vt, vh = _rows16(v, "v")
-    out_dt = F32 if out.dtype == torch.float32 else dt
-    if out.shape != q.shape or not out.is_contiguous() or (out_dt == dt and out.dtype != q.dtype):
+    qn, heads, *qs = _rows16(q, "q", dev)
+    kn, kv, *ks = _rows16(k, "k", dev)
+    _, _, *vs = _rows16(v, "v", dev)
+    out_dt = F32 if out.dtype is torch.float32 else dt
+    if out.shape != q.shape or not out.is_contiguous() or (out_dt == dt and out.dtype is not dtype):
         raise ValueError("out must be a contiguous tensor [n, n_heads, 128], fp32 or of q's dtype")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (qn, heads) or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 tensor [n, n_heads]")
-    return dt, qn, heads, kn, kv, (qt, qh), (kt, kh), (vt, vh), out_dt
+    if out.get_device() != dev:
+        raise _elsewhere("out", out, dev)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (qn, heads) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 tensor [n, n_heads]")
+        if lse.get_device() != dev:
+            raise _elsewhere("lse", lse, dev)
+    return dt, qn, heads, kn, kv, qs, ks, vs, out_dt
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
@@ -825,17 +856,16 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     [n, n_heads, 128] and keys cu_k[s] .. cu_k[s + 1] - 1 of k, v [m, n_kv_heads, 128] (bfloat16 or float16, any
     token and head strides that are multiples of 8); its i-th query of lq sees its first lk - lq + i + 1 keys.
     out [n, n_heads, 128] fp32 or of q's dtype, lse [n, n_heads] fp32; n_heads = 1 .. 16 times n_kv_heads."""
-    lib = load()
-    dt, qn, heads, kn, kv, qs, ks, vs, out_dt = _dense_args(q, k, v, out, lse)
-    n_seqs = _i32(cu_q, "cu_q") - 1
-    _i32(cu_k, "cu_k", n_seqs + 1)
-    on = _stream_of(stream, torch.cuda.current_device(), q=q, k=k, v=v, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse, ws=ws)
-    if qn == 0:
-        return out
-    _check("qsa_prompt_attention", lib.qsa_prompt_attention(
-        q.data_ptr(), *qs, k.data_ptr() or q.data_ptr(), *ks, v.data_ptr() or q.data_ptr(), *vs, dt, cu_q.data_ptr(),
-        cu_k.data_ptr(), n_seqs, qn, kn, heads, kv, HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else float(scale),
-        out.data_ptr(), out_dt, _ptr(lse), *_ws_args(ws), on))
+    lib, dev = load(), torch.cuda.current_device()
+    dt, qn, heads, kn, kv, qs, ks, vs, out_dt = _dense_args(q, k, v, out, lse, dev)
+    n_seqs = _length("cu_q", cu_q, dev) - 1
+    _vectors(n_seqs + 1, dev, ("cu_k", cu_k))
+    wp, wn = _workspace(ws, dev)
+    if qn:   # without keys k and v have no memory: q's stands in and is not read as keys
+        _check("qsa_prompt_attention", lib.qsa_prompt_attention(
+            q.data_ptr(), *qs, k.data_ptr() or q.data_ptr(), *ks, v.data_ptr() or q.data_ptr(), *vs, dt, cu_q.data_ptr(),
+            cu_k.data_ptr(), n_seqs, qn, kn, heads, kv, HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else float(scale),
+            out.data_ptr(), out_dt, _ptr(lse), wp, wn, _current_stream(dev) if stream is None else _stream(stream)))
     return out
 
 
@@ -847,26 +877,24 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, parents: t
     [n, n_kv_heads, 128] are sequence s's tree, at most max_nodes (<= 64) of them; parents [n] int32
     gives each one's parent in its tree (-1: none), always before it.  A node sees the n_tokens[s]
     tokens in the pages table[s], its ancestors and itself."""
-    lib = load()
-    dt, qn, heads, kn, kv, qs, ks, vs, out_dt = _dense_args(q, k, v, out, lse)
+    lib, dev = load(), torch.cuda.current_device()
+    dt, qn, heads, kn, kv, qs, ks, vs, out_dt = _dense_args(q, k, v, out, lse, dev)
     if kn != qn:
         raise ValueError("k and v must have a row per node")
-    pool_kv, cap = _pool(kcache, vcache_t, q.dtype)
+    pool_kv, cap = _pool(kcache, vcache_t, q.dtype, dev)
     if pool_kv != kv:
         raise ValueError("k, v and the pool must have the same KV heads")
-    n_seqs, width, stride = _table(table)
-    _i32(parents, "parents", qn)
-    _i32(cu_nodes, "cu_nodes", n_seqs + 1)
-    _i32(n_tokens, "n_tokens", n_seqs)
-    on = _stream_of(stream, torch.cuda.current_device(), q=q, k=k, v=v, parents=parents, cu_nodes=cu_nodes, kcache=kcache,
-                    vcache_t=vcache_t, table=table, n_tokens=n_tokens, out=out, lse=lse, ws=ws)
-    if qn == 0:
-        return out
-    _check("qsa_tree_attention", lib.qsa_tree_attention(
-        q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, dt, parents.data_ptr(), cu_nodes.data_ptr(), n_seqs, qn,
-        max_nodes, kcache.data_ptr(), vcache_t.data_ptr(), cap, table.data_ptr(), stride, width, n_tokens.data_ptr(), heads,
-        kv, HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else float(scale), out.data_ptr(), out_dt, _ptr(lse), *_ws_args(ws),
-        on))
+    n_seqs, width, stride = _table(table, dev)
+    _vectors(qn, dev, ("parents", parents))
+    _vectors(n_seqs + 1, dev, ("cu_nodes", cu_nodes))
+    _vectors(n_seqs, dev, ("n_tokens", n_tokens))
+    wp, wn = _workspace(ws, dev)
+    if qn:
+        _check("qsa_tree_attention", lib.qsa_tree_attention(
+            q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, dt, parents.data_ptr(), cu_nodes.data_ptr(), n_seqs, qn,
+            max_nodes, kcache.data_ptr(), vcache_t.data_ptr(), cap, table.data_ptr(), stride, width, n_tokens.data_ptr(),
+            heads, kv, HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else float(scale), out.data_ptr(), out_dt, _ptr(lse), wp,
+            wn, _current_stream(dev) if stream is None else _stream(stream)))
     return out
 
 
