@@ -695,7 +695,8 @@ qsa_status qsa_pages_append(const void *k, int64_t k_token_stride, int64_t k_hea
                             int head_dim, void *kcache, void *vcache_t, int capacity, void *ws, size_t ws_bytes,
                             qsa_stream stream);
 
-/* Workspace of the two attentions below for `rows` query rows (tokens) in all, in bytes; 0 for invalid sizes. */
+/* Workspace of the two attentions below for `rows` query rows (tokens) in all, in bytes; 0 for invalid sizes.  One for
+ * more rows serves fewer.  Zero-filled before its first use; every call leaves it reusable. */
 size_t qsa_attention_workspace_bytes(int rows, int n_heads, int n_kv_heads);
 
 /*
@@ -713,7 +714,8 @@ size_t qsa_attention_workspace_bytes(int rows, int n_heads, int n_kv_heads);
  *             head strides in elements, multiples of 8 (slices of a fused projection's rows are taken as
  *             they lie), 16-byte aligned; those of k and v >= 128 along an axis of more than one entry
  *   cu_q, cu_k [n_seqs + 1] int32 on the DEVICE, ascending from >= 0 to <= total_q and total_k; a
- *             value outside is clamped and a descent makes an empty sequence (either sets QSA_FLAG_NBLOCKS_CLAMPED)
+ *             value outside is clamped and a descent makes an empty sequence (either sets QSA_FLAG_NBLOCKS_CLAMPED;
+ *             when sequences of queries then overlap, nothing is computed)
  *   out       [total_q][n_heads][128] of out_dt: QSA_F32, or dt; 16-byte aligned
  *   lse       [total_q][n_heads] fp32 out, or NULL
  *   scale     softmax scale (host float), finite and > 0
@@ -721,7 +723,9 @@ size_t qsa_attention_workspace_bytes(int rows, int n_heads, int n_kv_heads);
  *
  * Rows of out and lse that belong to no sequence are left as they were; keys and values that a query does not see do
  * not touch it, whatever they hold.  Arithmetic: products on the tensor cores with fp32 sums, softmax
- * statistics in fp32, the weights of the product with v rounded to `dt`.
+ * statistics in fp32, the weights of the product with v rounded to `dt`.  Sums over the keys are formed in fp32
+ * before they are divided by the weights' sum: bf16 values of v above 2^80 in magnitude may overflow.
+ * Launch: as a programmatic dependent of the work before it on `stream`, as qsa_select_attention.
  * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides as above, head_dim != 128, n_heads not 1 to
  * 16 times n_kv_heads, n_kv_heads outside [1, 65535], n_seqs outside [1, 65535], total_q < 0 or total_q *
  * n_heads >= 2^30, total_k < 0 or total_k >= 2^30, a scale not finite or <= 0, out_dt other than QSA_F32 or dt, an

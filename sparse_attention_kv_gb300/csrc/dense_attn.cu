@@ -7,24 +7,37 @@
 //   S = Q K^T   tcgen05, M = 128 rows, N = 128 keys, into tensor memory
 //   P = exp2    one thread per row reads its 128 logits, writes the weights in 16 bits over them in tensor memory
 //   O += P V    tcgen05 with A = P from tensor memory, M = 128 rows, N = 128 dimensions
-// The rows of a tile are (token, head of the group) pairs, token-major, so every group size fills it, all rows of a
-// tile share one KV head's K and V, and a tile of 256 rows spans few tokens (16 at groups of 16): little of a causal
-// tile is masked, and one token's 16 heads already read a page once.  A CTA works on two streams of 128 rows in turn (the
-// tensor cores multiply for one while the other's softmax runs), which take the same K and V from shared memory.  m
-// moves only when a row's maximum has risen by more than 2^8 of weight (then l and O are scaled in place), since
-// any reference gives the same quotient: sums stay below 2^8 x keys, weights keep their relative precision.
+// The rows of a stream are (token, head of the group) pairs, token-major, 128 / group whole tokens: all rows share one KV
+// head's K and V, a tile of two streams spans few tokens (16 at groups of 16), so that little of a causal tile is masked, and
+// a single token's 16 heads read a page once.  A CTA works on both streams in turn: the tensor cores multiply for
+// one while the other's softmax runs, and both take the same K and V from shared memory.  Where no sequence fills more than
+// one stream (a decode step) both take the same rows and half of a step's keys each, and are joined at the end.
+// m moves only when a row's maximum has risen by more than 2^8 of weight (then l and O are scaled in place): any
+// reference gives the same quotient, sums stay below 2^8 x keys, weights keep their relative precision.
 //
-// Work: every (sequence, KV head, tile) is a run of steps; the CTAs of a persistent grid take equal shares of all runs laid
-// end to end, so one long context fills the GPU as well as many short ones.  A run that crosses a border is
-// joined by combine_kernel from the CTAs' partial (O, m, l).
+// Work: every (sequence, KV head, tile) is a run of steps; a persistent grid of one CTA per SM takes the runs whole or in
+// pieces (see Walk).  A run in pieces is joined by combine_kernel from the CTAs' partial (O, m, l).
 //
-// Roles: warps 0-3 and 4-7 softmax and epilogue of a stream, warp 8 TMA (a ring of 32 KB slots, K and V in turn), warp 9
-// the MMAs.  V of packed rows is an MN-major operand, V of a page a K-major one (its dimension comes before its token).
-// Values at places that a row does not see must not reach it as 0 x NaN: in steps that hold such places one stream's
-// warps clear what lies past the last row's view and any value that is not finite; the latter is added to the
-// rows that do see it at the end.
+// Roles: warp 0 finds the pieces, publishes them and copies (TMA; a ring of 32 KB slots, K and V in turn), warps 1 and 2
+// issue a stream's products, warp 3 clears values, warps 4-7 and 8-11 are a stream's softmax and epilogue.  V of packed
+// rows is an MN-major operand, V of a page a K-major one (its dimension comes before its token).
+// Values at places that a row does not see must not reach it as 0 x NaN: in steps that hold such places warp 3 clears what
+// lies past the last row's view and any value that is not finite; the latter is added at the end to the rows that see it.
 //
-// Every wait is bounded; on expiry the CTA raises QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees its tensor memory and exits.
+// What bounds it.  Prompts: the tensor cores.  A step of 256 rows and 128 keys is 2,048 cycles of MMA; it takes 2,250 to 2,450
+// (1.17-1.25 us at 1.95 GHz), the rest being the chain P ready -> P V -> S -> softmax (0.5 us) of a stream where it does
+// not fit beside the other one's products.  131,072 tokens under 256 queries x 64 heads: 0.63-0.66 ms, 1.67-1.76 PFLOP/s; one
+// prompt of 16,384 tokens, 64 heads in 4 groups: 2.4-2.55 ms, 1.72-1.83 PFLOP/s (a large library product runs at
+// 1.88 here).  Decode: HBM; one query at 258,000 tokens, 64 heads in 4 groups: 94-98 us, of which 88 the main kernel
+// (528 MB, 6.0 TB/s).  Short calls: about 13 us for a CTA's first piece (2 to find it, 2 until its first product, 2.2 for
+// its end), 4.4 us for a further one of a single step.
+// Measured on the way (16,384 tokens, ms): one warp issuing both streams, descriptors made in divergent code 5.19 (an MMA then
+// takes about 100 cycles to issue); Q by TMA, outputs in whole rows 3.81; two threads a row, two issuing warps in turn, descriptors in
+// uniform registers 2.86; a thread a row, weights passed on in two parts 2.70; steps that are not seen whole in
+// rolled loops (instruction fetches) 2.55; runs dealt out 2.48.
+//
+// Every wait is bounded; on expiry the CTA raises QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees its tensor memory
+// and exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -87,7 +100,7 @@ struct Params {
     uint32_t *flags;
 };
 
-// What a CTA works on at a time: steps s0 .. s1 - 1 of a run's n, for a tile of two streams.
+// What a CTA works on at a time: steps s0 .. s1 - 1 of a run's n, for a tile.
 struct Piece {
     int stop;             // no piece: the CTA is done
     int bad;              // a value in a step that not every row sees whole was not finite
@@ -361,7 +374,7 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
         q.load(p, s, say);
         return p.n_kv * q.cum(p, q.tiles);
     };
-    long long total = 0, first = 0;   // first: the weights of sequences 0 .. 31
+    long long total = 0, first = 0, rows = 0;   // first: the weights of sequences 0 .. 31
     int runs = 0, longest = 0;
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
         const long long x = weight(s0 + lane, tell);
@@ -370,6 +383,7 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
             w.mine = q;
         }
         total += warp_sum(x);
+        rows += warp_sum(q.lq);
         const bool in = s0 + lane < p.n_seqs;
         longest = max(longest, in && q.tiles > 0 ? q.work(p, q.tiles - 1) : 0);
         if (counted) {
@@ -383,6 +397,12 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     __syncwarp();
     w.tile = TREE ? (int)(blockIdx.x % (unsigned)p.row_tiles) : 0;
     w.rule = kBorder;
+    if (rows > p.total_q) {   // sequences that overlap would write rows twice, and be any amount of work: nothing is done
+        if (tell && lane == 0) atomicOr(p.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+        w.rule = kEven;
+        w.s0 = -1;
+        return;
+    }
     if (counted && runs <= p.shares) {
         constexpr int kTurns = (kMaxCtas + 31) / 32;
         int n[kTurns], steps = 0;
@@ -773,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)ct.tmem);
 
-    int it = 0;   // slots of the ring used so far
+    int it = 0;                      // slots of the ring used so far
+    uint32_t queries[2] = {0, 0};    // and Q tiles copied
     if (warp == 0) {
         // ---------------- pieces and copies: Q, K and V of each step, K first
         if (lane == 0) {
@@ -785,14 +806,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) ct.dealing = walk.rule == kDealt;
         Piece pc;
         int step = 0, no = 0;
-        uint32_t nq[2] = {0, 0};
         bool ok = true;
         const uint32_t qbytes = (uint32_t)(p.toks * p.group * 256);
         auto load_q = [&]() {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (!ok || pc.e[i] <= pc.s0) continue;
-                if (!(ok = wait_all(&ct.qempty[i], (nq[i]++ & 1u) ^ 1u, abort_flag)) || lane != 0) continue;
+                if (!(ok = wait_all(&ct.qempty[i], (queries[i] & 1u) ^ 1u, abort_flag))) continue;
+                ++queries[i];
+                if (lane != 0) continue;
                 uint8_t *to = smem + kOffQ + i * kQBytes;
                 mbar_expect_tx(&ct.qfull[i], qbytes);
                 const int row = pc.q0 + pc.tok0 + (HALVES ? 0 : i * p.toks);
@@ -1234,8 +1256,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (ct.abort && lane == 0) {   // copies and products in flight end before their memory goes
-        if (warp == 0)
+        if (warp == 0) {
             for (int i = max(0, it - kSlots); i < it; ++i) mbar_drain(&ct.full[i % kSlots], (uint32_t)(i / kSlots) & 1u);
+            for (int i = 0; i < 2; ++i)
+                if (queries[i] > 0) mbar_drain(&ct.qfull[i], (queries[i] - 1u) & 1u);
+        }
         if (warp == 1 || warp == 2) {
             mma_commit(&ct.drain[warp - 1]);
             mbar_drain(&ct.drain[warp - 1], 0);
@@ -1416,7 +1441,7 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.rows_cap = rows_cap(most, p.group);
     p.by_group = (65536u + (uint32_t)p.group - 1u) / (uint32_t)p.group;
     p.scale = a.scale;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.scale_log2 = a.scale < 2e38f ? a.scale * 1.4426950408889634f : 3e38f;
     p.out = a.out;
     p.out_f32 = a.out_dt == QSA_F32;
     p.lse = a.lse;

@@ -124,6 +124,15 @@ def test_prompt_bad_ranges_are_flagged():
     assert torch.equal(out, good) and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
 
 
+def test_sequences_that_overlap_are_refused_on_the_device():
+    q, k, v = normal(1, 40, 4, 128, dt=BF16), normal(2, 40, 2, 128, dt=BF16), normal(3, 40, 2, 128, dt=BF16)
+    out, ls, ws = _prompt(q, k, v, None, None, cu_q=i32([0, 30, 5, 40]), cu_k=i32([0, 10, 20, 40]))
+    assert torch.isnan(out).all() and torch.isnan(ls).all() and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+    good, lse, _ = _prompt(q, k, v, [40], [40])          # keys may be shared: both sequences see the first 20
+    out, ls, ws = _prompt(q, k, v, [20, 20], None, cu_k=i32([0, 20, 0]))
+    assert torch.equal(out[:20], good[:20]) and (out[20:] == 0).all() and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+
+
 def test_prompt_large_logits_and_late_rises():
     """Logits in the hundreds, and a maximum that rises in every tile."""
     for dt in (BF16, F16):
