@@ -492,10 +492,11 @@ __global__ void __launch_bounds__(kRowThreads) pages_append_kernel(PageTable t, 
     const int tid = threadIdx.x;
     if (tid == 0) unit.row = -1;
     __syncthreads();
+    const bool tell = blockIdx.x == gridDim.x - 1 && blockIdx.y == 0;   // looks at every row
     int before = 0;
-    for (int r0 = 0; r0 < t.n_rows && before <= (int)blockIdx.x; r0 += kRowThreads) {
+    for (int r0 = 0; r0 < t.n_rows && (tell || before <= (int)blockIdx.x); r0 += kRowThreads) {
         const int row = r0 + tid;
-        const int np = row < t.n_rows ? pages_of(span_of(t, a, row, blockIdx.x == 0 && blockIdx.y == 0)) : 0;
+        const int np = row < t.n_rows ? pages_of(span_of(t, a, row, tell)) : 0;
         int total;
         const int at = before + block_excl_scan<kRowThreads>(np, sm, total);
         if ((int)blockIdx.x >= at && (int)blockIdx.x < at + np) {

@@ -267,6 +267,22 @@ def test_append_drops_what_has_no_place():
     assert torch.equal(kc, kw) and torch.equal(vc, vw) and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
 
 
+@pytest.mark.parametrize("bad", [0, 255, 256, 599])
+def test_append_looks_at_every_row_for_its_flags(bad):
+    """600 rows of one token each, one of them with no place: behind the first pages, and without a page of its own."""
+    rows, kv = 600, 1
+    k, v = normal(1, rows, kv, 128, dt=torch.bfloat16), normal(2, rows, kv, 128, dt=torch.bfloat16)
+    first = [3] * rows
+    first[bad] = 64
+    table = [[p] for p in range(rows)]
+    kc, vc = random_pool(5, kv, rows, torch.bfloat16)
+    kw, vw = kc.clone(), vc.clone()
+    ws = qsa.alloc_pages_workspace(rows, rows)
+    qsa.pages_append(k, v, i32(table), i32(first), i32(cu([1] * rows)), kc, vc, ws=ws)
+    paged.Pool(table, first, [0] * rows).append(k, v, first, cu([1] * rows), kw, vw)
+    assert torch.equal(kc, kw) and torch.equal(vc, vw) and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
+
+
 @pytest.mark.parametrize("captured", [False, True])
 def test_a_generation_over_pages(captured):
     """Prompts attended and appended, sequences forked, trees of drafts attended, their accepted nodes appended
