@@ -714,11 +714,12 @@ size_t qsa_attention_workspace_bytes(int rows, int n_heads, int n_kv_heads);
  *             head strides in elements, multiples of 8 (slices of a fused projection's rows are taken as
  *             they lie), 16-byte aligned; those of k and v >= 128 along an axis of more than one entry
  *   cu_q, cu_k [n_seqs + 1] int32 on the DEVICE, ascending from >= 0 to <= total_q and total_k; a
- *             value outside is clamped and a descent makes an empty sequence (either sets QSA_FLAG_NBLOCKS_CLAMPED;
- *             when sequences of queries then overlap, nothing is computed)
+ *             value outside is clamped and a descent makes an empty sequence (either sets QSA_FLAG_NBLOCKS_CLAMPED).
+ *             A query in two sequences gets either one's result; when the sequences together hold more than
+ *             total_q queries, nothing is computed.  Sequences may share keys
  *   out       [total_q][n_heads][128] of out_dt: QSA_F32, or dt; 16-byte aligned
  *   lse       [total_q][n_heads] fp32 out, or NULL
- *   scale     softmax scale (host float), finite and > 0
+ *   scale     softmax scale (host float), finite and > 0; scaled logits must lie within fp32's range
  *   ws        a workspace of at least qsa_attention_workspace_bytes(total_q, n_heads, n_kv_heads) bytes
  *
  * Rows of out and lse that belong to no sequence are left as they were; keys and values that a query does not see do

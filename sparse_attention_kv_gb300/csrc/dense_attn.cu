@@ -262,7 +262,7 @@ struct Walk {
     Rule rule;
     int s, g, t, tile;
     long long at, x0, x1;   // kBorder: the beginning of the next run, and the CTA's share of all runs
-    int run, runs;          // kDealt: the next run
+    int run, runs;          // kDealt: the next run, more runs than shares
     bool begun;
     Seq<TREE> mine;         // up to 32 sequences: a lane each
     int s0, s1;             // kEven: the piece's steps; s0 < 0: no piece (any more)
@@ -320,8 +320,9 @@ struct Walk {
                 if (begun) {   // the copies of the run before are on their way
                     unsigned i = 0;
                     if ((threadIdx.x & 31) == 0) i = atomicAdd(p.dealt + 2 * tile, 1u);
-                    run = p.shares + (int)__shfl_sync(~0u, i, 0);
-                    if (run >= runs) break;
+                    i = __shfl_sync(~0u, i, 0);
+                    if (i >= (unsigned)(runs - p.shares)) break;
+                    run = p.shares + (int)i;
                 }
                 begun = true;
                 locate(p, ct, run);
@@ -426,7 +427,7 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
             if (__reduce_add_sync(~0u, pieces) <= p.shares) break;
             ++len;
         }
-        if (len <= even + kSlack || len == kWhole) {
+        if (len <= even + kSlack) {
             w.rule = kEven;
             w.s0 = -1;
             int before = 0;

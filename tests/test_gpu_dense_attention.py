@@ -306,3 +306,119 @@ def test_captured_calls_follow_their_inputs():
             check_attention(out, lse, _want_tree(q, k, v, par, nn, kc, vc, table, nt), BF16)
             check_attention(pout, plse, paged.prompt(q.double(), k.double(), v.double(), nn, nn, SCALE), BF16)
     assert qsa.read_flags(ws, stream=side) == 0
+
+
+# ------------------------------------------------------------------ how the work is shared out
+
+MANY = [(7 * i) % 41 for i in range(300)]            # with some of no queries
+# (queries, keys, KV heads, group): runs in equal pieces; dealt out, by sequences in a warp and by more; cut at equal distances,
+# by one long sequence and by more sequences than are counted
+SHARED_OUT = [([40], [5000], 2, 16), ([300] * 20, [300 + 9 * i for i in range(20)], 4, 16),
+              ([1 + i % 60 for i in range(200)], [70 + i for i in range(200)], 4, 8), ([4000, 30], [4000, 5000], 1, 16),
+              (MANY, [m + 3 * (i % 30) for i, m in enumerate(MANY)], 2, 3)]
+
+
+@pytest.mark.parametrize("lq,lk,kv,group", SHARED_OUT)
+def test_prompt_however_its_runs_are_shared_out(lq, lk, kv, group):
+    _check_prompt(lq, lk, kv, group, BF16, seed=5)
+
+
+TREES = [([3000, 10, 500], [40, 64, 3], 1, 16), ([300 + 20 * i for i in range(20)], [1 + 3 * i for i in range(20)], 4, 16),
+         ([10 * i for i in range(60)], [1 + i % 33 for i in range(60)], 2, 16), ([9000] + [100] * 40, [50] * 41, 2, 13),
+         ([5 * i for i in range(300)], [(5 * i) % 9 for i in range(300)], 1, 8), ([2 * i for i in range(300)], [1] * 300, 2, 16)]
+
+
+@pytest.mark.parametrize("n_tokens,nodes,kv,group", TREES)
+def test_tree_however_its_runs_are_shared_out(n_tokens, nodes, kv, group):
+    q, k, v, parents, kc, vc, table = _tree_inputs(61, n_tokens, nodes, kv, group, BF16)
+    out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens), BF16)
+    assert qsa.read_flags(ws) == 0
+
+
+def test_one_workspace_serves_calls_of_every_kind():
+    """Prompts and trees of all kinds in turn, twice: each leaves the workspace as the next one needs it."""
+    ws = qsa.alloc_attention_workspace(6100, 64, 4)
+    calls = []
+    for i, (lq, lk, kv, group) in enumerate(SHARED_OUT):
+        q, k, v = normal(i, sum(lq), kv * group, 128, dt=BF16), *(normal(9 + i, sum(lk), kv, 128, dt=BF16) for _ in "kv")
+        calls.append((lambda out, ls, w, a=(q, k, v, i32(cu(lq)), i32(cu(lk))): qsa.prompt_attention(*a, out, ls, ws=w), q, kv))
+        if i < len(TREES):
+            n_tokens, nodes, kv, group = TREES[i]
+            q, k, v, parents, kc, vc, table = _tree_inputs(71 + i, n_tokens, nodes, kv, group, BF16)
+            a = (q, k, v, i32(parents), i32(cu(nodes)), max(nodes), kc, vc, i32(table), i32(n_tokens))
+            calls.append((lambda out, ls, w, a=a: qsa.tree_attention(*a, out, ls, ws=w), q, kv))
+    first = []
+    for call, q, kv in calls:
+        out, ls = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        call(out, ls, qsa.alloc_attention_workspace(q.shape[0], q.shape[1], kv))
+        first.append((out, ls))
+    for _ in range(2):
+        for (call, q, _), (want, lse) in zip(calls, first):
+            out, ls = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device="cuda")
+            call(out, ls, ws)
+            assert torch.equal(out, want) and torch.equal(ls, lse)
+    assert qsa.read_flags(ws) == 0
+
+
+def test_two_streams_with_a_workspace_each():
+    lens, kv, group = [700, 40, 900], 2, 16
+    q, k, v = (normal(i, sum(lens), h, 128, dt=BF16) for i, h in ((1, kv * group), (2, kv), (3, kv)))
+    want, lse, _ = _prompt(q, k, v, lens, lens)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [qsa.alloc_attention_workspace(sum(lens), kv * group, kv) for _ in streams]
+    outs = [[torch.full_like(q, float("nan")) for _ in range(4)] for _ in streams]
+    c = i32(cu(lens))
+    torch.cuda.synchronize()
+    for i in range(4):
+        for st, ws, out in zip(streams, spaces, outs):
+            qsa.prompt_attention(q, k, v, c, c, out[i], ws=ws, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for out in outs for x in out)
+
+
+def test_a_captured_prompt_follows_its_lengths_from_kind_to_kind():
+    total, keys, kv, group = 2600, 5200, 1, 16
+    q, k, v = normal(1, total, kv * group, 128, dt=BF16), *(normal(2 + i, keys, kv, 128, dt=BF16) for i in range(2))
+    cq, ck = i32([0] * 21), i32([0] * 21)
+    ws = qsa.alloc_attention_workspace(total, kv * group, kv)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    qsa.prompt_attention(q, k, v, cq, ck, out, lse, ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        qsa.prompt_attention(q, k, v, cq, ck, out, lse, ws=ws)
+    for lq, lk in (([50], [5000]), ([130] * 20, [260] * 20), ([2600], [5200]), ([0, 0, 7], [0, 3, 2000]), ([130] * 20, [130] * 20)):
+        cq.copy_(i32(cu(lq + [0] * (20 - len(lq))))), ck.copy_(i32(cu(lk + [0] * (20 - len(lk)))))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        n, m = sum(lq), sum(lk)
+        check_attention(out[:n], lse[:n], paged.prompt(q[:n].double(), k[:m].double(), v[:m].double(), lq, lk, SCALE), BF16)
+        assert torch.isnan(out[n:]).all()
+    assert qsa.read_flags(ws) == 0
+
+
+@pytest.mark.parametrize("group,long", [(16, 5000), (3, 700), (16, 300)])
+def test_a_large_tree_is_not_touched_by_what_it_does_not_see(group, long):
+    """Two streams of rows, several tiles of them, a run in pieces: NaN behind the tokens and in nodes that are no ancestors."""
+    n_tokens, nodes, kv = [long, 77], [60, 44], 2
+    q, k, v, _, kc, vc, table = _tree_inputs(83, n_tokens, nodes, kv, group, BF16)
+    parents = [i - 2 if i >= 2 else -1 for m in nodes for i in range(m)]     # two paths: the even nodes and the odd ones
+    good, lse, _ = _tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    kc2, vc2 = torch.full_like(kc, float("nan")), torch.full_like(vc, float("nan"))
+    for s, n in enumerate(n_tokens):
+        for j in range((n + 63) // 64):
+            p, m = table[s][j], min(64, n - 64 * j)
+            kc2[:, 64 * p:64 * p + m], vc2[:, p, :, :m] = kc[:, 64 * p:64 * p + m], vc[:, p, :, :m]
+    for first in (0, 60):
+        k2, v2 = k.clone(), v.clone()
+        v2[first + 31] = float("inf")
+        k2[first + 33] = float("nan")
+        out, ls, ws = _tree(q, k2, v2, parents, nodes, kc2, vc2, table, n_tokens)
+        touched = torch.zeros(104, dtype=torch.bool)
+        touched[first + 31:first + nodes[first > 0]:2] = True
+        assert torch.equal(out[~touched], good[~touched]) and torch.equal(ls[~touched], lse[~touched])
+        assert not torch.isfinite(out[touched]).any() and torch.isnan(ls[first + 33]).all()
+        assert qsa.read_flags(ws) == 0
