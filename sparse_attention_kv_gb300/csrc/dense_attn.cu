@@ -42,6 +42,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "launch.h"
@@ -63,12 +64,15 @@ constexpr int kStageBytes = 4096;     // per softmax warp: 32 rows of 128 bytes 
 constexpr int kPieces = 4;            // pieces that are published ahead
 constexpr int kInfo = 8;              // steps whose page limits are held: more than the ring holds
 constexpr int kMaxCtas = 152;
-constexpr int kWhole = 8;             // runs of so few steps are not split
-constexpr int kRunKeys = 512;         // what a run's beginning and end cost, in keys
-constexpr int kTable = 256;           // sequences whose runs are counted in shared memory
-constexpr int kSlack = 8;             // steps that pieces of one length may lie above an even share
-constexpr int kShortRun = 16;         // steps of runs that are dealt out as they are, however few the shares hold
-constexpr int kMinShare = 384;        // least work, in keys, that a CTA is started for
+// How runs are shared out (measured in us, this side / the other):
+constexpr int kWhole = 8;       // runs of up to 8 steps are not split (4: a split one of 5 steps 15 / 18; 16: one of 12 steps 17 / 22)
+constexpr int kLeast = 3;       // steps of a piece of the others, at least (17 steps: in 3s 17.5, in 6s 19.6, in 2s 17.7)
+constexpr int kSlack = 4;       // steps that pieces of one length may lie above an even share (6 above: 64 nodes at 131,072 tokens 174 / 180)
+constexpr int kRunKeys = 512;   // what a run's beginning and end cost, in keys (1024: 4,096 tokens 206 / 193, a mixed batch 270 / 304; 256: 206 / 239)
+constexpr int kTable = 256;     // sequences whose runs are counted in shared memory
+constexpr int kShortRun = 16;   // steps of runs that are dealt out however few the shares hold (0: 1,024 tokens 29 / 35; 64: no better)
+constexpr int kMinShare = 384;  // least work, in keys, of a share: no share in the middle of a run is without a step
+constexpr int kManyParts = 8;   // parts of a run that combine_kernel shares out to its warps (38 parts 94 / 102; 64 sequences' two or three 360 / 348)
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
 
@@ -251,9 +255,11 @@ __device__ __forceinline__ int warp_scan(int v) {   // inclusive
 
 // A CTA's pieces one after another (one warp).  Which they are goes by one of three rules, the same in every CTA:
 //  kEven   no more runs than shares: each run in equal pieces, a share each, where that costs little against an even split
-//  kDealt  many runs, short against a share: whole, longest first within a (sequence, KV head), each to the next CTA that is free
+//  kDealt  more runs, those that end last short against a share: whole, longest first within a (sequence, KV head), each to the
+//          next CTA that is free
 //  kBorder otherwise: all runs laid end to end and cut at equal distances
-// Measured, us, kEven / kBorder: 5 trees over 900 tokens 23 / 28; kDealt / kBorder: 1,024 tokens 33 / 42, 16,384 tokens 2,450 / 2,560.
+// Measured, us: kEven / kBorder, 5 trees over 900 tokens 22 / 28; kDealt / kBorder, a prompt of 1,024 tokens 28 / 35, of 2,600
+// 89 / 100, of 16,384 2,450 / 2,520, 40 decodes of 2,500 tokens (8 heads; taken by kBorder) 105 / 85.
 enum Rule { kEven, kDealt, kBorder };
 
 template <bool TREE, bool HALVES>
@@ -377,6 +383,7 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     };
     long long total = 0, first = 0, rows = 0;   // first: the weights of sequences 0 .. 31
     int runs = 0, longest = 0;
+    Seq<TREE> last{};   // that has queries
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
         const long long x = weight(s0 + lane, tell);
         if (s0 == 0) {
@@ -391,6 +398,8 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
             const int mine = in ? p.n_kv * q.tiles : 0, incl = warp_scan(mine);
             if (in) ct.runs[s0 + lane + 1] = runs + incl;
             runs += __shfl_sync(~0u, incl, 31);
+            const unsigned some = __ballot_sync(~0u, q.tiles > 0);
+            if (some) last.take(q, 31 - __clz(some));
         }
     }
     longest = __reduce_max_sync(~0u, longest);
@@ -419,21 +428,23 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
         }
         steps = __reduce_add_sync(~0u, min(steps, 1 << 24));
         const int even = (steps + p.shares - 1) / p.shares;
-        int len = max(even, kWhole);   // of a piece, at most
-        while (len <= even + kSlack) {
+        int len = max(even, kLeast);   // of a piece, at most
+        auto pieces_of = [&](int n) { return n <= kWhole ? min(n, 1) : (n + len - 1) / len; };
+        const int most = len + kSlack;
+        while (len <= most) {
             int pieces = 0;
 #pragma unroll
-            for (int k = 0; k < kTurns; ++k) pieces += (n[k] + len - 1) / len;
+            for (int k = 0; k < kTurns; ++k) pieces += pieces_of(n[k]);
             if (__reduce_add_sync(~0u, pieces) <= p.shares) break;
             ++len;
         }
-        if (len <= even + kSlack) {
+        if (len <= most) {
             w.rule = kEven;
             w.s0 = -1;
             int before = 0;
 #pragma unroll
             for (int k = 0; k < kTurns; ++k) {
-                const int c = (n[k] + len - 1) / len, incl = warp_scan(c);
+                const int c = pieces_of(n[k]), incl = warp_scan(c);
                 const int part = (int)share - (before + incl - c);
                 const unsigned mine = __ballot_sync(~0u, part >= 0 && part < c);
                 if (mine) {
@@ -449,7 +460,9 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
             return;
         }
     }
-    if (counted && runs > p.shares && longest <= max(total / p.shares / 4, (long long)kShortRun * kKeys + kRunKeys)) {
+    // The CTAs end within a run of the last ones dealt, one a share: of a long last sequence its first tiles, short ones
+    const int tail = last.tiles > p.shares ? last.work(p, p.shares - 1) : longest;
+    if (counted && runs > p.shares && tail <= max(total / p.shares / (TREE ? 3 : 2), (long long)kShortRun * kKeys + kRunKeys)) {
         w.rule = kDealt;
         w.run = (int)share;
         w.runs = runs;
@@ -1284,11 +1297,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Runs that several CTAs worked on: a CTA per (share that a run begins in and does not end in, 32 rows), a lane per row.
 // The partials O_c of the shares from there to the run's end are weighted 2^(m_c - M).
 constexpr int kJoinWarps = 8;
-constexpr int kJoinDims = 4;   // groups of four dimensions a CTA joins where parts may be many
+constexpr int kJoinDims = 4;   // groups of four dimensions that a CTA joins where parts may be many,
+constexpr int kJoinGroups = 2; // and that a warp joins where they are few (4 loads' time for 64 sequences 3 us more; 1, idle CTAs 2 us)
 constexpr int kJoinTurns = (kMaxCtas + kJoinWarps - 1) / kJoinWarps;
 
 // MANY: few rows (a decode step), so a run may lie in many parts: the warps share them out and meet in shared memory.
-// Otherwise a warp takes four dimensions of all parts.
+// Otherwise a warp takes eight dimensions of all parts.
 template <bool F16, bool MANY>
 __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_constant__ Params p, int grid) {
     wait_prior_grid();
@@ -1319,9 +1333,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
         o.z = fmaf(f, y.z, o.z);
         o.w = fmaf(f, y.w, o.w);
     };
+    const size_t at = (size_t)(d.z + token) * p.n_heads + d.y * p.group + (r - tok * p.group);
+    auto put = [&](const float4 &x, float inv, int d4) { store4<F16>(p, at * 128 + 4 * d4, x.x * inv, x.y * inv, x.z * inv, x.w * inv); };
     float M = -INFINITY, L = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    int d4 = blockIdx.z * kJoinWarps + warp;
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if constexpr (MANY) {
         __shared__ float top[kJoinWarps][32], sums[kJoinWarps][32];
         __shared__ float4 joined[kJoinWarps][kJoinDims][32];
@@ -1340,7 +1355,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
         for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, top[w][lane]);
         float4 o[kJoinDims];
 #pragma unroll
-        for (int e = 0; e < kJoinDims; ++e) o[e] = x;
+        for (int e = 0; e < kJoinDims; ++e) o[e] = zero;
 #pragma unroll
         for (int k = 0; k < kJoinTurns; ++k) {
             const float f = ml[k].y == 0.0f ? 0.0f : ex2(ml[k].x - M);
@@ -1355,12 +1370,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
         __syncthreads();
         if (warp >= kJoinDims || !mine) return;
         L = 0.0f;
+        float4 x = zero;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
             add(x, 1.0f, joined[w][warp][lane]);
             L += sums[w][lane];
         }
-        d4 = blockIdx.z * kJoinDims + warp;
+        put(x, L == 0.0f ? 0.0f : 1.0f / L, blockIdx.z * kJoinDims + warp);
     } else {
         if (!mine) return;
 #pragma unroll 4
@@ -1368,19 +1384,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) combine_kernel(const __grid_c
             const float2 ml = sums_of(i);
             M = fmaxf(M, ml.y == 0.0f ? -INFINITY : ml.x);
         }
+        constexpr int kDims = kJoinGroups;
+        const int d0 = blockIdx.z * kJoinWarps * kDims + warp;
+        float4 x[kDims];
+#pragma unroll
+        for (int e = 0; e < kDims; ++e) x[e] = zero;
 #pragma unroll 4
         for (int i = 0; i <= parts; ++i) {
             const float2 ml = sums_of(i);
-            const float4 y = part_of(i, d4);
+            float4 y[kDims];
+#pragma unroll
+            for (int e = 0; e < kDims; ++e) y[e] = part_of(i, d0 + e * kJoinWarps);
             const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - M);
             L = fmaf(f, ml.y, L);
-            if (f != 0.0f) add(x, f, y);
+#pragma unroll
+            for (int e = 0; e < kDims; ++e)
+                if (f != 0.0f) add(x[e], f, y[e]);
         }
+#pragma unroll
+        for (int e = 0; e < kDims; ++e) put(x[e], L == 0.0f ? 0.0f : 1.0f / L, d0 + e * kJoinWarps);
     }
-    const size_t at = (size_t)(d.z + token) * p.n_heads + d.y * p.group + (r - tok * p.group);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    store4<F16>(p, at * 128 + 4 * d4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (d4 == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    if (warp == 0 && blockIdx.z == 0 && p.lse) p.lse[at] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // Rows of a tile that `tokens` tokens can fill.
@@ -1389,7 +1413,7 @@ int rows_cap(int tokens, int group) {
 }
 
 template <bool F16, bool TREE, bool HALVES>
-qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bool split, cudaStream_t s) {
+qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, int most_steps, cudaStream_t s) {
     static std::mutex mu;
     static bool opted_in[64] = {false};
     int dev = 0;
@@ -1407,10 +1431,11 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, bo
     }
     st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE, HALVES>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3],
                           m[4], p);
-    if (st != QSA_OK || !split) return st;
-    const bool many = p.rows_cap <= 64;
+    if (st != QSA_OK || most_steps <= kWhole) return st;
+    const long long runs = (long long)p.n_seqs * p.n_kv, parts = std::min<long long>(p.shares / runs, most_steps / kLeast);
+    const bool many = p.rows_cap <= 64 && parts >= kManyParts;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32), 32 / (many ? kJoinDims : kJoinWarps));
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows_cap / 32), 32 / (many ? kJoinDims : kJoinWarps * kJoinGroups));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
@@ -1436,7 +1461,9 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.n_kv = a.n_kv_heads;
     p.group = a.n_heads / a.n_kv_heads;
     p.toks = kRows / p.group;
-    const bool halves = (TREE ? a.max_nodes : a.total_q) <= p.toks;   // no tile holds a second stream's rows
+    // No tile holds a second stream's rows: both take the first's, half a step each (us, halves / whole steps: a query at 9,000
+    // tokens 20.3 / 22.1, 16 decodes of 500 tokens 17.1 / 18.4, 258,000 tokens 94.5 / 94.7)
+    const bool halves = (TREE ? a.max_nodes : a.total_q) <= p.toks;
     p.tile = halves ? p.toks : 2 * p.toks;
     const int most = TREE && a.max_nodes < a.total_q ? a.max_nodes : a.total_q;   // tokens of a sequence
     p.rows_cap = rows_cap(most, p.group);
@@ -1463,8 +1490,8 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     p.row_tiles = TREE ? (a.max_nodes + p.tile - 1) / p.tile : 1;
     p.shares = ctas / p.row_tiles;
     const int grid = p.shares * p.row_tiles;
-    // the longest run that the sizes allow
-    const bool split = (TREE ? 64ll * a.table.max_pages + kKeys : (long long)a.total_k) > kWhole * kKeys;
+    // of a run, as far as the sizes tell
+    const int most_steps = ((TREE ? 64 * a.table.max_pages : a.total_k) + kKeys - 1) / kKeys + (TREE ? 1 : 0);
     CUtensorMap m[5];
     const Rows16 &k = a.total_k > 0 ? a.k : a.q, &v = a.total_k > 0 ? a.v : a.q;   // without keys nothing is loaded
     const int rows = a.total_k > 0 ? a.total_k : 1, heads = a.total_k > 0 ? a.n_kv_heads : 1;
@@ -1482,8 +1509,8 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
             return st;
     }
     if (halves)
-        return a.dt == QSA_F16 ? launch_typed<true, TREE, true>(m, p, grid, split, s) : launch_typed<false, TREE, true>(m, p, grid, split, s);
-    return a.dt == QSA_F16 ? launch_typed<true, TREE, false>(m, p, grid, split, s) : launch_typed<false, TREE, false>(m, p, grid, split, s);
+        return a.dt == QSA_F16 ? launch_typed<true, TREE, true>(m, p, grid, most_steps, s) : launch_typed<false, TREE, true>(m, p, grid, most_steps, s);
+    return a.dt == QSA_F16 ? launch_typed<true, TREE, false>(m, p, grid, most_steps, s) : launch_typed<false, TREE, false>(m, p, grid, most_steps, s);
 }
 
 }  // namespace

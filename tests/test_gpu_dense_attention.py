@@ -315,7 +315,8 @@ MANY = [(7 * i) % 41 for i in range(300)]            # with some of no queries
 # by one long sequence and by more sequences than are counted
 SHARED_OUT = [([40], [5000], 2, 16), ([300] * 20, [300 + 9 * i for i in range(20)], 4, 16),
               ([1 + i % 60 for i in range(200)], [70 + i for i in range(200)], 4, 8), ([4000, 30], [4000, 5000], 1, 16),
-              (MANY, [m + 3 * (i % 30) for i, m in enumerate(MANY)], 2, 3)]
+              (MANY, [m + 3 * (i % 30) for i, m in enumerate(MANY)], 2, 3),
+              ([0] * 299 + [1], [0] * 299 + [2000], 1, 16), ([0] * 270 + [5] + [0] * 20 + [40], [7] * 270 + [9000] + [0] * 20 + [1100], 2, 4)]
 
 
 @pytest.mark.parametrize("lq,lk,kv,group", SHARED_OUT)
@@ -325,7 +326,8 @@ def test_prompt_however_its_runs_are_shared_out(lq, lk, kv, group):
 
 TREES = [([3000, 10, 500], [40, 64, 3], 1, 16), ([300 + 20 * i for i in range(20)], [1 + 3 * i for i in range(20)], 4, 16),
          ([10 * i for i in range(60)], [1 + i % 33 for i in range(60)], 2, 16), ([9000] + [100] * 40, [50] * 41, 2, 13),
-         ([5 * i for i in range(300)], [(5 * i) % 9 for i in range(300)], 1, 8), ([2 * i for i in range(300)], [1] * 300, 2, 16)]
+         ([5 * i for i in range(300)], [(5 * i) % 9 for i in range(300)], 1, 8), ([2 * i for i in range(300)], [1] * 300, 2, 16),
+         ([0] * 299 + [1500], [0] * 299 + [1], 1, 16), ([0] * 260 + [3000, 0, 500], [0] * 260 + [60, 0, 9], 2, 5)]
 
 
 @pytest.mark.parametrize("n_tokens,nodes,kv,group", TREES)
