@@ -4,12 +4,17 @@
 // What a page's entry in a table says is in qsa.h.  The bookkeeping reads and writes a few KB, so its time is a launch
 // and a chain of loads; what there is to choose is the number of steps in that chain.
 //  - fork, release: one CTA per row, references by atomics (integers: any order gives the same).
-//  - reserve: one CTA.  A thread, a warp or the whole CTA counts what a row lacks, by the entries it looks at; shared last pages are settled by rank among the rows that write
-//    (a row copies when more references than rows before it remain); one scan gives each row its part of the ascending list of
-//    free pages, from which its entries are filled.  The list is written no further than it is needed.
+//  - reserve: one CTA.  A thread, a warp or the whole CTA counts what a row lacks, by the entries it looks at; shared last
+//    pages are settled by rank among the rows that write (a row copies when more references than rows before it
+//    remain); one scan gives each row its part of the ascending list of free pages, from which its entries are filled.
+//    The list is written no further than it is needed.
 //  - compact: one CTA lists the free pages below the number of live ones and the live pages behind it, both in order,
 //    and pairs them; a second grid rewrites the table.
-//  - append: one CTA per (page touched, KV head): K rows as they are, V through shared memory into its dimension-major block.
+//  - append: a CTA looks a page up and takes some or all of its KV heads: K rows as they are, V through shared memory into its
+//    dimension-major block.  Bound by HBM: each row is read once and written once.
+// Measured: reserve and append for 8 sequences of up to 16 rows 11 us; for one of 131,072 rows, 4 KV heads, 97 us (537 MB, 5.5
+// TB/s; V transposed by words, by 16-bit elements 145); release, fork, reserve and the copied last pages for 8 sequences
+// forked into 64 14 us; the moves of 4,096 pages (4 KV heads, 55 % live) worked out and copied 52.5 us (of which 39 for the bytes).
 #include <cstdint>
 
 #include "launch.h"
@@ -21,9 +26,10 @@ namespace {
 
 constexpr int kRowThreads = 256;    // fork, release, append
 constexpr int kOneThreads = 1024;   // reserve, compact
-constexpr int kBatch = 4;           // table entries of a thread under way
-constexpr int kFew = 2;             // reserve: entries of a row that one thread looks at; a warp beyond,
-constexpr int kMany = 512;          // and the whole CTA beyond this
+constexpr int kBatch = 4;           // table entries of a thread under way (1: 2,049 of them 2 us more)
+// reserve: entries of a row that one thread looks at, that a warp does (a row each), and beyond them the whole CTA (row by row).  Us:
+constexpr int kFew = 2;             // 8 rows with up to 2 each 10.9, by warps 11.8; 8 a thread: 64 rows with 6 each 17.9 against 20, 8 with 2 11.1
+constexpr int kMany = 128;          // one row with 313: 20.4, by a warp 23.4; 8 rows with 47 by warps 17.7, by the CTA 26.4
 
 __device__ __forceinline__ void raise(uint32_t *flags, uint32_t bit) {
     if (flags) atomicOr(flags, bit);
@@ -611,7 +617,8 @@ qsa_status launch_pages_append(const PageTable &t, const PagesAppendArgs &a, cud
     long long units = a.n / 64 + 2ll * t.n_rows;
     if (units > a.n) units = a.n;
     cudaLaunchConfig_t cfg{};
-    // a CTA looks its page up once for all heads, unless the GPU would stay empty
+    // A CTA looks its page up once for all heads, unless the GPU would stay empty (us, so / a head each always: 4,000 rows of one
+    // token, 8 heads 93 / 223, 131,072 tokens in one row, 4 heads 97 / 95; all heads always: 8 rows of 16 tokens 11 / 15)
     const long long spread = 8ll * num_sms() / units;
     cfg.gridDim = dim3((unsigned)units, (unsigned)(spread < 1 ? 1 : spread < a.n_kv_heads ? spread : a.n_kv_heads));
     cfg.blockDim = dim3(kRowThreads);
