@@ -112,9 +112,16 @@ struct Piece {
     int q0, lq, k0, lk;
     int tok0;             // the tile's first token in its sequence
     int s0, s1, n;
+    int first;            // the step it begins with: first .. s1 - 1, then s0 .. first - 1
     int rows[2];          // rows of each stream
     int e[2];             // where each stream's steps end (<= s1; s0: none)
 };
+
+// The step in a piece's order that stands at place j of s0 .. s1 - 1.
+__device__ __forceinline__ int step_at(int j, int s0, int s1, int first) {
+    const int x = j + first - s0;
+    return x < s1 ? x : x - (s1 - s0);
+}
 
 struct Ctrl {
     uint64_t full[kSlots], empty[kSlots], clean[kSlots / 2], turn[2];
@@ -267,7 +274,8 @@ struct Walk {
     Seq<TREE> q;
     Rule rule;
     int s, g, t, tile;
-    long long at, x0, x1;   // kBorder: the beginning of the next run, and the CTA's share of all runs
+    long long at, x0, x1;   // kBorder: the beginning of the next run (from the last one down), and the CTA's share of all runs
+    int period, done;       // and steps of a share, steps taken
     int run, runs;          // kDealt: the next run, more runs than shares
     bool begun;
     Seq<TREE> mine;         // up to 32 sequences: a lane each
@@ -285,6 +293,7 @@ struct Walk {
         pc.s0 = from;
         pc.s1 = to;
         pc.n = n;
+        pc.first = from;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int first = pc.tok0 + (HALVES ? 0 : i * p.toks), toks = min(max(q.lq - first, 0), p.toks);
@@ -337,9 +346,10 @@ struct Walk {
             }
             return false;
         }
-        while (at < x1 && s < p.n_seqs) {
+        while (s >= 0) {
             const int n = q.steps(p, t), work = q.work(p, t);
             const long long from = at;
+            if (from + work <= x0) break;
             int a0 = 0, a1 = n;
             bool take = from >= x0;
             if (n > kWhole) {   // the step that begins nearest to a border; both sides of it compute the same
@@ -349,17 +359,26 @@ struct Walk {
                 take = a1 > a0;
             }
             take = fill(p, pc, a0, a1, n) && take;
-            at += work;
-            if (++t >= q.tiles) {
-                t = 0;
-                if (++g >= p.n_kv) {
-                    g = 0;
+            if (!TREE && take) {
+                // Runs of one KV head lie at all distances from one another, so that CTAs which began at their shares' beginnings
+                // would read all keys over and over from HBM.  Each takes the step that the others take now, modulo the
+                // share, if it has it (where both streams see all of the piece).
+                int r = (done - a0) % period;
+                if (r < 0) r += period;
+                if (a0 + r < a1 && (pc.e[0] == a1 || pc.e[0] == a0) && (pc.e[1] == a1 || pc.e[1] == a0)) pc.first = a0 + r;
+                done += a1 - a0 + kRunKeys / kKeys;
+            }
+            if (--t < 0) {
+                if (--g < 0) {
                     do {
-                        if (++s >= p.n_seqs) break;
+                        if (--s < 0) break;
                         q.load(p, s, false);
                     } while (q.tiles == 0);
+                    g = p.n_kv - 1;
                 }
+                t = q.tiles - 1;
             }
+            if (s >= 0) at -= q.work(p, t);
             if (take) return true;
         }
         return false;
@@ -473,36 +492,39 @@ __device__ void find_share(const Params &p, Ctrl &ct, Walk<TREE, HALVES> &w) {
     used = used < 1 ? 1 : used > p.shares ? p.shares : used;
     w.x0 = share < used ? mul_div(share, total, (unsigned)used) : total;
     w.x1 = share < used ? mul_div(share + 1, total, (unsigned)used) : total;
+    w.period = max((int)(total / used / kKeys), 1);
+    w.done = 0;
+    const long long x = w.x1 - 1;   // in the share's last run
     long long before = 0;
     w.at = w.x0;
-    w.s = p.n_seqs;
+    w.s = -1;
     w.g = w.t = 0;
     for (int s0 = 0; s0 < p.n_seqs && w.x0 < w.x1; s0 += 32) {
-        const long long x = s0 == 0 && p.n_seqs <= 32 && runs > p.shares ? first : weight(s0 + lane, false);
-        long long incl = x;
+        const long long y = s0 == 0 && p.n_seqs <= 32 && runs > p.shares ? first : weight(s0 + lane, false);
+        long long incl = y;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const long long y = __shfl_up_sync(~0u, incl, d);
-            if (lane >= d) incl += y;
+            const long long z = __shfl_up_sync(~0u, incl, d);
+            if (lane >= d) incl += z;
         }
-        const unsigned past = __ballot_sync(~0u, before + incl > w.x0);
+        const unsigned past = __ballot_sync(~0u, before + incl > x);
         if (past) {
             const int l = __ffs(past) - 1;
             w.s = s0 + l;
-            before += __shfl_sync(~0u, incl - x, l);
+            before += __shfl_sync(~0u, incl - y, l);
             break;
         }
         before += __shfl_sync(~0u, incl, 31);
     }
-    if (w.s < p.n_seqs) {
+    if (w.s >= 0) {
         q.take(q, w.s & 31);
-        const long long per = q.cum(p, q.tiles), in_seq = w.x0 - before;
+        const long long per = q.cum(p, q.tiles), in_seq = x - before;
         w.g = in_seq < (1ll << 31) && per < (1ll << 31) ? (int)((unsigned)in_seq / (unsigned)per) : (int)(in_seq / per);
         before += w.g * per;
-        int lo = 0, hi = q.tiles;   // cum(lo) <= x0 - before < cum(hi)
+        int lo = 0, hi = q.tiles;   // cum(lo) <= x - before < cum(hi)
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32, mid = min(lo + (lane + 1) * step, hi);
-            const unsigned over = __ballot_sync(~0u, q.cum(p, mid) > w.x0 - before);   // lane 31 reaches hi
+            const unsigned over = __ballot_sync(~0u, q.cum(p, mid) > x - before);   // lane 31 reaches hi
             const int l = __ffs(over) - 1;
             const int new_hi = min(lo + (l + 1) * step, hi);
             lo += l * step;
@@ -853,7 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int i = chunk * 32 + lane;
                 return i < nb ? p.table[(size_t)pc.s * p.table_stride + i] : -1;
             };
-            for (int j = pc.s0; ok && j < pc.s1; ++j, ++step) {
+            for (int j0 = pc.s0; ok && j0 < pc.s1; ++j0, ++step) {
+                const int j = TREE ? j0 : step_at(j0, pc.s0, pc.s1, pc.first);
                 const bool paged = TREE && j < pc.n - 1;
                 int page[2] = {0, 0};
                 if (paged) {
@@ -903,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tma_load_2d(to + h * 16384, &tm_vc, bar, 0, page[h] * 128);
                         }
                     }
-                    if (kv == 0 && j == pc.s0) load_q();   // behind the first K: the last piece may still read Q
+                    if (kv == 0 && j0 == pc.s0) load_q();   // behind the first K: the last piece may still read Q
                     if (!ok) {
                         ++it;
                         break;
@@ -944,7 +967,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok) {
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
             // a stream that is done with its steps still takes its turns and gives the other one's slots back
-            const int s0 = uniform(pp->s0), s1 = uniform(pp->s1), e = uniform(pp->e[st]), n = uniform(pp->n), lk = uniform(pp->lk);
+            const int s0 = uniform(pp->s0), s1 = uniform(pp->s1), e = uniform(pp->e[st]), n = uniform(pp->n), lk = uniform(pp->lk),
+                      first = uniform(pp->first);
             const int low = TREE ? lk : uniform(Seq<TREE>::keys_of(pp->lq, lk, pp->tok0));
             if (s1 > s0) {
                 ok = slot_full(it) && (e <= s0 || wait_all(&ct.qfull[st], nq++ & 1u, abort_flag)) && my_turn();
@@ -962,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int vslot = (it + 1) % kSlots;
                 const bool paged = TREE && j < n - 1, more = j + 1 < s1;
                 if (!(ok = slot_full(it + 1))) break;
-                if ((j + 1) * kKeys > low || (TREE && !paged)) {
+                if (((TREE ? j : step_at(j, s0, s1, first)) + 1) * kKeys > low || (TREE && !paged)) {
                     const int i = vslot >> 1;   // warp 3 clears what must not be read
                     if (!(ok = wait_all(&ct.clean[i], cleaned >> i & 1u, abort_flag))) break;
                     cleaned ^= 1u << i;
@@ -1018,12 +1042,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int base = 0;
         while (ok) {
             if (!(ok = pieces.next(abort_flag, pp)) || pp->stop) break;
-            const int s0 = pp->s0, s1 = pp->s1, n = pp->n, lq = pp->lq, lk = pp->lk;
+            const int s0 = pp->s0, s1 = pp->s1, n = pp->n, lq = pp->lq, lk = pp->lk, first = pp->first;
             const int low = TREE ? 0 : Seq<TREE>::keys_of(lq, lk, pp->tok0);
             const int high = TREE ? lq : Seq<TREE>::keys_of(lq, lk, min(pp->tok0 + p.tile, lq) - 1);
-            for (int j = s0; ok && j < s1; ++j) {
+            for (int j0 = s0; ok && j0 < s1; ++j0) {
+                const int j = TREE ? j0 : step_at(j0, s0, s1, first);
                 const bool paged = TREE && j < n - 1;
-                const int vit = base + 2 * (j - s0) + 1, vslot = vit % kSlots;
+                const int vit = base + 2 * (j0 - s0) + 1, vslot = vit % kSlots;
                 if (!(ok = wait_all(&ct.full[vslot], (uint32_t)(vit / kSlots) & 1u, abort_flag))) break;
                 // only a run's last steps hold such places
                 if (TREE ? paged && (j + 1) * kKeys <= lk : (j + 1) * kKeys <= low) {
@@ -1119,16 +1144,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 low = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + first_tok, pp->lq - 1));
             }
             float m = -INFINITY, l = 0.0f;
-            for (int j = s0; j < end; ++j) {
+            for (int j0 = s0; j0 < end; ++j0) {
                 ok = ok && wait_all(&ct.sfull[st], ns++ & 1u, abort_flag);
                 if (!HALVES && !ok) break;
                 tc_fence_after();
+                const int j = TREE ? j0 : step_at(j0, s0, pp->s1, pp->first);
                 // which keys this row sees, 32 a word; all of them in most steps
                 const bool paged = TREE && j < n - 1;
                 int valid[2] = {0, 0};
                 if (paged) {
-                    valid[0] = ct.info[(step0 + j - s0) % kInfo][0];
-                    valid[1] = ct.info[(step0 + j - s0) % kInfo][1];
+                    valid[0] = ct.info[(step0 + j0 - s0) % kInfo][0];
+                    valid[1] = ct.info[(step0 + j0 - s0) % kInfo][1];
                 }
                 const bool some = TREE ? (HALVES ? valid[st] : min(valid[0], valid[1])) < 64 : (j + 1) * kKeys > low;
                 auto sees = [&](int q) -> uint32_t {
@@ -1139,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // the row's reference, given the step's largest logit
                 auto settle = [&](float now) {
-                    if (j == s0) {
+                    if (j0 == s0) {
                         m = now;
                         return;
                     }
