@@ -131,7 +131,7 @@ struct Ctrl {
     Piece pieces[kPieces];
     uint32_t tmem;
     int abort;
-    int info[kInfo][2];   // valid tokens in each page of a step
+    int2 info[kInfo];     // valid tokens in each page of a step
     float2 other[kRows];  // HALVES: stream 1's (m, l)
     int runs[kTable + 1]; // runs of the sequences before each one
     int dealing;          // the CTAs take runs as they come free
@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             page[h] += pc.g * p.n_pages;
                         }
-                        if (lane == 0) ct.info[step % kInfo][h] = valid;
+                        if (lane == 0) (h ? ct.info[step % kInfo].y : ct.info[step % kInfo].x) = valid;
                     }
                 }
                 for (int kv = 0; kv < 2; ++kv, ++it) {
@@ -1144,17 +1144,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 low = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + first_tok, pp->lq - 1));
             }
             float m = -INFINITY, l = 0.0f;
-            for (int j0 = s0; j0 < end; ++j0) {
+            int place = step0, j = TREE ? s0 : pp->first;   // the step's place among all of the CTA's, and the step
+#pragma unroll 1
+            for (int left = end - s0; left > 0; --left, ++place, j = TREE || j + 1 < pp->s1 ? j + 1 : s0) {
                 ok = ok && wait_all(&ct.sfull[st], ns++ & 1u, abort_flag);
                 if (!HALVES && !ok) break;
                 tc_fence_after();
-                const int j = TREE ? j0 : step_at(j0, s0, pp->s1, pp->first);
                 // which keys this row sees, 32 a word; all of them in most steps
                 const bool paged = TREE && j < n - 1;
                 int valid[2] = {0, 0};
                 if (paged) {
-                    valid[0] = ct.info[(step0 + j0 - s0) % kInfo][0];
-                    valid[1] = ct.info[(step0 + j0 - s0) % kInfo][1];
+                    const int2 x = ct.info[place % kInfo];
+                    valid[0] = x.x;
+                    valid[1] = x.y;
                 }
                 const bool some = TREE ? (HALVES ? valid[st] : min(valid[0], valid[1])) < 64 : (j + 1) * kKeys > low;
                 auto sees = [&](int q) -> uint32_t {
@@ -1165,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // the row's reference, given the step's largest logit
                 auto settle = [&](float now) {
-                    if (j0 == s0) {
+                    if (left == end - s0) {
                         m = now;
                         return;
                     }

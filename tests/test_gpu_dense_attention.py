@@ -316,6 +316,7 @@ MANY = [(7 * i) % 41 for i in range(300)]            # with some of no queries
 SHARED_OUT = [([40], [5000], 2, 16), ([300] * 20, [300 + 9 * i for i in range(20)], 4, 16),
               ([1 + i % 60 for i in range(200)], [70 + i for i in range(200)], 4, 8), ([4000, 30], [4000, 5000], 1, 16),
               (MANY, [m + 3 * (i % 30) for i, m in enumerate(MANY)], 2, 3),
+              ([256], [8000], 4, 16), ([70, 250], [9000, 8200], 4, 15),
               ([0] * 299 + [1], [0] * 299 + [2000], 1, 16), ([0] * 270 + [5] + [0] * 20 + [40], [7] * 270 + [9000] + [0] * 20 + [1100], 2, 4)]
 
 
@@ -424,3 +425,21 @@ def test_a_large_tree_is_not_touched_by_what_it_does_not_see(group, long):
         assert torch.equal(out[~touched], good[~touched]) and torch.equal(ls[~touched], lse[~touched])
         assert not torch.isfinite(out[touched]).any() and torch.isnan(ls[first + 33]).all()
         assert qsa.read_flags(ws) == 0
+
+
+def test_a_chunk_cut_in_pieces_is_not_touched_by_what_it_does_not_see():
+    """A run's last, masked step need not be the last one that its CTA works on."""
+    lq, lk, kv, group = 256, 8000, 4, 16
+    q, k, v = normal(1, lq, kv * group, 128, dt=BF16), normal(2, lk, kv, 128, dt=BF16), normal(3, lk, kv, 128, dt=BF16)
+    good, lse, _ = _prompt(q, k, v, [lq], [lk])
+    for row in (1, 100, 255):                    # of the last 256 keys, seen from this query on
+        for bad in (float("nan"), -float("inf")):
+            k2, v2 = k.clone(), v.clone()
+            k2[lk - lq + row + 1:] = bad
+            v2[lk - lq + row, 1] = bad
+            out, ls, ws = _prompt(q, k2, v2, [lq], [lk])
+            assert torch.equal(out[:row], good[:row]) and torch.equal(ls[:row], lse[:row])
+            other = [h for h in range(kv * group) if h // group != 1]
+            assert torch.equal(out[row][other], good[row][other]) and torch.equal(ls[row], lse[row])
+            assert not torch.isfinite(out[row, group:2 * group]).any()
+            assert qsa.read_flags(ws) == 0
