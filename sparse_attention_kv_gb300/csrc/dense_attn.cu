@@ -1119,7 +1119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + kColS + st * 128, tO = tmem + lanes + kColO + st * 128;
-        const float c = p.scale_log2, rise = fminf(kRise / c, 1e38f);
         const int first_tok = HALVES ? 0 : st * p.toks;                     // of the stream, in a tile
         const int my_tok = first_tok + (int)(r * p.by_group >> 16);        // this row's
         constexpr int kCols = HALVES ? 64 : 128;                           // keys of a stream in a step
@@ -1133,20 +1132,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (true) {
             ok = pieces.next(abort_flag, pp) && ok;
             if ((HALVES ? any_of(3, 256, !ok) : !ok) || pp->stop) break;
-            const int s0 = pp->s0, end = pp->e[st], n = pp->n;
+            const int n = TREE ? pp->n : 0;
             // what this row sees
-            int lim = 0, low = 0;                       // prompts: keys of this row, of the stream's first one
+            int low = 0;                                // prompts: keys of the stream's first row
             unsigned long long nodes = 0ull;            // trees: of the drafts
             if constexpr (TREE) {
-                if (end == n && end > s0) nodes = ancestors(p, pp->q0, pp->lq, min(pp->tok0 + my_tok, pp->lq - 1));
+                if (pp->e[st] == n && n > pp->s0) nodes = ancestors(p, pp->q0, pp->lq, min(pp->tok0 + my_tok, pp->lq - 1));
             } else {
-                lim = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + my_tok, pp->lq - 1));
                 low = Seq<TREE>::keys_of(pp->lq, pp->lk, min(pp->tok0 + first_tok, pp->lq - 1));
             }
+            // Prompts: keys that this row sees.  What only half-seen steps and the end need is taken from the piece again there: the
+            // steps that are seen whole fill the registers (16,384 tokens 2.43 -> 2.32 ms).
+            auto limit = [&]() { return Seq<TREE>::keys_of(pp->lq, pp->lk, pp->tok0 + my_tok); };
             float m = -INFINITY, l = 0.0f;
-            int place = step0, j = TREE ? s0 : pp->first;   // the step's place among all of the CTA's, and the step
+            int place = step0, j = TREE ? pp->s0 : pp->first;   // the step's place among all of the CTA's, and the step
 #pragma unroll 1
-            for (int left = end - s0; left > 0; --left, ++place, j = TREE || j + 1 < pp->s1 ? j + 1 : s0) {
+            for (int left = pp->e[st] - pp->s0; left > 0; --left, ++place, j = TREE || j + 1 < pp->s1 ? j + 1 : pp->s0) {
                 ok = ok && wait_all(&ct.sfull[st], ns++ & 1u, abort_flag);
                 if (!HALVES && !ok) break;
                 tc_fence_after();
@@ -1159,6 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     valid[1] = x.y;
                 }
                 const bool some = TREE ? (HALVES ? valid[st] : min(valid[0], valid[1])) < 64 : (j + 1) * kKeys > low;
+                int lim = 0;
                 auto sees = [&](int q) -> uint32_t {
                     const int at = (HALVES ? 64 * st : 0) + 32 * q;   // the word's first key in the step
                     if (TREE && !paged) return at == 0 ? (uint32_t)nodes : at == 32 ? (uint32_t)(nodes >> 32) : 0u;
@@ -1167,14 +1169,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // the row's reference, given the step's largest logit
                 auto settle = [&](float now) {
-                    if (left == end - s0) {
-                        m = now;
+                    const bool risen = (now - m) * p.scale_log2 > kRise;   // from nothing seen, by anything
+                    if (!__any_sync(~0u, risen && m > -INFINITY)) {        // O is not there yet, or 0, where nothing was seen
+                        if (risen) m = now;
                         return;
                     }
-                    const bool risen = now > m + rise;
-                    if (!__any_sync(~0u, risen)) return;
                     // S of this step is complete, so every product before it is: O may be scaled in place
-                    const float f = risen ? ex2((m - now) * c) : 1.0f;
+                    const float f = risen ? ex2((m - now) * p.scale_log2) : 1.0f;
                     if (risen) m = now;
                     l *= f;
 #pragma unroll 1
@@ -1216,25 +1217,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top[(i >> 1) & 3] = fmaxf(top[(i >> 1) & 3], fmaxf(__uint_as_float(v[i >> 4][i & 15]),
                                                                            __uint_as_float(v[i >> 4][(i & 15) + 1])));
                     settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const float c = p.scale_log2, mc = m == -INFINITY ? 0.0f : m * c;
                     const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
                         for (int q = 0; q < kCols / 64; ++q) {   // 32 keys
-                            uint32_t w[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int k = h * (kCols / 2) + 32 * q + 2 * i;
-                                w[i] = weigh(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1]), c2, nm2, i);
+                            for (int i = 0; i < 16; ++i) {   // in place: pair i over value i
+                                const int k = h * (kCols / 2) + 32 * q + 2 * i, to = h * (kCols / 2) + 32 * q + i;
+                                v[to >> 4][to & 15] = weigh(__uint_as_float(v[k >> 4][k & 15]), __uint_as_float(v[k >> 4][(k & 15) + 1]), c2, nm2, i);
                             }
-                            tmem_st16(tS + h * (kCols / 4) + 16 * q, w);
+                            tmem_st16(tS + h * (kCols / 4) + 16 * q, v[(h * (kCols / 2) + 32 * q) >> 4]);
                         }
                         pass_on(h);
                     }
                 } else {
                     // 32 keys a round, read twice, in little code: short runs spend their time in steps like this one, and on
                     // fetching instructions
+                    if constexpr (!TREE) lim = limit();
                     auto logits_of = [&](int q, uint32_t (&x)[2][16]) {
                         tmem_ld16_nowait(tS + 32 * q, x[0]);
                         tmem_ld16_nowait(tS + 32 * q + 16, x[1]);
@@ -1255,7 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 16; ++i) now = fmaxf(now, fmaxf(__uint_as_float(x[0][i]), __uint_as_float(x[1][i])));
                     }
                     settle(now);
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const float c = p.scale_log2, mc = m == -INFINITY ? 0.0f : m * c;
                     const f32x2 c2 = pack2(c, c), nm2 = pack2(-mc, -mc);
 #pragma unroll 1
                     for (int q = 0; q < kCols / 32; ++q) {
@@ -1275,21 +1276,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!HALVES && !ok) break;
             const int rows = pp->rows[st];
-            if (HALVES || rows > (warp & 3) * 32 || end > s0) {
-                if (end > s0) {
+            const bool have = pp->e[st] > pp->s0;
+            if (HALVES || rows > (warp & 3) * 32 || have) {
+                if (have) {
                     ok = ok && wait_all(&ct.ofull[st], no++ & 1u, abort_flag);
                     if (!HALVES && !ok) break;
                     tc_fence_after();
                 }
-                finish<F16, TREE, HALVES>(p, ct, *pp, end > s0, tO, smem + kOffStage + (warp - 4) * kStageBytes,
-                                          reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, lim, nodes, rows);
+                finish<F16, TREE, HALVES>(p, ct, *pp, have, tO, smem + kOffStage + (warp - 4) * kStageBytes,
+                                          reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, TREE ? 0 : limit(), nodes, rows);
                 tc_fence_before();
-                if (HALVES && st == 0 && end > s0) {
+                if (HALVES && st == 0 && have) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ct.qempty[1]);
                 }
             }
-            step0 += pp->s1 - s0;
+            step0 += pp->s1 - pp->s0;
             __syncwarp();
             if (lane == 0) pieces.done();
             else ++pieces.no;
