@@ -25,16 +25,16 @@
 // lies past the last row's view and any value that is not finite; the latter is added at the end to the rows that see it.
 //
 // What bounds it.  Prompts: the tensor cores, and the power limit when calls last.  A step of 256 rows and 128 keys is 2,048
-// cycles of MMA; it takes 2,250 to 2,450 (1.17-1.25 us at 1.95 GHz), the rest being the chain P ready -> P V -> S -> softmax
-// (0.5 us) of a stream where it does not fit beside the other one's products.  256 queries x 64 heads behind 130,816 tokens: 0.59 ms
-// in a burst (1.85 PFLOP/s), 0.65 sustained; one prompt of 16,384 tokens, 64 heads in 4 groups: 2.3 (1.91) and 2.5 ms (a large
+// cycles of MMA; it takes 2,150 to 2,350 (1.1-1.2 us at 1.95 GHz), the rest being the chain P ready -> P V -> S -> softmax
+// (0.5 us) of a stream where it does not fit beside the other one's products.  256 queries x 64 heads behind 130,816 tokens: 0.56 ms
+// in a burst (1.96 PFLOP/s), 0.64 sustained; one prompt of 16,384 tokens, 64 heads in 4 groups: 2.18 (2.01) and 2.5 ms (a large
 // library product 1.88 and 1.72 PFLOP/s here).  Decode: HBM; one query at 258,000 tokens, 64 heads in 4 groups: 94-98 us, of which
 // 88 the main kernel (528 MB, 6.0 TB/s).  Short calls: about 13 us for a CTA's first piece (2 to find it, 2 until its first
 // product, 2.2 for its end), 4.4 us for a further one of a single step.
 // Measured on the way (16,384 tokens, ms): one warp issuing both streams, descriptors made in divergent code 5.19 (an MMA then
 // takes about 100 cycles to issue); Q by TMA, outputs in whole rows 3.81; two threads a row, two issuing warps in turn,
 // descriptors in uniform registers 2.86; a thread a row, weights passed on in two parts 2.70; steps that are not seen whole in
-// rolled loops (instruction fetches) 2.55; runs dealt out 2.48.
+// rolled loops (instruction fetches) 2.55; runs dealt out 2.48; fewer registers held over a step 2.30.
 //
 // Every wait is bounded; on expiry the CTA raises QSA_FLAG_WAIT_TIMEOUT, drains its copies and MMAs, frees its tensor memory
 // and exits.
