@@ -72,6 +72,7 @@ constexpr int kRunKeys = 512;   // what a run's beginning and end cost, in keys 
 constexpr int kTable = 256;     // sequences whose runs are counted in shared memory
 constexpr int kShortRun = 16;   // steps of runs that are dealt out however few the shares hold (0: 1,024 tokens 29 / 35; 64: no better)
 constexpr int kMinShare = 384;  // least work, in keys, of a share: no share in the middle of a run is without a step
+constexpr int kShortKeys = 2048; // a sequence's keys up to which rows leave by TMA: see launch()
 constexpr int kManyParts = 8;   // parts of a run that combine_kernel shares out to its warps (38 parts 94 / 102; 64 sequences' two or three 360 / 348)
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
@@ -644,12 +645,45 @@ __device__ __forceinline__ void store4(const Params &p, size_t at, float a, floa
     else *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) = make_uint2(pack16<F16>(a, b), pack16<F16>(c, d));
 }
 
+// A warp's 32 rows of out, normalised, by TMA: 32 dimensions a tile, from two buffers of the stage in turn.
+template <bool F16>
+__device__ __forceinline__ void tiles_out(uint32_t tO, uint8_t *stage, float inv, const CUtensorMap *tm_o, int head, int token) {
+    int lane;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));   // so that nothing that follows from it is held over the steps
+#pragma unroll 1
+    for (int d = 0; d < 128; d += 32) {
+        uint32_t o[2][16];
+        tmem_ld16_nowait(tO + d, o[0]);
+        tmem_ld16_nowait(tO + d + 16, o[1]);
+        bulk_wait_read<1>();   // the buffer that this round fills
+        __syncwarp();
+        tmem_wait_ld();
+        reg_fence(o[0]);
+        reg_fence(o[1]);
+        uint8_t *buffer = stage + (d & 32) * 64;
+        auto pair = [&](int i) {
+            return pack16<F16>(__uint_as_float(o[i >> 4][i & 15]) * inv, __uint_as_float(o[i >> 4][(i & 15) + 1]) * inv);
+        };
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)   // the 64-byte swizzle
+            *reinterpret_cast<uint4 *>(buffer + lane * 64 + (((i >> 3) ^ (lane >> 1 & 3)) << 4)) =
+                make_uint4(pair(i), pair(i + 2), pair(i + 4), pair(i + 6));
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(tm_o, buffer, d, head, token);
+            bulk_commit();
+        }
+    }
+}
+
 // The end of a piece for a warp's 32 rows: the output normalised, through `stage` so that a row's bytes are written
 // together, or the partial as it is.  have: there is an O in tensor memory.
 // HALVES: stream 1 hands what it has to stream 0 through `box` (32 KB), and stream 0 goes on.
-template <bool F16, bool TREE, bool HALVES>
+// TILES: rows that are all there leave by TMA.
+template <bool F16, bool TREE, bool HALVES, bool TILES>
 __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &pc, bool have, uint32_t tO, uint8_t *stage, float4 *box,
-                                       float m, float l, int lim, unsigned long long nodes, int rows) {
+                                       float m, float l, int lim, unsigned long long nodes, int rows, const CUtensorMap *tm_o) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, st = (warp - 4) >> 2, G = p.group;
     const int r = (warp & 3) * 32 + lane;
     const bool whole = pc.s0 == 0 && pc.s1 == pc.n, mine = r < rows, fix = pc.bad != 0;
@@ -679,6 +713,15 @@ __device__ __forceinline__ void finish(const Params &p, Ctrl &ct, const Piece &p
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if constexpr (TILES) {
+        if (whole && !fix && have && rows >= (warp & 3) * 32 + 32) {
+            tiles_out<F16>(tO, stage, inv, tm_o, pc.g * G, pc.q0 + pc.tok0 + st * p.toks + (int)((warp & 3) * 32 * p.by_group >> 16));
+            if (p.lse) p.lse[output(r)] = l == 0.0f ? -INFINITY : m * p.scale + logf(l);
+            return;
+        }
+        bulk_wait_read<0>();
+        __syncwarp();
+    }
     uint8_t *line = stage + lane * 128;
     const int unit = p.out_f32 ? 4 : 2;
     // 32 dimensions a round: in 16 bits two rounds make 128 bytes of each row, in 32 bits one
@@ -779,11 +822,12 @@ struct Pieces {
 };
 
 // HALVES: every tile has at most one stream's rows; both streams take them, each with half of a step's keys.
-template <bool F16, bool TREE, bool HALVES>
+template <bool F16, bool TREE, bool HALVES, bool TILES>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kc,
-                 const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ Params p) {
+                 const __grid_constant__ CUtensorMap tm_vc, const __grid_constant__ CUtensorMap tm_o,
+                 const __grid_constant__ Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem + kOffRing;
     Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + kOffCtrl);
@@ -814,8 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ct.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 0 && lane < 5) {
-        const CUtensorMap *m = lane == 0 ? &tm_q : lane == 1 ? &tm_k : lane == 2 ? &tm_v : lane == 3 ? &tm_kc : &tm_vc;
+    if (warp == 0 && lane < (TILES ? 6 : 5)) {
+        const CUtensorMap *m = lane == 0 ? &tm_q : lane == 1 ? &tm_k : lane == 2 ? &tm_v : lane == 3 ? &tm_kc : lane == 4 ? &tm_vc : &tm_o;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
     wait_prior_grid();   // nothing the caller wrote is read, and no tensor memory taken, before this
@@ -1283,8 +1327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!HALVES && !ok) break;
                     tc_fence_after();
                 }
-                finish<F16, TREE, HALVES>(p, ct, *pp, have, tO, smem + kOffStage + (warp - 4) * kStageBytes,
-                                          reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, TREE ? 0 : limit(), nodes, rows);
+                finish<F16, TREE, HALVES, TILES>(p, ct, *pp, have, tO, smem + kOffStage + (warp - 4) * kStageBytes,
+                                          reinterpret_cast<float4 *>(smem + kOffQ + kQBytes), m, l, TREE ? 0 : limit(), nodes, rows, &tm_o);
                 tc_fence_before();
                 if (HALVES && st == 0 && have) {
                     __syncwarp();
@@ -1296,6 +1340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) pieces.done();
             else ++pieces.no;
         }
+        if (TILES) bulk_wait();
         tc_fence_before();
     }
     __syncthreads();
@@ -1442,8 +1487,8 @@ int rows_cap(int tokens, int group) {
     return tokens > kRows / group ? 2 * kRows : (tokens * group + 31) / 32 * 32;
 }
 
-template <bool F16, bool TREE, bool HALVES>
-qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, int most_steps, cudaStream_t s) {
+template <bool F16, bool TREE, bool HALVES, bool TILES>
+qsa_status launch_typed(const CUtensorMap (&m)[6], const Params &p, int grid, int most_steps, cudaStream_t s) {
     static std::mutex mu;
     static bool opted_in[64] = {false};
     int dev = 0;
@@ -1453,14 +1498,14 @@ qsa_status launch_typed(const CUtensorMap (&m)[5], const Params &p, int grid, in
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!opted_in[dev]) {
-            st = check_cuda(cudaFuncSetAttribute(dense_kernel<F16, TREE, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+            st = check_cuda(cudaFuncSetAttribute(dense_kernel<F16, TREE, HALVES, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
                             "cudaFuncSetAttribute(dense attention)");
             if (st != QSA_OK) return st;
             opted_in[dev] = true;
         }
     }
-    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE, HALVES>, grid, kThreads, kSmem, s, m[0], m[1], m[2], m[3],
-                          m[4], p);
+    st = launch_dependent("dense_kernel launch", dense_kernel<F16, TREE, HALVES, TILES>, grid, kThreads, kSmem, s, m[0], m[1], m[2],
+                          m[3], m[4], m[5], p);
     if (st != QSA_OK || most_steps <= kWhole) return st;
     const long long runs = (long long)p.n_seqs * p.n_kv, parts = std::min<long long>(p.shares / runs, most_steps / kLeast);
     const bool many = p.rows_cap <= 64 && parts >= kManyParts;
@@ -1522,7 +1567,7 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
     const int grid = p.shares * p.row_tiles;
     // of a run, as far as the sizes tell
     const int most_steps = ((TREE ? 64 * a.table.max_pages : a.total_k) + kKeys - 1) / kKeys + (TREE ? 1 : 0);
-    CUtensorMap m[5];
+    CUtensorMap m[6];
     const Rows16 &k = a.total_k > 0 ? a.k : a.q, &v = a.total_k > 0 ? a.v : a.q;   // without keys nothing is loaded
     const int rows = a.total_k > 0 ? a.total_k : 1, heads = a.total_k > 0 ? a.n_kv_heads : 1;
     qsa_status st;
@@ -1532,15 +1577,30 @@ qsa_status launch(const DenseArgs &a, cudaStream_t s) {
         return st;
     m[3] = m[1];
     m[4] = m[2];
+    m[5] = m[0];
     if (TREE) {
         const uint64_t pages = (uint64_t)a.n_kv_heads * a.table.n_pages;
         if ((st = get_map(&m[3], a.kcache, 2, 128, pages * 64, 64)) != QSA_OK ||
             (st = get_map(&m[4], a.vcache_t, 2, 64, pages * 128, 128)) != QSA_OK)
             return st;
     }
+    const bool f16 = a.dt == QSA_F16;
     if (halves)
-        return a.dt == QSA_F16 ? launch_typed<true, TREE, true>(m, p, grid, most_steps, s) : launch_typed<false, TREE, true>(m, p, grid, most_steps, s);
-    return a.dt == QSA_F16 ? launch_typed<true, TREE, false>(m, p, grid, most_steps, s) : launch_typed<false, TREE, false>(m, p, grid, most_steps, s);
+        return f16 ? launch_typed<true, TREE, true, false>(m, p, grid, most_steps, s)
+                   : launch_typed<false, TREE, true, false>(m, p, grid, most_steps, s);
+    if constexpr (!TREE) {
+        // 16-bit rows of whole tokens a warp may leave by TMA: the lanes that read the stage back and store it take issue slots that the
+        // other warps need, but the branch costs the steps registers (us, by TMA / not: 20 prompts of 300 tokens 75 / 86, one of
+        // 1,024 25.8 / 26.6, 8 of 2,000 370 / 377, one of 4,096 170 / 168.5, of 8,192 602 / 587, 256 queries behind 130,816 591 / 575)
+        if (!p.out_f32 && 32 % p.group == 0 && a.total_k <= kShortKeys * (long long)a.n_seqs) {
+            const Rows16 out{a.out, (int64_t)a.n_heads * 128, 128};
+            if ((st = get_rows_map(&m[5], out, a.total_q, a.n_heads, true, 32 / p.group, p.group, 32)) != QSA_OK) return st;
+            return f16 ? launch_typed<true, false, false, true>(m, p, grid, most_steps, s)
+                       : launch_typed<false, false, false, true>(m, p, grid, most_steps, s);
+        }
+    }
+    return f16 ? launch_typed<true, TREE, false, false>(m, p, grid, most_steps, s)
+               : launch_typed<false, TREE, false, false>(m, p, grid, most_steps, s);
 }
 
 }  // namespace

@@ -258,7 +258,7 @@ struct PagesAppendArgs {
     void *kcache, *vcache_t;
 };
 qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads, bool heads_inner, uint32_t box_tokens,
-                        uint32_t box_heads);
+                        uint32_t box_heads, uint32_t box_dims = 64);
 qsa_status launch_pages_append(const PageTable &t, const PagesAppendArgs &a, cudaStream_t s);
 
 // Dense attention: causal over packed rows, or a tree of drafts over pages.

@@ -86,14 +86,14 @@ qsa_status get_map(CUtensorMap *out, const void *ptr, int esize, uint32_t inner,
 }
 
 // Rows of 128 16-bit values with any strides, as [heads][tokens][128] or, heads_inner, [tokens][heads][128]: boxes of
-// 64 values x box_tokens x box_heads.  Not cached: a call's rows are new.
+// 64 (or 32) values x box_tokens x box_heads, swizzled over the box's row.  Not cached: a call's rows are new.
 qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads, bool heads_inner, uint32_t box_tokens,
-                        uint32_t box_heads) {
+                        uint32_t box_heads, uint32_t box_dims) {
     auto fn = encode_fn();
     if (!fn) return fail(QSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const int t = heads_inner ? 2 : 1, h = 3 - t;
     cuuint64_t dims[3] = {128, 0, 0}, strides[2];
-    cuuint32_t box[3] = {64, 0, 0};
+    cuuint32_t box[3] = {box_dims, 0, 0};
     const cuuint32_t estr[3] = {1, 1, 1};
     dims[t] = (cuuint64_t)tokens;
     dims[h] = (cuuint64_t)heads;
@@ -103,8 +103,8 @@ qsa_status get_rows_map(CUtensorMap *out, const Rows16 &x, int tokens, int heads
     strides[t - 1] = tokens > 1 ? (cuuint64_t)x.token * 2 : 256;
     strides[h - 1] = heads > 1 ? (cuuint64_t)x.head * 2 : 256;
     const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(x.p), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, box_dims == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     return QSA_OK;
 }
