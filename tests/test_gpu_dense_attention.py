@@ -115,6 +115,37 @@ def test_prompt_unseen_rows_do_not_touch_it(group):
             assert torch.isnan(out[70 + 120:]).all() and torch.isnan(ls[70 + 120:]).all()
 
 
+@pytest.mark.parametrize("kv,group", [(1, 16), (2, 8), (3, 1), (1, 4), (2, 2)])
+def test_prompt_writes_no_row_beyond_its_sequences(kv, group):
+    """Sequences that end within a tile, a warp's rows, or with them; rows between and behind them stay as they were."""
+    toks = 128 // group
+    lens, gaps = [toks, 2 * toks, toks // 4, toks + 3 * toks // 4, 2 * toks + 1, 3], [0, 5, 1, 2, 7, 1, 9]
+    total = sum(lens) + sum(gaps)
+    q, k, v = normal(1, total, kv * group, 128, dt=F16), *(normal(2 + i, sum(lens), kv, 128, dt=F16) for i in range(2))
+    full, fl, _ = _prompt(q[:sum(lens)], k, v, lens, lens)
+    # the same sequences behind empty ones that own the gaps (no keys: rows of zeros), and with the gaps in no sequence
+    at = a = 0
+    qq = torch.empty_like(q)
+    cq, ck, mine = [0], [0], torch.zeros(total, dtype=torch.bool)
+    for gap, m in zip(gaps, lens):
+        cq.append(at + gap), ck.append(ck[-1])
+        at += gap
+        qq[at:at + m] = q[a:a + m]
+        mine[at:at + m] = True
+        cq.append(at + m), ck.append(ck[-1] + m)
+        at, a = at + m, a + m
+    out, ls, ws = _prompt(qq, k, v, None, None, cu_q=i32(cq), cu_k=i32(ck))
+    assert torch.equal(out[mine], full) and torch.equal(ls[mine], fl)
+    inside = ~mine
+    inside[at:] = False
+    assert (out[inside] == 0).all() and torch.isnan(out[at:]).all() and torch.isnan(ls[at:]).all()
+    assert qsa.read_flags(ws) == 0
+    for n, m in ((0, lens[0]), (sum(lens[:2]), lens[2])):         # one sequence in a larger output
+        out, ls, _ = _prompt(q, k, v, None, None, cu_q=i32([n, n + m]), cu_k=i32([n, n + m]))
+        check_attention(out[n:n + m], ls[n:n + m], paged.prompt(q[n:n + m].double(), k[n:n + m].double(), v[n:n + m].double(), [m], [m], SCALE), F16)
+        assert torch.isnan(out[:n]).all() and torch.isnan(out[n + m:]).all()
+
+
 def test_prompt_bad_ranges_are_flagged():
     q, k, v = normal(1, 40, 4, 128, dt=BF16), normal(2, 40, 2, 128, dt=BF16), normal(3, 40, 2, 128, dt=BF16)
     good, lse, _ = _prompt(q, k, v, [40], [40])
