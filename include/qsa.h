@@ -559,7 +559,7 @@ qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const 
  *
  * all on the DEVICE.  A step of generation: qsa_pages_reserve makes room behind the sequences,
  * qsa_pages_copy copies the pages that were shared and are about to be written,
- * qsa_pages_append writes the rows; qsa_pages_fork lets a sequence begin with another's pages,
+ * qsa_pages_append_reserved writes the rows of the sequences that got their room; qsa_pages_fork lets a sequence begin with another's pages,
  * qsa_pages_release gives pages back, qsa_pages_compact moves the live pages together.  The
  * attention of a prompt (qsa_prompt_attention) and of drafted tokens over the pages
  * (qsa_tree_attention) stand beside them.  No passage of the source pages defines these
@@ -622,8 +622,9 @@ qsa_status qsa_pages_release(int32_t *table, int64_t table_stride, int max_pages
  *   new_tokens  [n_rows] int32 out: n_tokens + add; n_tokens itself where the row could not be
  *               served: too few pages are free for it and the rows before it
  *               (QSA_FLAG_NO_PAGES), or it would pass max_pages entries (QSA_FLAG_NBLOCKS_CLAMPED).  Such a
- *               row is left as it was.  The pages such rows ask for count for the rows behind them
- *               that need any; a row that passes max_pages asks for none.
+ *               row is left as it was: its last page may still be shared, so nothing may be appended to
+ *               it (qsa_pages_append_reserved leaves it out).  The pages such rows ask for count for the
+ *               rows behind them that need any; a row that passes max_pages asks for none.
  *   copy_src, copy_dst [n_rows] int32 out: the page that row s shared and the one it has in
  *               its place, or -1 twice; qsa_pages_copy brings the contents over
  *   ws          a workspace of at least qsa_pages_workspace_bytes(n_rows, n_pages) bytes
@@ -665,8 +666,9 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
                           int n, void *ws, size_t ws_bytes, qsa_stream stream);
 
 /*
- * Append: K and V rows into the pages.  Row s takes cu_rows[s + 1] - cu_rows[s] rows, at positions
- * first[s], first[s] + 1, ...: entry e (cu_rows[s] <= e < cu_rows[s + 1]) is row rows[e] of k and v
+ * Append: K and V rows into the pages, whoever else refers to them: behind a reservation that may
+ * not have served every row, qsa_pages_append_reserved is the call to make.
+ * Row s takes cu_rows[s + 1] - cu_rows[s] rows, at positions first[s], first[s] + 1, ...: entry e (cu_rows[s] <= e < cu_rows[s + 1]) is row rows[e] of k and v
  * (row e itself when rows is NULL) and goes to page table[s][pos / 64].
  *
  *   k, v      row r of KV head g at k + r * k_token_stride + g * k_head_stride, 128 values of `dt`
@@ -694,6 +696,21 @@ qsa_status qsa_pages_append(const void *k, int64_t k_token_stride, int64_t k_hea
                             const int32_t *table, int64_t table_stride, int max_pages, int n_rows, int n_kv_heads,
                             int head_dim, void *kcache, void *vcache_t, int capacity, void *ws, size_t ws_bytes,
                             qsa_stream stream);
+
+/*
+ * As qsa_pages_append, up to where each row has room:
+ *
+ *   end       [n_rows] int32 on the DEVICE: row s's entries at or past position end[s] are dropped (no flag).
+ *             With qsa_pages_reserve's n_tokens as first and its new_tokens as end, a row that could not be
+ *             served, whose last page may be another sequence's too, writes nothing; the host need not know
+ * Errors: as qsa_pages_append's; a NULL end.
+ */
+qsa_status qsa_pages_append_reserved(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                                     int64_t v_token_stride, int64_t v_head_stride, qsa_dtype dt, int n_source,
+                                     const int32_t *rows, int n, const int32_t *cu_rows, const int32_t *first,
+                                     const int32_t *end, const int32_t *table, int64_t table_stride, int max_pages,
+                                     int n_rows, int n_kv_heads, int head_dim, void *kcache, void *vcache_t,
+                                     int capacity, void *ws, size_t ws_bytes, qsa_stream stream);
 
 /* Workspace of the two attentions below for `rows` query rows (tokens) in all, in bytes; 0 for invalid sizes.  One for
  * more rows serves fewer.  Zero-filled before its first use; every call leaves it reusable. */

@@ -197,14 +197,16 @@ class Pool:
         pad = [-1] * (len(self.refs) // 2 - len(high))
         return table, refs, high + pad, holes + pad
 
-    def append(self, k, v, first, cu, kcache, vcache_t, rows=None):
-        """Rows of k, v [n, kv, D] (tensors) into the pools, in place."""
+    def append(self, k, v, first, cu, kcache, vcache_t, rows=None, end=None):
+        """Rows of k, v [n, kv, D] (tensors) into the pools, in place; none at or past a row's end."""
         width, pages = len(self.table[0]), kcache.shape[1] // BT
         for s in range(len(self.table)):
             for e in range(cu[s], cu[s + 1]):
                 r, pos = (e if rows is None else rows[e]), first[s] + e - cu[s]
                 if pos < 0 or pos >= BT * width:
                     self.flags.add("clamp")
+                    continue
+                if end is not None and pos >= end[s]:
                     continue
                 p = self.table[s][pos // BT]
                 if not 0 <= p < pages:

@@ -116,6 +116,41 @@ size_t out_bytes(const DenseArgs &a) {
     return (size_t)a.total_q * a.n_heads * QSA_HEAD_DIM * (a.out_dt == QSA_F32 ? 4 : 2);
 }
 
+// a: everything but the pool and the table.
+qsa_status pages_append(const PagesAppendArgs &a, qsa_dtype dt, const int32_t *table, int64_t table_stride, int max_pages,
+                        int n_rows, int head_dim, int capacity, void *ws, size_t ws_bytes, qsa_stream stream) {
+    if (!a.k.p || !a.v.p || !a.cu_rows || !a.first || !table || !a.kcache || !a.vcache_t)
+        return fail(QSA_ERR_INVALID_ARG, "NULL k, v, cu_rows, first, table, kcache or vcache_t");
+    if (dt != QSA_BF16 && dt != QSA_F16)
+        return fail(QSA_ERR_UNSUPPORTED, "the paged cache takes bf16 or fp16 rows (dtype %d)", (int)dt);
+    if (head_dim != QSA_HEAD_DIM)
+        return fail(QSA_ERR_INVALID_ARG, "head_dim must be %d (got %d)", QSA_HEAD_DIM, head_dim);
+    if (a.n_kv_heads < 1 || a.n_kv_heads > 65535)
+        return fail(QSA_ERR_INVALID_ARG, "n_kv_heads must be in [1, 65535] (got %d)", a.n_kv_heads);
+    if (capacity < 64 || capacity % 64)
+        return fail(QSA_ERR_INVALID_ARG, "capacity must be a positive multiple of 64 (got %d)", capacity);
+    qsa_status st = check_table(table_stride, max_pages, n_rows, capacity / 64);
+    if (st != QSA_OK) return st;
+    if (a.n < 0 || a.n > (1 << 28) || a.n_source < 0 || a.n_source > (1 << 28) || (!a.rows && a.n != a.n_source))
+        return fail(QSA_ERR_INVALID_ARG, "bad numbers of rows (%d entries, %d rows)", a.n, a.n_source);
+    size_t kb, vb;
+    if ((st = check_rows16(a.k, "k", a.n_source, a.n_kv_heads, 0, &kb)) != QSA_OK ||
+        (st = check_rows16(a.v, "v", a.n_source, a.n_kv_heads, 0, &vb)) != QSA_OK)
+        return st;
+    if (misaligned(a.kcache, 16) || misaligned(a.vcache_t, 16))
+        return fail(QSA_ERR_INVALID_ARG, "kcache and vcache_t must be 16-byte aligned");
+    if ((st = check_ws(ws, ws_bytes, 256, true)) != QSA_OK) return st;
+    const size_t pool = (size_t)a.n_kv_heads * capacity * QSA_HEAD_DIM * 2;
+    const Range out[] = {{a.kcache, pool, "kcache"}, {a.vcache_t, pool, "vcache_t"}};
+    const Range in[] = {{a.k.p, kb, "k"}, {a.v.p, vb, "v"}, {a.rows, words(a.n), "rows"}, {a.cu_rows, words(n_rows + 1), "cu_rows"},
+                        {a.first, words(n_rows), "first"}, {a.end, words(n_rows), "end"},
+                        {table, table_bytes(table_stride, max_pages, n_rows), "table"}};
+    if ((st = check_apart(out, in)) != QSA_OK) return st;
+    if (a.n == 0) return QSA_OK;
+    return launch_pages_append(page_table(table, table_stride, max_pages, n_rows, capacity / 64, ws), a,
+                               static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 }  // namespace qsa
 
@@ -232,46 +267,21 @@ qsa_status qsa_pages_append(const void *k, int64_t k_token_stride, int64_t k_hea
                             const int32_t *table, int64_t table_stride, int max_pages, int n_rows, int n_kv_heads,
                             int head_dim, void *kcache, void *vcache_t, int capacity, void *ws, size_t ws_bytes,
                             qsa_stream stream) {
-    if (!k || !v || !cu_rows || !first || !table || !kcache || !vcache_t)
-        return fail(QSA_ERR_INVALID_ARG, "NULL k, v, cu_rows, first, table, kcache or vcache_t");
-    if (dt != QSA_BF16 && dt != QSA_F16)
-        return fail(QSA_ERR_UNSUPPORTED, "the paged cache takes bf16 or fp16 rows (dtype %d)", (int)dt);
-    if (head_dim != QSA_HEAD_DIM)
-        return fail(QSA_ERR_INVALID_ARG, "head_dim must be %d (got %d)", QSA_HEAD_DIM, head_dim);
-    if (n_kv_heads < 1 || n_kv_heads > 65535)
-        return fail(QSA_ERR_INVALID_ARG, "n_kv_heads must be in [1, 65535] (got %d)", n_kv_heads);
-    if (capacity < 64 || capacity % 64)
-        return fail(QSA_ERR_INVALID_ARG, "capacity must be a positive multiple of 64 (got %d)", capacity);
-    qsa_status st = check_table(table_stride, max_pages, n_rows, capacity / 64);
-    if (st != QSA_OK) return st;
-    if (n < 0 || n > (1 << 28) || n_source < 0 || n_source > (1 << 28) || (!rows && n != n_source))
-        return fail(QSA_ERR_INVALID_ARG, "bad numbers of rows (%d entries, %d rows)", n, n_source);
-    PagesAppendArgs a{};
-    a.k = {k, k_token_stride, k_head_stride};
-    a.v = {v, v_token_stride, v_head_stride};
-    size_t kb, vb;
-    if ((st = check_rows16(a.k, "k", n_source, n_kv_heads, 0, &kb)) != QSA_OK ||
-        (st = check_rows16(a.v, "v", n_source, n_kv_heads, 0, &vb)) != QSA_OK)
-        return st;
-    if (misaligned(kcache, 16) || misaligned(vcache_t, 16))
-        return fail(QSA_ERR_INVALID_ARG, "kcache and vcache_t must be 16-byte aligned");
-    if ((st = check_ws(ws, ws_bytes, 256, true)) != QSA_OK) return st;
-    const size_t pool = (size_t)n_kv_heads * capacity * QSA_HEAD_DIM * 2;
-    const Range out[] = {{kcache, pool, "kcache"}, {vcache_t, pool, "vcache_t"}};
-    const Range in[] = {{k, kb, "k"}, {v, vb, "v"}, {rows, words(n), "rows"}, {cu_rows, words(n_rows + 1), "cu_rows"},
-                        {first, words(n_rows), "first"}, {table, table_bytes(table_stride, max_pages, n_rows), "table"}};
-    if ((st = check_apart(out, in)) != QSA_OK) return st;
-    if (n == 0) return QSA_OK;
-    a.n_source = n_source;
-    a.rows = rows;
-    a.n = n;
-    a.cu_rows = cu_rows;
-    a.first = first;
-    a.n_kv_heads = n_kv_heads;
-    a.kcache = kcache;
-    a.vcache_t = vcache_t;
-    return launch_pages_append(page_table(table, table_stride, max_pages, n_rows, capacity / 64, ws), a,
-                               static_cast<cudaStream_t>(stream));
+    const PagesAppendArgs a{{k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, n_source, rows, n, cu_rows,
+                            first, nullptr, n_kv_heads, kcache, vcache_t};
+    return pages_append(a, dt, table, table_stride, max_pages, n_rows, head_dim, capacity, ws, ws_bytes, stream);
+}
+
+qsa_status qsa_pages_append_reserved(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                                     int64_t v_token_stride, int64_t v_head_stride, qsa_dtype dt, int n_source,
+                                     const int32_t *rows, int n, const int32_t *cu_rows, const int32_t *first,
+                                     const int32_t *end, const int32_t *table, int64_t table_stride, int max_pages,
+                                     int n_rows, int n_kv_heads, int head_dim, void *kcache, void *vcache_t,
+                                     int capacity, void *ws, size_t ws_bytes, qsa_stream stream) {
+    if (!end) return fail(QSA_ERR_INVALID_ARG, "NULL end");
+    const PagesAppendArgs a{{k, k_token_stride, k_head_stride}, {v, v_token_stride, v_head_stride}, n_source, rows, n, cu_rows,
+                            first, end, n_kv_heads, kcache, vcache_t};
+    return pages_append(a, dt, table, table_stride, max_pages, n_rows, head_dim, capacity, ws, ws_bytes, stream);
 }
 
 size_t qsa_attention_workspace_bytes(int rows, int n_heads, int n_kv_heads) {

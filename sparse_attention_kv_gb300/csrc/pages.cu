@@ -481,6 +481,7 @@ __device__ __forceinline__ Span span_of(const PageTable &t, const PagesAppendArg
     s.lo = s.first < 0 ? 0 : s.first;
     s.hi = end > most ? most : end;
     if (tell && c1 > c0 && (s.first < 0 || end > most)) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+    if (a.end) s.hi = min(s.hi, (long long)a.end[row]);   // where the row's room ends
     if (s.hi < s.lo || c1 == c0) s.hi = s.lo;
     return s;
 }

@@ -254,6 +254,7 @@ struct PagesAppendArgs {
     const int32_t *rows;   // or null
     int n;
     const int32_t *cu_rows, *first;
+    const int32_t *end;    // or null: as far as the entries go
     int n_kv_heads;
     void *kcache, *vcache_t;
 };

@@ -47,7 +47,7 @@ EXPORTS = ("qsa_workspace_bytes", "qsa_workspace_init", "qsa_block_scores", "qsa
            "qsa_select_attention", "qsa_vcache_transpose", "qsa_qcache_bytes", "qsa_qcache_append", "qsa_qcache_load",
            "qsa_select_attention_qcache", "qsa_block_weights_add", "qsa_evict_plan", "qsa_gather_blocks",
            "qsa_pages_workspace_bytes", "qsa_pages_fork", "qsa_pages_release", "qsa_pages_reserve", "qsa_pages_compact",
-           "qsa_pages_copy", "qsa_pages_append", "qsa_attention_workspace_bytes", "qsa_prompt_attention",
+           "qsa_pages_copy", "qsa_pages_append", "qsa_pages_append_reserved", "qsa_attention_workspace_bytes", "qsa_prompt_attention",
            "qsa_tree_attention", "qsa_read_flags", "qsa_auto_path", "qsa_last_error", "qsa_version")
 MERGE_CAP = 4096   # candidates per query qsa_merge_candidates holds (n_shards x k)
 
@@ -136,6 +136,9 @@ def load() -> ctypes.CDLL:
     lib.qsa_pages_append.argtypes = [*rows16, *rows16, i32, i32, vp, i32, vp, vp, vp, i64, i32, i32, i32, i32, vp, vp, i32,
                                      vp, sz, vp]
     lib.qsa_pages_append.restype = i32
+    lib.qsa_pages_append_reserved.argtypes = [*rows16, *rows16, i32, i32, vp, i32, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp,
+                                              vp, i32, vp, sz, vp]
+    lib.qsa_pages_append_reserved.restype = i32
     lib.qsa_attention_workspace_bytes.argtypes = [i32, i32, i32]
     lib.qsa_attention_workspace_bytes.restype = sz
     lib.qsa_prompt_attention.argtypes = [*rows16, *rows16, *rows16, i32, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, i32,
@@ -792,10 +795,12 @@ def _pool(kcache: torch.Tensor, vcache_t: torch.Tensor, dtype, dev: int) -> tupl
 
 def pages_append(k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, first: torch.Tensor, cu_rows: torch.Tensor,
                  kcache: torch.Tensor, vcache_t: torch.Tensor, rows: torch.Tensor | None = None,
-                 ws: torch.Tensor | None = None, stream=None) -> None:
+                 ws: torch.Tensor | None = None, stream=None, end: torch.Tensor | None = None) -> None:
     """K and V rows [n, n_kv_heads, 128] into the pages of table [n_rows, max_pages] at positions
     first[s], first[s] + 1, ...: entries cu_rows[s] .. cu_rows[s + 1] - 1 are row s's, and name the
-    rows of k and v (rows int32, e.g. the accepted drafts) or are them (rows None)."""
+    rows of k and v (rows int32, e.g. the accepted drafts) or are them (rows None).  Positions at or past end[s]
+    ([n_rows] int32) are dropped: with pages_reserve's new_tokens, a row that it could not serve writes
+    nothing.  Without it such a row would write into a last page that it may share."""
     lib, dev = load(), torch.cuda.current_device()
     dt = _qdtype(k, "k")
     if v.dtype is not k.dtype or v.shape != k.shape:
@@ -806,13 +811,18 @@ def pages_append(k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, first: t
     n_rows, width, stride = _table(table, dev)
     _vectors(n_rows, dev, ("first", first))
     _vectors(n_rows + 1, dev, ("cu_rows", cu_rows))
+    if end is not None:
+        _vectors(n_rows, dev, ("end", end))
     entries = n if rows is None else _length("rows", rows, dev)
     wp, wn = _workspace(ws, dev)
     if entries and n:
-        _check("qsa_pages_append", lib.qsa_pages_append(
-            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, n, _ptr(rows), entries, cu_rows.data_ptr(), first.data_ptr(),
-            table.data_ptr(), stride, width, n_rows, kv, HEAD_DIM, kcache.data_ptr(), vcache_t.data_ptr(), cap, wp, wn,
-            _current_stream(dev) if stream is None else _stream(stream)))
+        source = (k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dt, n, _ptr(rows), entries, cu_rows.data_ptr(), first.data_ptr())
+        pool = (table.data_ptr(), stride, width, n_rows, kv, HEAD_DIM, kcache.data_ptr(), vcache_t.data_ptr(), cap, wp, wn,
+                _current_stream(dev) if stream is None else _stream(stream))
+        if end is None:
+            _check("qsa_pages_append", lib.qsa_pages_append(*source, *pool))
+        else:
+            _check("qsa_pages_append_reserved", lib.qsa_pages_append_reserved(*source, end.data_ptr(), *pool))
 
 
 def attention_workspace_bytes(rows: int, n_heads: int, n_kv_heads: int) -> int:

@@ -267,6 +267,83 @@ def test_append_drops_what_has_no_place():
     assert torch.equal(kc, kw) and torch.equal(vc, vw) and qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED
 
 
+@pytest.mark.parametrize("pick", [False, True])
+@pytest.mark.parametrize("kv,lens,first,end", [(1, [1], [0], [0]), (1, [1], [0], [1]), (2, [70, 5, 200, 64], [60, 100, 3, 64], [100, 100, 130, 128]),
+                                               (3, [130, 130, 130], [1, 1, 1], [-5, 64, 2 ** 31 - 1]), (1, [1] * 300, [63] * 300, [63, 64] * 150)])
+def test_append_ends_where_a_row_has_room(kv, lens, first, end, pick):
+    rows, dt = len(lens), torch.float16
+    width = max((f + m + 63) // 64 for f, m in zip(first, lens))
+    table = [list(range(s * width, (s + 1) * width)) for s in range(rows)]
+    n, pages = sum(lens), rows * width
+    k, v = normal(3, n + 2, kv, 128, dt=dt), normal(4, n + 2, kv, 128, dt=dt)
+    idx = np.random.default_rng(rows).integers(0, n + 2, size=n).tolist() if pick else None
+    if not pick:
+        k, v = k[:n], v[:n]
+    kc, vc = random_pool(5, kv, pages, dt)
+    kw, vw = kc.clone(), vc.clone()
+    pool = paged.Pool(table, first, [1] * pages)
+    ws = qsa.alloc_pages_workspace(rows, pages)
+    qsa.pages_append(k, v, i32(table), i32(first), i32(cu(lens)), kc, vc, rows=i32(idx) if pick else None, ws=ws, end=i32(end))
+    pool.append(k, v, first, cu(lens), kw, vw, idx, end)
+    assert torch.equal(kc, kw) and torch.equal(vc, vw) and qsa.read_flags(ws) == 0 and not pool.flags
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_row_that_found_no_pages_writes_nothing(captured):
+    """Rows 1 and 2 are forks of row 0 that went back into its last page; the pool has a page for one of them, then
+    for none: who is refused leaves the others' rows as they are, and is served once there is room."""
+    kv, pages, rows, dt = 2, 4, 3, torch.bfloat16
+    kc, vc, table, n, refs = qsa.alloc_pages(rows, 4, pages, kv)
+    ws = qsa.alloc_pages_workspace(rows, pages)
+    new, cs, cd, add, cum = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (rows, rows, rows, rows, rows + 1))
+    k, v = normal(1, 200, kv, 128, dt=dt), normal(2, 200, kv, 128, dt=dt)
+
+    def step():
+        qsa.pages_reserve(table, n, refs, add, new, cs, cd, ws=ws)
+        qsa.pages_copy([kc.view(kv, pages, 64, 128), vc], cs, cd, ws=ws)
+        qsa.pages_append(k, v, table, n, cum, kc, vc, rows=idx, ws=ws, end=new)
+        n.copy_(new)
+
+    def run(lens, picked):
+        add.copy_(i32(lens)), cum.copy_(i32(cu(lens)))
+        idx.fill_(-1)
+        idx[:len(picked)] = i32(picked)
+        if graph is None:
+            step()
+        else:
+            graph.replay()
+        for s in range(rows):
+            if new[s] > before[s]:
+                side[s] = [torch.cat((side[s][0], k[picked[sum(lens[:s]):sum(lens[:s + 1])]])),
+                           torch.cat((side[s][1], v[picked[sum(lens[:s]):sum(lens[:s + 1])]]))]
+        before[:] = n.tolist()
+        assert before == [len(x[0]) for x in side]
+        for s in range(rows):
+            pk, pv, ok = paged.paged_rows(kc, vc, table[s].tolist(), before[s])
+            assert ok.all() and torch.equal(pk, side[s][0]) and torch.equal(pv, side[s][1]), s
+        return qsa.read_flags(ws)
+
+    idx = torch.full((200,), -1, dtype=torch.int32, device="cuda")
+    none = [k[:0], v[:0]]
+    side, before, graph = [list(none) for _ in range(rows)], [0] * rows, None
+    assert run([120, 0, 0], list(range(120))) == 0
+    qsa.pages_fork(table, n, refs, i32([0, 0]), i32([1, 2]), ws=ws)
+    qsa.pages_release(table, n, refs, i32([-1, 100, 90]), ws=ws)
+    side[1], side[2] = [x[:100] for x in side[0]], [x[:90] for x in side[0]]
+    before[:] = [120, 100, 90]
+    if captured:
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+    # pages 2 and 3 are free: row 1 asks for three, row 2 for one behind it
+    assert run([0, 150, 5], list(range(155))) == qsa.FLAG_NO_PAGES and before == [120, 100, 90]
+    assert run([3, 0, 3], [7, 8, 9, 1, 2, 3]) == 0 and before == [123, 100, 93]            # a page each
+    assert run([5, 30, 2], list(range(37))) == qsa.FLAG_NO_PAGES and before == [128, 100, 95]   # rows 0 and 2 need none
+    assert refs.tolist() == [3, 1, 1, 1]
+
+
 @pytest.mark.parametrize("bad", [0, 255, 256, 599])
 def test_append_looks_at_every_row_for_its_flags(bad):
     """600 rows of one token each, one of them with no place: behind the first pages, and without a page of its own."""

@@ -84,6 +84,18 @@ def test_reserve_by_hand_when_pages_run_out():
     assert p.reserve([1, -2])[0] == [64, 3] and p.flags == {"clamp"}
 
 
+def test_a_row_that_found_no_pages_appends_nothing():
+    """A fork that goes on from within its parent's last page, in a full pool: without its end it writes there."""
+    k = torch.arange(5.0)[:, None, None].expand(5, 1, 128).double() + 1
+    for end in (False, True):
+        p = paged.Pool([[0, 1, -1], [0, 1, -1]], [128, 100], [2, 2])
+        new, src, dst = p.reserve([0, 5])
+        assert new == [128, 100] and src == dst == [-1, -1] and p.flags == {"pages"} and p.table[1] == [0, 1, -1]
+        kc, vc = torch.zeros(1, 128, 128).double(), torch.zeros(1, 2, 128, 64).double()
+        p.append(k, k, p.n, [0, 0, 5], kc, vc, end=new if end else None)
+        assert bool(kc.any()) == bool(vc.any()) == (not end)       # the other's tokens 100 .. 104
+
+
 # ------------------------------------------------------------------ refusals of the library
 
 STATUS = {"ARG": qsa.ERR_INVALID_ARG, "UNSUPPORTED": qsa.ERR_UNSUPPORTED, "WS": qsa.ERR_WORKSPACE, "OK": qsa.OK}
@@ -179,6 +191,19 @@ def test_append_rejects_bad_arguments_before_launch(lib, case, status):
     _expect(lib, lib.qsa_pages_append(a["k"], *a["ks"], a["v"], *a["vs"], a["dt"], a["source"], a["idx"], a["n"], a["cu"], a["first"],
                                       a["table"], a["stride"], a["width"], a["rows"], a["kv"], a["D"], a["kc"], a["vc"], a["cap"],
                                       a["ws"], a["ws_bytes"], None), status)
+
+
+@pytest.mark.parametrize("case,status", [
+    (dict(end=None), "ARG"), (dict(end="kc+64"), "ARG"), (dict(vc="end"), "ARG"), (dict(k=None), "ARG"), (dict(first=None), "ARG"),
+    (dict(kc=FAKE + 8), "ARG"), (dict(ks=(12, 128)), "ARG"), (dict(D=64), "ARG"), (dict(cap=100), "ARG"), (dict(rows=4097), "ARG"),
+    (dict(n=-1), "ARG"), (dict(idx=None, n=5), "ARG"), (dict(dt=qsa.F32), "UNSUPPORTED"), (dict(ws_bytes=255), "WS"), (dict(n=0), "OK"),
+    (dict(n=0, end="first"), "OK")])
+def test_append_reserved_rejects_bad_arguments_before_launch(lib, case, status):
+    a = _resolve(_args(["k", "v", "idx", "cu", "first", "end", "table", "kc", "vc"], ks=(512, 128), vs=(512, 128), dt=qsa.BF16, source=8,
+                       n=4, kv=4, D=128, cap=6400), case)
+    _expect(lib, lib.qsa_pages_append_reserved(a["k"], *a["ks"], a["v"], *a["vs"], a["dt"], a["source"], a["idx"], a["n"], a["cu"],
+                                               a["first"], a["end"], a["table"], a["stride"], a["width"], a["rows"], a["kv"], a["D"],
+                                               a["kc"], a["vc"], a["cap"], a["ws"], a["ws_bytes"], None), status)
 
 
 DENSE = [
@@ -282,6 +307,14 @@ def test_binding_checks_the_pages(lib, monkeypatch):
         qsa.alloc_pages(1, 1, 4, 1, dtype=torch.float32)
     with pytest.raises(ValueError):
         qsa.alloc_pages_workspace(5000, 10)
+
+
+@pytest.mark.parametrize("end", [_i32(3), _i32(4, 1), _i32(8)[::2], _i32(4).long()])
+def test_binding_checks_where_an_append_ends(lib, monkeypatch, end):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    rows, kc, vc = torch.zeros(6, 2, 128).half(), torch.zeros(2, 640, 128).half(), torch.zeros(2, 10, 128, 64).half()
+    with pytest.raises(ValueError, match="end"):
+        qsa.pages_append(rows, rows, _i32(4, 10), _i32(4), _i32(5), kc, vc, end=end)
 
 
 def test_binding_checks_the_attentions(lib, monkeypatch):
