@@ -677,8 +677,8 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
  *             QSA_FLAG_BAD_ID, but for -1) and its position left as it was
  *   rows      [n] int32 on the DEVICE, e.g. the accepted nodes of a draft; or NULL
  *   n         entries in all, an upper bound on cu_rows (n = n_source when rows is NULL)
- *   cu_rows   [n_rows + 1] int32 on the DEVICE, ascending, clamped to [0, n] (and a descent to no
- *             rows; either sets QSA_FLAG_NBLOCKS_CLAMPED)
+ *   cu_rows   [n_rows + 1] int32 on the DEVICE, ascending, clamped to [0, n] (QSA_FLAG_NBLOCKS_CLAMPED).
+ *             Where it descends, that row and all behind it take no entries (with the same flag)
  *   first     [n_rows] int32 on the DEVICE (n_tokens before the step); a position below 0 or at or past
  *             64 max_pages is dropped (QSA_FLAG_NBLOCKS_CLAMPED), one whose table entry is no page too
  *             (QSA_FLAG_BAD_ID)

@@ -200,9 +200,15 @@ class Pool:
     def append(self, k, v, first, cu, kcache, vcache_t, rows=None, end=None):
         """Rows of k, v [n, kv, D] (tensors) into the pools, in place; none at or past a row's end."""
         width, pages = len(self.table[0]), kcache.shape[1] // BT
+        entries = k.shape[0] if rows is None else len(rows)
         for s in range(len(self.table)):
-            for e in range(cu[s], cu[s + 1]):
-                r, pos = (e if rows is None else rows[e]), first[s] + e - cu[s]
+            if not 0 <= cu[s] <= cu[s + 1] <= entries:
+                self.flags.add("clamp")
+            if cu[s + 1] < cu[s]:            # neither this row nor the ones behind it
+                break
+            c0, c1 = (min(max(c, 0), entries) for c in cu[s:s + 2])
+            for e in range(c0, c1):
+                r, pos = (e if rows is None else rows[e]), first[s] + e - c0
                 if pos < 0 or pos >= BT * width:
                     self.flags.add("clamp")
                     continue

@@ -468,11 +468,13 @@ struct Span {
     int e0;            // first entry
     long long lo, hi;  // positions
     int first;
+    bool falls;        // cu_rows descends here
 };
 __device__ __forceinline__ Span span_of(const PageTable &t, const PagesAppendArgs &a, int row, bool tell) {
     Span s;
     int c0 = a.cu_rows[row], c1 = a.cu_rows[row + 1];
     if (tell && (c0 < 0 || c0 > a.n || c1 < c0 || c1 > a.n)) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
+    s.falls = c1 < c0;
     c0 = min(max(c0, 0), a.n);
     c1 = min(max(c1, c0), a.n);
     s.e0 = c0;
@@ -494,27 +496,37 @@ __global__ void __launch_bounds__(kRowThreads) pages_append_kernel(PageTable t, 
     // nor eight tokens of a dimension going out meet a bank twice
     __shared__ uint4 tile[64][16];
     __shared__ int source[64];
+    __shared__ int fall;   // the first row at which cu_rows descends, of those looked at
     wait_prior_grid();
     allow_dependent_launch();
     const int tid = threadIdx.x;
-    if (tid == 0) unit.row = -1;
+    if (tid == 0) {
+        unit.row = -1;
+        fall = t.n_rows;
+    }
     __syncthreads();
     const bool tell = blockIdx.x == gridDim.x - 1 && blockIdx.y == 0;   // looks at every row
     int before = 0;
     for (int r0 = 0; r0 < t.n_rows && (tell || before <= (int)blockIdx.x); r0 += kRowThreads) {
         const int row = r0 + tid;
-        const int np = row < t.n_rows ? pages_of(span_of(t, a, row, tell)) : 0;
-        int total;
+        int np = 0, total;
+        if (row < t.n_rows) {
+            const Span s = span_of(t, a, row, tell);
+            np = pages_of(s);
+            if (s.falls) atomicMin(&fall, row);
+        }
         const int at = before + block_excl_scan<kRowThreads>(np, sm, total);
         if ((int)blockIdx.x >= at && (int)blockIdx.x < at + np) {
             unit.row = row;
             unit.index = (int)blockIdx.x - at;
         }
-        before += total;
+        if (before <= (int)blockIdx.x) before += total;   // up to 2^28 pages a turn; in all they may be more than an int holds
     }
     __syncthreads();
+    // Rows up to a descent hold n entries at most, and the grid has a CTA for each of their pages.  Those behind it could
+    // hold the same ones over again: they take none.
     const int row = unit.row;
-    if (row < 0) return;
+    if (row < 0 || row > fall) return;
     const Span s = span_of(t, a, row, false);
     const int b = (int)(s.lo >> 6) + unit.index;
     const int page = t.table[(size_t)row * t.stride + b];

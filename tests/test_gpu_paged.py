@@ -344,6 +344,25 @@ def test_a_row_that_found_no_pages_writes_nothing(captured):
     assert refs.tolist() == [3, 1, 1, 1]
 
 
+@pytest.mark.parametrize("cuts", [[0, 6400, 0, 6400], [6400, 0, 6400, 6400, 0, 99_999], [-9, 64, 0, 6400], [0, 3200, 100, 3300],
+                                  [0] * 300 + [6400, 0, 6400], [0, 6400, 0, 6400] + [6400] * 900, [0, 99_999, 6400, 6000, 6400],
+                                  [0, 100] + [100] * 254 + [50, 6400], [0, 100] + [100] * 255 + [50, 6400]])
+def test_append_stops_where_the_rows_entries_descend(cuts):
+    """The rows before a descent of cu_rows are written, the ones behind it, which may take entries again, are not."""
+    kv, n, rows = 1, 6400, len(cuts) - 1
+    k, v = normal(1, n, kv, 128, dt=torch.bfloat16), normal(2, n, kv, 128, dt=torch.bfloat16)
+    lens = [max(0, min(max(b, 0), n) - min(max(a, 0), n)) for a, b in zip(cuts, cuts[1:])]
+    at = cu([(m + 63) // 64 for m in lens])              # pages for all of them
+    table = [list(range(a, b)) + [-1] * (100 - b + a) for a, b in zip(at, at[1:])]
+    kc, vc = random_pool(5, kv, at[-1], torch.bfloat16)
+    kw, vw = kc.clone(), vc.clone()
+    pool, ws = paged.Pool(table, [0] * rows, [1] * at[-1]), qsa.alloc_pages_workspace(rows, at[-1])
+    qsa.pages_append(k, v, i32(table), i32([0] * rows), i32(cuts), kc, vc, ws=ws)
+    pool.append(k, v, [0] * rows, cuts, kw, vw)
+    assert torch.equal(kc, kw) and torch.equal(vc, vw)
+    assert qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED and pool.flags == {"clamp"}
+
+
 @pytest.mark.parametrize("bad", [0, 255, 256, 599])
 def test_append_looks_at_every_row_for_its_flags(bad):
     """600 rows of one token each, one of them with no place: behind the first pages, and without a page of its own."""

@@ -96,6 +96,14 @@ def test_a_row_that_found_no_pages_appends_nothing():
         assert bool(kc.any()) == bool(vc.any()) == (not end)       # the other's tokens 100 .. 104
 
 
+def test_rows_behind_a_descent_take_no_entries():
+    k = torch.arange(6.0)[:, None, None].expand(6, 1, 128).double() + 1
+    p = paged.Pool([[0], [1], [2]], [0] * 3, [1] * 3)
+    kc, vc = torch.zeros(1, 192, 128).double(), torch.zeros(1, 3, 128, 64).double()
+    p.append(k, k, [0, 0, 0], [0, 6, 0, 6], kc, vc)
+    assert torch.equal(kc[0, :6, 0], k[:, 0, 0]) and not kc[:, 6:].any() and p.flags == {"clamp"}
+
+
 # ------------------------------------------------------------------ refusals of the library
 
 STATUS = {"ARG": qsa.ERR_INVALID_ARG, "UNSUPPORTED": qsa.ERR_UNSUPPORTED, "WS": qsa.ERR_WORKSPACE, "OK": qsa.OK}
