@@ -591,7 +591,7 @@ size_t qsa_pages_workspace_bytes(int n_rows, int n_pages);
  * without tokens are released.
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, QSA_MAX_TABLE_ROWS],
  * n_pages outside [1, QSA_MAX_PAGES], max_pages outside [1, QSA_MAX_PAGES], table_stride <
- * max_pages, n outside [0, n_rows], arrays that overlap; QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not
+ * max_pages, n outside [0, n_rows], arrays that overlap each other or the workspace; QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not
  * 256-byte aligned.
  */
 qsa_status qsa_pages_fork(int32_t *table, int64_t table_stride, int max_pages, int32_t *n_tokens, int n_rows,
@@ -660,7 +660,7 @@ qsa_status qsa_pages_compact(const int32_t *table, int64_t table_stride, int max
  *             qsa_pages_reserve and qsa_pages_compact are so); a src id may repeat
  *   ws        a workspace of at least 256 bytes (its flags word is used), or NULL
  * Errors: as qsa_gather_blocks's, n outside [0, QSA_MAX_PAGES], an array whose src is not its dst,
- * arrays that overlap each other or the ids.
+ * arrays that overlap each other, the ids or the workspace.
  */
 qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int32_t *src_ids, const int32_t *dst_ids,
                           int n, void *ws, size_t ws_bytes, qsa_stream stream);
@@ -687,7 +687,7 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
  * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides not multiples of 8,
  * head_dim != 128, n_kv_heads outside [1, 65535], capacity not a positive multiple of 64 or above 64 *
  * QSA_MAX_PAGES, n_rows, max_pages or table_stride as above, n or n_source outside [0, 2^28],
- * rows NULL and n != n_source, a pool that overlaps an input; QSA_ERR_UNSUPPORTED for another dtype; QSA_ERR_WORKSPACE as
+ * rows NULL and n != n_source, a pool that overlaps an input, a workspace that overlaps either; QSA_ERR_UNSUPPORTED for another dtype; QSA_ERR_WORKSPACE as
  * above.
  */
 qsa_status qsa_pages_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,

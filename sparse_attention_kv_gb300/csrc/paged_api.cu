@@ -28,6 +28,7 @@ qsa_status check_apart(const Range (&out)[NO], const Range (&in)[NI]) {
     return QSA_OK;
 }
 
+constexpr size_t kFlagBytes = 256;   // of a workspace, in front: the flags word and what else every call keeps there
 qsa_status check_ws(const void *ws, size_t ws_bytes, size_t want, bool may_be_null) {
     if (!ws && may_be_null) return QSA_OK;
     if (!ws || ws_bytes < want || misaligned(ws, 256))
@@ -139,9 +140,9 @@ qsa_status pages_append(const PagesAppendArgs &a, qsa_dtype dt, const int32_t *t
         return st;
     if (misaligned(a.kcache, 16) || misaligned(a.vcache_t, 16))
         return fail(QSA_ERR_INVALID_ARG, "kcache and vcache_t must be 16-byte aligned");
-    if ((st = check_ws(ws, ws_bytes, 256, true)) != QSA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, kFlagBytes, true)) != QSA_OK) return st;
     const size_t pool = (size_t)a.n_kv_heads * capacity * QSA_HEAD_DIM * 2;
-    const Range out[] = {{a.kcache, pool, "kcache"}, {a.vcache_t, pool, "vcache_t"}};
+    const Range out[] = {{a.kcache, pool, "kcache"}, {a.vcache_t, pool, "vcache_t"}, {ws, kFlagBytes, "ws"}};
     const Range in[] = {{a.k.p, kb, "k"}, {a.v.p, vb, "v"}, {a.rows, words(a.n), "rows"}, {a.cu_rows, words(n_rows + 1), "cu_rows"},
                         {a.first, words(n_rows), "first"}, {a.end, words(n_rows), "end"},
                         {table, table_bytes(table_stride, max_pages, n_rows), "table"}};
@@ -171,9 +172,9 @@ qsa_status qsa_pages_fork(int32_t *table, int64_t table_stride, int max_pages, i
     qsa_status st = check_table(table_stride, max_pages, n_rows, n_pages);
     if (st != QSA_OK) return st;
     if (n < 0 || n > n_rows) return fail(QSA_ERR_INVALID_ARG, "n must be in [0, n_rows] (got %d)", n);
-    if ((st = check_ws(ws, ws_bytes, 256, true)) != QSA_OK) return st;
+    if ((st = check_ws(ws, ws_bytes, kFlagBytes, true)) != QSA_OK) return st;
     const Range out[] = {{table, table_bytes(table_stride, max_pages, n_rows), "table"}, {n_tokens, words(n_rows), "n_tokens"},
-                         {refs, words(n_pages), "refs"}};
+                         {refs, words(n_pages), "refs"}, {ws, kFlagBytes, "ws"}};
     const Range in[] = {{src, words(n), "src"}, {dst, words(n), "dst"}};
     if ((st = check_apart(out, in)) != QSA_OK) return st;
     if (n == 0) return QSA_OK;
@@ -186,9 +187,9 @@ qsa_status qsa_pages_release(int32_t *table, int64_t table_stride, int max_pages
                              qsa_stream stream) {
     if (!table || !n_tokens || !refs || !keep) return fail(QSA_ERR_INVALID_ARG, "NULL table, n_tokens, refs or keep");
     qsa_status st = check_table(table_stride, max_pages, n_rows, n_pages);
-    if (st != QSA_OK || (st = check_ws(ws, ws_bytes, 256, true)) != QSA_OK) return st;
+    if (st != QSA_OK || (st = check_ws(ws, ws_bytes, kFlagBytes, true)) != QSA_OK) return st;
     const Range out[] = {{table, table_bytes(table_stride, max_pages, n_rows), "table"}, {n_tokens, words(n_rows), "n_tokens"},
-                         {refs, words(n_pages), "refs"}};
+                         {refs, words(n_pages), "refs"}, {ws, kFlagBytes, "ws"}};
     const Range in[] = {{keep == n_tokens ? nullptr : keep, words(n_rows), "keep"}};
     if ((st = check_apart(out, in)) != QSA_OK) return st;
     return launch_pages_release(page_table(table, table_stride, max_pages, n_rows, n_pages, ws), n_tokens, refs, keep,
@@ -204,7 +205,7 @@ qsa_status qsa_pages_reserve(int32_t *table, int64_t table_stride, int max_pages
     if (st != QSA_OK || (st = check_ws(ws, ws_bytes, pages_ws_bytes(n_rows, n_pages), false)) != QSA_OK) return st;
     const Range out[] = {{table, table_bytes(table_stride, max_pages, n_rows), "table"}, {refs, words(n_pages), "refs"},
                          {new_tokens, words(n_rows), "new_tokens"}, {copy_src, words(n_rows), "copy_src"},
-                         {copy_dst, words(n_rows), "copy_dst"}};
+                         {copy_dst, words(n_rows), "copy_dst"}, {ws, pages_ws_bytes(n_rows, n_pages), "ws"}};
     const Range in[] = {{n_tokens, words(n_rows), "n_tokens"}, {add, words(n_rows), "add"}};
     if ((st = check_apart(out, in)) != QSA_OK) return st;
     return launch_pages_reserve(page_table(table, table_stride, max_pages, n_rows, n_pages, ws), n_tokens, refs, add,
@@ -221,7 +222,8 @@ qsa_status qsa_pages_compact(const int32_t *table, int64_t table_stride, int max
     if (st != QSA_OK || (st = check_ws(ws, ws_bytes, pages_ws_bytes(n_rows, n_pages), false)) != QSA_OK) return st;
     const size_t tb = table_bytes(table_stride, max_pages, n_rows);
     const Range out[] = {{table_out, tb, "table_out"}, {refs_out, words(n_pages), "refs_out"},
-                         {copy_src, words(n_pages / 2), "copy_src"}, {copy_dst, words(n_pages / 2), "copy_dst"}};
+                         {copy_src, words(n_pages / 2), "copy_src"}, {copy_dst, words(n_pages / 2), "copy_dst"},
+                         {ws, pages_ws_bytes(n_rows, n_pages), "ws"}};
     const Range in[] = {{table == table_out ? nullptr : table, tb, "table"},
                         {refs == refs_out ? nullptr : refs, words(n_pages), "refs"}};
     if ((st = check_apart(out, in)) != QSA_OK) return st;
@@ -235,7 +237,11 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
     if (n_arrays < 1 || n_arrays > QSA_GATHER_MAX_ARRAYS)
         return fail(QSA_ERR_INVALID_ARG, "n_arrays must be in [1, %d] (got %d)", QSA_GATHER_MAX_ARRAYS, n_arrays);
     if (n < 0 || n > QSA_MAX_PAGES) return fail(QSA_ERR_INVALID_ARG, "n must be in [0, %d] (got %d)", QSA_MAX_PAGES, n);
+    qsa_status st = check_ws(ws, ws_bytes, kFlagBytes, true);
+    if (st != QSA_OK) return st;
+    const Range flags[] = {{ws, kFlagBytes, "ws"}};
     const Range ids[] = {{src_ids, words(n), "src_ids"}, {dst_ids, words(n), "dst_ids"}};
+    if ((st = check_apart(flags, ids)) != QSA_OK) return st;
     for (int i = 0; i < n_arrays; ++i) {
         const qsa_block_array &x = arrays[i];
         if (!x.dst || x.src != x.dst) return fail(QSA_ERR_INVALID_ARG, "array %d: src must be dst, the pool", i);
@@ -247,16 +253,14 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
                         (long long)x.block_bytes);
         if (misaligned(x.dst, 4)) return fail(QSA_ERR_INVALID_ARG, "array %d: must be 4-byte aligned", i);
         const Range pool[] = {{x.dst, (size_t)x.n_rows * x.dst_blocks * x.block_bytes, "an array"}};
-        const qsa_status st = check_apart(pool, ids);
-        if (st != QSA_OK) return st;
+        if ((st = check_apart(pool, ids)) != QSA_OK || (st = check_apart(pool, flags)) != QSA_OK) return st;
         for (int j = 0; j < i; ++j) {
             const qsa_block_array &y = arrays[j];
             const Range other[] = {{y.dst, (size_t)y.n_rows * y.dst_blocks * y.block_bytes, "another one"}};
             if (overlap(pool[0], other[0])) return fail(QSA_ERR_INVALID_ARG, "array %d overlaps array %d", i, j);
         }
     }
-    const qsa_status st = check_ws(ws, ws_bytes, 256, true);
-    if (st != QSA_OK || n == 0) return st;
+    if (n == 0) return QSA_OK;
     return launch_gather_blocks(arrays, n_arrays, src_ids, dst_ids, n, static_cast<uint32_t *>(ws),
                                 static_cast<cudaStream_t>(stream));
 }

@@ -214,6 +214,46 @@ def test_append_reserved_rejects_bad_arguments_before_launch(lib, case, status):
                                                a["kc"], a["vc"], a["cap"], a["ws"], a["ws_bytes"], None), status)
 
 
+@pytest.mark.parametrize("name,over,status", [
+    (c, o, "ARG") for c, os in dict(fork="table+0 n+0 refs+0 src+0 dst+0", release="table+0 n+0 refs+0 keep+0",
+                                    reserve="table+0 n+0 refs+0 add+0 new+0 src+0 dst+0", compact="table+0 refs+0 tout+0 rout+0 src+0 dst+0",
+                                    append="k+0 v+0 idx+0 cu+0 first+0 table+0 kc+256 vc+1638144",
+                                    append_reserved="k+0 end+0 kc+1638144", copy="pool+0 pool+8448 ids+0 to+0").items() for o in os.split()] + [
+    # the workspace begins before the array and reaches into it; and right in front of it and behind it
+    ("fork", "table-256", "OK"), ("fork", "table-0", "ARG"), ("reserve", "refs-512", "ARG"), ("reserve", "refs-256", "ARG"),
+    ("compact", "rout-512", "ARG"), ("copy", "pool-256", "OK"), ("copy", "pool+12800", "OK"), ("append", "kc-256", "OK")])
+def test_a_workspace_that_overlaps_is_refused(lib, name, over, status):
+    """100 pages, 4 rows: fork, release, copy and append use 256 bytes of it, reserve and compact 768."""
+    names = ["table", "n", "refs", "src", "dst", "keep", "add", "new", "tout", "rout", "k", "v", "idx", "cu", "first", "end", "kc", "vc",
+             "pool", "ids", "to"]
+    a = _args(names, ks=(512, 128), vs=(512, 128))
+    for n in names:
+        a[n] &= ~255
+    array, sign, off = over.partition("+" if "+" in over else "-")
+    ws = (a[array] + int(sign + off), 4096)
+    t, tail = (a["table"], a["stride"], a["width"]), (*ws, None)
+    assert lib.qsa_pages_workspace_bytes(4, 100) == 768
+    if name == "fork":          # of no rows: a call that passes the checks launches nothing
+        count = 0 if status == "OK" else 3
+        st = lib.qsa_pages_fork(*t, a["n"], 4, a["refs"], 100, a["src"], a["dst"], count, *tail)
+    elif name == "release":
+        st = lib.qsa_pages_release(*t, a["n"], 4, a["refs"], 100, a["keep"], *tail)
+    elif name == "reserve":
+        st = lib.qsa_pages_reserve(*t, a["n"], 4, a["refs"], 100, a["add"], a["new"], a["src"], a["dst"], *tail)
+    elif name == "compact":
+        st = lib.qsa_pages_compact(*t, 4, a["refs"], 100, a["tout"], a["rout"], a["src"], a["dst"], *tail)
+    elif name == "copy":
+        packed = (qsa.BlockArray * 1)(qsa.BlockArray(a["pool"], a["pool"], 128, 1, 100, 100))
+        st = lib.qsa_pages_copy(packed, 1, a["ids"], a["to"], 0 if status == "OK" else 4, *tail)
+    else:
+        n = 0 if status == "OK" else 4
+        end = (a["end"],) if name == "append_reserved" else ()
+        f = getattr(lib, "qsa_pages_" + name)
+        st = f(a["k"], 512, 128, a["v"], 512, 128, qsa.BF16, 8, a["idx"], n, a["cu"], a["first"], *end, *t, 4, 1, 128, a["kc"], a["vc"],
+               6400, *tail)
+    _expect(lib, st, status)
+
+
 DENSE = [
     (dict(q=None), "ARG"), (dict(k=None), "ARG"), (dict(v=None), "ARG"), (dict(cu=None), "ARG"), (dict(out=None), "ARG"),
     (dict(q=FAKE + 8), "ARG"), (dict(v=FAKE + 2), "ARG"), (dict(out=FAKE + 8), "ARG"), (dict(qs=(100, 128)), "ARG"),
