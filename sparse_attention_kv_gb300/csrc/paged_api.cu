@@ -6,7 +6,7 @@ namespace {
 
 bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0; }
 
-// A range of memory that a call reads or writes; p may be null.
+// A range of memory that a call reads or writes; p may be null.  An empty one overlaps nothing.
 struct Range {
     const void *p;
     size_t n;
@@ -14,7 +14,7 @@ struct Range {
 };
 bool overlap(const Range &a, const Range &b) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a0 < b0 + b.n && b0 < a0 + a.n;
+    return a.p && b.p && a.n && b.n && a0 < b0 + b.n && b0 < a0 + a.n;
 }
 // No output shares a byte with another output or an input.
 template <int NO, int NI>

@@ -145,6 +145,19 @@ def _resolve(a, case):
     return a
 
 
+def test_an_empty_array_overlaps_nothing(lib):
+    """Of no entries, cut from an arena anywhere."""
+    a = _args(["table", "n", "refs", "src", "dst", "k", "v", "cu", "first", "kc", "vc", "idx"])
+    t = (a["table"], a["stride"], a["width"])
+    for at in (a["table"] + 40, a["n"] + 4, a["refs"] + 8):
+        _expect(lib, lib.qsa_pages_fork(*t, a["n"], 4, a["refs"], 100, at, at, 0, None, 0, None), "OK")
+    packed = (qsa.BlockArray * 1)(qsa.BlockArray(a["kc"], a["kc"], 64, 1, 8, 8))
+    _expect(lib, lib.qsa_pages_copy(packed, 1, a["kc"] + 64, a["kc"] + 64, 0, None, 0, None), "OK")
+    for k, idx in ((a["kc"] + 256, a["idx"]), (a["k"], a["vc"] + 256)):
+        _expect(lib, lib.qsa_pages_append(k, 512, 128, a["v"], 512, 128, qsa.BF16, 0, idx, 0, a["cu"], a["first"], *t, 4, 4, 128, a["kc"],
+                                          a["vc"], 6400, None, 0, None), "OK")
+
+
 @pytest.mark.parametrize("case,status", TABLE + [
     (dict(n=None), "ARG"), (dict(keep=None), "ARG"), (dict(keep="n+4"), "ARG"), (dict(keep="refs"), "ARG"), (dict(n="table"), "ARG")])
 def test_release_rejects_bad_arguments_before_launch(lib, case, status):
