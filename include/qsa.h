@@ -554,7 +554,8 @@ qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const 
  *
  *     table    [n_rows][table_stride] int32: the pages of sequence (row) s in order, page
  *              table[s][j] holding its tokens 64 j .. 64 j + 63; -1 behind the last one
- *     n_tokens [n_rows] int32: tokens of each sequence (its row may hold more pages than they fill)
+ *     n_tokens [n_rows] int32: tokens of each sequence (its row may hold more pages than they fill; a
+ *              sequence is shortened by qsa_pages_release, which gives back what lies behind)
  *     refs     [n_pages] int32: how many entries of the table hold each page; 0 = free
  *
  * all on the DEVICE.  A step of generation: qsa_pages_reserve makes room behind the sequences,
@@ -621,10 +622,12 @@ qsa_status qsa_pages_release(int32_t *table, int64_t table_stride, int max_pages
  *   add         [n_rows] int32 on the DEVICE (negative: as 0, with QSA_FLAG_NBLOCKS_CLAMPED)
  *   new_tokens  [n_rows] int32 out: n_tokens + add; n_tokens itself where the row could not be
  *               served: too few pages are free for it and the rows before it
- *               (QSA_FLAG_NO_PAGES), or it would pass max_pages entries (QSA_FLAG_NBLOCKS_CLAMPED).  Such a
+ *               (QSA_FLAG_NO_PAGES), it would pass max_pages entries (QSA_FLAG_NBLOCKS_CLAMPED), or its new
+ *               tokens would lie in a page behind its own ones that has other references, as after n_tokens
+ *               was lowered by hand (QSA_FLAG_BAD_ID; qsa_pages_release gives that page back).  Such a
  *               row is left as it was: its last page may still be shared, so nothing may be appended to
  *               it (qsa_pages_append_reserved leaves it out).  The pages such rows ask for count for the
- *               rows behind them that need any; a row that passes max_pages asks for none.
+ *               rows behind them that need any; the rows of the last two kinds ask for none.
  *   copy_src, copy_dst [n_rows] int32 out: the page that row s shared and the one it has in
  *               its place, or -1 twice; qsa_pages_copy brings the contents over
  *   ws          a workspace of at least qsa_pages_workspace_bytes(n_rows, n_pages) bytes

@@ -144,6 +144,10 @@ class Pool:
             if n < 0 or n + more > BT * width:
                 self.flags.add("clamp")
                 continue
+            past = [self.table[s][j] for j in range((n + BT - 1) // BT, (n + more + BT - 1) // BT)] if more > 0 else []
+            if any(self._page(p) and held[p] > 1 for p in past):
+                self.flags.add("id")             # another row's page behind the tokens
+                continue
             want = []
             shared = keeps = False
             if more > 0:

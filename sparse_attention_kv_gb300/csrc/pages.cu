@@ -137,6 +137,7 @@ __device__ __forceinline__ unsigned long long scan_all(unsigned long long v, uns
 }
 
 // What a row of reserve does with its last page.
+// (kPast: the row is refused for where its tokens would go, past its entries or in a page that others refer to.)
 enum : uint8_t { kWhole = 0, kCopies = 1, kKeeps = 2, kPast = 3 };
 
 // The entries that a row's new tokens need, [b0, b1), and whether it has any.
@@ -176,12 +177,14 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
     int held[4];   // references of the pool's first pages, on their way meanwhile
 #pragma unroll
     for (int e = 0; e < 4; ++e) held[e] = tid * 4 + e < t.n_pages ? refs[tid * 4 + e] : 1;
-    // what each row lacks: entries that are no page (a bad one counts as none)
+    // what each row lacks: entries that are no page (a bad one counts as none).  A page behind its tokens that others refer to
+    // as well may hold theirs: the row is refused.  (Rows in step with their pages have none there, and nothing is loaded.)
     bool any_warp = false, any_all = false;
     for (int row = tid; row < t.n_rows; row += kOneThreads) {
         const Wants w = wants_of(t, n_tokens, add, row, true);
         const int32_t *a = t.table + (size_t)row * t.stride;
         int lacks = 0, page = -1;
+        bool others = false;
         if (w.past) raise(t.flags, QSA_FLAG_NBLOCKS_CLAMPED);
         if (w.b1 - w.b0 <= kFew) {
             int p[kFew];
@@ -192,6 +195,7 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
             for (int i = 0; i < kFew; ++i) {
                 lacks += w.b0 + i < w.b1 && !is_page(t, p[i]);
                 if (p[i] < -1 || p[i] >= t.n_pages) raise(t.flags, QSA_FLAG_BAD_ID);
+                others = others || (w.b0 + i < w.b1 && is_page(t, p[i]) && refs[p[i]] > 1);
             }
         } else {
             if (w.n & 63) page = a[w.n >> 6];
@@ -203,8 +207,9 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
             page = -1;
             ++lacks;
         }
-        last[row] = page;
-        what[row] = w.past ? kPast : kWhole;
+        if (others) raise(t.flags, QSA_FLAG_BAD_ID);
+        last[row] = others ? -1 : page;
+        what[row] = w.past || others ? kPast : kWhole;
         needs[row] = lacks;
     }
     if (__syncthreads_or(any_warp))
@@ -213,14 +218,24 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
             if (w.b1 - w.b0 <= kFew || w.b1 - w.b0 > kMany) continue;
             const int32_t *a = t.table + (size_t)row * t.stride;
             int lacks = 0;
+            bool others = false;
 #pragma unroll 4
             for (int b = w.b0 + lane; b < w.b1; b += 32) {
                 const int p = a[b];
                 lacks += !is_page(t, p);
                 if (p < -1 || p >= t.n_pages) raise(t.flags, QSA_FLAG_BAD_ID);
+                others = others || (is_page(t, p) && refs[p] > 1);
             }
             lacks = __reduce_add_sync(~0u, lacks);
-            if (lane == 0) needs[row] += lacks;
+            others = __any_sync(~0u, others);
+            if (lane == 0) {
+                needs[row] += lacks;
+                if (others) {
+                    raise(t.flags, QSA_FLAG_BAD_ID);
+                    last[row] = -1;
+                    what[row] = kPast;
+                }
+            }
         }
     if (__syncthreads_or(any_all))
         for (int row = 0; row < t.n_rows; ++row) {
@@ -228,19 +243,27 @@ __global__ void __launch_bounds__(kOneThreads) pages_reserve_kernel(PageTable t,
             if (w.b1 - w.b0 <= kMany) continue;
             const int32_t *a = t.table + (size_t)row * t.stride;
             int lacks = 0;
+            bool others = false;
 #pragma unroll 4
             for (int b = w.b0 + tid; b < w.b1; b += kOneThreads) {
                 const int p = a[b];
                 lacks += !is_page(t, p);
                 if (p < -1 || p >= t.n_pages) raise(t.flags, QSA_FLAG_BAD_ID);
+                others = others || (is_page(t, p) && refs[p] > 1);
             }
             lacks = __reduce_add_sync(~0u, lacks);
             if (lane == 0) atomicAdd(&needs[row], lacks);
+            if (others) {   // the same by every thread that says so
+                raise(t.flags, QSA_FLAG_BAD_ID);
+                last[row] = -1;
+                what[row] = kPast;
+            }
         }
     __syncthreads();
     // rows that share their last page: the k-th of them to write copies while more than k references remain
     for (int row = tid; row < t.n_rows; row += kOneThreads) {
         const int page = last[row];
+        if (what[row] == kPast) needs[row] = 0;   // asks for none
         if (page < 0) continue;
         const int all = refs[page];
         if (all <= 1) continue;

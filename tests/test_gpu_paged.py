@@ -147,6 +147,29 @@ def test_reserve_settles_shared_pages():
     assert cs.tolist() == [-1] * 5
 
 
+@pytest.mark.parametrize("behind", [1, 2, 3, 40, 128, 129, 2000])
+@pytest.mark.parametrize("partial", [0, 1])
+def test_reserve_leaves_rows_with_shared_pages_behind_their_tokens(behind, partial):
+    """Rows 0 and 1 have the same pages; row 1's length was lowered by hand, by a page and by all of them.  Released, it is served."""
+    width, n = behind + 6, 64 * (behind + 3)
+    shared = list(range(behind + 3))
+    table = [shared + [-1] * 3, shared + [-1] * 3, [behind + 3] + [-1] * (width - 1), [behind + 4] + [-1] * (width - 1)]
+    refs = [2] * (behind + 3) + [1, 1] + [0] * (2 * behind + 20)
+    for left in (64 * 3 - partial, n - 64 - partial):
+        b = Both(table, [n, left, 64, 1], refs)
+        room = n - left
+        new, cs, cd = b.reserve([0, room, 70, 1])
+        assert new.tolist() == [n, left, 134, 2] and b.table[1].tolist() == table[1]
+        b.n.copy_(new)
+        b.pool.n = new.tolist()
+        b.release([-1, left, -1, -1])
+        new, cs, cd = b.reserve([0, room, 1, 1])
+        assert new.tolist() == [n, n, 135, 3] and (cs[1] >= 0) == bool(partial)
+    b = Both(table, [n, 64, 64, 1], refs)                # reserved pages of its own behind shared ones, and without new tokens
+    b.reserve([64, 0, 0, 0])
+    b.reserve([1, 1, 1, 1])
+
+
 def test_reserve_without_enough_pages():
     refs = [1, 1, 0, 1, 0, 2]
     table = [[0, -1, -1], [1, -1, -1], [3, 5, -1], [5, -1, -1]]

@@ -96,6 +96,16 @@ def test_a_row_that_found_no_pages_appends_nothing():
         assert bool(kc.any()) == bool(vc.any()) == (not end)       # the other's tokens 100 .. 104
 
 
+def test_reserve_by_hand_over_a_shared_page_behind_the_tokens():
+    """Row 1's length was lowered by hand: page 1 behind its tokens is row 0's too.  Released, it gets a page of its own."""
+    p = paged.Pool([[0, 1, -1], [0, 1, -1], [2, -1, -1]], [128, 64, 64], [2, 2, 1, 0, 0])
+    assert p.reserve([0, 5, 1]) == ([128, 64, 65], [-1] * 3, [-1] * 3) and p.flags == {"id"}
+    assert p.table == [[0, 1, -1], [0, 1, -1], [2, 3, -1]] and p.refs == [2, 2, 1, 1, 0]
+    p.flags.clear()
+    p.release([-1, 64, -1])
+    assert p.reserve([0, 5, 0])[0] == [128, 69, 64] and p.table[1] == [0, 4, -1] and p.refs == [2, 1, 1, 1, 1] and not p.flags
+
+
 def test_rows_behind_a_descent_take_no_entries():
     k = torch.arange(6.0)[:, None, None].expand(6, 1, 128).double() + 1
     p = paged.Pool([[0], [1], [2]], [0] * 3, [1] * 3)
