@@ -589,7 +589,8 @@ size_t qsa_pages_workspace_bytes(int n_rows, int n_pages);
  * Entry i is skipped, with QSA_FLAG_BAD_ID, when src[i] or dst[i] is no row, when dst[i] is an
  * earlier dst or any src of the call, or when it still has tokens (release it first).  An
  * entry with src[i] = -1 and dst[i] = -1 is skipped without a flag.  Pages that the row dst[i] reserved
- * without tokens are released.
+ * without tokens are released.  An entry of src[i]'s row below its tokens that is no page becomes -1 in
+ * dst[i]'s (QSA_FLAG_BAD_ID); a length outside [0, 64 max_pages] is clamped (QSA_FLAG_NBLOCKS_CLAMPED).
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, QSA_MAX_TABLE_ROWS],
  * n_pages outside [1, QSA_MAX_PAGES], max_pages outside [1, QSA_MAX_PAGES], table_stride <
  * max_pages, n outside [0, n_rows], arrays that overlap each other or the workspace; QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not

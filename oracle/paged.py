@@ -111,11 +111,18 @@ class Pool:
             for p in self.table[b]:
                 if self._page(p):
                     self._drop(p)
-            nb = (self.n[a] + BT - 1) // BT
-            self.table[b] = [p if j < nb else -1 for j, p in enumerate(self.table[a])]
-            for p in self.table[b][:nb]:
-                self.refs[p] += 1
-            self.n[b] = self.n[a]
+            n = min(max(self.n[a], 0), BT * width)
+            if n != self.n[a]:
+                self.flags.add("clamp")
+            self.table[b] = [-1] * width
+            for j in range((n + BT - 1) // BT):
+                p = self.table[a][j]
+                if self._page(p):
+                    self.table[b][j] = p
+                    self.refs[p] += 1
+                else:
+                    self.flags.add("id")
+            self.n[b] = n
 
     def release(self, keep):
         for s, left in enumerate(keep):

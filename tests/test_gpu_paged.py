@@ -200,6 +200,27 @@ def test_bad_entries_are_flagged_and_left():
     c.compact(True)
 
 
+@pytest.mark.parametrize("bad", [-1, -2, 8, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("at,tokens", [(0, 200), (1, 200), (3, 200), (3, 192), (2, 129), (1, 64)])
+def test_fork_of_a_row_with_entries_that_are_no_page(at, tokens, bad):
+    """Below the tokens such an entry becomes -1 and is flagged; behind them it is not looked at."""
+    table = [[0, 1, 2, 3], [5, -1, -1, -1], [-1] * 4, [7, 7, -1, -1]]
+    table[0][at] = bad
+    refs = [1, 1, 1, 1, 0, 1, 0, 2]
+    if at < 4:
+        refs[at] = 0
+    b = Both(table, [tokens, 0, 0, 0], refs)
+    b.fork([0, -1, 0], [1, -1, 3])
+    assert (b.table[1].tolist()[at] == -1) and b.refs[-1] == 0
+
+
+@pytest.mark.parametrize("n", [257, 2 ** 31 - 1, -1, -2 ** 31, 256, 0])
+def test_fork_of_a_row_whose_length_is_out_of_range(n):
+    b = Both([[0, 1, 2, 3], [-1] * 4], [n, 0], [1] * 4 + [0])
+    b.fork([0], [1])
+    assert b.n.tolist() == [n, min(max(n, 0), 256)]
+
+
 @pytest.mark.parametrize("rows,width,pages", SIZES + [(2, 3, 2), (40, 300, 20_000)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_compact_matches_the_definition(rows, width, pages, in_place):

@@ -76,6 +76,15 @@ def test_pages_by_hand():
     assert not p.flags
 
 
+def test_fork_by_hand_from_a_row_with_entries_that_are_no_page():
+    p = paged.Pool([[0, -1, 9, 1], [-1] * 4, [-1] * 4], [200, 0, 0], [1, 1, 0])
+    p.fork([0], [1])
+    assert p.table[1] == [0, -1, -1, 1] and p.n[1] == 200 and p.refs == [2, 2, 0] and p.flags == {"id"}
+    p = paged.Pool([[0, 1], [-1] * 2, [-1] * 2], [300, 0, -7], [1, 1])
+    p.fork([0], [1])
+    assert p.table[1] == [0, 1] and p.n == [300, 128, -7] and p.refs == [2, 2] and p.flags == {"clamp"}
+
+
 def test_reserve_by_hand_when_pages_run_out():
     p = paged.Pool([[0, -1], [1, -1], [2, -1]], [64, 64, 10], [1, 1, 1, 0])
     new, _, _ = p.reserve([1, 1, 1])                    # one free page: row 0 has it, row 2 needs none
