@@ -186,6 +186,23 @@ def test_prompt_is_the_same_every_time_and_in_any_batch():
         assert torch.equal(out, first) and torch.equal(ls, l1)
 
 
+@pytest.mark.parametrize("kv,group,dt", [(2, 7, F16), (4, 16, BF16), (1, 1, BF16)])
+def test_a_prompt_alone_and_in_batches(kv, group, dt):
+    """Each sequence by itself, in batches of all kinds and in either order: how its work is cut, and so its last bits, may differ."""
+    lq, lk = [300, 1, 77, 0, 1200, 16], [300, 2500, 900, 40, 1200, 3]
+    q, k, v = (normal(91 + i, n, h, 128, dt=dt) for i, (n, h) in enumerate(((sum(lq), kv * group), (sum(lk), kv), (sum(lk), kv))))
+    qs, ks, vs = q.split(lq), k.split(lk), v.split(lk)
+    want = [paged.prompt(a.double(), b.double(), c.double(), [a.shape[0]], [b.shape[0]], SCALE) if a.shape[0] else None
+            for a, b, c in zip(qs, ks, vs)]
+    for batch in ([0], [1], [2], [4], [5], [0, 5], [5, 0, 2], [3, 0, 2, 5], [1, 4], list(range(6)), list(range(5, -1, -1)), [0, 2] * 40):
+        m, n = [lq[s] for s in batch], [lk[s] for s in batch]
+        out, lse, ws = _prompt(torch.cat([qs[s] for s in batch]), torch.cat([ks[s] for s in batch]), torch.cat([vs[s] for s in batch]), m, n)
+        assert qsa.read_flags(ws) == 0
+        for s, o, e in zip(batch, out.split(m), lse.split(m)):
+            if lq[s]:
+                check_attention(o, e, want[s], dt)
+
+
 # ------------------------------------------------------------------ trees
 
 def _tree_inputs(seed, n_tokens, nodes, kv, group, dt, spare=3):
@@ -293,6 +310,21 @@ def test_tree_bad_pages_parents_and_lengths_are_flagged():
     out, lse, ws = _tree(q, k, v, parents, nodes, kc, vc, table, [-5, wide + 1])   # as 0 and the row's width
     assert qsa.read_flags(ws) == qsa.FLAG_NBLOCKS_CLAMPED | qsa.FLAG_BAD_ID
     check_attention(out, lse, _want_tree(q, k, v, parents, nodes, kc, vc, table, [0, wide]), BF16)
+
+
+@pytest.mark.parametrize("kv,group,dt", [(2, 7, F16), (8, 8, BF16)])
+def test_a_tree_alone_and_in_batches(kv, group, dt):
+    n_tokens, nodes = [900, 0, 64, 5000, 333], [3, 9, 1, 20, 64]
+    q, k, v, parents, kc, vc, table = _tree_inputs(97, n_tokens, nodes, kv, group, dt)
+    at = cu(nodes)
+    want = _want_tree(q, k, v, parents, nodes, kc, vc, table, n_tokens)
+    for batch in ([0], [1], [2], [3], [4], [0, 1], [3, 2, 0], list(range(5)), list(range(4, -1, -1))):
+        rows = [i for s in batch for i in range(at[s], at[s + 1])]
+        m = [nodes[s] for s in batch]
+        out, lse, ws = _tree(q[rows], k[rows], v[rows], [parents[i] for i in rows], m, kc, vc, [table[s] for s in batch],
+                             [n_tokens[s] for s in batch])
+        check_attention(out, lse, [x[rows] for x in want], dt)
+        assert qsa.read_flags(ws) == 0
 
 
 def test_tree_of_one_node_is_the_last_row_of_a_prompt():
