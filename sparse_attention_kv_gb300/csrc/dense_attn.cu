@@ -71,9 +71,11 @@ constexpr int kSlack = 4;       // steps that pieces of one length may lie above
 constexpr int kRunKeys = 512;   // what a run's beginning and end cost, in keys (1024: 4,096 tokens 206 / 193, a mixed batch 270 / 304; 256: 206 / 239)
 constexpr int kTable = 256;     // sequences whose runs are counted in shared memory
 constexpr int kShortRun = 16;   // steps of runs that are dealt out however few the shares hold (0: 1,024 tokens 29 / 35; 64: no better)
-constexpr int kMinShare = 384;  // least work, in keys, of a share: no share in the middle of a run is without a step
+constexpr int kMinShare = 384;  // work, in keys, for each share that is used, the last one's rounded up: they hold half of it each at least
 constexpr int kShortKeys = 2048; // a sequence's keys up to which rows leave by TMA: see launch()
 constexpr int kManyParts = 8;   // parts of a run that combine_kernel shares out to its warps (38 parts 94 / 102; 64 sequences' two or three 360 / 348)
+// The join takes a share without a part for its run's end: borders a step apart have another step begin nearest to them.
+static_assert(kMinShare / 2 >= kKeys, "a share in the middle of a run has a step of it");
 constexpr float kRise = 8.0f;         // log2 of the largest weight before the reference moves
 constexpr uint32_t kColO = 0, kColS = 256;   // + 128 x stream
 
