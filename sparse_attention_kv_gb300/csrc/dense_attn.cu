@@ -14,6 +14,9 @@
 // one stream (a decode step) both take the same rows and half of a step's keys each, and are joined at the end.
 // m moves only when a row's maximum has risen by more than 2^8 of weight (then l and O are scaled in place): any
 // reference gives the same quotient, sums stay below 2^8 x keys, weights keep their relative precision.
+// The product with V takes the weights in V's 16 bits, as kind::f16 wants its A; l sums them before that rounding, since lse comes
+// from l too and would be off by up to half a step of that type.  So a row that one key outweighs, whose weight is no power
+// of two (it came after m was set), has V off by that much (2^-8 bf16, 2^-11 fp16), in an fp32 out as well; over many keys it averages out.
 //
 // Work: every (sequence, KV head, tile) is a run of steps; a persistent grid of one CTA per SM takes the runs whole or in
 // pieces (see Walk).  A run in pieces is joined by combine_kernel from the CTAs' partial (O, m, l).
@@ -268,8 +271,8 @@ __device__ __forceinline__ int warp_scan(int v) {   // inclusive
 //  kDealt  more runs, those that end last short against a share: whole, longest first within a (sequence, KV head), each to the
 //          next CTA that is free
 //  kBorder otherwise: all runs laid end to end and cut at equal distances
-// Measured, us: kEven / kBorder, 5 trees over 900 tokens 22 / 28; kDealt / kBorder, a prompt of 1,024 tokens 28 / 35, of 2,600
-// 89 / 100, of 16,384 2,450 / 2,520, 40 decodes of 2,500 tokens (8 heads; taken by kBorder) 105 / 85.
+// Measured, us: kEven / kBorder, 5 trees over 900 tokens 24 / 30; kDealt / kBorder, a prompt of 1,024 tokens 27 / 34, of 2,600
+// 85 / 97, of 16,384 2,213 / 2,280, 40 decodes of 2,500 tokens (8 heads; taken by kBorder) 104 / 88.
 enum Rule { kEven, kDealt, kBorder };
 
 template <bool TREE, bool HALVES>

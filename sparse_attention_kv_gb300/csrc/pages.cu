@@ -11,8 +11,9 @@
 //  - compact: one CTA lists the free pages below the number of live ones and the live pages behind it, both in order,
 //    and pairs them; a second grid rewrites the table.
 //  - append: a CTA looks a page up and takes some or all of its KV heads: K rows as they are, V through shared memory into its
-//    dimension-major block.  Bound by HBM: each row is read once and written once.
-// Measured: reserve and append for 8 sequences of up to 16 rows 11 us; for one of 131,072 rows, 4 KV heads, 97 us (537 MB, 5.5
+//    dimension-major block.  Bound by HBM where rows are long: each is read once and written once; where they are many and short,
+//    by the rows before its own that every CTA sums up (4,000 rows of a token, 8 heads, 132 us, with ends 139).
+// Measured: reserve and append for 8 sequences of up to 16 rows 11 us, back to back 5.5 and 3.6; for one of 131,072 rows, 4 KV heads, 97 us (537 MB, 5.5
 // TB/s; V transposed by words, by 16-bit elements 145); release, fork, reserve and the copied last pages for 8 sequences
 // forked into 64 14 us; the moves of 4,096 pages (4 KV heads, 55 % live) worked out and copied 52.5 us (of which 39 for the bytes).
 #include <cstdint>
@@ -483,10 +484,11 @@ __global__ void __launch_bounds__(kRowThreads) pages_retable_kernel(PageTable t,
     }
 }
 
-// Exclusive and total sums of a per-row count over the CTA, for the row that holds unit `unit`.
+// What a CTA of the append writes: the index-th page that a row's entries touch; row < 0: nothing.
 struct Unit {
-    int row, index;   // the index-th page that the row's entries touch; row < 0: no such unit
+    int row, index;
 };
+// The entries of a row, and where they go.
 struct Span {
     int e0;            // first entry
     long long lo, hi;  // positions
@@ -654,7 +656,7 @@ qsa_status launch_pages_append(const PageTable &t, const PagesAppendArgs &a, cud
     if (units > a.n) units = a.n;
     cudaLaunchConfig_t cfg{};
     // A CTA looks its page up once for all heads, unless the GPU would stay empty (us, so / a head each always: 4,000 rows of one
-    // token, 8 heads 93 / 223, 131,072 tokens in one row, 4 heads 97 / 95; all heads always: 8 rows of 16 tokens 11 / 15)
+    // token, 8 heads 132 / 401, 131,072 tokens in one row, 4 heads 82 / 79; all heads always: 8 rows of 16 tokens 3.6 / 8.0)
     const long long spread = 8ll * num_sms() / units;
     cfg.gridDim = dim3((unsigned)units, (unsigned)(spread < 1 ? 1 : spread < a.n_kv_heads ? spread : a.n_kv_heads));
     cfg.blockDim = dim3(kRowThreads);

@@ -13,7 +13,7 @@ if not torch.cuda.is_available():
 from oracle import paged  # noqa: E402
 from sparse_attention_kv_gb300 import qsa  # noqa: E402
 
-from .paged_cases import check_attention, cu, i32, normal, random_parents, random_pool, random_table  # noqa: E402
+from .paged_cases import HALF, check_attention, cu, i32, normal, random_parents, random_pool, random_table  # noqa: E402
 
 BF16, F16 = torch.bfloat16, torch.float16
 SCALE = 128 ** -0.5
@@ -184,6 +184,19 @@ def test_prompt_is_the_same_every_time_and_in_any_batch():
     for _ in range(3):
         out, ls, _ = _prompt(q, k, v, [500, 400], [500, 400], ws=ws)
         assert torch.equal(out, first) and torch.equal(ls, l1)
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("lq,lk", [([300], [300]), ([3], [5000]), ([40, 900], [700, 900])])
+def test_a_constant_value_comes_back_within_a_weights_rounding(lq, lk, dt):
+    """The weights of the product are rounded, those that are summed are not: each term is off by HALF[dt] of itself at most, so the
+    sum is; 2^-14 for fp32 sums, and half fp16's least step, 2^-25, for each weight below its normal range, the largest being 1 at
+    least, as in check_attention.  Late keys that outweigh the others by up to 2^8 are the worst case for it."""
+    q, k = normal(1, sum(lq), 16, 128, dt=dt), normal(2, sum(lk), 1, 128, dt=dt)
+    k[1::7] = (q[:1, :1] * torch.linspace(0.0, 0.4, k[1::7].shape[0], device="cuda")[:, None, None]).to(dt)
+    v = torch.full_like(k, 1.3)
+    out, lse, _ = _prompt(q, k, v, lq, lk, out_dt=torch.float32)
+    assert ((out.double() / v[0, 0, 0].double() - 1).abs() <= HALF[dt] + 2.0 ** -14 + (2.0 ** -25 * max(lk) if dt == F16 else 0.0)).all()
 
 
 @pytest.mark.parametrize("kv,group,dt", [(2, 7, F16), (4, 16, BF16), (1, 1, BF16)])
