@@ -560,7 +560,8 @@ qsa_status qsa_gather_blocks(const qsa_block_array *arrays, int n_arrays, const 
  *
  * all on the DEVICE.  A step of generation: qsa_pages_reserve makes room behind the sequences,
  * qsa_pages_copy copies the pages that were shared and are about to be written,
- * qsa_pages_append_reserved writes the rows of the sequences that got their room; qsa_pages_fork lets a sequence begin with another's pages,
+ * qsa_pages_append_reserved writes the rows of the sequences that got their room; qsa_pages_fork
+ * lets a sequence begin with another's pages,
  * qsa_pages_release gives pages back, qsa_pages_compact moves the live pages together.  The
  * attention of a prompt (qsa_prompt_attention) and of drafted tokens over the pages
  * (qsa_tree_attention) stand beside them.  No passage of the source pages defines these
@@ -593,7 +594,8 @@ size_t qsa_pages_workspace_bytes(int n_rows, int n_pages);
  * dst[i]'s (QSA_FLAG_BAD_ID); a length outside [0, 64 max_pages] is clamped (QSA_FLAG_NBLOCKS_CLAMPED).
  * Errors: QSA_ERR_INVALID_ARG for NULL pointers, n_rows outside [1, QSA_MAX_TABLE_ROWS],
  * n_pages outside [1, QSA_MAX_PAGES], max_pages outside [1, QSA_MAX_PAGES], table_stride <
- * max_pages, n outside [0, n_rows], arrays that overlap each other or the workspace; QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not
+ * max_pages, n outside [0, n_rows], arrays that overlap each other or the workspace;
+ * QSA_ERR_WORKSPACE for a ws smaller than 256 bytes or not
  * 256-byte aligned.
  */
 qsa_status qsa_pages_fork(int32_t *table, int64_t table_stride, int max_pages, int32_t *n_tokens, int n_rows,
@@ -672,7 +674,8 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
 /*
  * Append: K and V rows into the pages, whoever else refers to them: behind a reservation that may
  * not have served every row, qsa_pages_append_reserved is the call to make.
- * Row s takes cu_rows[s + 1] - cu_rows[s] rows, at positions first[s], first[s] + 1, ...: entry e (cu_rows[s] <= e < cu_rows[s + 1]) is row rows[e] of k and v
+ * Row s takes cu_rows[s + 1] - cu_rows[s] rows, at positions first[s], first[s] + 1, ...: entry e
+ * (cu_rows[s] <= e < cu_rows[s + 1]) is row rows[e] of k and v
  * (row e itself when rows is NULL) and goes to page table[s][pos / 64].
  *
  *   k, v      row r of KV head g at k + r * k_token_stride + g * k_head_stride, 128 values of `dt`
@@ -691,7 +694,8 @@ qsa_status qsa_pages_copy(const qsa_block_array *arrays, int n_arrays, const int
  * Errors: QSA_ERR_INVALID_ARG for NULL or misaligned pointers, strides not multiples of 8,
  * head_dim != 128, n_kv_heads outside [1, 65535], capacity not a positive multiple of 64 or above 64 *
  * QSA_MAX_PAGES, n_rows, max_pages or table_stride as above, n or n_source outside [0, 2^28],
- * rows NULL and n != n_source, a pool that overlaps an input, a workspace that overlaps either; QSA_ERR_UNSUPPORTED for another dtype; QSA_ERR_WORKSPACE as
+ * rows NULL and n != n_source, a pool that overlaps an input, a workspace that overlaps either;
+ * QSA_ERR_UNSUPPORTED for another dtype; QSA_ERR_WORKSPACE as
  * above.
  */
 qsa_status qsa_pages_append(const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
@@ -770,7 +774,7 @@ qsa_status qsa_prompt_attention(const void *q, int64_t q_token_stride, int64_t q
  * that puts a parent before its children).  A node sees every token of the sequence, its
  * ancestors and itself; formulas as for qsa_prompt_attention.  One node per sequence is an ordinary
  * decode step.  The nodes' K and V rows come with the call and are not in the pages yet
- * (qsa_pages_append writes those that are accepted).
+ * (qsa_pages_append_reserved writes those that are accepted).
  *
  *   q, k, v   as for qsa_prompt_attention, [total_nodes] rows
  *   parents   [total_nodes] int32 on the DEVICE: the parent's place in its tree (0 for its first node), or

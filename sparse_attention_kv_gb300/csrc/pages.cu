@@ -13,7 +13,7 @@
 //  - append: a CTA looks a page up and takes some or all of its KV heads: K rows as they are, V through shared memory into its
 //    dimension-major block.  Bound by HBM where rows are long: each is read once and written once; where they are many and short,
 //    by the rows before its own that every CTA sums up (4,000 rows of a token, 8 heads, 132 us, with ends 139).
-// Measured: reserve and append for 8 sequences of up to 16 rows 11 us, back to back 5.5 and 3.6; for one of 131,072 rows, 4 KV heads, 97 us (537 MB, 5.5
+// Measured: reserve and append for 8 sequences of up to 16 rows 11 us; for one of 131,072 rows, 4 KV heads, 97 us (537 MB, 5.5
 // TB/s; V transposed by words, by 16-bit elements 145); release, fork, reserve and the copied last pages for 8 sequences
 // forked into 64 14 us; the moves of 4,096 pages (4 KV heads, 55 % live) worked out and copied 52.5 us (of which 39 for the bytes).
 #include <cstdint>
